@@ -172,6 +172,8 @@ def prepare(case, seed):
             lay.S.copy_(S)
             lay.Pt.copy_(P)
             st.update(layer=lay, cache=StateCache(lay, n, case["bits"]), S=None)
+        else:
+            st["U"] = torch.zeros(2 * n, R, dv, device="cuda", dtype=torch.bfloat16)
         return st
 
     lens, dt, batch = _lens(case), DT[case["act"]], case["batch"]
@@ -213,6 +215,7 @@ def prepare(case, seed):
                                 st["start"], seqs=st["seqs"], has_state=st["has_state"])
     else:
         st["S"] = S
+        st["U"] = torch.zeros(batch, R, dv, device="cuda", dtype=dt)
     return st
 
 
@@ -262,7 +265,8 @@ def _plain_prefill(st):
     S = S.reshape(n, H, dk, dv)
     st["S"][rows] = S
     o = o.reshape(X, n, H, C, dv).permute(1, 0, 3, 2, 4).reshape(n, L, H, dv)[there]
-    return {"o": o.to(st["q"].dtype), "S": st["S"], "U": _sketch(S, st).to(st["q"].dtype)}
+    st["U"][rows] = _sketch(S, st).to(st["U"].dtype)
+    return {"o": o.to(st["q"].dtype), "S": st["S"], "U": st["U"]}
 
 
 def _plain_cache(st):
@@ -281,8 +285,8 @@ def _plain_cache(st):
     held_scale[slots] = scale
     S = (held[slots].float() * held_scale[slots]).reshape(n, H, dk, dv)
     st["S"][dst] = S
-    U = _sketch(S, st).to(torch.bfloat16)
-    return {"S": st["S"], "U": U}
+    st["U"][dst] = _sketch(S, st).to(st["U"].dtype)
+    return {"S": st["S"], "U": st["U"]}
 
 
 def _plain_norm(st):
@@ -311,18 +315,25 @@ def run(st):
     if op == "prefill":
         lay, pr = st["layer"], st["prompts"]
         lay.prefill(pr)
-        return {"o": pr.o, "S": lay.S, "U": lay.U[st["seqs"].long()]}
+        return {"o": pr.o, "S": lay.S, "U": lay.U}
     if op == "cache":
         lay = st["layer"]
         lay.save_state(st["cache"], st["src"], st["slots"])
         lay.load_state(st["cache"], st["dst"], st["slots"])
-        return {"S": lay.S, "U": lay.U[st["dst"].long()]}
+        return {"S": lay.S, "U": lay.U}
     from ssm_decode_amd.serving import group_norm
     group_norm(st["x"], st["norm"], st["y"], gate=st["gate"])
     return {"y": st["y"]}
 
 
 # ---------------------------------------------------------- 64-bit values
+def _at(rows, n, x):
+    """x in the given rows of n, zeros in the others."""
+    y = torch.zeros(n, *x.shape[1:], device=x.device, dtype=x.dtype)
+    y[rows.long()] = x
+    return y
+
+
 def exact(case, seed):
     st = prepare(case, seed)
     if case["op"] == "norm":
@@ -355,7 +366,7 @@ def exact(case, seed):
         live = amax >= TINY
         back = torch.where(live, torch.round(x / torch.where(live, s, torch.ones_like(s))) * s, torch.zeros_like(x)).flatten(-2)
         S[st["dst"].long()] = back
-        return {"S": S, "U": sketch(back)}
+        return {"S": S, "U": _at(st["dst"], len(S), sketch(back))}
     # the recurrence, token by token, every prompt and head at once
     rows = st["seqs"].long()
     S0 = st["S"].double()
@@ -377,7 +388,7 @@ def exact(case, seed):
     back = torch.empty_like(S)
     back[order] = S
     S0[rows] = back
-    return {"o": o, "S": S0, "U": sketch(back)}
+    return {"o": o, "S": S0, "U": _at(st["seqs"], len(S0), sketch(back))}
 
 
 # ------------------------------------------------------------------- work
