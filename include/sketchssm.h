@@ -120,8 +120,18 @@ extern "C" {
 /* bits OR-ed into *err by the kernels */
 #define SKSSM_ERRBIT_COUNT 1  /* count outside [0, W] (or == W at a read) */
 #define SKSSM_ERRBIT_GROUP 2  /* Mamba-2 heads of one B/C group disagree on count */
-#define SKSSM_ERRBIT_SEQ 4    /* sketchssm_flush_seqs: a listed index outside [0, batch),
-                                 or a tile claimed twice (a sequence listed twice) */
+#define SKSSM_ERRBIT_SEQ 4    /* sketchssm_flush_seqs, _prefill, _state_save, _state_load: a
+                                 listed index outside [0, batch), or a sequence listed twice
+                                 (flush_seqs: a tile claimed twice); _prefill: a prompt
+                                 whose token range is not valid */
+
+#define SKSSM_ERRBIT_SLOT 8   /* sketchssm_state_save/_load: a cache slot outside [0, slots), or
+                                 a slot that an earlier entry of a save's list has */
+
+/* activations of sketchssm_group_norm */
+#define SKSSM_ACT_NONE 0
+#define SKSSM_ACT_SILU 1    /* x / (1 + exp(-x)) */
+#define SKSSM_ACT_SIGMOID 2 /* 1 / (1 + exp(-x)) */
 
 /* Supported shapes: (dk, dv) in {(16,32), (64,64), (128,64), (128,128)};
  * 1 <= W <= 32; 0 <= r_h <= min(dk, 16), except r_h <= dk when dk == 16
@@ -309,6 +319,116 @@ int64_t sketchssm_workspace_bytes(const sketchssm_layer* layer);
  * call, so nothing needs clearing. */
 int sketchssm_read_noalloc(const sketchssm_layer* layer, const sketchssm_buffers* bufs,
                            const sketchssm_step* step, void* hip_stream);
+
+/* Prompts of the gated delta rule: token rows of nseq prompts, one behind the
+ * other.  Rows are [H][dk] or [H][dv] elements in a row; the strides are the
+ * elements from one token's row to the next (rows may be slices of one
+ * projection's output), at least a row, at most 2^31 - 1, and a multiple of
+ * 16 bytes for q, k, v and o. */
+typedef struct {
+  const void* q;             /* [tokens][H][dk] act dtype */
+  const void* k;             /* [tokens][H][dk] act dtype */
+  const void* v;             /* [tokens][H][dv] act dtype */
+  const float* gate;         /* alpha [tokens][H] fp32 */
+  const float* beta;         /* [tokens][H] fp32 */
+  void* o;                   /* [tokens][H][dv] act dtype (output); overlaps no input */
+  int64_t q_stride, k_stride, v_stride, gate_stride, beta_stride, o_stride;
+  int32_t tokens;            /* rows of q, k, v, gate, beta and o */
+  int32_t nseq;              /* prompts, at most layer->batch */
+  const int32_t* seq_start;  /* DEVICE [nseq + 1]: prompt i holds the tokens from seq_start[i] up to
+                                seq_start[i + 1]; 0 <= seq_start[i] <= seq_start[i + 1] <= tokens */
+  const int32_t* seqs;       /* DEVICE [nseq]: the sequence of prompt i, distinct; NULL: sequence i */
+  const int32_t* has_state;  /* DEVICE [nseq]: 0: prompt i starts from a zero state (its sequence's
+                                is not read); NULL: every prompt goes on from its state */
+  int32_t prime;             /* 1: also write the sketch U = S^T P (a dense-fallback head's state copy)
+                                of the new states; 0: leave the sketch as it is */
+  void* work;                /* workspace of sketchssm_prefill_workspace_bytes (16-byte aligned; may be
+                                NULL when that is 0), overwritten by the call */
+  int64_t work_bytes;        /* bytes at work */
+} sketchssm_prompts;
+
+/* Prompts through the gated delta rule (SKSSM_GDN): for each of a prompt's
+ * tokens in order, as sketchssm_full_step,
+ *   S <- alpha (I - beta k k^T) S + beta k v^T,  o = S^T q,
+ * and, with prime, the sketch that sketchssm_read starts from.  A sequence's
+ * ring must be empty (count 0): a tile with buffered entries sets
+ * SKSSM_ERRBIT_COUNT and is left untouched (flush it first).  A prompt with
+ * a bad range or sequence sets SKSSM_ERRBIT_SEQ and is skipped; where a
+ * sequence is listed twice, the first prompt has it.  A prompt of no tokens
+ * leaves its state (or writes the zero state), with prime its sketch too.
+ * Token rows that no prompt holds are neither read nor written.  Other
+ * families return SKSSM_EDIM; prime with SKSSM_COEF_STATE is SKSSM_EFLAG (a
+ * state-dependent map is formed by sketchssm_flush with SKSSM_FLUSH_ALL).
+ * nseq = 0 launches nothing. */
+int sketchssm_prefill(const sketchssm_layer* layer, const sketchssm_buffers* bufs,
+                      const sketchssm_prompts* prompts, void* hip_stream);
+
+/* Bytes of prompts->work that sketchssm_prefill needs for up to this many
+ * tokens and prompts, or a negative SKSSM_E* code.  Calls that may overlap
+ * need a workspace each. */
+int64_t sketchssm_prefill_workspace_bytes(const sketchssm_layer* layer, int32_t tokens, int32_t nseq);
+
+/* A pool of slots that each hold the states of one sequence's heads in 8 or
+ * 4 bits.  32 consecutive values of a state row (along dv) share a scale:
+ * scale = max|x| / 127 (8 bits) or / 7 (4 bits), code = x / scale rounded to
+ * nearest even, and a code stands for code * scale.  A block whose largest
+ * magnitude is under 2^-100 is held as zeros; one with an infinity or a NaN
+ * reads back as NaN. */
+typedef struct {
+  void* codes;               /* DEVICE [slots][H][dk][dv] two's complement codes of `bits` bits (4 bits:
+                                two to a byte, the lower column in the low half) */
+  float* scale;              /* DEVICE [slots][H][dk][dv / 32] */
+  int32_t slots;
+  int32_t bits;              /* 8 or 4, otherwise SKSSM_EDTYPE */
+} sketchssm_state_cache;
+
+/* Quantise the states of sequences seqs[0..n) into cache slots slots[0..n)
+ * (DEVICE int32 arrays, 4-byte aligned; any family).  A sequence may be
+ * saved to several slots.  The ring must be empty: a tile with buffered
+ * entries sets SKSSM_ERRBIT_COUNT and its part of the slot is left as it was
+ * (flush it first).  An index out of range sets SKSSM_ERRBIT_SEQ or
+ * SKSSM_ERRBIT_SLOT and the entry is skipped; of entries with the same slot
+ * the first is taken.  n = 0 launches nothing. */
+int sketchssm_state_save(const sketchssm_layer* layer, const sketchssm_buffers* bufs,
+                         const sketchssm_state_cache* cache, const int32_t* seqs,
+                         const int32_t* slots, int32_t n, void* hip_stream);
+
+/* Read cache slots slots[0..n) back into the states of sequences seqs[0..n)
+ * (distinct; a slot may be read into several sequences), empty their rings
+ * (count 0) and, with prime (0 or 1), write their sketches as
+ * sketchssm_prefill does.  Errors as sketchssm_state_save; of entries with
+ * the same sequence the first is taken. */
+int sketchssm_state_load(const sketchssm_layer* layer, const sketchssm_buffers* bufs,
+                         const sketchssm_state_cache* cache, const int32_t* seqs,
+                         const int32_t* slots, int32_t n, int32_t prime, void* hip_stream);
+
+/* Group norm of rows whose channels come last, with an activation and a gate
+ * (what the layers apply to o behind the state read).  For each row and each
+ * group of `width` channels, with a = the activation:
+ *   x' = gate_first ? x * a(gate) : x       (gate NULL: x' = x)
+ *   n  = (x' - mean) / sqrt(var + eps)      (centred 0: mean = 0, var = the mean of squares)
+ *   y  = n * weight + bias,  then  y * a(gate) where the gate comes after,
+ *        a(y) where there is no gate.
+ * Statistics and arithmetic are fp32, rounded once to y. */
+typedef struct {
+  const void* x;             /* [rows][groups][width] */
+  const void* gate;          /* [rows][groups][width], or NULL */
+  void* y;                   /* [rows][groups][width]; may be x or gate itself */
+  const float* weight;       /* [groups][width], or [width] for every group; NULL: 1 */
+  const float* bias;         /* as weight; NULL: 0 */
+  int64_t x_stride, gate_stride, y_stride; /* elements from a row to the next: at least a row, at most
+                                2^31 - 1, a multiple of 16 bytes */
+  int64_t rows;
+  int32_t groups;            /* 1 to 65535 */
+  int32_t width;             /* 8 to 8192, a multiple of 8 */
+  int32_t dtype;             /* of x, gate and y: SKSSM_F32 or SKSSM_BF16 */
+  int32_t group_weights;     /* 1: weight and bias are [groups][width]; 0: [width] */
+  int32_t centred;           /* 0 or 1 */
+  int32_t activation;        /* SKSSM_ACT_* */
+  int32_t gate_first;        /* 0 or 1 */
+  float eps;                 /* finite, >= 0 */
+} sketchssm_norm;
+int sketchssm_group_norm(const sketchssm_norm* norm, void* hip_stream);
 
 /* Library version (major * 10000 + minor * 100 + patch). */
 int sketchssm_version(void);

@@ -1,8 +1,8 @@
 """ctypes binding of libsketchssm.so (argument marshalling only).
 
-The four entry points keep the C names: ``sketchssm_read``,
-``sketchssm_flush``, ``sketchssm_full_step``, ``sketchssm_replay_step``.
-Each takes the three argument structs (or pointers to them) and a HIP stream
+The entry points keep the C names; those of the decode steps are
+``sketchssm_read``, ``sketchssm_flush``, ``sketchssm_full_step`` and
+``sketchssm_replay_step``.  Each of these takes the three argument structs (or pointers to them) and a HIP stream
 handle, and returns the library's status code.  Loading fails loudly when the
 library has not been built: there is no fallback path.
 """
@@ -23,11 +23,13 @@ SKSSM_PULLBACK_SERIAL, SKSSM_PULLBACK_WY, SKSSM_PULLBACK_PROJ = 0, 1, 2
 SKSSM_OK, SKSSM_EINVAL, SKSSM_EDIM, SKSSM_EDTYPE, SKSSM_EFLAG, SKSSM_ELAUNCH = 0, -1, -2, -3, -4, -5
 SKSSM_ESCRATCH = -6
 SKSSM_NOALLOC_SCRATCH_BYTES = 16777216
-SKSSM_ERRBIT_COUNT, SKSSM_ERRBIT_GROUP, SKSSM_ERRBIT_SEQ = 1, 2, 4
+SKSSM_ERRBIT_COUNT, SKSSM_ERRBIT_GROUP, SKSSM_ERRBIT_SEQ, SKSSM_ERRBIT_SLOT = 1, 2, 4, 8
+SKSSM_ACT_NONE, SKSSM_ACT_SILU, SKSSM_ACT_SIGMOID = 0, 1, 2
 
 ENTRY_POINTS = ("sketchssm_read", "sketchssm_flush", "sketchssm_flush_seqs", "sketchssm_full_step",
                 "sketchssm_replay_step", "sketchssm_workspace_bytes", "sketchssm_read_noalloc",
-                "sketchssm_version")
+                "sketchssm_prefill", "sketchssm_prefill_workspace_bytes", "sketchssm_state_save",
+                "sketchssm_state_load", "sketchssm_group_norm", "sketchssm_version")
 
 
 class sketchssm_layer(C.Structure):
@@ -49,6 +51,28 @@ class sketchssm_buffers(C.Structure):
 class sketchssm_step(C.Structure):
     _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("gate", C.c_void_p),
                 ("beta", C.c_void_p), ("o", C.c_void_p)]
+
+
+class sketchssm_prompts(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("gate", C.c_void_p),
+                ("beta", C.c_void_p), ("o", C.c_void_p),
+                ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("gate_stride", C.c_int64), ("beta_stride", C.c_int64), ("o_stride", C.c_int64),
+                ("tokens", C.c_int32), ("nseq", C.c_int32), ("seq_start", C.c_void_p),
+                ("seqs", C.c_void_p), ("has_state", C.c_void_p), ("prime", C.c_int32),
+                ("work", C.c_void_p), ("work_bytes", C.c_int64)]
+
+
+class sketchssm_state_cache(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scale", C.c_void_p), ("slots", C.c_int32), ("bits", C.c_int32)]
+
+
+class sketchssm_norm(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("gate", C.c_void_p), ("y", C.c_void_p), ("weight", C.c_void_p),
+                ("bias", C.c_void_p), ("x_stride", C.c_int64), ("gate_stride", C.c_int64),
+                ("y_stride", C.c_int64), ("rows", C.c_int64), ("groups", C.c_int32), ("width", C.c_int32),
+                ("dtype", C.c_int32), ("group_weights", C.c_int32), ("centred", C.c_int32),
+                ("activation", C.c_int32), ("gate_first", C.c_int32), ("eps", C.c_float)]
 
 
 _lib = None
@@ -83,6 +107,17 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         lib.sketchssm_flush_seqs.restype = C.c_int
         lib.sketchssm_workspace_bytes.argtypes = [L]
         lib.sketchssm_workspace_bytes.restype = C.c_int64
+        Ca, Pr = C.POINTER(sketchssm_state_cache), C.POINTER(sketchssm_prompts)
+        lib.sketchssm_prefill.argtypes = [L, Bf, Pr, C.c_void_p]
+        lib.sketchssm_prefill_workspace_bytes.argtypes = [L, C.c_int32, C.c_int32]
+        lib.sketchssm_prefill_workspace_bytes.restype = C.c_int64
+        lib.sketchssm_state_save.argtypes = [L, Bf, Ca, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p]
+        lib.sketchssm_state_load.argtypes = [L, Bf, Ca, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
+                                             C.c_void_p]
+        lib.sketchssm_group_norm.argtypes = [C.POINTER(sketchssm_norm), C.c_void_p]
+        for name in ("sketchssm_prefill", "sketchssm_state_save", "sketchssm_state_load",
+                     "sketchssm_group_norm"):
+            getattr(lib, name).restype = C.c_int
         lib.sketchssm_version.argtypes = []
         lib.sketchssm_version.restype = C.c_int
         _lib = lib
@@ -132,6 +167,31 @@ def sketchssm_replay_step(layer, bufs, step, stream=None) -> int:
 
 def sketchssm_workspace_bytes(layer) -> int:
     return load().sketchssm_workspace_bytes(_ref(layer, sketchssm_layer))
+
+
+def sketchssm_prefill(layer, bufs, prompts, stream=None) -> int:
+    return load().sketchssm_prefill(_ref(layer, sketchssm_layer), _ref(bufs, sketchssm_buffers),
+                                    _ref(prompts, sketchssm_prompts), stream)
+
+
+def sketchssm_prefill_workspace_bytes(layer, tokens, nseq) -> int:
+    return load().sketchssm_prefill_workspace_bytes(_ref(layer, sketchssm_layer), int(tokens), int(nseq))
+
+
+def sketchssm_state_save(layer, bufs, cache, seqs, slots, n, stream=None) -> int:
+    """seqs, slots: device addresses of n int32 indices (or None with n = 0)."""
+    return load().sketchssm_state_save(_ref(layer, sketchssm_layer), _ref(bufs, sketchssm_buffers),
+                                       _ref(cache, sketchssm_state_cache), seqs, slots, int(n), stream)
+
+
+def sketchssm_state_load(layer, bufs, cache, seqs, slots, n, prime, stream=None) -> int:
+    return load().sketchssm_state_load(_ref(layer, sketchssm_layer), _ref(bufs, sketchssm_buffers),
+                                       _ref(cache, sketchssm_state_cache), seqs, slots, int(n), int(prime),
+                                       stream)
+
+
+def sketchssm_group_norm(norm, stream=None) -> int:
+    return load().sketchssm_group_norm(_ref(norm, sketchssm_norm), stream)
 
 
 def sketchssm_version() -> int:

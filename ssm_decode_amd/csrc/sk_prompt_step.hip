@@ -1,0 +1,188 @@
+// Prompts through the gated delta rule, one token at a time:
+//   u = beta (v - alpha S^T k),  S <- alpha S + k u^T,  o = S^T q.
+// One workgroup per (prompt, head); a wave holds 32 columns of the tile, all
+// of its rows, in registers for the whole prompt (the columns of S never mix,
+// so the waves of a tile meet only where the tokens are staged).
+//
+// A prompt of a few tokens is bound by its state's traffic (4 dk dv bytes in
+// and out); a long one by the arithmetic, 8 dk dv operations a token on the
+// vector units, so long bf16 prompts take the chunked form.
+#include "sk_serve_device.hpp"
+
+namespace sk {
+namespace {
+
+constexpr int TB = 16;    // tokens staged at a time
+
+template <typename AT> struct Chunk16 { static constexpr int N = 16 / (int)sizeof(AT); };
+
+__device__ __forceinline__ void put_chunk(float* dst, const uint4& r, const bf16*) {
+  reinterpret_cast<float4*>(dst)[0] = make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
+                                                  __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+  reinterpret_cast<float4*>(dst)[1] = make_float4(__uint_as_float(r.z << 16), __uint_as_float(r.z & 0xffff0000u),
+                                                  __uint_as_float(r.w << 16), __uint_as_float(r.w & 0xffff0000u));
+}
+__device__ __forceinline__ void put_chunk(float* dst, const uint4& r, const float*) {
+  *reinterpret_cast<uint4*>(dst) = r;
+}
+
+// Rows of D elements of up to TB tokens: global -> registers -> LDS as fp32.
+template <int D, int NT, typename AT>
+struct Rows {
+  static constexpr int N = Chunk16<AT>::N, CPR = D / N, U = (TB * CPR + NT - 1) / NT;
+  uint4 r[U];
+  __device__ __forceinline__ void load(const AT* base, int64_t stride, int nt) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = threadIdx.x + NT * u, t = c / CPR;
+      if (t < nt) r[u] = *reinterpret_cast<const uint4*>(base + t * stride + (c - t * CPR) * N);
+    }
+  }
+  __device__ __forceinline__ void stage(float* lds, int nt) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = threadIdx.x + NT * u, t = c / CPR;
+      if (t < nt) put_chunk(lds + t * D + (c - t * CPR) * N, r[u], (const AT*)nullptr);
+    }
+  }
+};
+
+template <int DK, int DV, typename AT>
+__global__ void __launch_bounds__(DV * 2) prompt_step_kernel(PromptParams p) {
+  constexpr int NT = DV * 2, MB = DK / 16;
+  __shared__ __align__(16) float s_k[TB * DK], s_q[TB * DK], s_v[TB * DV], s_ab[2 * TB];
+
+  const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H;
+  // a prompt of another length belongs to the other form's launch (which
+  // reports it where its range is not valid)
+  const int len0 = p.start[i + 1] - p.start[i];
+  if (len0 < p.len_lo && len0 >= 0) return;
+  if (len0 > p.len_hi) return;
+  const PromptTile t = prompt_tile(p, i, h);
+  if (!t.ok) return;
+
+  const int tid = threadIdx.x, lane = tid & 63, cg = lane & 15, rg = lane >> 4;
+  const int col0 = 32 * (tid >> 6), col = col0 + 2 * cg;
+  float* Sg = p.S + ((size_t)t.b * p.H + h) * DK * DV + (size_t)(4 * rg) * DV + col;
+
+  const AT* kp = reinterpret_cast<const AT*>(p.k) + t.s0 * p.ks + (int64_t)h * DK;
+  const AT* qp = reinterpret_cast<const AT*>(p.q) + t.s0 * p.qs + (int64_t)h * DK;
+  const AT* vp = reinterpret_cast<const AT*>(p.v) + t.s0 * p.vs + (int64_t)h * DV;
+  const float* ap = p.gate + t.s0 * p.gs + h;
+  const float* bp = p.beta + t.s0 * p.bs + h;
+  AT* op = reinterpret_cast<AT*>(p.o) + t.s0 * p.os + (int64_t)h * DV + col;
+
+  // the small loads first, then the state
+  Rows<DK, NT, AT> rk, rq;
+  Rows<DV, NT, AT> rv;
+  float ab = 0.f;
+  auto fetch = [&](int t0, int nt) {
+    rk.load(kp + t0 * p.ks, p.ks, nt);
+    rq.load(qp + t0 * p.qs, p.qs, nt);
+    rv.load(vp + t0 * p.vs, p.vs, nt);
+    if (tid < TB) {
+      if (tid < nt) ab = ap[(t0 + tid) * p.gs];
+    } else if (tid < 2 * TB && tid - TB < nt) {
+      ab = bp[(t0 + tid - TB) * p.bs];
+    }
+  };
+  int nt = t.len < TB ? t.len : TB;
+  fetch(0, nt);
+
+  float s[MB][2][4];
+  if (!p.has_state || p.has_state[i] != 0) {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float x[2];
+        ldn_nt<2>(Sg + (size_t)(16 * mb + v) * DV, x);
+        s[mb][0][v] = x[0];
+        s[mb][1][v] = x[1];
+      }
+  } else {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) s[mb][0][v] = s[mb][1][v] = 0.f;
+  }
+
+  for (int t0 = 0; t0 < t.len; t0 += TB) {
+    rk.stage(s_k, nt);
+    rq.stage(s_q, nt);
+    rv.stage(s_v, nt);
+    if (tid < 2 * TB) s_ab[tid] = ab;
+    __syncthreads();
+    const int now = nt, left = t.len - t0 - TB;
+    if (left > 0) {                        // the next block's loads, in flight over this one
+      nt = left < TB ? left : TB;
+      fetch(t0 + TB, nt);
+    }
+    for (int j = 0; j < now; ++j) {
+      float kk[MB][4];
+      float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        ld4(s_k + j * DK + 16 * mb + 4 * rg, kk[mb]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          a0 += s[mb][0][v] * kk[mb][v];
+          a1 += s[mb][1][v] * kk[mb][v];
+        }
+      }
+      a0 = xsum<4, 2>(a0);                 // over the four row groups
+      a1 = xsum<4, 2>(a1);
+      const float al = s_ab[j], be = s_ab[TB + j];
+      float vv[2];
+      ldn<2>(s_v + j * DV + col, vv);
+      const float u0 = be * (vv[0] - al * a0), u1 = be * (vv[1] - al * a1);
+      float o0 = 0.f, o1 = 0.f;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        float qq[4];
+        ld4(s_q + j * DK + 16 * mb + 4 * rg, qq);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          s[mb][0][v] = al * s[mb][0][v] + kk[mb][v] * u0;
+          s[mb][1][v] = al * s[mb][1][v] + kk[mb][v] * u1;
+          o0 += s[mb][0][v] * qq[v];
+          o1 += s[mb][1][v] * qq[v];
+        }
+      }
+      const float o2[2] = {xsum<4, 2>(o0), xsum<4, 2>(o1)};
+      if (rg == 0) stn<2>(op + (t0 + j) * p.os, o2);
+    }
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float x[2] = {s[mb][0][v], s[mb][1][v]};
+      stn_nt<2>(Sg + (size_t)(16 * mb + v) * DV, x);
+    }
+  if (p.prime) sketch_tile<DK, DV, AT>(p.sk, s, t.b, h, col0, lane);
+}
+
+template <int DK, int DV>
+int launch_shape(int act, const PromptParams& p, hipStream_t st) {
+  const dim3 grid(p.nseq * p.H), block(DV * 2);
+  if (act == DT_F32)
+    hipLaunchKernelGGL((prompt_step_kernel<DK, DV, float>), grid, block, 0, st, p);
+  else
+    hipLaunchKernelGGL((prompt_step_kernel<DK, DV, bf16>), grid, block, 0, st, p);
+  return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+}  // namespace
+
+int launch_prompt_step(int dk, int dv, int act, const PromptParams& p, hipStream_t st) {
+  if (dk == 16 && dv == 32) return launch_shape<16, 32>(act, p, st);
+  if (dk == 64 && dv == 64) return launch_shape<64, 64>(act, p, st);
+  if (dk == 128 && dv == 64) return launch_shape<128, 64>(act, p, st);
+  if (dk == 128 && dv == 128) return launch_shape<128, 128>(act, p, st);
+  return -2;
+}
+
+}  // namespace sk

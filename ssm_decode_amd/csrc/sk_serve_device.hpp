@@ -1,0 +1,91 @@
+// Device code shared by the prompt and state-cache kernels: which prompt a
+// workgroup may take, and the sketch of a tile held in registers.
+#pragma once
+
+#include "sk_device.hpp"
+#include "sk_serve.hpp"
+
+namespace sk {
+
+typedef float f32x4s __attribute__((ext_vector_type(4)));
+
+// Whether an entry before position i of a device list names the same index
+// (every thread of the workgroup takes part; uniform result).
+__device__ __forceinline__ bool listed_before(const int32_t* list, int i, int idx) {
+  int dup = 0;
+  for (int j = threadIdx.x; j < i; j += blockDim.x) dup |= list[j] == idx;
+  return __syncthreads_or(dup) != 0;
+}
+
+// The sequence, first token and length of prompt i, checked: an index
+// outside the batch, a range outside the tokens, or a sequence that an
+// earlier prompt of the list has (the earlier one keeps it) reports
+// ERRBIT_SEQ; a tile whose ring still holds entries ERRBIT_COUNT.  ok is
+// uniform over the workgroup.
+struct PromptTile {
+  int b, s0, len;
+  bool ok;
+};
+__device__ __forceinline__ PromptTile prompt_tile(const PromptParams& p, int i, int h) {
+  PromptTile t;
+  t.s0 = p.start[i];
+  const int s1 = p.start[i + 1];
+  t.len = s1 - t.s0;
+  t.b = p.seqs ? p.seqs[i] : i;
+  int bad = 0;
+  if (t.b < 0 || t.b >= p.B || t.s0 < 0 || s1 < t.s0 || s1 > p.tokens) {
+    bad = ERRBIT_SEQ;
+  } else {
+    if (p.seqs && listed_before(p.seqs, i, t.b)) bad = ERRBIT_SEQ;
+    if (!bad && p.count[(size_t)t.b * p.H + h] != 0) bad = ERRBIT_COUNT;
+  }
+  if (bad && threadIdx.x == 0) atomicOr(p.err, bad);
+  t.ok = bad == 0;
+  return t;
+}
+
+// Registers of a wave's 32 columns of a tile, as the flush holds them: with
+// cg = lane % 16 and rg = lane / 16,
+//   s[mb][c][v] = S[16 mb + 4 rg + v][col0 + 2 cg + c].
+// The layout is the A operand of v_mfma_f32_16x16x4_f32 for S^T (K-step
+// (mb, v) covers rows 16 mb + 4 k + v), so the sketch needs no data movement:
+// lane holds u_j, j = cg, at columns col0 + 2 (4 rg + vv) + c.
+template <int DK, int DV, typename UT>
+__device__ __forceinline__ void sketch_tile(const SketchOut& sk, const float (&s)[DK / 16][2][4], int b, int h,
+                                            int col0, int lane) {
+  constexpr int MB = DK / 16;
+  const int cg = lane & 15, rg = lane >> 4;
+  const int off = sk.off[h], r = sk.off[h + 1] - off;
+  if (r == 0) {                       // a dense-fallback head: the state copy
+    int slot = 0;
+    while (slot + 1 < sk.ndense && sk.dense_list[slot] != h) ++slot;
+    UT* C = reinterpret_cast<UT*>(sk.Sc) + ((size_t)b * sk.ndense + slot) * DK * DV + col0 + 2 * cg;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float x[2] = {s[mb][0][v], s[mb][1][v]};
+        stn<2>(C + (size_t)(16 * mb + 4 * rg + v) * DV, x);
+      }
+    return;
+  }
+  f32x4s u0 = {0.f, 0.f, 0.f, 0.f}, u1 = u0;
+  const float* pr = sk.Pt + (size_t)(off + (cg < r ? cg : 0)) * DK + 4 * rg;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    float x[4];
+    ld4(pr + 16 * mb, x);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      u0 = __builtin_amdgcn_mfma_f32_16x16x4f32(s[mb][0][v], x[v], u0, 0, 0, 0);
+      u1 = __builtin_amdgcn_mfma_f32_16x16x4f32(s[mb][1][v], x[v], u1, 0, 0, 0);
+    }
+  }
+  if (cg < r) {                       // (columns j >= r repeat row 0 and are dropped)
+    UT* U = reinterpret_cast<UT*>(sk.U) + ((size_t)b * sk.R + off + cg) * DV + col0 + 8 * rg;
+    const float x[8] = {u0[0], u1[0], u0[1], u1[1], u0[2], u1[2], u0[3], u1[3]};
+    stn<8>(U, x);
+  }
+}
+
+}  // namespace sk

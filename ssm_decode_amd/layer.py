@@ -25,6 +25,10 @@ def current_stream_handle() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _stream_of(stream):
+    return C.c_void_p(current_stream_handle() if stream is None else stream)
+
+
 @dataclass
 class DeviceStep:
     """One decode step's device tensors (layouts as in include/sketchssm.h)."""
@@ -137,7 +141,7 @@ class DecodeLayer:
 
     # ---------------------------------------------------------------- calls
     def _stream(self, stream):
-        return C.c_void_p(current_stream_handle() if stream is None else stream)
+        return _stream_of(stream)
 
     def read(self, step: DeviceStep, stream=None) -> int:
         return abi.sketchssm_read(self._layer, self._bufs, step.struct(), self._stream(stream))
@@ -167,6 +171,29 @@ class DecodeLayer:
 
     def replay_step(self, step: DeviceStep, stream=None) -> int:
         return abi.sketchssm_replay_step(self._layer, self._bufs, step.struct(), self._stream(stream))
+
+    def prefill(self, prompts, stream=None) -> int:
+        """Prompts (serving.Prompts) through the gated delta rule: their outputs,
+        the sequences' new states and, with prompts.prime, their sketches."""
+        with torch.cuda.device(self.S.device):
+            return abi.sketchssm_prefill(self._layer, self._bufs, prompts.struct, self._stream(stream))
+
+    def save_state(self, cache, seqs, slots, stream=None) -> int:
+        """Quantise the states of sequences seqs into the slots of a
+        serving.StateCache (int32 device tensors)."""
+        cache.check(self, seqs, slots)
+        with torch.cuda.device(self.S.device):
+            return abi.sketchssm_state_save(self._layer, self._bufs, cache.struct, _ptr(seqs), _ptr(slots),
+                                            seqs.numel(), self._stream(stream))
+
+    def load_state(self, cache, seqs, slots, prime: bool = True, stream=None) -> int:
+        """Read slots of a serving.StateCache back into the states of sequences
+        seqs (distinct), empty their rings and, with prime, write their
+        sketches."""
+        cache.check(self, seqs, slots)
+        with torch.cuda.device(self.S.device):
+            return abi.sketchssm_state_load(self._layer, self._bufs, cache.struct, _ptr(seqs), _ptr(slots),
+                                            seqs.numel(), int(prime), self._stream(stream))
 
     def error_word(self) -> int:
         return int(self.err[0].item())

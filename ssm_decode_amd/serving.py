@@ -1,0 +1,153 @@
+"""What a serving loop runs around the decode steps, on torch tensors: prompts
+through the gated delta rule (``Prompts``, ``DecodeLayer.prefill``), the
+quantised state cache (``StateCache``, ``DecodeLayer.save_state`` and
+``load_state``) and the norm of the layers' outputs (``OutputNorm``,
+``group_norm``).  The tensors are checked here, where a wrong one would have
+a kernel read what it must not; the work runs in the HIP library."""
+from __future__ import annotations
+
+import ctypes as C
+from typing import Optional
+
+import torch
+
+from . import abi
+from .layer import DTYPE, TORCH_DTYPE, DecodeLayer, _ptr, _stream_of
+
+ACT = {"none": abi.SKSSM_ACT_NONE, "silu": abi.SKSSM_ACT_SILU, "sigmoid": abi.SKSSM_ACT_SIGMOID}
+
+
+def _rows(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device) -> int:
+    """Checks a tensor of token rows (each row contiguous, the rows at any
+    stride) and gives the elements from one row to the next."""
+    if tuple(x.shape) != shape or x.dtype != dtype or x.device != device:
+        raise ValueError(f"{name}: a {dtype} tensor of shape {shape} on {device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
+    row = 1
+    for n, s in zip(reversed(shape[1:]), reversed(x.stride()[1:])):
+        if n != 1 and s != row:
+            raise ValueError(f"{name}: every row has to be contiguous, got strides {x.stride()}")
+        row *= n
+    return x.stride(0) if shape[0] > 1 else row
+
+
+def _indices(name: str, x: torch.Tensor, n: Optional[int], device: torch.device) -> None:
+    if x.dtype != torch.int32 or x.dim() != 1 or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{name}: a contiguous 1-d int32 tensor on {device}")
+    if n is not None and x.numel() != n:
+        raise ValueError(f"{name}: {n} entries, got {x.numel()}")
+
+
+class Prompts:
+    """Token rows of several prompts, one behind the other, for
+    ``DecodeLayer.prefill``: q, k [tokens, H, dk], v, o [tokens, H, dv] in the
+    layer's activation dtype, gate (alpha) and beta [tokens, H] fp32 (rows at
+    any stride of whole 16 bytes: slices of one projection will do);
+    seq_start [n + 1] int32: prompt i holds tokens seq_start[i] up to
+    seq_start[i + 1]; seqs [n]: its sequence (None: sequence i); has_state
+    [n]: 0 starts it from a zero state (None: every prompt goes on from its
+    sequence's state); prime: also write the sketches of the new states.  The
+    index tensors are read on the device at the call, the tensors are held,
+    and the workspace is allocated once: calls that may overlap take a
+    ``Prompts`` each."""
+
+    def __init__(self, layer: DecodeLayer, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: torch.Tensor,
+                 beta: torch.Tensor, o: torch.Tensor, seq_start: torch.Tensor,
+                 seqs: Optional[torch.Tensor] = None, has_state: Optional[torch.Tensor] = None,
+                 prime: bool = True):
+        dev, at = layer.S.device, TORCH_DTYPE[layer.act]
+        N, H = q.shape[0], layer.H
+        strides = [_rows("q", q, (N, H, layer.dk), at, dev), _rows("k", k, (N, H, layer.dk), at, dev),
+                   _rows("v", v, (N, H, layer.dv), at, dev), _rows("gate", gate, (N, H), torch.float32, dev),
+                   _rows("beta", beta, (N, H), torch.float32, dev), _rows("o", o, (N, H, layer.dv), at, dev)]
+        _indices("seq_start", seq_start, None, dev)
+        n = seq_start.numel() - 1
+        if n < 0:
+            raise ValueError("seq_start: the prompts' first tokens and the end of the last")
+        for name, x in (("seqs", seqs), ("has_state", has_state)):
+            if x is not None:
+                _indices(name, x, n, dev)
+        need = abi.sketchssm_prefill_workspace_bytes(layer.layer_struct, N, n)
+        if need < 0:
+            raise ValueError(f"prompts that this layer does not take (code {need})")
+        self.q, self.k, self.v, self.gate, self.beta, self.o = q, k, v, gate, beta, o
+        self.seq_start, self.seqs, self.has_state, self.prime = seq_start, seqs, has_state, prime
+        self.work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        self._struct = abi.sketchssm_prompts(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(beta), _ptr(o), *strides, N, n, _ptr(seq_start),
+            _ptr(seqs), _ptr(has_state), int(prime), _ptr(self.work), need)
+
+    @property
+    def struct(self) -> abi.sketchssm_prompts:
+        return self._struct
+
+
+class StateCache:
+    """A pool of ``slots`` slots, each for one sequence's states of a layer in
+    8 or 4 bits: codes [slots, H, dk, dv] int8 (4 bits: [.., dv / 2] uint8, the
+    lower column in the low half) and scale [slots, H, dk, dv / 32]."""
+
+    def __init__(self, layer: DecodeLayer, slots: int, bits: int = 8):
+        if bits not in (8, 4):
+            raise ValueError("bits: 8 or 4")
+        if slots < 0:
+            raise ValueError("slots: 0 or more")
+        H, dk, dv, dev = layer.H, layer.dk, layer.dv, layer.S.device
+        self.slots, self.bits, self.shape = slots, bits, (H, dk, dv)
+        self.codes = (torch.zeros((slots, H, dk, dv), dtype=torch.int8, device=dev) if bits == 8 else
+                      torch.zeros((slots, H, dk, dv // 2), dtype=torch.uint8, device=dev))
+        self.scale = torch.zeros((slots, H, dk, dv // 32), dtype=torch.float32, device=dev)
+        self._struct = abi.sketchssm_state_cache(_ptr(self.codes), _ptr(self.scale), slots, bits)
+
+    @property
+    def struct(self) -> abi.sketchssm_state_cache:
+        return self._struct
+
+    def check(self, layer: DecodeLayer, seqs: torch.Tensor, slots: torch.Tensor) -> None:
+        """Raises ValueError where these entries of this cache are none of the layer's."""
+        if self.shape != (layer.H, layer.dk, layer.dv) or self.codes.device != layer.S.device:
+            raise ValueError(f"a cache of states {self.shape} on {self.codes.device}, not of this layer's")
+        _indices("seqs", seqs, None, layer.S.device)
+        _indices("slots", slots, seqs.numel(), layer.S.device)
+
+
+class OutputNorm:
+    """How a layer's outputs are normalised: over each group of channels, by
+    the root mean square or (centred) by mean and variance, times weight plus
+    bias (fp32, [groups, width], or [width] for every group; None: 1 and 0),
+    with an activation ("none", "silu" or "sigmoid") of the gate, multiplied
+    on before the norm (gate_first) or after it; without a gate the
+    activation is that of the result."""
+
+    def __init__(self, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                 eps: float = 1e-5, act: str = "silu", centred: bool = False, gate_first: bool = False):
+        for name, x in (("weight", weight), ("bias", bias)):
+            if x is not None and (x.dtype != torch.float32 or not x.is_contiguous() or x.dim() not in (1, 2)):
+                raise ValueError(f"{name}: a contiguous fp32 tensor [groups, width] or [width]")
+        if weight is not None and bias is not None and weight.shape != bias.shape:
+            raise ValueError("weight and bias: of one shape")
+        if act not in ACT:
+            raise ValueError(f"act: one of {tuple(ACT)}")
+        self.weight, self.bias, self.eps, self.act = weight, bias, float(eps), act
+        self.centred, self.gate_first = bool(centred), bool(gate_first)
+
+
+def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optional[torch.Tensor] = None,
+               stream=None) -> int:
+    """y = the group norm of x [rows, groups, width] (bf16 or fp32, rows at any
+    stride of whole 16 bytes), gated; y may be x.  Returns the library's
+    code."""
+    act = next((k for k, v in TORCH_DTYPE.items() if v == x.dtype), None)
+    if x.dim() != 3 or act is None or x.device.type != "cuda":
+        raise ValueError("x: a bf16 or fp32 device tensor [rows, groups, width]")
+    shape, dev = tuple(x.shape), x.device
+    xs, ys = _rows("x", x, shape, x.dtype, dev), _rows("y", y, shape, x.dtype, dev)
+    zs = _rows("gate", gate, shape, x.dtype, dev) if gate is not None else 0
+    w = norm.weight if norm.weight is not None else norm.bias
+    for name, t in (("weight", norm.weight), ("bias", norm.bias)):
+        if t is not None and (tuple(t.shape) not in (shape[1:], shape[2:]) or t.device != dev):
+            raise ValueError(f"{name}: {shape[1:]} or {shape[2:]} on {dev}, got {tuple(t.shape)} on {t.device}")
+    st = abi.sketchssm_norm(_ptr(x), _ptr(gate), _ptr(y), _ptr(norm.weight), _ptr(norm.bias), xs, zs, ys,
+                            shape[0], shape[1], shape[2], DTYPE[act], int(w is not None and w.dim() == 2),
+                            int(norm.centred), ACT[norm.act], int(norm.gate_first), norm.eps)
+    with torch.cuda.device(dev):
+        return abi.sketchssm_group_norm(st, _stream_of(stream))
