@@ -1,0 +1,112 @@
+// Prompts through the gated delta rule in chunks of 64 tokens (bf16
+// activations).  With alpha_i, beta_i of a chunk's tokens, g_i the product of
+// the decays up to token i, D_ij the product of those after j up to i (so that
+// no quotient of decays occurs), and S_0 the state before the chunk:
+//   A_ij = beta_i D_ij (k_i . k_j)  for j < i,       T = (I + A)^-1 diag(beta)
+//   P_ij = D_ij (q_i . k_j)         for j <= i
+//   R = V - diag(g) K S_0,   U = T R
+//   O = diag(g) Q S_0 + P U,   S <- g_C S_0 + K^T diag(D_C) U
+// T and P do not depend on the state: one launch forms them for every chunk of
+// every prompt and head at once; a second goes through each prompt's chunks in
+// order.
+//
+// Precision.  The state is fp32, and so must be what is added to it.  Products
+// run on the bf16 matrix cores with each fp32 operand as an exact sum of three
+// bf16 values (its top 8 bits, the next 8, the last 8): a product with bf16
+// data (K, K^T) takes three instructions, one of two fp32 operands (T R) the
+// six whose terms reach 2^-24 of it.  What only reaches the output, which is
+// rounded to bf16 at 2^-9, takes the first two values (2^-16).  The fp32 matrix
+// instructions have a sixteenth of the bf16 ones' rate.
+#pragma once
+
+#include "sk_serve_device.hpp"
+
+namespace sk {
+
+constexpr int PC = PROMPT_CHUNK;                 // tokens of a chunk
+constexpr int FRAGS = 6;                         // fragments of a lower-triangular 64 x 64 operand
+constexpr int FRAG_BYTES = 1024;                 // 64 lanes x 8 bf16
+constexpr int T_BYTES = FRAGS * 3 * FRAG_BYTES, P_BYTES = FRAGS * 2 * FRAG_BYTES;
+// workspace of a chunk and head: the fragments of T (three values each), then
+// of P (two), then g [64] and D_C [64] in fp32
+constexpr int CHUNK_WORK_BYTES = T_BYTES + P_BYTES + 2 * PC * 4;
+static_assert(PC == 64 && CHUNK_WORK_BYTES == PROMPT_CHUNK_WORK, "workspace of a chunk");
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ bf16x8 as_frag(const u32x4& x) { return __builtin_bit_cast(bf16x8, x); }
+
+// The chunk slot that prompt i's first chunk has: prompts that are behind one
+// another never share a slot, and there are at most tokens / 64 + nseq.
+__device__ __forceinline__ int first_slot(int start, int i) { return (start >> 6) + i; }
+
+// Matrix instruction for waves of CW columns, and where its operands lie.  A
+// block of 32 rows x CW columns is NB registers of a lane, and register r is
+// row index(lane, r): eight consecutive rows for each step of the k axis, which
+// is the B operand of the next product as it stands.  For that the rows that
+// go into the A operand are permuted: MFMA row m of tile t is row(m, t).
+template <int CW> struct Mf;
+template <> struct Mf<32> {
+  typedef f32x16 Acc;
+  static constexpr int MT = 32, KS = 16, TILES = 1, STEPS = 2, NB = 16;
+  static __device__ __forceinline__ Acc mm(bf16x8 a, bf16x8 b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ int row(int m, int) {
+    return (m & 19) | ((m & 4) << 1) | ((m & 8) >> 1);
+  }
+  static __device__ __forceinline__ int index(int lane, int r) { return 16 * (r >> 3) + 8 * (lane >> 5) + (r & 7); }
+  static __device__ __forceinline__ int swizzle(int row) { return row & 15; }
+};
+template <> struct Mf<16> {
+  typedef f32x4s Acc;
+  static constexpr int MT = 16, KS = 32, TILES = 2, STEPS = 1, NB = 8;
+  static __device__ __forceinline__ Acc mm(bf16x8 a, bf16x8 b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ int row(int m, int t) { return ((m & 12) << 1) | (t << 2) | (m & 3); }
+  static __device__ __forceinline__ int index(int lane, int r) { return 8 * (lane >> 4) + r; }
+  static __device__ __forceinline__ int swizzle(int row) { return (row & 3) | ((row >> 1) & 12); }
+};
+
+// Row and first k index, within a 32 x 32 block, of lane's part of fragment f
+// (0 or 1: the tile or the step) of that block.
+template <int CW>
+__device__ __forceinline__ void frag_at(int lane, int f, int* row, int* k) {
+  using M = Mf<CW>;
+  const int t = M::TILES == 2 ? f : 0, s = M::STEPS == 2 ? f : 0;
+  *row = M::row(lane % M::MT, t);
+  *k = s * M::KS + 8 * (lane / M::MT);
+}
+
+// Eight fp32 values as bf16 fragments whose sum they are (three: exactly; the
+// first two leave at most 2^-16 of a value).
+__device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
+  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+__device__ __forceinline__ float below(float x) {    // x less its top 8 bits
+  return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+}
+template <int TERMS>
+__device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[TERMS]) {
+  float r[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = x[e];
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) {
+    u32x4 w;
+    w.x = high_halves(r[0], r[1]);
+    w.y = high_halves(r[2], r[3]);
+    w.z = high_halves(r[4], r[5]);
+    w.w = high_halves(r[6], r[7]);
+    out[t] = as_frag(w);
+    if (t + 1 < TERMS) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = below(r[e]);
+    }
+  }
+}
+
+}  // namespace sk

@@ -53,11 +53,9 @@ __global__ void __launch_bounds__(DV * 2) prompt_step_kernel(PromptParams p) {
   __shared__ __align__(16) float s_k[TB * DK], s_q[TB * DK], s_v[TB * DV], s_ab[2 * TB];
 
   const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H;
-  // a prompt of another length belongs to the other form's launch (which
-  // reports it where its range is not valid)
-  const int len0 = p.start[i + 1] - p.start[i];
-  if (len0 < p.len_lo && len0 >= 0) return;
-  if (len0 > p.len_hi) return;
+  // a longer prompt belongs to the chunked form's launch (which reports it
+  // where its range is not valid)
+  if ((int64_t)p.start[i + 1] - p.start[i] > p.len_hi) return;
   const PromptTile t = prompt_tile(p, i, h);
   if (!t.ok) return;
 

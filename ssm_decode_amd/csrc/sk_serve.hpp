@@ -26,7 +26,7 @@ struct SketchOut {
 struct PromptParams {
   int B, H;
   int tokens, nseq;
-  int len_lo, len_hi;       // prompts of this many tokens are taken by the launch
+  int len_lo, len_hi;       // the launch takes prompts of more than len_lo and up to len_hi tokens
   int nslots;               // chunk slots of the workspace (chunked form)
   const void* q;
   const void* k;
@@ -73,6 +73,15 @@ struct NormParams {
   float eps;
 };
 
+// Chunked form (bf16 activations): tokens of a chunk, workspace of a chunk and
+// head, and whether the shape has it.
+constexpr int PROMPT_CHUNK = 64;
+constexpr int PROMPT_CHUNK_WORK = 30 * 1024 + 512;
+inline bool prompt_chunked(int dk, int act) { return act == DT_BF16 && dk >= 64; }
+// Chunk slots that nseq prompts of together up to `tokens` tokens may take.
+inline int64_t prompt_slots(int64_t tokens, int64_t nseq) { return tokens / PROMPT_CHUNK + nseq; }
+
+int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st);
 int launch_prompt_step(int dk, int dv, int act, const PromptParams& p, hipStream_t st);
 int launch_state_save(int dk, int dv, const CacheParams& p, hipStream_t st);
 int launch_state_load(int dk, int dv, int sketch, const CacheParams& p, hipStream_t st);

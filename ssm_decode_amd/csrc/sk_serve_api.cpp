@@ -13,6 +13,13 @@ namespace {
 
 constexpr int kMaxWidth = 8192;
 
+// Prompts of up to this many tokens go token by token where the launch has
+// both kinds.
+constexpr int kShort = 16;
+bool chunks(const sketchssm_layer* L, int32_t tokens) {
+  return sk::prompt_chunked(L->dk, L->act_dtype) && tokens > kShort;
+}
+
 bool aligned(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // A row stride whose rows stay 16-byte aligned and do not overlap.
@@ -90,7 +97,10 @@ int64_t sketchssm_prefill_workspace_bytes(const sketchssm_layer* layer, int32_t 
   try {
     if (int rc = check_layer(layer)) return rc;
     if (layer->family != SKSSM_GDN || tokens < 0 || nseq < 0 || nseq > layer->batch) return SKSSM_EDIM;
-    return 0;
+    if (!chunks(layer, tokens)) return 0;
+    const int64_t tiles = sk::prompt_slots(tokens, nseq) * layer->heads;
+    if (tiles > INT32_MAX / 2) return SKSSM_EDIM;
+    return tiles * sk::PROMPT_CHUNK_WORK;
   } catch (...) {
     return SKSSM_ELAUNCH;
   }
@@ -148,9 +158,18 @@ int sketchssm_prefill(const sketchssm_layer* layer, const sketchssm_buffers* buf
     p.prime = pr->prime;
     if (pr->prime) fill_sketch(&p.sk, layer, bufs);
     p.work = pr->work;
-    p.len_lo = 0;
+    hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
     p.len_hi = INT32_MAX;
-    return sk::launch_prompt_step(dk, dv, layer->act_dtype, p, reinterpret_cast<hipStream_t>(hip_stream));
+    if (chunks(layer, pr->tokens)) {
+      // mostly long prompts: the chunked form takes the short ones too, and one
+      // launch is saved; otherwise the two share them by their lengths
+      const bool all = pr->tokens > (int64_t)sk::PROMPT_CHUNK * pr->nseq;
+      p.nslots = (int)sk::prompt_slots(pr->tokens, pr->nseq);
+      p.len_lo = all ? -1 : kShort;
+      if ((rc = sk::launch_prompt_chunks(dk, dv, p, st)) || all) return rc;
+      p.len_hi = kShort;
+    }
+    return sk::launch_prompt_step(dk, dv, layer->act_dtype, p, st);
   } catch (...) {
     return SKSSM_ELAUNCH;
   }

@@ -18,10 +18,11 @@ __device__ __forceinline__ bool listed_before(const int32_t* list, int i, int id
 }
 
 // The sequence, first token and length of prompt i, checked: an index
-// outside the batch, a range outside the tokens, or a sequence that an
-// earlier prompt of the list has (the earlier one keeps it) reports
-// ERRBIT_SEQ; a tile whose ring still holds entries ERRBIT_COUNT.  ok is
-// uniform over the workgroup.
+// outside the batch, a range outside the tokens or not behind those of the
+// prompts before it (so that no two prompts share tokens or chunk slots), or
+// a sequence that an earlier prompt of the list has (the earlier one keeps
+// it) reports ERRBIT_SEQ; a tile whose ring still holds entries
+// ERRBIT_COUNT.  ok is uniform over the workgroup.
 struct PromptTile {
   int b, s0, len;
   bool ok;
@@ -30,16 +31,22 @@ __device__ __forceinline__ PromptTile prompt_tile(const PromptParams& p, int i, 
   PromptTile t;
   t.s0 = p.start[i];
   const int s1 = p.start[i + 1];
-  t.len = s1 - t.s0;
   t.b = p.seqs ? p.seqs[i] : i;
   int bad = 0;
   if (t.b < 0 || t.b >= p.B || t.s0 < 0 || s1 < t.s0 || s1 > p.tokens) {
     bad = ERRBIT_SEQ;
-  } else {
-    if (p.seqs && listed_before(p.seqs, i, t.b)) bad = ERRBIT_SEQ;
-    if (!bad && p.count[(size_t)t.b * p.H + h] != 0) bad = ERRBIT_COUNT;
+  } else if (p.nseq > 1) {
+    int wrong = 0;
+    for (int j = threadIdx.x; j <= p.nseq; j += blockDim.x) {
+      const int s = p.start[j];
+      wrong |= j < i ? s > t.s0 : j > i + 1 ? s < s1 : 0;
+      if (p.seqs && j < i) wrong |= p.seqs[j] == t.b;
+    }
+    if (__syncthreads_or(wrong)) bad = ERRBIT_SEQ;
   }
+  if (!bad && p.count[(size_t)t.b * p.H + h] != 0) bad = ERRBIT_COUNT;
   if (bad && threadIdx.x == 0) atomicOr(p.err, bad);
+  t.len = s1 - t.s0;
   t.ok = bad == 0;
   return t;
 }
