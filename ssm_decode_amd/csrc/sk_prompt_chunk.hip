@@ -242,33 +242,57 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
 
 // ------------------------------------------------------ chunk after chunk
 // One workgroup of four waves per (prompt, head, part of the columns); a wave
-// holds CW columns of the state, all rows, in registers.  K, Q, K^T, T and P
-// are staged in LDS for the four waves; the next chunk's loads are in flight
-// over the present one.
-template <int DK, int DV, int CW>
+// holds CW columns of the state, all rows, in registers.  K, Q, V, T and P
+// are in LDS twice: the next chunk's copy, straight from memory, is in flight
+// over the present chunk.  K^T comes from K by transposing reads.
+template <int DK, int CW>
 struct ChunkLds {
   static constexpr int VC = 4 * CW;              // columns of the workgroup
   static constexpr int K = 0;
   static constexpr int Q = K + PC * DK * 2;
-  static constexpr int KT = Q + PC * DK * 2;
-  static constexpr int V = KT + PC * DK * 2;     // wave after wave: [64][CW], then the outputs
+  static constexpr int V = Q + PC * DK * 2;      // wave after wave: [64][CW], then the outputs [CW][64]
   static constexpr int W = V + PC * VC * 2;      // a chunk's workspace as it is
-  static constexpr int BYTES = W + CHUNK_WORK_BYTES;
+  static constexpr int BUF = W + (CHUNK_WORK_BYTES + 1023) / 1024 * 1024;
+  static constexpr int BYTES = 2 * BUF;
+  static_assert(BYTES <= 160 * 1024, "LDS of a CU");
 };
+
+// 16 bytes of each active lane from memory to LDS at lds + 16 * lane, in
+// flight until the wave's next wait for its memory counter.  (The compiler
+// would have every LDS read wait for a copy that it knows of, also where the
+// two are in different buffers.)
+__device__ __forceinline__ void copy16(const void* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(reinterpret_cast<uint64_t>(g)),
+               "s"(lds)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+// Within each 16 lanes, lane i gives the address of four values: 4 rows (i / 4)
+// of 16 (4 (i % 4) ..); it receives column i of the four rows.
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bf16x4 read_tr(const void* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+      (__attribute__((address_space(3))) bf16x4*)const_cast<void*>(p));
+}
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
 
 template <int DK, int DV, int CW>
 __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   using M = Mf<CW>;
-  using L = ChunkLds<DK, DV, CW>;
+  using L = ChunkLds<DK, CW>;
   typedef typename M::Acc Acc;
   constexpr int VC = L::VC, PARTS = DV / VC, PPR = DK / 8, NB = M::NB, DB = DK / 32;
   constexpr int AR = NB / M::TILES;              // registers of a tile
-  __shared__ __align__(16) unsigned char smem[L::BYTES];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  int bid = blockIdx.x;
-  const int part = bid % PARTS;
-  bid /= PARTS;
-  const int i = bid / p.H, h = bid - i * p.H;
+  __shared__ __align__(1024) unsigned char smem[L::BYTES];
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // (the parts of a tile are a multiple of nseq * H workgroups apart: mostly
+  // on the same XCD, whose cache then serves the K, Q, T and P that they share)
+  const int tiles = p.nseq * p.H, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
+  const int i = tile / p.H, h = tile - i * p.H;
   if ((int64_t)p.start[i + 1] - p.start[i] <= p.len_lo) return;
   const PromptTile pt = prompt_tile(p, i, h);
   if (!pt.ok) return;
@@ -276,6 +300,46 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   const int n = lane % M::MT, hi = lane / M::MT;           // column, part of the k axis
   const int col = part * VC + wv * CW + n;
   float* Sg = p.S + ((size_t)pt.b * p.H + h) * DK * DV + col;
+
+  const bf16* kp = reinterpret_cast<const bf16*>(p.k) + pt.s0 * p.ks + (int64_t)h * DK;
+  const bf16* qp = reinterpret_cast<const bf16*>(p.q) + pt.s0 * p.qs + (int64_t)h * DK;
+  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + pt.s0 * p.vs + (int64_t)h * DV + part * VC + wv * CW;
+  bf16* op = reinterpret_cast<bf16*>(p.o) + pt.s0 * p.os + (int64_t)h * DV + part * VC + wv * CW;
+  const unsigned char* wp = reinterpret_cast<const unsigned char*>(p.work) +
+                            ((size_t)first_slot(pt.s0, i) * p.H + h) * CHUNK_WORK_BYTES;
+
+  // rows of K and Q with their 16-byte pieces swizzled
+  auto swz = [](int row) { return (PPR == 16 ? M::swizzle(row) : M::swizzle(row) >> 1) & (PPR - 1); };
+  auto piece = [&](int row, int pc) { return row * PPR + (pc ^ swz(row)); };
+  // A chunk's copies, in units of 64 pieces that the waves share out.  Rows
+  // behind the prompt's end repeat its last: their beta in T is 0, their
+  // columns of P meet only zeros, and their outputs are not stored.
+  const uint32_t lds0 = lds_address(smem);
+  constexpr int VPR = CW / 8, WU = (CHUNK_WORK_BYTES / 16 + 63) / 64;
+  auto copies = [&](int t0, int nt, int buf) {
+    const uint32_t l0 = lds0 + buf * L::BUF;
+#pragma unroll
+    for (int u = 0; u < PPR / 4; ++u) {
+      const int unit = 4 * u + wv, c = 64 * unit + lane, row = c / PPR, pc = (c % PPR) ^ swz(row);
+      const int64_t t = t0 + (row < nt ? row : nt - 1);
+      copy16(kp + t * p.ks + pc * 8, l0 + L::K + unit * 1024);
+      copy16(qp + t * p.qs + pc * 8, l0 + L::Q + unit * 1024);
+    }
+#pragma unroll
+    for (int u = 0; u < VPR; ++u) {
+      const int c = 64 * u + lane, row = c / VPR;
+      const int64_t t = t0 + (row < nt ? row : nt - 1);
+      copy16(vp + t * p.vs + (c % VPR) * 8, l0 + L::V + wv * PC * CW * 2 + u * 1024);
+    }
+    const unsigned char* w = wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES;
+#pragma unroll
+    for (int u = 0; u < (WU + 3) / 4; ++u) {
+      const int unit = 4 * u + wv;
+      if (unit * 1024 + lane * 16 < CHUNK_WORK_BYTES) copy16(w + unit * 1024 + lane * 16, l0 + L::W + unit * 1024);
+    }
+  };
+  int nt = pt.len < PC ? pt.len : PC;
+  if (pt.len > 0) copies(0, nt, 0);
 
   // the state, block after block of 32 rows
   Acc S[DB][M::TILES];
@@ -286,246 +350,248 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
     for (int r = 0; r < NB; ++r)
       S[db][r / AR][r % AR] = cont ? Sg[(size_t)(32 * db + M::index(lane, r)) * DV] : 0.f;
 
-  // staging: a thread takes eight columns of four consecutive tokens of K (so
-  // that it can write K^T in runs of four tokens), any pieces of the rest
-  const bf16* kp = reinterpret_cast<const bf16*>(p.k) + pt.s0 * p.ks + (int64_t)h * DK;
-  const bf16* qp = reinterpret_cast<const bf16*>(p.q) + pt.s0 * p.qs + (int64_t)h * DK;
-  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + pt.s0 * p.vs + (int64_t)h * DV + part * VC + wv * CW;
-  bf16* op = reinterpret_cast<bf16*>(p.o) + pt.s0 * p.os + (int64_t)h * DV + part * VC + wv * CW;
-  const unsigned char* wp = reinterpret_cast<const unsigned char*>(p.work) +
-                            ((size_t)first_slot(pt.s0, i) * p.H + h) * CHUNK_WORK_BYTES;
-  constexpr int KT4 = PC * PPR / 4 / 256 > 0 ? PC * PPR / 4 / 256 : 1;   // groups of four tokens a thread
-  constexpr int QU = PC * PPR / 256;
-  constexpr int VPR = CW / 8, VU = PC * VPR / 64;                         // pieces of a row, of a lane
-  constexpr int WU = (CHUNK_WORK_BYTES / 16 + 255) / 256;
-  constexpr bool KALL = PC * PPR / 4 >= 256;
-  u32x4 rk[KT4][4], rq[QU], rv[VU], rw[WU];
-  const u32x4 none = u32x4{0, 0, 0, 0};
-  auto fetch = [&](int t0, int nt) {
-#pragma unroll
-    for (int u = 0; u < KT4; ++u) {
-      const int c = tid + 256 * u, t4 = c / PPR * 4, pc = c % PPR;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        rk[u][e] = none;
-        if ((KALL || t4 < PC) && t4 + e < nt)
-          rk[u][e] = *reinterpret_cast<const u32x4*>(kp + (t0 + t4 + e) * p.ks + pc * 8);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < QU; ++u) {
-      const int c = tid + 256 * u, t = c / PPR, pc = c % PPR;
-      rq[u] = none;
-      if (t < nt) rq[u] = *reinterpret_cast<const u32x4*>(qp + (t0 + t) * p.qs + pc * 8);
-    }
-#pragma unroll
-    for (int u = 0; u < VU; ++u) {
-      const int c = lane + 64 * u, t = c / VPR, pc = c % VPR;
-      rv[u] = none;
-      if (t < nt) rv[u] = *reinterpret_cast<const u32x4*>(vp + (t0 + t) * p.vs + pc * 8);
-    }
-    const u32x4* w = reinterpret_cast<const u32x4*>(wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES);
-#pragma unroll
-    for (int u = 0; u < WU; ++u) {
-      const int c = tid + 256 * u;
-      rw[u] = w[c < CHUNK_WORK_BYTES / 16 ? c : 0];
-    }
-  };
-  u32x4* s_k = reinterpret_cast<u32x4*>(smem + L::K);
-  u32x4* s_q = reinterpret_cast<u32x4*>(smem + L::Q);
-  unsigned char* s_kt = smem + L::KT;
-  bf16* s_v = reinterpret_cast<bf16*>(smem + L::V) + wv * PC * CW;
-  u32x4* s_w = reinterpret_cast<u32x4*>(smem + L::W);
-  const float* s_g = reinterpret_cast<const float*>(smem + L::W + T_BYTES + P_BYTES);
-  auto piece = [](int row, int pc) {
-    return row * PPR + (pc ^ ((PPR == 16 ? M::swizzle(row) : M::swizzle(row) >> 1) & (PPR - 1)));
-  };
-  // K^T rows of 64 tokens (128 bytes, eight pieces): swizzled so that both the
-  // writes (rows eight apart) and the reads (neighbouring rows) spread
-  auto kt_piece = [](int d, int pc) { return d * 8 + (pc ^ (((d >> 1) ^ (d >> 4)) & 7)); };
-  auto stage = [&]() {
-#pragma unroll
-    for (int u = 0; u < KT4; ++u) {
-      const int c = tid + 256 * u, t4 = c / PPR * 4, pc = c % PPR;
-      if (KALL || t4 < PC) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s_k[piece(t4 + e, pc)] = rk[u][e];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          auto word = [&](int a) {
-            const u32x4& x = rk[u][a];
-            return e < 2 ? x.x : e < 4 ? x.y : e < 6 ? x.z : x.w;
-          };
-          const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
-          const uint2 w = make_uint2(__builtin_amdgcn_perm(word(1), word(0), sel),
-                                     __builtin_amdgcn_perm(word(3), word(2), sel));
-          *reinterpret_cast<uint2*>(s_kt + kt_piece(8 * pc + e, t4 >> 3) * 16 + (t4 & 4) * 2) = w;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < QU; ++u) {
-      const int c = tid + 256 * u;
-      s_q[piece(c / PPR, c % PPR)] = rq[u];
-    }
-#pragma unroll
-    for (int u = 0; u < VU; ++u) reinterpret_cast<u32x4*>(s_v)[lane + 64 * u] = rv[u];
-#pragma unroll
-    for (int u = 0; u < WU; ++u) {
-      const int c = tid + 256 * u;
-      if (c < CHUNK_WORK_BYTES / 16) s_w[c] = rw[u];
-    }
-  };
-
   int arow[2], ak[2];
 #pragma unroll
   for (int f = 0; f < 2; ++f) frag_at<CW>(lane, f, &arow[f], &ak[f]);
-  // fragment f of block (rb, kb) of a row-major operand
-  auto frag_k = [&](const u32x4* s, int rb, int kb, int f) { return as_frag(s[piece(32 * rb + arow[f], (32 * kb + ak[f]) >> 3)]); };
-  auto frag_kt = [&](int rb, int kb, int f) {
-    return as_frag(reinterpret_cast<const u32x4*>(s_kt)[kt_piece(32 * rb + arow[f], (32 * kb + ak[f]) >> 3)]);
+  const unsigned char* sb = smem;                // the present chunk's buffer
+  // fragment f of block (rb, kb) of K or Q
+  auto frag_k = [&](int at, int rb, int kb, int f) {
+    return as_frag(reinterpret_cast<const u32x4*>(sb + at)[piece(32 * rb + arow[f], (32 * kb + ak[f]) >> 3)]);
   };
-  auto frag_t = [&](int f, int term) { return as_frag(s_w[(f * 3 + term) * 64 + lane]); };
-  auto frag_p = [&](int f, int term) { return as_frag(s_w[T_BYTES / 16 + (f * 2 + term) * 64 + lane]); };
+  // of K^T: eight tokens from 32 kb + ak of the rows that the lane's group of 16
+  // gives the addresses of: lane i those of tokens i / 4 and i / 4 + 4
+  const int ti = (lane & 15) >> 2, tc = 4 * (lane & 3), tg = M::MT == 32 ? lane & 16 : 0;
+  auto frag_kt = [&](int rb, int kb, int f) {
+    const int d = 32 * rb + M::row(tg + tc, M::TILES == 2 ? f : 0), t = 32 * kb + ak[f] + ti;
+    const unsigned char* s = sb + L::K + (d & 7) * 2;
+    return join(read_tr(s + piece(t, d >> 3) * 16), read_tr(s + piece(t + 4, d >> 3) * 16));
+  };
+  auto frag_t = [&](int f, int term) { return as_frag(reinterpret_cast<const u32x4*>(sb + L::W)[(f * 3 + term) * 64 + lane]); };
+  auto frag_p = [&](int f, int term) {
+    return as_frag(reinterpret_cast<const u32x4*>(sb + L::W + T_BYTES)[(f * 2 + term) * 64 + lane]);
+  };
   auto block8 = [&](const Acc (&a)[M::TILES], int s, float (&x)[8]) {    // the B operand of step s
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = a[(8 * s + e) / AR][(8 * s + e) % AR];
   };
+  // the wave's outputs of a chunk, as whole rows: lane's 8 columns of OU tokens
+  constexpr int OU = NB / 8 * 2, OG = CW / 8;    // OG column groups, 4 / OG groups of 16 tokens at a time
+  u32x4 out[OU];
+  const int og = (lane >> 4) % OG, ot = (lane >> 4) / OG * 16 + (lane & 15);
+  auto store_out = [&](int t0, int cnt) {
+#pragma unroll
+    for (int u = 0; u < OU; ++u) {
+      const int t = ot + u * (64 / OG);
+      if (t < cnt) *reinterpret_cast<u32x4*>(op + (int64_t)(t0 + t) * p.os + og * 8) = out[u];
+    }
+  };
 
-  int nt = pt.len < PC ? pt.len : PC;
-  fetch(0, nt);
-  for (int t0 = 0; t0 < pt.len; t0 += PC) {
-    stage();
+  int t0 = 0;
+  for (int buf = 0; t0 < pt.len; t0 += PC, buf ^= 1) {
+    // this wave's copies for the chunk have landed, then everybody's; and
+    // everybody has read the other buffer
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    const int now = nt, left = pt.len - t0 - PC;
+    sb = smem + buf * L::BUF;
+    if (t0 > 0) store_out(t0 - PC, PC);
+    const int left = pt.len - t0 - PC;
     if (left > 0) {
       nt = left < PC ? left : PC;
-      fetch(t0 + PC, nt);
+      copies(t0 + PC, nt, buf ^ 1);
     }
+    const float* s_g = reinterpret_cast<const float*>(sb + L::W + T_BYTES + P_BYTES);
+    unsigned char* s_v = smem + buf * L::BUF + L::V + wv * PC * CW * 2;
 
-    // K S and Q S
-    Acc R[2][M::TILES], O[2][M::TILES];
+    // Each step of a product (KS values of its k axis) has its A fragments read
+    // from LDS and its B operand split during the step before, so that neither
+    // LDS latency nor vector work stands between two steps' matrix
+    // instructions; the barriers keep the compiler from undoing that.
+    constexpr int NF = M::TILES, J1 = DB * M::STEPS, J2 = 2 * M::STEPS;
+    Acc R[2][NF], O[2][NF], U[2][NF];
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-      for (int t = 0; t < M::TILES; ++t)
+      for (int t = 0; t < NF; ++t)
 #pragma unroll
-        for (int r = 0; r < AR; ++r) R[rb][t][r] = O[rb][t][r] = 0.f;
+        for (int r = 0; r < AR; ++r) R[rb][t][r] = O[rb][t][r] = U[rb][t][r] = 0.f;
+    bf16x8 ft[2][2][NF][3];                              // T fragments: [step parity][rb][tile][value]
+    bf16x8 b[2][3];
+    auto load_t = [&](int j) {
+      const int kb = j / M::STEPS, sp = j % M::STEPS;
 #pragma unroll
-    for (int kb = 0; kb < DB; ++kb)
+      for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-      for (int s = 0; s < M::STEPS; ++s) {
-        float x[8];
-        bf16x8 b[3];
-        block8(S[kb], s, x);
-        split8<3>(x, b);
+        for (int t = 0; t < NF; ++t)
+          if (rb >= kb) {
+#pragma unroll
+            for (int v = 0; v < 3; ++v) ft[j & 1][rb][t][v] = frag_t((rb + kb) * 2 + (NF == 2 ? t : sp), v);
+          }
+    };
+    {  // K S and Q S
+      bf16x8 fk[2][2][NF], fq[2][2][NF];
+      auto load_kq = [&](int j) {
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-          for (int t = 0; t < M::TILES; ++t) {
-            const int f = M::TILES == 2 ? t : s;
-            const bf16x8 fk = frag_k(s_k, rb, kb, f), fq = frag_k(s_q, rb, kb, f);
-            R[rb][t] = M::mm(fk, b[0], R[rb][t]);
-            O[rb][t] = M::mm(fq, b[0], O[rb][t]);
-            R[rb][t] = M::mm(fk, b[1], R[rb][t]);
-            O[rb][t] = M::mm(fq, b[1], O[rb][t]);
-            R[rb][t] = M::mm(fk, b[2], R[rb][t]);
+          for (int t = 0; t < NF; ++t) {
+            fk[j & 1][rb][t] = frag_k(L::K, rb, j / M::STEPS, NF == 2 ? t : j % M::STEPS);
+            fq[j & 1][rb][t] = frag_k(L::Q, rb, j / M::STEPS, NF == 2 ? t : j % M::STEPS);
           }
+      };
+      auto split_s = [&](int j) {
+        float x[8];
+        block8(S[j / M::STEPS], j % M::STEPS, x);
+        split8<3>(x, b[j & 1]);
+      };
+      load_kq(0);
+      split_s(0);
+#pragma unroll
+      for (int j = 0; j < J1; ++j) {
+        if (j + 1 < J1) {
+          load_kq(j + 1);
+          split_s(j + 1);
+        } else {
+          load_t(0);
+        }
+#pragma unroll
+        for (int v = 0; v < 3; ++v)
+#pragma unroll
+          for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+            for (int t = 0; t < NF; ++t) {
+              R[rb][t] = M::mm(fk[j & 1][rb][t], b[j & 1][v], R[rb][t]);
+              if (v < 2) O[rb][t] = M::mm(fq[j & 1][rb][t], b[j & 1][v], O[rb][t]);
+            }
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
     // R = V - g (K S);  O = g (Q S)
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-      for (int r = 0; r < NB; ++r) {
-        const int t = 32 * rb + M::index(lane, r);
-        const float gam = s_g[t];
-        R[rb][r / AR][r % AR] = to_f32(s_v[t * CW + n]) - gam * R[rb][r / AR][r % AR];
-        O[rb][r / AR][r % AR] *= gam;
+      for (int s8 = 0; s8 < NB / 8; ++s8) {
+        // V's column n, eight tokens: as K^T, from rows of CW values
+        const int tk = 32 * rb + M::index(lane, 8 * s8);
+        const unsigned char* sv = s_v + ((tk + ti) * CW + tg + tc) * 2;
+        const bf16x8 v8 = join(read_tr(sv), read_tr(sv + 4 * CW * 2));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = 8 * s8 + e;
+          const float gam = s_g[tk + e];
+          R[rb][r / AR][r % AR] = (float)v8[e] - gam * R[rb][r / AR][r % AR];
+          O[rb][r / AR][r % AR] *= gam;
+        }
       }
-    // U = T R
-    Acc U[2][M::TILES];
-#pragma unroll
-    for (int rb = 0; rb < 2; ++rb)
-#pragma unroll
-      for (int t = 0; t < M::TILES; ++t)
-#pragma unroll
-        for (int r = 0; r < AR; ++r) U[rb][t][r] = 0.f;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int s = 0; s < M::STEPS; ++s) {
-        float x[8];
-        bf16x8 b[3];
-        block8(R[kb], s, x);
-        split8<3>(x, b);
-#pragma unroll
-        for (int rb = kb; rb < 2; ++rb)
-#pragma unroll
-          for (int t = 0; t < M::TILES; ++t) {
-            const int f = (rb + kb) * 2 + (M::TILES == 2 ? t : s);
-            const bf16x8 a0 = frag_t(f, 0), a1 = frag_t(f, 1), a2 = frag_t(f, 2);
-            U[rb][t] = M::mm(a0, b[2], U[rb][t]);
-            U[rb][t] = M::mm(a2, b[0], U[rb][t]);
-            U[rb][t] = M::mm(a1, b[1], U[rb][t]);
-            U[rb][t] = M::mm(a0, b[1], U[rb][t]);
-            U[rb][t] = M::mm(a1, b[0], U[rb][t]);
-            U[rb][t] = M::mm(a0, b[0], U[rb][t]);
-          }
-      }
-    // O += P U;  S = g_C S + K^T (D_C U)
     const float gC = s_g[PC - 1];
+    bf16x8 fp[2][2][NF][2], fs[2][DB][NF];
+    auto load_ps = [&](int j) {
+      const int kb = j / M::STEPS, sp = j % M::STEPS;
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+      for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-      for (int t = 0; t < M::TILES; ++t)
+        for (int t = 0; t < NF; ++t)
+          if (rb >= kb) {
 #pragma unroll
-        for (int r = 0; r < AR; ++r) S[db][t][r] *= gC;
+            for (int v = 0; v < 2; ++v) fp[j & 1][rb][t][v] = frag_p((rb + kb) * 2 + (NF == 2 ? t : sp), v);
+          }
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+      for (int db = 0; db < DB; ++db)
 #pragma unroll
-      for (int s = 0; s < M::STEPS; ++s) {
+        for (int t = 0; t < NF; ++t) fs[j & 1][db][t] = frag_kt(db, kb, NF == 2 ? t : sp);
+    };
+    {  // U = T R;  S = g_C S meanwhile
+      auto split_r = [&](int j) {
         float x[8];
-        bf16x8 b2[2], b[3];
-        block8(U[kb], s, x);
-        split8<2>(x, b2);
+        block8(R[j / M::STEPS], j % M::STEPS, x);
+        split8<3>(x, b[j & 1]);
+      };
+      split_r(0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= s_g[PC + 32 * kb + M::index(lane, 8 * s + e)];
-        split8<3>(x, b);
+      for (int j = 0; j < J2; ++j) {
+        if (j + 1 < J2) {
+          load_t(j + 1);
+          split_r(j + 1);
+        } else {
+          load_ps(0);
+        }
+        const int kb = j / M::STEPS;
+        constexpr int TA[6] = {0, 2, 1, 0, 1, 0}, TB[6] = {2, 0, 1, 1, 0, 0};   // the smaller products first
 #pragma unroll
-        for (int rb = kb; rb < 2; ++rb)
+        for (int v = 0; v < 6; ++v)
 #pragma unroll
-          for (int t = 0; t < M::TILES; ++t) {
-            const int f = (rb + kb) * 2 + (M::TILES == 2 ? t : s);
-            const bf16x8 a0 = frag_p(f, 0), a1 = frag_p(f, 1);
-            O[rb][t] = M::mm(a0, b2[1], O[rb][t]);
-            O[rb][t] = M::mm(a1, b2[0], O[rb][t]);
-            O[rb][t] = M::mm(a0, b2[0], O[rb][t]);
-          }
+          for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
+            for (int t = 0; t < NF; ++t)
+              if (rb >= kb) U[rb][t] = M::mm(ft[j & 1][rb][t][TA[v]], b[j & 1][TB[v]], U[rb][t]);
 #pragma unroll
-          for (int t = 0; t < M::TILES; ++t) {
-            const bf16x8 a = frag_kt(db, kb, M::TILES == 2 ? t : s);
-            S[db][t] = M::mm(a, b[2], S[db][t]);
-            S[db][t] = M::mm(a, b[1], S[db][t]);
-            S[db][t] = M::mm(a, b[0], S[db][t]);
-          }
+        for (int db = j * DB / J2; db < (j + 1) * DB / J2; ++db)
+#pragma unroll
+          for (int t = 0; t < NF; ++t)
+#pragma unroll
+            for (int r = 0; r < AR; ++r) S[db][t][r] *= gC;
+        __builtin_amdgcn_sched_barrier(0);
       }
-    // the outputs leave through the wave's own part of LDS as whole rows
+    }
+    {  // O += P U;  S += K^T (D_C U)
+      bf16x8 c[2][2];
+      auto split_u = [&](int j) {
+        float x[8];
+        block8(U[j / M::STEPS], j % M::STEPS, x);
+        split8<2>(x, c[j & 1]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= s_g[PC + 32 * (j / M::STEPS) + M::index(lane, 8 * (j % M::STEPS) + e)];
+        split8<3>(x, b[j & 1]);
+      };
+      split_u(0);
+#pragma unroll
+      for (int j = 0; j < J2; ++j) {
+        if (j + 1 < J2) {
+          load_ps(j + 1);
+          split_u(j + 1);
+        }
+        const int kb = j / M::STEPS;
+        constexpr int PA[3] = {0, 1, 0}, PB[3] = {1, 0, 0};
+#pragma unroll
+        for (int v = 0; v < 3; ++v) {
+#pragma unroll
+          for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+            for (int t = 0; t < NF; ++t)
+              if (rb >= kb) O[rb][t] = M::mm(fp[j & 1][rb][t][PA[v]], c[j & 1][PB[v]], O[rb][t]);
+        }
+#pragma unroll
+        for (int v = 2; v >= 0; --v)
+#pragma unroll
+          for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int t = 0; t < NF; ++t) S[db][t] = M::mm(fs[j & 1][db][t], b[j & 1][v], S[db][t]);
+        if (j + 1 < J2) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // the outputs, columns of 64 tokens (eight swizzled pieces), over the wave's
+    // part of V, and back as rows of eight columns by transposing reads
     wave_lds_sync();
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-      for (int r = 0; r < NB; ++r)
-        s_v[(32 * rb + M::index(lane, r)) * CW + n] = f32_to_bf16(O[rb][r / AR][r % AR]);
+      for (int s8 = 0; s8 < NB / 8; ++s8) {
+        bf16x8 w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = (__bf16)O[rb][(8 * s8 + e) / AR][(8 * s8 + e) % AR];
+        const int pc = (32 * rb + M::index(lane, 8 * s8)) >> 3;
+        *reinterpret_cast<bf16x8*>(s_v + n * 128 + (pc ^ (n & 7)) * 16) = w;
+      }
     wave_lds_sync();
 #pragma unroll
-    for (int u = 0; u < VU; ++u) {
-      const int c = lane + 64 * u, t = c / VPR, pc = c % VPR;
-      if (t < now) *reinterpret_cast<u32x4*>(op + (t0 + t) * p.os + pc * 8) = reinterpret_cast<const u32x4*>(s_v)[c];
+    for (int u = 0; u < OU; ++u) {
+      // lane i of a group: column 8 og + i / 4 (and + 4), tokens 4 (i % 4) ..
+      const int t = (lane >> 4) / OG * 16 + u * (64 / OG) + tc, c = 8 * og + ti;
+      auto at = [&](int cc) { return s_v + cc * 128 + ((t >> 3) ^ (cc & 7)) * 16 + (t & 7) * 2; };
+      out[u] = __builtin_bit_cast(u32x4, join(read_tr(at(c)), read_tr(at(c + 4))));
     }
-    __syncthreads();                             // every wave has read this chunk's operands
+    wave_lds_sync();
   }
+  if (pt.len > 0) store_out(t0 - PC, pt.len - (t0 - PC));
 
 #pragma unroll
   for (int db = 0; db < DB; ++db)
@@ -566,7 +632,7 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
 
 template <int DK, int DV, int CW>
 int launch(const PromptParams& p, hipStream_t st) {
-  using L = ChunkLds<DK, DV, CW>;
+  using L = ChunkLds<DK, CW>;
   hipLaunchKernelGGL((prompt_prep_kernel<DK, CW>), dim3((unsigned)p.nslots * p.H), dim3(256), 0, st, p);
   hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, CW>), dim3((unsigned)p.nseq * p.H * (DV / L::VC)), dim3(256), 0,
                      st, p);
