@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
 // holds CW columns of the state, all rows, in registers.  K, Q, V, T and P
 // are in LDS twice: the next chunk's copy, straight from memory, is in flight
 // over the present chunk.  K^T comes from K by transposing reads.
-template <int DK, int CW>
+template <int DK, int CW, int BUFS>
 struct ChunkLds {
   static constexpr int VC = 4 * CW;              // columns of the workgroup
   static constexpr int K = 0;
@@ -253,8 +253,8 @@ struct ChunkLds {
   static constexpr int V = Q + PC * DK * 2;      // wave after wave: [64][CW], then the outputs [CW][64]
   static constexpr int W = V + PC * VC * 2;      // a chunk's workspace as it is
   static constexpr int BUF = W + (CHUNK_WORK_BYTES + 1023) / 1024 * 1024;
-  static constexpr int BYTES = 2 * BUF;
-  static_assert(BYTES <= 160 * 1024, "LDS of a CU");
+  static constexpr int BYTES = BUFS * BUF;
+  static_assert(BYTES <= BUFS * 80 * 1024, "two workgroups of one buffer, or one of two, on a CU");
 };
 
 // 16 bytes of each active lane from memory to LDS at lds + 16 * lane, in
@@ -280,13 +280,28 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int DK, int DV, int CW>
-__global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
+// Asks for a step's instructions in the order: a matrix instruction, LDS reads
+// (of the next step's fragments), vector work (the next step's split), and so
+// on.  One wave's vector work runs in the shadow of its matrix instructions
+// only where it stands between them.
+template <int MFMAS, int READS, int VALU>
+__device__ __forceinline__ void interleave() {
+  if constexpr (MFMAS > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    interleave<MFMAS - 1, READS, VALU>();
+  }
+}
+
+template <int DK, int DV, int CW, int BUFS>
+__global__ void __launch_bounds__(256, 3 - BUFS) prompt_chunk_kernel(PromptParams p) {
   using M = Mf<CW>;
-  using L = ChunkLds<DK, CW>;
+  using L = ChunkLds<DK, CW, BUFS>;
   typedef typename M::Acc Acc;
   constexpr int VC = L::VC, PARTS = DV / VC, PPR = DK / 8, NB = M::NB, DB = DK / 32;
   constexpr int AR = NB / M::TILES;              // registers of a tile
+  constexpr int PIPE = BUFS - 1;                 // one wave a SIMD: it overlaps its own steps
   __shared__ __align__(1024) unsigned char smem[L::BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   // (the parts of a tile are a multiple of nseq * H workgroups apart: mostly
@@ -315,28 +330,45 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   // behind the prompt's end repeat its last: their beta in T is 0, their
   // columns of P meet only zeros, and their outputs are not stored.
   const uint32_t lds0 = lds_address(smem);
-  constexpr int VPR = CW / 8, WU = (CHUNK_WORK_BYTES / 16 + 63) / 64;
+  constexpr int VPR = CW / 8, KU = PPR / 4, KROWS = 256 / PPR, VROWS = 64 / VPR;
+  constexpr int WFULL = CHUNK_WORK_BYTES / 16 / 64, WREST = CHUNK_WORK_BYTES / 16 % 64;
+  const int krow = (wv * 64 + lane) / PPR, kpc = lane % PPR, vrow = lane / VPR;
+  const unsigned char* wp0 = wp + lane * 16 + wv * 1024;
   auto copies = [&](int t0, int nt, int buf) {
     const uint32_t l0 = lds0 + buf * L::BUF;
+    if (nt == PC) {                                        // uniform: a whole chunk
+      const bf16* kc = kp + (t0 + krow) * p.ks;
+      const bf16* qc = qp + (t0 + krow) * p.qs;
+      const bf16* vc = vp + (t0 + vrow) * p.vs + (lane % VPR) * 8;
 #pragma unroll
-    for (int u = 0; u < PPR / 4; ++u) {
-      const int unit = 4 * u + wv, c = 64 * unit + lane, row = c / PPR, pc = (c % PPR) ^ swz(row);
-      const int64_t t = t0 + (row < nt ? row : nt - 1);
-      copy16(kp + t * p.ks + pc * 8, l0 + L::K + unit * 1024);
-      copy16(qp + t * p.qs + pc * 8, l0 + L::Q + unit * 1024);
-    }
+      for (int u = 0; u < KU; ++u) {
+        const int pc = (kpc ^ swz(krow + KROWS * u)) * 8;
+        copy16(kc + (u * KROWS * p.ks + pc), l0 + L::K + (4 * u + wv) * 1024);
+        copy16(qc + (u * KROWS * p.qs + pc), l0 + L::Q + (4 * u + wv) * 1024);
+      }
 #pragma unroll
-    for (int u = 0; u < VPR; ++u) {
-      const int c = 64 * u + lane, row = c / VPR;
-      const int64_t t = t0 + (row < nt ? row : nt - 1);
-      copy16(vp + t * p.vs + (c % VPR) * 8, l0 + L::V + wv * PC * CW * 2 + u * 1024);
+      for (int u = 0; u < VPR; ++u)
+        copy16(vc + u * VROWS * p.vs, l0 + L::V + wv * PC * CW * 2 + u * 1024);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < KU; ++u) {
+        const int row = krow + KROWS * u, pc = (kpc ^ swz(row)) * 8;
+        const int64_t t = t0 + (row < nt ? row : nt - 1);
+        copy16(kp + t * p.ks + pc, l0 + L::K + (4 * u + wv) * 1024);
+        copy16(qp + t * p.qs + pc, l0 + L::Q + (4 * u + wv) * 1024);
+      }
+#pragma unroll 1
+      for (int u = 0; u < VPR; ++u) {
+        const int row = vrow + VROWS * u;
+        const int64_t t = t0 + (row < nt ? row : nt - 1);
+        copy16(vp + t * p.vs + (lane % VPR) * 8, l0 + L::V + wv * PC * CW * 2 + u * 1024);
+      }
     }
-    const unsigned char* w = wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES;
+    const unsigned char* w = wp0 + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES;
 #pragma unroll
-    for (int u = 0; u < (WU + 3) / 4; ++u) {
-      const int unit = 4 * u + wv;
-      if (unit * 1024 + lane * 16 < CHUNK_WORK_BYTES) copy16(w + unit * 1024 + lane * 16, l0 + L::W + unit * 1024);
-    }
+    for (int u = 0; u < WFULL / 4; ++u) copy16(w + u * 4096, l0 + L::W + (4 * u + wv) * 1024);
+    constexpr int U = WFULL / 4 * 4;
+    if (U + wv < WFULL || (U + wv == WFULL && lane < WREST)) copy16(w + U * 1024, l0 + L::W + (U + wv) * 1024);
   };
   int nt = pt.len < PC ? pt.len : PC;
   if (pt.len > 0) copies(0, nt, 0);
@@ -378,27 +410,26 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   constexpr int OU = NB / 8 * 2, OG = CW / 8;    // OG column groups, 4 / OG groups of 16 tokens at a time
   u32x4 out[OU];
   const int og = (lane >> 4) % OG, ot = (lane >> 4) / OG * 16 + (lane & 15);
+  bf16* op0 = op + ot * p.os + og * 8;
   auto store_out = [&](int t0, int cnt) {
 #pragma unroll
     for (int u = 0; u < OU; ++u) {
-      const int t = ot + u * (64 / OG);
-      if (t < cnt) *reinterpret_cast<u32x4*>(op + (int64_t)(t0 + t) * p.os + og * 8) = out[u];
+      if (ot + u * (64 / OG) < cnt)
+        *reinterpret_cast<u32x4*>(op0 + (int64_t)t0 * p.os + u * (64 / OG) * p.os) = out[u];
     }
   };
 
   int t0 = 0;
-  for (int buf = 0; t0 < pt.len; t0 += PC, buf ^= 1) {
-    // this wave's copies for the chunk have landed, then everybody's; and
-    // everybody has read the other buffer
+  for (int buf = 0; t0 < pt.len; t0 += PC, buf ^= PIPE) {
+    // this wave's copies for the chunk have landed, then everybody's; with two
+    // buffers, everybody has read the other
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     sb = smem + buf * L::BUF;
     if (t0 > 0) store_out(t0 - PC, PC);
     const int left = pt.len - t0 - PC;
-    if (left > 0) {
-      nt = left < PC ? left : PC;
-      copies(t0 + PC, nt, buf ^ 1);
-    }
+    nt = left < PC ? left : PC;
+    if (PIPE && left > 0) copies(t0 + PC, nt, buf ^ 1);
     const float* s_g = reinterpret_cast<const float*>(sb + L::W + T_BYTES + P_BYTES);
     unsigned char* s_v = smem + buf * L::BUF + L::V + wv * PC * CW * 2;
 
@@ -414,8 +445,8 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
       for (int t = 0; t < NF; ++t)
 #pragma unroll
         for (int r = 0; r < AR; ++r) R[rb][t][r] = O[rb][t][r] = U[rb][t][r] = 0.f;
-    bf16x8 ft[2][2][NF][3];                              // T fragments: [step parity][rb][tile][value]
-    bf16x8 b[2][3];
+    bf16x8 ft[BUFS][2][NF][3];                              // T fragments: [step parity][rb][tile][value]
+    bf16x8 b[BUFS][3];
     auto load_t = [&](int j) {
       const int kb = j / M::STEPS, sp = j % M::STEPS;
 #pragma unroll
@@ -424,32 +455,34 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
         for (int t = 0; t < NF; ++t)
           if (rb >= kb) {
 #pragma unroll
-            for (int v = 0; v < 3; ++v) ft[j & 1][rb][t][v] = frag_t((rb + kb) * 2 + (NF == 2 ? t : sp), v);
+            for (int v = 0; v < 3; ++v) ft[j & PIPE][rb][t][v] = frag_t((rb + kb) * 2 + (NF == 2 ? t : sp), v);
           }
     };
     {  // K S and Q S
-      bf16x8 fk[2][2][NF], fq[2][2][NF];
+      bf16x8 fk[BUFS][2][NF], fq[BUFS][2][NF];
       auto load_kq = [&](int j) {
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
           for (int t = 0; t < NF; ++t) {
-            fk[j & 1][rb][t] = frag_k(L::K, rb, j / M::STEPS, NF == 2 ? t : j % M::STEPS);
-            fq[j & 1][rb][t] = frag_k(L::Q, rb, j / M::STEPS, NF == 2 ? t : j % M::STEPS);
+            fk[j & PIPE][rb][t] = frag_k(L::K, rb, j / M::STEPS, NF == 2 ? t : j % M::STEPS);
+            fq[j & PIPE][rb][t] = frag_k(L::Q, rb, j / M::STEPS, NF == 2 ? t : j % M::STEPS);
           }
       };
       auto split_s = [&](int j) {
         float x[8];
         block8(S[j / M::STEPS], j % M::STEPS, x);
-        split8<3>(x, b[j & 1]);
+        split8<3>(x, b[j & PIPE]);
       };
-      load_kq(0);
-      split_s(0);
+      if (PIPE) {
+        load_kq(0);
+        split_s(0);
+      }
 #pragma unroll
       for (int j = 0; j < J1; ++j) {
-        if (j + 1 < J1) {
-          load_kq(j + 1);
-          split_s(j + 1);
+        if (j + PIPE < J1) {
+          load_kq(j + PIPE);
+          split_s(j + PIPE);
         } else {
           load_t(0);
         }
@@ -459,10 +492,13 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
           for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
             for (int t = 0; t < NF; ++t) {
-              R[rb][t] = M::mm(fk[j & 1][rb][t], b[j & 1][v], R[rb][t]);
-              if (v < 2) O[rb][t] = M::mm(fq[j & 1][rb][t], b[j & 1][v], O[rb][t]);
+              R[rb][t] = M::mm(fk[j & PIPE][rb][t], b[j & PIPE][v], R[rb][t]);
+              if (v < 2) O[rb][t] = M::mm(fq[j & PIPE][rb][t], b[j & PIPE][v], O[rb][t]);
             }
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (PIPE) {
+          interleave<10 * NF, 1, (NF == 1 ? 6 : 3)>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
     // R = V - g (K S);  O = g (Q S)
@@ -483,7 +519,7 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
         }
       }
     const float gC = s_g[PC - 1];
-    bf16x8 fp[2][2][NF][2], fs[2][DB][NF];
+    bf16x8 fp[BUFS][2][NF][2], fs[BUFS][DB][NF];
     auto load_ps = [&](int j) {
       const int kb = j / M::STEPS, sp = j % M::STEPS;
 #pragma unroll
@@ -492,25 +528,25 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
         for (int t = 0; t < NF; ++t)
           if (rb >= kb) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v) fp[j & 1][rb][t][v] = frag_p((rb + kb) * 2 + (NF == 2 ? t : sp), v);
+            for (int v = 0; v < 2; ++v) fp[j & PIPE][rb][t][v] = frag_p((rb + kb) * 2 + (NF == 2 ? t : sp), v);
           }
 #pragma unroll
       for (int db = 0; db < DB; ++db)
 #pragma unroll
-        for (int t = 0; t < NF; ++t) fs[j & 1][db][t] = frag_kt(db, kb, NF == 2 ? t : sp);
+        for (int t = 0; t < NF; ++t) fs[j & PIPE][db][t] = frag_kt(db, kb, NF == 2 ? t : sp);
     };
     {  // U = T R;  S = g_C S meanwhile
       auto split_r = [&](int j) {
         float x[8];
         block8(R[j / M::STEPS], j % M::STEPS, x);
-        split8<3>(x, b[j & 1]);
+        split8<3>(x, b[j & PIPE]);
       };
-      split_r(0);
+      if (PIPE) split_r(0);
 #pragma unroll
       for (int j = 0; j < J2; ++j) {
-        if (j + 1 < J2) {
-          load_t(j + 1);
-          split_r(j + 1);
+        if (j + PIPE < J2) {
+          load_t(j + PIPE);
+          split_r(j + PIPE);
         } else {
           load_ps(0);
         }
@@ -522,32 +558,36 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
           for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
             for (int t = 0; t < NF; ++t)
-              if (rb >= kb) U[rb][t] = M::mm(ft[j & 1][rb][t][TA[v]], b[j & 1][TB[v]], U[rb][t]);
+              if (rb >= kb) U[rb][t] = M::mm(ft[j & PIPE][rb][t][TA[v]], b[j & PIPE][TB[v]], U[rb][t]);
 #pragma unroll
         for (int db = j * DB / J2; db < (j + 1) * DB / J2; ++db)
 #pragma unroll
           for (int t = 0; t < NF; ++t)
 #pragma unroll
             for (int r = 0; r < AR; ++r) S[db][t][r] *= gC;
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (PIPE) {
+          if (kb == 0) interleave<12 * NF, 1, (NF == 1 ? 6 : 4)>();
+          else interleave<6 * NF, 2, (NF == 1 ? 9 : 6)>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
     {  // O += P U;  S += K^T (D_C U)
-      bf16x8 c[2][2];
+      bf16x8 c[BUFS][2];
       auto split_u = [&](int j) {
         float x[8];
         block8(U[j / M::STEPS], j % M::STEPS, x);
-        split8<2>(x, c[j & 1]);
+        split8<2>(x, c[j & PIPE]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= s_g[PC + 32 * (j / M::STEPS) + M::index(lane, 8 * (j % M::STEPS) + e)];
-        split8<3>(x, b[j & 1]);
+        split8<3>(x, b[j & PIPE]);
       };
-      split_u(0);
+      if (PIPE) split_u(0);
 #pragma unroll
       for (int j = 0; j < J2; ++j) {
-        if (j + 1 < J2) {
-          load_ps(j + 1);
-          split_u(j + 1);
+        if (j + PIPE < J2) {
+          load_ps(j + PIPE);
+          split_u(j + PIPE);
         }
         const int kb = j / M::STEPS;
         constexpr int PA[3] = {0, 1, 0}, PB[3] = {1, 0, 0};
@@ -557,15 +597,18 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
           for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
             for (int t = 0; t < NF; ++t)
-              if (rb >= kb) O[rb][t] = M::mm(fp[j & 1][rb][t][PA[v]], c[j & 1][PB[v]], O[rb][t]);
+              if (rb >= kb) O[rb][t] = M::mm(fp[j & PIPE][rb][t][PA[v]], c[j & PIPE][PB[v]], O[rb][t]);
         }
 #pragma unroll
         for (int v = 2; v >= 0; --v)
 #pragma unroll
           for (int db = 0; db < DB; ++db)
 #pragma unroll
-            for (int t = 0; t < NF; ++t) S[db][t] = M::mm(fs[j & 1][db][t], b[j & 1][v], S[db][t]);
-        if (j + 1 < J2) __builtin_amdgcn_sched_barrier(0);
+            for (int t = 0; t < NF; ++t) S[db][t] = M::mm(fs[j & PIPE][db][t], b[j & PIPE][v], S[db][t]);
+        if constexpr (PIPE) if (j + 1 < J2) {
+          interleave<(3 * DB + 3) * NF, 1, (NF == 1 ? 6 : 4)>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
     // the outputs, columns of 64 tokens (eight swizzled pieces), over the wave's
@@ -590,6 +633,10 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
       out[u] = __builtin_bit_cast(u32x4, join(read_tr(at(c)), read_tr(at(c + 4))));
     }
     wave_lds_sync();
+    if (!PIPE && left > 0) {                     // one buffer: everybody has read it
+      __syncthreads();
+      copies(t0 + PC, nt, 0);
+    }
   }
   if (pt.len > 0) store_out(t0 - PC, pt.len - (t0 - PC));
 
@@ -630,21 +677,21 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   }
 }
 
-template <int DK, int DV, int CW>
+template <int DK, int DV, int CW, int BUFS>
 int launch(const PromptParams& p, hipStream_t st) {
-  using L = ChunkLds<DK, CW>;
   hipLaunchKernelGGL((prompt_prep_kernel<DK, CW>), dim3((unsigned)p.nslots * p.H), dim3(256), 0, st, p);
-  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, CW>), dim3((unsigned)p.nseq * p.H * (DV / L::VC)), dim3(256), 0,
-                     st, p);
+  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, CW, BUFS>), dim3((unsigned)p.nseq * p.H * (DV / (4 * CW))), dim3(256),
+                     0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 }  // namespace
 
 int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st) {
-  if (dk == 64 && dv == 64) return launch<64, 64, 16>(p, st);
-  if (dk == 128 && dv == 64) return launch<128, 64, 16>(p, st);
-  if (dk == 128 && dv == 128) return launch<128, 128, 32>(p, st);
+  const bool few = p.nseq * p.H <= 256;
+  if (dk == 64 && dv == 64) return few ? launch<64, 64, 16, 2>(p, st) : launch<64, 64, 16, 1>(p, st);
+  if (dk == 128 && dv == 64) return few ? launch<128, 64, 16, 2>(p, st) : launch<128, 64, 16, 1>(p, st);
+  if (dk == 128 && dv == 128) return few ? launch<128, 128, 16, 2>(p, st) : launch<128, 128, 32, 1>(p, st);
   return -2;
 }
 

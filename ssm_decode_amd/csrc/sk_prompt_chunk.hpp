@@ -97,15 +97,15 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[TERMS]
 #pragma unroll
   for (int t = 0; t < TERMS; ++t) {
     u32x4 w;
-    w.x = high_halves(r[0], r[1]);
-    w.y = high_halves(r[2], r[3]);
-    w.z = high_halves(r[4], r[5]);
-    w.w = high_halves(r[6], r[7]);
-    out[t] = as_frag(w);
-    if (t + 1 < TERMS) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[e] = below(r[e]);
+    for (int e = 0; e < 4; ++e) {
+      w[e] = high_halves(r[2 * e], r[2 * e + 1]);
+      if (t + 1 < TERMS) {
+        r[2 * e] = below(r[2 * e]);
+        r[2 * e + 1] = below(r[2 * e + 1]);
+      }
     }
+    out[t] = as_frag(w);
   }
 }
 
