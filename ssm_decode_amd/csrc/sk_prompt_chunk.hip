@@ -10,7 +10,7 @@ namespace {
 // by substitution in 16 x 16 blocks, joined to 32 and 64 by fp32 products.
 constexpr int LS = PC + 4;                       // row stride of the fp32 matrices in LDS
 
-template <int DK, int CW>
+template <int DK>
 __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   constexpr int KB = PC * DK * 2;                // bytes of K or Q in LDS
   constexpr int MB = PC * LS * 4;                // bytes of A or P in LDS
@@ -205,10 +205,7 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   for (int c = tid; c < FRAGS * 64; c += 256) {
     const int f = c >> 6, ln = c & 63, pair = f >> 1;
     const int rb = pair > 0, kb = pair == 2;
-    int row, k;
-    frag_at<CW>(ln, f & 1, &row, &k);
-    row += 32 * rb;
-    k += 32 * kb;
+    const int row = 32 * rb + block_row(ln & 15, f & 1), k = 32 * kb + 8 * (ln >> 4);
     float t[8], v[8], a4[4];
 #pragma unroll
     for (int e = 0; e < 8; e += 4) {
@@ -241,20 +238,27 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
 }
 
 // ------------------------------------------------------ chunk after chunk
-// One workgroup of four waves per (prompt, head, part of the columns); a wave
-// holds CW columns of the state, all rows, in registers.  K, Q, V, T and P
-// are in LDS twice: the next chunk's copy, straight from memory, is in flight
-// over the present chunk.  K^T comes from K by transposing reads.
-template <int DK, int CW, int BUFS>
+// One workgroup of four waves per (prompt, head, 64 columns); a wave holds 16
+// columns of the state, all rows, in registers.  K, Q, V, T and P are in LDS
+// twice: the next chunk's copy, straight from memory, is in flight over the
+// present chunk.  K^T and V's columns come by transposing LDS reads.
+//
+// What bounds it is the chain from chunk to chunk, so a chunk's instructions
+// are laid out by hand in regions: in each, the matrix instructions of one
+// step, the LDS reads of the next step's fragments, and the vector work (three
+// value splits above all) that a later step needs; the vector work runs in the
+// shadow of the matrix instructions only where it stands between them.
+constexpr int VC = 64;                           // columns of a workgroup
+
+template <int DK>
 struct ChunkLds {
-  static constexpr int VC = 4 * CW;              // columns of the workgroup
   static constexpr int K = 0;
   static constexpr int Q = K + PC * DK * 2;
-  static constexpr int V = Q + PC * DK * 2;      // wave after wave: [64][CW], then the outputs [CW][64]
+  static constexpr int V = Q + PC * DK * 2;      // wave after wave: [64][16], then the outputs [16][64]
   static constexpr int W = V + PC * VC * 2;      // a chunk's workspace as it is
   static constexpr int BUF = W + (CHUNK_WORK_BYTES + 1023) / 1024 * 1024;
-  static constexpr int BYTES = BUFS * BUF;
-  static_assert(BYTES <= BUFS * 80 * 1024, "two workgroups of one buffer, or one of two, on a CU");
+  static constexpr int BYTES = 2 * BUF;
+  static_assert(BYTES <= 160 * 1024, "LDS of a CU");
 };
 
 // 16 bytes of each active lane from memory to LDS at lds + 16 * lane, in
@@ -280,418 +284,391 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Asks for a step's instructions in the order: a matrix instruction, LDS reads
-// (of the next step's fragments), vector work (the next step's split), and so
-// on.  One wave's vector work runs in the shadow of its matrix instructions
-// only where it stands between them.
-template <int MFMAS, int READS, int VALU>
+// The end of a region: its instructions in the order of N times a matrix
+// instruction, READS LDS reads and VALU vector instructions (as far as there
+// are any), and nothing moved across.
+template <int N, int READS, int VALU>
 __device__ __forceinline__ void interleave() {
-  if constexpr (MFMAS > 0) {
+  if constexpr (N > 0) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-    interleave<MFMAS - 1, READS, VALU>();
+    if constexpr (VALU > 0) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    interleave<N - 1, READS, VALU>();
   }
 }
+template <int N, int READS, int VALU>
+__device__ __forceinline__ void region() {
+  interleave<N, READS, VALU>();
+  __builtin_amdgcn_sched_barrier(0);
+}
 
-template <int DK, int DV, int CW, int BUFS>
-__global__ void __launch_bounds__(256, 3 - BUFS) prompt_chunk_kernel(PromptParams p) {
-  using M = Mf<CW>;
-  using L = ChunkLds<DK, CW, BUFS>;
-  typedef typename M::Acc Acc;
-  constexpr int VC = L::VC, PARTS = DV / VC, PPR = DK / 8, NB = M::NB, DB = DK / 32;
-  constexpr int AR = NB / M::TILES;              // registers of a tile
-  constexpr int PIPE = BUFS - 1;                 // one wave a SIMD: it overlaps its own steps
+template <int DK, int DV>
+__global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
+  using L = ChunkLds<DK>;
+  constexpr int PPR = DK / 8, DB = DK / 32;      // 16-byte pieces of a row, blocks of 32 rows
   __shared__ __align__(1024) unsigned char smem[L::BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // (the parts of a tile are a multiple of nseq * H workgroups apart: mostly
-  // on the same XCD, whose cache then serves the K, Q, T and P that they share)
+  const int n = lane & 15, hi = lane >> 4;
+  // (the parts of a tile are nseq * H workgroups apart: mostly on one XCD,
+  // whose cache then serves the K, Q, T and P that they share)
   const int tiles = p.nseq * p.H, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
   const int i = tile / p.H, h = tile - i * p.H;
   if ((int64_t)p.start[i + 1] - p.start[i] <= p.len_lo) return;
   const PromptTile pt = prompt_tile(p, i, h);
   if (!pt.ok) return;
 
-  const int n = lane % M::MT, hi = lane / M::MT;           // column, part of the k axis
-  const int col = part * VC + wv * CW + n;
-  float* Sg = p.S + ((size_t)pt.b * p.H + h) * DK * DV + col;
-
+  const int c0 = part * VC + wv * 16;            // the wave's first column
+  float* Sg = p.S + ((size_t)pt.b * p.H + h) * DK * DV + c0 + n;
   const bf16* kp = reinterpret_cast<const bf16*>(p.k) + pt.s0 * p.ks + (int64_t)h * DK;
   const bf16* qp = reinterpret_cast<const bf16*>(p.q) + pt.s0 * p.qs + (int64_t)h * DK;
-  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + pt.s0 * p.vs + (int64_t)h * DV + part * VC + wv * CW;
-  bf16* op = reinterpret_cast<bf16*>(p.o) + pt.s0 * p.os + (int64_t)h * DV + part * VC + wv * CW;
+  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + pt.s0 * p.vs + (int64_t)h * DV + c0;
   const unsigned char* wp = reinterpret_cast<const unsigned char*>(p.work) +
                             ((size_t)first_slot(pt.s0, i) * p.H + h) * CHUNK_WORK_BYTES;
 
-  // rows of K and Q with their 16-byte pieces swizzled
-  auto swz = [](int row) { return (PPR == 16 ? M::swizzle(row) : M::swizzle(row) >> 1) & (PPR - 1); };
-  auto piece = [&](int row, int pc) { return row * PPR + (pc ^ swz(row)); };
-  // A chunk's copies, in units of 64 pieces that the waves share out.  Rows
-  // behind the prompt's end repeat its last: their beta in T is 0, their
-  // columns of P meet only zeros, and their outputs are not stored.
-  const uint32_t lds0 = lds_address(smem);
-  constexpr int VPR = CW / 8, KU = PPR / 4, KROWS = 256 / PPR, VROWS = 64 / VPR;
-  constexpr int WFULL = CHUNK_WORK_BYTES / 16 / 64, WREST = CHUNK_WORK_BYTES / 16 % 64;
-  const int krow = (wv * 64 + lane) / PPR, kpc = lane % PPR, vrow = lane / VPR;
-  const unsigned char* wp0 = wp + lane * 16 + wv * 1024;
-  auto copies = [&](int t0, int nt, int buf) {
-    const uint32_t l0 = lds0 + buf * L::BUF;
-    if (nt == PC) {                                        // uniform: a whole chunk
-      const bf16* kc = kp + (t0 + krow) * p.ks;
-      const bf16* qc = qp + (t0 + krow) * p.qs;
-      const bf16* vc = vp + (t0 + vrow) * p.vs + (lane % VPR) * 8;
-#pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        const int pc = (kpc ^ swz(krow + KROWS * u)) * 8;
-        copy16(kc + (u * KROWS * p.ks + pc), l0 + L::K + (4 * u + wv) * 1024);
-        copy16(qc + (u * KROWS * p.qs + pc), l0 + L::Q + (4 * u + wv) * 1024);
-      }
-#pragma unroll
-      for (int u = 0; u < VPR; ++u)
-        copy16(vc + u * VROWS * p.vs, l0 + L::V + wv * PC * CW * 2 + u * 1024);
-    } else {
-#pragma unroll 1
-      for (int u = 0; u < KU; ++u) {
-        const int row = krow + KROWS * u, pc = (kpc ^ swz(row)) * 8;
-        const int64_t t = t0 + (row < nt ? row : nt - 1);
-        copy16(kp + t * p.ks + pc, l0 + L::K + (4 * u + wv) * 1024);
-        copy16(qp + t * p.qs + pc, l0 + L::Q + (4 * u + wv) * 1024);
-      }
-#pragma unroll 1
-      for (int u = 0; u < VPR; ++u) {
-        const int row = vrow + VROWS * u;
-        const int64_t t = t0 + (row < nt ? row : nt - 1);
-        copy16(vp + t * p.vs + (lane % VPR) * 8, l0 + L::V + wv * PC * CW * 2 + u * 1024);
-      }
-    }
-    const unsigned char* w = wp0 + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES;
-#pragma unroll
-    for (int u = 0; u < WFULL / 4; ++u) copy16(w + u * 4096, l0 + L::W + (4 * u + wv) * 1024);
-    constexpr int U = WFULL / 4 * 4;
-    if (U + wv < WFULL || (U + wv == WFULL && lane < WREST)) copy16(w + U * 1024, l0 + L::W + (U + wv) * 1024);
+  // ------------------------------------------------------------- copies
+  // Rows of K and Q have their 16-byte pieces swizzled so that the rows of a
+  // fragment spread over the banks.
+  auto swz = [](int row) {
+    const int s = (row & 3) | ((row >> 1) & 12);
+    return (PPR == 16 ? s : s >> 1) & (PPR - 1);
   };
-  int nt = pt.len < PC ? pt.len : PC;
-  if (pt.len > 0) copies(0, nt, 0);
+  auto piece = [&](int row, int pc) { return row * PPR + (pc ^ swz(row)); };
+  const uint32_t lds0 = lds_address(smem);
+  constexpr int KU = PPR / 4, KROWS = 256 / PPR;           // a wave's units of 64 pieces of K, rows from one to the next
+  constexpr int WFULL = CHUNK_WORK_BYTES / 1024, WREST = CHUNK_WORK_BYTES / 16 % 64;
+  constexpr int WU = (WFULL + 4) / 4, UNITS = 2 * KU + 2 + WU;
+  static_assert(WREST > 0 && WFULL % 4 != 3, "the last unit of the workspace is a part");
+  const int krow = (wv * 64 + lane) / PPR, kpc = lane % PPR, vrow = lane >> 1, vpc = (lane & 1) * 8;
+  // unit u of the whole chunk at t0 into a buffer: K, Q, then the workspace, V last
+  auto copy_unit = [&](int u, int t0, uint32_t l0) {
+    if (u < 2 * KU) {
+      const int v = u < KU ? u : u - KU, row = krow + KROWS * v;
+      const int64_t st = u < KU ? p.ks : p.qs;
+      const bf16* src = (u < KU ? kp : qp) + (int64_t)(t0 + krow) * st + v * KROWS * st;
+      copy16(src + (kpc ^ swz(row)) * 8, l0 + (u < KU ? L::K : L::Q) + (4 * v + wv) * 1024);
+    } else if (u < 2 * KU + WU) {
+      const int unit = 4 * (u - 2 * KU) + wv;
+      const unsigned char* src = wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES + unit * 1024 + lane * 16;
+      if (unit < WFULL || (unit == WFULL && lane < WREST)) copy16(src, l0 + L::W + unit * 1024);
+    } else {
+      const int v = u - 2 * KU - WU;
+      copy16(vp + (int64_t)(t0 + vrow) * p.vs + v * 32 * p.vs + vpc, l0 + L::V + wv * 2048 + v * 1024);
+    }
+  };
+  // The whole of a chunk that may be a prompt's last: rows behind its end
+  // repeat its last one (their beta in T is 0, their columns of P meet only
+  // zeros, and their outputs are not stored).
+  auto copy_all = [&](int t0, int nt, uint32_t l0) {
+    auto at = [&](int row) { return (int64_t)(t0 + (row < nt ? row : nt - 1)); };
+#pragma unroll 1
+    for (int v = 0; v < KU; ++v) {
+      const int row = krow + KROWS * v, pc = (kpc ^ swz(row)) * 8;
+      copy16(kp + at(row) * p.ks + pc, l0 + L::K + (4 * v + wv) * 1024);
+      copy16(qp + at(row) * p.qs + pc, l0 + L::Q + (4 * v + wv) * 1024);
+    }
+#pragma unroll 1
+    for (int v = 0; v < 2; ++v)
+      copy16(vp + at(vrow + 32 * v) * p.vs + vpc, l0 + L::V + wv * 2048 + v * 1024);
+#pragma unroll 1
+    for (int u = 2 * KU; u < 2 * KU + WU; ++u) copy_unit(u, t0, l0);
+  };
+  if (pt.len > 0) copy_all(0, pt.len < PC ? pt.len : PC, lds0);
 
-  // the state, block after block of 32 rows
-  Acc S[DB][M::TILES];
+  // --------------------------------------------------------- fragments
+  const unsigned char* sb = smem;                // the present chunk's buffer
+  const int ti = n >> 2, tc = 4 * (n & 3);
+  auto frag_kq = [&](int at, int rb, int t, int kb) {      // tile t of block (rb, kb) of K or Q
+    return as_frag(reinterpret_cast<const u32x4*>(sb + at)[piece(32 * rb + block_row(n, t), 4 * kb + hi)]);
+  };
+  auto frag_kt = [&](int db, int t, int kb) {              // of K^T: tokens 32 kb + 8 hi ..
+    const int d = 32 * db + block_row(tc, t), tok = 32 * kb + 8 * hi + ti;
+    const unsigned char* s = sb + L::K + (d & 7) * 2;
+    return join(read_tr(s + piece(tok, d >> 3) * 16), read_tr(s + piece(tok + 4, d >> 3) * 16));
+  };
+  auto frag_t = [&](int f, int v) { return as_frag(reinterpret_cast<const u32x4*>(sb + L::W)[(f * 3 + v) * 64 + lane]); };
+  auto frag_p = [&](int f, int v) {
+    return as_frag(reinterpret_cast<const u32x4*>(sb + L::W + T_BYTES)[(f * 2 + v) * 64 + lane]);
+  };
+  typedef f32x4s Block[2];                       // 32 rows x 16 columns
+  auto rows8 = [](const f32x4s (&a)[2], float (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = a[e >> 2][e & 3];
+  };
+
+  Block S[DB];
   const bool cont = !p.has_state || p.has_state[i] != 0;
 #pragma unroll
   for (int db = 0; db < DB; ++db)
 #pragma unroll
-    for (int r = 0; r < NB; ++r)
-      S[db][r / AR][r % AR] = cont ? Sg[(size_t)(32 * db + M::index(lane, r)) * DV] : 0.f;
+    for (int e = 0; e < 8; ++e) S[db][e >> 2][e & 3] = cont ? Sg[(size_t)(32 * db + 8 * hi + e) * DV] : 0.f;
 
-  int arow[2], ak[2];
+  // The wave's outputs of a chunk leave in the next chunk's time: from LDS,
+  // columns of 64 tokens in eight swizzled pieces, as rows of eight columns.
+  bf16* op = reinterpret_cast<bf16*>(p.o) + pt.s0 * p.os + (int64_t)h * DV + c0;
+  u32x4 out[2];
+  const int og = hi & 1, ot = 16 * (hi >> 1);
+  bf16* op0 = op + (int64_t)(ot + n) * p.os + og * 8;
+  auto read_out = [&](const unsigned char* s) {
 #pragma unroll
-  for (int f = 0; f < 2; ++f) frag_at<CW>(lane, f, &arow[f], &ak[f]);
-  const unsigned char* sb = smem;                // the present chunk's buffer
-  // fragment f of block (rb, kb) of K or Q
-  auto frag_k = [&](int at, int rb, int kb, int f) {
-    return as_frag(reinterpret_cast<const u32x4*>(sb + at)[piece(32 * rb + arow[f], (32 * kb + ak[f]) >> 3)]);
-  };
-  // of K^T: eight tokens from 32 kb + ak of the rows that the lane's group of 16
-  // gives the addresses of: lane i those of tokens i / 4 and i / 4 + 4
-  const int ti = (lane & 15) >> 2, tc = 4 * (lane & 3), tg = M::MT == 32 ? lane & 16 : 0;
-  auto frag_kt = [&](int rb, int kb, int f) {
-    const int d = 32 * rb + M::row(tg + tc, M::TILES == 2 ? f : 0), t = 32 * kb + ak[f] + ti;
-    const unsigned char* s = sb + L::K + (d & 7) * 2;
-    return join(read_tr(s + piece(t, d >> 3) * 16), read_tr(s + piece(t + 4, d >> 3) * 16));
-  };
-  auto frag_t = [&](int f, int term) { return as_frag(reinterpret_cast<const u32x4*>(sb + L::W)[(f * 3 + term) * 64 + lane]); };
-  auto frag_p = [&](int f, int term) {
-    return as_frag(reinterpret_cast<const u32x4*>(sb + L::W + T_BYTES)[(f * 2 + term) * 64 + lane]);
-  };
-  auto block8 = [&](const Acc (&a)[M::TILES], int s, float (&x)[8]) {    // the B operand of step s
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = a[(8 * s + e) / AR][(8 * s + e) % AR];
-  };
-  // the wave's outputs of a chunk, as whole rows: lane's 8 columns of OU tokens
-  constexpr int OU = NB / 8 * 2, OG = CW / 8;    // OG column groups, 4 / OG groups of 16 tokens at a time
-  u32x4 out[OU];
-  const int og = (lane >> 4) % OG, ot = (lane >> 4) / OG * 16 + (lane & 15);
-  bf16* op0 = op + ot * p.os + og * 8;
-  auto store_out = [&](int t0, int cnt) {
-#pragma unroll
-    for (int u = 0; u < OU; ++u) {
-      if (ot + u * (64 / OG) < cnt)
-        *reinterpret_cast<u32x4*>(op0 + (int64_t)t0 * p.os + u * (64 / OG) * p.os) = out[u];
+    for (int u = 0; u < 2; ++u) {                // lane i of a group: column 8 og + i / 4 (and + 4), tokens 4 (i % 4) ..
+      const int t = ot + 32 * u + tc, c = 8 * og + ti;
+      auto at = [&](int cc) { return s + cc * 128 + ((t >> 3) ^ (cc & 7)) * 16 + (t & 7) * 2; };
+      out[u] = __builtin_bit_cast(u32x4, join(read_tr(at(c)), read_tr(at(c + 4))));
     }
   };
+  auto store_out = [&](int t0, int cnt) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (ot + n + 32 * u < cnt) *reinterpret_cast<u32x4*>(op0 + ((int64_t)t0 + 32 * u) * p.os) = out[u];
+  };
 
+  bf16x8 ss[DB][3];                              // the state's split blocks
+  {
+    float x[8];
+    rows8(S[0], x);
+    split8<3>(x, ss[0]);
+  }
   int t0 = 0;
-  for (int buf = 0; t0 < pt.len; t0 += PC, buf ^= PIPE) {
-    // this wave's copies for the chunk have landed, then everybody's; with two
-    // buffers, everybody has read the other
+  for (int buf = 0; t0 < pt.len; t0 += PC, buf ^= 1) {
+    // this wave's copies for the chunk have landed, then everybody's; and
+    // everybody has read the other buffer
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     sb = smem + buf * L::BUF;
-    if (t0 > 0) store_out(t0 - PC, PC);
-    const int left = pt.len - t0 - PC;
-    nt = left < PC ? left : PC;
-    if (PIPE && left > 0) copies(t0 + PC, nt, buf ^ 1);
     const float* s_g = reinterpret_cast<const float*>(sb + L::W + T_BYTES + P_BYTES);
-    unsigned char* s_v = smem + buf * L::BUF + L::V + wv * PC * CW * 2;
+    const unsigned char* s_v = sb + L::V + wv * 2048;
+    const int left = pt.len - t0 - PC;
+    const uint32_t lnext = lds0 + (buf ^ 1) * L::BUF;
+    const bool whole = left >= PC;               // uniform: the next chunk is whole
+    auto copies = [&](int from, int to) {
+      if (whole) {
+#pragma unroll
+        for (int u = from; u < to; ++u)
+          if (u < UNITS) copy_unit(u, t0 + PC, lnext);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
 
-    // Each step of a product (KS values of its k axis) has its A fragments read
-    // from LDS and its B operand split during the step before, so that neither
-    // LDS latency nor vector work stands between two steps' matrix
-    // instructions; the barriers keep the compiler from undoing that.
-    constexpr int NF = M::TILES, J1 = DB * M::STEPS, J2 = 2 * M::STEPS;
-    Acc R[2][NF], O[2][NF], U[2][NF];
-#pragma unroll
-    for (int rb = 0; rb < 2; ++rb)
-#pragma unroll
-      for (int t = 0; t < NF; ++t)
-#pragma unroll
-        for (int r = 0; r < AR; ++r) R[rb][t][r] = O[rb][t][r] = U[rb][t][r] = 0.f;
-    bf16x8 ft[BUFS][2][NF][3];                              // T fragments: [step parity][rb][tile][value]
-    bf16x8 b[BUFS][3];
-    auto load_t = [&](int j) {
-      const int kb = j / M::STEPS, sp = j % M::STEPS;
+    // what the chunk's beginning needs from LDS, all at once
+    bf16x8 fa[2][2][2], ft[2][2][2][3], fp[2][2][2][2], fs[2][DB][2], vv[2];
+    float gm[2][8], dm[2][8];
+    auto load_kq = [&](int at, int j) {
 #pragma unroll
       for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-        for (int t = 0; t < NF; ++t)
-          if (rb >= kb) {
-#pragma unroll
-            for (int v = 0; v < 3; ++v) ft[j & PIPE][rb][t][v] = frag_t((rb + kb) * 2 + (NF == 2 ? t : sp), v);
-          }
+        for (int t = 0; t < 2; ++t) fa[j & 1][rb][t] = frag_kq(at, rb, t, j % DB);
     };
-    {  // K S and Q S
-      bf16x8 fk[BUFS][2][NF], fq[BUFS][2][NF];
-      auto load_kq = [&](int j) {
+    load_kq(L::K, 0);
+    if (t0 > 0) read_out(smem + (buf ^ 1) * L::BUF + L::V + wv * 2048);
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      ldn<8>(s_g + 32 * rb + 8 * hi, gm[rb]);
+      ldn<8>(s_g + PC + 32 * rb + 8 * hi, dm[rb]);
+      const unsigned char* sv = s_v + (32 * rb + 8 * hi + ti) * 32 + tc * 2;
+      vv[rb] = join(read_tr(sv), read_tr(sv + 4 * 32));
+    }
+    const float gC = s_g[PC - 1];
+    __builtin_amdgcn_sched_barrier(0);
+    if (t0 > 0) store_out(t0 - PC, PC);
+    if (left > 0 && !whole) copy_all(t0 + PC, left, lnext);
+    __builtin_amdgcn_sched_barrier(0);
+
+    Block R[2], O[2], U[2];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) R[rb][t] = O[rb][t] = U[rb][t] = f32x4s{0.f, 0.f, 0.f, 0.f};
+    // R = K S (three values of S)
+#pragma unroll
+    for (int j = 0; j < DB; ++j) {
+      if (j + 1 < DB) {
+        load_kq(L::K, j + 1);
+        float x[8];
+        rows8(S[j + 1], x);
+        split8<3>(x, ss[j + 1]);
+      } else {
+        load_kq(L::Q, DB);                       // (block 0 of Q, into the buffer that follows)
+      }
+#pragma unroll
+      for (int v = 0; v < 3; ++v)
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-          for (int t = 0; t < NF; ++t) {
-            fk[j & PIPE][rb][t] = frag_k(L::K, rb, j / M::STEPS, NF == 2 ? t : j % M::STEPS);
-            fq[j & PIPE][rb][t] = frag_k(L::Q, rb, j / M::STEPS, NF == 2 ? t : j % M::STEPS);
-          }
-      };
-      auto split_s = [&](int j) {
-        float x[8];
-        block8(S[j / M::STEPS], j % M::STEPS, x);
-        split8<3>(x, b[j & PIPE]);
-      };
-      if (PIPE) {
-        load_kq(0);
-        split_s(0);
-      }
-#pragma unroll
-      for (int j = 0; j < J1; ++j) {
-        if (j + PIPE < J1) {
-          load_kq(j + PIPE);
-          split_s(j + PIPE);
-        } else {
-          load_t(0);
-        }
-#pragma unroll
-        for (int v = 0; v < 3; ++v)
-#pragma unroll
-          for (int rb = 0; rb < 2; ++rb)
-#pragma unroll
-            for (int t = 0; t < NF; ++t) {
-              R[rb][t] = M::mm(fk[j & PIPE][rb][t], b[j & PIPE][v], R[rb][t]);
-              if (v < 2) O[rb][t] = M::mm(fq[j & PIPE][rb][t], b[j & PIPE][v], O[rb][t]);
-            }
-        if constexpr (PIPE) {
-          interleave<10 * NF, 1, (NF == 1 ? 6 : 3)>();
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
+          for (int t = 0; t < 2; ++t) R[rb][t] = mm32(fa[j & 1][rb][t], ss[j][v], R[rb][t]);
+      region<12, 1, 4>();
+      copies(3 * j, 3 * j + 3);
     }
-    // R = V - g (K S);  O = g (Q S)
+    bf16x8 br[2][3];
+    auto load_t = [&](int kb) {
 #pragma unroll
-    for (int rb = 0; rb < 2; ++rb)
+      for (int rb = kb; rb < 2; ++rb)
 #pragma unroll
-      for (int s8 = 0; s8 < NB / 8; ++s8) {
-        // V's column n, eight tokens: as K^T, from rows of CW values
-        const int tk = 32 * rb + M::index(lane, 8 * s8);
-        const unsigned char* sv = s_v + ((tk + ti) * CW + tg + tc) * 2;
-        const bf16x8 v8 = join(read_tr(sv), read_tr(sv + 4 * CW * 2));
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int r = 8 * s8 + e;
-          const float gam = s_g[tk + e];
-          R[rb][r / AR][r % AR] = (float)v8[e] - gam * R[rb][r / AR][r % AR];
-          O[rb][r / AR][r % AR] *= gam;
-        }
-      }
-    const float gC = s_g[PC - 1];
-    bf16x8 fp[BUFS][2][NF][2], fs[BUFS][DB][NF];
-    auto load_ps = [&](int j) {
-      const int kb = j / M::STEPS, sp = j % M::STEPS;
+          for (int v = 0; v < 3; ++v) ft[kb][rb][t][v] = frag_t((rb + kb) * 2 + t, v);
+    };
+    // O = Q S (two values);  R = V - g (K S) and its split meanwhile
+#pragma unroll
+    for (int j = 0; j < DB; ++j) {
+      if (j + 1 < DB) load_kq(L::Q, DB + j + 1);
+      else load_t(0);
+#pragma unroll
+      for (int v = 1; v >= 0; --v)
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) O[rb][t] = mm32(fa[(DB + j) & 1][rb][t], ss[j][v], O[rb][t]);
 #pragma unroll
       for (int rb = 0; rb < 2; ++rb)
+        if (j == (rb + 1) * DB / 4) {
+          float x[8];
 #pragma unroll
-        for (int t = 0; t < NF; ++t)
-          if (rb >= kb) {
+          for (int e = 0; e < 8; ++e) x[e] = (float)vv[rb][e] - gm[rb][e] * R[rb][e >> 2][e & 3];
+          split8<3>(x, br[rb]);
+        }
+      region<8, 2, 8>();
+      copies(3 * DB + 2 * j, 3 * DB + 2 * j + 2);
+    }
+    bf16x8 bu[2][3], bo[2][2];
+    auto split_u = [&](int kb) {
+      float x[8];
+      rows8(U[kb], x);
+      split8<2>(x, bo[kb]);
 #pragma unroll
-            for (int v = 0; v < 2; ++v) fp[j & PIPE][rb][t][v] = frag_p((rb + kb) * 2 + (NF == 2 ? t : sp), v);
-          }
+      for (int e = 0; e < 8; ++e) x[e] *= dm[kb][e];
+      split8<3>(x, bu[kb]);
+    };
+    auto load_ps = [&](int kb) {
+#pragma unroll
+      for (int rb = kb; rb < 2; ++rb)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) fp[kb][rb][t][v] = frag_p((rb + kb) * 2 + t, v);
 #pragma unroll
       for (int db = 0; db < DB; ++db)
 #pragma unroll
-        for (int t = 0; t < NF; ++t) fs[j & PIPE][db][t] = frag_kt(db, kb, NF == 2 ? t : sp);
+        for (int t = 0; t < 2; ++t) fs[kb][db][t] = frag_kt(db, t, kb);
     };
-    {  // U = T R;  S = g_C S meanwhile
-      auto split_r = [&](int j) {
-        float x[8];
-        block8(R[j / M::STEPS], j % M::STEPS, x);
-        split8<3>(x, b[j & PIPE]);
-      };
-      if (PIPE) split_r(0);
+    // U = T R, the smaller products first; O = g O and S = g_C S meanwhile
+    constexpr int TA[6] = {0, 2, 1, 0, 1, 0}, TB[6] = {2, 0, 1, 1, 0, 0};
 #pragma unroll
-      for (int j = 0; j < J2; ++j) {
-        if (j + PIPE < J2) {
-          load_t(j + PIPE);
-          split_r(j + PIPE);
-        } else {
-          load_ps(0);
+    for (int kb = 0; kb < 2; ++kb) {
+      if (kb == 0) load_t(1);
+      else load_ps(0);
+#pragma unroll
+      for (int v = 0; v < 6; ++v)
+#pragma unroll
+        for (int rb = kb; rb < 2; ++rb)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) U[rb][t] = mm32(ft[kb][rb][t][TA[v]], br[kb][TB[v]], U[rb][t]);
+      if (kb == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+          for (int rb = 0; rb < 2; ++rb) O[rb][e >> 2][e & 3] *= gm[rb][e];
+#pragma unroll
+          for (int db = 0; db < DB; ++db) S[db][e >> 2][e & 3] *= gC;
         }
-        const int kb = j / M::STEPS;
-        constexpr int TA[6] = {0, 2, 1, 0, 1, 0}, TB[6] = {2, 0, 1, 1, 0, 0};   // the smaller products first
-#pragma unroll
-        for (int v = 0; v < 6; ++v)
-#pragma unroll
-          for (int rb = 0; rb < 2; ++rb)
-#pragma unroll
-            for (int t = 0; t < NF; ++t)
-              if (rb >= kb) U[rb][t] = M::mm(ft[j & PIPE][rb][t][TA[v]], b[j & PIPE][TB[v]], U[rb][t]);
-#pragma unroll
-        for (int db = j * DB / J2; db < (j + 1) * DB / J2; ++db)
-#pragma unroll
-          for (int t = 0; t < NF; ++t)
-#pragma unroll
-            for (int r = 0; r < AR; ++r) S[db][t][r] *= gC;
-        if constexpr (PIPE) {
-          if (kb == 0) interleave<12 * NF, 1, (NF == 1 ? 6 : 4)>();
-          else interleave<6 * NF, 2, (NF == 1 ? 9 : 6)>();
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        region<24, 1, 2>();
+        copies(5 * DB, 5 * DB + 2);
+      } else {
+        split_u(0);                              // (U's first block has no second step)
+        region<12, 2, 7>();
       }
     }
-    {  // O += P U;  S += K^T (D_C U)
-      bf16x8 c[BUFS][2];
-      auto split_u = [&](int j) {
-        float x[8];
-        block8(U[j / M::STEPS], j % M::STEPS, x);
-        split8<2>(x, c[j & PIPE]);
+    // O += P U;  S += K^T (D_C U)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= s_g[PC + 32 * (j / M::STEPS) + M::index(lane, 8 * (j % M::STEPS) + e)];
-        split8<3>(x, b[j & PIPE]);
-      };
-      if (PIPE) split_u(0);
+    for (int kb = 0; kb < 2; ++kb) {
+      if (kb == 0) {
+        load_ps(1);
+        split_u(1);
+      }
+      constexpr int PA[3] = {0, 1, 0}, PB[3] = {1, 0, 0};
 #pragma unroll
-      for (int j = 0; j < J2; ++j) {
-        if (j + PIPE < J2) {
-          load_ps(j + PIPE);
-          split_u(j + PIPE);
-        }
-        const int kb = j / M::STEPS;
-        constexpr int PA[3] = {0, 1, 0}, PB[3] = {1, 0, 0};
+      for (int v = 0; v < 3; ++v)
 #pragma unroll
-        for (int v = 0; v < 3; ++v) {
+        for (int rb = kb; rb < 2; ++rb)
 #pragma unroll
-          for (int rb = 0; rb < 2; ++rb)
+          for (int t = 0; t < 2; ++t) O[rb][t] = mm32(fp[kb][rb][t][PA[v]], bo[kb][PB[v]], O[rb][t]);
 #pragma unroll
-            for (int t = 0; t < NF; ++t)
-              if (rb >= kb) O[rb][t] = M::mm(fp[j & PIPE][rb][t][PA[v]], c[j & PIPE][PB[v]], O[rb][t]);
-        }
+      for (int d0 = 0; d0 < DB; d0 += 2)         // (two blocks at a time: the first are done early)
 #pragma unroll
         for (int v = 2; v >= 0; --v)
 #pragma unroll
-          for (int db = 0; db < DB; ++db)
+          for (int db = d0; db < d0 + 2; ++db)
 #pragma unroll
-            for (int t = 0; t < NF; ++t) S[db][t] = M::mm(fs[j & PIPE][db][t], b[j & PIPE][v], S[db][t]);
-        if constexpr (PIPE) if (j + 1 < J2) {
-          interleave<(3 * DB + 3) * NF, 1, (NF == 1 ? 6 : 4)>();
-          __builtin_amdgcn_sched_barrier(0);
-        }
+            for (int t = 0; t < 2; ++t) S[db][t] = mm32(fs[kb][db][t], bu[kb][v], S[db][t]);
+      if (kb == 0) {
+        region<12 + 6 * DB, 1, 3>();
+        copies(5 * DB + 2, UNITS);
       }
     }
-    // the outputs, columns of 64 tokens (eight swizzled pieces), over the wave's
-    // part of V, and back as rows of eight columns by transposing reads
-    wave_lds_sync();
+    unsigned char* so = smem + buf * L::BUF + L::V + wv * 2048;
 #pragma unroll
-    for (int rb = 0; rb < 2; ++rb)
+    for (int rb = 0; rb < 2; ++rb) {
+      bf16x8 w;
 #pragma unroll
-      for (int s8 = 0; s8 < NB / 8; ++s8) {
-        bf16x8 w;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = (__bf16)O[rb][(8 * s8 + e) / AR][(8 * s8 + e) % AR];
-        const int pc = (32 * rb + M::index(lane, 8 * s8)) >> 3;
-        *reinterpret_cast<bf16x8*>(s_v + n * 128 + (pc ^ (n & 7)) * 16) = w;
-      }
-    wave_lds_sync();
-#pragma unroll
-    for (int u = 0; u < OU; ++u) {
-      // lane i of a group: column 8 og + i / 4 (and + 4), tokens 4 (i % 4) ..
-      const int t = (lane >> 4) / OG * 16 + u * (64 / OG) + tc, c = 8 * og + ti;
-      auto at = [&](int cc) { return s_v + cc * 128 + ((t >> 3) ^ (cc & 7)) * 16 + (t & 7) * 2; };
-      out[u] = __builtin_bit_cast(u32x4, join(read_tr(at(c)), read_tr(at(c + 4))));
+      for (int e = 0; e < 8; ++e) w[e] = (__bf16)O[rb][e >> 2][e & 3];
+      *reinterpret_cast<bf16x8*>(so + n * 128 + ((4 * rb + hi) ^ (n & 7)) * 16) = w;
     }
-    wave_lds_sync();
-    if (!PIPE && left > 0) {                     // one buffer: everybody has read it
-      __syncthreads();
-      copies(t0 + PC, nt, 0);
-    }
+    float x[8];
+    rows8(S[0], x);
+    split8<3>(x, ss[0]);
+    region<6 + 6 * DB, 0, 3>();
   }
-  if (pt.len > 0) store_out(t0 - PC, pt.len - (t0 - PC));
+  if (pt.len > 0) {
+    wave_lds_sync();
+    read_out(sb + L::V + wv * 2048);
+    store_out(t0 - PC, pt.len - (t0 - PC));
+  }
 
 #pragma unroll
   for (int db = 0; db < DB; ++db)
 #pragma unroll
-    for (int r = 0; r < NB; ++r) Sg[(size_t)(32 * db + M::index(lane, r)) * DV] = S[db][r / AR][r % AR];
+    for (int e = 0; e < 8; ++e) Sg[(size_t)(32 * db + 8 * hi + e) * DV] = S[db][e >> 2][e & 3];
   if (!p.prime) return;
   const int off = p.sk.off[h], rank = p.sk.off[h + 1] - off;
   if (rank == 0) {                               // a dense-fallback head: the state copy
     int slot = 0;
     while (slot + 1 < p.sk.ndense && p.sk.dense_list[slot] != h) ++slot;
-    bf16* C = reinterpret_cast<bf16*>(p.sk.Sc) + ((size_t)pt.b * p.sk.ndense + slot) * DK * DV + col;
+    bf16* C = reinterpret_cast<bf16*>(p.sk.Sc) + ((size_t)pt.b * p.sk.ndense + slot) * DK * DV + c0 + n;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
-      for (int r = 0; r < NB; ++r)
-        C[(size_t)(32 * db + M::index(lane, r)) * DV] = f32_to_bf16(S[db][r / AR][r % AR]);
+      for (int e = 0; e < 8; ++e) C[(size_t)(32 * db + 8 * hi + e) * DV] = f32_to_bf16(S[db][e >> 2][e & 3]);
     return;
   }
-  bf16* Ug = reinterpret_cast<bf16*>(p.sk.U) + ((size_t)pt.b * p.sk.R + off) * DV + col;
+  bf16* Ug = reinterpret_cast<bf16*>(p.sk.U) + ((size_t)pt.b * p.sk.R + off) * DV + c0 + n;
   for (int j = 0; j < rank; ++j) {               // u_j = S^T p_j
     const float* P = p.sk.Pt + (size_t)(off + j) * DK + 8 * hi;
     float a = 0.f;
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+    for (int db = 0; db < DB; ++db) {
+      float x[8], w[8];
+      rows8(S[db], x);
+      ldn<8>(P + 32 * db, w);
 #pragma unroll
-      for (int s = 0; s < M::STEPS; ++s) {
-        float x[8], w[8];
-        block8(S[db], s, x);
-        ldn<8>(P + 32 * db + M::KS * s, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a += x[e] * w[e];
-      }
-    if (M::MT == 16) a += __shfl_xor(a, 16);
-    a += __shfl_xor(a, 32);
+      for (int e = 0; e < 8; ++e) a += x[e] * w[e];
+    }
+    a = xsum<4, 2>(a);                           // over the four row groups
     if (hi == 0) Ug[(size_t)j * DV] = f32_to_bf16(a);
   }
 }
 
-template <int DK, int DV, int CW, int BUFS>
+template <int DK, int DV>
 int launch(const PromptParams& p, hipStream_t st) {
-  hipLaunchKernelGGL((prompt_prep_kernel<DK, CW>), dim3((unsigned)p.nslots * p.H), dim3(256), 0, st, p);
-  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, CW, BUFS>), dim3((unsigned)p.nseq * p.H * (DV / (4 * CW))), dim3(256),
-                     0, st, p);
+  hipLaunchKernelGGL((prompt_prep_kernel<DK>), dim3((unsigned)p.nslots * p.H), dim3(256), 0, st, p);
+  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV>), dim3((unsigned)p.nseq * p.H * (DV / VC)), dim3(256), 0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 }  // namespace
 
 int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st) {
-  const bool few = p.nseq * p.H <= 256;
-  if (dk == 64 && dv == 64) return few ? launch<64, 64, 16, 2>(p, st) : launch<64, 64, 16, 1>(p, st);
-  if (dk == 128 && dv == 64) return few ? launch<128, 64, 16, 2>(p, st) : launch<128, 64, 16, 1>(p, st);
-  if (dk == 128 && dv == 128) return few ? launch<128, 128, 16, 2>(p, st) : launch<128, 128, 32, 1>(p, st);
+  if (dk == 64 && dv == 64) return launch<64, 64>(p, st);
+  if (dk == 128 && dv == 64) return launch<128, 64>(p, st);
+  if (dk == 128 && dv == 128) return launch<128, 128>(p, st);
   return -2;
 }
 

@@ -42,43 +42,14 @@ __device__ __forceinline__ bf16x8 as_frag(const u32x4& x) { return __builtin_bit
 // another never share a slot, and there are at most tokens / 64 + nseq.
 __device__ __forceinline__ int first_slot(int start, int i) { return (start >> 6) + i; }
 
-// Matrix instruction for waves of CW columns, and where its operands lie.  A
-// block of 32 rows x CW columns is NB registers of a lane, and register r is
-// row index(lane, r): eight consecutive rows for each step of the k axis, which
-// is the B operand of the next product as it stands.  For that the rows that
-// go into the A operand are permuted: MFMA row m of tile t is row(m, t).
-template <int CW> struct Mf;
-template <> struct Mf<32> {
-  typedef f32x16 Acc;
-  static constexpr int MT = 32, KS = 16, TILES = 1, STEPS = 2, NB = 16;
-  static __device__ __forceinline__ Acc mm(bf16x8 a, bf16x8 b, Acc c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ int row(int m, int) {
-    return (m & 19) | ((m & 4) << 1) | ((m & 8) >> 1);
-  }
-  static __device__ __forceinline__ int index(int lane, int r) { return 16 * (r >> 3) + 8 * (lane >> 5) + (r & 7); }
-  static __device__ __forceinline__ int swizzle(int row) { return row & 15; }
-};
-template <> struct Mf<16> {
-  typedef f32x4s Acc;
-  static constexpr int MT = 16, KS = 32, TILES = 2, STEPS = 1, NB = 8;
-  static __device__ __forceinline__ Acc mm(bf16x8 a, bf16x8 b, Acc c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ int row(int m, int t) { return ((m & 12) << 1) | (t << 2) | (m & 3); }
-  static __device__ __forceinline__ int index(int lane, int r) { return 8 * (lane >> 4) + r; }
-  static __device__ __forceinline__ int swizzle(int row) { return (row & 3) | ((row >> 1) & 12); }
-};
-
-// Row and first k index, within a 32 x 32 block, of lane's part of fragment f
-// (0 or 1: the tile or the step) of that block.
-template <int CW>
-__device__ __forceinline__ void frag_at(int lane, int f, int* row, int* k) {
-  using M = Mf<CW>;
-  const int t = M::TILES == 2 ? f : 0, s = M::STEPS == 2 ? f : 0;
-  *row = M::row(lane % M::MT, t);
-  *k = s * M::KS + 8 * (lane / M::MT);
+// Operands of v_mfma_f32_16x16x32_bf16 (hi = lane / 16, n = lane % 16).  A
+// block of 32 rows x 16 columns is two result tiles of four registers; MFMA
+// row m of tile t is row ((m & 12) << 1) | (t << 2) | (m & 3) of the block, so
+// that a lane's eight registers are rows 8 hi .. 8 hi + 7 of column n: the B
+// operand of the next product as they stand, and runs of eight tokens.
+__device__ __forceinline__ int block_row(int m, int t) { return ((m & 12) << 1) | (t << 2) | (m & 3); }
+__device__ __forceinline__ f32x4s mm32(bf16x8 a, bf16x8 b, f32x4s c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 // Eight fp32 values as bf16 fragments whose sum they are (three: exactly; the
