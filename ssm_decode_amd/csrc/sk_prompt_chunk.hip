@@ -1,4 +1,6 @@
 // The two launches of the chunked form (see sk_prompt_chunk.hpp).
+#include <type_traits>
+
 #include "sk_prompt_chunk.hpp"
 
 namespace sk {
@@ -256,7 +258,7 @@ struct ChunkLds {
   static constexpr int Q = K + PC * DK * 2;
   static constexpr int V = Q + PC * DK * 2;      // wave after wave: [64][16], then the outputs [16][64]
   static constexpr int W = V + PC * VC * 2;      // a chunk's workspace as it is
-  static constexpr int BUF = W + (CHUNK_WORK_BYTES + 1023) / 1024 * 1024;
+  static constexpr int BUF = W + CHUNK_WORK_BYTES + PROMPT_WORK_OVER;
   static constexpr int BYTES = 2 * BUF;
   static_assert(BYTES <= 160 * 1024, "LDS of a CU");
 };
@@ -302,6 +304,20 @@ __device__ __forceinline__ void region() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// The prompt of rank r by length, for up to 64 prompts (a lane each): the last
+// workgroups to start are then the shortest.  More prompts are taken as listed.
+__device__ __forceinline__ int longest_first(const PromptParams& p, int r) {
+  if (p.nseq > 64) return r;
+  const int lane = threadIdx.x & 63, mine = lane < p.nseq ? lane : 0;
+  const int len = p.start[mine + 1] - p.start[mine];
+  int before = 0;
+  for (int j = 0; j < p.nseq; ++j) {
+    const int other = __builtin_amdgcn_readlane(len, j);
+    before += other > len || (other == len && j < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < p.nseq && before == r));
+}
+
 template <int DK, int DV>
 __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   using L = ChunkLds<DK>;
@@ -312,7 +328,7 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   // (the parts of a tile are nseq * H workgroups apart: mostly on one XCD,
   // whose cache then serves the K, Q, T and P that they share)
   const int tiles = p.nseq * p.H, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
-  const int i = tile / p.H, h = tile - i * p.H;
+  const int i = longest_first(p, tile / p.H), h = tile % p.H;
   if ((int64_t)p.start[i + 1] - p.start[i] <= p.len_lo) return;
   const PromptTile pt = prompt_tile(p, i, h);
   if (!pt.ok) return;
@@ -335,25 +351,44 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   auto piece = [&](int row, int pc) { return row * PPR + (pc ^ swz(row)); };
   const uint32_t lds0 = lds_address(smem);
   constexpr int KU = PPR / 4, KROWS = 256 / PPR;           // a wave's units of 64 pieces of K, rows from one to the next
-  constexpr int WFULL = CHUNK_WORK_BYTES / 1024, WREST = CHUNK_WORK_BYTES / 16 % 64;
-  constexpr int WU = (WFULL + 4) / 4, UNITS = 2 * KU + 2 + WU;
-  static_assert(WREST > 0 && WFULL % 4 != 3, "the last unit of the workspace is a part");
+  // (the workspace's last units reach into what lies behind it)
+  constexpr int WU = (CHUNK_WORK_BYTES + PROMPT_WORK_OVER) / 4096, UNITS = 2 * KU + 2 + WU;
+  static_assert((CHUNK_WORK_BYTES + PROMPT_WORK_OVER) % 4096 == 0, "whole units for each of the four waves");
   const int krow = (wv * 64 + lane) / PPR, kpc = lane % PPR, vrow = lane >> 1, vpc = (lane & 1) * 8;
-  // unit u of the whole chunk at t0 into a buffer: K, Q, then the workspace, V last
-  auto copy_unit = [&](int u, int t0, uint32_t l0) {
-    if (u < 2 * KU) {
-      const int v = u < KU ? u : u - KU, row = krow + KROWS * v;
-      const int64_t st = u < KU ? p.ks : p.qs;
-      const bf16* src = (u < KU ? kp : qp) + (int64_t)(t0 + krow) * st + v * KROWS * st;
-      copy16(src + (kpc ^ swz(row)) * 8, l0 + (u < KU ? L::K : L::Q) + (4 * v + wv) * 1024);
+  // unit u of a whole chunk into a buffer: K, Q, then the workspace, V last.
+  // The lane's addresses go from chunk to chunk; the swizzle of K and Q rows
+  // differs between a wave's even and odd units only.
+  const bf16 *kc[2], *qc[2], *vc = vp + (int64_t)vrow * p.vs + vpc;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const int pc = (kpc ^ swz(krow + KROWS * v)) * 8;
+    kc[v] = kp + (int64_t)krow * p.ks + pc;
+    qc[v] = qp + (int64_t)krow * p.qs + pc;
+  }
+  const unsigned char* wc = wp + wv * 1024 + lane * 16;
+  const int64_t kstep = KROWS * p.ks, qstep = KROWS * p.qs;
+  auto copy_unit = [&](int u, uint32_t l0) {
+    if (u < KU) {
+      copy16(kc[u & 1] + u * kstep, l0 + L::K + (4 * u + wv) * 1024);
+    } else if (u < 2 * KU) {
+      const int v = u - KU;
+      copy16(qc[v & 1] + v * qstep, l0 + L::Q + (4 * v + wv) * 1024);
     } else if (u < 2 * KU + WU) {
-      const int unit = 4 * (u - 2 * KU) + wv;
-      const unsigned char* src = wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES + unit * 1024 + lane * 16;
-      if (unit < WFULL || (unit == WFULL && lane < WREST)) copy16(src, l0 + L::W + unit * 1024);
+      const int v = u - 2 * KU;
+      copy16(wc + v * 4096, l0 + L::W + (4 * v + wv) * 1024);
     } else {
       const int v = u - 2 * KU - WU;
-      copy16(vp + (int64_t)(t0 + vrow) * p.vs + v * 32 * p.vs + vpc, l0 + L::V + wv * 2048 + v * 1024);
+      copy16(vc + v * 32 * p.vs, l0 + L::V + wv * 2048 + v * 1024);
     }
+  };
+  auto next_chunk = [&]() {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      kc[v] += PC * p.ks;
+      qc[v] += PC * p.qs;
+    }
+    vc += PC * p.vs;
+    wc += (size_t)p.H * CHUNK_WORK_BYTES;
   };
   // The whole of a chunk that may be a prompt's last: rows behind its end
   // repeat its last one (their beta in T is 0, their columns of P meet only
@@ -370,7 +405,9 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
     for (int v = 0; v < 2; ++v)
       copy16(vp + at(vrow + 32 * v) * p.vs + vpc, l0 + L::V + wv * 2048 + v * 1024);
 #pragma unroll 1
-    for (int u = 2 * KU; u < 2 * KU + WU; ++u) copy_unit(u, t0, l0);
+    for (int v = 0; v < WU; ++v)
+      copy16(wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES + (4 * v + wv) * 1024 + lane * 16,
+             l0 + L::W + (4 * v + wv) * 1024);
   };
   if (pt.len > 0) copy_all(0, pt.len < PC ? pt.len : PC, lds0);
 
@@ -428,8 +465,11 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
     rows8(S[0], x);
     split8<3>(x, ss[0]);
   }
-  int t0 = 0;
-  for (int buf = 0; t0 < pt.len; t0 += PC, buf ^= 1) {
+  int t0 = 0, buf = 0;
+  // one chunk; `more`: a whole one follows (no branch may then stand between
+  // two regions, or work for the second is not done in the first)
+  auto chunk = [&](auto more) {
+    constexpr bool MORE = decltype(more)::value;
     // this wave's copies for the chunk have landed, then everybody's; and
     // everybody has read the other buffer
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -439,17 +479,15 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
     const unsigned char* s_v = sb + L::V + wv * 2048;
     const int left = pt.len - t0 - PC;
     const uint32_t lnext = lds0 + (buf ^ 1) * L::BUF;
-    const bool whole = left >= PC;               // uniform: the next chunk is whole
     auto copies = [&](int from, int to) {
-      if (whole) {
+      if constexpr (MORE) {
 #pragma unroll
         for (int u = from; u < to; ++u)
-          if (u < UNITS) copy_unit(u, t0 + PC, lnext);
+          if (u < UNITS) copy_unit(u, lnext);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     };
 
-    // what the chunk's beginning needs from LDS, all at once
     bf16x8 fa[2][2][2], ft[2][2][2][3], fp[2][2][2][2], fs[2][DB][2], vv[2];
     float gm[2][8], dm[2][8];
     auto load_kq = [&](int at, int j) {
@@ -459,18 +497,11 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
         for (int t = 0; t < 2; ++t) fa[j & 1][rb][t] = frag_kq(at, rb, t, j % DB);
     };
     load_kq(L::K, 0);
-    if (t0 > 0) read_out(smem + (buf ^ 1) * L::BUF + L::V + wv * 2048);
-#pragma unroll
-    for (int rb = 0; rb < 2; ++rb) {
-      ldn<8>(s_g + 32 * rb + 8 * hi, gm[rb]);
-      ldn<8>(s_g + PC + 32 * rb + 8 * hi, dm[rb]);
-      const unsigned char* sv = s_v + (32 * rb + 8 * hi + ti) * 32 + tc * 2;
-      vv[rb] = join(read_tr(sv), read_tr(sv + 4 * 32));
-    }
-    const float gC = s_g[PC - 1];
     __builtin_amdgcn_sched_barrier(0);
-    if (t0 > 0) store_out(t0 - PC, PC);
-    if (left > 0 && !whole) copy_all(t0 + PC, left, lnext);
+    if (t0 > 0) read_out(smem + (buf ^ 1) * L::BUF + L::V + wv * 2048);
+    const float gC = s_g[PC - 1];
+    next_chunk();
+    if (!MORE && left > 0) copy_all(t0 + PC, left, lnext);
     __builtin_amdgcn_sched_barrier(0);
 
     Block R[2], O[2], U[2];
@@ -495,9 +526,18 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
         for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
           for (int t = 0; t < 2; ++t) R[rb][t] = mm32(fa[j & 1][rb][t], ss[j][v], R[rb][t]);
+      if (j < 2) {                               // what R and U need besides
+        const int rb = j;
+        ldn<8>(s_g + 32 * rb + 8 * hi, gm[rb]);
+        ldn<8>(s_g + PC + 32 * rb + 8 * hi, dm[rb]);
+        const unsigned char* sv = s_v + (32 * rb + 8 * hi + ti) * 32 + tc * 2;
+        vv[rb] = join(read_tr(sv), read_tr(sv + 4 * 32));
+      }
       region<12, 1, 4>();
-      copies(3 * j, 3 * j + 3);
+      copies(2 * j, 2 * j + 2);
     }
+    if (t0 > 0) store_out(t0 - PC, PC);
+    __builtin_amdgcn_sched_barrier(0);
     bf16x8 br[2][3];
     auto load_t = [&](int kb) {
 #pragma unroll
@@ -527,7 +567,7 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
           split8<3>(x, br[rb]);
         }
       region<8, 2, 8>();
-      copies(3 * DB + 2 * j, 3 * DB + 2 * j + 2);
+      copies(2 * DB + j, 2 * DB + j + 1);
     }
     bf16x8 bu[2][3], bo[2][2];
     auto split_u = [&](int kb) {
@@ -571,10 +611,11 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
           for (int db = 0; db < DB; ++db) S[db][e >> 2][e & 3] *= gC;
         }
         region<24, 1, 2>();
-        copies(5 * DB, 5 * DB + 2);
+        copies(3 * DB, 3 * DB + 2);
       } else {
         split_u(0);                              // (U's first block has no second step)
         region<12, 2, 7>();
+        copies(3 * DB + 2, 3 * DB + 3);
       }
     }
     // O += P U;  S += K^T (D_C U)
@@ -601,7 +642,7 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
             for (int t = 0; t < 2; ++t) S[db][t] = mm32(fs[kb][db][t], bu[kb][v], S[db][t]);
       if (kb == 0) {
         region<12 + 6 * DB, 1, 3>();
-        copies(5 * DB + 2, UNITS);
+        copies(3 * DB + 3, UNITS);
       }
     }
     unsigned char* so = smem + buf * L::BUF + L::V + wv * 2048;
@@ -616,7 +657,11 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
     rows8(S[0], x);
     split8<3>(x, ss[0]);
     region<6 + 6 * DB, 0, 3>();
-  }
+    t0 += PC;
+    buf ^= 1;
+  };
+  while (pt.len - t0 >= 2 * PC) chunk(std::true_type{});
+  while (t0 < pt.len) chunk(std::false_type{});
   if (pt.len > 0) {
     wave_lds_sync();
     read_out(sb + L::V + wv * 2048);

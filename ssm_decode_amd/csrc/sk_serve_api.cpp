@@ -100,7 +100,7 @@ int64_t sketchssm_prefill_workspace_bytes(const sketchssm_layer* layer, int32_t 
     if (!chunks(layer, tokens)) return 0;
     const int64_t tiles = sk::prompt_slots(tokens, nseq) * layer->heads;
     if (tiles > INT32_MAX / 2) return SKSSM_EDIM;
-    return tiles * sk::PROMPT_CHUNK_WORK;
+    return tiles * sk::PROMPT_CHUNK_WORK + sk::PROMPT_WORK_OVER;
   } catch (...) {
     return SKSSM_ELAUNCH;
   }
