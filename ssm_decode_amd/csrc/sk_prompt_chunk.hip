@@ -22,7 +22,9 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   float* s_A = reinterpret_cast<float*>(s_big);
   float* s_P = reinterpret_cast<float*>(s_big + MB);
 
-  const int slot = blockIdx.x / p.H, h = blockIdx.x - slot * p.H;
+  // (the last chunks first: what the next launch begins with is then the most
+  // recent in the memory-side cache)
+  const int rslot = blockIdx.x / p.H, h = blockIdx.x - rslot * p.H, slot = p.nslots - 1 - rslot;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   // the last prompt whose first slot is not behind this one
   int i = -1;
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
 }
 
 // ------------------------------------------------------ chunk after chunk
-// One workgroup of four waves per (prompt, head, 64 columns); a wave holds 16
+// One workgroup of NW waves per (prompt, head, 16 NW columns); a wave holds 16
 // columns of the state, all rows, in registers.  K, Q, V, T and P are in LDS
 // twice: the next chunk's copy, straight from memory, is in flight over the
 // present chunk.  K^T and V's columns come by transposing LDS reads.
@@ -250,14 +252,12 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
 // step, the LDS reads of the next step's fragments, and the vector work (three
 // value splits above all) that a later step needs; the vector work runs in the
 // shadow of the matrix instructions only where it stands between them.
-constexpr int VC = 64;                           // columns of a workgroup
-
-template <int DK>
+template <int DK, int NW>
 struct ChunkLds {
   static constexpr int K = 0;
   static constexpr int Q = K + PC * DK * 2;
   static constexpr int V = Q + PC * DK * 2;      // wave after wave: [64][16], then the outputs [16][64]
-  static constexpr int W = V + PC * VC * 2;      // a chunk's workspace as it is
+  static constexpr int W = V + PC * NW * 32;     // a chunk's workspace as it is
   static constexpr int BUF = W + CHUNK_WORK_BYTES + PROMPT_WORK_OVER;
   static constexpr int BYTES = 2 * BUF;
   static_assert(BYTES <= 160 * 1024, "LDS of a CU");
@@ -318,11 +318,14 @@ __device__ __forceinline__ int longest_first(const PromptParams& p, int r) {
   return __builtin_ctzll(__ballot(lane < p.nseq && before == r));
 }
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
-  using L = ChunkLds<DK>;
+template <int DK, int DV, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p) {
+  using L = ChunkLds<DK, NW>;
   constexpr int PPR = DK / 8, DB = DK / 32;      // 16-byte pieces of a row, blocks of 32 rows
-  __shared__ __align__(1024) unsigned char smem[L::BYTES];
+  // (dynamic: a workgroup of four waves, alone on its CU by its LDS, would
+  // otherwise be given more than 256 registers a lane, half of them accumulation
+  // registers that vector instructions reach by moves only)
+  extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, hi = lane >> 4;
   // (the parts of a tile are nseq * H workgroups apart: mostly on one XCD,
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   const PromptTile pt = prompt_tile(p, i, h);
   if (!pt.ok) return;
 
-  const int c0 = part * VC + wv * 16;            // the wave's first column
+  const int c0 = part * NW * 16 + wv * 16;       // the wave's first column
   float* Sg = p.S + ((size_t)pt.b * p.H + h) * DK * DV + c0 + n;
   const bf16* kp = reinterpret_cast<const bf16*>(p.k) + pt.s0 * p.ks + (int64_t)h * DK;
   const bf16* qp = reinterpret_cast<const bf16*>(p.q) + pt.s0 * p.qs + (int64_t)h * DK;
@@ -350,10 +353,12 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   };
   auto piece = [&](int row, int pc) { return row * PPR + (pc ^ swz(row)); };
   const uint32_t lds0 = lds_address(smem);
-  constexpr int KU = PPR / 4, KROWS = 256 / PPR;           // a wave's units of 64 pieces of K, rows from one to the next
-  // (the workspace's last units reach into what lies behind it)
-  constexpr int WU = (CHUNK_WORK_BYTES + PROMPT_WORK_OVER) / 4096, UNITS = 2 * KU + 2 + WU;
-  static_assert((CHUNK_WORK_BYTES + PROMPT_WORK_OVER) % 4096 == 0, "whole units for each of the four waves");
+  constexpr int KU = PPR / NW, KROWS = 64 * NW / PPR;      // a wave's units of 64 pieces of K, rows from one to the next
+  // (the workspace's last unit reaches into what lies behind it; there is one
+  // unit less than the waves take, and the last takes the first once more)
+  constexpr int WUNITS = (CHUNK_WORK_BYTES + PROMPT_WORK_OVER) / 1024, WU = (WUNITS + 1) / NW, UNITS = 2 * KU + 2 + WU;
+  static_assert((CHUNK_WORK_BYTES + PROMPT_WORK_OVER) % 1024 == 0 && (WUNITS + 1) % NW == 0, "units of the waves");
+  const int wlast = (WU - 1) * NW + wv < WUNITS ? (WU - 1) * NW + wv : 0;
   const int krow = (wv * 64 + lane) / PPR, kpc = lane % PPR, vrow = lane >> 1, vpc = (lane & 1) * 8;
   // unit u of a whole chunk into a buffer: K, Q, then the workspace, V last.
   // The lane's addresses go from chunk to chunk; the swizzle of K and Q rows
@@ -365,17 +370,17 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
     kc[v] = kp + (int64_t)krow * p.ks + pc;
     qc[v] = qp + (int64_t)krow * p.qs + pc;
   }
-  const unsigned char* wc = wp + wv * 1024 + lane * 16;
+  const unsigned char* wc = wp + lane * 16;
   const int64_t kstep = KROWS * p.ks, qstep = KROWS * p.qs;
   auto copy_unit = [&](int u, uint32_t l0) {
     if (u < KU) {
-      copy16(kc[u & 1] + u * kstep, l0 + L::K + (4 * u + wv) * 1024);
+      copy16(kc[u & 1] + u * kstep, l0 + L::K + (NW * u + wv) * 1024);
     } else if (u < 2 * KU) {
       const int v = u - KU;
-      copy16(qc[v & 1] + v * qstep, l0 + L::Q + (4 * v + wv) * 1024);
+      copy16(qc[v & 1] + v * qstep, l0 + L::Q + (NW * v + wv) * 1024);
     } else if (u < 2 * KU + WU) {
-      const int v = u - 2 * KU;
-      copy16(wc + v * 4096, l0 + L::W + (4 * v + wv) * 1024);
+      const int unit = u < 2 * KU + WU - 1 ? NW * (u - 2 * KU) + wv : wlast;
+      copy16(wc + unit * 1024, l0 + L::W + unit * 1024);
     } else {
       const int v = u - 2 * KU - WU;
       copy16(vc + v * 32 * p.vs, l0 + L::V + wv * 2048 + v * 1024);
@@ -398,16 +403,17 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
 #pragma unroll 1
     for (int v = 0; v < KU; ++v) {
       const int row = krow + KROWS * v, pc = (kpc ^ swz(row)) * 8;
-      copy16(kp + at(row) * p.ks + pc, l0 + L::K + (4 * v + wv) * 1024);
-      copy16(qp + at(row) * p.qs + pc, l0 + L::Q + (4 * v + wv) * 1024);
+      copy16(kp + at(row) * p.ks + pc, l0 + L::K + (NW * v + wv) * 1024);
+      copy16(qp + at(row) * p.qs + pc, l0 + L::Q + (NW * v + wv) * 1024);
     }
 #pragma unroll 1
     for (int v = 0; v < 2; ++v)
       copy16(vp + at(vrow + 32 * v) * p.vs + vpc, l0 + L::V + wv * 2048 + v * 1024);
 #pragma unroll 1
-    for (int v = 0; v < WU; ++v)
-      copy16(wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES + (4 * v + wv) * 1024 + lane * 16,
-             l0 + L::W + (4 * v + wv) * 1024);
+    for (int v = 0; v < WU; ++v) {
+      const int unit = v + 1 < WU ? NW * v + wv : wlast;
+      copy16(wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES + unit * 1024 + lane * 16, l0 + L::W + unit * 1024);
+    }
   };
   if (pt.len > 0) copy_all(0, pt.len < PC ? pt.len : PC, lds0);
 
@@ -701,19 +707,20 @@ __global__ void __launch_bounds__(256, 1) prompt_chunk_kernel(PromptParams p) {
   }
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int NW>
 int launch(const PromptParams& p, hipStream_t st) {
   hipLaunchKernelGGL((prompt_prep_kernel<DK>), dim3((unsigned)p.nslots * p.H), dim3(256), 0, st, p);
-  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV>), dim3((unsigned)p.nseq * p.H * (DV / VC)), dim3(256), 0, st, p);
+  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, NW>), dim3((unsigned)p.nseq * p.H * (DV / (16 * NW))), dim3(64 * NW),
+                     (ChunkLds<DK, NW>::BYTES), st, p);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 }  // namespace
 
 int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st) {
-  if (dk == 64 && dv == 64) return launch<64, 64>(p, st);
-  if (dk == 128 && dv == 64) return launch<128, 64>(p, st);
-  if (dk == 128 && dv == 128) return launch<128, 128>(p, st);
+  if (dk == 64 && dv == 64) return launch<64, 64, 4>(p, st);
+  if (dk == 128 && dv == 64) return launch<128, 64, 4>(p, st);
+  if (dk == 128 && dv == 128) return p.nseq * p.H <= 128 ? launch<128, 128, 4>(p, st) : launch<128, 128, 8>(p, st);
   return -2;
 }
 

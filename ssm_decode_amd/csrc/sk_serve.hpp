@@ -77,7 +77,7 @@ struct NormParams {
 // head, and whether the shape has it.
 constexpr int PROMPT_CHUNK = 64;
 constexpr int PROMPT_CHUNK_WORK = 30 * 1024 + 512;
-constexpr int PROMPT_WORK_OVER = 1536;    // read, not used, behind the last one
+constexpr int PROMPT_WORK_OVER = 512;    // read, not used, behind the last one
 inline bool prompt_chunked(int dk, int act) { return act == DT_BF16 && dk >= 64; }
 // Chunk slots that nseq prompts of together up to `tokens` tokens may take.
 inline int64_t prompt_slots(int64_t tokens, int64_t nseq) { return tokens / PROMPT_CHUNK + nseq; }

@@ -134,18 +134,18 @@ def test_prefill_workspace():
     assert abi.sketchssm_prefill_workspace_bytes(_layer(OK_OFF), 1, 1) == abi.SKSSM_EDIM
     assert abi.sketchssm_prefill_workspace_bytes(gdn(), 0, 0) == 0
     # the chunked form (bf16, dk >= 64, more than 16 tokens): a slot for every 64
-    # tokens and one for every prompt, 30.5 KiB for each of its heads, and 1.5 KiB
+    # tokens and one for every prompt, 30.5 KiB for each of its heads, and 0.5 KiB
     L = gdn(dk=64, dv=64, act=abi.SKSSM_BF16, sk=abi.SKSSM_BF16)
     assert abi.sketchssm_prefill_workspace_bytes(L, 16, 2) == 0
-    assert abi.sketchssm_prefill_workspace_bytes(L, 17, 2) == 2 * 4 * 31232 + 1536
-    assert abi.sketchssm_prefill_workspace_bytes(L, 640, 2) == 12 * 4 * 31232 + 1536
-    assert abi.sketchssm_prefill_workspace_bytes(L, (1 << 31) - 1, 2) == (33554431 + 2) * 4 * 31232 + 1536
+    assert abi.sketchssm_prefill_workspace_bytes(L, 17, 2) == 2 * 4 * 31232 + 512
+    assert abi.sketchssm_prefill_workspace_bytes(L, 640, 2) == 12 * 4 * 31232 + 512
+    assert abi.sketchssm_prefill_workspace_bytes(L, (1 << 31) - 1, 2) == (33554431 + 2) * 4 * 31232 + 512
     assert abi.sketchssm_prefill_workspace_bytes(gdn(), 640, 2) == 0
     big = _layer(np.arange(129) * 4, family=abi.SKSSM_GDN, heads=128, groups=128, dk=64, dv=64, act=abi.SKSSM_BF16,
                  sk=abi.SKSSM_BF16)
     assert abi.sketchssm_prefill_workspace_bytes(big, (1 << 31) - 1, 2) == abi.SKSSM_EDIM
     strides = dict(q_stride=256, k_stride=256, v_stride=256, o_stride=256, tokens=640)
-    for bad in (dict(work=None), dict(work=FAKE + 8), dict(work_bytes=12 * 4 * 31232 + 1535)):
+    for bad in (dict(work=None), dict(work=FAKE + 8), dict(work_bytes=12 * 4 * 31232 + 511)):
         assert abi.sketchssm_prefill(L, _bufs(), prompts(**strides, **bad)) == abi.SKSSM_EINVAL
 
 
