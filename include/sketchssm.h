@@ -323,8 +323,8 @@ int sketchssm_read_noalloc(const sketchssm_layer* layer, const sketchssm_buffers
 /* Prompts of the gated delta rule: token rows of nseq prompts, one behind the
  * other.  Rows are [H][dk] or [H][dv] elements in a row; the strides are the
  * elements from one token's row to the next (rows may be slices of one
- * projection's output), at least a row, at most 2^31 - 1, and a multiple of
- * 16 bytes for q, k, v and o. */
+ * projection's output), at least a row, at most 2^25, and a multiple of 16
+ * bytes for q, k, v and o. */
 typedef struct {
   const void* q;             /* [tokens][H][dk] act dtype */
   const void* k;             /* [tokens][H][dk] act dtype */
@@ -417,7 +417,7 @@ typedef struct {
   const float* weight;       /* [groups][width], or [width] for every group; NULL: 1 */
   const float* bias;         /* as weight; NULL: 0 */
   int64_t x_stride, gate_stride, y_stride; /* elements from a row to the next: at least a row, at most
-                                2^31 - 1, a multiple of 16 bytes */
+                                2^25, a multiple of 16 bytes */
   int64_t rows;
   int32_t groups;            /* 1 to 65535 */
   int32_t width;             /* 8 to 8192, a multiple of 8 */

@@ -26,18 +26,27 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   // recent in the memory-side cache)
   const int rslot = blockIdx.x / p.H, h = blockIdx.x - rslot * p.H, slot = p.nslots - 1 - rslot;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  // the last prompt whose first slot is not behind this one
-  int i = -1;
+  // the last prompt taken in chunks whose first slot is not behind this one
+  int i = -1, rank = 0, ranks = 0;
   for (int j0 = 0; j0 < p.nseq; j0 += 64) {
-    const int j = j0 + lane;
-    const unsigned long long m = __ballot(j < p.nseq && first_slot(p.start[j < p.nseq ? j : 0], j) <= slot);
-    if (m) i = j0 + 63 - __clzll(m);
+    const int j = j0 + lane < p.nseq ? j0 + lane : p.nseq - 1;
+    const int a = p.start[j];
+    const bool mine = j0 + lane < p.nseq && (int64_t)p.start[j + 1] - a > p.len_lo;
+    const unsigned long long all = __ballot(mine);
+    const int r = ranks + __popcll(all & ((1ull << lane) - 1));
+    const unsigned long long m = __ballot(mine && first_slot(a, r) <= slot);
+    if (m) {
+      const int l = 63 - __clzll(m);
+      i = j0 + l;
+      rank = ranks + __popcll(all & ((1ull << l) - 1));
+    }
+    ranks += __popcll(all);
   }
   if (i < 0) return;
   const int s0 = p.start[i], s1 = p.start[i + 1];
-  if (s0 < 0 || s1 < s0 || s1 > p.tokens) return;      // (reported by the other launch)
-  const int c0 = (slot - first_slot(s0, i)) * PC, len = s1 - s0;
-  if (c0 >= len || len <= p.len_lo) return;
+  if (s0 < 0 || s1 < s0 || s1 > p.tokens) return;      // (the other launches report it)
+  const int c0 = (slot - first_slot(s0, rank)) * PC, len = s1 - s0;
+  if (c0 >= len) return;
   const int nt = len - c0 < PC ? len - c0 : PC;
   const int64_t tok = (int64_t)s0 + c0;
 
@@ -263,13 +272,13 @@ struct ChunkLds {
   static_assert(BYTES <= 160 * 1024, "LDS of a CU");
 };
 
-// 16 bytes of each active lane from memory to LDS at lds + 16 * lane, in
-// flight until the wave's next wait for its memory counter.  (The compiler
-// would have every LDS read wait for a copy that it knows of, also where the
-// two are in different buffers.)
-__device__ __forceinline__ void copy16(const void* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(reinterpret_cast<uint64_t>(g)),
-               "s"(lds)
+// 16 bytes of each lane, from base + its offset in memory to lds + 16 * lane
+// in LDS (base and lds are uniform), in flight until the wave's next wait for
+// its memory counter.  (The compiler would have every LDS read wait for a copy
+// that it knows of, also where the two are in different buffers.)
+__device__ __forceinline__ void copy16(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset),
+               "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
                : "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -304,18 +313,41 @@ __device__ __forceinline__ void region() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// The prompt of rank r by length, for up to 64 prompts (a lane each): the last
-// workgroups to start are then the shortest.  More prompts are taken as listed.
-__device__ __forceinline__ int longest_first(const PromptParams& p, int r) {
-  if (p.nseq > 64) return r;
-  const int lane = threadIdx.x & 63, mine = lane < p.nseq ? lane : 0;
-  const int len = p.start[mine + 1] - p.start[mine];
-  int before = 0;
-  for (int j = 0; j < p.nseq; ++j) {
-    const int other = __builtin_amdgcn_readlane(len, j);
-    before += other > len || (other == len && j < lane);
+// The x-th of the prompts taken in chunks (-1: there are not so many), and its
+// rank among them as listed.  Up to 64 prompts are taken longest first (a lane
+// each), so that the last workgroups to start are the shortest; more are taken
+// as listed.
+__device__ __forceinline__ int chunked_prompt(const PromptParams& p, int x, int* rank) {
+  const int lane = threadIdx.x & 63;
+  if (p.nseq <= 64) {
+    const int j = lane < p.nseq ? lane : 0;
+    const int len = p.start[j + 1] - p.start[j];
+    const bool mine = lane < p.nseq && len > p.len_lo;
+    const unsigned long long all = __ballot(mine);
+    int before = 0;
+    for (int k = 0; k < p.nseq; ++k) {
+      const int other = __builtin_amdgcn_readlane(len, k);
+      before += (all >> k & 1) && (other > len || (other == len && k < lane));
+    }
+    const unsigned long long m = __ballot(mine && before == x);
+    if (!m) return -1;
+    const int i = __builtin_ctzll(m);
+    *rank = __popcll(all & ((1ull << i) - 1));
+    return i;
   }
-  return __builtin_ctzll(__ballot(lane < p.nseq && before == r));
+  int ranks = 0;
+  for (int j0 = 0; j0 < p.nseq; j0 += 64) {
+    const int j = j0 + lane < p.nseq ? j0 + lane : p.nseq - 1;
+    const bool mine = j0 + lane < p.nseq && (int64_t)p.start[j + 1] - p.start[j] > p.len_lo;
+    const unsigned long long all = __ballot(mine);
+    const unsigned long long m = __ballot(mine && ranks + __popcll(all & ((1ull << lane) - 1)) == x);
+    if (m) {
+      *rank = x;
+      return j0 + __builtin_ctzll(m);
+    }
+    ranks += __popcll(all);
+  }
+  return -1;
 }
 
 template <int DK, int DV, int NW>
@@ -328,21 +360,23 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, hi = lane >> 4;
-  // (the parts of a tile are nseq * H workgroups apart: mostly on one XCD,
+  // (the parts of a tile are nchunked * H workgroups apart: mostly on one XCD,
   // whose cache then serves the K, Q, T and P that they share)
-  const int tiles = p.nseq * p.H, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
-  const int i = longest_first(p, tile / p.H), h = tile % p.H;
-  if ((int64_t)p.start[i + 1] - p.start[i] <= p.len_lo) return;
-  const PromptTile pt = prompt_tile(p, i, h);
-  if (!pt.ok) return;
+  const int tiles = p.nchunked * p.H, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
+  const int h = tile % p.H;
+  int rank = 0;
+  const int i = chunked_prompt(p, tile / p.H, &rank);
+  if (i < 0) return;
+  const int s0 = p.start[i], len = p.start[i + 1] - s0, b = p.seqs ? p.seqs[i] : i;
+  if (!prompt_ok(p, i, h, b)) return;
 
   const int c0 = part * NW * 16 + wv * 16;       // the wave's first column
-  float* Sg = p.S + ((size_t)pt.b * p.H + h) * DK * DV + c0 + n;
-  const bf16* kp = reinterpret_cast<const bf16*>(p.k) + pt.s0 * p.ks + (int64_t)h * DK;
-  const bf16* qp = reinterpret_cast<const bf16*>(p.q) + pt.s0 * p.qs + (int64_t)h * DK;
-  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + pt.s0 * p.vs + (int64_t)h * DV + c0;
+  float* Sg = p.S + ((size_t)b * p.H + h) * DK * DV + c0 + n;
+  const bf16* kp = reinterpret_cast<const bf16*>(p.k) + s0 * p.ks + (int64_t)h * DK;      // (all uniform)
+  const bf16* qp = reinterpret_cast<const bf16*>(p.q) + s0 * p.qs + (int64_t)h * DK;
+  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + s0 * p.vs + (int64_t)h * DV + c0;
   const unsigned char* wp = reinterpret_cast<const unsigned char*>(p.work) +
-                            ((size_t)first_slot(pt.s0, i) * p.H + h) * CHUNK_WORK_BYTES;
+                            ((size_t)first_slot(s0, rank) * p.H + h) * CHUNK_WORK_BYTES;
 
   // ------------------------------------------------------------- copies
   // Rows of K and Q have their 16-byte pieces swizzled so that the rows of a
@@ -359,63 +393,55 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   constexpr int WUNITS = (CHUNK_WORK_BYTES + PROMPT_WORK_OVER) / 1024, WU = (WUNITS + 1) / NW, UNITS = 2 * KU + 2 + WU;
   static_assert((CHUNK_WORK_BYTES + PROMPT_WORK_OVER) % 1024 == 0 && (WUNITS + 1) % NW == 0, "units of the waves");
   const int wlast = (WU - 1) * NW + wv < WUNITS ? (WU - 1) * NW + wv : 0;
-  const int krow = (wv * 64 + lane) / PPR, kpc = lane % PPR, vrow = lane >> 1, vpc = (lane & 1) * 8;
-  // unit u of a whole chunk into a buffer: K, Q, then the workspace, V last.
-  // The lane's addresses go from chunk to chunk; the swizzle of K and Q rows
-  // differs between a wave's even and odd units only.
-  const bf16 *kc[2], *qc[2], *vc = vp + (int64_t)vrow * p.vs + vpc;
-#pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    const int pc = (kpc ^ swz(krow + KROWS * v)) * 8;
-    kc[v] = kp + (int64_t)krow * p.ks + pc;
-    qc[v] = qp + (int64_t)krow * p.qs + pc;
-  }
-  const unsigned char* wc = wp + lane * 16;
+  const int krow = (wv * 64 + lane) / PPR, kpc = lane % PPR, vrow = lane >> 1;
+  // Byte offset of a lane's piece from a chunk's first row (unsigned 32 bits: 63
+  // rows of at most 2^25 elements fit).  Rows behind the prompt's end repeat its
+  // last one (`last` is its number in the chunk): their beta in T is 0, their
+  // columns of P meet only zeros, and their outputs are not stored.
+  auto koff = [&](int v, int64_t st, int last) {
+    const int row = krow + KROWS * v;
+    return (uint32_t)((row < last ? row : last) * st * 2) + (uint32_t)(kpc ^ swz(row)) * 16;
+  };
+  auto voff = [&](int v, int last) {
+    const int row = vrow + 32 * v;
+    return (uint32_t)((row < last ? row : last) * p.vs * 2) + (uint32_t)(lane & 1) * 16;
+  };
+  // In a whole chunk, the offsets of a wave's first unit from its own first row
+  // (of K and Q also with the swizzle of its odd units: it has a period of 32
+  // rows); the units' rows are added to the uniform base.
+  const uint32_t krow2 = (uint32_t)(krow * p.ks * 2), qrow2 = (uint32_t)(krow * p.qs * 2);
+  const uint32_t sw[2] = {(uint32_t)(kpc ^ swz(krow)) * 16, (uint32_t)(kpc ^ swz(krow + KROWS)) * 16};
+  const uint32_t vo = voff(0, PC), wo = lane * 16;
   const int64_t kstep = KROWS * p.ks, qstep = KROWS * p.qs;
-  auto copy_unit = [&](int u, uint32_t l0) {
+  // unit u of the whole chunk at t0 into a buffer: K, Q, then the workspace, V last
+  auto copy_unit = [&](int u, int t0, uint32_t l0) {
     if (u < KU) {
-      copy16(kc[u & 1] + u * kstep, l0 + L::K + (NW * u + wv) * 1024);
+      copy16(kp + (int64_t)t0 * p.ks + u * kstep, krow2 + sw[u & 1], l0 + L::K + (NW * u + wv) * 1024);
     } else if (u < 2 * KU) {
       const int v = u - KU;
-      copy16(qc[v & 1] + v * qstep, l0 + L::Q + (NW * v + wv) * 1024);
+      copy16(qp + (int64_t)t0 * p.qs + v * qstep, qrow2 + sw[v & 1], l0 + L::Q + (NW * v + wv) * 1024);
     } else if (u < 2 * KU + WU) {
       const int unit = u < 2 * KU + WU - 1 ? NW * (u - 2 * KU) + wv : wlast;
-      copy16(wc + unit * 1024, l0 + L::W + unit * 1024);
+      copy16(wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES + unit * 1024, wo, l0 + L::W + unit * 1024);
     } else {
       const int v = u - 2 * KU - WU;
-      copy16(vc + v * 32 * p.vs, l0 + L::V + wv * 2048 + v * 1024);
+      copy16(vp + (t0 + 32 * v) * p.vs, vo, l0 + L::V + wv * 2048 + v * 1024);
     }
   };
-  auto next_chunk = [&]() {
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      kc[v] += PC * p.ks;
-      qc[v] += PC * p.qs;
-    }
-    vc += PC * p.vs;
-    wc += (size_t)p.H * CHUNK_WORK_BYTES;
-  };
-  // The whole of a chunk that may be a prompt's last: rows behind its end
-  // repeat its last one (their beta in T is 0, their columns of P meet only
-  // zeros, and their outputs are not stored).
+  // the whole of a chunk that may be a prompt's last
   auto copy_all = [&](int t0, int nt, uint32_t l0) {
-    auto at = [&](int row) { return (int64_t)(t0 + (row < nt ? row : nt - 1)); };
 #pragma unroll 1
     for (int v = 0; v < KU; ++v) {
-      const int row = krow + KROWS * v, pc = (kpc ^ swz(row)) * 8;
-      copy16(kp + at(row) * p.ks + pc, l0 + L::K + (NW * v + wv) * 1024);
-      copy16(qp + at(row) * p.qs + pc, l0 + L::Q + (NW * v + wv) * 1024);
+      copy16(kp + t0 * p.ks, koff(v, p.ks, nt - 1), l0 + L::K + (NW * v + wv) * 1024);
+      copy16(qp + t0 * p.qs, koff(v, p.qs, nt - 1), l0 + L::Q + (NW * v + wv) * 1024);
     }
 #pragma unroll 1
     for (int v = 0; v < 2; ++v)
-      copy16(vp + at(vrow + 32 * v) * p.vs + vpc, l0 + L::V + wv * 2048 + v * 1024);
-#pragma unroll 1
-    for (int v = 0; v < WU; ++v) {
-      const int unit = v + 1 < WU ? NW * v + wv : wlast;
-      copy16(wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES + unit * 1024 + lane * 16, l0 + L::W + unit * 1024);
-    }
+      copy16(vp + t0 * p.vs, voff(v, nt - 1), l0 + L::V + wv * 2048 + v * 1024);
+#pragma unroll
+    for (int u = 2 * KU; u < 2 * KU + WU; ++u) copy_unit(u, t0, l0);
   };
-  if (pt.len > 0) copy_all(0, pt.len < PC ? pt.len : PC, lds0);
+  if (len > 0) copy_all(0, len < PC ? len : PC, lds0);
 
   // --------------------------------------------------------- fragments
   const unsigned char* sb = smem;                // the present chunk's buffer
@@ -447,10 +473,10 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 
   // The wave's outputs of a chunk leave in the next chunk's time: from LDS,
   // columns of 64 tokens in eight swizzled pieces, as rows of eight columns.
-  bf16* op = reinterpret_cast<bf16*>(p.o) + pt.s0 * p.os + (int64_t)h * DV + c0;
+  bf16* op = reinterpret_cast<bf16*>(p.o) + s0 * p.os + (int64_t)h * DV + c0;
   u32x4 out[2];
   const int og = hi & 1, ot = 16 * (hi >> 1);
-  bf16* op0 = op + (int64_t)(ot + n) * p.os + og * 8;
+  const uint32_t oo = (uint32_t)((ot + n) * p.os * 2) + og * 16;
   auto read_out = [&](const unsigned char* s) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {                // lane i of a group: column 8 og + i / 4 (and + 4), tokens 4 (i % 4) ..
@@ -462,7 +488,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   auto store_out = [&](int t0, int cnt) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      if (ot + n + 32 * u < cnt) *reinterpret_cast<u32x4*>(op0 + ((int64_t)t0 + 32 * u) * p.os) = out[u];
+      if (ot + n + 32 * u < cnt)
+        *reinterpret_cast<u32x4*>(reinterpret_cast<unsigned char*>(op + (t0 + 32 * u) * p.os) + oo) = out[u];
   };
 
   bf16x8 ss[DB][3];                              // the state's split blocks
@@ -483,13 +510,13 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     sb = smem + buf * L::BUF;
     const float* s_g = reinterpret_cast<const float*>(sb + L::W + T_BYTES + P_BYTES);
     const unsigned char* s_v = sb + L::V + wv * 2048;
-    const int left = pt.len - t0 - PC;
+    const int left = len - t0 - PC;
     const uint32_t lnext = lds0 + (buf ^ 1) * L::BUF;
     auto copies = [&](int from, int to) {
       if constexpr (MORE) {
 #pragma unroll
         for (int u = from; u < to; ++u)
-          if (u < UNITS) copy_unit(u, lnext);
+          if (u < UNITS) copy_unit(u, t0 + PC, lnext);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -506,7 +533,6 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     __builtin_amdgcn_sched_barrier(0);
     if (t0 > 0) read_out(smem + (buf ^ 1) * L::BUF + L::V + wv * 2048);
     const float gC = s_g[PC - 1];
-    next_chunk();
     if (!MORE && left > 0) copy_all(t0 + PC, left, lnext);
     __builtin_amdgcn_sched_barrier(0);
 
@@ -666,12 +692,12 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     t0 += PC;
     buf ^= 1;
   };
-  while (pt.len - t0 >= 2 * PC) chunk(std::true_type{});
-  while (t0 < pt.len) chunk(std::false_type{});
-  if (pt.len > 0) {
+  while (len - t0 >= 2 * PC) chunk(std::true_type{});
+  while (t0 < len) chunk(std::false_type{});
+  if (len > 0) {
     wave_lds_sync();
     read_out(sb + L::V + wv * 2048);
-    store_out(t0 - PC, pt.len - (t0 - PC));
+    store_out(t0 - PC, len - (t0 - PC));
   }
 
 #pragma unroll
@@ -679,19 +705,19 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll
     for (int e = 0; e < 8; ++e) Sg[(size_t)(32 * db + 8 * hi + e) * DV] = S[db][e >> 2][e & 3];
   if (!p.prime) return;
-  const int off = p.sk.off[h], rank = p.sk.off[h + 1] - off;
-  if (rank == 0) {                               // a dense-fallback head: the state copy
+  const int off = p.sk.off[h], r = p.sk.off[h + 1] - off;
+  if (r == 0) {                                  // a dense-fallback head: the state copy
     int slot = 0;
     while (slot + 1 < p.sk.ndense && p.sk.dense_list[slot] != h) ++slot;
-    bf16* C = reinterpret_cast<bf16*>(p.sk.Sc) + ((size_t)pt.b * p.sk.ndense + slot) * DK * DV + c0 + n;
+    bf16* C = reinterpret_cast<bf16*>(p.sk.Sc) + ((size_t)b * p.sk.ndense + slot) * DK * DV + c0 + n;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
       for (int e = 0; e < 8; ++e) C[(size_t)(32 * db + 8 * hi + e) * DV] = f32_to_bf16(S[db][e >> 2][e & 3]);
     return;
   }
-  bf16* Ug = reinterpret_cast<bf16*>(p.sk.U) + ((size_t)pt.b * p.sk.R + off) * DV + c0 + n;
-  for (int j = 0; j < rank; ++j) {               // u_j = S^T p_j
+  bf16* Ug = reinterpret_cast<bf16*>(p.sk.U) + ((size_t)b * p.sk.R + off) * DV + c0 + n;
+  for (int j = 0; j < r; ++j) {                  // u_j = S^T p_j
     const float* P = p.sk.Pt + (size_t)(off + j) * DK + 8 * hi;
     float a = 0.f;
 #pragma unroll
@@ -710,7 +736,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 template <int DK, int DV, int NW>
 int launch(const PromptParams& p, hipStream_t st) {
   hipLaunchKernelGGL((prompt_prep_kernel<DK>), dim3((unsigned)p.nslots * p.H), dim3(256), 0, st, p);
-  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, NW>), dim3((unsigned)p.nseq * p.H * (DV / (16 * NW))), dim3(64 * NW),
+  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, NW>), dim3((unsigned)p.nchunked * p.H * (DV / (16 * NW))), dim3(64 * NW),
                      (ChunkLds<DK, NW>::BYTES), st, p);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
@@ -720,7 +746,7 @@ int launch(const PromptParams& p, hipStream_t st) {
 int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st) {
   if (dk == 64 && dv == 64) return launch<64, 64, 4>(p, st);
   if (dk == 128 && dv == 64) return launch<128, 64, 4>(p, st);
-  if (dk == 128 && dv == 128) return p.nseq * p.H <= 128 ? launch<128, 128, 4>(p, st) : launch<128, 128, 8>(p, st);
+  if (dk == 128 && dv == 128) return p.nchunked * p.H <= 128 ? launch<128, 128, 4>(p, st) : launch<128, 128, 8>(p, st);
   return -2;
 }
 

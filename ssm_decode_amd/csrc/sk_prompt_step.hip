@@ -16,26 +16,29 @@ constexpr int TB = 16;    // tokens staged at a time
 
 template <typename AT> struct Chunk16 { static constexpr int N = 16 / (int)sizeof(AT); };
 
-__device__ __forceinline__ void put_chunk(float* dst, const uint4& r, const bf16*) {
-  reinterpret_cast<float4*>(dst)[0] = make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
-                                                  __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
-  reinterpret_cast<float4*>(dst)[1] = make_float4(__uint_as_float(r.z << 16), __uint_as_float(r.z & 0xffff0000u),
-                                                  __uint_as_float(r.w << 16), __uint_as_float(r.w & 0xffff0000u));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void put_chunk(float* dst, const u32x4& r, const bf16*) {
+  const u32x4 a = {r[0] << 16, r[0] & 0xffff0000u, r[1] << 16, r[1] & 0xffff0000u};
+  const u32x4 b = {r[2] << 16, r[2] & 0xffff0000u, r[3] << 16, r[3] & 0xffff0000u};
+  reinterpret_cast<u32x4*>(dst)[0] = a;
+  reinterpret_cast<u32x4*>(dst)[1] = b;
 }
-__device__ __forceinline__ void put_chunk(float* dst, const uint4& r, const float*) {
-  *reinterpret_cast<uint4*>(dst) = r;
+__device__ __forceinline__ void put_chunk(float* dst, const u32x4& r, const float*) {
+  *reinterpret_cast<u32x4*>(dst) = r;
 }
 
 // Rows of D elements of up to TB tokens: global -> registers -> LDS as fp32.
 template <int D, int NT, typename AT>
 struct Rows {
   static constexpr int N = Chunk16<AT>::N, CPR = D / N, U = (TB * CPR + NT - 1) / NT;
-  uint4 r[U];
+  u32x4 r[U];
   __device__ __forceinline__ void load(const AT* base, int64_t stride, int nt) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = threadIdx.x + NT * u, t = c / CPR;
-      if (t < nt) r[u] = *reinterpret_cast<const uint4*>(base + t * stride + (c - t * CPR) * N);
+      r[u] = u32x4{0, 0, 0, 0};
+      if (t < nt) r[u] = *reinterpret_cast<const u32x4*>(base + t * stride + (c - t * CPR) * N);
     }
   }
   __device__ __forceinline__ void stage(float* lds, int nt) const {
@@ -53,42 +56,20 @@ __global__ void __launch_bounds__(DV * 2) prompt_step_kernel(PromptParams p) {
   __shared__ __align__(16) float s_k[TB * DK], s_q[TB * DK], s_v[TB * DV], s_ab[2 * TB];
 
   const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H;
-  // a longer prompt belongs to the chunked form's launch (which reports it
-  // where its range is not valid)
-  if ((int64_t)p.start[i + 1] - p.start[i] > p.len_hi) return;
-  const PromptTile t = prompt_tile(p, i, h);
-  if (!t.ok) return;
+  const int s0 = p.start[i], len = p.start[i + 1] - s0;
+  // (a longer prompt belongs to the chunked form's launch; so that a refused
+  // list is reported, the first prompt's workgroups go on to the checks)
+  if (i > 0 && (unsigned)len > (unsigned)p.len_hi) return;
+  const int b = p.seqs ? p.seqs[i] : i;
+  const bool in = b >= 0 && b < p.B;
 
   const int tid = threadIdx.x, lane = tid & 63, cg = lane & 15, rg = lane >> 4;
   const int col0 = 32 * (tid >> 6), col = col0 + 2 * cg;
-  float* Sg = p.S + ((size_t)t.b * p.H + h) * DK * DV + (size_t)(4 * rg) * DV + col;
+  float* Sg = p.S + ((size_t)(in ? b : 0) * p.H + h) * DK * DV + (size_t)(4 * rg) * DV + col;
 
-  const AT* kp = reinterpret_cast<const AT*>(p.k) + t.s0 * p.ks + (int64_t)h * DK;
-  const AT* qp = reinterpret_cast<const AT*>(p.q) + t.s0 * p.qs + (int64_t)h * DK;
-  const AT* vp = reinterpret_cast<const AT*>(p.v) + t.s0 * p.vs + (int64_t)h * DV;
-  const float* ap = p.gate + t.s0 * p.gs + h;
-  const float* bp = p.beta + t.s0 * p.bs + h;
-  AT* op = reinterpret_cast<AT*>(p.o) + t.s0 * p.os + (int64_t)h * DV + col;
-
-  // the small loads first, then the state
-  Rows<DK, NT, AT> rk, rq;
-  Rows<DV, NT, AT> rv;
-  float ab = 0.f;
-  auto fetch = [&](int t0, int nt) {
-    rk.load(kp + t0 * p.ks, p.ks, nt);
-    rq.load(qp + t0 * p.qs, p.qs, nt);
-    rv.load(vp + t0 * p.vs, p.vs, nt);
-    if (tid < TB) {
-      if (tid < nt) ab = ap[(t0 + tid) * p.gs];
-    } else if (tid < 2 * TB && tid - TB < nt) {
-      ab = bp[(t0 + tid - TB) * p.bs];
-    }
-  };
-  int nt = t.len < TB ? t.len : TB;
-  fetch(0, nt);
-
+  // the state's loads are in flight over the checks and the tokens' first loads
   float s[MB][2][4];
-  if (!p.has_state || p.has_state[i] != 0) {
+  if (in && (!p.has_state || p.has_state[i] != 0)) {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -104,50 +85,84 @@ __global__ void __launch_bounds__(DV * 2) prompt_step_kernel(PromptParams p) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) s[mb][0][v] = s[mb][1][v] = 0.f;
   }
+  if (!prompt_ok(p, i, h, b) || len > p.len_hi) return;
 
-  for (int t0 = 0; t0 < t.len; t0 += TB) {
+  const AT* kp = reinterpret_cast<const AT*>(p.k) + s0 * p.ks + (int64_t)h * DK;
+  const AT* qp = reinterpret_cast<const AT*>(p.q) + s0 * p.qs + (int64_t)h * DK;
+  const AT* vp = reinterpret_cast<const AT*>(p.v) + s0 * p.vs + (int64_t)h * DV;
+  const float* ap = p.gate + s0 * p.gs + h;
+  const float* bp = p.beta + s0 * p.bs + h;
+  AT* op = reinterpret_cast<AT*>(p.o) + s0 * p.os + (int64_t)h * DV + col;
+
+  Rows<DK, NT, AT> rk, rq;
+  Rows<DV, NT, AT> rv;
+  float ab = 0.f;
+  auto fetch = [&](int t0, int nt) {
+    rk.load(kp + t0 * p.ks, p.ks, nt);
+    rq.load(qp + t0 * p.qs, p.qs, nt);
+    rv.load(vp + t0 * p.vs, p.vs, nt);
+    if (tid < TB) {
+      if (tid < nt) ab = ap[(t0 + tid) * p.gs];
+    } else if (tid < 2 * TB && tid - TB < nt) {
+      ab = bp[(t0 + tid - TB) * p.bs];
+    }
+  };
+  int nt = len < TB ? len : TB;
+  fetch(0, nt);
+
+  for (int t0 = 0; t0 < len; t0 += TB) {
     rk.stage(s_k, nt);
     rq.stage(s_q, nt);
     rv.stage(s_v, nt);
     if (tid < 2 * TB) s_ab[tid] = ab;
     __syncthreads();
-    const int now = nt, left = t.len - t0 - TB;
+    const int now = nt, left = len - t0 - TB;
     if (left > 0) {                        // the next block's loads, in flight over this one
       nt = left < TB ? left : TB;
       fetch(t0 + TB, nt);
     }
+    float kk[MB][4], vv[2], al, be;
+    auto token = [&](int j) {                // a token's key, value and factors
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) ld4(s_k + j * DK + 16 * mb + 4 * rg, kk[mb]);
+      ldn<2>(s_v + j * DV + col, vv);
+      al = s_ab[j];
+      be = s_ab[TB + j];
+    };
+    token(0);
+#pragma unroll 1
     for (int j = 0; j < now; ++j) {
-      float kk[MB][4];
+      float qq[MB][4];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) ld4(s_q + j * DK + 16 * mb + 4 * rg, qq[mb]);
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        ld4(s_k + j * DK + 16 * mb + 4 * rg, kk[mb]);
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           a0 += s[mb][0][v] * kk[mb][v];
           a1 += s[mb][1][v] * kk[mb][v];
         }
-      }
-      a0 = xsum<4, 2>(a0);                 // over the four row groups
-      a1 = xsum<4, 2>(a1);
-      const float al = s_ab[j], be = s_ab[TB + j];
-      float vv[2];
-      ldn<2>(s_v + j * DV + col, vv);
+      a0 = row_groups_sum(a0);
+      a1 = row_groups_sum(a1);
       const float u0 = be * (vv[0] - al * a0), u1 = be * (vv[1] - al * a1);
-      float o0 = 0.f, o1 = 0.f;
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        float qq[4];
-        ld4(s_q + j * DK + 16 * mb + 4 * rg, qq);
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           s[mb][0][v] = al * s[mb][0][v] + kk[mb][v] * u0;
           s[mb][1][v] = al * s[mb][1][v] + kk[mb][v] * u1;
-          o0 += s[mb][0][v] * qq[v];
-          o1 += s[mb][1][v] * qq[v];
         }
-      }
-      const float o2[2] = {xsum<4, 2>(o0), xsum<4, 2>(o1)};
+      if (j + 1 < now) token(j + 1);         // in flight over this token's output
+      float o0 = 0.f, o1 = 0.f;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          o0 += s[mb][0][v] * qq[mb][v];
+          o1 += s[mb][1][v] * qq[mb][v];
+        }
+      const float o2[2] = {row_groups_sum(o0), row_groups_sum(o1)};
       if (rg == 0) stn<2>(op + (t0 + j) * p.os, o2);
     }
     __syncthreads();
@@ -160,7 +175,7 @@ __global__ void __launch_bounds__(DV * 2) prompt_step_kernel(PromptParams p) {
       const float x[2] = {s[mb][0][v], s[mb][1][v]};
       stn_nt<2>(Sg + (size_t)(16 * mb + v) * DV, x);
     }
-  if (p.prime) sketch_tile<DK, DV, AT>(p.sk, s, t.b, h, col0, lane);
+  if (p.prime) sketch_tile<DK, DV, AT>(p.sk, s, b, h, col0, lane);
 }
 
 template <int DK, int DV>

@@ -27,7 +27,7 @@ struct PromptParams {
   int B, H;
   int tokens, nseq;
   int len_lo, len_hi;       // the launch takes prompts of more than len_lo and up to len_hi tokens
-  int nslots;               // chunk slots of the workspace (chunked form)
+  int nchunked, nslots;     // chunked form: prompts it may have, chunk slots of the workspace
   const void* q;
   const void* k;
   const void* v;
@@ -79,8 +79,8 @@ constexpr int PROMPT_CHUNK = 64;
 constexpr int PROMPT_CHUNK_WORK = 30 * 1024 + 512;
 constexpr int PROMPT_WORK_OVER = 512;    // read, not used, behind the last one
 inline bool prompt_chunked(int dk, int act) { return act == DT_BF16 && dk >= 64; }
-// Chunk slots that nseq prompts of together up to `tokens` tokens may take.
-inline int64_t prompt_slots(int64_t tokens, int64_t nseq) { return tokens / PROMPT_CHUNK + nseq; }
+// Chunk slots that n prompts of together up to `tokens` tokens may take.
+inline int64_t prompt_slots(int64_t tokens, int64_t n) { return tokens / PROMPT_CHUNK + n; }
 
 int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st);
 int launch_prompt_step(int dk, int dv, int act, const PromptParams& p, hipStream_t st);

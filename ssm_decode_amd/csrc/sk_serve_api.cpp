@@ -16,15 +16,29 @@ constexpr int kMaxWidth = 8192;
 // Prompts of up to this many tokens go token by token where the launch has
 // both kinds.
 constexpr int kShort = 16;
-bool chunks(const sketchssm_layer* L, int32_t tokens) {
-  return sk::prompt_chunked(L->dk, L->act_dtype) && tokens > kShort;
+
+// How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
+// none), all of them or those of more than kShort tokens.
+struct Plan {
+  int64_t chunked;
+  bool all;
+};
+Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
+  if (!sk::prompt_chunked(L->dk, L->act_dtype) || tokens <= kShort || nseq == 0) return {0, false};
+  // mostly long prompts: the chunked form takes the short ones too, and one
+  // launch is saved
+  if (tokens > sk::PROMPT_CHUNK * nseq) return {nseq, true};
+  const int64_t most = tokens / (kShort + 1);
+  return {most < nseq ? most : nseq, false};
 }
 
 bool aligned(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// A row stride whose rows stay 16-byte aligned and do not overlap.
+// A row stride whose rows stay 16-byte aligned and do not overlap (the kernels'
+// offsets within a group of rows are 32 bits).
+constexpr int64_t kMaxStride = 1 << 25;
 bool row_stride(int64_t stride, int64_t row, int esize) {
-  return stride >= row && stride <= INT32_MAX && (stride * esize) % 16 == 0;
+  return stride >= row && stride <= kMaxStride && (stride * esize) % 16 == 0;
 }
 
 int check_layer(const sketchssm_layer* L) {
@@ -97,8 +111,9 @@ int64_t sketchssm_prefill_workspace_bytes(const sketchssm_layer* layer, int32_t 
   try {
     if (int rc = check_layer(layer)) return rc;
     if (layer->family != SKSSM_GDN || tokens < 0 || nseq < 0 || nseq > layer->batch) return SKSSM_EDIM;
-    if (!chunks(layer, tokens)) return 0;
-    const int64_t tiles = sk::prompt_slots(tokens, nseq) * layer->heads;
+    const Plan pl = plan(layer, tokens, nseq);
+    if (pl.chunked == 0) return 0;
+    const int64_t tiles = sk::prompt_slots(tokens, pl.chunked) * layer->heads;
     if (tiles > INT32_MAX / 2) return SKSSM_EDIM;
     return tiles * sk::PROMPT_CHUNK_WORK + sk::PROMPT_WORK_OVER;
   } catch (...) {
@@ -128,7 +143,7 @@ int sketchssm_prefill(const sketchssm_layer* layer, const sketchssm_buffers* buf
       if (!row_stride(pr->q_stride, (int64_t)H * dk, es) || !row_stride(pr->k_stride, (int64_t)H * dk, es) ||
           !row_stride(pr->v_stride, (int64_t)H * dv, es) || !row_stride(pr->o_stride, (int64_t)H * dv, es))
         return SKSSM_EDIM;
-      if (pr->gate_stride < H || pr->beta_stride < H || pr->gate_stride > INT32_MAX || pr->beta_stride > INT32_MAX)
+      if (pr->gate_stride < H || pr->beta_stride < H || pr->gate_stride > kMaxStride || pr->beta_stride > kMaxStride)
         return SKSSM_EDIM;
     }
     if (need > 0 && (!aligned(pr->work, 16) || pr->work_bytes < need)) return SKSSM_EINVAL;
@@ -160,13 +175,12 @@ int sketchssm_prefill(const sketchssm_layer* layer, const sketchssm_buffers* buf
     p.work = pr->work;
     hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
     p.len_hi = INT32_MAX;
-    if (chunks(layer, pr->tokens)) {
-      // mostly long prompts: the chunked form takes the short ones too, and one
-      // launch is saved; otherwise the two share them by their lengths
-      const bool all = pr->tokens > (int64_t)sk::PROMPT_CHUNK * pr->nseq;
-      p.nslots = (int)sk::prompt_slots(pr->tokens, pr->nseq);
-      p.len_lo = all ? -1 : kShort;
-      if ((rc = sk::launch_prompt_chunks(dk, dv, p, st)) || all) return rc;
+    const Plan pl = plan(layer, pr->tokens, pr->nseq);
+    if (pl.chunked > 0) {
+      p.nchunked = (int)pl.chunked;
+      p.nslots = (int)sk::prompt_slots(pr->tokens, pl.chunked);
+      p.len_lo = pl.all ? -1 : kShort;
+      if ((rc = sk::launch_prompt_chunks(dk, dv, p, st)) || pl.all) return rc;
       p.len_hi = kShort;
     }
     return sk::launch_prompt_step(dk, dv, layer->act_dtype, p, st);

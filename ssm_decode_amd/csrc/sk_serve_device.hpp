@@ -17,38 +17,34 @@ __device__ __forceinline__ bool listed_before(const int32_t* list, int i, int id
   return __syncthreads_or(dup) != 0;
 }
 
-// The sequence, first token and length of prompt i, checked: an index
-// outside the batch, a range outside the tokens or not behind those of the
-// prompts before it (so that no two prompts share tokens or chunk slots), or
-// a sequence that an earlier prompt of the list has (the earlier one keeps
-// it) reports ERRBIT_SEQ; a tile whose ring still holds entries
-// ERRBIT_COUNT.  ok is uniform over the workgroup.
-struct PromptTile {
-  int b, s0, len;
-  bool ok;
-};
-__device__ __forceinline__ PromptTile prompt_tile(const PromptParams& p, int i, int h) {
-  PromptTile t;
-  t.s0 = p.start[i];
-  const int s1 = p.start[i + 1];
-  t.b = p.seqs ? p.seqs[i] : i;
-  int bad = 0;
-  if (t.b < 0 || t.b >= p.B || t.s0 < 0 || s1 < t.s0 || s1 > p.tokens) {
-    bad = ERRBIT_SEQ;
-  } else if (p.nseq > 1) {
-    int wrong = 0;
-    for (int j = threadIdx.x; j <= p.nseq; j += blockDim.x) {
-      const int s = p.start[j];
-      wrong |= j < i ? s > t.s0 : j > i + 1 ? s < s1 : 0;
-      if (p.seqs && j < i) wrong |= p.seqs[j] == t.b;
-    }
-    if (__syncthreads_or(wrong)) bad = ERRBIT_SEQ;
+// Prompt i and its sequence, checked.  A list of first tokens that falls
+// anywhere, or leaves [0, tokens], reports ERRBIT_SEQ and is refused whole (so
+// that no two prompts share tokens, and at most tokens / n prompts have n
+// tokens); an index outside the batch, or a sequence that an earlier prompt
+// has (which keeps it), refuses this prompt; a tile whose ring still holds
+// entries reports ERRBIT_COUNT.  Uniform over the workgroup, whose threads
+// all take part.
+__device__ __forceinline__ bool prompt_ok(const PromptParams& p, int i, int h, int b) {
+  int wrong = 0;
+  for (int j = threadIdx.x; j < p.nseq; j += blockDim.x) {
+    const int s0 = p.start[j], s1 = p.start[j + 1];
+    wrong |= s0 < 0 || s1 < s0 || s1 > p.tokens;
+    if (p.seqs && j < i) wrong |= p.seqs[j] == b;
   }
-  if (!bad && p.count[(size_t)t.b * p.H + h] != 0) bad = ERRBIT_COUNT;
+  wrong |= b < 0 || b >= p.B;
+  int bad = __syncthreads_or(wrong) ? ERRBIT_SEQ : 0;
+  if (!bad && p.count[(size_t)b * p.H + h] != 0) bad = ERRBIT_COUNT;
   if (bad && threadIdx.x == 0) atomicOr(p.err, bad);
-  t.len = s1 - t.s0;
-  t.ok = bad == 0;
-  return t;
+  return bad == 0;
+}
+
+// Sum over the four rows of 16 lanes; every lane receives it.  (Lane swaps are
+// vector instructions: no LDS permute in the chain from token to token.)
+__device__ __forceinline__ float row_groups_sum(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // Registers of a wave's 32 columns of a tile, as the flush holds them: with

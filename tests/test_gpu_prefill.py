@@ -220,20 +220,43 @@ def test_refused_entries_leave_everything_else():
             assert lay.count[3].tolist() == [1] * H
 
 
-@pytest.mark.parametrize("starts,skip", [
-    ([100, 30, 60, 200], (0, 1, 2)), ([0, 70, 60, 200], (0, 1, 2)), ([-5, 70, 140, 200], (0,)), ([0, 70, 140, 999], (2,)),
-    ([0, 100, 100, 100], ()), ([0, 2000000000, 140, 200], (0, 1, 2)),
-    ([-2147483648, 2147483647, 140, 200], (0, 1, 2)), ([0, 70, 140, 60], (0, 1, 2))])
-def test_bad_token_ranges(starts, skip):
+@pytest.mark.parametrize("starts", [
+    [100, 30, 60, 200], [0, 70, 60, 200], [-5, 70, 140, 200], [0, 70, 140, 999], [0, 2000000000, 140, 200],
+    [-2147483648, 2147483647, 140, 200], [0, 70, 140, 60], [0, 5, 3, 9], [0, 3, 9, 201], [300, 300, 300, 300]])
+@pytest.mark.parametrize("tokens", [200, 150, 12])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_a_bad_list_of_tokens_is_refused_whole(starts, tokens, act):
+    lay = make_layer(3, 2, 64, 64, act, seed=15)
+    tok = make_tokens(tokens, 2, 64, 64, act, seed=16)
+    S0, U0 = lay.S.clone(), lay.U.clone()
+    run(lay, tok, None, starts=starts)
+    assert lay.error_word() == abi.SKSSM_ERRBIT_SEQ
+    assert torch.equal(lay.S, S0) and torch.equal(lay.U, U0) and (tok[5].float() == torch.tensor(SENTINEL).to(tok[5].dtype).float()).all()
+
+
+@pytest.mark.parametrize("starts", [[0, 100, 100, 100], [50, 60, 150, 170], [0, 0, 0, 200], [200, 200, 200, 200]])
+def test_lists_that_leave_tokens_out(starts):
     lay = make_layer(3, 2, 64, 64, "bf16", seed=15)
     tok = make_tokens(200, 2, 64, 64, "bf16", seed=16)
     S0 = lay.S.clone()
     run(lay, tok, None, starts=starts)
-    assert lay.error_word() == (abi.SKSSM_ERRBIT_SEQ if skip else 0)
-    for i in skip:
-        assert torch.equal(lay.S[i], S0[i])
-    lens = [0 if i in skip else starts[i + 1] - starts[i] for i in range(3)]
-    check(lay, S0, tok, lens, starts, [0, 1, 2], [1] * 3, skip=skip)
+    assert lay.error_word() == 0
+    check(lay, S0, tok, [b - a for a, b in zip(starts, starts[1:])], starts, [0, 1, 2], [1] * 3)
+
+
+@pytest.mark.parametrize("n,lens", [(70, "mixed"), (70, "long"), (200, "mixed")])
+def test_many_prompts(n, lens):
+    """More prompts than a wave's lanes, short and long among them."""
+    rng = np.random.default_rng(n)
+    lens = (rng.choice([0, 1, 3, 16, 17, 40, 64, 130], n) if lens == "mixed" else rng.integers(60, 140, n)).tolist()
+    lay = make_layer(n, 2, 64, 64, "bf16", seed=70)
+    tok = make_tokens(sum(lens), 2, 64, 64, "bf16", seed=71)
+    S0 = lay.S.clone()
+    seqs = rng.permutation(n).tolist()
+    has = rng.integers(0, 2, n).tolist()
+    _, starts = run(lay, tok, lens, seqs=seqs, has=has)
+    assert lay.error_word() == 0
+    check(lay, S0, tok, lens, starts, seqs, has)
 
 
 def test_no_prompts_and_empty_prompts():
@@ -284,7 +307,7 @@ def test_a_prompt_in_two_parts_equals_it_in_one():
 def test_long_row_strides():
     """Rows so far apart that offsets pass 32 bits."""
     N, H, dk, dv = 70, 2, 64, 64
-    stride = (1 << 25) + 8                       # 70 rows: over 2^31 elements, 4.7 GB
+    stride = 1 << 25                             # 70 rows: over 2^31 elements, 4.7 GB
     lay = make_layer(1, H, dk, dv, "bf16", seed=24)
     q, k, v, al, be, o = make_tokens(N, H, dk, dv, "bf16", seed=25)
     far = torch.empty(N * stride, device="cuda", dtype=torch.bfloat16)

@@ -111,8 +111,8 @@ def test_prefill_dense_heads_need_their_copies():
     (dict(tokens=-1), abi.SKSSM_EDIM), (dict(nseq=-1), abi.SKSSM_EDIM), (dict(nseq=3), abi.SKSSM_EDIM),
     (dict(q_stride=60), abi.SKSSM_EDIM), (dict(q_stride=66), abi.SKSSM_EDIM), (dict(k_stride=0), abi.SKSSM_EDIM),
     (dict(v_stride=-128), abi.SKSSM_EDIM), (dict(o_stride=124), abi.SKSSM_EDIM), (dict(gate_stride=3), abi.SKSSM_EDIM),
-    (dict(beta_stride=0), abi.SKSSM_EDIM), (dict(beta_stride=1 << 31), abi.SKSSM_EDIM),
-    (dict(q_stride=1 << 32), abi.SKSSM_EDIM), (dict(prime=2), abi.SKSSM_EFLAG), (dict(prime=-1), abi.SKSSM_EFLAG),
+    (dict(beta_stride=0), abi.SKSSM_EDIM), (dict(beta_stride=(1 << 25) + 4), abi.SKSSM_EDIM),
+    (dict(q_stride=(1 << 25) + 64), abi.SKSSM_EDIM), (dict(prime=2), abi.SKSSM_EFLAG), (dict(prime=-1), abi.SKSSM_EFLAG),
 ])
 def test_prefill_sizes_and_flags(over, code):
     assert abi.sketchssm_prefill(gdn(), _bufs(), prompts(**over)) == code
@@ -137,7 +137,8 @@ def test_prefill_workspace():
     # tokens and one for every prompt, 30.5 KiB for each of its heads, and 0.5 KiB
     L = gdn(dk=64, dv=64, act=abi.SKSSM_BF16, sk=abi.SKSSM_BF16)
     assert abi.sketchssm_prefill_workspace_bytes(L, 16, 2) == 0
-    assert abi.sketchssm_prefill_workspace_bytes(L, 17, 2) == 2 * 4 * 31232 + 512
+    assert abi.sketchssm_prefill_workspace_bytes(L, 17, 2) == 1 * 4 * 31232 + 512      # one prompt of 17 at most
+    assert abi.sketchssm_prefill_workspace_bytes(L, 128, 2) == 4 * 4 * 31232 + 512
     assert abi.sketchssm_prefill_workspace_bytes(L, 640, 2) == 12 * 4 * 31232 + 512
     assert abi.sketchssm_prefill_workspace_bytes(L, (1 << 31) - 1, 2) == (33554431 + 2) * 4 * 31232 + 512
     assert abi.sketchssm_prefill_workspace_bytes(gdn(), 640, 2) == 0
@@ -195,7 +196,7 @@ def test_cache_calls():
     (dict(groups=65536, width=8), abi.SKSSM_EDIM), (dict(width=0), abi.SKSSM_EDIM), (dict(width=12), abi.SKSSM_EDIM),
     (dict(width=8200), abi.SKSSM_EDIM), (dict(x_stride=124), abi.SKSSM_EDIM), (dict(x_stride=130), abi.SKSSM_EDIM),
     (dict(y_stride=-128), abi.SKSSM_EDIM), (dict(gate_stride=0), abi.SKSSM_EDIM),
-    (dict(y_stride=1 << 31), abi.SKSSM_EDIM), (dict(dtype=2), abi.SKSSM_EDTYPE), (dict(dtype=-1), abi.SKSSM_EDTYPE),
+    (dict(y_stride=(1 << 25) + 64), abi.SKSSM_EDIM), (dict(dtype=2), abi.SKSSM_EDTYPE), (dict(dtype=-1), abi.SKSSM_EDTYPE),
     (dict(activation=3), abi.SKSSM_EFLAG), (dict(activation=-1), abi.SKSSM_EFLAG), (dict(centred=2), abi.SKSSM_EFLAG),
     (dict(gate_first=-1), abi.SKSSM_EFLAG), (dict(group_weights=2), abi.SKSSM_EFLAG),
 ])
