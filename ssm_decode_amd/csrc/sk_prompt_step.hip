@@ -1,7 +1,7 @@
 // Prompts through the gated delta rule, one token at a time:
 //   u = beta (v - alpha S^T k),  S <- alpha S + k u^T,  o = S^T q.
-// One workgroup per (prompt, head); a wave holds 32 columns of the tile, all
-// of its rows, in registers for the whole prompt (the columns of S never mix,
+// One workgroup per (prompt, head); a wave holds 16 or 32 columns of the tile,
+// all of its rows, in registers for the whole prompt (the columns of S never mix,
 // so the waves of a tile meet only where the tokens are staged).
 //
 // A prompt of a few tokens is bound by its state's traffic (4 dk dv bytes in
@@ -50,9 +50,30 @@ struct Rows {
   }
 };
 
-template <int DK, int DV, typename AT>
-__global__ void __launch_bounds__(DV * 2) prompt_step_kernel(PromptParams p) {
-  constexpr int NT = DV * 2, MB = DK / 16;
+// A lane's part of column c's product with a token's vector.  (One running sum:
+// four that do not wait for one another measured slower, f32_heads64 212 us
+// against 187, step_b256 225 against 206, where they also cost a wave a SIMD.)
+template <int MB, int NCC>
+__device__ __forceinline__ float column_dot(const float (&s)[MB][NCC][4], const float (&x)[MB][4], int c) {
+  float a = 0.f;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) a += s[mb][c][v] * x[mb][v];
+  return a;
+}
+
+// NCC: columns of a lane.  Two where the state's traffic bounds the prompt
+// (bf16, up to kShort tokens: 8-byte loads and stores); one in fp32, whose
+// prompts of any length come here and are bound by the chain from token to
+// token: half the arithmetic of a token, with its key and value read from LDS
+// one token ahead (64 x 64 tiles, 512 tokens: 187 us against 256 with two columns).
+template <typename AT> constexpr int lane_columns() { return sizeof(AT) == 2 ? 2 : 1; }
+
+template <int DK, int DV, typename AT, int NCC = lane_columns<AT>()>
+__global__ void __launch_bounds__(DV * 4 / NCC) prompt_step_kernel(PromptParams p) {
+  constexpr int NT = DV * 4 / NCC, MB = DK / 16;
+  constexpr bool AHEAD = NCC == 1;
   __shared__ __align__(16) float s_k[TB * DK], s_q[TB * DK], s_v[TB * DV], s_ab[2 * TB];
 
   const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H;
@@ -64,26 +85,33 @@ __global__ void __launch_bounds__(DV * 2) prompt_step_kernel(PromptParams p) {
   const bool in = b >= 0 && b < p.B;
 
   const int tid = threadIdx.x, lane = tid & 63, cg = lane & 15, rg = lane >> 4;
-  const int col0 = 32 * (tid >> 6), col = col0 + 2 * cg;
+  const int col0 = 16 * NCC * (tid >> 6), col = col0 + NCC * cg;
   float* Sg = p.S + ((size_t)(in ? b : 0) * p.H + h) * DK * DV + (size_t)(4 * rg) * DV + col;
 
   // the state's loads are in flight over the checks and the tokens' first loads
-  float s[MB][2][4];
+  float s[MB][NCC][4];
   if (in && (!p.has_state || p.has_state[i] != 0)) {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        float x[2];
-        ldn_nt<2>(Sg + (size_t)(16 * mb + v) * DV, x);
-        s[mb][0][v] = x[0];
-        s[mb][1][v] = x[1];
+        const float* at = Sg + (size_t)(16 * mb + v) * DV;
+        if constexpr (NCC == 2) {
+          float x[2];
+          ldn_nt<2>(at, x);
+          s[mb][0][v] = x[0];
+          s[mb][1][v] = x[1];
+        } else {
+          s[mb][0][v] = *at;
+        }
       }
   } else {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) s[mb][0][v] = s[mb][1][v] = 0.f;
+      for (int c = 0; c < NCC; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) s[mb][c][v] = 0.f;
   }
   if (!prompt_ok(p, i, h, b) || len > p.len_hi) return;
 
@@ -121,49 +149,40 @@ __global__ void __launch_bounds__(DV * 2) prompt_step_kernel(PromptParams p) {
       nt = left < TB ? left : TB;
       fetch(t0 + TB, nt);
     }
-    float kk[MB][4], vv[2], al, be;
+    float kk[MB][4], vv[NCC], al, be;
     auto token = [&](int j) {                // a token's key, value and factors
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) ld4(s_k + j * DK + 16 * mb + 4 * rg, kk[mb]);
-      ldn<2>(s_v + j * DV + col, vv);
+      ldn<NCC>(s_v + j * DV + col, vv);
       al = s_ab[j];
       be = s_ab[TB + j];
     };
-    token(0);
+    if (AHEAD) token(0);
 #pragma unroll 1
     for (int j = 0; j < now; ++j) {
+      if (!AHEAD) token(j);
       float qq[MB][4];
+      auto query = [&]() {
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) ld4(s_q + j * DK + 16 * mb + 4 * rg, qq[mb]);
-      float a0 = 0.f, a1 = 0.f;
+        for (int mb = 0; mb < MB; ++mb) ld4(s_q + j * DK + 16 * mb + 4 * rg, qq[mb]);
+      };
+      if (AHEAD) query();
+      float u[NCC];
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          a0 += s[mb][0][v] * kk[mb][v];
-          a1 += s[mb][1][v] * kk[mb][v];
-        }
-      a0 = row_groups_sum(a0);
-      a1 = row_groups_sum(a1);
-      const float u0 = be * (vv[0] - al * a0), u1 = be * (vv[1] - al * a1);
+      for (int c = 0; c < NCC; ++c)
+        u[c] = be * (vv[c] - al * row_groups_sum(column_dot<MB, NCC>(s, kk, c)));
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          s[mb][0][v] = al * s[mb][0][v] + kk[mb][v] * u0;
-          s[mb][1][v] = al * s[mb][1][v] + kk[mb][v] * u1;
-        }
-      if (j + 1 < now) token(j + 1);         // in flight over this token's output
-      float o0 = 0.f, o1 = 0.f;
+        for (int c = 0; c < NCC; ++c)
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
+          for (int v = 0; v < 4; ++v) s[mb][c][v] = al * s[mb][c][v] + kk[mb][v] * u[c];
+      if (AHEAD && j + 1 < now) token(j + 1);        // in flight over this token's output
+      if (!AHEAD) query();
+      float o[NCC];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          o0 += s[mb][0][v] * qq[mb][v];
-          o1 += s[mb][1][v] * qq[mb][v];
-        }
-      const float o2[2] = {row_groups_sum(o0), row_groups_sum(o1)};
-      if (rg == 0) stn<2>(op + (t0 + j) * p.os, o2);
+      for (int c = 0; c < NCC; ++c) o[c] = row_groups_sum(column_dot<MB, NCC>(s, qq, c));
+      if (rg == 0) stn<NCC>(op + (t0 + j) * p.os, o);
     }
     __syncthreads();
   }
@@ -172,19 +191,24 @@ __global__ void __launch_bounds__(DV * 2) prompt_step_kernel(PromptParams p) {
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float x[2] = {s[mb][0][v], s[mb][1][v]};
-      stn_nt<2>(Sg + (size_t)(16 * mb + v) * DV, x);
+      float* at = Sg + (size_t)(16 * mb + v) * DV;
+      if constexpr (NCC == 2) {
+        const float x[2] = {s[mb][0][v], s[mb][1][v]};
+        stn_nt<2>(at, x);
+      } else {
+        *at = s[mb][0][v];
+      }
     }
-  if (p.prime) sketch_tile<DK, DV, AT>(p.sk, s, b, h, col0, lane);
+  if (p.prime) sketch_tile<DK, DV, AT, NCC>(p.sk, s, b, h, col0, lane);
 }
 
 template <int DK, int DV>
 int launch_shape(int act, const PromptParams& p, hipStream_t st) {
-  const dim3 grid(p.nseq * p.H), block(DV * 2);
+  const dim3 grid(p.nseq * p.H);
   if (act == DT_F32)
-    hipLaunchKernelGGL((prompt_step_kernel<DK, DV, float>), grid, block, 0, st, p);
+    hipLaunchKernelGGL((prompt_step_kernel<DK, DV, float>), grid, dim3(DV * 4 / lane_columns<float>()), 0, st, p);
   else
-    hipLaunchKernelGGL((prompt_step_kernel<DK, DV, bf16>), grid, block, 0, st, p);
+    hipLaunchKernelGGL((prompt_step_kernel<DK, DV, bf16>), grid, dim3(DV * 4 / lane_columns<bf16>()), 0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 

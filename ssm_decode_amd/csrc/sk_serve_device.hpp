@@ -47,14 +47,14 @@ __device__ __forceinline__ float row_groups_sum(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// Registers of a wave's 32 columns of a tile, as the flush holds them: with
-// cg = lane % 16 and rg = lane / 16,
-//   s[mb][c][v] = S[16 mb + 4 rg + v][col0 + 2 cg + c].
+// Registers of a wave's 16 NCC columns of a tile (NCC = 2: as the flush holds
+// them): with cg = lane % 16 and rg = lane / 16,
+//   s[mb][c][v] = S[16 mb + 4 rg + v][col0 + NCC cg + c].
 // The layout is the A operand of v_mfma_f32_16x16x4_f32 for S^T (K-step
 // (mb, v) covers rows 16 mb + 4 k + v), so the sketch needs no data movement:
-// lane holds u_j, j = cg, at columns col0 + 2 (4 rg + vv) + c.
-template <int DK, int DV, typename UT>
-__device__ __forceinline__ void sketch_tile(const SketchOut& sk, const float (&s)[DK / 16][2][4], int b, int h,
+// lane holds u_j, j = cg, at columns col0 + NCC (4 rg + vv) + c.
+template <int DK, int DV, typename UT, int NCC>
+__device__ __forceinline__ void sketch_tile(const SketchOut& sk, const float (&s)[DK / 16][NCC][4], int b, int h,
                                             int col0, int lane) {
   constexpr int MB = DK / 16;
   const int cg = lane & 15, rg = lane >> 4;
@@ -62,32 +62,39 @@ __device__ __forceinline__ void sketch_tile(const SketchOut& sk, const float (&s
   if (r == 0) {                       // a dense-fallback head: the state copy
     int slot = 0;
     while (slot + 1 < sk.ndense && sk.dense_list[slot] != h) ++slot;
-    UT* C = reinterpret_cast<UT*>(sk.Sc) + ((size_t)b * sk.ndense + slot) * DK * DV + col0 + 2 * cg;
+    UT* C = reinterpret_cast<UT*>(sk.Sc) + ((size_t)b * sk.ndense + slot) * DK * DV + col0 + NCC * cg;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const float x[2] = {s[mb][0][v], s[mb][1][v]};
-        stn<2>(C + (size_t)(16 * mb + 4 * rg + v) * DV, x);
+        float x[NCC];
+#pragma unroll
+        for (int c = 0; c < NCC; ++c) x[c] = s[mb][c][v];
+        stn<NCC>(C + (size_t)(16 * mb + 4 * rg + v) * DV, x);
       }
     return;
   }
-  f32x4s u0 = {0.f, 0.f, 0.f, 0.f}, u1 = u0;
+  f32x4s u[NCC];
+#pragma unroll
+  for (int c = 0; c < NCC; ++c) u[c] = f32x4s{0.f, 0.f, 0.f, 0.f};
   const float* pr = sk.Pt + (size_t)(off + (cg < r ? cg : 0)) * DK + 4 * rg;
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb) {
     float x[4];
     ld4(pr + 16 * mb, x);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      u0 = __builtin_amdgcn_mfma_f32_16x16x4f32(s[mb][0][v], x[v], u0, 0, 0, 0);
-      u1 = __builtin_amdgcn_mfma_f32_16x16x4f32(s[mb][1][v], x[v], u1, 0, 0, 0);
-    }
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int c = 0; c < NCC; ++c) u[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(s[mb][c][v], x[v], u[c], 0, 0, 0);
   }
   if (cg < r) {                       // (columns j >= r repeat row 0 and are dropped)
-    UT* U = reinterpret_cast<UT*>(sk.U) + ((size_t)b * sk.R + off + cg) * DV + col0 + 8 * rg;
-    const float x[8] = {u0[0], u1[0], u0[1], u1[1], u0[2], u1[2], u0[3], u1[3]};
-    stn<8>(U, x);
+    UT* U = reinterpret_cast<UT*>(sk.U) + ((size_t)b * sk.R + off + cg) * DV + col0 + 4 * NCC * rg;
+    float x[4 * NCC];
+#pragma unroll
+    for (int vv = 0; vv < 4; ++vv)
+#pragma unroll
+      for (int c = 0; c < NCC; ++c) x[NCC * vv + c] = u[c][vv];
+    stn<4 * NCC>(U, x);
   }
 }
 

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(DV * 2) state_load_kernel(CacheParams p) {
       s[mb][1][v] = x[1];
       stn_nt<2>(Sg + (size_t)m * DV, x);
     }
-  if (p.prime) sketch_tile<DK, DV, UT>(p.sk, s, b, h, col0, lane);
+  if (p.prime) sketch_tile<DK, DV, UT, 2>(p.sk, s, b, h, col0, lane);
   if (tid == 0) p.count[(size_t)b * p.H + h] = 0;
 }
 
