@@ -50,19 +50,6 @@ struct Rows {
   }
 };
 
-// A lane's part of column c's product with a token's vector.  (One running sum:
-// four that do not wait for one another measured slower, f32_heads64 212 us
-// against 187, step_b256 225 against 206, where they also cost a wave a SIMD.)
-template <int MB, int NCC>
-__device__ __forceinline__ float column_dot(const float (&s)[MB][NCC][4], const float (&x)[MB][4], int c) {
-  float a = 0.f;
-#pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) a += s[mb][c][v] * x[mb][v];
-  return a;
-}
-
 // NCC: columns of a lane.  Two where the state's traffic bounds the prompt
 // (bf16, up to kShort tokens: 8-byte loads and stores); one in fp32, whose
 // prompts of any length come here and are bound by the chain from token to
@@ -169,8 +156,14 @@ __global__ void __launch_bounds__(DV * 4 / NCC) prompt_step_kernel(PromptParams 
       if (AHEAD) query();
       float u[NCC];
 #pragma unroll
-      for (int c = 0; c < NCC; ++c)
-        u[c] = be * (vv[c] - al * row_groups_sum(column_dot<MB, NCC>(s, kk, c)));
+      for (int c = 0; c < NCC; ++c) {
+        float a = 0.f;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) a += s[mb][c][v] * kk[mb][v];
+        u[c] = be * (vv[c] - al * row_groups_sum(a));
+      }
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -181,7 +174,14 @@ __global__ void __launch_bounds__(DV * 4 / NCC) prompt_step_kernel(PromptParams 
       if (!AHEAD) query();
       float o[NCC];
 #pragma unroll
-      for (int c = 0; c < NCC; ++c) o[c] = row_groups_sum(column_dot<MB, NCC>(s, qq, c));
+      for (int c = 0; c < NCC; ++c) {
+        float a = 0.f;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) a += s[mb][c][v] * qq[mb][v];
+        o[c] = row_groups_sum(a);
+      }
       if (rg == 0) stn<NCC>(op + (t0 + j) * p.os, o);
     }
     __syncthreads();
