@@ -281,6 +281,18 @@ __device__ __forceinline__ void copy16(const void* base, uint32_t offset, uint32
                "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
                : "memory");
 }
+// Four runs of 1 KiB, one behind the other in memory and in LDS (the
+// instruction's offset counts for both addresses).
+__device__ __forceinline__ void copy16x4(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\ts_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, %1\n\t"
+      "global_load_lds_dwordx4 %0, %1 offset:1024\n\t"
+      "global_load_lds_dwordx4 %0, %1 offset:2048\n\t"
+      "global_load_lds_dwordx4 %0, %1 offset:3072" ::"v"(offset),
+      "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
+      : "memory");
+}
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
@@ -388,11 +400,13 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   auto piece = [&](int row, int pc) { return row * PPR + (pc ^ swz(row)); };
   const uint32_t lds0 = lds_address(smem);
   constexpr int KU = PPR / NW, KROWS = 64 * NW / PPR;      // a wave's units of 64 pieces of K, rows from one to the next
-  // (the workspace's last unit reaches into what lies behind it; there is one
-  // unit less than the waves take, and the last takes the first once more)
-  constexpr int WUNITS = (CHUNK_WORK_BYTES + PROMPT_WORK_OVER) / 1024, WU = (WUNITS + 1) / NW, UNITS = 2 * KU + 2 + WU;
-  static_assert((CHUNK_WORK_BYTES + PROMPT_WORK_OVER) % 1024 == 0 && (WUNITS + 1) % NW == 0, "units of the waves");
-  const int wlast = (WU - 1) * NW + wv < WUNITS ? (WU - 1) * NW + wv : 0;
+  // The workspace in runs of 1 KiB, RUNS to a wave; the last reaches into what
+  // lies behind it, and the last wave begins one run early (there is one less
+  // than the waves take).
+  constexpr int WRUNS = (CHUNK_WORK_BYTES + PROMPT_WORK_OVER) / 1024, RUNS = (WRUNS + 1) / NW;
+  static_assert((CHUNK_WORK_BYTES + PROMPT_WORK_OVER) % 1024 == 0 && (WRUNS + 1) % NW == 0 && RUNS % 4 == 0, "runs");
+  constexpr int WU = RUNS / 4, UNITS = 2 * KU + WU + 2;
+  const int run0 = (wv < NW - 1 ? wv * RUNS : WRUNS - RUNS) * 1024;
   const int krow = (wv * 64 + lane) / PPR, kpc = lane % PPR, vrow = lane >> 1;
   // Byte offset of a lane's piece from a chunk's first row (unsigned 32 bits: 63
   // rows of at most 2^25 elements fit).  Rows behind the prompt's end repeat its
@@ -412,36 +426,43 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   const uint32_t krow2 = (uint32_t)(krow * p.ks * 2), qrow2 = (uint32_t)(krow * p.qs * 2);
   const uint32_t sw[2] = {(uint32_t)(kpc ^ swz(krow)) * 16, (uint32_t)(kpc ^ swz(krow + KROWS)) * 16};
   const uint32_t vo = voff(0, PC), wo = lane * 16;
-  const int64_t kstep = KROWS * p.ks, qstep = KROWS * p.qs;
-  // unit u of the whole chunk at t0 into a buffer: K, Q, then the workspace, V last
-  auto copy_unit = [&](int u, int t0, uint32_t l0) {
+  // unit u of a whole chunk into a buffer: K, Q, then the workspace, V last.
+  // The uniform addresses go from chunk to chunk.
+  const bf16 *kc = kp, *qc = qp, *vc = vp;
+  const unsigned char* wc = wp + run0;
+  auto copy_unit = [&](int u, uint32_t l0) {
     if (u < KU) {
-      copy16(kp + (int64_t)t0 * p.ks + u * kstep, krow2 + sw[u & 1], l0 + L::K + (NW * u + wv) * 1024);
+      copy16(kc + u * KROWS * p.ks, krow2 + sw[u & 1], l0 + L::K + (NW * u + wv) * 1024);
     } else if (u < 2 * KU) {
       const int v = u - KU;
-      copy16(qp + (int64_t)t0 * p.qs + v * qstep, qrow2 + sw[v & 1], l0 + L::Q + (NW * v + wv) * 1024);
+      copy16(qc + v * KROWS * p.qs, qrow2 + sw[v & 1], l0 + L::Q + (NW * v + wv) * 1024);
     } else if (u < 2 * KU + WU) {
-      const int unit = u < 2 * KU + WU - 1 ? NW * (u - 2 * KU) + wv : wlast;
-      copy16(wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_BYTES + unit * 1024, wo, l0 + L::W + unit * 1024);
+      const int v = u - 2 * KU;
+      copy16x4(wc + v * 4096, wo, l0 + L::W + run0 + v * 4096);
     } else {
       const int v = u - 2 * KU - WU;
-      copy16(vp + (t0 + 32 * v) * p.vs, vo, l0 + L::V + wv * 2048 + v * 1024);
+      copy16(vc + 32 * v * p.vs, vo, l0 + L::V + wv * 2048 + v * 1024);
     }
+  };
+  auto next_chunk = [&]() {
+    kc += PC * p.ks;
+    qc += PC * p.qs;
+    vc += PC * p.vs;
+    wc += (size_t)p.H * CHUNK_WORK_BYTES;
   };
   // the whole of a chunk that may be a prompt's last
-  auto copy_all = [&](int t0, int nt, uint32_t l0) {
+  auto copy_last = [&](int nt, uint32_t l0) {
 #pragma unroll 1
     for (int v = 0; v < KU; ++v) {
-      copy16(kp + t0 * p.ks, koff(v, p.ks, nt - 1), l0 + L::K + (NW * v + wv) * 1024);
-      copy16(qp + t0 * p.qs, koff(v, p.qs, nt - 1), l0 + L::Q + (NW * v + wv) * 1024);
+      copy16(kc, koff(v, p.ks, nt - 1), l0 + L::K + (NW * v + wv) * 1024);
+      copy16(qc, koff(v, p.qs, nt - 1), l0 + L::Q + (NW * v + wv) * 1024);
     }
 #pragma unroll 1
-    for (int v = 0; v < 2; ++v)
-      copy16(vp + t0 * p.vs, voff(v, nt - 1), l0 + L::V + wv * 2048 + v * 1024);
+    for (int v = 0; v < 2; ++v) copy16(vc, voff(v, nt - 1), l0 + L::V + wv * 2048 + v * 1024);
 #pragma unroll
-    for (int u = 2 * KU; u < 2 * KU + WU; ++u) copy_unit(u, t0, l0);
+    for (int u = 2 * KU; u < 2 * KU + WU; ++u) copy_unit(u, l0);
   };
-  if (len > 0) copy_all(0, len < PC ? len : PC, lds0);
+  if (len > 0) copy_last(len < PC ? len : PC, lds0);
 
   // --------------------------------------------------------- fragments
   const unsigned char* sb = smem;                // the present chunk's buffer
@@ -516,7 +537,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
       if constexpr (MORE) {
 #pragma unroll
         for (int u = from; u < to; ++u)
-          if (u < UNITS) copy_unit(u, t0 + PC, lnext);
+          if (u < UNITS) copy_unit(u, lnext);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -533,7 +554,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     __builtin_amdgcn_sched_barrier(0);
     if (t0 > 0) read_out(smem + (buf ^ 1) * L::BUF + L::V + wv * 2048);
     const float gC = s_g[PC - 1];
-    if (!MORE && left > 0) copy_all(t0 + PC, left, lnext);
+    next_chunk();
+    if (!MORE && left > 0) copy_last(left, lnext);
     __builtin_amdgcn_sched_barrier(0);
 
     Block R[2], O[2], U[2];
