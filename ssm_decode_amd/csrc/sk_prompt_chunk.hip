@@ -6,6 +6,29 @@
 namespace sk {
 namespace {
 
+// The prompt that has a slot (of 2^shift tokens: chunks, or segments of a
+// prompt), and its rank among those taken in chunks: the last whose first slot
+// is not behind this one (-1: none; its own end is for the caller to check).
+__device__ __forceinline__ int slot_prompt(const PromptParams& p, int slot, int shift, int* rank) {
+  const int lane = threadIdx.x & 63;
+  int i = -1, ranks = 0;
+  for (int j0 = 0; j0 < p.nseq; j0 += 64) {
+    const int j = j0 + lane < p.nseq ? j0 + lane : p.nseq - 1;
+    const int a = p.start[j];
+    const bool mine = j0 + lane < p.nseq && (int64_t)p.start[j + 1] - a > p.len_lo;
+    const unsigned long long all = __ballot(mine);
+    const int r = ranks + __popcll(all & ((1ull << lane) - 1));
+    const unsigned long long m = __ballot(mine && first_slot(a, r, shift) <= slot);
+    if (m) {
+      const int l = 63 - __clzll(m);
+      i = j0 + l;
+      *rank = ranks + __popcll(all & ((1ull << l) - 1));
+    }
+    ranks += __popcll(all);
+  }
+  return i;
+}
+
 // ------------------------------------------------------------ T and P
 // One workgroup of four waves per (chunk slot, head).  K K^T and Q K^T on the
 // bf16 matrix cores (exact products, fp32 sums); the unit triangular inverse
@@ -26,26 +49,12 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   // recent in the memory-side cache)
   const int rslot = blockIdx.x / p.H, h = blockIdx.x - rslot * p.H, slot = p.nslots - 1 - rslot;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  // the last prompt taken in chunks whose first slot is not behind this one
-  int i = -1, rank = 0, ranks = 0;
-  for (int j0 = 0; j0 < p.nseq; j0 += 64) {
-    const int j = j0 + lane < p.nseq ? j0 + lane : p.nseq - 1;
-    const int a = p.start[j];
-    const bool mine = j0 + lane < p.nseq && (int64_t)p.start[j + 1] - a > p.len_lo;
-    const unsigned long long all = __ballot(mine);
-    const int r = ranks + __popcll(all & ((1ull << lane) - 1));
-    const unsigned long long m = __ballot(mine && first_slot(a, r) <= slot);
-    if (m) {
-      const int l = 63 - __clzll(m);
-      i = j0 + l;
-      rank = ranks + __popcll(all & ((1ull << l) - 1));
-    }
-    ranks += __popcll(all);
-  }
+  int rank;
+  const int i = slot_prompt(p, slot, 6, &rank);
   if (i < 0) return;
   const int s0 = p.start[i], s1 = p.start[i + 1];
   if (s0 < 0 || s1 < s0 || s1 > p.tokens) return;      // (the other launches report it)
-  const int c0 = (slot - first_slot(s0, rank)) * PC, len = s1 - s0;
+  const int c0 = (slot - first_slot(s0, rank, 6)) * PC, len = s1 - s0;
   if (c0 >= len) return;
   const int nt = len - c0 < PC ? len - c0 : PC;
   const int64_t tok = (int64_t)s0 + c0;
@@ -362,7 +371,15 @@ __device__ __forceinline__ int chunked_prompt(const PromptParams& p, int x, int*
   return -1;
 }
 
-template <int DK, int DV, int NW>
+// Where few tiles have many tokens (p.seg_shift != 0), prompts are cut into
+// segments of 2^seg_shift tokens, and three launches take the place of one:
+//   1. STATE: the segments but the last, at once, without outputs: each from a
+//      zero state (the first from the prompt's), which gives B, and, as further
+//      columns, from the identity with no values, which gives the segment's
+//      transition M: the state behind a segment is M S + B;
+//   2. prompt_join_kernel: the states between the segments, in order;
+//   3. the segments at once, each from the state before it, with outputs.
+template <int DK, int DV, int NW, bool OUT>
 __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p) {
   using L = ChunkLds<DK, NW>;
   constexpr int PPR = DK / 8, DB = DK / 32;      // 16-byte pieces of a row, blocks of 32 rows
@@ -372,23 +389,41 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, hi = lane >> 4;
-  // (the parts of a tile are nchunked * H workgroups apart: mostly on one XCD,
-  // whose cache then serves the K, Q, T and P that they share)
-  const int tiles = p.nchunked * p.H, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
+  // (the parts of a tile are as many workgroups apart as there are tiles: mostly
+  // on one XCD, whose cache then serves the K, Q, T and P that they share)
+  const int tiles = (p.seg_shift ? p.nsegs : p.nchunked) * p.H, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
   const int h = tile % p.H;
-  int rank = 0;
-  const int i = chunked_prompt(p, tile / p.H, &rank);
+  int rank = 0, seg = 0;
+  const int i = p.seg_shift ? slot_prompt(p, tile / p.H, p.seg_shift, &rank) : chunked_prompt(p, tile / p.H, &rank);
   if (i < 0) return;
-  const int s0 = p.start[i], len = p.start[i + 1] - s0, b = p.seqs ? p.seqs[i] : i;
+  int s0 = p.start[i], len = p.start[i + 1] - s0;
+  const int b = p.seqs ? p.seqs[i] : i;
+  bool last = true;                              // the prompt's last segment
+  static_assert(DV <= DK, "a state fits the place of a transition");
+  constexpr int VPARTS = DV / (16 * NW);
+  const bool unit = !OUT && part >= VPARTS;      // columns of the identity
+  const int slot0 = first_slot(s0, rank, 6);
+  float* own = nullptr;                          // this segment's B (then the state behind it) and M
+  constexpr int SEG_FLOATS = DK * (DV + DK);
+  if (p.seg_shift) {
+    seg = tile / p.H - first_slot(s0, rank, p.seg_shift);
+    const int64_t from = (int64_t)seg << p.seg_shift;
+    if (from >= len && seg > 0) return;
+    last = len - from <= (1 << p.seg_shift);
+    if (!OUT && (last || (unit && seg == 0))) return;
+    own = p.seg + ((size_t)(tile / p.H) * p.H + h) * SEG_FLOATS;
+    s0 += (int)from;
+    len = last ? len - (int)from : 1 << p.seg_shift;
+  }
   if (!prompt_ok(p, i, h, b)) return;
 
-  const int c0 = part * NW * 16 + wv * 16;       // the wave's first column
+  const int c0 = (unit ? part - VPARTS : part) * NW * 16 + wv * 16;       // the wave's first column
   float* Sg = p.S + ((size_t)b * p.H + h) * DK * DV + c0 + n;
   const bf16* kp = reinterpret_cast<const bf16*>(p.k) + s0 * p.ks + (int64_t)h * DK;      // (all uniform)
   const bf16* qp = reinterpret_cast<const bf16*>(p.q) + s0 * p.qs + (int64_t)h * DK;
-  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + s0 * p.vs + (int64_t)h * DV + c0;
+  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + s0 * p.vs + (int64_t)h * DV + (unit ? 0 : c0);
   const unsigned char* wp = reinterpret_cast<const unsigned char*>(p.work) +
-                            ((size_t)first_slot(s0, rank) * p.H + h) * CHUNK_WORK_BYTES;
+                            ((size_t)(slot0 + (seg << (p.seg_shift ? p.seg_shift - 6 : 0))) * p.H + h) * CHUNK_WORK_BYTES;
 
   // ------------------------------------------------------------- copies
   // Rows of K and Q have their 16-byte pieces swizzled so that the rows of a
@@ -435,7 +470,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
       copy16(kc + u * KROWS * p.ks, krow2 + sw[u & 1], l0 + L::K + (NW * u + wv) * 1024);
     } else if (u < 2 * KU) {
       const int v = u - KU;
-      copy16(qc + v * KROWS * p.qs, qrow2 + sw[v & 1], l0 + L::Q + (NW * v + wv) * 1024);
+      if (OUT) copy16(qc + v * KROWS * p.qs, qrow2 + sw[v & 1], l0 + L::Q + (NW * v + wv) * 1024);
     } else if (u < 2 * KU + WU) {
       const int v = u - 2 * KU;
       copy16x4(wc + v * 4096, wo, l0 + L::W + run0 + v * 4096);
@@ -455,7 +490,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll 1
     for (int v = 0; v < KU; ++v) {
       copy16(kc, koff(v, p.ks, nt - 1), l0 + L::K + (NW * v + wv) * 1024);
-      copy16(qc, koff(v, p.qs, nt - 1), l0 + L::Q + (NW * v + wv) * 1024);
+      if (OUT) copy16(qc, koff(v, p.qs, nt - 1), l0 + L::Q + (NW * v + wv) * 1024);
     }
 #pragma unroll 1
     for (int v = 0; v < 2; ++v) copy16(vc, voff(v, nt - 1), l0 + L::V + wv * 2048 + v * 1024);
@@ -486,11 +521,34 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   };
 
   Block S[DB];
-  const bool cont = !p.has_state || p.has_state[i] != 0;
+  {
+    // the prompt's state or zero; behind the first segment the state before it,
+    // or, where that is not known yet, zero or the identity
+    // (the first segment has no use for M: its place keeps the state that the
+    // prompt starts from, which the last segment of the third launch overwrites
+    // while the first may not have read it yet)
+    const float* from = Sg;
+    bool read = seg == 0 ? !p.has_state || p.has_state[i] != 0 : OUT;
+    if (seg > 0) from = own - (size_t)p.H * SEG_FLOATS + c0 + n;
+    if (OUT && seg == 0 && !last) {
+      from = own + DK * DV + c0 + n;
+      read = true;
+    }
 #pragma unroll
-  for (int db = 0; db < DB; ++db)
+    for (int db = 0; db < DB; ++db)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) S[db][e >> 2][e & 3] = cont ? Sg[(size_t)(32 * db + 8 * hi + e) * DV] : 0.f;
+      for (int e = 0; e < 8; ++e) {
+        const int row = 32 * db + 8 * hi + e;
+        S[db][e >> 2][e & 3] = read ? from[(size_t)row * DV] : unit && row == c0 + n ? 1.f : 0.f;
+      }
+    if (!OUT && seg == 0) {
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          own[DK * DV + (size_t)(32 * db + 8 * hi + e) * DV + c0 + n] = S[db][e >> 2][e & 3];
+    }
+  }
 
   // The wave's outputs of a chunk leave in the next chunk's time: from LDS,
   // columns of 64 tokens in eight swizzled pieces, as rows of eight columns.
@@ -552,10 +610,13 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     };
     load_kq(L::K, 0);
     __builtin_amdgcn_sched_barrier(0);
-    if (t0 > 0) read_out(smem + (buf ^ 1) * L::BUF + L::V + wv * 2048);
+    if (OUT && t0 > 0) read_out(smem + (buf ^ 1) * L::BUF + L::V + wv * 2048);
     const float gC = s_g[PC - 1];
     next_chunk();
-    if (!MORE && left > 0) copy_last(left, lnext);
+    if (!MORE && left > 0) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the outputs are read where V will land
+      copy_last(left, lnext);
+    }
     __builtin_amdgcn_sched_barrier(0);
 
     Block R[2], O[2], U[2];
@@ -571,7 +632,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
         float x[8];
         rows8(S[j + 1], x);
         split8<3>(x, ss[j + 1]);
-      } else {
+      } else if (OUT) {
         load_kq(L::Q, DB);                       // (block 0 of Q, into the buffer that follows)
       }
 #pragma unroll
@@ -590,7 +651,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
       region<12, 1, 4>();
       copies(2 * j, 2 * j + 2);
     }
-    if (t0 > 0) store_out(t0 - PC, PC);
+    if (OUT && t0 > 0) store_out(t0 - PC, PC);
     __builtin_amdgcn_sched_barrier(0);
     bf16x8 br[2][3];
     auto load_t = [&](int kb) {
@@ -601,33 +662,41 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll
           for (int v = 0; v < 3; ++v) ft[kb][rb][t][v] = frag_t((rb + kb) * 2 + t, v);
     };
+    auto split_r = [&](int rb) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = !OUT && unit ? 0.f : (float)vv[rb][e];
+        x[e] = v - gm[rb][e] * R[rb][e >> 2][e & 3];
+      }
+      split8<3>(x, br[rb]);
+    };
     // O = Q S (two values);  R = V - g (K S) and its split meanwhile
 #pragma unroll
     for (int j = 0; j < DB; ++j) {
-      if (j + 1 < DB) load_kq(L::Q, DB + j + 1);
-      else load_t(0);
+      if constexpr (OUT) {
+        if (j + 1 < DB) load_kq(L::Q, DB + j + 1);
+        else load_t(0);
 #pragma unroll
-      for (int v = 1; v >= 0; --v)
+        for (int v = 1; v >= 0; --v)
 #pragma unroll
-        for (int rb = 0; rb < 2; ++rb)
+          for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) O[rb][t] = mm32(fa[(DB + j) & 1][rb][t], ss[j][v], O[rb][t]);
+            for (int t = 0; t < 2; ++t) O[rb][t] = mm32(fa[(DB + j) & 1][rb][t], ss[j][v], O[rb][t]);
+      } else if (j == 0) {
+        load_t(0);
+      }
 #pragma unroll
       for (int rb = 0; rb < 2; ++rb)
-        if (j == (rb + 1) * DB / 4) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = (float)vv[rb][e] - gm[rb][e] * R[rb][e >> 2][e & 3];
-          split8<3>(x, br[rb]);
-        }
-      region<8, 2, 8>();
+        if (j == (rb + 1) * DB / 4) split_r(rb);
+      if constexpr (OUT) region<8, 2, 8>();
       copies(2 * DB + j, 2 * DB + j + 1);
     }
     bf16x8 bu[2][3], bo[2][2];
     auto split_u = [&](int kb) {
       float x[8];
       rows8(U[kb], x);
-      split8<2>(x, bo[kb]);
+      if (OUT) split8<2>(x, bo[kb]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] *= dm[kb][e];
       split8<3>(x, bu[kb]);
@@ -638,7 +707,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int v = 0; v < 2; ++v) fp[kb][rb][t][v] = frag_p((rb + kb) * 2 + t, v);
+          for (int v = 0; v < 2; ++v)
+            if (OUT) fp[kb][rb][t][v] = frag_p((rb + kb) * 2 + t, v);
 #pragma unroll
       for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -660,7 +730,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
 #pragma unroll
-          for (int rb = 0; rb < 2; ++rb) O[rb][e >> 2][e & 3] *= gm[rb][e];
+          for (int rb = 0; rb < 2; ++rb)
+            if (OUT) O[rb][e >> 2][e & 3] *= gm[rb][e];
 #pragma unroll
           for (int db = 0; db < DB; ++db) S[db][e >> 2][e & 3] *= gC;
         }
@@ -685,7 +756,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll
         for (int rb = kb; rb < 2; ++rb)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) O[rb][t] = mm32(fp[kb][rb][t][PA[v]], bo[kb][PB[v]], O[rb][t]);
+          for (int t = 0; t < 2; ++t)
+            if (OUT) O[rb][t] = mm32(fp[kb][rb][t][PA[v]], bo[kb][PB[v]], O[rb][t]);
 #pragma unroll
       for (int d0 = 0; d0 < DB; d0 += 2)         // (two blocks at a time: the first are done early)
 #pragma unroll
@@ -695,13 +767,13 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll
             for (int t = 0; t < 2; ++t) S[db][t] = mm32(fs[kb][db][t], bu[kb][v], S[db][t]);
       if (kb == 0) {
-        region<12 + 6 * DB, 1, 3>();
+        region<(OUT ? 12 : 0) + 6 * DB, 1, 3>();
         copies(3 * DB + 3, UNITS);
       }
     }
     unsigned char* so = smem + buf * L::BUF + L::V + wv * 2048;
 #pragma unroll
-    for (int rb = 0; rb < 2; ++rb) {
+    for (int rb = 0; rb < (OUT ? 2 : 0); ++rb) {
       bf16x8 w;
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = (__bf16)O[rb][e >> 2][e & 3];
@@ -710,23 +782,26 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     float x[8];
     rows8(S[0], x);
     split8<3>(x, ss[0]);
-    region<6 + 6 * DB, 0, 3>();
+    region<(OUT ? 6 : 0) + 6 * DB, 0, 3>();
     t0 += PC;
     buf ^= 1;
   };
   while (len - t0 >= 2 * PC) chunk(std::true_type{});
   while (t0 < len) chunk(std::false_type{});
-  if (len > 0) {
+  if (OUT && len > 0) {
     wave_lds_sync();
     read_out(sb + L::V + wv * 2048);
     store_out(t0 - PC, len - (t0 - PC));
   }
 
+  if (OUT && !last) return;                      // (the state behind a segment is known already)
+  float* to = OUT ? Sg : own + (unit ? DK * DV : 0) + c0 + n;
+  const int ld = unit ? DK : DV;
 #pragma unroll
   for (int db = 0; db < DB; ++db)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) Sg[(size_t)(32 * db + 8 * hi + e) * DV] = S[db][e >> 2][e & 3];
-  if (!p.prime) return;
+    for (int e = 0; e < 8; ++e) to[(size_t)(32 * db + 8 * hi + e) * ld] = S[db][e >> 2][e & 3];
+  if (!OUT || !p.prime) return;
   const int off = p.sk.off[h], r = p.sk.off[h + 1] - off;
   if (r == 0) {                                  // a dense-fallback head: the state copy
     int slot = 0;
@@ -755,20 +830,102 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   }
 }
 
-template <int DK, int DV, int NW>
+// The states between a prompt's segments: S behind segment g is M_g S + B_g,
+// written over B_g.  One workgroup per (prompt, head), a wave per 16 columns,
+// in fp32 throughout: a tile of S (rows 4 hi + r of column n) is the B operand
+// of v_mfma_f32_16x16x4_f32 with K-step r over rows {4 k + r}, so M is read as
+// runs of four columns (from LDS, one segment ahead, its pieces swizzled by
+// row) and the state never leaves its registers.
+template <int DK, int DV>
+__global__ void __launch_bounds__(4 * DV) prompt_join_kernel(PromptParams p) {
+  constexpr int TB = DK / 16, SEG_FLOATS = DK * (DV + DK), PPR = DK / 4, NW = DV / 16, RUNS = DK * DK * 4 / 1024 / NW;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int x = blockIdx.x / p.H, h = blockIdx.x - x * p.H;
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hi = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = wv * 16;
+  int rank = 0;
+  const int i = chunked_prompt(p, x, &rank);
+  if (i < 0) return;
+  const int s0 = p.start[i], len = p.start[i + 1] - s0;
+  const int segs = (int)(((int64_t)len + (1 << p.seg_shift) - 1) >> p.seg_shift);
+  if (!prompt_ok(p, i, h, p.seqs ? p.seqs[i] : i) || segs < 3) return;
+  float* seg = p.seg + ((size_t)first_slot(s0, rank, p.seg_shift) * p.H + h) * SEG_FLOATS;
+  const size_t step = (size_t)p.H * SEG_FLOATS;
+  const uint32_t lds0 = lds_address(smem);
+  auto copy = [&](int g) {                       // M_g into its buffer
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) {
+      const int c = 64 * (u * NW + wv) + lane, row = c / PPR, pc = c % PPR;
+      copy16(seg + g * step + DK * DV, (row * PPR + (pc ^ (row & 15))) * 16,
+             lds0 + (g & 1) * DK * DK * 4 + (u * NW + wv) * 1024);
+    }
+  };
+  f32x4s S[TB], N[TB];
+  auto block = [&](const float* B, f32x4s (&v)[TB]) {
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[tb][r] = B[(size_t)(16 * tb + 4 * hi + r) * DV + c0 + n];
+  };
+  copy(1);
+  block(seg, S);
+  block(seg + step, N);
+  for (int g = 1; g + 1 < segs; ++g) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (g + 2 < segs) copy(g + 1);
+    const float* Mg = reinterpret_cast<const float*>(smem + (g & 1) * DK * DK * 4);
+#pragma unroll
+    for (int kb = 0; kb < TB; ++kb)
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) {
+        float a[4];
+        ld4(Mg + ((16 * tb + n) * PPR + ((4 * kb + hi) ^ n)) * 4, a);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) N[tb] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], S[kb][r], N[tb], 0, 0, 0);
+      }
+    float* B = seg + g * step;
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+      S[tb] = N[tb];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) B[(size_t)(16 * tb + 4 * hi + r) * DV + c0 + n] = S[tb][r];
+    }
+    if (g + 2 < segs) block(B + step, N);
+  }
+}
+
+template <int DK, int DV, int NW, bool OUT>
+void launch_chunks(const PromptParams& p, hipStream_t st) {
+  const unsigned tiles = (unsigned)(p.seg_shift ? p.nsegs : p.nchunked) * p.H;
+  const unsigned parts = OUT ? DV / (16 * NW) : (DV + DK) / (16 * NW);
+  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, NW, OUT>), dim3(tiles * parts), dim3(64 * NW), (ChunkLds<DK, NW>::BYTES),
+                     st, p);
+}
+
+template <int DK, int DV>
 int launch(const PromptParams& p, hipStream_t st) {
+  constexpr int NW = DV / 16;                    // a workgroup has all columns of a tile
   hipLaunchKernelGGL((prompt_prep_kernel<DK>), dim3((unsigned)p.nslots * p.H), dim3(256), 0, st, p);
-  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, NW>), dim3((unsigned)p.nchunked * p.H * (DV / (16 * NW))), dim3(64 * NW),
-                     (ChunkLds<DK, NW>::BYTES), st, p);
+  if (p.seg_shift) {
+    launch_chunks<DK, DV, NW, false>(p, st);
+    hipLaunchKernelGGL((prompt_join_kernel<DK, DV>), dim3((unsigned)p.nchunked * p.H), dim3(4 * DV), 2 * DK * DK * 4, st,
+                       p);
+    launch_chunks<DK, DV, NW, true>(p, st);
+  } else if (p.nchunked * p.H <= 128) {          // .. unless that leaves CUs idle
+    launch_chunks<DK, DV, 4, true>(p, st);
+  } else {
+    launch_chunks<DK, DV, NW, true>(p, st);
+  }
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 }  // namespace
 
 int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st) {
-  if (dk == 64 && dv == 64) return launch<64, 64, 4>(p, st);
-  if (dk == 128 && dv == 64) return launch<128, 64, 4>(p, st);
-  if (dk == 128 && dv == 128) return p.nchunked * p.H <= 128 ? launch<128, 128, 4>(p, st) : launch<128, 128, 8>(p, st);
+  if (dk == 64 && dv == 64) return launch<64, 64>(p, st);
+  if (dk == 128 && dv == 64) return launch<128, 64>(p, st);
+  if (dk == 128 && dv == 128) return launch<128, 128>(p, st);
   return -2;
 }
 

@@ -38,10 +38,11 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ bf16x8 as_frag(const u32x4& x) { return __builtin_bit_cast(bf16x8, x); }
 
-// The slot of a prompt's first chunk, for the r-th of the prompts that are
-// taken in chunks: those of prompts that are behind one another are apart, and
-// there are at most tokens / 64 + their number.
-__device__ __forceinline__ int first_slot(int start, int r) { return (start >> 6) + r; }
+// The slot of a prompt's first chunk (shift 6) or segment of 2^shift tokens, for
+// the r-th of the prompts that are taken in chunks: those of prompts that are
+// behind one another are apart, and there are at most tokens / 2^shift + their
+// number.
+__device__ __forceinline__ int first_slot(int start, int r, int shift) { return (start >> shift) + r; }
 
 // Operands of v_mfma_f32_16x16x32_bf16 (hi = lane / 16, n = lane % 16).  A
 // block of 32 rows x 16 columns is two result tiles of four registers; MFMA

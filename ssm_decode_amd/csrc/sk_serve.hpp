@@ -28,6 +28,8 @@ struct PromptParams {
   int tokens, nseq;
   int len_lo, len_hi;       // the launch takes prompts of more than len_lo and up to len_hi tokens
   int nchunked, nslots;     // chunked form: prompts it may have, chunk slots of the workspace
+  int seg_shift, nsegs;     // prompts cut into segments of 2^seg_shift tokens (0: not), their slots
+  float* seg;               // [nsegs][H] states behind the segments (dk x dv) and their transitions (dk x dk)
   const void* q;
   const void* k;
   const void* v;
@@ -79,8 +81,8 @@ constexpr int PROMPT_CHUNK = 64;
 constexpr int PROMPT_CHUNK_WORK = 30 * 1024 + 512;
 constexpr int PROMPT_WORK_OVER = 512;    // read, not used, behind the last one
 inline bool prompt_chunked(int dk, int act) { return act == DT_BF16 && dk >= 64; }
-// Chunk slots that n prompts of together up to `tokens` tokens may take.
-inline int64_t prompt_slots(int64_t tokens, int64_t n) { return tokens / PROMPT_CHUNK + n; }
+// Slots of 2^shift tokens that n prompts of together up to `tokens` tokens may take.
+inline int64_t prompt_slots(int64_t tokens, int64_t n, int shift) { return (tokens >> shift) + n; }
 
 int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st);
 int launch_prompt_step(int dk, int dv, int act, const PromptParams& p, hipStream_t st);

@@ -16,20 +16,39 @@ constexpr int kMaxWidth = 8192;
 // Prompts of up to this many tokens go token by token where the launch has
 // both kinds.
 constexpr int kShort = 16;
+constexpr int kSplitTiles = 48, kSegTiles = 256, kMinSegShift = 9, kMinSegs = 4;
 
 // How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
-// none), all of them or those of more than kShort tokens.
+// none), all of them or those of more than kShort tokens; in segments of
+// 2^seg_shift tokens (0: whole), with the bytes of their states at seg_at.
 struct Plan {
-  int64_t chunked;
+  int64_t chunked, slots, nsegs, seg_at, bytes;
   bool all;
+  int seg_shift;
 };
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
-  if (!sk::prompt_chunked(L->dk, L->act_dtype) || tokens <= kShort || nseq == 0) return {0, false};
+  Plan p{};
+  if (!sk::prompt_chunked(L->dk, L->act_dtype) || tokens <= kShort || nseq == 0) return p;
   // mostly long prompts: the chunked form takes the short ones too, and one
   // launch is saved
-  if (tokens > sk::PROMPT_CHUNK * nseq) return {nseq, true};
+  p.all = tokens > sk::PROMPT_CHUNK * nseq;
   const int64_t most = tokens / (kShort + 1);
-  return {most < nseq ? most : nseq, false};
+  p.chunked = p.all || nseq < most ? nseq : most;
+  p.slots = sk::prompt_slots(tokens, p.chunked, 6);
+  p.bytes = p.slots * L->heads * sk::PROMPT_CHUNK_WORK + sk::PROMPT_WORK_OVER;
+  // Few tiles with many tokens: segments, as long as one of each tile fills the
+  // CUs about once
+  if (p.chunked * L->heads <= kSplitTiles) {
+    int shift = kMinSegShift;
+    while ((tokens >> shift) * L->heads > kSegTiles) ++shift;
+    if ((tokens >> shift) >= kMinSegs * p.chunked) {
+      p.seg_shift = shift;
+      p.nsegs = sk::prompt_slots(tokens, p.chunked, shift);
+      p.seg_at = (p.bytes + 255) / 256 * 256;
+      p.bytes = p.seg_at + p.nsegs * L->heads * (int64_t)L->dk * (L->dk + L->dv) * 4;
+    }
+  }
+  return p;
 }
 
 bool aligned(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -112,10 +131,7 @@ int64_t sketchssm_prefill_workspace_bytes(const sketchssm_layer* layer, int32_t 
     if (int rc = check_layer(layer)) return rc;
     if (layer->family != SKSSM_GDN || tokens < 0 || nseq < 0 || nseq > layer->batch) return SKSSM_EDIM;
     const Plan pl = plan(layer, tokens, nseq);
-    if (pl.chunked == 0) return 0;
-    const int64_t tiles = sk::prompt_slots(tokens, pl.chunked) * layer->heads;
-    if (tiles > INT32_MAX / 2) return SKSSM_EDIM;
-    return tiles * sk::PROMPT_CHUNK_WORK + sk::PROMPT_WORK_OVER;
+    return pl.slots * layer->heads > INT32_MAX / 2 ? SKSSM_EDIM : pl.bytes;
   } catch (...) {
     return SKSSM_ELAUNCH;
   }
@@ -178,7 +194,10 @@ int sketchssm_prefill(const sketchssm_layer* layer, const sketchssm_buffers* buf
     const Plan pl = plan(layer, pr->tokens, pr->nseq);
     if (pl.chunked > 0) {
       p.nchunked = (int)pl.chunked;
-      p.nslots = (int)sk::prompt_slots(pr->tokens, pl.chunked);
+      p.nslots = (int)pl.slots;
+      p.seg_shift = pl.seg_shift;
+      p.nsegs = (int)pl.nsegs;
+      p.seg = reinterpret_cast<float*>(static_cast<char*>(pr->work) + pl.seg_at);
       p.len_lo = pl.all ? -1 : kShort;
       if ((rc = sk::launch_prompt_chunks(dk, dv, p, st)) || pl.all) return rc;
       p.len_hi = kShort;

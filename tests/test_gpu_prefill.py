@@ -259,6 +259,51 @@ def test_many_prompts(n, lens):
     check(lay, S0, tok, lens, starts, seqs, has)
 
 
+@pytest.mark.parametrize("dk,dv", SHAPES[1:])
+@pytest.mark.parametrize("lens", [[2048], [2049], [2111, 0, 1700], [3000, 5, 1], [512, 513, 3100], [1, 4097]],
+                         ids=lambda x: "-".join(map(str, x)))
+def test_few_long_prompts(dk, dv, lens):
+    """Few tiles with many tokens: prompts in segments (of 512 tokens here), the
+    first from its state and from zero, prompts of one segment among them."""
+    H, n = 1, len(lens)
+    lay = make_layer(n + 1, H, dk, dv, "bf16", seed=80, ranks=[5])
+    tok = make_tokens(sum(lens), H, dk, dv, "bf16", seed=81, packed=True, pad=2, alpha=None)
+    tok[3][:] = 1 - (1 - tok[3]) * 0.02            # slow decays: a segment's start is felt at its end
+    S0 = lay.S.clone()
+    seqs, has = [n - i for i in range(n)], [(i + 1) % 2 for i in range(n)]
+    for rep in range(2):                           # the same workspace twice, from the same states
+        lay.S.copy_(S0)
+        _, starts = run(lay, tok, lens, seqs=seqs, has=has)
+        assert lay.error_word() == 0
+        check(lay, S0, tok, lens, starts, seqs, has)
+
+
+def test_few_long_prompts_refused_and_replayed():
+    """A refused prompt among segmented ones, and a captured call."""
+    lens = [1500, 1600, 1400]
+    N = sum(lens)
+    lay = make_layer(3, 1, 64, 64, "bf16", seed=82, ranks=[0])
+    tok = make_tokens(N, 1, 64, 64, "bf16", seed=83)
+    S0 = lay.S.clone()
+    lay.count[2] = 2
+    run(lay, tok, lens, seqs=[0, 2, 0])
+    assert lay.error_word() == abi.SKSSM_ERRBIT_SEQ | abi.SKSSM_ERRBIT_COUNT
+    check(lay, S0, tok, lens, [0, 1500, 3100, 4500], [0, 2, 0], [1] * 3, skip=(1, 2))
+    lay.count.zero_()
+    pr = Prompts(lay, *tok, torch.tensor([0, 1500, 3100, 4500], dtype=torch.int32, device="cuda"))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        assert lay.prefill(pr) == 0
+    for rep in range(3):
+        for dst, src in zip(tok, make_tokens(N, 1, 64, 64, "bf16", seed=84 + rep)):
+            dst.copy_(src)
+        lay.S.copy_(S0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        check(lay, S0, tok, lens, [0, 1500, 3100, 4500], [0, 1, 2], [1] * 3)
+
+
 def test_no_prompts_and_empty_prompts():
     lay = make_layer(3, 2, 64, 64, "bf16", seed=17)
     S0 = lay.S.clone()
