@@ -389,9 +389,12 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, hi = lane >> 4;
-  // (the parts of a tile are as many workgroups apart as there are tiles: mostly
-  // on one XCD, whose cache then serves the K, Q, T and P that they share)
-  const int tiles = (p.seg_shift ? p.nsegs : p.nchunked) * p.H, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
+  // The parts of a tile are eight workgroups apart: on one XCD at one time, so
+  // that its cache serves the K, Q, T and P that they share.
+  constexpr int VPARTS = DV / (16 * NW), PARTS = VPARTS + (OUT ? 0 : DK / (16 * NW));
+  const int tiles = (p.seg_shift ? p.nsegs : p.nchunked) * p.H;
+  const int part = blockIdx.x / 8 % PARTS, tile = blockIdx.x / (8 * PARTS) * 8 + blockIdx.x % 8;
+  if (tile >= tiles) return;
   const int h = tile % p.H;
   int rank = 0, seg = 0;
   const int i = p.seg_shift ? slot_prompt(p, tile / p.H, p.seg_shift, &rank) : chunked_prompt(p, tile / p.H, &rank);
@@ -400,7 +403,6 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   const int b = p.seqs ? p.seqs[i] : i;
   bool last = true;                              // the prompt's last segment
   static_assert(DV <= DK, "a state fits the place of a transition");
-  constexpr int VPARTS = DV / (16 * NW);
   const bool unit = !OUT && part >= VPARTS;      // columns of the identity
   const int slot0 = first_slot(s0, rank, 6);
   float* own = nullptr;                          // this segment's B (then the state behind it) and M
@@ -441,7 +443,10 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   constexpr int WRUNS = (CHUNK_WORK_BYTES + PROMPT_WORK_OVER) / 1024, RUNS = (WRUNS + 1) / NW;
   static_assert((CHUNK_WORK_BYTES + PROMPT_WORK_OVER) % 1024 == 0 && (WRUNS + 1) % NW == 0 && RUNS % 4 == 0, "runs");
   constexpr int WU = RUNS / 4, UNITS = 2 * KU + WU + 2;
-  const int run0 = (wv < NW - 1 ? wv * RUNS : WRUNS - RUNS) * 1024;
+  // (without outputs P is not needed: of eight waves two have nothing but P and
+  // take the last's runs once more)
+  const bool tail = wv == NW - 1 || (!OUT && wv * RUNS * 1024 >= T_BYTES);
+  const int run0 = (tail ? WRUNS - RUNS : wv * RUNS) * 1024;
   const int krow = (wv * 64 + lane) / PPR, kpc = lane % PPR, vrow = lane >> 1;
   // Byte offset of a lane's piece from a chunk's first row (unsigned 32 bits: 63
   // rows of at most 2^25 elements fit).  Rows behind the prompt's end repeat its
@@ -831,18 +836,19 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 }
 
 // The states between a prompt's segments: S behind segment g is M_g S + B_g,
-// written over B_g.  One workgroup per (prompt, head), a wave per 16 columns,
-// in fp32 throughout: a tile of S (rows 4 hi + r of column n) is the B operand
+// written over B_g.  One workgroup of four waves per (prompt, head, 64
+// columns), a wave per 16 (a SIMD each: the fp32 products bound a step, 64 x
+// 128 x 128 of them 4 us), in fp32 throughout: a tile of S (rows 4 hi + r of column n) is the B operand
 // of v_mfma_f32_16x16x4_f32 with K-step r over rows {4 k + r}, so M is read as
 // runs of four columns (from LDS, one segment ahead, its pieces swizzled by
 // row) and the state never leaves its registers.
 template <int DK, int DV>
-__global__ void __launch_bounds__(4 * DV) prompt_join_kernel(PromptParams p) {
-  constexpr int TB = DK / 16, SEG_FLOATS = DK * (DV + DK), PPR = DK / 4, NW = DV / 16, RUNS = DK * DK * 4 / 1024 / NW;
+__global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams p) {
+  constexpr int TB = DK / 16, SEG_FLOATS = DK * (DV + DK), PPR = DK / 4, NW = 4, RUNS = DK * DK * 4 / 1024 / NW;
   extern __shared__ __align__(1024) unsigned char smem[];
-  const int x = blockIdx.x / p.H, h = blockIdx.x - x * p.H;
+  const int tile = blockIdx.x % (p.nchunked * p.H), x = tile / p.H, h = tile - x * p.H;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hi = lane >> 4;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = wv * 16;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = blockIdx.x / (p.nchunked * p.H) * 64 + wv * 16;
   int rank = 0;
   const int i = chunked_prompt(p, x, &rank);
   if (i < 0) return;
@@ -898,8 +904,8 @@ __global__ void __launch_bounds__(4 * DV) prompt_join_kernel(PromptParams p) {
 template <int DK, int DV, int NW, bool OUT>
 void launch_chunks(const PromptParams& p, hipStream_t st) {
   const unsigned tiles = (unsigned)(p.seg_shift ? p.nsegs : p.nchunked) * p.H;
-  const unsigned parts = OUT ? DV / (16 * NW) : (DV + DK) / (16 * NW);
-  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, NW, OUT>), dim3(tiles * parts), dim3(64 * NW), (ChunkLds<DK, NW>::BYTES),
+  constexpr unsigned PARTS = OUT ? DV / (16 * NW) : (DV + DK) / (16 * NW);
+  hipLaunchKernelGGL((prompt_chunk_kernel<DK, DV, NW, OUT>), dim3((tiles + 7) / 8 * 8 * PARTS), dim3(64 * NW), (ChunkLds<DK, NW>::BYTES),
                      st, p);
 }
 
@@ -909,8 +915,8 @@ int launch(const PromptParams& p, hipStream_t st) {
   hipLaunchKernelGGL((prompt_prep_kernel<DK>), dim3((unsigned)p.nslots * p.H), dim3(256), 0, st, p);
   if (p.seg_shift) {
     launch_chunks<DK, DV, NW, false>(p, st);
-    hipLaunchKernelGGL((prompt_join_kernel<DK, DV>), dim3((unsigned)p.nchunked * p.H), dim3(4 * DV), 2 * DK * DK * 4, st,
-                       p);
+    hipLaunchKernelGGL((prompt_join_kernel<DK, DV>), dim3((unsigned)p.nchunked * p.H * (DV / 64)), dim3(256),
+                       2 * DK * DK * 4, st, p);
     launch_chunks<DK, DV, NW, true>(p, st);
   } else if (p.nchunked * p.H <= 128) {          // .. unless that leaves CUs idle
     launch_chunks<DK, DV, 4, true>(p, st);

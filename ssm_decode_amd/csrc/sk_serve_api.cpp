@@ -16,7 +16,13 @@ constexpr int kMaxWidth = 8192;
 // Prompts of up to this many tokens go token by token where the launch has
 // both kinds.
 constexpr int kShort = 16;
-constexpr int kSplitTiles = 48, kSegTiles = 256, kMinSegShift = 9, kMinSegs = 4;
+// Prompts in segments: up to kSplitTiles (prompt, head) tiles, at least kMinSegs
+// segments of 2^kMinSegShift tokens or more to a prompt on average, at most
+// kMaxSegs (the states between them are joined in order, about 6 us each) and
+// kSegTiles of all tiles (the CUs).  Measured on 128 x 128 tiles, whole and in
+// segments: 32 tiles of 16384 tokens 841 and 686 us, 8 of 12000 512 and 214;
+// what stays whole: 32 of 2048 tokens 112 and 156, 64 of 8192 530 and 606.
+constexpr int kSplitTiles = 48, kSegTiles = 256, kMinSegShift = 10, kMinSegs = 4, kMaxSegs = 12;
 
 // How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
 // none), all of them or those of more than kShort tokens; in segments of
@@ -40,7 +46,7 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   // CUs about once
   if (p.chunked * L->heads <= kSplitTiles) {
     int shift = kMinSegShift;
-    while ((tokens >> shift) * L->heads > kSegTiles) ++shift;
+    while ((tokens >> shift) * L->heads > kSegTiles || (tokens >> shift) > kMaxSegs * p.chunked) ++shift;
     if ((tokens >> shift) >= kMinSegs * p.chunked) {
       p.seg_shift = shift;
       p.nsegs = sk::prompt_slots(tokens, p.chunked, shift);

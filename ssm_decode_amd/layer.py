@@ -29,6 +29,15 @@ def _stream_of(stream):
     return C.c_void_p(current_stream_handle() if stream is None else stream)
 
 
+def _on_device(index: int, call, stream):
+    """call(stream handle) with the device current that the tensors are on, on
+    its current stream where none is given."""
+    if torch.cuda.current_device() == index:
+        return call(_stream_of(stream))
+    with torch.cuda.device(index):
+        return call(_stream_of(stream))
+
+
 @dataclass
 class DeviceStep:
     """One decode step's device tensors (layouts as in include/sketchssm.h)."""
@@ -175,25 +184,23 @@ class DecodeLayer:
     def prefill(self, prompts, stream=None) -> int:
         """Prompts (serving.Prompts) through the gated delta rule: their outputs,
         the sequences' new states and, with prompts.prime, their sketches."""
-        with torch.cuda.device(self.S.device):
-            return abi.sketchssm_prefill(self._layer, self._bufs, prompts.struct, self._stream(stream))
+        return _on_device(self.S.device.index, lambda st: abi.sketchssm_prefill(
+            self._layer, self._bufs, prompts.struct, st), stream)
 
     def save_state(self, cache, seqs, slots, stream=None) -> int:
         """Quantise the states of sequences seqs into the slots of a
         serving.StateCache (int32 device tensors)."""
         cache.check(self, seqs, slots)
-        with torch.cuda.device(self.S.device):
-            return abi.sketchssm_state_save(self._layer, self._bufs, cache.struct, _ptr(seqs), _ptr(slots),
-                                            seqs.numel(), self._stream(stream))
+        return _on_device(self.S.device.index, lambda st: abi.sketchssm_state_save(
+            self._layer, self._bufs, cache.struct, _ptr(seqs), _ptr(slots), seqs.numel(), st), stream)
 
     def load_state(self, cache, seqs, slots, prime: bool = True, stream=None) -> int:
         """Read slots of a serving.StateCache back into the states of sequences
         seqs (distinct), empty their rings and, with prime, write their
         sketches."""
         cache.check(self, seqs, slots)
-        with torch.cuda.device(self.S.device):
-            return abi.sketchssm_state_load(self._layer, self._bufs, cache.struct, _ptr(seqs), _ptr(slots),
-                                            seqs.numel(), int(prime), self._stream(stream))
+        return _on_device(self.S.device.index, lambda st: abi.sketchssm_state_load(
+            self._layer, self._bufs, cache.struct, _ptr(seqs), _ptr(slots), seqs.numel(), int(prime), st), stream)
 
     def error_word(self) -> int:
         return int(self.err[0].item())

@@ -12,22 +12,25 @@ from typing import Optional
 import torch
 
 from . import abi
-from .layer import DTYPE, TORCH_DTYPE, DecodeLayer, _ptr, _stream_of
+from .layer import DTYPE, TORCH_DTYPE, DecodeLayer, _on_device, _ptr
 
+_DTYPES = {TORCH_DTYPE[k]: v for k, v in DTYPE.items()}
 ACT = {"none": abi.SKSSM_ACT_NONE, "silu": abi.SKSSM_ACT_SILU, "sigmoid": abi.SKSSM_ACT_SIGMOID}
 
 
 def _rows(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device) -> int:
     """Checks a tensor of token rows (each row contiguous, the rows at any
     stride) and gives the elements from one row to the next."""
-    if tuple(x.shape) != shape or x.dtype != dtype or x.device != device:
-        raise ValueError(f"{name}: a {dtype} tensor of shape {shape} on {device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
-    row = 1
-    for n, s in zip(reversed(shape[1:]), reversed(x.stride()[1:])):
-        if n != 1 and s != row:
-            raise ValueError(f"{name}: every row has to be contiguous, got strides {x.stride()}")
-        row *= n
-    return x.stride(0) if shape[0] > 1 else row
+    if x.shape != shape or x.dtype != dtype or x.device != device:
+        raise ValueError(f"{name}: a {dtype} tensor of shape {tuple(shape)} on {device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
+    if x.is_contiguous() and shape[0] > 1:
+        return x.stride(0)
+    strides, row = x.stride(), 1
+    for d in range(len(shape) - 1, 0, -1):
+        if strides[d] != row and shape[d] != 1:
+            raise ValueError(f"{name}: every row has to be contiguous, got strides {strides}")
+        row *= shape[d]
+    return strides[0] if shape[0] > 1 else row
 
 
 def _indices(name: str, x: torch.Tensor, n: Optional[int], device: torch.device) -> None:
@@ -136,18 +139,17 @@ def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optiona
     """y = the group norm of x [rows, groups, width] (bf16 or fp32, rows at any
     stride of whole 16 bytes), gated; y may be x.  Returns the library's
     code."""
-    act = next((k for k, v in TORCH_DTYPE.items() if v == x.dtype), None)
-    if x.dim() != 3 or act is None or x.device.type != "cuda":
+    dt, shape, dev = x.dtype, x.shape, x.device
+    if len(shape) != 3 or dt not in _DTYPES or dev.type != "cuda":
         raise ValueError("x: a bf16 or fp32 device tensor [rows, groups, width]")
-    shape, dev = tuple(x.shape), x.device
-    xs, ys = _rows("x", x, shape, x.dtype, dev), _rows("y", y, shape, x.dtype, dev)
-    zs = _rows("gate", gate, shape, x.dtype, dev) if gate is not None else 0
+    xs, ys = _rows("x", x, shape, dt, dev), _rows("y", y, shape, dt, dev)
+    zs = _rows("gate", gate, shape, dt, dev) if gate is not None else 0
     w = norm.weight if norm.weight is not None else norm.bias
-    for name, t in (("weight", norm.weight), ("bias", norm.bias)):
-        if t is not None and (tuple(t.shape) not in (shape[1:], shape[2:]) or t.device != dev):
-            raise ValueError(f"{name}: {shape[1:]} or {shape[2:]} on {dev}, got {tuple(t.shape)} on {t.device}")
+    if w is not None:
+        for name, t in (("weight", norm.weight), ("bias", norm.bias)):
+            if t is not None and ((t.shape != shape[1:] and t.shape != shape[2:]) or t.device != dev):
+                raise ValueError(f"{name}: {tuple(shape[1:])} or {tuple(shape[2:])} on {dev}, got {tuple(t.shape)} on {t.device}")
     st = abi.sketchssm_norm(_ptr(x), _ptr(gate), _ptr(y), _ptr(norm.weight), _ptr(norm.bias), xs, zs, ys,
-                            shape[0], shape[1], shape[2], DTYPE[act], int(w is not None and w.dim() == 2),
+                            shape[0], shape[1], shape[2], _DTYPES[dt], int(w is not None and w.dim() == 2),
                             int(norm.centred), ACT[norm.act], int(norm.gate_first), norm.eps)
-    with torch.cuda.device(dev):
-        return abi.sketchssm_group_norm(st, _stream_of(stream))
+    return _on_device(dev.index, lambda s: abi.sketchssm_group_norm(st, s), stream)

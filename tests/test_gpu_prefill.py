@@ -260,15 +260,15 @@ def test_many_prompts(n, lens):
 
 
 @pytest.mark.parametrize("dk,dv", SHAPES[1:])
-@pytest.mark.parametrize("lens", [[2048], [2049], [2111, 0, 1700], [3000, 5, 1], [512, 513, 3100], [1, 4097]],
+@pytest.mark.parametrize("lens", [[4096], [4097], [5000, 0, 7300], [12300, 5, 1], [1024, 1025, 10300], [1, 8200], [2048] * 4 + [12300]],
                          ids=lambda x: "-".join(map(str, x)))
 def test_few_long_prompts(dk, dv, lens):
-    """Few tiles with many tokens: prompts in segments (of 512 tokens here), the
+    """Few tiles with many tokens: prompts in segments (of 1024 tokens here), the
     first from its state and from zero, prompts of one segment among them."""
     H, n = 1, len(lens)
     lay = make_layer(n + 1, H, dk, dv, "bf16", seed=80, ranks=[5])
     tok = make_tokens(sum(lens), H, dk, dv, "bf16", seed=81, packed=True, pad=2, alpha=None)
-    tok[3][:] = 1 - (1 - tok[3]) * 0.02            # slow decays: a segment's start is felt at its end
+    tok[3][:] = 1 - (1 - tok[3]) * 0.01            # slow decays: a segment's start is felt at its end
     S0 = lay.S.clone()
     seqs, has = [n - i for i in range(n)], [(i + 1) % 2 for i in range(n)]
     for rep in range(2):                           # the same workspace twice, from the same states
@@ -280,7 +280,7 @@ def test_few_long_prompts(dk, dv, lens):
 
 def test_few_long_prompts_refused_and_replayed():
     """A refused prompt among segmented ones, and a captured call."""
-    lens = [1500, 1600, 1400]
+    lens = [4500, 4600, 4400]
     N = sum(lens)
     lay = make_layer(3, 1, 64, 64, "bf16", seed=82, ranks=[0])
     tok = make_tokens(N, 1, 64, 64, "bf16", seed=83)
@@ -288,9 +288,9 @@ def test_few_long_prompts_refused_and_replayed():
     lay.count[2] = 2
     run(lay, tok, lens, seqs=[0, 2, 0])
     assert lay.error_word() == abi.SKSSM_ERRBIT_SEQ | abi.SKSSM_ERRBIT_COUNT
-    check(lay, S0, tok, lens, [0, 1500, 3100, 4500], [0, 2, 0], [1] * 3, skip=(1, 2))
+    check(lay, S0, tok, lens, [0, 4500, 9100, 13500], [0, 2, 0], [1] * 3, skip=(1, 2))
     lay.count.zero_()
-    pr = Prompts(lay, *tok, torch.tensor([0, 1500, 3100, 4500], dtype=torch.int32, device="cuda"))
+    pr = Prompts(lay, *tok, torch.tensor([0, 4500, 9100, 13500], dtype=torch.int32, device="cuda"))
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         assert lay.prefill(pr) == 0
@@ -301,7 +301,7 @@ def test_few_long_prompts_refused_and_replayed():
         torch.cuda.synchronize()
         g.replay()
         torch.cuda.synchronize()
-        check(lay, S0, tok, lens, [0, 1500, 3100, 4500], [0, 1, 2], [1] * 3)
+        check(lay, S0, tok, lens, [0, 4500, 9100, 13500], [0, 1, 2], [1] * 3)
 
 
 def test_no_prompts_and_empty_prompts():

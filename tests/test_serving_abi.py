@@ -141,12 +141,12 @@ def test_prefill_workspace():
     assert abi.sketchssm_prefill_workspace_bytes(L, 128, 2) == 4 * 4 * 31232 + 512
     assert abi.sketchssm_prefill_workspace_bytes(L, 640, 2) == 12 * 4 * 31232 + 512
     # few tiles with many tokens: also a state and a transition (fp32) for each
-    # slot of 512 tokens or more and head
+    # slot of 1024 tokens or more and head, at most 12 to a prompt on average
     need = lambda t, n, shift: -(-((t // 64 + n) * 4 * 31232 + 512) // 256) * 256 + ((t >> shift) + n) * 4 * 64 * 128 * 4  # noqa: E731
-    assert abi.sketchssm_prefill_workspace_bytes(L, 4095, 2) == (63 + 2) * 4 * 31232 + 512
-    assert abi.sketchssm_prefill_workspace_bytes(L, 4096, 2) == need(4096, 2, 9)
-    assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 17, 2) == need(1 << 17, 2, 11)
-    assert abi.sketchssm_prefill_workspace_bytes(L, (1 << 31) - 1, 2) == need((1 << 31) - 1, 2, 25)
+    assert abi.sketchssm_prefill_workspace_bytes(L, 8191, 2) == (127 + 2) * 4 * 31232 + 512
+    assert abi.sketchssm_prefill_workspace_bytes(L, 8192, 2) == need(8192, 2, 10)
+    assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 17, 2) == need(1 << 17, 2, 13)
+    assert abi.sketchssm_prefill_workspace_bytes(L, (1 << 31) - 1, 2) == need((1 << 31) - 1, 2, 27)
     assert abi.sketchssm_prefill_workspace_bytes(gdn(), 640, 2) == 0
     big = _layer(np.arange(129) * 4, family=abi.SKSSM_GDN, heads=128, groups=128, dk=64, dv=64, act=abi.SKSSM_BF16,
                  sk=abi.SKSSM_BF16)
