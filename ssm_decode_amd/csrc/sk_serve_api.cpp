@@ -12,6 +12,8 @@
 namespace {
 
 constexpr int kMaxWidth = 8192;
+// (tiles of a launch: its threads, 256 or 512 to a tile, are counted in 32 bits)
+constexpr int64_t kMaxTiles = (1 << 22) - 1;
 
 // Prompts of up to this many tokens go token by token where the launch has
 // both kinds.
@@ -102,7 +104,7 @@ int check_cache(const sketchssm_layer* L, const sketchssm_buffers* B, const sket
   if (!B || !C) return SKSSM_EINVAL;
   if (C->bits != 8 && C->bits != 4) return SKSSM_EDTYPE;
   if (C->slots < 0 || n < 0) return SKSSM_EDIM;
-  if ((int64_t)n * L->heads > INT32_MAX / 2) return SKSSM_EDIM;
+  if ((int64_t)n * L->heads > kMaxTiles) return SKSSM_EDIM;
   if (n == 0) return SKSSM_OK;
   if (!aligned(seqs, 4) || !aligned(slots, 4)) return SKSSM_EINVAL;
   if (!aligned(B->S, 16) || !aligned(B->count, 16) || !aligned(B->err, 16)) return SKSSM_EINVAL;
@@ -136,8 +138,9 @@ int64_t sketchssm_prefill_workspace_bytes(const sketchssm_layer* layer, int32_t 
   try {
     if (int rc = check_layer(layer)) return rc;
     if (layer->family != SKSSM_GDN || tokens < 0 || nseq < 0 || nseq > layer->batch) return SKSSM_EDIM;
+    if ((int64_t)nseq * layer->heads > kMaxTiles) return SKSSM_EDIM;
     const Plan pl = plan(layer, tokens, nseq);
-    return pl.slots * layer->heads > INT32_MAX / 2 ? SKSSM_EDIM : pl.bytes;
+    return pl.slots * layer->heads > kMaxTiles ? SKSSM_EDIM : pl.bytes;
   } catch (...) {
     return SKSSM_ELAUNCH;
   }

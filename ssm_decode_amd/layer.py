@@ -182,10 +182,20 @@ class DecodeLayer:
         return abi.sketchssm_replay_step(self._layer, self._bufs, step.struct(), self._stream(stream))
 
     def prefill(self, prompts, stream=None) -> int:
-        """Prompts (serving.Prompts) through the gated delta rule: their outputs,
-        the sequences' new states and, with prompts.prime, their sketches."""
-        return _on_device(self.S.device.index, lambda st: abi.sketchssm_prefill(
+        """Prompts (serving.Prompts) through the gated delta rule: their outputs
+        (normalised, where the prompts have a norm), the sequences' new states
+        and, with prompts.prime, their sketches."""
+        rc = _on_device(self.S.device.index, lambda st: abi.sketchssm_prefill(
             self._layer, self._bufs, prompts.struct, st), stream)
+        if rc == 0 and prompts.norm is not None:
+            rc = self.normalise(prompts.o, prompts.norm, prompts.norm_gate, stream)
+        return rc
+
+    def normalise(self, o, norm, gate=None, stream=None) -> int:
+        """The norm (serving.OutputNorm) of outputs o [rows, H, dv] (a step's or
+        prompts'), in place; gate: a tensor like o."""
+        from .serving import group_norm
+        return group_norm(o, norm, o, gate, stream)
 
     def save_state(self, cache, seqs, slots, stream=None) -> int:
         """Quantise the states of sequences seqs into the slots of a

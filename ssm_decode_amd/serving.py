@@ -48,15 +48,17 @@ class Prompts:
     seq_start [n + 1] int32: prompt i holds tokens seq_start[i] up to
     seq_start[i + 1]; seqs [n]: its sequence (None: sequence i); has_state
     [n]: 0 starts it from a zero state (None: every prompt goes on from its
-    sequence's state); prime: also write the sketches of the new states.  The
-    index tensors are read on the device at the call, the tensors are held,
-    and the workspace is allocated once: calls that may overlap take a
-    ``Prompts`` each."""
+    sequence's state); prime: also write the sketches of the new states; norm
+    (with norm_gate, like o): an ``OutputNorm`` of o, applied in place behind
+    the prompts (to all token rows).  The index tensors are read on the device
+    at the call, the tensors are held, and the workspace is allocated once:
+    calls that may overlap take a ``Prompts`` each."""
 
     def __init__(self, layer: DecodeLayer, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: torch.Tensor,
                  beta: torch.Tensor, o: torch.Tensor, seq_start: torch.Tensor,
                  seqs: Optional[torch.Tensor] = None, has_state: Optional[torch.Tensor] = None,
-                 prime: bool = True):
+                 prime: bool = True, norm: Optional["OutputNorm"] = None,
+                 norm_gate: Optional[torch.Tensor] = None):
         dev, at = layer.S.device, TORCH_DTYPE[layer.act]
         N, H = q.shape[0], layer.H
         strides = [_rows("q", q, (N, H, layer.dk), at, dev), _rows("k", k, (N, H, layer.dk), at, dev),
@@ -69,6 +71,9 @@ class Prompts:
         for name, x in (("seqs", seqs), ("has_state", has_state)):
             if x is not None:
                 _indices(name, x, n, dev)
+        if norm_gate is not None:
+            _rows("norm_gate", norm_gate, (N, H, layer.dv), at, dev)
+        self.norm, self.norm_gate = norm, norm_gate
         need = abi.sketchssm_prefill_workspace_bytes(layer.layer_struct, N, n)
         if need < 0:
             raise ValueError(f"prompts that this layer does not take (code {need})")

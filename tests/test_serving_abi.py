@@ -146,7 +146,10 @@ def test_prefill_workspace():
     assert abi.sketchssm_prefill_workspace_bytes(L, 8191, 2) == (127 + 2) * 4 * 31232 + 512
     assert abi.sketchssm_prefill_workspace_bytes(L, 8192, 2) == need(8192, 2, 10)
     assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 17, 2) == need(1 << 17, 2, 13)
-    assert abi.sketchssm_prefill_workspace_bytes(L, (1 << 31) - 1, 2) == need((1 << 31) - 1, 2, 27)
+    assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 25, 2) == need(1 << 25, 2, 21)
+    # at most 2^22 - 1 chunks of heads, prompts of heads, or entries of heads
+    assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 26, 2) == abi.SKSSM_EDIM
+    assert abi.sketchssm_prefill_workspace_bytes(gdn(batch=1 << 20), 1 << 20, 1 << 20) == abi.SKSSM_EDIM
     assert abi.sketchssm_prefill_workspace_bytes(gdn(), 640, 2) == 0
     big = _layer(np.arange(129) * 4, family=abi.SKSSM_GDN, heads=128, groups=128, dk=64, dv=64, act=abi.SKSSM_BF16,
                  sk=abi.SKSSM_BF16)
