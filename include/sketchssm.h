@@ -122,9 +122,8 @@ extern "C" {
 #define SKSSM_ERRBIT_GROUP 2  /* Mamba-2 heads of one B/C group disagree on count */
 #define SKSSM_ERRBIT_SEQ 4    /* sketchssm_flush_seqs, _prefill, _state_save, _state_load: a
                                  listed index outside [0, batch), or a sequence listed twice
-                                 (flush_seqs: a tile claimed twice); _prefill: a prompt
-                                 whose token range is not valid */
-
+                                 (flush_seqs: a tile claimed twice); _prefill: a list of
+                                 first tokens that falls, or leaves [0, tokens] */
 #define SKSSM_ERRBIT_SLOT 8   /* sketchssm_state_save/_load: a cache slot outside [0, slots), or
                                  a slot that an earlier entry of a save's list has */
 
@@ -352,11 +351,17 @@ typedef struct {
  *   S <- alpha (I - beta k k^T) S + beta k v^T,  o = S^T q,
  * and, with prime, the sketch that sketchssm_read starts from.  A sequence's
  * ring must be empty (count 0): a tile with buffered entries sets
- * SKSSM_ERRBIT_COUNT and is left untouched (flush it first).  A prompt with
- * a bad range or sequence sets SKSSM_ERRBIT_SEQ and is skipped; where a
- * sequence is listed twice, the first prompt has it.  A prompt of no tokens
- * leaves its state (or writes the zero state), with prime its sketch too.
- * Token rows that no prompt holds are neither read nor written.  Other
+ * SKSSM_ERRBIT_COUNT and is left untouched (flush it first).  A sequence
+ * outside the batch sets SKSSM_ERRBIT_SEQ and its prompt is skipped; where one
+ * is listed twice, the first prompt has it.  A seq_start that falls anywhere or
+ * leaves [0, tokens] sets SKSSM_ERRBIT_SEQ and nothing is written.  A prompt of
+ * no tokens leaves its state (or writes the zero state), with prime its sketch
+ * too.  Token rows that no prompt holds are neither read nor written.
+ * Sums run in fp32; prompts of more than 16 tokens (dk >= 64) go in chunks of 64
+ * tokens, whose products are those of fp32 operands.  An infinity or a NaN
+ * in a token's row or in the state reaches, besides what the recurrence brings
+ * it to, the outputs of its head and prompt from the start of its chunk (of
+ * sketchssm_prefill's own choice, at most 64 tokens back) on.  Other
  * families return SKSSM_EDIM; prime with SKSSM_COEF_STATE is SKSSM_EFLAG (a
  * state-dependent map is formed by sketchssm_flush with SKSSM_FLUSH_ALL).
  * nseq = 0 launches nothing. */
@@ -364,8 +369,10 @@ int sketchssm_prefill(const sketchssm_layer* layer, const sketchssm_buffers* buf
                       const sketchssm_prompts* prompts, void* hip_stream);
 
 /* Bytes of prompts->work that sketchssm_prefill needs for up to this many
- * tokens and prompts, or a negative SKSSM_E* code.  Calls that may overlap
- * need a workspace each. */
+ * tokens and prompts, or a negative SKSSM_E* code (the same that the call would
+ * return: at most 2^22 - 1 chunks of 64 tokens, or prompts, times heads).  A
+ * workspace for more tokens or prompts need not do for fewer: ask for the sizes
+ * of the call.  Calls that may overlap need a workspace each. */
 int64_t sketchssm_prefill_workspace_bytes(const sketchssm_layer* layer, int32_t tokens, int32_t nseq);
 
 /* A pool of slots that each hold the states of one sequence's heads in 8 or
@@ -419,6 +426,9 @@ typedef struct {
   int64_t x_stride, gate_stride, y_stride; /* elements from a row to the next: at least a row, at most
                                 2^25, a multiple of 16 bytes */
   int64_t rows;
+  const int32_t* first;      /* DEVICE, or NULL (0): only the rows from *first ..            */
+  const int32_t* end;        /* DEVICE, or NULL (rows): .. up to *end, within [0, rows), are read
+                                and written (prompts' seq_start and its last entry) */
   int32_t groups;            /* 1 to 65535 */
   int32_t width;             /* 8 to 8192, a multiple of 8 */
   int32_t dtype;             /* of x, gate and y: SKSSM_F32 or SKSSM_BF16 */

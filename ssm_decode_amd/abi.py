@@ -70,7 +70,8 @@ class sketchssm_state_cache(C.Structure):
 class sketchssm_norm(C.Structure):
     _fields_ = [("x", C.c_void_p), ("gate", C.c_void_p), ("y", C.c_void_p), ("weight", C.c_void_p),
                 ("bias", C.c_void_p), ("x_stride", C.c_int64), ("gate_stride", C.c_int64),
-                ("y_stride", C.c_int64), ("rows", C.c_int64), ("groups", C.c_int32), ("width", C.c_int32),
+                ("y_stride", C.c_int64), ("rows", C.c_int64), ("first", C.c_void_p), ("end", C.c_void_p),
+                ("groups", C.c_int32), ("width", C.c_int32),
                 ("dtype", C.c_int32), ("group_weights", C.c_int32), ("centred", C.c_int32),
                 ("activation", C.c_int32), ("gate_first", C.c_int32), ("eps", C.c_float)]
 

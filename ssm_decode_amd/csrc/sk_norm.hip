@@ -80,7 +80,10 @@ __global__ void __launch_bounds__(NORM_THREADS) group_norm_kernel(NormParams p) 
       return s_part[0] + s_part[1] + s_part[2] + s_part[3];
     }
   };
-  for (int64_t row = (int64_t)blockIdx.x * rpw + rl; row < p.rows; row += (int64_t)gridDim.x * rpw) {
+  int64_t lo = p.first ? *p.first : 0, end = p.end ? *p.end : p.rows;
+  lo = lo > 0 ? lo : 0;
+  end = end < p.rows ? end : p.rows;
+  for (int64_t row = lo + (int64_t)blockIdx.x * rpw + rl; row < end; row += (int64_t)gridDim.x * rpw) {
     float x[VPL][N], z[VPL][N];
 #pragma unroll
     for (int u = 0; u < VPL; ++u) {

@@ -49,11 +49,14 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   // recent in the memory-side cache)
   const int rslot = blockIdx.x / p.H, h = blockIdx.x - rslot * p.H, slot = p.nslots - 1 - rslot;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  // (a refused list may have no prompt that any other launch comes to: it is
+  // reported here)
+  if (rslot == 0) prompt_ok(p, 0, h, p.seqs ? p.seqs[0] : 0);
   int rank;
   const int i = slot_prompt(p, slot, 6, &rank);
   if (i < 0) return;
   const int s0 = p.start[i], s1 = p.start[i + 1];
-  if (s0 < 0 || s1 < s0 || s1 > p.tokens) return;      // (the other launches report it)
+  if (s0 < 0 || s1 < s0 || s1 > p.tokens) return;
   const int c0 = (slot - first_slot(s0, rank, 6)) * PC, len = s1 - s0;
   if (c0 >= len) return;
   const int nt = len - c0 < PC ? len - c0 : PC;
@@ -296,9 +299,9 @@ __device__ __forceinline__ void copy16x4(const void* base, uint32_t offset, uint
   asm volatile(
       "s_mov_b32 m0, %2\n\ts_nop 0\n\t"
       "global_load_lds_dwordx4 %0, %1\n\t"
-      "global_load_lds_dwordx4 %0, %1 offset:1024\n\t"
-      "global_load_lds_dwordx4 %0, %1 offset:2048\n\t"
-      "global_load_lds_dwordx4 %0, %1 offset:3072" ::"v"(offset),
+      "global_load_lds_dwordx4 %0, %1 offset:0x400\n\t"
+      "global_load_lds_dwordx4 %0, %1 offset:0x800\n\t"
+      "global_load_lds_dwordx4 %0, %1 offset:0xc00" ::"v"(offset),
       "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
       : "memory");
 }

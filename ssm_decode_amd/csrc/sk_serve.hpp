@@ -69,6 +69,8 @@ struct NormParams {
   const float* bias;
   int64_t xs, zs, ys;       // elements from a row to the next
   int64_t rows;
+  const int32_t* first;     // rows *first up to *end (null: 0, rows)
+  const int32_t* end;
   int groups, width;
   int wgs;                  // elements from a group's weight to the next (0: shared)
   int centred, act, gate_first;

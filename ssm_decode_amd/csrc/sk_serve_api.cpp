@@ -259,6 +259,7 @@ int sketchssm_group_norm(const sketchssm_norm* nm, void* hip_stream) {
     if ((nm->centred != 0 && nm->centred != 1) || (nm->gate_first != 0 && nm->gate_first != 1)) return SKSSM_EFLAG;
     if (!(isfinite(nm->eps) && nm->eps >= 0.f)) return SKSSM_EINVAL;
     if (nm->rows == 0) return SKSSM_OK;
+    if ((nm->first && !aligned(nm->first, 4)) || (nm->end && !aligned(nm->end, 4))) return SKSSM_EINVAL;
     const int64_t row = (int64_t)nm->groups * nm->width;
     if (!aligned(nm->x, 16) || !aligned(nm->y, 16) || (nm->gate && !aligned(nm->gate, 16))) return SKSSM_EINVAL;
     if ((nm->weight && !aligned(nm->weight, 16)) || (nm->bias && !aligned(nm->bias, 16))) return SKSSM_EINVAL;
@@ -276,6 +277,8 @@ int sketchssm_group_norm(const sketchssm_norm* nm, void* hip_stream) {
     p.zs = nm->gate_stride;
     p.ys = nm->y_stride;
     p.rows = nm->rows;
+    p.first = nm->first;
+    p.end = nm->end;
     p.groups = nm->groups;
     p.width = nm->width;
     p.wgs = nm->group_weights ? nm->width : 0;

@@ -188,14 +188,14 @@ class DecodeLayer:
         rc = _on_device(self.S.device.index, lambda st: abi.sketchssm_prefill(
             self._layer, self._bufs, prompts.struct, st), stream)
         if rc == 0 and prompts.norm is not None:
-            rc = self.normalise(prompts.o, prompts.norm, prompts.norm_gate, stream)
+            rc = self.normalise(prompts.o, prompts.norm, prompts.norm_gate, stream, prompts.seq_start)
         return rc
 
-    def normalise(self, o, norm, gate=None, stream=None) -> int:
+    def normalise(self, o, norm, gate=None, stream=None, rows=None) -> int:
         """The norm (serving.OutputNorm) of outputs o [rows, H, dv] (a step's or
-        prompts'), in place; gate: a tensor like o."""
+        prompts'), in place; gate: a tensor like o; rows as serving.group_norm's."""
         from .serving import group_norm
-        return group_norm(o, norm, o, gate, stream)
+        return group_norm(o, norm, o, gate, stream, rows)
 
     def save_state(self, cache, seqs, slots, stream=None) -> int:
         """Quantise the states of sequences seqs into the slots of a

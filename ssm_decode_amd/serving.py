@@ -50,7 +50,7 @@ class Prompts:
     [n]: 0 starts it from a zero state (None: every prompt goes on from its
     sequence's state); prime: also write the sketches of the new states; norm
     (with norm_gate, like o): an ``OutputNorm`` of o, applied in place behind
-    the prompts (to all token rows).  The index tensors are read on the device
+    the prompts (to the rows from seq_start[0] up to seq_start[n]).  The index tensors are read on the device
     at the call, the tensors are held, and the workspace is allocated once:
     calls that may overlap take a ``Prompts`` each."""
 
@@ -140,10 +140,11 @@ class OutputNorm:
 
 
 def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optional[torch.Tensor] = None,
-               stream=None) -> int:
+               stream=None, rows: Optional[torch.Tensor] = None) -> int:
     """y = the group norm of x [rows, groups, width] (bf16 or fp32, rows at any
-    stride of whole 16 bytes), gated; y may be x.  Returns the library's
-    code."""
+    stride of whole 16 bytes), gated; y may be x.  rows: an int32 device
+    tensor, say prompts' seq_start: only the rows from its first up to its last
+    entry, which are read on the device.  Returns the library's code."""
     dt, shape, dev = x.dtype, x.shape, x.device
     if len(shape) != 3 or dt not in _DTYPES or dev.type != "cuda":
         raise ValueError("x: a bf16 or fp32 device tensor [rows, groups, width]")
@@ -154,7 +155,14 @@ def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optiona
         for name, t in (("weight", norm.weight), ("bias", norm.bias)):
             if t is not None and ((t.shape != shape[1:] and t.shape != shape[2:]) or t.device != dev):
                 raise ValueError(f"{name}: {tuple(shape[1:])} or {tuple(shape[2:])} on {dev}, got {tuple(t.shape)} on {t.device}")
+    first = end = None
+    if rows is not None:
+        _indices("rows", rows, None, dev)
+        if rows.numel() == 0:
+            raise ValueError("rows: the first row and the end")
+        first = rows.data_ptr()
+        end = first + 4 * (rows.numel() - 1)
     st = abi.sketchssm_norm(_ptr(x), _ptr(gate), _ptr(y), _ptr(norm.weight), _ptr(norm.bias), xs, zs, ys,
-                            shape[0], shape[1], shape[2], _DTYPES[dt], int(w is not None and w.dim() == 2),
+                            shape[0], first, end, shape[1], shape[2], _DTYPES[dt], int(w is not None and w.dim() == 2),
                             int(norm.centred), ACT[norm.act], int(norm.gate_first), norm.eps)
     return _on_device(dev.index, lambda s: abi.sketchssm_group_norm(st, s), stream)

@@ -123,3 +123,20 @@ def test_graph_replays():
         g.replay()
         torch.cuda.synchronize()
         check(x, y, norm, z)
+
+
+@pytest.mark.parametrize("lo,hi", [(0, 40), (3, 37), (7, 8), (5, 5), (20, 10), (-4, 12), (30, 900), (-9, -2), (41, 50)])
+def test_part_of_the_rows(lo, hi):
+    """Rows from the first up to the last entry of a device list, within [0, rows);
+    the others are left as they were, in place too."""
+    for width in (64, 2056):
+        x = data(40, 3, width, torch.bfloat16, 4)
+        rows = torch.tensor([lo, 17, hi], dtype=torch.int32, device="cuda")
+        norm, y = OutputNorm(None, act="none"), x.clone()
+        assert group_norm(y, norm, y, rows=rows) == 0
+        a, b = max(lo, 0), min(hi, 40)
+        inside = slice(a, max(a, b))
+        check(x[inside], y[inside], norm, None)
+        out = torch.ones(40, dtype=torch.bool)
+        out[inside] = False
+        assert torch.equal(y[out], x[out])

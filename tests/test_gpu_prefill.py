@@ -452,3 +452,16 @@ def test_prompt_then_decode_window():
     assert np.linalg.norm(got - o) <= 1e-5 * np.linalg.norm(o)
     assert np.linalg.norm(f64(lay.S) - S) <= 1e-5 * np.linalg.norm(S)
     assert lay.error_word() == 0
+
+
+@pytest.mark.parametrize("tokens,starts", [(200, [150, 100, 50, 10]), (13000, [13000, 0]), (13000, [14000, 15000]),
+                                           (13000, [-2000, 12000]), (13000, [9000, 8000, 12500])])
+def test_a_list_that_only_falls_is_reported(tokens, starts):
+    """Lists whose prompts no workgroup of the chunks comes to."""
+    n = len(starts) - 1
+    lay = make_layer(n, 1, 64, 64, "bf16", seed=15, ranks=[4])
+    tok = make_tokens(tokens, 1, 64, 64, "bf16", seed=16)
+    S0 = lay.S.clone()
+    run(lay, tok, None, starts=starts)
+    assert lay.error_word() == abi.SKSSM_ERRBIT_SEQ
+    assert torch.equal(lay.S, S0) and (tok[5].float() == torch.tensor(SENTINEL).to(tok[5].dtype).float()).all()

@@ -57,7 +57,8 @@ def test_serving_loop(act, tol):
     def prompts(lens, seqs, has):
         starts = np.concatenate([[0], np.cumsum(lens)])
         tok, N = tokens(int(starts[-1])), int(starts[-1])
-        o, z = torch.empty((N, H, dv), device="cuda", dtype=dt), rand(N, H, dv).to(dt)
+        tok = tuple(torch.cat([x, x[:3]]) for x in tok)          # rows behind the last prompt
+        o, z = torch.full((N + 3, H, dv), 5.0, device="cuda", dtype=dt), rand(N + 3, H, dv).to(dt)
         p = Prompts(lay, *tok, o, ints(*starts.tolist()), ints(*seqs), ints(*has), norm=norm, norm_gate=z)
         assert lay.prefill(p) == 0
         want = np.zeros((N, H, dv))
@@ -67,7 +68,8 @@ def test_serving_loop(act, tol):
                 S[b] = 0
             for t in range(starts[i], starts[i + 1]):
                 want[t] = step(b, t, t64)
-        near(f64(o), ref.group_norm(want, f64(norm.weight), None, f64(z), 1e-5, "silu", False, False))
+        near(f64(o[:N]), ref.group_norm(want, f64(norm.weight), None, f64(z[:N]), 1e-5, "silu", False, False))
+        assert (o[N:] == 5).all()
 
     def window():
         for w in range(W):
