@@ -20,6 +20,7 @@ CFLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-I", os.path.join(ROOT, "include"), "-Wall", "-Wno-unused-function"]
 SOURCES = ["sk_api.cpp", "sk_m2.hip", "sk_gdn.hip", "sk_kda.hip", "sk_m2_f32.hip", "sk_gdn_f32.hip",
            "sk_kda_f32.hip", "sk_noalloc.hip", "sk_serve_api.cpp", "sk_prompt_step.hip", "sk_prompt_chunk.hip",
+           "sk_prompt_chunk_f32.hip",
            "sk_state_cache.hip", "sk_norm.hip"]
 
 

@@ -1,4 +1,5 @@
-// The two launches of the chunked form (see sk_prompt_chunk.hpp).
+// The launches of the chunked form: T and P of every chunk, then, for bf16
+// activations, the chunks in order (sk_prompt_chunk.hpp has the mathematics).
 #include <type_traits>
 
 #include "sk_prompt_chunk.hpp"
@@ -6,38 +7,17 @@
 namespace sk {
 namespace {
 
-// The prompt that has a slot (of 2^shift tokens: chunks, or segments of a
-// prompt), and its rank among those taken in chunks: the last whose first slot
-// is not behind this one (-1: none; its own end is for the caller to check).
-__device__ __forceinline__ int slot_prompt(const PromptParams& p, int slot, int shift, int* rank) {
-  const int lane = threadIdx.x & 63;
-  int i = -1, ranks = 0;
-  for (int j0 = 0; j0 < p.nseq; j0 += 64) {
-    const int j = j0 + lane < p.nseq ? j0 + lane : p.nseq - 1;
-    const int a = p.start[j];
-    const bool mine = j0 + lane < p.nseq && (int64_t)p.start[j + 1] - a > p.len_lo;
-    const unsigned long long all = __ballot(mine);
-    const int r = ranks + __popcll(all & ((1ull << lane) - 1));
-    const unsigned long long m = __ballot(mine && first_slot(a, r, shift) <= slot);
-    if (m) {
-      const int l = 63 - __clzll(m);
-      i = j0 + l;
-      *rank = ranks + __popcll(all & ((1ull << l) - 1));
-    }
-    ranks += __popcll(all);
-  }
-  return i;
-}
-
 // ------------------------------------------------------------ T and P
 // One workgroup of four waves per (chunk slot, head).  K K^T and Q K^T on the
-// bf16 matrix cores (exact products, fp32 sums); the unit triangular inverse
-// by substitution in 16 x 16 blocks, joined to 32 and 64 by fp32 products.
+// matrix cores (bf16: exact products, fp32 sums; fp32: fp32 instructions, 64
+// columns of K and Q at a time); the unit triangular inverse by substitution in
+// 16 x 16 blocks, joined to 32 and 64 by fp32 products.
 constexpr int LS = PC + 4;                       // row stride of the fp32 matrices in LDS
 
-template <int DK>
+template <int DK, typename AT>
 __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
-  constexpr int KB = PC * DK * 2;                // bytes of K or Q in LDS
+  constexpr bool F32 = sizeof(AT) == 4;
+  constexpr int KB = PC * (F32 ? 64 * 4 : DK * 2);     // bytes of K or Q in LDS
   constexpr int MB = PC * LS * 4;                // bytes of A or P in LDS
   constexpr int BIG = 2 * KB > 2 * MB ? 2 * KB : 2 * MB;
   __shared__ __align__(16) unsigned char s_big[BIG];   // K and Q, then A (T in its place) and P
@@ -62,24 +42,27 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   const int nt = len - c0 < PC ? len - c0 : PC;
   const int64_t tok = (int64_t)s0 + c0;
 
-  // K and Q, rows of DK with their 16-byte pieces swizzled, zeros behind nt
-  constexpr int PPR = DK / 8;
+  // K and Q, rows of DK (or 64) with their 16-byte pieces swizzled, zeros behind nt
+  constexpr int PPR = F32 ? 16 : DK / 8, EPP = 16 / (int)sizeof(AT);
   auto piece = [](int row, int pc) { return row * PPR + (pc ^ ((PPR == 16 ? row : row >> 1) & (PPR - 1))); };
   u32x4* s_k = reinterpret_cast<u32x4*>(s_big);
   u32x4* s_q = reinterpret_cast<u32x4*>(s_big + KB);
-  const bf16* kp = reinterpret_cast<const bf16*>(p.k) + tok * p.ks + (int64_t)h * DK;
-  const bf16* qp = reinterpret_cast<const bf16*>(p.q) + tok * p.qs + (int64_t)h * DK;
+  const AT* kp = reinterpret_cast<const AT*>(p.k) + tok * p.ks + (int64_t)h * DK;
+  const AT* qp = reinterpret_cast<const AT*>(p.q) + tok * p.qs + (int64_t)h * DK;
+  auto stage = [&](int col) {
 #pragma unroll
-  for (int u = 0; u < PC * PPR / 256; ++u) {
-    const int c = tid + 256 * u, row = c / PPR, pc = c % PPR;
-    u32x4 a = u32x4{0, 0, 0, 0}, b = a;
-    if (row < nt) {
-      a = *reinterpret_cast<const u32x4*>(kp + row * p.ks + pc * 8);
-      b = *reinterpret_cast<const u32x4*>(qp + row * p.qs + pc * 8);
+    for (int u = 0; u < PC * PPR / 256; ++u) {
+      const int c = tid + 256 * u, row = c / PPR, pc = c % PPR;
+      u32x4 a = u32x4{0, 0, 0, 0}, b = a;
+      if (row < nt) {
+        a = *reinterpret_cast<const u32x4*>(kp + row * p.ks + col + pc * EPP);
+        b = *reinterpret_cast<const u32x4*>(qp + row * p.qs + col + pc * EPP);
+      }
+      s_k[piece(row, pc)] = a;
+      s_q[piece(row, pc)] = b;
     }
-    s_k[piece(row, pc)] = a;
-    s_q[piece(row, pc)] = b;
-  }
+  };
+  stage(0);
   if (tid < PC) {
     s_al[tid] = tid < nt ? p.gate[(tok + tid) * p.gs + h] : 1.f;
     s_be[tid] = tid < nt ? p.beta[(tok + tid) * p.bs + h] : 0.f;
@@ -112,19 +95,36 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
     *tj = t - *ti * (*ti + 1) / 2;
   };
 #pragma unroll
-  for (int n = 0; n < 3; ++n) {
-    const int t = wv + 4 * n;
-    ak[n] = aq[n] = f32x4s{0.f, 0.f, 0.f, 0.f};
-    if (t < 10) {                                       // uniform over the wave
-      int ti, tj;
-      tile_of(t, &ti, &tj);
+  for (int n = 0; n < 3; ++n) ak[n] = aq[n] = f32x4s{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < DK / 32; ++s) {
-        const bf16x8 fk = as_frag(s_k[piece(16 * ti + cg, 4 * s + g)]);
-        const bf16x8 fq = as_frag(s_q[piece(16 * ti + cg, 4 * s + g)]);
-        const bf16x8 fb = as_frag(s_k[piece(16 * tj + cg, 4 * s + g)]);
-        ak[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fk, fb, ak[n], 0, 0, 0);
-        aq[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq, fb, aq[n], 0, 0, 0);
+  for (int col = 0; col < DK; col += F32 ? 64 : DK) {
+    if (col > 0) {
+      __syncthreads();
+      stage(col);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const int t = wv + 4 * n;
+      if (t < 10) {                                     // uniform over the wave
+        int ti, tj;
+        tile_of(t, &ti, &tj);
+#pragma unroll
+        for (int s = 0; s < PPR / 4; ++s) {
+          const u32x4 fk = s_k[piece(16 * ti + cg, 4 * s + g)], fq = s_q[piece(16 * ti + cg, 4 * s + g)];
+          const u32x4 fb = s_k[piece(16 * tj + cg, 4 * s + g)];
+          if constexpr (F32) {                          // K-step e: columns 16 s + 4 k + e
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float b = __uint_as_float(fb[e]);
+              ak[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fk[e]), b, ak[n], 0, 0, 0);
+              aq[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fq[e]), b, aq[n], 0, 0, 0);
+            }
+          } else {
+            ak[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(fk), as_frag(fb), ak[n], 0, 0, 0);
+            aq[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(fq), as_frag(fb), aq[n], 0, 0, 0);
+          }
+        }
       }
     }
   }
@@ -226,8 +226,22 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   __syncthreads();
 
   // fragments of T diag(beta) and P, and the row factors
-  unsigned char* W = reinterpret_cast<unsigned char*>(p.work) + ((size_t)slot * p.H + h) * CHUNK_WORK_BYTES;
-  for (int c = tid; c < FRAGS * 64; c += 256) {
+  constexpr int WORK = F32 ? CHUNK_WORK_F32 : CHUNK_WORK_BYTES;
+  unsigned char* W = reinterpret_cast<unsigned char*>(p.work) + ((size_t)slot * p.H + h) * WORK;
+  for (int c = tid; c < (F32 ? F32_TILES * 64 : 0); c += 256) {
+    const int ln = c & 63;
+    int rb, kb;
+    tile_of(c >> 6, &rb, &kb);
+    const int row = 16 * rb + (ln & 15), k = 16 * kb + 4 * (ln >> 4);
+    float t[4], v[4];
+    ld4(s_A + row * LS + k, t);
+    ld4(s_P + row * LS + k, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] *= s_be[k + e];
+    stn<4>(reinterpret_cast<float*>(W + c * 16), t);
+    stn<4>(reinterpret_cast<float*>(W + F32_TILES * FRAG_BYTES + c * 16), v);
+  }
+  for (int c = tid; c < (F32 ? 0 : FRAGS * 64); c += 256) {
     const int f = c >> 6, ln = c & 63, pair = f >> 1;
     const int rb = pair > 0, kb = pair == 2;
     const int row = 32 * rb + block_row(ln & 15, f & 1), k = 32 * kb + 8 * (ln >> 4);
@@ -256,7 +270,7 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
     float pre = s_pre[tid], suf = s_suf[tid];
     for (int n = 0; n < b; ++n) pre *= s_blk[n];
     for (int n = b + 1; n < 4; ++n) suf *= s_blk[n];
-    float* G = reinterpret_cast<float*>(W + T_BYTES + P_BYTES);
+    float* G = reinterpret_cast<float*>(W + WORK - 2 * PC * 4);
     G[tid] = pre;
     G[PC + tid] = suf;
   }
@@ -284,15 +298,6 @@ struct ChunkLds {
   static_assert(BYTES <= 160 * 1024, "LDS of a CU");
 };
 
-// 16 bytes of each lane, from base + its offset in memory to lds + 16 * lane
-// in LDS (base and lds are uniform), in flight until the wave's next wait for
-// its memory counter.  (The compiler would have every LDS read wait for a copy
-// that it knows of, also where the two are in different buffers.)
-__device__ __forceinline__ void copy16(const void* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset),
-               "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
-               : "memory");
-}
 // Four runs of 1 KiB, one behind the other in memory and in LDS (the
 // instruction's offset counts for both addresses).
 __device__ __forceinline__ void copy16x4(const void* base, uint32_t offset, uint32_t lds) {
@@ -304,9 +309,6 @@ __device__ __forceinline__ void copy16x4(const void* base, uint32_t offset, uint
       "global_load_lds_dwordx4 %0, %1 offset:0xc00" ::"v"(offset),
       "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
       : "memory");
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 // Within each 16 lanes, lane i gives the address of four values: 4 rows (i / 4)
 // of 16 (4 (i % 4) ..); it receives column i of the four rows.
@@ -335,43 +337,6 @@ template <int N, int READS, int VALU>
 __device__ __forceinline__ void region() {
   interleave<N, READS, VALU>();
   __builtin_amdgcn_sched_barrier(0);
-}
-
-// The x-th of the prompts taken in chunks (-1: there are not so many), and its
-// rank among them as listed.  Up to 64 prompts are taken longest first (a lane
-// each), so that the last workgroups to start are the shortest; more are taken
-// as listed.
-__device__ __forceinline__ int chunked_prompt(const PromptParams& p, int x, int* rank) {
-  const int lane = threadIdx.x & 63;
-  if (p.nseq <= 64) {
-    const int j = lane < p.nseq ? lane : 0;
-    const int len = p.start[j + 1] - p.start[j];
-    const bool mine = lane < p.nseq && len > p.len_lo;
-    const unsigned long long all = __ballot(mine);
-    int before = 0;
-    for (int k = 0; k < p.nseq; ++k) {
-      const int other = __builtin_amdgcn_readlane(len, k);
-      before += (all >> k & 1) && (other > len || (other == len && k < lane));
-    }
-    const unsigned long long m = __ballot(mine && before == x);
-    if (!m) return -1;
-    const int i = __builtin_ctzll(m);
-    *rank = __popcll(all & ((1ull << i) - 1));
-    return i;
-  }
-  int ranks = 0;
-  for (int j0 = 0; j0 < p.nseq; j0 += 64) {
-    const int j = j0 + lane < p.nseq ? j0 + lane : p.nseq - 1;
-    const bool mine = j0 + lane < p.nseq && (int64_t)p.start[j + 1] - p.start[j] > p.len_lo;
-    const unsigned long long all = __ballot(mine);
-    const unsigned long long m = __ballot(mine && ranks + __popcll(all & ((1ull << lane) - 1)) == x);
-    if (m) {
-      *rank = x;
-      return j0 + __builtin_ctzll(m);
-    }
-    ranks += __popcll(all);
-  }
-  return -1;
 }
 
 // Where few tiles have many tokens (p.seg_shift != 0), prompts are cut into
@@ -913,9 +878,14 @@ void launch_chunks(const PromptParams& p, hipStream_t st) {
 }
 
 template <int DK, int DV>
-int launch(const PromptParams& p, hipStream_t st) {
+int launch(int act, const PromptParams& p, hipStream_t st) {
   constexpr int NW = DV / 16;                    // a workgroup has all columns of a tile
-  hipLaunchKernelGGL((prompt_prep_kernel<DK>), dim3((unsigned)p.nslots * p.H), dim3(256), 0, st, p);
+  const dim3 prep((unsigned)p.nslots * p.H);
+  if (act == DT_F32) {
+    hipLaunchKernelGGL((prompt_prep_kernel<DK, float>), prep, dim3(256), 0, st, p);
+    return launch_prompt_chunks_f32(DK, DV, p, st);
+  }
+  hipLaunchKernelGGL((prompt_prep_kernel<DK, bf16>), prep, dim3(256), 0, st, p);
   if (p.seg_shift) {
     launch_chunks<DK, DV, NW, false>(p, st);
     hipLaunchKernelGGL((prompt_join_kernel<DK, DV>), dim3((unsigned)p.nchunked * p.H * (DV / 64)), dim3(256),
@@ -931,10 +901,10 @@ int launch(const PromptParams& p, hipStream_t st) {
 
 }  // namespace
 
-int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st) {
-  if (dk == 64 && dv == 64) return launch<64, 64>(p, st);
-  if (dk == 128 && dv == 64) return launch<128, 64>(p, st);
-  if (dk == 128 && dv == 128) return launch<128, 128>(p, st);
+int launch_prompt_chunks(int dk, int dv, int act, const PromptParams& p, hipStream_t st) {
+  if (dk == 64 && dv == 64) return launch<64, 64>(act, p, st);
+  if (dk == 128 && dv == 64) return launch<128, 64>(act, p, st);
+  if (dk == 128 && dv == 128) return launch<128, 128>(act, p, st);
   return -2;
 }
 

@@ -1,5 +1,4 @@
-// Prompts through the gated delta rule in chunks of 64 tokens (bf16
-// activations).  With alpha_i, beta_i of a chunk's tokens, g_i the product of
+// Prompts through the gated delta rule in chunks of 64 tokens.  With alpha_i, beta_i of a chunk's tokens, g_i the product of
 // the decays up to token i, D_ij the product of those after j up to i (so that
 // no quotient of decays occurs), and S_0 the state before the chunk:
 //   A_ij = beta_i D_ij (k_i . k_j)  for j < i,       T = (I + A)^-1 diag(beta)
@@ -16,7 +15,8 @@
 // data (K, K^T) takes three instructions, one of two fp32 operands (T R) the
 // six whose terms reach 2^-24 of it.  What only reaches the output, which is
 // rounded to bf16 at 2^-9, takes the first two values (2^-16).  The fp32 matrix
-// instructions have a sixteenth of the bf16 ones' rate.
+// instructions have a sixteenth of the bf16 ones' rate; fp32 activations use
+// them throughout (K and Q would have to be split too, 9 products for 8).
 #pragma once
 
 #include "sk_serve_device.hpp"
@@ -30,11 +30,15 @@ constexpr int T_BYTES = FRAGS * 3 * FRAG_BYTES, P_BYTES = FRAGS * 2 * FRAG_BYTES
 // workspace of a chunk and head: the fragments of T (three values each), then
 // of P (two), then g [64] and D_C [64] in fp32
 constexpr int CHUNK_WORK_BYTES = T_BYTES + P_BYTES + 2 * PC * 4;
-static_assert(PC == 64 && CHUNK_WORK_BYTES == PROMPT_CHUNK_WORK, "workspace of a chunk");
+// in fp32: the 16 x 16 tiles of T on and below the diagonal, then of P, as A
+// operands of the fp32 instruction (four columns a lane), then the same factors
+constexpr int F32_TILES = 10;
+constexpr int CHUNK_WORK_F32 = 2 * F32_TILES * FRAG_BYTES + 2 * PC * 4;
+static_assert(PC == 64 && CHUNK_WORK_BYTES == PROMPT_CHUNK_WORK && CHUNK_WORK_F32 == PROMPT_CHUNK_WORK_F32,
+              "workspace of a chunk");
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ bf16x8 as_frag(const u32x4& x) { return __builtin_bit_cast(bf16x8, x); }
 
@@ -80,6 +84,79 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[TERMS]
     }
     out[t] = as_frag(w);
   }
+}
+
+// The prompt that has a slot (of 2^shift tokens: chunks, or segments of a
+// prompt), and its rank among those taken in chunks: the last whose first slot
+// is not behind this one (-1: none; its own end is for the caller to check).
+__device__ __forceinline__ int slot_prompt(const PromptParams& p, int slot, int shift, int* rank) {
+  const int lane = threadIdx.x & 63;
+  int i = -1, ranks = 0;
+  for (int j0 = 0; j0 < p.nseq; j0 += 64) {
+    const int j = j0 + lane < p.nseq ? j0 + lane : p.nseq - 1;
+    const int a = p.start[j];
+    const bool mine = j0 + lane < p.nseq && (int64_t)p.start[j + 1] - a > p.len_lo;
+    const unsigned long long all = __ballot(mine);
+    const int r = ranks + __popcll(all & ((1ull << lane) - 1));
+    const unsigned long long m = __ballot(mine && first_slot(a, r, shift) <= slot);
+    if (m) {
+      const int l = 63 - __clzll(m);
+      i = j0 + l;
+      *rank = ranks + __popcll(all & ((1ull << l) - 1));
+    }
+    ranks += __popcll(all);
+  }
+  return i;
+}
+
+// The x-th of the prompts taken in chunks (-1: there are not so many), and its
+// rank among them as listed.  Up to 64 prompts are taken longest first (a lane
+// each), so that the last workgroups to start are the shortest; more are taken
+// as listed.
+__device__ __forceinline__ int chunked_prompt(const PromptParams& p, int x, int* rank) {
+  const int lane = threadIdx.x & 63;
+  if (p.nseq <= 64) {
+    const int j = lane < p.nseq ? lane : 0;
+    const int len = p.start[j + 1] - p.start[j];
+    const bool mine = lane < p.nseq && len > p.len_lo;
+    const unsigned long long all = __ballot(mine);
+    int before = 0;
+    for (int k = 0; k < p.nseq; ++k) {
+      const int other = __builtin_amdgcn_readlane(len, k);
+      before += (all >> k & 1) && (other > len || (other == len && k < lane));
+    }
+    const unsigned long long m = __ballot(mine && before == x);
+    if (!m) return -1;
+    const int i = __builtin_ctzll(m);
+    *rank = __popcll(all & ((1ull << i) - 1));
+    return i;
+  }
+  int ranks = 0;
+  for (int j0 = 0; j0 < p.nseq; j0 += 64) {
+    const int j = j0 + lane < p.nseq ? j0 + lane : p.nseq - 1;
+    const bool mine = j0 + lane < p.nseq && (int64_t)p.start[j + 1] - p.start[j] > p.len_lo;
+    const unsigned long long all = __ballot(mine);
+    const unsigned long long m = __ballot(mine && ranks + __popcll(all & ((1ull << lane) - 1)) == x);
+    if (m) {
+      *rank = x;
+      return j0 + __builtin_ctzll(m);
+    }
+    ranks += __popcll(all);
+  }
+  return -1;
+}
+
+// 16 bytes of each lane, from base + its offset in memory to lds + 16 * lane
+// in LDS (base and lds are uniform), in flight until the wave's next wait for
+// its memory counter.  (The compiler would have every LDS read wait for a copy
+// that it knows of, also where the two are in different buffers.)
+__device__ __forceinline__ void copy16(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset),
+               "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
 }  // namespace sk

@@ -77,16 +77,19 @@ struct NormParams {
   float eps;
 };
 
-// Chunked form (bf16 activations): tokens of a chunk, workspace of a chunk and
-// head, and whether the shape has it.
+// Chunked form: tokens of a chunk, workspace of a chunk and head by activation
+// type, and whether the shape has it.
 constexpr int PROMPT_CHUNK = 64;
 constexpr int PROMPT_CHUNK_WORK = 30 * 1024 + 512;
 constexpr int PROMPT_WORK_OVER = 512;    // read, not used, behind the last one
-inline bool prompt_chunked(int dk, int act) { return act == DT_BF16 && dk >= 64; }
+constexpr int PROMPT_CHUNK_WORK_F32 = 20 * 1024 + 512;
+inline bool prompt_chunked(int dk) { return dk >= 64; }
+inline int prompt_chunk_work(int act) { return act == DT_F32 ? PROMPT_CHUNK_WORK_F32 : PROMPT_CHUNK_WORK; }
 // Slots of 2^shift tokens that n prompts of together up to `tokens` tokens may take.
 inline int64_t prompt_slots(int64_t tokens, int64_t n, int shift) { return (tokens >> shift) + n; }
 
-int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t st);
+int launch_prompt_chunks(int dk, int dv, int act, const PromptParams& p, hipStream_t st);
+int launch_prompt_chunks_f32(int dk, int dv, const PromptParams& p, hipStream_t st);
 int launch_prompt_step(int dk, int dv, int act, const PromptParams& p, hipStream_t st);
 int launch_state_save(int dk, int dv, const CacheParams& p, hipStream_t st);
 int launch_state_load(int dk, int dv, int sketch, const CacheParams& p, hipStream_t st);

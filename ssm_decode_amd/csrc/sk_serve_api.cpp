@@ -36,17 +36,17 @@ struct Plan {
 };
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   Plan p{};
-  if (!sk::prompt_chunked(L->dk, L->act_dtype) || tokens <= kShort || nseq == 0) return p;
+  if (!sk::prompt_chunked(L->dk) || tokens <= kShort || nseq == 0) return p;
   // mostly long prompts: the chunked form takes the short ones too, and one
   // launch is saved
   p.all = tokens > sk::PROMPT_CHUNK * nseq;
   const int64_t most = tokens / (kShort + 1);
   p.chunked = p.all || nseq < most ? nseq : most;
   p.slots = sk::prompt_slots(tokens, p.chunked, 6);
-  p.bytes = p.slots * L->heads * sk::PROMPT_CHUNK_WORK + sk::PROMPT_WORK_OVER;
+  p.bytes = p.slots * L->heads * sk::prompt_chunk_work(L->act_dtype) + sk::PROMPT_WORK_OVER;
   // Few tiles with many tokens: segments, as long as one of each tile fills the
   // CUs about once
-  if (p.chunked * L->heads <= kSplitTiles) {
+  if (L->act_dtype == SKSSM_BF16 && p.chunked * L->heads <= kSplitTiles) {
     int shift = kMinSegShift;
     while ((tokens >> shift) * L->heads > kSegTiles || (tokens >> shift) > kMaxSegs * p.chunked) ++shift;
     if ((tokens >> shift) >= kMinSegs * p.chunked) {
@@ -208,7 +208,7 @@ int sketchssm_prefill(const sketchssm_layer* layer, const sketchssm_buffers* buf
       p.nsegs = (int)pl.nsegs;
       p.seg = reinterpret_cast<float*>(static_cast<char*>(pr->work) + pl.seg_at);
       p.len_lo = pl.all ? -1 : kShort;
-      if ((rc = sk::launch_prompt_chunks(dk, dv, p, st)) || pl.all) return rc;
+      if ((rc = sk::launch_prompt_chunks(dk, dv, layer->act_dtype, p, st)) || pl.all) return rc;
       p.len_hi = kShort;
     }
     return sk::launch_prompt_step(dk, dv, layer->act_dtype, p, st);

@@ -50,7 +50,7 @@ int launch_gdn(int, int, int, int, int, int, const Params&, hipStream_t) { retur
 int launch_kda(int, int, int, int, int, int, const Params&, hipStream_t) { return 0; }
 int noalloc_scratch(void** out) { *out = nullptr; return 0; }
 
-int launch_prompt_chunks(int dk, int dv, const PromptParams& p, hipStream_t) {
+int launch_prompt_chunks(int dk, int dv, int, const PromptParams& p, hipStream_t) {
   ++g_launches;
   for (int rep = 0; rep < 6; ++rep) {
     std::vector<int> start(p.nseq + 1);
