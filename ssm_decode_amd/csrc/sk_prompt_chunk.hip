@@ -321,24 +321,6 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// The end of a region: its instructions in the order of N times a matrix
-// instruction, READS LDS reads and VALU vector instructions (as far as there
-// are any), and nothing moved across.
-template <int N, int READS, int VALU>
-__device__ __forceinline__ void interleave() {
-  if constexpr (N > 0) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
-    if constexpr (VALU > 0) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-    interleave<N - 1, READS, VALU>();
-  }
-}
-template <int N, int READS, int VALU>
-__device__ __forceinline__ void region() {
-  interleave<N, READS, VALU>();
-  __builtin_amdgcn_sched_barrier(0);
-}
-
 // Where few tiles have many tokens (p.seg_shift != 0), prompts are cut into
 // segments of 2^seg_shift tokens, and three launches take the place of one:
 //   1. STATE: the segments but the last, at once, without outputs: each from a

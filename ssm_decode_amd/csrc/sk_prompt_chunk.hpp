@@ -159,4 +159,22 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
+// The end of a region: its instructions in the order of N times a matrix
+// instruction, READS LDS reads and VALU vector instructions (as far as there
+// are any), and nothing moved across.
+template <int N, int READS, int VALU>
+__device__ __forceinline__ void interleave() {
+  if constexpr (N > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    if constexpr (VALU > 0) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    interleave<N - 1, READS, VALU>();
+  }
+}
+template <int N, int READS, int VALU>
+__device__ __forceinline__ void region() {
+  interleave<N, READS, VALU>();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 }  // namespace sk

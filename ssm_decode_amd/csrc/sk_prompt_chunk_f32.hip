@@ -12,6 +12,8 @@
 // beside the triangles, of 32 cycles for 2048.  K and T, P are in LDS twice, Q
 // once (its next copy starts when the chunk's outputs have it behind them), V
 // comes to registers a chunk ahead.
+#include <type_traits>
+
 #include "sk_prompt_chunk.hpp"
 
 namespace sk {
@@ -35,7 +37,7 @@ __device__ __forceinline__ f32x4s mm4(float a, float b, f32x4s c) {
 }
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(64 * NW, 1) prompt_chunk_f32_kernel(PromptParams p) {
+__global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptParams p) {
   using L = F32Lds<DK>;
   constexpr int PPR = DK / 4, MB = DK / 16, TB = PC / 16, PARTS = DV / (16 * NW);
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -55,49 +57,71 @@ __global__ void __launch_bounds__(64 * NW, 1) prompt_chunk_f32_kernel(PromptPara
   const int c0 = part * NW * 16 + wv * 16;       // the wave's first column
   const float* kp = reinterpret_cast<const float*>(p.k) + s0 * p.ks + (int64_t)h * DK;
   const float* qp = reinterpret_cast<const float*>(p.q) + s0 * p.qs + (int64_t)h * DK;
-  const float* vp = reinterpret_cast<const float*>(p.v) + s0 * p.vs + (int64_t)h * DV + c0 + n;
-  float* op = reinterpret_cast<float*>(p.o) + s0 * p.os + (int64_t)h * DV + c0 + n;
+  const float* vp = reinterpret_cast<const float*>(p.v) + s0 * p.vs + (int64_t)h * DV + c0;      // (all uniform)
+  float* op = reinterpret_cast<float*>(p.o) + s0 * p.os + (int64_t)h * DV + c0;
   const unsigned char* wp = reinterpret_cast<const unsigned char*>(p.work) +
                             ((size_t)first_slot(s0, rank, 6) * p.H + h) * CHUNK_WORK_F32;
   const uint32_t lds0 = lds_address(smem);
 
-  // 64 rows of K or Q from token t0 on; 16-byte pieces swizzled by row.  A unit
-  // is 64 pieces; rows behind the prompt's end repeat its last one (their beta
-  // in T is 0, their columns of P meet only zeros).
-  auto piece = [](int row, int pc) { return row * PPR + (pc ^ (row & 15)); };
-  auto copy_rows = [&](const float* base, int64_t stride, int t0, uint32_t lds) {
-    constexpr int RPU = 64 / PPR;                // rows of a unit
-    const int end = len - t0 < PC ? len - t0 - 1 : PC - 1;
+  // 64 rows of K or Q; 16-byte pieces swizzled by row.  A unit is 64 pieces.  In a
+  // whole chunk a lane's offset from the unit's first row is the same in all of
+  // a wave's units but for the swizzle, whose period is 16 rows.
+  constexpr int RPU = 64 / PPR, KU = PPR / NW;   // rows of a unit, a wave's units
+  auto swz = [&](int v) { return (uint32_t)((lane % PPR) ^ (((NW * v + wv) * RPU + lane / PPR) & 15)) * 16; };
+  constexpr int PERIOD = 16 / (NW * RPU) > 0 ? 16 / (NW * RPU) : 1;
+  const uint32_t krow = (uint32_t)(lane / PPR * p.ks * 4), qrow = (uint32_t)(lane / PPR * p.qs * 4);
+  uint32_t sw[PERIOD];
 #pragma unroll
-    for (int v = 0; v < PPR / NW; ++v) {
+  for (int v = 0; v < PERIOD; ++v) sw[v] = swz(v);
+  const float *kc = kp + wv * RPU * p.ks, *qc = qp + wv * RPU * p.qs, *vc = vp;      // (uniform, of the next chunk)
+  const int run0 = (wv * RUNS < WRUNS - RUNS ? wv * RUNS : WRUNS - RUNS) * 1024;     // (the last wave's runs end with the workspace)
+  const unsigned char* wc = wp + run0;
+  auto copy_k = [&](int v, uint32_t lds) { copy16(kc + v * NW * RPU * p.ks, krow + sw[v % PERIOD], lds + (NW * v + wv) * 1024); };
+  auto copy_q = [&](int v, uint32_t lds) { copy16(qc + v * NW * RPU * p.qs, qrow + sw[v % PERIOD], lds + (NW * v + wv) * 1024); };
+  auto copy_w = [&](int u, uint32_t lds) { copy16(wc + u * 1024, lane * 16, lds + run0 + u * 1024); };
+  auto next_chunk = [&]() {
+    kc += PC * p.ks;
+    qc += PC * p.qs;
+    vc += PC * p.vs;
+    wc += (size_t)p.H * CHUNK_WORK_F32;
+  };
+  // .. and of a chunk that may be the prompt's last: rows behind its end repeat
+  // its last one (their beta in T is 0, their columns of P meet only zeros)
+  auto copy_rows = [&](const float* base, int64_t stride, int t0, uint32_t lds) {
+    const int end = len - t0 < PC ? len - t0 - 1 : PC - 1;
+#pragma unroll 1
+    for (int v = 0; v < KU; ++v) {
       const int u = NW * v + wv, row0 = u * RPU, from = row0 < end ? row0 : end;      // (uniform)
       const int row = row0 + lane / PPR, left = (row < end ? row : end) - from;
-      copy16(base + (t0 + from) * stride, (uint32_t)(left * stride * 4) + (uint32_t)((lane % PPR) ^ (row & 15)) * 16,
-             lds + u * 1024);
+      copy16(base + (t0 + from) * stride, (uint32_t)(left * stride * 4) + swz(v), lds + u * 1024);
     }
   };
-  auto copy_work = [&](int t0, uint32_t lds) {   // (the last wave's runs end with the workspace)
-    const int run0 = wv * RUNS < WRUNS - RUNS ? wv * RUNS : WRUNS - RUNS;
-    const unsigned char* w = wp + (size_t)(t0 / PC) * p.H * CHUNK_WORK_F32 + run0 * 1024;
-#pragma unroll
-    for (int u = 0; u < RUNS; ++u) copy16(w + u * 1024, lane * 16, lds + (run0 + u) * 1024);
-  };
+  const uint32_t vo = (uint32_t)(4 * hi * p.vs + n) * 4;
   float vv[TB][4];
-  auto load_v = [&](int t0) {
+  auto load_v = [&](int tb) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      vv[tb][r] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(vc + (16 * tb + r) * p.vs) + vo);
+  };
+  auto load_v_last = [&](int t0) {
     const int end = len - t0 < PC ? len - t0 - 1 : PC - 1;
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = 16 * tb + 4 * hi + r;
-        vv[tb][r] = vp[(t0 + (row < end ? row : end)) * p.vs];
+        vv[tb][r] = vp[(t0 + (row < end ? row : end)) * p.vs + n];
       }
   };
+  auto copy_last = [&](int t0, int buf) {        // (K, T and P)
+    copy_rows(kp, p.ks, t0, lds0 + L::K + buf * L::KBYTES);
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) copy_w(u, lds0 + L::W + buf * L::WBYTES);
+  };
   if (len > 0) {
-    copy_rows(kp, p.ks, 0, lds0 + L::K);
+    copy_last(0, 0);
     copy_rows(qp, p.qs, 0, lds0 + L::Q);
-    copy_work(0, lds0 + L::W);
-    load_v(0);
+    load_v_last(0);
   }
 
   float* Sg = p.S + ((size_t)b * p.H + h) * DK * DV + (size_t)(4 * hi) * DV + c0 + n;
@@ -110,105 +134,168 @@ __global__ void __launch_bounds__(64 * NW, 1) prompt_chunk_f32_kernel(PromptPara
       for (int r = 0; r < 4; ++r) S[mb][r] = read ? Sg[(size_t)(16 * mb + r) * DV] : 0.f;
   }
 
-  int buf = 0;
-  for (int t0 = 0; t0 < len; t0 += PC, buf ^= 1) {
+  // a chunk's outputs leave in the next chunk's time (the wait at its start
+  // would wait for them too)
+  float out[TB][4];
+  const uint32_t oo = (uint32_t)(4 * hi * p.os + n) * 4;
+  auto store_out = [&](int t0, int tb, int cnt) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (cnt >= PC || 16 * tb + 4 * hi + r < cnt)
+        *reinterpret_cast<float*>(reinterpret_cast<char*>(op + (t0 + 16 * tb + r) * p.os) + oo) = out[tb][r];
+  };
+
+  // A lane's byte offsets into rows of K or Q: of four columns 16 kb + 4 hi .. of
+  // row 16 tb + n (kb % 4 = m), and of column 16 mb + n of row 16 kb + 4 hi + r
+  // (mb % 4 = m).  The swizzle leaves the rest of both indices to constants.
+  constexpr int ROWB = DK * 4;
+  uint32_t by_row[4], by_col[4][4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    by_row[m] = n * ROWB + (4 * (m ^ (n >> 2)) + (hi ^ (n & 3))) * 16;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) by_col[m][r] = (4 * hi + r) * ROWB + (4 * (m ^ hi) + ((n >> 2) ^ r)) * 16 + (n & 3) * 4;
+  }
+
+  int t0 = 0, buf = 0;
+  // one chunk; `more`: a whole one follows.  Steps of up to 16 matrix
+  // instructions, in each the reads of the next one's A operands.
+  auto chunk = [&](auto more) {
+    constexpr bool MORE = decltype(more)::value;
     // this wave's copies for the chunk have landed, then everybody's; and
-    // everybody has read the other buffers
+    // everybody has read the other buffers.  (V's loads too: the compiler, which
+    // does not know of the copies, would wait for the next chunk's with them.)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    const bool more = len - t0 > PC;
-    if (more) {
-      copy_rows(kp, p.ks, t0 + PC, lds0 + L::K + (buf ^ 1) * L::KBYTES);
-      copy_work(t0 + PC, lds0 + L::W + (buf ^ 1) * L::WBYTES);
-    }
-    const float* s_k = reinterpret_cast<const float*>(smem + L::K + buf * L::KBYTES);
-    const float* s_q = reinterpret_cast<const float*>(smem + L::Q);
-    const float* s_w = reinterpret_cast<const float*>(smem + L::W + buf * L::WBYTES);
-    const float* s_g = s_w + 2 * F32_TILES * 256;
-    const f32x4s zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4s R[TB], O[TB], U[TB];
-    // K S and Q S
-    auto times_state = [&](const float* m, f32x4s (&out)[TB]) {
-#pragma unroll
-      for (int tb = 0; tb < TB; ++tb) out[tb] = zero;
-#pragma unroll
-      for (int kb = 0; kb < MB; ++kb) {
-        float a[TB][4];
-#pragma unroll
-        for (int tb = 0; tb < TB; ++tb) ld4(m + piece(16 * tb + n, 4 * kb + hi) * 4, a[tb]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int tb = 0; tb < TB; ++tb) out[tb] = mm4(a[tb][r], S[kb][r], out[tb]);
-      }
-    };
-    times_state(s_q, O);
-    __syncthreads();                             // everybody has read Q
-    if (more) copy_rows(qp, p.qs, t0 + PC, lds0 + L::Q);
-    times_state(s_k, R);
-    float g[TB][4];
-#pragma unroll
-    for (int tb = 0; tb < TB; ++tb) {
-      ld4(s_g + 16 * tb + 4 * hi, g[tb]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        R[tb][r] = vv[tb][r] - g[tb][r] * R[tb][r];
-        O[tb][r] *= g[tb][r];
-      }
-    }
-    if (more) load_v(t0 + PC);
-    // U = T R, O += P U: tile (tb, kb) is the (tb (tb + 1) / 2 + kb)-th
-    auto triangle = [&](const float* m, const f32x4s (&in)[TB], f32x4s (&out)[TB]) {
-#pragma unroll
-      for (int kb = 0; kb < TB; ++kb) {
-        float a[TB][4];
-#pragma unroll
-        for (int tb = kb; tb < TB; ++tb) ld4(m + (tb * (tb + 1) / 2 + kb) * 256 + lane * 4, a[tb]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int tb = kb; tb < TB; ++tb) out[tb] = mm4(a[tb][r], in[kb][r], out[tb]);
-      }
-    };
-#pragma unroll
-    for (int tb = 0; tb < TB; ++tb) U[tb] = zero;
-    triangle(s_w, R, U);
-    triangle(s_w + F32_TILES * 256, U, O);
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * tb + 4 * hi + r;
-        if (t0 + row < len) op[(t0 + row) * p.os] = O[tb][r];
-      }
-    // S = g_C S + K^T (D_C U)
-    const float gC = s_g[PC - 1];
+      for (int r = 0; r < 4; ++r) asm volatile("" : "+v"(vv[tb][r]));
+    __syncthreads();
+    const unsigned char *s_k = smem + L::K + buf * L::KBYTES, *s_q = smem + L::Q;
+    const float* s_w = reinterpret_cast<const float*>(smem + L::W + buf * L::WBYTES);
+    const float* s_g = s_w + 2 * F32_TILES * 256;
+    const uint32_t knext = lds0 + L::K + (buf ^ 1) * L::KBYTES, wnext = lds0 + L::W + (buf ^ 1) * L::WBYTES;
+    const bool tail = !MORE && len - t0 > PC;    // the prompt's end follows
+    const f32x4s zero = {0.f, 0.f, 0.f, 0.f};
+
+    float a[2][4][4], g[TB][4], d[TB][4];
+    auto load_rows = [&](const unsigned char* s, int kb, int at) {
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb) {
-      float d[4];
-      ld4(s_g + PC + 16 * tb + 4 * hi, d);
+      for (int tb = 0; tb < TB; ++tb)
+        ld4(reinterpret_cast<const float*>(s + by_row[kb & 3] + (kb >> 2) * 256 + tb * 16 * ROWB), a[at & 1][tb]);
+    };
+    // column kb of a triangle: tile (tb, kb) is the (tb (tb + 1) / 2 + kb)-th
+    auto load_tri = [&](const float* m, int kb, int at) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) U[tb][r] *= d[r];
-    }
+      for (int tb = kb; tb < TB; ++tb) ld4(m + (tb * (tb + 1) / 2 + kb) * 256 + lane * 4, a[at & 1][tb]);
+    };
+    auto load_kt = [&](int kb, int m0, int at) {
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[mb][r] *= gC;
-#pragma unroll
-    for (int kb = 0; kb < TB; ++kb)
-#pragma unroll
-      for (int m0 = 0; m0 < MB; m0 += 4) {
-        float a[4][4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            a[m][r] = s_k[piece(16 * kb + 4 * hi + r, 4 * (m0 + m) + (n >> 2)) * 4 + (n & 3)];
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
+          a[at & 1][m][r] = *reinterpret_cast<const float*>(s_k + by_col[m][r] + m0 * 64 + kb * 16 * ROWB);
+    };
+    auto times = [&](int at, const f32x4s& in, f32x4s* out, int from) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) S[m0 + m] = mm4(a[m][r], U[kb][r], S[m0 + m]);
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int m = from; m < 4; ++m) out[m] = mm4(a[at & 1][m][r], in[r], out[m]);
+    };
+    f32x4s R[TB], O[TB], U[TB];
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) R[tb] = O[tb] = U[tb] = zero;
+    load_rows(s_k, 0, 0);
+    next_chunk();
+    __builtin_amdgcn_sched_barrier(0);
+    if (tail) copy_last(t0 + PC, buf ^ 1);
+    // K S
+#pragma unroll
+    for (int kb = 0; kb < MB; ++kb) {
+      if (kb + 1 < MB) load_rows(s_k, kb + 1, kb + 1);
+      else load_rows(s_q, 0, MB);
+      if (kb < TB) ld4(s_g + 16 * kb + 4 * hi, g[kb]);
+      times(kb, S[kb], R, 0);
+      region<16, 1, 2>();
+      if (MORE) {
+#pragma unroll
+        for (int u = kb * KU / MB; u < (kb + 1) * KU / MB; ++u) copy_k(u, knext);
+#pragma unroll
+        for (int u = kb * RUNS / MB; u < (kb + 1) * RUNS / MB; ++u) copy_w(u, wnext);
       }
+    }
+    // Q S;  R = V - g (K S) meanwhile
+#pragma unroll
+    for (int kb = 0; kb < MB; ++kb) {
+      if (kb + 1 < MB) load_rows(s_q, kb + 1, kb + 1);
+      else load_tri(s_w, 0, MB);
+      if (kb < TB) {
+        ld4(s_g + PC + 16 * kb + 4 * hi, d[kb]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) R[kb][r] = vv[kb][r] - g[kb][r] * R[kb][r];
+      }
+      times(kb, S[kb], O, 0);
+      region<16, 1, 2>();
+    }
+    if (t0 > 0) {
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) store_out(t0 - PC, tb, PC);
+    }
+    const float gC = s_g[PC - 1];
+    __syncthreads();                             // everybody has read Q
+    if (tail) {
+      copy_rows(qp, p.qs, t0 + PC, lds0 + L::Q);
+      load_v_last(t0 + PC);
+    }
+    // U = T R;  S = g_C S and O = g O meanwhile
+    constexpr int STEPS = 1 + MB / 4;            // of the last part, for each block of tokens
+#pragma unroll
+    for (int kb = 0; kb < TB; ++kb) {
+      if (kb + 1 < TB) load_tri(s_w, kb + 1, kb + 1);
+      else load_tri(s_w + F32_TILES * 256, 0, TB);
+      times(kb, R[kb], U, kb);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) O[kb][r] *= g[kb][r];
+#pragma unroll
+      for (int mb = kb * MB / TB; mb < (kb + 1) * MB / TB; ++mb)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[mb][r] *= gC;
+      region<4 * (TB - 1), 1, 4>();
+      if (MORE) {
+#pragma unroll
+        for (int u = kb * KU / TB; u < (kb + 1) * KU / TB; ++u) copy_q(u, lds0 + L::Q);
+        load_v(kb);
+      }
+    }
+    // O += P U;  S += K^T (D_C U)
+#pragma unroll
+    for (int kb = 0; kb < TB; ++kb) {
+      load_kt(kb, 0, kb * STEPS + 1);
+      times(kb * STEPS, U[kb], O, kb);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) U[kb][r] *= d[kb][r];
+      region<16, 2, 2>();
+#pragma unroll
+      for (int m0 = 0; m0 < MB; m0 += 4) {
+        const int at = kb * STEPS + 1 + m0 / 4;
+        if (m0 + 4 < MB) load_kt(kb, m0 + 4, at + 1);
+        else if (kb + 1 < TB) load_tri(s_w + F32_TILES * 256, kb + 1, at + 1);
+        times(at, U[kb], S + m0, 0);
+        region<16, 1, 2>();
+      }
+    }
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) out[tb][r] = O[tb][r];
+    t0 += PC;
+    buf ^= 1;
+  };
+  while (len - t0 >= 2 * PC) chunk(std::true_type{});
+  while (t0 < len) chunk(std::false_type{});
+  if (len > 0) {
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) store_out(t0 - PC, tb, len - (t0 - PC));
   }
 
   float s[MB][1][4];
