@@ -357,7 +357,7 @@ typedef struct {
  * leaves [0, tokens] sets SKSSM_ERRBIT_SEQ and nothing is written.  A prompt of
  * no tokens leaves its state (or writes the zero state), with prime its sketch
  * too.  Token rows that no prompt holds are neither read nor written.
- * Sums run in fp32; prompts of more than 16 tokens (dk >= 64) go in chunks of 64
+ * Sums run in fp32; longer prompts (dk >= 64) go in chunks of 64
  * tokens, whose products are those of fp32 operands.  An infinity or a NaN
  * in a token's row or in the state reaches, besides what the recurrence brings
  * it to, the outputs of its head and prompt from the start of its chunk (of

@@ -16,8 +16,13 @@ constexpr int kMaxWidth = 8192;
 constexpr int64_t kMaxTiles = (1 << 22) - 1;
 
 // Prompts of up to this many tokens go token by token where the launch has
-// both kinds.
-constexpr int kShort = 16;
+// both kinds.  A chunk's two launches take about as long for 4 tokens as for 64,
+// the other form's time grows by the token; measured, token by token and in
+// chunks (us): bf16 128 x 128, 1024 tiles of 24 tokens 76 and 97, of 32 92 and 99,
+// 64 tiles of 16 22 and 25, of 24 29 and 25; fp32 128 x 128, 1024 tiles of 32 133
+// and 160, 64 tiles of 32 32 and 31; 64 x 64, 1024 tiles of 64 tokens 60 and 82
+// (fp32 68 and 97), 128 tiles of fp32 of 32 18 and 24, of 64 30 and 25.
+int short_prompt(const sketchssm_layer* L) { return L->dk == 64 ? 48 : L->act_dtype == SKSSM_F32 ? 32 : 24; }
 // Prompts in segments: up to kSplitTiles (prompt, head) tiles, at least kMinSegs
 // segments of 2^kMinSegShift tokens or more to a prompt on average, at most
 // kMaxSegs (the states between them are joined in order, about 6 us each) and
@@ -27,7 +32,7 @@ constexpr int kShort = 16;
 constexpr int kSplitTiles = 48, kSegTiles = 256, kMinSegShift = 10, kMinSegs = 4, kMaxSegs = 12;
 
 // How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
-// none), all of them or those of more than kShort tokens; in segments of
+// none), all of them or those of more than short_prompt tokens; in segments of
 // 2^seg_shift tokens (0: whole), with the bytes of their states at seg_at.
 struct Plan {
   int64_t chunked, slots, nsegs, seg_at, bytes;
@@ -36,11 +41,12 @@ struct Plan {
 };
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   Plan p{};
-  if (!sk::prompt_chunked(L->dk) || tokens <= kShort || nseq == 0) return p;
+  const int shrt = short_prompt(L);
+  if (!sk::prompt_chunked(L->dk) || tokens <= shrt || nseq == 0) return p;
   // mostly long prompts: the chunked form takes the short ones too, and one
   // launch is saved
   p.all = tokens > sk::PROMPT_CHUNK * nseq;
-  const int64_t most = tokens / (kShort + 1);
+  const int64_t most = tokens / (shrt + 1);
   p.chunked = p.all || nseq < most ? nseq : most;
   p.slots = sk::prompt_slots(tokens, p.chunked, 6);
   p.bytes = p.slots * L->heads * sk::prompt_chunk_work(L->act_dtype) + sk::PROMPT_WORK_OVER;
@@ -207,9 +213,9 @@ int sketchssm_prefill(const sketchssm_layer* layer, const sketchssm_buffers* buf
       p.seg_shift = pl.seg_shift;
       p.nsegs = (int)pl.nsegs;
       p.seg = reinterpret_cast<float*>(static_cast<char*>(pr->work) + pl.seg_at);
-      p.len_lo = pl.all ? -1 : kShort;
+      p.len_lo = pl.all ? -1 : short_prompt(layer);
       if ((rc = sk::launch_prompt_chunks(dk, dv, layer->act_dtype, p, st)) || pl.all) return rc;
-      p.len_hi = kShort;
+      p.len_hi = short_prompt(layer);
     }
     return sk::launch_prompt_step(dk, dv, layer->act_dtype, p, st);
   } catch (...) {

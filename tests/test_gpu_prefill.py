@@ -465,3 +465,18 @@ def test_a_list_that_only_falls_is_reported(tokens, starts):
     run(lay, tok, None, starts=starts)
     assert lay.error_word() == abi.SKSSM_ERRBIT_SEQ
     assert torch.equal(lay.S, S0) and (tok[5].float() == torch.tensor(SENTINEL).to(tok[5].dtype).float()).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_short_and_long_prompts_together(dk, dv, act):
+    """Lengths about those where a prompt changes from one form to the other."""
+    lens = [16, 17, 24, 25, 1, 32, 33, 0, 48, 49, 64, 65]
+    n = len(lens)
+    lay = make_layer(n, 3, dk, dv, act, seed=90)
+    tok = make_tokens(sum(lens), 3, dk, dv, act, seed=91, packed=True, pad=1)
+    S0 = lay.S.clone()
+    seqs, has = list(range(n))[::-1], [i % 3 > 0 for i in range(n)]
+    _, starts = run(lay, tok, lens, seqs=seqs, has=[int(x) for x in has])
+    assert lay.error_word() == 0
+    check(lay, S0, tok, lens, starts, seqs, has)
