@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   constexpr int MB = PC * LS * 4;                // bytes of A or P in LDS
   constexpr int BIG = 2 * KB > 2 * MB ? 2 * KB : 2 * MB;
   __shared__ __align__(16) unsigned char s_big[BIG];   // K and Q, then A (T in its place) and P
-  __shared__ float s_al[PC], s_be[PC], s_pre[PC], s_suf[PC], s_blk[4], s_din[PC * 17];
+  __shared__ __align__(16) float s_al[PC], s_be[PC], s_pre[PC], s_suf[PC], s_blk[4], s_mid[16], s_din[PC * 17];
   float* s_A = reinterpret_cast<float*>(s_big);
   float* s_P = reinterpret_cast<float*>(s_big + MB);
 
@@ -84,18 +84,41 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
     s_suf[lane] = d;
     s_pre[lane] = pre;
     if (jl == 15) s_blk[b] = pre;
+    wave_lds_sync();
+    if (lane < 16) {                                    // over the blocks between two
+      float mid = 1.f;
+#pragma unroll
+      for (int t = 1; t < 3; ++t)
+        if (t > (lane & 3) && t < (lane >> 2)) mid *= s_blk[t];
+      s_mid[lane] = mid;
+    }
   }
   __syncthreads();
 
-  // tiles (ti, tj), tj <= ti, of K K^T and Q K^T
+  // tiles (ti, tj), tj <= ti, of K K^T and Q K^T: the t-th, t = wave + 4 n (the
+  // last ones repeat tile 9 and are dropped: no branch between the products)
   f32x4s ak[3], aq[3];
   const int cg = lane & 15, g = lane >> 4;
   auto tile_of = [](int t, int* ti, int* tj) {
     *ti = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
     *tj = t - *ti * (*ti + 1) / 2;
   };
+  int ti[3], tj[3];
+  float D[3][4], be[3][4];                              // D_ij and beta_i of the lane's results
 #pragma unroll
-  for (int n = 0; n < 3; ++n) ak[n] = aq[n] = f32x4s{0.f, 0.f, 0.f, 0.f};
+  for (int n = 0; n < 3; ++n) {
+    tile_of(wv + 4 * n < 10 ? wv + 4 * n : 9, &ti[n], &tj[n]);
+    ak[n] = aq[n] = f32x4s{0.f, 0.f, 0.f, 0.f};
+    const float across = s_mid[4 * ti[n] + tj[n]] * s_suf[16 * tj[n] + cg];
+    float pre[4];
+    ld4(s_pre + 16 * ti[n] + 4 * g, pre);
+    ld4(s_be + 16 * ti[n] + 4 * g, be[n]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float in = s_din[(16 * ti[n] + 4 * g + r) * 17 + cg];
+      D[n][r] = ti[n] == tj[n] ? in : pre[r] * across;
+    }
+  }
 #pragma unroll
   for (int col = 0; col < DK; col += F32 ? 64 : DK) {
     if (col > 0) {
@@ -104,26 +127,21 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
       __syncthreads();
     }
 #pragma unroll
-    for (int n = 0; n < 3; ++n) {
-      const int t = wv + 4 * n;
-      if (t < 10) {                                     // uniform over the wave
-        int ti, tj;
-        tile_of(t, &ti, &tj);
+    for (int s = 0; s < PPR / 4; ++s) {
 #pragma unroll
-        for (int s = 0; s < PPR / 4; ++s) {
-          const u32x4 fk = s_k[piece(16 * ti + cg, 4 * s + g)], fq = s_q[piece(16 * ti + cg, 4 * s + g)];
-          const u32x4 fb = s_k[piece(16 * tj + cg, 4 * s + g)];
-          if constexpr (F32) {                          // K-step e: columns 16 s + 4 k + e
+      for (int n = 0; n < 3; ++n) {
+        const u32x4 fk = s_k[piece(16 * ti[n] + cg, 4 * s + g)], fq = s_q[piece(16 * ti[n] + cg, 4 * s + g)];
+        const u32x4 fb = s_k[piece(16 * tj[n] + cg, 4 * s + g)];
+        if constexpr (F32) {                            // K-step e: columns 16 s + 4 k + e
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float b = __uint_as_float(fb[e]);
-              ak[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fk[e]), b, ak[n], 0, 0, 0);
-              aq[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fq[e]), b, aq[n], 0, 0, 0);
-            }
-          } else {
-            ak[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(fk), as_frag(fb), ak[n], 0, 0, 0);
-            aq[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(fq), as_frag(fb), aq[n], 0, 0, 0);
+          for (int e = 0; e < 4; ++e) {
+            const float b = __uint_as_float(fb[e]);
+            ak[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fk[e]), b, ak[n], 0, 0, 0);
+            aq[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fq[e]), b, aq[n], 0, 0, 0);
           }
+        } else {
+          ak[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(fk), as_frag(fb), ak[n], 0, 0, 0);
+          aq[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(fq), as_frag(fb), aq[n], 0, 0, 0);
         }
       }
     }
@@ -131,21 +149,15 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   __syncthreads();                                      // K and Q are read: A and P over them
 #pragma unroll
   for (int n = 0; n < 3; ++n) {
-    const int t = wv + 4 * n;
-    if (t < 10) {
-      int ti, tj;
-      tile_of(t, &ti, &tj);
-      float mid = 1.f;
-      for (int b = tj + 1; b < ti; ++b) mid *= s_blk[b];
-      const int j = 16 * tj + cg;
+    if (wv + 4 * n < 10) {                              // uniform over the wave
+      const int j = 16 * tj[n] + cg;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int ii = 16 * ti + 4 * g + r;
-        const float D = ti == tj ? s_din[ii * 17 + cg] : s_pre[ii] * mid * s_suf[j];
+        const int ii = 16 * ti[n] + 4 * g + r;
         // (selected, not multiplied by a zero: nothing above the diagonal may
         // reach the sums)
-        s_A[ii * LS + j] = j < ii ? s_be[ii] * D * ak[n][r] : 0.f;
-        s_P[ii * LS + j] = j <= ii ? D * aq[n][r] : 0.f;
+        s_A[ii * LS + j] = j < ii ? be[n][r] * D[n][r] * ak[n][r] : 0.f;
+        s_P[ii * LS + j] = j <= ii ? D[n][r] * aq[n][r] : 0.f;
       }
     }
   }
