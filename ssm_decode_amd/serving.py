@@ -162,7 +162,8 @@ def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optiona
             raise ValueError("rows: the first row and the end")
         first = rows.data_ptr()
         end = first + 4 * (rows.numel() - 1)
-    st = abi.sketchssm_norm(_ptr(x), _ptr(gate), _ptr(y), _ptr(norm.weight), _ptr(norm.bias), xs, zs, ys,
+    w_at, b_at, z_at = (t.data_ptr() if t is not None else None for t in (norm.weight, norm.bias, gate))
+    st = abi.sketchssm_norm(x.data_ptr(), z_at, y.data_ptr(), w_at, b_at, xs, zs, ys,
                             shape[0], first, end, shape[1], shape[2], _DTYPES[dt], int(w is not None and w.dim() == 2),
                             int(norm.centred), ACT[norm.act], int(norm.gate_first), norm.eps)
     return _on_device(dev.index, lambda s: abi.sketchssm_group_norm(st, s), stream)
