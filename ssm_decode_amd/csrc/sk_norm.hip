@@ -16,7 +16,34 @@ namespace {
 
 constexpr int NORM_THREADS = 256;
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 template <typename T> struct Vec { static constexpr int N = 16 / (int)sizeof(T); };
+
+// 16 bytes as fp32 values, and back.
+__device__ __forceinline__ void unpack(const u32x4& w, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(w[e] << 16);
+    x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const u32x4& w, float (&x)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
+}
+__device__ __forceinline__ u32x4 pack(const float (&x)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = (uint32_t)f32_to_bf16(x[2 * e]) | ((uint32_t)f32_to_bf16(x[2 * e + 1]) << 16);
+  return w;
+}
+__device__ __forceinline__ u32x4 pack(const float (&x)[4]) {
+  u32x4 w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(x[e]);
+  return w;
+}
 
 // Sum over aligned groups of L lanes (L a power of two up to 64).
 template <int L>
@@ -39,7 +66,7 @@ __device__ __forceinline__ float activation(float x, int act) {
 // of a lane.  Thread position in a row: group * LPG + lane; `tpr` = groups *
 // LPG threads make a row where that is at most the workgroup, otherwise
 // blockIdx.y selects the part of the row.
-template <typename T, int LPG, int VPL>
+template <typename T, int LPG, int VPL, bool PAST>
 __global__ void __launch_bounds__(NORM_THREADS) group_norm_kernel(NormParams p) {
   constexpr int N = Vec<T>::N;
   __shared__ float s_part[4];
@@ -91,8 +118,8 @@ __global__ void __launch_bounds__(NORM_THREADS) group_norm_kernel(NormParams p) 
 #pragma unroll
       for (int e = 0; e < N; ++e) x[u][e] = z[u][e] = 0.f;
       if (c < nvec) {
-        ldn<N>(X + row * p.xs + c * N, x[u]);
-        if (p.gate) ldn<N>(Z + row * p.zs + c * N, z[u]);
+        unpack(*reinterpret_cast<const u32x4*>(X + row * p.xs + c * N), x[u]);
+        if (p.gate) unpack(*reinterpret_cast<const u32x4*>(Z + row * p.zs + c * N), z[u]);
       }
     }
     if (p.gate && p.gate_first) {
@@ -131,7 +158,9 @@ __global__ void __launch_bounds__(NORM_THREADS) group_norm_kernel(NormParams p) 
           if (!p.gate) y[e] = activation(y[e], p.act);
           else if (!p.gate_first) y[e] *= activation(z[u][e], p.act);
         }
-        stn<N>(Y + row * p.ys + c * N, y);
+        u32x4* at = reinterpret_cast<u32x4*>(Y + row * p.ys + c * N);
+        if (PAST) __builtin_nontemporal_store(pack(y), at);
+        else *at = pack(y);
       }
     }
   }
@@ -143,11 +172,15 @@ int launch(const NormParams& p, hipStream_t st) {
   const int64_t rpw = tpr < NORM_THREADS ? NORM_THREADS / tpr : 1;
   const int64_t parts = tpr < NORM_THREADS ? 1 : (tpr + NORM_THREADS - 1) / NORM_THREADS;
   int64_t rows = (p.rows + rpw - 1) / rpw;
-  // 16 workgroups for each of the 256 CUs, and further rows in turn
-  const int64_t most = (4096 + parts - 1) / parts;
+  // 64 workgroups for each of the 256 CUs, and further rows in turn (16384 x 32
+  // groups of 128, 403 MB: 16 a CU 87 us, 32 79, 64 76, one for every row 82); an
+  // output beyond the 32 MiB of the L2s is stored past them (71 us)
+  const int64_t most = (16384 + parts - 1) / parts;
   if (rows > most) rows = most;
-  hipLaunchKernelGGL((group_norm_kernel<T, LPG, VPL>), dim3((unsigned)rows, (unsigned)parts), dim3(NORM_THREADS), 0,
-                     st, p);
+  const bool past = p.rows > (32 << 20) / ((int64_t)p.groups * p.width * (int)sizeof(T));
+  const dim3 grid((unsigned)rows, (unsigned)parts), block(NORM_THREADS);
+  if (past) hipLaunchKernelGGL((group_norm_kernel<T, LPG, VPL, true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((group_norm_kernel<T, LPG, VPL, false>), grid, block, 0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 

@@ -140,3 +140,17 @@ def test_part_of_the_rows(lo, hi):
         out = torch.ones(40, dtype=torch.bool)
         out[inside] = False
         assert torch.equal(y[out], x[out])
+
+
+@pytest.mark.parametrize("dt,rows,groups,width", [(torch.bfloat16, 16387, 8, 136), (torch.float32, 700, 3, 4104)])
+def test_outputs_beyond_the_caches(dt, rows, groups, width):
+    """More than 32 MiB of output, in place, with every row's neighbours at a stride."""
+    x = data(rows, groups, width, dt, 5, pad=8)
+    norm, whole = OutputNorm(None, torch.full((width,), 0.5, device="cuda"), act="none"), x.clone()
+    store = torch.full((rows, groups * width + 8), 3.0, device="cuda", dtype=dt)
+    y = store[:, :groups * width].unflatten(1, (groups, width))
+    y.copy_(x)
+    assert rows * groups * width * x.element_size() > 32 << 20
+    assert group_norm(y, norm, y) == 0
+    check(whole, y, norm, None)
+    assert (store[:, groups * width:] == 3).all()
