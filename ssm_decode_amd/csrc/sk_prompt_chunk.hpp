@@ -1,6 +1,7 @@
-// Prompts through the gated delta rule in chunks of 64 tokens.  With alpha_i, beta_i of a chunk's tokens, g_i the product of
-// the decays up to token i, D_ij the product of those after j up to i (so that
-// no quotient of decays occurs), and S_0 the state before the chunk:
+// Prompts through the gated delta rule in chunks of 64 tokens.  With alpha_i,
+// beta_i of a chunk's tokens, g_i the product of the decays up to token i, D_ij the
+// product of those after j up to i (so that no quotient of decays occurs), and S_0
+// the state before the chunk:
 //   A_ij = beta_i D_ij (k_i . k_j)  for j < i,       T = (I + A)^-1 diag(beta)
 //   P_ij = D_ij (q_i . k_j)         for j <= i
 //   R = V - diag(g) K S_0,   U = T R
@@ -16,7 +17,7 @@
 // six whose terms reach 2^-24 of it.  What only reaches the output, which is
 // rounded to bf16 at 2^-9, takes the first two values (2^-16).  The fp32 matrix
 // instructions have a sixteenth of the bf16 ones' rate; fp32 activations use
-// them throughout (K and Q would have to be split too, 9 products for 8).
+// them throughout, since K and Q would have to be split too.
 #pragma once
 
 #include "sk_serve_device.hpp"

@@ -8,8 +8,9 @@
 // nothing moves between K S, T R, P U and K^T U; the A operands are runs of
 // four columns from LDS (of K^T, single values: four rows of 16 in 64 banks).
 //
-// Bound by the matrix instructions: 2 (3 dk dv + 40 dv) 64 operations a chunk
-// beside the triangles, of 32 cycles for 2048.  K and T, P are in LDS twice, Q
+// Bound by the matrix instructions: 64 x 64, 272 a wave and chunk at 32 cycles, 4.0
+// of the 5.1 us that a chunk takes (45 us for 8; branches between the products and
+// outputs stored in their own chunk: 56).  K and T, P are in LDS twice, Q
 // once (its next copy starts when the chunk's outputs have it behind them), V
 // comes to registers a chunk ahead.
 #include <type_traits>
