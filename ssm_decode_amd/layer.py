@@ -186,6 +186,7 @@ class DecodeLayer:
         """Prompts (serving.Prompts) through the gated delta rule: their outputs
         (normalised, where the prompts have a norm), the sequences' new states
         and, with prompts.prime, their sketches."""
+        prompts.check(self)
         rc = _on_device(self.S.device.index, lambda st: abi.sketchssm_prefill(
             self._layer, self._bufs, prompts.struct, st), stream)
         if rc == 0 and prompts.norm is not None:

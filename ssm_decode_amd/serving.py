@@ -40,6 +40,10 @@ def _indices(name: str, x: torch.Tensor, n: Optional[int], device: torch.device)
         raise ValueError(f"{name}: {n} entries, got {x.numel()}")
 
 
+def _shape(layer: DecodeLayer) -> tuple:
+    return layer.family, layer.B, layer.H, layer.dk, layer.dv, layer.act, layer.S.device
+
+
 class Prompts:
     """Token rows of several prompts, one behind the other, for
     ``DecodeLayer.prefill``: q, k [tokens, H, dk], v, o [tokens, H, dv] in the
@@ -73,7 +77,12 @@ class Prompts:
                 _indices(name, x, n, dev)
         if norm_gate is not None:
             _rows("norm_gate", norm_gate, (N, H, layer.dv), at, dev)
+        if norm is not None:
+            norm.check((H, layer.dv), dev)
+        elif norm_gate is not None:
+            raise ValueError("norm_gate: without a norm")
         self.norm, self.norm_gate = norm, norm_gate
+        self.shape = _shape(layer)
         need = abi.sketchssm_prefill_workspace_bytes(layer.layer_struct, N, n)
         if need < 0:
             raise ValueError(f"prompts that this layer does not take (code {need})")
@@ -87,6 +96,11 @@ class Prompts:
     @property
     def struct(self) -> abi.sketchssm_prompts:
         return self._struct
+
+    def check(self, layer: DecodeLayer) -> None:
+        """Raises ValueError where these prompts are none of the layer's."""
+        if self.shape != _shape(layer):
+            raise ValueError(f"prompts of a layer {self.shape}, not {_shape(layer)}")
 
 
 class StateCache:
@@ -138,6 +152,12 @@ class OutputNorm:
         self.weight, self.bias, self.eps, self.act = weight, bias, float(eps), act
         self.centred, self.gate_first = bool(centred), bool(gate_first)
 
+    def check(self, shape, device: torch.device) -> None:
+        """Raises ValueError where weight or bias do not fit [groups, width] on the device."""
+        for name, t in (("weight", self.weight), ("bias", self.bias)):
+            if t is not None and ((t.shape != shape and t.shape != shape[1:]) or t.device != device):
+                raise ValueError(f"{name}: {tuple(shape)} or {tuple(shape[1:])} on {device}, got {tuple(t.shape)} on {t.device}")
+
 
 def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optional[torch.Tensor] = None,
                stream=None, rows: Optional[torch.Tensor] = None) -> int:
@@ -150,11 +170,8 @@ def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optiona
         raise ValueError("x: a bf16 or fp32 device tensor [rows, groups, width]")
     xs, ys = _rows("x", x, shape, dt, dev), _rows("y", y, shape, dt, dev)
     zs = _rows("gate", gate, shape, dt, dev) if gate is not None else 0
+    norm.check(shape[1:], dev)
     w = norm.weight if norm.weight is not None else norm.bias
-    if w is not None:
-        for name, t in (("weight", norm.weight), ("bias", norm.bias)):
-            if t is not None and ((t.shape != shape[1:] and t.shape != shape[2:]) or t.device != dev):
-                raise ValueError(f"{name}: {tuple(shape[1:])} or {tuple(shape[2:])} on {dev}, got {tuple(t.shape)} on {t.device}")
     first = end = None
     if rows is not None:
         _indices("rows", rows, None, dev)

@@ -235,9 +235,10 @@ def test_a_bad_list_of_tokens_is_refused_whole(starts, tokens, act):
 
 
 @pytest.mark.parametrize("starts", [[0, 100, 100, 100], [50, 60, 150, 170], [0, 0, 0, 200], [200, 200, 200, 200]])
-def test_lists_that_leave_tokens_out(starts):
-    lay = make_layer(3, 2, 64, 64, "bf16", seed=15)
-    tok = make_tokens(200, 2, 64, 64, "bf16", seed=16)
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_lists_that_leave_tokens_out(starts, act):
+    lay = make_layer(3, 2, 64, 64, act, seed=15)
+    tok = make_tokens(200, 2, 64, 64, act, seed=16)
     S0 = lay.S.clone()
     run(lay, tok, None, starts=starts)
     assert lay.error_word() == 0
@@ -245,12 +246,13 @@ def test_lists_that_leave_tokens_out(starts):
 
 
 @pytest.mark.parametrize("n,lens", [(70, "mixed"), (70, "long"), (200, "mixed")])
-def test_many_prompts(n, lens):
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_many_prompts(n, lens, act):
     """More prompts than a wave's lanes, short and long among them."""
     rng = np.random.default_rng(n)
     lens = (rng.choice([0, 1, 3, 16, 17, 40, 64, 130], n) if lens == "mixed" else rng.integers(60, 140, n)).tolist()
-    lay = make_layer(n, 2, 64, 64, "bf16", seed=70)
-    tok = make_tokens(sum(lens), 2, 64, 64, "bf16", seed=71)
+    lay = make_layer(n, 2, 64, 64, act, seed=70)
+    tok = make_tokens(sum(lens), 2, 64, 64, act, seed=71)
     S0 = lay.S.clone()
     seqs = rng.permutation(n).tolist()
     has = rng.integers(0, 2, n).tolist()
@@ -304,10 +306,11 @@ def test_few_long_prompts_refused_and_replayed():
         check(lay, S0, tok, lens, [0, 4500, 9100, 13500], [0, 1, 2], [1] * 3)
 
 
-def test_no_prompts_and_empty_prompts():
-    lay = make_layer(3, 2, 64, 64, "bf16", seed=17)
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_no_prompts_and_empty_prompts(act):
+    lay = make_layer(3, 2, 64, 64, act, seed=17)
     S0 = lay.S.clone()
-    tok = make_tokens(0, 2, 64, 64, "bf16")
+    tok = make_tokens(0, 2, 64, 64, act)
     run(lay, tok, [])
     assert torch.equal(lay.S, S0)
     run(lay, tok, [0, 0, 0], has=[1, 0, 1])
@@ -315,10 +318,11 @@ def test_no_prompts_and_empty_prompts():
     check(lay, S0, tok, [0, 0, 0], [0] * 4, [0, 1, 2], [1, 0, 1])
 
 
-def test_nan_stays_in_its_own_prompt_and_head():
-    lay = make_layer(3, 2, 64, 64, "bf16", seed=18)
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_nan_stays_in_its_own_prompt_and_head(act):
+    lay = make_layer(3, 2, 64, 64, act, seed=18)
     lens = [70, 80, 50]
-    tok = make_tokens(200, 2, 64, 64, "bf16", seed=19)
+    tok = make_tokens(200, 2, 64, 64, act, seed=19)
     tok[2][75, 1, 5] = float("nan")
     tok[2][76, 0, 7] = float("inf")
     run(lay, tok, lens)
@@ -329,17 +333,19 @@ def test_nan_stays_in_its_own_prompt_and_head():
     assert torch.isfinite(tok[5].float()[:70]).all() and torch.isfinite(tok[5].float()[150:]).all()
 
 
-def test_zero_state_ignores_what_the_buffer_held():
-    lay = make_layer(2, 2, 64, 64, "bf16", seed=20)
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_zero_state_ignores_what_the_buffer_held(act):
+    lay = make_layer(2, 2, 64, 64, act, seed=20)
     lay.S.fill_(float("nan"))
-    tok = make_tokens(150, 2, 64, 64, "bf16", seed=21)
+    tok = make_tokens(150, 2, 64, 64, act, seed=21)
     run(lay, tok, [100, 50], has=[0, 0])
     check(lay, torch.zeros_like(lay.S), tok, [100, 50], [0, 100, 150], [0, 1], [0, 0])
 
 
-def test_a_prompt_in_two_parts_equals_it_in_one():
-    a, b = make_layer(1, 2, 128, 128, "bf16", seed=22), make_layer(1, 2, 128, 128, "bf16", seed=22)
-    tok = make_tokens(300, 2, 128, 128, "bf16", seed=23)
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_a_prompt_in_two_parts_equals_it_in_one(act):
+    a, b = make_layer(1, 2, 128, 128, act, seed=22), make_layer(1, 2, 128, 128, act, seed=22)
+    tok = make_tokens(300, 2, 128, 128, act, seed=23)
     S0 = a.S.clone()
     run(a, tok, [300])
     o = torch.empty_like(tok[5])
@@ -349,13 +355,14 @@ def test_a_prompt_in_two_parts_equals_it_in_one():
     check(b, S0, tok[:5] + (o,), [300], [0, 300], [0], [1])
 
 
-def test_long_row_strides():
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_long_row_strides(act):
     """Rows so far apart that offsets pass 32 bits."""
     N, H, dk, dv = 70, 2, 64, 64
-    stride = 1 << 25                             # 70 rows: over 2^31 elements, 4.7 GB
-    lay = make_layer(1, H, dk, dv, "bf16", seed=24)
-    q, k, v, al, be, o = make_tokens(N, H, dk, dv, "bf16", seed=25)
-    far = torch.empty(N * stride, device="cuda", dtype=torch.bfloat16)
+    stride = 1 << 25                             # 70 rows: over 2^31 elements
+    lay = make_layer(1, H, dk, dv, act, seed=24)
+    q, k, v, al, be, o = make_tokens(N, H, dk, dv, act, seed=25)
+    far = torch.empty(N * stride, device="cuda", dtype=TORCH_DTYPE[act])
     at = lambda i, d: far.as_strided((N, H, d), (stride, d, 1), i * 1024)  # noqa: E731
     tok = []
     for i, (x, d) in enumerate(((q, dk), (k, dk), (v, dv), (o, dv))):
@@ -368,10 +375,11 @@ def test_long_row_strides():
     check(lay, S0, tok, [N], starts, [0], [1])
 
 
-def test_on_another_stream_and_twice_at_once():
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_on_another_stream_and_twice_at_once(act):
     """Two layers' prompts on two streams, each with its own workspace."""
-    lays = [make_layer(2, 3, 128, 128, "bf16", seed=26 + i) for i in range(2)]
-    toks = [make_tokens(400, 3, 128, 128, "bf16", seed=28 + i) for i in range(2)]
+    lays = [make_layer(2, 3, 128, 128, act, seed=26 + i) for i in range(2)]
+    toks = [make_tokens(400, 3, 128, 128, act, seed=28 + i) for i in range(2)]
     S0 = [x.S.clone() for x in lays]
     start = torch.tensor([0, 150, 400], dtype=torch.int32, device="cuda")
     pr = [Prompts(lay, *tok, start) for lay, tok in zip(lays, toks)]
@@ -385,9 +393,10 @@ def test_on_another_stream_and_twice_at_once():
         check(lays[i], S0[i], toks[i], [150, 250], [0, 150, 400], [0, 1], [1, 1])
 
 
-def test_same_call_twice_gives_the_same_bits():
-    lay = make_layer(4, 3, 128, 128, "bf16", seed=30)
-    tok = make_tokens(500, 3, 128, 128, "bf16", seed=31)
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_same_call_twice_gives_the_same_bits(act):
+    lay = make_layer(4, 3, 128, 128, act, seed=30)
+    tok = make_tokens(500, 3, 128, 128, act, seed=31)
     S0, outs = lay.S.clone(), []
     for _ in range(2):
         lay.S.copy_(S0)
@@ -398,12 +407,13 @@ def test_same_call_twice_gives_the_same_bits():
 
 
 @pytest.mark.parametrize("lens", [[3, 9], [100, 90]], ids=["short", "long"])
-def test_graph_replays(lens):
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_graph_replays(lens, act):
     """Captured once, replayed with other prompts in the same buffers and eager
     work between the replays."""
     N = sum(lens)
-    lay = make_layer(2, 2, 128, 128, "bf16", seed=32)
-    tok = make_tokens(N, 2, 128, 128, "bf16", seed=33)
+    lay = make_layer(2, 2, 128, 128, act, seed=32)
+    tok = make_tokens(N, 2, 128, 128, act, seed=33)
     starts = [0, lens[0], N]
     pr = Prompts(lay, *tok, torch.tensor(starts, dtype=torch.int32, device="cuda"))
     S0 = lay.S.clone()
@@ -413,7 +423,7 @@ def test_graph_replays(lens):
     with torch.cuda.graph(g):
         assert lay.prefill(pr) == 0
     for rep in range(4):
-        new = make_tokens(N, 2, 128, 128, "bf16", seed=40 + rep)
+        new = make_tokens(N, 2, 128, 128, act, seed=40 + rep)
         for dst, src in zip(tok, new):
             dst.copy_(src)
         lay.S.copy_(S0)
@@ -480,3 +490,31 @@ def test_short_and_long_prompts_together(dk, dv, act):
     _, starts = run(lay, tok, lens, seqs=seqs, has=[int(x) for x in has])
     assert lay.error_word() == 0
     check(lay, S0, tok, lens, starts, seqs, has)
+
+
+@pytest.mark.parametrize("act,n", [("bf16", 3), ("bf16", 100), ("f32", 3), ("f32", 100), ("bf16", 9000)])
+def test_the_last_of_very_many_states(act, n):
+    """States whose offsets pass 32 bits: of 2^17 + 8 sequences of one 128 x 128
+    head, the first and the last."""
+    B, dk, dv = (1 << 17) + 8, 128, 128
+    off = np.array([0, 3], dtype=np.int32)
+    lay = DecodeLayer("gdn", B, 1, 1, dk, dv, 1, act, act, off)
+    assert lay.S.numel() > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(95)
+    lay.Pt.copy_(torch.randn(lay.Pt.shape, generator=g, device="cuda") / dk ** 0.5)
+    lay.Cmap.copy_(lay.Pt)
+    ends = [0, B - 1]
+    for b in ends:
+        lay.S[b] = 0.1 * torch.randn(lay.S[b].shape, generator=g, device="cuda")
+    tok = make_tokens(2 * n, 1, dk, dv, act, seed=96, alpha=1 - 0.001 * torch.rand((2 * n, 1), generator=g, device="cuda"))
+    first = {b: f64(lay.S[b]) for b in ends}
+    _, starts = run(lay, tok, [n, n], seqs=ends)
+    assert lay.error_word() == 0
+    t64 = [f64(x) for x in tok]
+    for i, b in enumerate(ends):
+        sl = slice(i * n, (i + 1) * n)
+        o, S, top = ref.delta_rule(t64[0][sl, 0], t64[1][sl, 0], t64[2][sl, 0], t64[3][sl, 0], t64[4][sl, 0], first[b][0])
+        # as in check: (dk + 8) roundings of 2^-24 a token of the largest column norm
+        lim = n * (dk + 8) * EPS32 * top
+        assert np.abs(f64(lay.S[b, 0]) - S).max() <= lim
+    assert not lay.S[1:B - 1:4096].any()

@@ -226,3 +226,24 @@ def test_restored_sequence_decodes_on():
             o[h] = oo[0]
     got = st.o[1].double().cpu().numpy()
     assert np.linalg.norm(got - o) <= 1e-5 * np.linalg.norm(o)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_the_last_of_very_many_slots(bits):
+    """Codes whose offsets pass 32 bits (2^31 elements of 8 bits, 2^32 of 4)."""
+    H, dk, dv = 16, 128, 128
+    slots = (1 << (13 if bits == 8 else 14)) + 3
+    lay = DecodeLayer("gdn", 2, H, H, dk, dv, 2, "bf16", "bf16", np.arange(H + 1, dtype=np.int32) * 2)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    lay.S.copy_(torch.randn(lay.S.shape, generator=g, device="cuda"))
+    S0, cache = lay.S.clone(), StateCache(lay, slots, bits)
+    assert cache.codes.numel() > 1 << 31
+    dev = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    assert lay.save_state(cache, dev(0, 1), dev(slots - 1, 0)) == 0
+    assert lay.load_state(cache, dev(1, 0), dev(slots - 1, 0)) == 0
+    # half a step of each block's scale, and the product's rounding
+    step = S0.abs().unflatten(-1, (-1, 32)).amax(-1) / (127 if bits == 8 else 7)
+    for b in (0, 1):
+        err = (lay.S[b] - S0[1 - b]).abs().unflatten(-1, (-1, 32)).amax(-1)
+        assert (err <= 0.5001 * step[1 - b]).all()
+    assert not cache.codes[1:slots - 1:512].any() and lay.error_word() == 0

@@ -230,7 +230,7 @@ def test_norm_nothing_to_do():
 # -------------------------------------------------------------- Python layer
 class _Layer:
     """What Prompts and StateCache look at of a layer, on the CPU."""
-    act, B, H, dk, dv = "f32", 2, 4, 16, 32
+    family, act, B, H, dk, dv = "gdn", "f32", 2, 4, 16, 32
     S = torch.zeros(2, 4, 16, 32)
     layer_struct = gdn()
 
@@ -263,6 +263,27 @@ def test_prompts_take_strided_rows():
 def test_prompts_refuse_wrong_tensors(over):
     with pytest.raises(ValueError):
         Prompts(_Layer(), **_tokens(**over))
+
+
+def test_prompts_belong_to_layers_of_their_shape():
+    p = Prompts(_Layer(), **_tokens())
+    p.check(_Layer())
+    for name, value in (("H", 5), ("B", 3), ("dk", 64), ("dv", 64), ("act", "bf16"), ("family", "kda"),
+                        ("S", torch.zeros(1, device="meta"))):
+        other = type("Other", (_Layer,), {name: value})
+        with pytest.raises(ValueError):
+            p.check(other())
+
+
+def test_prompts_refuse_norms_that_do_not_fit():
+    z = torch.zeros(5, 4, 32)
+    Prompts(_Layer(), **_tokens(), norm=OutputNorm(torch.ones(4, 32)), norm_gate=z)
+    Prompts(_Layer(), **_tokens(), norm=OutputNorm(torch.ones(32)))
+    for kw in (dict(norm=OutputNorm(torch.ones(4, 16))), dict(norm=OutputNorm(None, torch.ones(5, 32))),
+               dict(norm=OutputNorm(torch.ones(32, device="meta"))), dict(norm_gate=z),
+               dict(norm=OutputNorm(), norm_gate=z[:4])):
+        with pytest.raises(ValueError):
+            Prompts(_Layer(), **_tokens(), **kw)
 
 
 def test_state_cache_refuses_wrong_entries():
