@@ -18,6 +18,11 @@ namespace {
 
 constexpr int QB = 32;                     // values that share a scale
 constexpr int SAVE_THREADS = 256;
+// Up to this many tiles are saved by several workgroups each.  Measured, a
+// workgroup a tile and split (us): 128 x 128 in 8 bits, 32 tiles 8.7 and 3.4, 512 14.4 and
+// 11.9, 1024 22.7 and 21.8, 2048 39.9 and 40.7, 4096 70 and 78; 64 x 64, 32 tiles 4.0
+// and 3.3, 2048 11.2 and 12.0.
+constexpr int kSplitSave = 1024;
 
 // round(x / s) to nearest even, exactly: a quotient from the reciprocal is
 // off by at most one, and its remainder, a multiple of the smaller operand's
@@ -40,11 +45,13 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
   return x > y ? x : y;
 }
 
-// One workgroup per (entry, head): a lane takes 8 consecutive values, so a
-// block is a quad of lanes and a wave reads 2 KiB in a row.
-template <int DK, int DV, int BITS>
+// One workgroup per (entry, head), or PARTS of them where there are few tiles: a
+// lane takes 8 consecutive values, so a block is a quad of lanes and a wave
+// reads 2 KiB in a row.
+template <int DK, int DV, int BITS, int PARTS>
 __global__ void __launch_bounds__(SAVE_THREADS) state_save_kernel(CacheParams p) {
-  constexpr int ITEMS = DK * DV / 8, U = (ITEMS + SAVE_THREADS - 1) / SAVE_THREADS;
+  constexpr int ALL = DK * DV / 8, ITEMS = ALL / PARTS, U = (ITEMS + SAVE_THREADS - 1) / SAVE_THREADS;
+  static_assert(ALL % PARTS == 0 && ITEMS % 4 == 0, "whole blocks");
   const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H, tid = threadIdx.x;
   const int b = p.seqs[i], slot = p.slot[i];
   int bad = 0;
@@ -55,10 +62,11 @@ __global__ void __launch_bounds__(SAVE_THREADS) state_save_kernel(CacheParams p)
     if (tid == 0) atomicOr(p.err, bad);
     return;
   }
-  const float* S = p.S + ((size_t)b * p.H + h) * DK * DV;
+  const int first = (int)blockIdx.y * ITEMS * 8;
+  const float* S = p.S + ((size_t)b * p.H + h) * DK * DV + first;
   const size_t tile = (size_t)slot * p.H + h;
-  float* scale = p.scale + tile * (DK * DV / QB);
-  char* codes = reinterpret_cast<char*>(p.codes) + tile * (DK * DV * BITS / 8);
+  float* scale = p.scale + tile * (DK * DV / QB) + first / QB;
+  char* codes = reinterpret_cast<char*>(p.codes) + tile * (DK * DV * BITS / 8) + first * BITS / 8;
   float x[U][8];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -163,13 +171,22 @@ __global__ void __launch_bounds__(DV * 2) state_load_kernel(CacheParams p) {
   if (tid == 0) p.count[(size_t)b * p.H + h] = 0;
 }
 
+template <int DK, int DV, int PARTS>
+void launch_save(const CacheParams& p, hipStream_t st) {
+  const dim3 grid(p.n * p.H, PARTS);
+  if (p.bits == 8)
+    hipLaunchKernelGGL((state_save_kernel<DK, DV, 8, PARTS>), grid, dim3(SAVE_THREADS), 0, st, p);
+  else
+    hipLaunchKernelGGL((state_save_kernel<DK, DV, 4, PARTS>), grid, dim3(SAVE_THREADS), 0, st, p);
+}
+
 template <int DK, int DV>
 int save_shape(const CacheParams& p, hipStream_t st) {
-  const dim3 grid(p.n * p.H);
-  if (p.bits == 8)
-    hipLaunchKernelGGL((state_save_kernel<DK, DV, 8>), grid, dim3(SAVE_THREADS), 0, st, p);
+  constexpr int PARTS = DK * DV >= 8 * SAVE_THREADS ? DK * DV / (8 * SAVE_THREADS) : 1;
+  if (p.n * p.H <= kSplitSave)
+    launch_save<DK, DV, PARTS>(p, st);
   else
-    hipLaunchKernelGGL((state_save_kernel<DK, DV, 4>), grid, dim3(SAVE_THREADS), 0, st, p);
+    launch_save<DK, DV, 1>(p, st);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 

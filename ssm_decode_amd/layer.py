@@ -204,7 +204,7 @@ class DecodeLayer:
         serving.StateCache (int32 device tensors)."""
         cache.check(self, seqs, slots)
         return _on_device(self.S.device.index, lambda st: abi.sketchssm_state_save(
-            self._layer, self._bufs, cache.struct, _ptr(seqs), _ptr(slots), seqs.numel(), st), stream)
+            self._layer, self._bufs, cache.struct, seqs.data_ptr(), slots.data_ptr(), seqs.numel(), st), stream)
 
     def load_state(self, cache, seqs, slots, prime: bool = True, stream=None) -> int:
         """Read slots of a serving.StateCache back into the states of sequences
@@ -212,7 +212,7 @@ class DecodeLayer:
         sketches."""
         cache.check(self, seqs, slots)
         return _on_device(self.S.device.index, lambda st: abi.sketchssm_state_load(
-            self._layer, self._bufs, cache.struct, _ptr(seqs), _ptr(slots), seqs.numel(), int(prime), st), stream)
+            self._layer, self._bufs, cache.struct, seqs.data_ptr(), slots.data_ptr(), seqs.numel(), int(prime), st), stream)
 
     def error_word(self) -> int:
         return int(self.err[0].item())

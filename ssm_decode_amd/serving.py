@@ -7,6 +7,7 @@ a kernel read what it must not; the work runs in the HIP library."""
 from __future__ import annotations
 
 import ctypes as C
+import math
 from typing import Optional
 
 import torch
@@ -23,8 +24,8 @@ def _rows(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: 
     stride) and gives the elements from one row to the next."""
     if x.shape != shape or x.dtype != dtype or x.device != device:
         raise ValueError(f"{name}: a {dtype} tensor of shape {tuple(shape)} on {device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
-    if x.is_contiguous() and shape[0] > 1:
-        return x.stride(0)
+    if x.is_contiguous():
+        return math.prod(shape[1:])
     strides, row = x.stride(), 1
     for d in range(len(shape) - 1, 0, -1):
         if strides[d] != row and shape[d] != 1:
@@ -154,9 +155,9 @@ class OutputNorm:
 
     def check(self, shape, device: torch.device) -> None:
         """Raises ValueError where weight or bias do not fit [groups, width] on the device."""
-        for name, t in (("weight", self.weight), ("bias", self.bias)):
-            if t is not None and ((t.shape != shape and t.shape != shape[1:]) or t.device != device):
-                raise ValueError(f"{name}: {tuple(shape)} or {tuple(shape[1:])} on {device}, got {tuple(t.shape)} on {t.device}")
+        for t in (self.weight, self.bias):
+            if t is not None and (t.shape != shape[2 - t.dim():] or t.device != device):
+                raise ValueError(f"weight and bias: {tuple(shape)} or {tuple(shape[1:])} on {device}, got {tuple(t.shape)} on {t.device}")
 
 
 def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optional[torch.Tensor] = None,
@@ -179,8 +180,9 @@ def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optiona
             raise ValueError("rows: the first row and the end")
         first = rows.data_ptr()
         end = first + 4 * (rows.numel() - 1)
-    w_at, b_at, z_at = (t.data_ptr() if t is not None else None for t in (norm.weight, norm.bias, gate))
-    st = abi.sketchssm_norm(x.data_ptr(), z_at, y.data_ptr(), w_at, b_at, xs, zs, ys,
+    st = abi.sketchssm_norm(x.data_ptr(), gate.data_ptr() if gate is not None else None, y.data_ptr(),
+                            norm.weight.data_ptr() if norm.weight is not None else None,
+                            norm.bias.data_ptr() if norm.bias is not None else None, xs, zs, ys,
                             shape[0], first, end, shape[1], shape[2], _DTYPES[dt], int(w is not None and w.dim() == 2),
                             int(norm.centred), ACT[norm.act], int(norm.gate_first), norm.eps)
     return _on_device(dev.index, lambda s: abi.sketchssm_group_norm(st, s), stream)
