@@ -42,7 +42,12 @@ struct Plan {
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   Plan p{};
   const int shrt = short_prompt(L);
-  if (!sk::prompt_chunked(L->dk) || tokens <= shrt || nseq == 0) return p;
+  if (!sk::prompt_chunked(L->dk) || nseq == 0) return p;
+  // No prompt is longer unless others are empty (a decode batch through this
+  // call): one launch for all, which takes a long prompt too (256 sequences of 32
+  // heads of 128 x 128, with the chunks' launches and without: a token each 209 and
+  // 195 us, 100 in one prompt 208 and 182, 200 in one 218 and 230).
+  if (tokens - nseq < shrt) return p;
   // mostly long prompts: the chunked form takes the short ones too, and one
   // launch is saved
   p.all = tokens > sk::PROMPT_CHUNK * nseq;

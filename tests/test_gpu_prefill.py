@@ -518,3 +518,18 @@ def test_the_last_of_very_many_states(act, n):
         lim = n * (dk + 8) * EPS32 * top
         assert np.abs(f64(lay.S[b, 0]) - S).max() <= lim
     assert not lay.S[1:B - 1:4096].any()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_a_long_prompt_among_empty_ones(dk, dv, act):
+    """As many tokens as prompts, as a decode batch has, but most in one prompt."""
+    n, lens = 150, [0] * 150
+    lens[3], lens[70], lens[149] = 1, 130, 2
+    lay = make_layer(n, 2, dk, dv, act, seed=97)
+    tok = make_tokens(n, 2, dk, dv, act, seed=98)      # (rows behind the last prompt's end)
+    S0 = lay.S.clone()
+    has = [i % 2 for i in range(n)]
+    _, starts = run(lay, tok, lens, has=has)
+    assert lay.error_word() == 0
+    check(lay, S0, tok, lens, starts, list(range(n)), has)

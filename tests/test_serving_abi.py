@@ -137,7 +137,8 @@ def test_prefill_workspace():
     # and one for every prompt, 30.5 KiB for each of its heads, and 0.5 KiB
     L = gdn(dk=64, dv=64, act=abi.SKSSM_BF16, sk=abi.SKSSM_BF16)
     assert abi.sketchssm_prefill_workspace_bytes(L, 48, 2) == 0
-    assert abi.sketchssm_prefill_workspace_bytes(L, 49, 2) == 1 * 4 * 31232 + 512      # one prompt of 49 at most
+    assert abi.sketchssm_prefill_workspace_bytes(L, 49, 2) == 0                        # 48 and 1
+    assert abi.sketchssm_prefill_workspace_bytes(L, 50, 2) == 1 * 4 * 31232 + 512      # one prompt of 49 at most
     # fp32: 20.5 KiB; dk = 128: more than 24 tokens (fp32: 32)
     F = gdn(dk=64, dv=64)
     assert abi.sketchssm_prefill_workspace_bytes(F, 48, 2) == 0
@@ -145,8 +146,8 @@ def test_prefill_workspace():
     assert abi.sketchssm_prefill_workspace_bytes(F, 1 << 17, 2) == (2048 + 2) * 4 * 20992 + 512
     for act, short in ((abi.SKSSM_BF16, 24), (abi.SKSSM_F32, 32)):
         G = gdn(dk=128, dv=64, act=act, sk=act)
-        assert abi.sketchssm_prefill_workspace_bytes(G, short, 2) == 0
-        assert abi.sketchssm_prefill_workspace_bytes(G, short + 1, 2) > 0
+        assert abi.sketchssm_prefill_workspace_bytes(G, short + 1, 2) == 0
+        assert abi.sketchssm_prefill_workspace_bytes(G, short + 2, 2) > 0
     assert abi.sketchssm_prefill_workspace_bytes(L, 128, 2) == 4 * 4 * 31232 + 512
     assert abi.sketchssm_prefill_workspace_bytes(L, 640, 2) == 12 * 4 * 31232 + 512
     # few tiles with many tokens: also a state and a transition (fp32) for each
