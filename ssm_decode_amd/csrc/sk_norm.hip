@@ -5,7 +5,7 @@
 //   y  = n * weight + bias, times act(z) where the gate comes after, or
 //        act(y) where there is no gate.
 // Bound by memory: x (and z) read once, y written once (16384 x 32 groups of 128
-// in bf16: 403 MB in 71 us, 5.7 TB/s).  A lane keeps its
+// in bf16, call behind call: 403 MB in 77 us, 5.2 TB/s).  A lane keeps its
 // 16-byte vectors of a group in registers, so the variance is that of the
 // held values about their mean (two passes over registers, one over memory),
 // and a thread keeps its channels' weights while it goes from row to row.
@@ -21,7 +21,12 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <typename T> struct Vec { static constexpr int N = 16 / (int)sizeof(T); };
 
-// 16 bytes as fp32 values, and back.
+// 16 bytes, past the caches' keeping or not; as fp32 values, and back.
+template <bool PAST>
+__device__ __forceinline__ u32x4 read16(const void* p) {
+  const u32x4* at = reinterpret_cast<const u32x4*>(p);
+  return PAST ? __builtin_nontemporal_load(at) : *at;
+}
 __device__ __forceinline__ void unpack(const u32x4& w, float (&x)[8]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -119,8 +124,8 @@ __global__ void __launch_bounds__(NORM_THREADS) group_norm_kernel(NormParams p) 
 #pragma unroll
       for (int e = 0; e < N; ++e) x[u][e] = z[u][e] = 0.f;
       if (c < nvec) {
-        unpack(*reinterpret_cast<const u32x4*>(X + row * p.xs + c * N), x[u]);
-        if (p.gate) unpack(*reinterpret_cast<const u32x4*>(Z + row * p.zs + c * N), z[u]);
+        unpack(read16<PAST>(X + row * p.xs + c * N), x[u]);
+        if (p.gate) unpack(read16<PAST>(Z + row * p.zs + c * N), z[u]);
       }
     }
     if (p.gate && p.gate_first) {
@@ -174,8 +179,9 @@ int launch(const NormParams& p, hipStream_t st) {
   const int64_t parts = tpr < NORM_THREADS ? 1 : (tpr + NORM_THREADS - 1) / NORM_THREADS;
   int64_t rows = (p.rows + rpw - 1) / rpw;
   // 64 workgroups for each of the 256 CUs, and further rows in turn (16384 x 32
-  // groups of 128, 403 MB: 16 a CU 87 us, 32 79, 64 76, one for every row 82); an
-  // output beyond the 32 MiB of the L2s is stored past them (71 us)
+  // groups of 128, 403 MB, traced: 16 a CU 87 us, 32 79, 64 76, one for every row
+  // 82).  Where the output is beyond the 32 MiB of the L2s, it is stored and the
+  // inputs are read past them (call behind call 81.7, 78.8 and 77.4 us).
   const int64_t most = (16384 + parts - 1) / parts;
   if (rows > most) rows = most;
   const bool past = p.rows > (32 << 20) / ((int64_t)p.groups * p.width * (int)sizeof(T));
