@@ -9,7 +9,7 @@
 //
 // Both directions are bound by memory: 4 bytes a value on the state's side,
 // bits / 8 + 1/8 on the cache's (128 sequences of 32 heads of 128 x 128 in 8 bits:
-// 344 MB in 71 us to the cache, 4.8 TB/s, and 352 MB in 59 us back, 6.0; 96 of 128
+// 344 MB in 67 us to the cache, 5.1 TB/s, and 352 MB in 58 us back, 6.0; 96 of 128
 // heads of 128 x 64 in 4 bits: 466 MB in 92 us and 479 MB in 78).
 #include "sk_serve_device.hpp"
 
@@ -19,21 +19,25 @@ namespace {
 constexpr int QB = 32;                     // values that share a scale
 constexpr int SAVE_THREADS = 256;
 // Up to this many tiles are saved by several workgroups each.  Measured, a
-// workgroup a tile and split (us): 128 x 128 in 8 bits, 32 tiles 8.7 and 3.4, 512 14.4 and
-// 11.9, 1024 22.7 and 21.8, 2048 39.9 and 40.7, 4096 70 and 78; 64 x 64, 32 tiles 4.0
-// and 3.3, 2048 11.2 and 12.0.
-constexpr int kSplitSave = 1024;
+// workgroup a tile and split (us): 128 x 128 in 8 bits, 32 tiles 5.7 and 3.4, 512
+// 11.4 and 11.2, 1024 19.5 and 20.8, 4096 65 and 76; 64 x 64, 32 tiles 3.6 and 3.2, 512
+// 4.5 and 4.3, 2048 9.9 and 11.2.
+constexpr int kSplitSave = 512;
 
-// round(x / s) to nearest even, exactly: a quotient from the reciprocal is
-// off by at most one, and its remainder, a multiple of the smaller operand's
-// unit that is at most about s, is exact in one fma.
-__device__ __forceinline__ int code_of(float x, float s, float inv) {
-  float c = rintf(x * inv);
+// 1.5 * 2^23: a sum with it is rounded to a whole number (to nearest even), which
+// is then the low bits of the sum.
+constexpr float WHOLE = 12582912.f;
+
+// round(x / s) to nearest even, exactly, as WHOLE + code, from c, the rounded
+// product with s's reciprocal: c is off by at most one, and its remainder, a
+// multiple of the smaller operand's unit that is at most about s, is exact in one
+// fma.
+__device__ __forceinline__ float exact_code(float x, float s, float c) {
   const float r = fmaf(-c, s, x), half = 0.5f * s;
   const bool odd = ((int)c & 1) != 0;
   if (r > half || (r == half && odd)) c += 1.f;
   else if (r < -half || (r == -half && odd)) c -= 1.f;
-  return (int)c;
+  return c + WHOLE;
 }
 
 // max over the four lanes of a quad, NaN-keeping (integer maximum of the
@@ -94,22 +98,35 @@ __global__ void __launch_bounds__(SAVE_THREADS) state_save_kernel(CacheParams p)
       const bool finite = m < 0x7f800000u, live = finite && amax >= 0x1p-100f;
       const float s = live ? amax / (BITS == 8 ? 127.f : 7.f) : (finite ? 0.f : __uint_as_float(0x7fc00000u));
       const float inv = live ? 1.f / s : 0.f;
-      int q[8];
+      // The product with the rounded reciprocal is off by at most 2^-24 of a
+      // quotient up to 127, 8e-6: a code is right where the product is no nearer
+      // than 2e-5 to a half.  The others (4e-5 of them) are put right with their
+      // wave's eight values.
+      uint32_t q[8];
+      float near = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = live ? code_of(x[u][e], s, inv) : 0;
+      for (int e = 0; e < 8; ++e) {
+        const float w = fmaf(x[u][e], inv, WHOLE);
+        near = fmaxf(near, fabsf(fmaf(x[u][e], inv, -(w - WHOLE))));
+        q[e] = __float_as_uint(w);
+      }
+      if (__any(near > 0.49998f)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (live) q[e] = __float_as_uint(exact_code(x[u][e], s, __uint_as_float(q[e]) - WHOLE));
+      }
       if constexpr (BITS == 8) {
-        uint2 w = make_uint2(0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w.x |= (uint32_t)(q[e] & 255) << (8 * e);
-          w.y |= (uint32_t)(q[4 + e] & 255) << (8 * e);
-        }
-        reinterpret_cast<uint2*>(codes)[c] = w;
+        auto four = [&](int e) {               // their low bytes
+          const uint32_t a = __builtin_amdgcn_perm(q[e + 1], q[e], 0x0c0c0400u);
+          const uint32_t b = __builtin_amdgcn_perm(q[e + 3], q[e + 2], 0x04000c0cu);
+          return live ? a | b : 0u;
+        };
+        reinterpret_cast<uint2*>(codes)[c] = make_uint2(four(0), four(4));
       } else {
         uint32_t w = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w |= (uint32_t)(q[e] & 15) << (4 * e);
-        reinterpret_cast<uint32_t*>(codes)[c] = w;
+        for (int e = 0; e < 8; ++e) w |= (q[e] & 15) << (4 * e);
+        reinterpret_cast<uint32_t*>(codes)[c] = live ? w : 0;
       }
       if ((tid & 3) == 0) scale[c >> 2] = s;
     }
