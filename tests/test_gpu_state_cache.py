@@ -247,3 +247,30 @@ def test_the_last_of_very_many_slots(bits):
         err = (lay.S[b] - S0[1 - b]).abs().unflatten(-1, (-1, 32)).amax(-1)
         assert (err <= 0.5001 * step[1 - b]).all()
     assert not cache.codes[1:slots - 1:512].any() and lay.error_word() == 0
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_many_sequences_at_once(bits, dk, dv):
+    """More tiles than are split over workgroups, values near the borders between
+    codes among them."""
+    B, H = 131, 5
+    lay = make_layer(B, H, dk, dv, "bf16", seed=dk + bits)
+    m = 127 if bits == 8 else 7
+    blocks = lay.S.unflatten(-1, (-1, 32))
+    top = blocks[..., :1].abs() + 1
+    g = torch.Generator(device="cuda").manual_seed(17)
+    odd = torch.randint(-m, m, blocks.shape, generator=g, device="cuda") + 0.5
+    near = (odd / m * top).clamp(-top, top)              # a half, or a rounding beside it
+    near = torch.nextafter(near, torch.randn(near.shape, generator=g, device="cuda") * 9)
+    blocks.copy_(torch.where(torch.rand(near.shape, generator=g, device="cuda") < 0.3, near, blocks.clamp(-top, top)))
+    blocks[..., :1] = top
+    cache = StateCache(lay, B, bits)
+    order = torch.randperm(B, generator=torch.Generator().manual_seed(3)).int().cuda()
+    assert lay.save_state(cache, order, torch.arange(B, dtype=torch.int32, device="cuda")) == 0
+    S, seqs = lay.S.cpu().numpy(), order.tolist()
+    codes, scales = codes_of(cache), cache.scale.cpu().numpy()
+    for slot, b in enumerate(seqs):
+        c, s = ref.quantise(S[b], bits)
+        assert np.array_equal(codes[slot], c) and np.array_equal(scales[slot], s)
+    assert lay.error_word() == 0
