@@ -5,7 +5,7 @@
 //   y  = n * weight + bias, times act(z) where the gate comes after, or
 //        act(y) where there is no gate.
 // Bound by memory: x (and z) read once, y written once (16384 x 32 groups of 128
-// in bf16, call behind call: 403 MB in 77 us, 5.2 TB/s).  A lane keeps its
+// in bf16, call behind call: 403 MB in 65.5 us, 6.1 TB/s).  A lane keeps its
 // 16-byte vectors of a group in registers, so the variance is that of the
 // held values about their mean (two passes over registers, one over memory),
 // and a thread keeps its channels' weights while it goes from row to row.
@@ -18,6 +18,7 @@ namespace {
 constexpr int NORM_THREADS = 256;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 template <typename T> struct Vec { static constexpr int N = 16 / (int)sizeof(T); };
 
@@ -41,7 +42,10 @@ __device__ __forceinline__ void unpack(const u32x4& w, float (&x)[4]) {
 __device__ __forceinline__ u32x4 pack(const float (&x)[8]) {
   u32x4 w;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = (uint32_t)f32_to_bf16(x[2 * e]) | ((uint32_t)f32_to_bf16(x[2 * e + 1]) << 16);
+  for (int e = 0; e < 4; ++e) {                  // (one instruction: to nearest even)
+    const bf16x2 v = {(__bf16)x[2 * e], (__bf16)x[2 * e + 1]};
+    w[e] = __builtin_bit_cast(uint32_t, v);
+  }
   return w;
 }
 __device__ __forceinline__ u32x4 pack(const float (&x)[4]) {
@@ -61,10 +65,12 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// act: 0 none, 1 SiLU, 2 sigmoid
+// act: 0 none, 1 SiLU, 2 sigmoid.  (The reciprocal instruction is off by at most
+// 2^-23, as the exponential is; an exact quotient is ten instructions more, which
+// beside the conversions kept the kernel from its memory's rate.)
 __device__ __forceinline__ float activation(float x, int act) {
   if (act == 0) return x;
-  const float s = 1.f / (1.f + __expf(-x));
+  const float s = __builtin_amdgcn_rcpf(1.f + __expf(-x));
   return act == 1 ? x * s : s;
 }
 
@@ -179,9 +185,9 @@ int launch(const NormParams& p, hipStream_t st) {
   const int64_t parts = tpr < NORM_THREADS ? 1 : (tpr + NORM_THREADS - 1) / NORM_THREADS;
   int64_t rows = (p.rows + rpw - 1) / rpw;
   // 64 workgroups for each of the 256 CUs, and further rows in turn (16384 x 32
-  // groups of 128, 403 MB, traced: 16 a CU 87 us, 32 79, 64 76, one for every row
-  // 82).  Where the output is beyond the 32 MiB of the L2s, it is stored and the
-  // inputs are read past them (call behind call 81.7, 78.8 and 77.4 us).
+  // groups of 128, 403 MB: 16 a CU 77.3 us, 32 70.6, 64 65.5, 128 67.8, one for
+  // every row 67.7).  Where the output is beyond the 32 MiB of the L2s, it is
+  // stored and the inputs are read past them (74.7 and 65.5 us).
   const int64_t most = (16384 + parts - 1) / parts;
   if (rows > most) rows = most;
   const bool past = p.rows > (32 << 20) / ((int64_t)p.groups * p.width * (int)sizeof(T));
