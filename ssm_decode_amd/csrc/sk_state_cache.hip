@@ -9,7 +9,7 @@
 //
 // Both directions are bound by memory: 4 bytes a value on the state's side,
 // bits / 8 + 1/8 on the cache's (128 sequences of 32 heads of 128 x 128 in 8 bits:
-// 344 MB in 67 us to the cache, 5.1 TB/s, and 352 MB in 58 us back, 6.0; 96 of 128
+// 344 MB in 66 us to the cache, 5.2 TB/s, and 352 MB in 58 us back, 6.0; 96 of 128
 // heads of 128 x 64 in 4 bits: 466 MB in 92 us and 479 MB in 78).
 #include "sk_serve_device.hpp"
 
@@ -19,9 +19,9 @@ namespace {
 constexpr int QB = 32;                     // values that share a scale
 constexpr int SAVE_THREADS = 256;
 // Up to this many tiles are saved by several workgroups each.  Measured, a
-// workgroup a tile and split (us): 128 x 128 in 8 bits, 32 tiles 5.7 and 3.4, 512
-// 11.4 and 11.2, 1024 19.5 and 20.8, 4096 65 and 76; 64 x 64, 32 tiles 3.6 and 3.2, 512
-// 4.5 and 4.3, 2048 9.9 and 11.2.
+// workgroup a tile and split (us): 128 x 128 in 8 bits, 32 tiles 5.4 and 3.3, 512
+// 10.9 and 10.3, 1024 18.4 and 19.1, 4096 64 and 69; 64 x 64, 32 tiles 3.4 and 3.1, 512
+// 4.5 and 4.2, 2048 9.8 and 10.3.
 constexpr int kSplitSave = 512;
 
 // 1.5 * 2^23: a sum with it is rounded to a whole number (to nearest even), which
@@ -58,24 +58,14 @@ __global__ void __launch_bounds__(SAVE_THREADS) state_save_kernel(CacheParams p)
   static_assert(ALL % PARTS == 0 && ITEMS % 4 == 0, "whole blocks");
   const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H, tid = threadIdx.x;
   const int b = p.seqs[i], slot = p.slot[i];
-  int bad = 0;
-  if (b < 0 || b >= p.B) bad = ERRBIT_SEQ;
-  else if (slot < 0 || slot >= p.slots || listed_before(p.slot, i, slot)) bad = ERRBIT_SLOT;
-  else if (p.count[(size_t)b * p.H + h] != 0) bad = ERRBIT_COUNT;
-  if (bad) {
-    if (tid == 0) atomicOr(p.err, bad);
-    return;
-  }
+  const bool in = b >= 0 && b < p.B;
   const int first = (int)blockIdx.y * ITEMS * 8;
   const float* S = p.S + ((size_t)b * p.H + h) * DK * DV + first;
-  const size_t tile = (size_t)slot * p.H + h;
-  float* scale = p.scale + tile * (DK * DV / QB) + first / QB;
-  char* codes = reinterpret_cast<char*>(p.codes) + tile * (DK * DV * BITS / 8) + first * BITS / 8;
-  float x[U][8];
+  float x[U][8];                             // (in flight over the checks)
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = tid + SAVE_THREADS * u;
-    if (ITEMS % SAVE_THREADS == 0 || c < ITEMS) {
+    if (in && (ITEMS % SAVE_THREADS == 0 || c < ITEMS)) {
       float a[4], d[4];
       ldn_nt<4>(S + 8 * c, a);
       ldn_nt<4>(S + 8 * c + 4, d);
@@ -83,6 +73,17 @@ __global__ void __launch_bounds__(SAVE_THREADS) state_save_kernel(CacheParams p)
       for (int e = 0; e < 4; ++e) { x[u][e] = a[e]; x[u][4 + e] = d[e]; }
     }
   }
+  int bad = 0;
+  if (!in) bad = ERRBIT_SEQ;
+  else if (slot < 0 || slot >= p.slots || listed_before(p.slot, i, slot)) bad = ERRBIT_SLOT;
+  else if (p.count[(size_t)b * p.H + h] != 0) bad = ERRBIT_COUNT;
+  if (bad) {
+    if (tid == 0) atomicOr(p.err, bad);
+    return;
+  }
+  const size_t tile = (size_t)slot * p.H + h;
+  float* scale = p.scale + tile * (DK * DV / QB) + first / QB;
+  char* codes = reinterpret_cast<char*>(p.codes) + tile * (DK * DV * BITS / 8) + first * BITS / 8;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = tid + SAVE_THREADS * u;
