@@ -9,23 +9,25 @@ namespace {
 
 // ------------------------------------------------------------ T and P
 // One workgroup of four waves per (chunk slot, head).  K K^T and Q K^T on the
-// matrix cores (bf16: exact products, fp32 sums; fp32: fp32 instructions, 64
-// columns of K and Q at a time); the unit triangular inverse by substitution in
-// 16 x 16 blocks, joined to 32 and 64 by fp32 products.  Alone a workgroup takes
-// 8.8 us, a chain of loads, products, inverse and joins; many at once are bound by
-// memory (8224 of 128 columns: 268 MB of K and Q in, 256 MB of T and P out, in 115 us).
+// matrix cores (bf16: exact products, fp32 sums; fp32: fp32 instructions); the unit
+// triangular inverse by substitution in 16 x 16 blocks, joined to 32 and 64 by
+// fp32 products.  Alone a workgroup takes about 8 us, a chain of loads, products,
+// inverse and joins, so what counts is how many a CU has at once: K and Q come in
+// stages, and A and P, which waits in registers, take the same place in LDS (8224 of
+// 128 columns, 268 MB of K and Q in, 256 MB of T and P out: three a CU 164 us, four,
+// with A and P apart, 115, six 92, 5.7 TB/s; six with 88 bytes of spills 159).
 constexpr int LS = PC + 4;                       // row stride of the fp32 matrices in LDS
 
 template <int DK, typename AT>
-__global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
+__global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kernel(PromptParams p) {
   constexpr bool F32 = sizeof(AT) == 4;
-  constexpr int KB = PC * (F32 ? 64 * 4 : DK * 2);     // bytes of K or Q in LDS
-  constexpr int MB = PC * LS * 4;                // bytes of A or P in LDS
-  constexpr int BIG = 2 * KB > 2 * MB ? 2 * KB : 2 * MB;
-  __shared__ __align__(16) unsigned char s_big[BIG];   // K and Q, then A (T in its place) and P
+  // K and Q come in stages of 128 bytes of a row (8 pieces), two ahead in registers
+  constexpr int PPR = 8, EPP = 16 / (int)sizeof(AT), STAGES = DK / (PPR * EPP), U = PC * PPR / 256;
+  constexpr int KB = PC * PPR * 16;              // bytes of a stage of K or Q in LDS
+  constexpr int MB = PC * LS * 4;                // bytes of A (T in its place), then P, over them
+  __shared__ __align__(16) unsigned char s_big[2 * KB > MB ? 2 * KB : MB];
   __shared__ __align__(16) float s_al[PC], s_be[PC], s_pre[PC], s_suf[PC], s_blk[4], s_mid[16], s_din[PC * 17];
   float* s_A = reinterpret_cast<float*>(s_big);
-  float* s_P = reinterpret_cast<float*>(s_big + MB);
 
   // (the last chunks first: what the next launch begins with is then the most
   // recent in the memory-side cache)
@@ -44,31 +46,39 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   const int nt = len - c0 < PC ? len - c0 : PC;
   const int64_t tok = (int64_t)s0 + c0;
 
-  // K and Q, rows of DK (or 64) with their 16-byte pieces swizzled, zeros behind nt
-  constexpr int PPR = F32 ? 16 : DK / 8, EPP = 16 / (int)sizeof(AT);
-  auto piece = [](int row, int pc) { return row * PPR + (pc ^ ((PPR == 16 ? row : row >> 1) & (PPR - 1))); };
+  // pieces swizzled, zeros behind nt
+  auto piece = [](int row, int pc) { return row * PPR + (pc ^ ((row >> 1) & (PPR - 1))); };
   u32x4* s_k = reinterpret_cast<u32x4*>(s_big);
   u32x4* s_q = reinterpret_cast<u32x4*>(s_big + KB);
   const AT* kp = reinterpret_cast<const AT*>(p.k) + tok * p.ks + (int64_t)h * DK;
   const AT* qp = reinterpret_cast<const AT*>(p.q) + tok * p.qs + (int64_t)h * DK;
-  auto stage = [&](int col) {
+  u32x4 rk[2][U], rq[2][U];
+  auto fetch = [&](int st) {
 #pragma unroll
-    for (int u = 0; u < PC * PPR / 256; ++u) {
-      const int c = tid + 256 * u, row = c / PPR, pc = c % PPR;
-      u32x4 a = u32x4{0, 0, 0, 0}, b = a;
+    for (int u = 0; u < U; ++u) {
+      const int c = tid + 256 * u, row = c / PPR, col = (st * PPR + c % PPR) * EPP;
+      rk[st & 1][u] = rq[st & 1][u] = u32x4{0, 0, 0, 0};
       if (row < nt) {
-        a = *reinterpret_cast<const u32x4*>(kp + row * p.ks + col + pc * EPP);
-        b = *reinterpret_cast<const u32x4*>(qp + row * p.qs + col + pc * EPP);
+        rk[st & 1][u] = *reinterpret_cast<const u32x4*>(kp + row * p.ks + col);
+        rq[st & 1][u] = *reinterpret_cast<const u32x4*>(qp + row * p.qs + col);
       }
-      s_k[piece(row, pc)] = a;
-      s_q[piece(row, pc)] = b;
     }
   };
-  stage(0);
+  auto stage = [&](int st) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = tid + 256 * u;
+      s_k[piece(c / PPR, c % PPR)] = rk[st & 1][u];
+      s_q[piece(c / PPR, c % PPR)] = rq[st & 1][u];
+    }
+  };
+  fetch(0);
+  if (STAGES > 1) fetch(1);
   if (tid < PC) {
     s_al[tid] = tid < nt ? p.gate[(tok + tid) * p.gs + h] : 1.f;
     s_be[tid] = tid < nt ? p.beta[(tok + tid) * p.bs + h] : 0.f;
   }
+  stage(0);
   __syncthreads();
 
   // decays: within blocks of 16 (D_ij for i, j of a block), from a block's
@@ -106,28 +116,19 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
     *tj = t - *ti * (*ti + 1) / 2;
   };
   int ti[3], tj[3];
-  float D[3][4], be[3][4];                              // D_ij and beta_i of the lane's results
 #pragma unroll
   for (int n = 0; n < 3; ++n) {
     tile_of(wv + 4 * n < 10 ? wv + 4 * n : 9, &ti[n], &tj[n]);
     ak[n] = aq[n] = f32x4s{0.f, 0.f, 0.f, 0.f};
-    const float across = s_mid[4 * ti[n] + tj[n]] * s_suf[16 * tj[n] + cg];
-    float pre[4];
-    ld4(s_pre + 16 * ti[n] + 4 * g, pre);
-    ld4(s_be + 16 * ti[n] + 4 * g, be[n]);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float in = s_din[(16 * ti[n] + 4 * g + r) * 17 + cg];
-      D[n][r] = ti[n] == tj[n] ? in : pre[r] * across;
-    }
   }
 #pragma unroll
-  for (int col = 0; col < DK; col += F32 ? 64 : DK) {
-    if (col > 0) {
+  for (int st = 0; st < STAGES; ++st) {
+    if (st > 0) {
       __syncthreads();
-      stage(col);
+      stage(st);
       __syncthreads();
     }
+    if (st + 2 < STAGES) fetch(st + 2);
 #pragma unroll
     for (int s = 0; s < PPR / 4; ++s) {
 #pragma unroll
@@ -148,7 +149,21 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
       }
     }
   }
-  __syncthreads();                                      // K and Q are read: A and P over them
+  __builtin_amdgcn_sched_barrier(0);
+  float D[3][4], be[3][4];                              // D_ij and beta_i of the lane's results
+#pragma unroll
+  for (int n = 0; n < 3; ++n) {
+    const float across = s_mid[4 * ti[n] + tj[n]] * s_suf[16 * tj[n] + cg];
+    float pre[4];
+    ld4(s_pre + 16 * ti[n] + 4 * g, pre);
+    ld4(s_be + 16 * ti[n] + 4 * g, be[n]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float in = s_din[(16 * ti[n] + 4 * g + r) * 17 + cg];
+      D[n][r] = ti[n] == tj[n] ? in : pre[r] * across;
+    }
+  }
+  __syncthreads();                                      // K and Q are read: A over them
 #pragma unroll
   for (int n = 0; n < 3; ++n) {
     if (wv + 4 * n < 10) {                              // uniform over the wave
@@ -159,7 +174,7 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
         // (selected, not multiplied by a zero: nothing above the diagonal may
         // reach the sums)
         s_A[ii * LS + j] = j < ii ? be[n][r] * D[n][r] * ak[n][r] : 0.f;
-        s_P[ii * LS + j] = j <= ii ? D[n][r] * aq[n][r] : 0.f;
+        aq[n][r] = j <= ii ? D[n][r] * aq[n][r] : 0.f;
       }
     }
   }
@@ -167,7 +182,6 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   for (int c = tid; c < 2 * 256; c += 256) {
     const int b = c >> 8, r = (c >> 4) & 15, cc = c & 15;
     s_A[(32 * b + r) * LS + 32 * b + 16 + cc] = 0.f;
-    s_P[(32 * b + r) * LS + 32 * b + 16 + cc] = 0.f;
   }
   __syncthreads();
 
@@ -242,43 +256,47 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(PromptParams p) {
   // fragments of T diag(beta) and P, and the row factors
   constexpr int WORK = F32 ? CHUNK_WORK_F32 : CHUNK_WORK_BYTES;
   unsigned char* W = reinterpret_cast<unsigned char*>(p.work) + ((size_t)slot * p.H + h) * WORK;
-  for (int c = tid; c < (F32 ? F32_TILES * 64 : 0); c += 256) {
-    const int ln = c & 63;
-    int rb, kb;
-    tile_of(c >> 6, &rb, &kb);
-    const int row = 16 * rb + (ln & 15), k = 16 * kb + 4 * (ln >> 4);
-    float t[4], v[4];
-    ld4(s_A + row * LS + k, t);
-    ld4(s_P + row * LS + k, v);
+  auto tiles = [&](unsigned char* to, bool beta) {      // fp32: four columns a lane
+    for (int c = tid; c < F32_TILES * 64; c += 256) {
+      const int ln = c & 63;
+      int rb, kb;
+      tile_of(c >> 6, &rb, &kb);
+      const int row = 16 * rb + (ln & 15), k = 16 * kb + 4 * (ln >> 4);
+      float t[4];
+      ld4(s_A + row * LS + k, t);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t[e] *= s_be[k + e];
-    stn<4>(reinterpret_cast<float*>(W + c * 16), t);
-    stn<4>(reinterpret_cast<float*>(W + F32_TILES * FRAG_BYTES + c * 16), v);
-  }
-  for (int c = tid; c < (F32 ? 0 : FRAGS * 64); c += 256) {
-    const int f = c >> 6, ln = c & 63, pair = f >> 1;
-    const int rb = pair > 0, kb = pair == 2;
-    const int row = 32 * rb + block_row(ln & 15, f & 1), k = 32 * kb + 8 * (ln >> 4);
-    float t[8], v[8], a4[4];
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      ld4(s_A + row * LS + k + e, a4);
-#pragma unroll
-      for (int d = 0; d < 4; ++d) t[e + d] = a4[d] * s_be[k + e + d];
-      ld4(s_P + row * LS + k + e, a4);
-#pragma unroll
-      for (int d = 0; d < 4; ++d) v[e + d] = a4[d];
+      for (int e = 0; e < 4; ++e) t[e] *= beta ? s_be[k + e] : 1.f;
+      stn<4>(reinterpret_cast<float*>(to + c * 16), t);
     }
-    bf16x8 ts[3], ps[2];
-    split8<3>(t, ts);
-    split8<2>(v, ps);
+  };
+  auto frags = [&](unsigned char* to, auto terms, bool beta) {      // bf16: eight, split
+    constexpr int TERMS = decltype(terms)::value;
+    for (int c = tid; c < FRAGS * 64; c += 256) {
+      const int f = c >> 6, ln = c & 63, pair = f >> 1;
+      const int rb = pair > 0, kb = pair == 2;
+      const int row = 32 * rb + block_row(ln & 15, f & 1), k = 32 * kb + 8 * (ln >> 4);
+      float t[8];
+      ldn<8>(s_A + row * LS + k, t);
 #pragma unroll
-    for (int n = 0; n < 3; ++n)
-      *reinterpret_cast<bf16x8*>(W + (f * 3 + n) * FRAG_BYTES + ln * 16) = ts[n];
+      for (int e = 0; e < 8; ++e) t[e] *= beta ? s_be[k + e] : 1.f;
+      bf16x8 v[TERMS];
+      split8<TERMS>(t, v);
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-      *reinterpret_cast<bf16x8*>(W + T_BYTES + (f * 2 + n) * FRAG_BYTES + ln * 16) = ps[n];
-  }
+      for (int n = 0; n < TERMS; ++n) *reinterpret_cast<bf16x8*>(to + (f * TERMS + n) * FRAG_BYTES + ln * 16) = v[n];
+    }
+  };
+  if constexpr (F32) tiles(W, true);
+  else frags(W, std::integral_constant<int, 3>{}, true);
+  __syncthreads();                                      // T is read: P over it (what is above stays 0)
+#pragma unroll
+  for (int n = 0; n < 3; ++n)
+    if (wv + 4 * n < 10) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s_A[(16 * ti[n] + 4 * g + r) * LS + 16 * tj[n] + cg] = aq[n][r];
+    }
+  __syncthreads();
+  if constexpr (F32) tiles(W + F32_TILES * FRAG_BYTES, false);
+  else frags(W + T_BYTES, std::integral_constant<int, 2>{}, false);
   if (tid < PC) {
     const int b = tid >> 4;
     float pre = s_pre[tid], suf = s_suf[tid];
@@ -323,7 +341,7 @@ __device__ __forceinline__ void copy16x4(const void* base, uint32_t offset, uint
       "global_load_lds_dwordx4 %0, %1 offset:0x800\n\t"
       "global_load_lds_dwordx4 %0, %1 offset:0xc00" ::"v"(offset),
       "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
-      : "memory", "m0");
+      : "memory");
 }
 // Within each 16 lanes, lane i gives the address of four values: 4 rows (i / 4)
 // of 16 (4 (i % 4) ..); it receives column i of the four rows.
