@@ -819,19 +819,21 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 }
 
 // The states between a prompt's segments: S behind segment g is M_g S + B_g,
-// written over B_g.  One workgroup of four waves per (prompt, head, 64
-// columns), a wave per 16 (a SIMD each: the fp32 products bound a step, 64 x
-// 128 x 128 of them 4 us), in fp32 throughout: a tile of S (rows 4 hi + r of column n) is the B operand
-// of v_mfma_f32_16x16x4_f32 with K-step r over rows {4 k + r}, so M is read as
-// runs of four columns (from LDS, one segment ahead, its pieces swizzled by
-// row) and the state never leaves its registers.
+// written over B_g.  One workgroup of four waves per (prompt, head, 32 columns), a
+// wave per 16 columns and half of the rows (the fp32 products bound a step: 64 x 128
+// x 16 of them a wave 1.9 us; all rows in a wave and 64 columns a workgroup took 6.4 us
+// a step), in fp32 throughout: a tile of S (rows 4 hi + r of column n) is the B
+// operand of v_mfma_f32_16x16x4_f32 with K-step r over rows {4 k + r}, so M is read as
+// runs of four columns (from LDS, one segment ahead, its pieces swizzled by row),
+// the state stays in registers, and the halves are exchanged as they are.
 template <int DK, int DV>
 __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams p) {
-  constexpr int TB = DK / 16, SEG_FLOATS = DK * (DV + DK), PPR = DK / 4, NW = 4, RUNS = DK * DK * 4 / 1024 / NW;
-  extern __shared__ __align__(1024) unsigned char smem[];
+  constexpr int TB = DK / 16, HB = TB / 2, SEG_FLOATS = DK * (DV + DK), PPR = DK / 4, NW = 4, RUNS = DK * DK * 4 / 1024 / NW;
+  extern __shared__ __align__(1024) unsigned char smem[];      // M twice, then the halves of S
   const int tile = blockIdx.x % (p.nchunked * p.H), x = tile / p.H, h = tile - x * p.H;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hi = lane >> 4;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), c0 = blockIdx.x / (p.nchunked * p.H) * 64 + wv * 16;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), cw = wv & 1, half = (wv >> 1) * HB;
+  const int c0 = blockIdx.x / (p.nchunked * p.H) * 32 + cw * 16;
   int rank = 0;
   const int i = chunked_prompt(p, x, &rank);
   if (i < 0) return;
@@ -841,6 +843,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams p) {
   float* seg = p.seg + ((size_t)first_slot(s0, rank, p.seg_shift) * p.H + h) * SEG_FLOATS;
   const size_t step = (size_t)p.H * SEG_FLOATS;
   const uint32_t lds0 = lds_address(smem);
+  f32x4s* s_x = reinterpret_cast<f32x4s*>(smem + 2 * DK * DK * 4) + cw * TB * 64 + lane;
   auto copy = [&](int g) {                       // M_g into its buffer
 #pragma unroll
     for (int u = 0; u < RUNS; ++u) {
@@ -849,25 +852,29 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams p) {
              lds0 + (g & 1) * DK * DK * 4 + (u * NW + wv) * 1024);
     }
   };
-  f32x4s S[TB], N[TB];
-  auto block = [&](const float* B, f32x4s (&v)[TB]) {
+  f32x4s S[TB], N[HB];
+  auto tile_at = [&](const float* B, int tb) {
+    f32x4s v;
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[tb][r] = B[(size_t)(16 * tb + 4 * hi + r) * DV + c0 + n];
+    for (int r = 0; r < 4; ++r) v[r] = B[(size_t)(16 * tb + 4 * hi + r) * DV + c0 + n];
+    return v;
   };
   copy(1);
-  block(seg, S);
-  block(seg + step, N);
+#pragma unroll
+  for (int tb = 0; tb < TB; ++tb) S[tb] = tile_at(seg, tb);
+#pragma unroll
+  for (int tb = 0; tb < HB; ++tb) N[tb] = tile_at(seg + step, half + tb);
   for (int g = 1; g + 1 < segs; ++g) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int tb = 0; tb < HB; ++tb) asm volatile("" : "+v"(N[tb]));      // (or its wait would be for the copies too)
     __syncthreads();
     if (g + 2 < segs) copy(g + 1);
-    const float* Mg = reinterpret_cast<const float*>(smem + (g & 1) * DK * DK * 4);
+    const float* Mg = reinterpret_cast<const float*>(smem + (g & 1) * DK * DK * 4) + half * 16 * DK;
 #pragma unroll
     for (int kb = 0; kb < TB; ++kb)
 #pragma unroll
-      for (int tb = 0; tb < TB; ++tb) {
+      for (int tb = 0; tb < HB; ++tb) {
         float a[4];
         ld4(Mg + ((16 * tb + n) * PPR + ((4 * kb + hi) ^ n)) * 4, a);
 #pragma unroll
@@ -875,12 +882,18 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptParams p) {
       }
     float* B = seg + g * step;
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb) {
-      S[tb] = N[tb];
+    for (int tb = 0; tb < HB; ++tb) {
+      s_x[(half + tb) * 64] = N[tb];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) B[(size_t)(16 * tb + 4 * hi + r) * DV + c0 + n] = S[tb][r];
+      for (int r = 0; r < 4; ++r) B[(size_t)(16 * (half + tb) + 4 * hi + r) * DV + c0 + n] = N[tb][r];
     }
-    if (g + 2 < segs) block(B + step, N);
+    if (g + 2 < segs) {
+#pragma unroll
+      for (int tb = 0; tb < HB; ++tb) N[tb] = tile_at(B + step, half + tb);
+      __syncthreads();
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) S[tb] = s_x[tb * 64];
+    }
   }
 }
 
@@ -903,8 +916,8 @@ int launch(int act, const PromptParams& p, hipStream_t st) {
   hipLaunchKernelGGL((prompt_prep_kernel<DK, bf16>), prep, dim3(256), 0, st, p);
   if (p.seg_shift) {
     launch_chunks<DK, DV, NW, false>(p, st);
-    hipLaunchKernelGGL((prompt_join_kernel<DK, DV>), dim3((unsigned)p.nchunked * p.H * (DV / 64)), dim3(256),
-                       2 * DK * DK * 4, st, p);
+    hipLaunchKernelGGL((prompt_join_kernel<DK, DV>), dim3((unsigned)p.nchunked * p.H * (DV / 32)), dim3(256),
+                       2 * DK * DK * 4 + 2 * DK * 64, st, p);
     launch_chunks<DK, DV, NW, true>(p, st);
   } else if (p.nchunked * p.H <= 128) {
     // .. unless that leaves CUs idle (128 x 128, 2048 tokens each, with four and
