@@ -25,11 +25,13 @@ constexpr int64_t kMaxTiles = (1 << 22) - 1;
 int short_prompt(const sketchssm_layer* L) { return L->dk == 64 ? 48 : L->act_dtype == SKSSM_F32 ? 32 : 24; }
 // Prompts in segments: up to kSplitTiles (prompt, head) tiles, at least kMinSegs
 // segments of 2^kMinSegShift tokens or more to a prompt on average, at most
-// kMaxSegs (the states between them are joined in order, about 6 us each) and
-// kSegTiles of all tiles (the CUs).  Measured on 128 x 128 tiles, whole and in
-// segments: 32 tiles of 16384 tokens 841 and 686 us, 8 of 12000 512 and 214;
-// what stays whole: 32 of 2048 tokens 112 and 156, 64 of 8192 530 and 606.
-constexpr int kSplitTiles = 48, kSegTiles = 256, kMinSegShift = 10, kMinSegs = 4, kMaxSegs = 12;
+// kMaxSegs (the states between them are joined in order, 4 us each) and kSegTiles
+// of all tiles (the CUs).  Measured on 128 x 128 tiles, whole and in segments (us): 8
+// tiles of 2048 tokens 100 and 94, of 4096 185 and 112, of 12000 505 and 205; 32 of
+// 2048 112 and 112, of 16384 815 and 574; 4 of 32768 1322 and 265 (in at most 24, 319);
+// what stays whole: 8 of 1600 in three 82 and 88; 48 of 4096 221 and 253; 64 of 16384
+// 953 and 1035.
+constexpr int kSplitTiles = 32, kSegTiles = 256, kMinSegShift = 9, kMinSegs = 4, kMaxSegs = 48;
 
 // How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
 // none), all of them or those of more than short_prompt tokens; in segments of

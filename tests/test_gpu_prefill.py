@@ -262,10 +262,10 @@ def test_many_prompts(n, lens, act):
 
 
 @pytest.mark.parametrize("dk,dv", SHAPES[1:])
-@pytest.mark.parametrize("lens", [[4096], [4097], [5000, 0, 7300], [12300, 5, 1], [1024, 1025, 10300], [1, 8200], [2048] * 4 + [12300]],
+@pytest.mark.parametrize("lens", [[4096], [4097], [5000, 0, 7300], [12300, 5, 1], [1024, 1025, 10300], [1, 8200], [2048] * 4 + [12300], [2048], [2049], [511, 512, 513, 6700]],
                          ids=lambda x: "-".join(map(str, x)))
 def test_few_long_prompts(dk, dv, lens):
-    """Few tiles with many tokens: prompts in segments (of 1024 tokens here), the
+    """Few tiles with many tokens: prompts in segments (of 512 tokens here), the
     first from its state and from zero, prompts of one segment among them."""
     H, n = 1, len(lens)
     lay = make_layer(n + 1, H, dk, dv, "bf16", seed=80, ranks=[5])

@@ -151,12 +151,12 @@ def test_prefill_workspace():
     assert abi.sketchssm_prefill_workspace_bytes(L, 128, 2) == 4 * 4 * 31232 + 512
     assert abi.sketchssm_prefill_workspace_bytes(L, 640, 2) == 12 * 4 * 31232 + 512
     # few tiles with many tokens: also a state and a transition (fp32) for each
-    # slot of 1024 tokens or more and head, at most 12 to a prompt on average
+    # slot of 512 tokens or more and head, at most 48 to a prompt on average
     need = lambda t, n, shift: -(-((t // 64 + n) * 4 * 31232 + 512) // 256) * 256 + ((t >> shift) + n) * 4 * 64 * 128 * 4  # noqa: E731
-    assert abi.sketchssm_prefill_workspace_bytes(L, 8191, 2) == (127 + 2) * 4 * 31232 + 512
-    assert abi.sketchssm_prefill_workspace_bytes(L, 8192, 2) == need(8192, 2, 10)
-    assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 17, 2) == need(1 << 17, 2, 13)
-    assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 25, 2) == need(1 << 25, 2, 21)
+    assert abi.sketchssm_prefill_workspace_bytes(L, 4095, 2) == (63 + 2) * 4 * 31232 + 512
+    assert abi.sketchssm_prefill_workspace_bytes(L, 4096, 2) == need(4096, 2, 9)
+    assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 17, 2) == need(1 << 17, 2, 11)
+    assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 25, 2) == need(1 << 25, 2, 19)
     # at most 2^22 - 1 chunks of heads, prompts of heads, or entries of heads
     assert abi.sketchssm_prefill_workspace_bytes(L, 1 << 26, 2) == abi.SKSSM_EDIM
     assert abi.sketchssm_prefill_workspace_bytes(gdn(batch=1 << 20), 1 << 20, 1 << 20) == abi.SKSSM_EDIM
