@@ -46,9 +46,10 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   const int shrt = short_prompt(L);
   if (!sk::prompt_chunked(L->dk) || nseq == 0) return p;
   // No prompt is longer unless others are empty (a decode batch through this
-  // call): one launch for all, which takes a long prompt too (256 sequences of 32
-  // heads of 128 x 128, with the chunks' launches and without: a token each 209 and
-  // 195 us, 100 in one prompt 208 and 182, 200 in one 218 and 230).
+  // call): one launch for all, which takes a long prompt too (32 heads of 128 x
+  // 128, with the chunks' launches and without: 256 sequences, a token each, 209 and
+  // 195 us, 100 in one prompt 208 and 182, 200 in one 218 and 230; 48 sequences 50
+  // and 43; 1024 780 and 750, 1018 tokens in one prompt 807 and 1044).
   if (tokens - nseq < shrt) return p;
   // mostly long prompts: the chunked form takes the short ones too, and one
   // launch is saved
