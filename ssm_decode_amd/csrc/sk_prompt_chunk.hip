@@ -269,24 +269,30 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
       stn<4>(reinterpret_cast<float*>(to + c * 16), t);
     }
   };
-  auto frags = [&](unsigned char* to, auto terms, bool beta) {      // bf16: eight, split
-    constexpr int TERMS = decltype(terms)::value;
+  auto frags = [&](unsigned char* to, bool is_t) {      // bf16: eight columns a lane, of T split
     for (int c = tid; c < FRAGS * 64; c += 256) {
       const int f = c >> 6, ln = c & 63, pair = f >> 1;
       const int rb = pair > 0, kb = pair == 2;
       const int row = 32 * rb + block_row(ln & 15, f & 1), k = 32 * kb + 8 * (ln >> 4);
       float t[8];
       ldn<8>(s_A + row * LS + k, t);
+      if (is_t) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] *= beta ? s_be[k + e] : 1.f;
-      bf16x8 v[TERMS];
-      split8<TERMS>(t, v);
+        for (int e = 0; e < 8; ++e) t[e] *= s_be[k + e];
+        bf16x8 v[3];
+        split8(t, v);
 #pragma unroll
-      for (int n = 0; n < TERMS; ++n) *reinterpret_cast<bf16x8*>(to + (f * TERMS + n) * FRAG_BYTES + ln * 16) = v[n];
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(to + (f * 3 + n) * FRAG_BYTES + ln * 16) = v[n];
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          *reinterpret_cast<f32x4s*>(to + (f * 2 + n) * FRAG_BYTES + ln * 16) =
+              f32x4s{t[4 * n], t[4 * n + 1], t[4 * n + 2], t[4 * n + 3]};
+      }
     }
   };
   if constexpr (F32) tiles(W, true);
-  else frags(W, std::integral_constant<int, 3>{}, true);
+  else frags(W, true);
   __syncthreads();                                      // T is read: P over it (what is above stays 0)
 #pragma unroll
   for (int n = 0; n < 3; ++n)
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
     }
   __syncthreads();
   if constexpr (F32) tiles(W + F32_TILES * FRAG_BYTES, false);
-  else frags(W + T_BYTES, std::integral_constant<int, 2>{}, false);
+  else frags(W + T_BYTES, false);
   if (tid < PC) {
     const int b = tid >> 4;
     float pre = s_pre[tid], suf = s_suf[tid];
@@ -499,8 +505,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     return join(read_tr(s + piece(tok, d >> 3) * 16), read_tr(s + piece(tok + 4, d >> 3) * 16));
   };
   auto frag_t = [&](int f, int v) { return as_frag(reinterpret_cast<const u32x4*>(sb + L::W)[(f * 3 + v) * 64 + lane]); };
-  auto frag_p = [&](int f, int v) {
-    return as_frag(reinterpret_cast<const u32x4*>(sb + L::W + T_BYTES)[(f * 2 + v) * 64 + lane]);
+  auto frag_p = [&](int f, int v) {              // columns 4 v .. of the lane's eight
+    return reinterpret_cast<const f32x4s*>(sb + L::W + T_BYTES)[(f * 2 + v) * 64 + lane];
   };
   typedef f32x4s Block[2];                       // 32 rows x 16 columns
   auto rows8 = [](const f32x4s (&a)[2], float (&x)[8]) {
@@ -563,7 +569,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
   {
     float x[8];
     rows8(S[0], x);
-    split8<3>(x, ss[0]);
+    split8(x, ss[0]);
   }
   int t0 = 0, buf = 0;
   // one chunk; `more`: a whole one follows (no branch may then stand between
@@ -588,7 +594,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
       }
     };
 
-    bf16x8 fa[2][2][2], ft[2][2][2][3], fp[2][2][2][2], fs[2][DB][2], vv[2];
+    bf16x8 fa[2][2][2], ft[2][2][2][3], fs[2][DB][2], vv[2];
+    f32x4s fp[2][2][2][2];
     float gm[2][8], dm[2][8];
     auto load_kq = [&](int at, int j) {
 #pragma unroll
@@ -619,7 +626,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
         load_kq(L::K, j + 1);
         float x[8];
         rows8(S[j + 1], x);
-        split8<3>(x, ss[j + 1]);
+        split8(x, ss[j + 1]);
       } else if (OUT) {
         load_kq(L::Q, DB);                       // (block 0 of Q, into the buffer that follows)
       }
@@ -657,16 +664,16 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
         const float v = !OUT && unit ? 0.f : (float)vv[rb][e];
         x[e] = v - gm[rb][e] * R[rb][e >> 2][e & 3];
       }
-      split8<3>(x, br[rb]);
+      split8(x, br[rb]);
     };
-    // O = Q S (two values);  R = V - g (K S) and its split meanwhile
+    // O = Q S (three values);  R = V - g (K S) and its split meanwhile
 #pragma unroll
     for (int j = 0; j < DB; ++j) {
       if constexpr (OUT) {
         if (j + 1 < DB) load_kq(L::Q, DB + j + 1);
         else load_t(0);
 #pragma unroll
-        for (int v = 1; v >= 0; --v)
+        for (int v = 2; v >= 0; --v)
 #pragma unroll
           for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
@@ -677,17 +684,16 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll
       for (int rb = 0; rb < 2; ++rb)
         if (j == (rb + 1) * DB / 4) split_r(rb);
-      if constexpr (OUT) region<8, 2, 8>();
+      if constexpr (OUT) region<12, 2, 5>();
       copies(2 * DB + j, 2 * DB + j + 1);
     }
-    bf16x8 bu[2][3], bo[2][2];
+    bf16x8 bu[2][3];
     auto split_u = [&](int kb) {
       float x[8];
       rows8(U[kb], x);
-      if (OUT) split8<2>(x, bo[kb]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] *= dm[kb][e];
-      split8<3>(x, bu[kb]);
+      split8(x, bu[kb]);
     };
     auto load_ps = [&](int kb) {
 #pragma unroll
@@ -731,21 +737,13 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
         copies(3 * DB + 2, 3 * DB + 3);
       }
     }
-    // O += P U;  S += K^T (D_C U)
+    // S += K^T (D_C U);  O += P U (fp32 instructions)
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       if (kb == 0) {
         load_ps(1);
         split_u(1);
       }
-      constexpr int PA[3] = {0, 1, 0}, PB[3] = {1, 0, 0};
-#pragma unroll
-      for (int v = 0; v < 3; ++v)
-#pragma unroll
-        for (int rb = kb; rb < 2; ++rb)
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (OUT) O[rb][t] = mm32(fp[kb][rb][t][PA[v]], bo[kb][PB[v]], O[rb][t]);
 #pragma unroll
       for (int d0 = 0; d0 < DB; d0 += 2)         // (two blocks at a time: the first are done early)
 #pragma unroll
@@ -754,8 +752,15 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
           for (int db = d0; db < d0 + 2; ++db)
 #pragma unroll
             for (int t = 0; t < 2; ++t) S[db][t] = mm32(fs[kb][db][t], bu[kb][v], S[db][t]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int rb = kb; rb < 2; ++rb)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (OUT) O[rb][t] = mm4(fp[kb][rb][t][e >> 2][e & 3], U[kb][e >> 2][e & 3], O[rb][t]);
       if (kb == 0) {
-        region<(OUT ? 12 : 0) + 6 * DB, 1, 3>();
+        region<(OUT ? 32 : 0) + 6 * DB, 1, 3>();
         copies(3 * DB + 3, UNITS);
       }
     }
@@ -769,8 +774,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     }
     float x[8];
     rows8(S[0], x);
-    split8<3>(x, ss[0]);
-    region<(OUT ? 6 : 0) + 6 * DB, 0, 3>();
+    split8(x, ss[0]);
+    region<(OUT ? 16 : 0) + 6 * DB, 0, 3>();
     t0 += PC;
     buf ^= 1;
   };

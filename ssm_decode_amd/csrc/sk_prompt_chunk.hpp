@@ -10,14 +10,16 @@
 // every prompt and head at once; a second goes through each prompt's chunks in
 // order.
 //
-// Precision.  The state is fp32, and so must be what is added to it.  Products
-// run on the bf16 matrix cores with each fp32 operand as an exact sum of three
-// bf16 values (its top 8 bits, the next 8, the last 8): a product with bf16
-// data (K, K^T) takes three instructions, one of two fp32 operands (T R) the
-// six whose terms reach 2^-24 of it.  What only reaches the output, which is
-// rounded to bf16 at 2^-9, takes the first two values (2^-16).  The fp32 matrix
-// instructions have a sixteenth of the bf16 ones' rate; fp32 activations use
-// them throughout, since K and Q would have to be split too.
+// Precision.  The state is fp32, and so is every product.  They run on the bf16
+// matrix cores with each fp32 operand as an exact sum of three bf16 values (its
+// top 8 bits, the next 8, the last 8): a product with bf16 data (K, Q, K^T)
+// takes three instructions, one of two fp32 operands (T R) the six whose terms
+// reach 2^-24 of it.  P U, which only the outputs wait for, takes the fp32
+// instructions, a sixteenth of the bf16 ones' rate: P in three values beside T's
+// would be too much for LDS twice, and splitting it in registers for six
+// instructions takes as long (24 prompts, 16062 tokens, 32 heads of 128 x 128: 371
+// and 373 us).  fp32 activations use them throughout, since K and Q would have
+// to be split too.
 #pragma once
 
 #include "sk_serve_device.hpp"
@@ -29,7 +31,8 @@ constexpr int FRAGS = 6;                         // fragments of a lower-triangu
 constexpr int FRAG_BYTES = 1024;                 // 64 lanes x 8 bf16
 constexpr int T_BYTES = FRAGS * 3 * FRAG_BYTES, P_BYTES = FRAGS * 2 * FRAG_BYTES;
 // workspace of a chunk and head: the fragments of T (three values each), then
-// of P (two), then g [64] and D_C [64] in fp32
+// of P (in fp32, the lower four columns of a lane's eight, then the upper), then
+// g [64] and D_C [64]
 constexpr int CHUNK_WORK_BYTES = T_BYTES + P_BYTES + 2 * PC * 4;
 // in fp32: the 16 x 16 tiles of T on and below the diagonal, then of P, as A
 // operands of the fp32 instruction (four columns a lane), then the same factors
@@ -58,27 +61,28 @@ __device__ __forceinline__ int block_row(int m, int t) { return ((m & 12) << 1) 
 __device__ __forceinline__ f32x4s mm32(bf16x8 a, bf16x8 b, f32x4s c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+__device__ __forceinline__ f32x4s mm4(float a, float b, f32x4s c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
 
-// Eight fp32 values as bf16 fragments whose sum they are (three: exactly; the
-// first two leave at most 2^-16 of a value).
+// Eight fp32 values as three bf16 fragments whose exact sum they are.
 __device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
   return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
 }
 __device__ __forceinline__ float below(float x) {    // x less its top 8 bits
   return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
 }
-template <int TERMS>
-__device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[TERMS]) {
+__device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[3]) {
   float r[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) r[e] = x[e];
 #pragma unroll
-  for (int t = 0; t < TERMS; ++t) {
+  for (int t = 0; t < 3; ++t) {
     u32x4 w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       w[e] = high_halves(r[2 * e], r[2 * e + 1]);
-      if (t + 1 < TERMS) {
+      if (t < 2) {
         r[2 * e] = below(r[2 * e]);
         r[2 * e + 1] = below(r[2 * e + 1]);
       }

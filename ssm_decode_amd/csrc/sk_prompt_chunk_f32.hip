@@ -33,10 +33,6 @@ struct F32Lds {
   static_assert(BYTES <= 160 * 1024, "LDS of a CU");
 };
 
-__device__ __forceinline__ f32x4s mm4(float a, float b, f32x4s c) {
-  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
-}
-
 template <int DK, int DV>
 __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptParams p) {
   using L = F32Lds<DK>;
