@@ -347,7 +347,7 @@ __device__ __forceinline__ void copy16x4(const void* base, uint32_t offset, uint
       "global_load_lds_dwordx4 %0, %1 offset:0x800\n\t"
       "global_load_lds_dwordx4 %0, %1 offset:0xc00" ::"v"(offset),
       "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
-      : "memory");
+      : "memory", "m0");
 }
 // Within each 16 lanes, lane i gives the address of four values: 4 rows (i / 4)
 // of 16 (4 (i % 4) ..); it receives column i of the four rows.

@@ -158,7 +158,7 @@ __device__ __forceinline__ int chunked_prompt(const PromptParams& p, int x, int*
 __device__ __forceinline__ void copy16(const void* base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset),
                "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
