@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] *= s_be[k + e];
         bf16x8 v[3];
-        split8(t, v);
+        split8<true>(t, v);
 #pragma unroll
         for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(to + (f * 3 + n) * FRAG_BYTES + ln * 16) = v[n];
       } else {
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
         const float v = !OUT && unit ? 0.f : (float)vv[rb][e];
         x[e] = v - gm[rb][e] * R[rb][e >> 2][e & 3];
       }
-      split8(x, br[rb]);
+      split8<true>(x, br[rb]);
     };
     // O = Q S (three values);  R = V - g (K S) and its split meanwhile
 #pragma unroll

@@ -11,10 +11,9 @@
 // order.
 //
 // Precision.  The state is fp32, and so is every product.  They run on the bf16
-// matrix cores with each fp32 operand as an exact sum of three bf16 values (its
-// top 8 bits, the next 8, the last 8): a product with bf16 data (K, Q, K^T)
-// takes three instructions, one of two fp32 operands (T R) the six whose terms
-// reach 2^-24 of it.  P U, which only the outputs wait for, takes the fp32
+// matrix cores with each fp32 operand as an exact sum of three bf16 values: a
+// product with bf16 data (K, Q, K^T) takes three instructions, one of two fp32
+// operands (T R) the six whose terms reach 2^-24 of it.  P U, which only the outputs wait for, takes the fp32
 // instructions, a sixteenth of the bf16 ones' rate: P in three values beside T's
 // would be too much for LDS twice, and splitting it in registers for six
 // instructions takes as long (24 prompts, 16062 tokens, 32 heads of 128 x 128: 371
@@ -65,13 +64,13 @@ __device__ __forceinline__ f32x4s mm4(float a, float b, f32x4s c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// Eight fp32 values as three bf16 fragments whose exact sum they are.
-__device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
-  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-}
-__device__ __forceinline__ float below(float x) {    // x less its top 8 bits
-  return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-}
+// Eight fp32 values as three bf16 fragments whose exact sum they are.  Cut, a value
+// leaves up to 2^-7 of itself to the second and 2^-15 to the third; to nearest
+// (values under 2^128 (1 - 2^-9)), 2^-8 and 2^-17, so that a product of two values
+// to nearest without its three smallest terms is off by at most 2^-24 (cut: 2^-21,
+// always towards zero).
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+template <bool NEAREST = false>
 __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[3]) {
   float r[8];
 #pragma unroll
@@ -81,10 +80,16 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[3]) {
     u32x4 w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      w[e] = high_halves(r[2 * e], r[2 * e + 1]);
+      const float lo = r[2 * e], hi = r[2 * e + 1];
+      if (NEAREST) {
+        const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+        w[e] = __builtin_bit_cast(uint32_t, v);
+      } else {
+        w[e] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+      }
       if (t < 2) {
-        r[2 * e] = below(r[2 * e]);
-        r[2 * e + 1] = below(r[2 * e + 1]);
+        r[2 * e] = lo - __uint_as_float(NEAREST ? w[e] << 16 : __float_as_uint(lo) & 0xffff0000u);
+        r[2 * e + 1] = hi - __uint_as_float((NEAREST ? w[e] : __float_as_uint(hi)) & 0xffff0000u);
       }
     }
     out[t] = as_frag(w);

@@ -83,3 +83,28 @@ def test_the_tokens_of_a_chunk_read_by_queries_have_all_their_bits(dk, dv, act, 
     both = sum(np.abs(qq[np.arange(N), :, c])[:, :, None] * bb[c][:, :, None] * vv[c]
                for c in (a.cpu().numpy(), a.cpu().numpy() + 1))
     compare(lay, tok, S0, (n + 16)[:, None, None] * both)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", SHAPES[1:])
+def test_the_triangular_product_keeps_what_reaches_2_to_minus_24(dk, dv, act):
+    """Keys of one element each, no values, no decay: row j of the state becomes
+    S - beta S, of which the operands' low bits are a good part.  Roundings of
+    2^-24 of S: the product's, its two lower parts' sums with S (the last sum is
+    exact), one for the product's terms that may be left out: four, by a factor
+    that is under 1 + 2^-6."""
+    N, H = 64, 2
+    lay = make_layer(1, H, dk, dv, act, seed=204)
+    ones = 1 + 2.0 ** -7 - 2.0 ** -23           # eight bits 1.0000000, then ones throughout
+    lay.S.copy_(torch.sign(lay.S) * ones * torch.exp2(torch.floor(50 * lay.S)))
+    q, k, v, al, be, o = make_tokens(N, H, dk, dv, act, seed=205)
+    k.zero_()
+    k[torch.arange(N), :, torch.arange(N)] = 1
+    v.zero_()
+    al.fill_(1.0)
+    be.fill_(ones)
+    S0 = f64(lay.S)
+    run(lay, (q, k, v, al, be, o), [N])
+    want = S0.copy()
+    want[:, :, :N] -= float(be[0, 0]) * S0[:, :, :N]
+    assert (np.abs(f64(lay.S) - want) <= 4 * EPS32 * (1 + 2.0 ** -6) * np.abs(S0)).all()
