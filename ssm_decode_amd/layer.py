@@ -39,6 +39,25 @@ def _on_device(index: int, call, stream):
         return call(_stream_of(stream))
 
 
+class _StreamUses:
+    """The streams that calls have put work with these tensors on: dropped while
+    it runs, their memory waits for it (the allocator knows of the stream alone
+    that it was asked on)."""
+
+    def __init__(self, *tensors):
+        self.tensors = [t for t in tensors if t is not None and t.device.type == "cuda"]
+        self.seen = {torch._C._cuda_getCurrentRawStream(self.tensors[0].device.index)} if self.tensors else set()
+
+    def add(self, handle: int) -> int:
+        if handle not in self.seen and self.tensors:
+            dev = self.tensors[0].device
+            st = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+            for t in self.tensors:
+                t.record_stream(st)
+            self.seen.add(handle)
+        return handle
+
+
 @dataclass
 class DeviceStep:
     """One decode step's device tensors (layouts as in include/sketchssm.h)."""
@@ -188,7 +207,7 @@ class DecodeLayer:
         and, with prompts.prime, their sketches."""
         prompts.check(self)
         rc = _on_device(self.S.device.index, lambda st: abi.sketchssm_prefill(
-            self._layer, self._bufs, prompts.struct, st), stream)
+            self._layer, self._bufs, prompts.struct, prompts.uses.add(st)), stream)
         if rc == 0 and prompts.norm is not None:
             rc = self.normalise(prompts.o, prompts.norm, prompts.norm_gate, stream, prompts.seq_start)
         return rc
@@ -204,7 +223,8 @@ class DecodeLayer:
         serving.StateCache (int32 device tensors)."""
         cache.check(self, seqs, slots)
         return _on_device(self.S.device.index, lambda st: abi.sketchssm_state_save(
-            self._layer, self._bufs, cache.struct, seqs.data_ptr(), slots.data_ptr(), seqs.numel(), st), stream)
+            self._layer, self._bufs, cache.struct, seqs.data_ptr(), slots.data_ptr(), seqs.numel(), cache.uses.add(st)),
+            stream)
 
     def load_state(self, cache, seqs, slots, prime: bool = True, stream=None) -> int:
         """Read slots of a serving.StateCache back into the states of sequences
@@ -212,7 +232,8 @@ class DecodeLayer:
         sketches."""
         cache.check(self, seqs, slots)
         return _on_device(self.S.device.index, lambda st: abi.sketchssm_state_load(
-            self._layer, self._bufs, cache.struct, seqs.data_ptr(), slots.data_ptr(), seqs.numel(), int(prime), st), stream)
+            self._layer, self._bufs, cache.struct, seqs.data_ptr(), slots.data_ptr(), seqs.numel(), int(prime),
+            cache.uses.add(st)), stream)
 
     def error_word(self) -> int:
         return int(self.err[0].item())

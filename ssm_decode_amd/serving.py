@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import abi
-from .layer import DTYPE, TORCH_DTYPE, DecodeLayer, _on_device, _ptr
+from .layer import DTYPE, TORCH_DTYPE, DecodeLayer, _on_device, _ptr, _StreamUses
 
 _DTYPES = {TORCH_DTYPE[k]: v for k, v in DTYPE.items()}
 ACT = {"none": abi.SKSSM_ACT_NONE, "silu": abi.SKSSM_ACT_SILU, "sigmoid": abi.SKSSM_ACT_SIGMOID}
@@ -57,7 +57,9 @@ class Prompts:
     (with norm_gate, like o): an ``OutputNorm`` of o, applied in place behind
     the prompts (to the rows from seq_start[0] up to seq_start[n]).  The index tensors are read on the device
     at the call, the tensors are held, and the workspace is allocated once:
-    calls that may overlap take a ``Prompts`` each."""
+    calls that may overlap take a ``Prompts`` each.  It may be dropped once its
+    calls are made, on any stream that outlives it; a graph that captured one
+    needs it for as long as it is replayed."""
 
     def __init__(self, layer: DecodeLayer, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: torch.Tensor,
                  beta: torch.Tensor, o: torch.Tensor, seq_start: torch.Tensor,
@@ -90,6 +92,8 @@ class Prompts:
         self.q, self.k, self.v, self.gate, self.beta, self.o = q, k, v, gate, beta, o
         self.seq_start, self.seqs, self.has_state, self.prime = seq_start, seqs, has_state, prime
         self.work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        self.uses = _StreamUses(q, k, v, gate, beta, o, seq_start, seqs, has_state, norm_gate, self.work,
+                                *((norm.weight, norm.bias) if norm is not None else ()))
         self._struct = abi.sketchssm_prompts(
             _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(beta), _ptr(o), *strides, N, n, _ptr(seq_start),
             _ptr(seqs), _ptr(has_state), int(prime), _ptr(self.work), need)
@@ -107,7 +111,8 @@ class Prompts:
 class StateCache:
     """A pool of ``slots`` slots, each for one sequence's states of a layer in
     8 or 4 bits: codes [slots, H, dk, dv] int8 (4 bits: [.., dv / 2] uint8, the
-    lower column in the low half) and scale [slots, H, dk, dv / 32]."""
+    lower column in the low half) and scale [slots, H, dk, dv / 32].  It may be
+    dropped as ``Prompts`` may."""
 
     def __init__(self, layer: DecodeLayer, slots: int, bits: int = 8):
         if bits not in (8, 4):
@@ -119,6 +124,7 @@ class StateCache:
         self.codes = (torch.zeros((slots, H, dk, dv), dtype=torch.int8, device=dev) if bits == 8 else
                       torch.zeros((slots, H, dk, dv // 2), dtype=torch.uint8, device=dev))
         self.scale = torch.zeros((slots, H, dk, dv // 32), dtype=torch.float32, device=dev)
+        self.uses = _StreamUses(self.codes, self.scale)
         self._struct = abi.sketchssm_state_cache(_ptr(self.codes), _ptr(self.scale), slots, bits)
 
     @property
