@@ -55,7 +55,8 @@ class Prompts:
     [n]: 0 starts it from a zero state (None: every prompt goes on from its
     sequence's state); prime: also write the sketches of the new states; norm
     (with norm_gate, like o): an ``OutputNorm`` of o, applied in place behind
-    the prompts (to the rows from seq_start[0] up to seq_start[n]).  The index tensors are read on the device
+    the prompts (to the rows from seq_start[0] up to seq_start[n], a refused
+    prompt's among them: what o holds there then is undefined).  The index tensors are read on the device
     at the call, the tensors are held, and the workspace is allocated once:
     calls that may overlap take a ``Prompts`` each.  It may be dropped once its
     calls are made, on any stream that outlives it; a graph that captured one
@@ -79,9 +80,14 @@ class Prompts:
             if x is not None:
                 _indices(name, x, n, dev)
         if norm_gate is not None:
-            _rows("norm_gate", norm_gate, (N, H, layer.dv), at, dev)
+            # (what the norm would refuse is refused here: behind the prompts the states have moved on)
+            st, es = _rows("norm_gate", norm_gate, (N, H, layer.dv), at, dev), norm_gate.element_size()
+            if norm_gate.data_ptr() % 16 or st * es % 16 or not H * layer.dv <= st <= 1 << 25:
+                raise ValueError("norm_gate: rows at whole 16 bytes, at most 2^25 elements apart")
         if norm is not None:
             norm.check((H, layer.dv), dev)
+            if H > 65535:
+                raise ValueError("norm: at most 65535 heads")
         elif norm_gate is not None:
             raise ValueError("norm_gate: without a norm")
         self.norm, self.norm_gate = norm, norm_gate
@@ -154,6 +160,8 @@ class OutputNorm:
                 raise ValueError(f"{name}: a contiguous fp32 tensor [groups, width] or [width]")
         if weight is not None and bias is not None and weight.shape != bias.shape:
             raise ValueError("weight and bias: of one shape")
+        if not (math.isfinite(C.c_float(eps).value) and eps >= 0):
+            raise ValueError("eps: finite in fp32, 0 or more")
         if act not in ACT:
             raise ValueError(f"act: one of {tuple(ACT)}")
         self.weight, self.bias, self.eps, self.act = weight, bias, float(eps), act
@@ -164,6 +172,8 @@ class OutputNorm:
         for t in (self.weight, self.bias):
             if t is not None and (t.shape != shape[2 - t.dim():] or t.device != device):
                 raise ValueError(f"weight and bias: {tuple(shape)} or {tuple(shape[1:])} on {device}, got {tuple(t.shape)} on {t.device}")
+            if t is not None and t.data_ptr() % 16:
+                raise ValueError("weight and bias: at whole 16 bytes")
 
 
 def group_norm(x: torch.Tensor, norm: OutputNorm, y: torch.Tensor, gate: Optional[torch.Tensor] = None,

@@ -314,3 +314,22 @@ def test_output_norm_refuses_wrong_tensors():
     x = torch.zeros(3, 2, 8)
     with pytest.raises(ValueError):
         group_norm(x, OutputNorm(), x)                   # host memory
+
+
+def test_prompts_refuse_norms_that_the_call_would_refuse():
+    """What sketchssm_group_norm would refuse behind the prompts, whose states
+    would then have moved on."""
+    for eps in (float("nan"), float("inf"), -1e-5, 1e39):
+        with pytest.raises(ValueError):
+            OutputNorm(eps=eps)
+    ok = torch.zeros(2000)
+    at = next(i for i in range(4) if (ok.data_ptr() + 4 * i) % 16 == 0)
+    w = ok[at + 1:at + 33]
+    rows = ok[at:at + 5 * 132].view(5, 132)[:, :128].unflatten(1, (4, 32))
+    Prompts(_Layer(), **_tokens(), norm=OutputNorm(ok[at:at + 32]), norm_gate=rows)
+    odd = torch.zeros(5, 130)[:, :128].unflatten(1, (4, 32))
+    for kw in (dict(norm=OutputNorm(w)), dict(norm=OutputNorm(None, w)), dict(norm=OutputNorm(), norm_gate=odd),
+               dict(norm=OutputNorm(), norm_gate=ok[at + 1:at + 641].view(5, 4, 32)),
+               dict(norm=OutputNorm(), norm_gate=torch.zeros(1, 4, 32).expand(5, 4, 32))):
+        with pytest.raises(ValueError):
+            Prompts(_Layer(), **_tokens(), **kw)
