@@ -156,6 +156,10 @@ __device__ __forceinline__ int chunked_prompt(const PromptParams& p, int x, int*
   return -1;
 }
 
+// (The compiler warns that it would not save m0, a reserved register, around the
+// statement; it has nothing there to save.)
+#pragma clang diagnostic ignored "-Winline-asm"
+
 // 16 bytes of each lane, from base + its offset in memory to lds + 16 * lane
 // in LDS (base and lds are uniform), in flight until the wave's next wait for
 // its memory counter.  (The compiler would have every LDS read wait for a copy
