@@ -359,9 +359,10 @@ typedef struct {
  * too.  Token rows that no prompt holds are neither read nor written.
  * Sums run in fp32; longer prompts (dk >= 64) go in chunks of 64
  * tokens, whose products are those of fp32 operands.  An infinity or a NaN
- * in a token's row or in the state reaches, besides what the recurrence brings
- * it to, the outputs of its head and prompt from the start of its chunk (of
- * sketchssm_prefill's own choice, at most 64 tokens back) on.  Other
+ * in a token's row or in the state reaches what the recurrence brings it to
+ * (as one or the other) and no earlier token.  An overflow of finite numbers,
+ * the square of a key's norm among them, may in a chunk reach its head's
+ * outputs from the chunk's start on.  Other
  * families return SKSSM_EDIM; prime with SKSSM_COEF_STATE is SKSSM_EFLAG (a
  * state-dependent map is formed by sketchssm_flush with SKSSM_FLUSH_ALL).
  * nseq = 0 launches nothing. */

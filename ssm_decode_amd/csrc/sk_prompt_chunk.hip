@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
   constexpr int MB = PC * LS * 4;                // bytes of A (T in its place), then P, over them
   __shared__ __align__(16) unsigned char s_big[2 * KB > MB ? 2 * KB : MB];
   __shared__ __align__(16) float s_al[PC], s_be[PC], s_pre[PC], s_suf[PC], s_blk[4], s_mid[16], s_din[PC * 17];
+  __shared__ int s_lim;
   float* s_A = reinterpret_cast<float*>(s_big);
 
   // (the last chunks first: what the next launch begins with is then the most
@@ -74,9 +75,16 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
   };
   fetch(0);
   if (STAGES > 1) fetch(1);
-  if (tid < PC) {
-    s_al[tid] = tid < nt ? p.gate[(tok + tid) * p.gs + h] : 1.f;
-    s_be[tid] = tid < nt ? p.beta[(tok + tid) * p.bs + h] : 0.f;
+  // s_lim: the first token with an infinity or a NaN in its key or factors (PC:
+  // none).  From it on T and the keys' factors are those of no tokens, and g is
+  // NaN, which takes the next launch's outputs from there on, and the state, with
+  // it; tokens before see nothing of it.
+  if (wv == 0) {
+    const float al = tid < nt ? p.gate[(tok + tid) * p.gs + h] : 1.f, be = tid < nt ? p.beta[(tok + tid) * p.bs + h] : 0.f;
+    s_al[tid] = al;
+    s_be[tid] = be;
+    const unsigned long long m = __ballot(!finite(al) || !finite(be));
+    if (tid == 0) s_lim = m ? __builtin_ctzll(m) : PC;
   }
   stage(0);
   __syncthreads();
@@ -150,6 +158,13 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
     }
   }
   __builtin_amdgcn_sched_barrier(0);
+  // (a key with one has no finite product with itself; one whose square
+  // overflows counts as such)
+#pragma unroll
+  for (int n = 0; n < 3; ++n)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (ti[n] == tj[n] && 4 * g + r == cg && !finite(ak[n][r])) atomicMin(&s_lim, 16 * ti[n] + cg);
   float D[3][4], be[3][4];                              // D_ij and beta_i of the lane's results
 #pragma unroll
   for (int n = 0; n < 3; ++n) {
@@ -164,6 +179,8 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
     }
   }
   __syncthreads();                                      // K and Q are read: A over them
+  const int lim = s_lim;
+  if (tid >= lim && tid < PC) s_be[tid] = 0.f;
 #pragma unroll
   for (int n = 0; n < 3; ++n) {
     if (wv + 4 * n < 10) {                              // uniform over the wave
@@ -173,7 +190,7 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
         const int ii = 16 * ti[n] + 4 * g + r;
         // (selected, not multiplied by a zero: nothing above the diagonal may
         // reach the sums)
-        s_A[ii * LS + j] = j < ii ? be[n][r] * D[n][r] * ak[n][r] : 0.f;
+        s_A[ii * LS + j] = j < ii && ii < lim ? be[n][r] * D[n][r] * ak[n][r] : 0.f;
         aq[n][r] = j <= ii ? D[n][r] * aq[n][r] : 0.f;
       }
     }
@@ -309,7 +326,7 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
     for (int n = 0; n < b; ++n) pre *= s_blk[n];
     for (int n = b + 1; n < 4; ++n) suf *= s_blk[n];
     float* G = reinterpret_cast<float*>(W + WORK - 2 * PC * 4);
-    G[tid] = pre;
+    G[tid] = tid < lim ? pre : __builtin_nanf("");
     G[PC + tid] = suf;
   }
 }
@@ -571,6 +588,12 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     rows8(S[0], x);
     split8(x, ss[0]);
   }
+  // Where R is no finite number it is left out, so that it reaches no earlier
+  // token, and the state's column becomes NaN; `wrong`: the wave's columns to
+  // which that came, from the chunk at wrong_t0 on, whose outputs are put right at
+  // the end.
+  uint32_t wrong = 0;
+  int wrong_t0 = 0;
   int t0 = 0, buf = 0;
   // one chunk; `more`: a whole one follows (no branch may then stand between
   // two regions, or work for the second is not done in the first)
@@ -649,6 +672,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     if (OUT && t0 > 0) store_out(t0 - PC, PC);
     __builtin_amdgcn_sched_barrier(0);
     bf16x8 br[2][3];
+    bool bad = false;                            // R has no finite number there: left out (see `wrong`)
     auto load_t = [&](int kb) {
 #pragma unroll
       for (int rb = kb; rb < 2; ++rb)
@@ -663,6 +687,9 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
       for (int e = 0; e < 8; ++e) {
         const float v = !OUT && unit ? 0.f : (float)vv[rb][e];
         x[e] = v - gm[rb][e] * R[rb][e >> 2][e & 3];
+        const bool ok = finite(x[e]);
+        bad |= !ok;
+        x[e] = ok ? x[e] : 0.f;
       }
       split8<true>(x, br[rb]);
     };
@@ -721,13 +748,14 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll
           for (int t = 0; t < 2; ++t) U[rb][t] = mm32(ft[kb][rb][t][TA[v]], br[kb][TB[v]], U[rb][t]);
       if (kb == 0) {
+        const float gS = column_poison(bad, gC, t0, &wrong, &wrong_t0);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
 #pragma unroll
           for (int rb = 0; rb < 2; ++rb)
             if (OUT) O[rb][e >> 2][e & 3] *= gm[rb][e];
 #pragma unroll
-          for (int db = 0; db < DB; ++db) S[db][e >> 2][e & 3] *= gC;
+          for (int db = 0; db < DB; ++db) S[db][e >> 2][e & 3] *= gS;
         }
         region<24, 1, 2>();
         copies(3 * DB, 3 * DB + 2);
@@ -787,6 +815,17 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     store_out(t0 - PC, len - (t0 - PC));
   }
 
+  if (OUT && (wrong >> n & 1)) {
+    // from the token with an infinity or a NaN, in its value or (g says) in its
+    // key or factors, or, where the state or a sum has one, all of that chunk
+    int t = wrong_t0;
+    for (; t < len; ++t) {
+      const float g = reinterpret_cast<const float*>(wp + (size_t)(t >> 6) * p.H * CHUNK_WORK_BYTES + T_BYTES + P_BYTES)[t & 63];
+      if (!finite(g) || (vp[t * p.vs + n] & 0x7f80) == 0x7f80) break;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (t = (t < len ? t : wrong_t0) + hi; t < len; t += 4) op[t * p.os + n] = 0x7fc0;
+  }
   if (OUT && !last) return;                      // (the state behind a segment is known already)
   float* to = OUT ? Sg : own + (unit ? DK * DV : 0) + c0 + n;
   const int ld = unit ? DK : DV;

@@ -64,6 +64,8 @@ __device__ __forceinline__ f32x4s mm4(float a, float b, f32x4s c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
+
 // Eight fp32 values as three bf16 fragments whose exact sum they are.  Cut, a value
 // leaves up to 2^-7 of itself to the second and 2^-15 to the third; to nearest
 // (values under 2^128 (1 - 2^-9)), 2^-8 and 2^-17, so that a product of two values
@@ -159,6 +161,17 @@ __device__ __forceinline__ int chunked_prompt(const PromptParams& p, int x, int*
 // (The compiler warns that it would not save m0, a reserved register, around the
 // statement; it has nothing there to save.)
 #pragma clang diagnostic ignored "-Winline-asm"
+
+// x, or NaN in the columns (n = lane % 16) of which a lane of the four has `bad`;
+// `wrong` collects these columns, and *t0 becomes the first `now` that had one.
+__device__ __forceinline__ float column_poison(bool bad, float x, int now, uint32_t* wrong, int* t0) {
+  const unsigned long long all = __ballot(bad);
+  uint32_t m = (uint32_t)(all | all >> 32);
+  m = (m | m >> 16) & 0xffff;
+  *t0 = *wrong ? *t0 : now;
+  *wrong |= m;
+  return m >> (threadIdx.x & 15) & 1 ? __builtin_nanf("") : x;
+}
 
 // 16 bytes of each lane, from base + its offset in memory to lds + 16 * lane
 // in LDS (base and lds are uniform), in flight until the wave's next wait for

@@ -154,6 +154,9 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
     for (int r = 0; r < 4; ++r) by_col[m][r] = (4 * hi + r) * ROWB + (4 * (m ^ hi) + ((n >> 2) ^ r)) * 16 + (n & 3) * 4;
   }
 
+  // (as in bf16: columns where R is no finite number)
+  uint32_t wrong = 0;
+  int wrong_t0 = 0;
   int t0 = 0, buf = 0;
   // one chunk; `more`: a whole one follows.  Steps of up to 16 matrix
   // instructions, in each the reads of the next one's A operands.
@@ -222,6 +225,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
       }
     }
     // Q S;  R = V - g (K S) meanwhile
+    bool bad = false;
 #pragma unroll
     for (int kb = 0; kb < MB; ++kb) {
       if (kb + 1 < MB) load_rows(s_q, kb + 1, kb + 1);
@@ -229,7 +233,12 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
       if (kb < TB) {
         ld4(s_g + PC + 16 * kb + 4 * hi, d[kb]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) R[kb][r] = vv[kb][r] - g[kb][r] * R[kb][r];
+        for (int r = 0; r < 4; ++r) {
+          const float x = vv[kb][r] - g[kb][r] * R[kb][r];
+          const bool ok = finite(x);
+          bad |= !ok;
+          R[kb][r] = ok ? x : 0.f;
+        }
       }
       times(kb, S[kb], O, 0);
       region<16, 1, 2>();
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) store_out(t0 - PC, tb, PC);
     }
-    const float gC = s_g[PC - 1];
+    const float gC = column_poison(bad, s_g[PC - 1], t0, &wrong, &wrong_t0);
     __syncthreads();                             // everybody has read Q
     if (tail) {
       copy_rows(qp, p.qs, t0 + PC, lds0 + L::Q);
@@ -295,6 +304,15 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
     for (int tb = 0; tb < TB; ++tb) store_out(t0 - PC, tb, len - (t0 - PC));
   }
 
+  if (wrong >> n & 1) {
+    int t = wrong_t0;
+    for (; t < len; ++t) {
+      const float g = reinterpret_cast<const float*>(wp + (size_t)(t >> 6) * p.H * CHUNK_WORK_F32 + 2 * F32_TILES * FRAG_BYTES)[t & 63];
+      if (!finite(g) || !finite(vp[t * p.vs + n])) break;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (t = (t < len ? t : wrong_t0) + hi; t < len; t += 4) op[t * p.os + n] = __builtin_nanf("");
+  }
   float s[MB][1][4];
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
