@@ -815,16 +815,14 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     store_out(t0 - PC, len - (t0 - PC));
   }
 
-  if (OUT && (wrong >> n & 1)) {
-    // from the token with an infinity or a NaN, in its value or (g says) in its
-    // key or factors, or, where the state or a sum has one, all of that chunk
-    int t = wrong_t0;
-    for (; t < len; ++t) {
+  if (OUT && wrong) {                            // (g says where a key or factor has one)
+    const int first = first_wrong(wrong, wrong_t0, len, [&](int t) {
       const float g = reinterpret_cast<const float*>(wp + (size_t)(t >> 6) * p.H * CHUNK_WORK_BYTES + T_BYTES + P_BYTES)[t & 63];
-      if (!finite(g) || (vp[t * p.vs + n] & 0x7f80) == 0x7f80) break;
-    }
+      return !finite(g) || (vp[t * p.vs + n] & 0x7f80) == 0x7f80;
+    });
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    for (t = (t < len ? t : wrong_t0) + hi; t < len; t += 4) op[t * p.os + n] = 0x7fc0;
+    if (wrong >> n & 1)
+      for (int t = first + hi; t < len; t += 4) op[t * p.os + n] = 0x7fc0;
   }
   if (OUT && !last) return;                      // (the state behind a segment is known already)
   float* to = OUT ? Sg : own + (unit ? DK * DV : 0) + c0 + n;

@@ -304,14 +304,14 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
     for (int tb = 0; tb < TB; ++tb) store_out(t0 - PC, tb, len - (t0 - PC));
   }
 
-  if (wrong >> n & 1) {
-    int t = wrong_t0;
-    for (; t < len; ++t) {
+  if (wrong) {
+    const int first = first_wrong(wrong, wrong_t0, len, [&](int t) {
       const float g = reinterpret_cast<const float*>(wp + (size_t)(t >> 6) * p.H * CHUNK_WORK_F32 + 2 * F32_TILES * FRAG_BYTES)[t & 63];
-      if (!finite(g) || !finite(vp[t * p.vs + n])) break;
-    }
+      return !finite(g) || !finite(vp[t * p.vs + n]);
+    });
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    for (t = (t < len ? t : wrong_t0) + hi; t < len; t += 4) op[t * p.os + n] = __builtin_nanf("");
+    if (wrong >> n & 1)
+      for (int t = first + hi; t < len; t += 4) op[t * p.os + n] = __builtin_nanf("");
   }
   float s[MB][1][4];
 #pragma unroll
