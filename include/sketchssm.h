@@ -379,7 +379,8 @@ int64_t sketchssm_prefill_workspace_bytes(const sketchssm_layer* layer, int32_t 
 /* A pool of slots that each hold the states of one sequence's heads in 8 or
  * 4 bits.  32 consecutive values of a state row (along dv) share a scale:
  * scale = max|x| / 127 (8 bits) or / 7 (4 bits), code = x / scale rounded to
- * nearest even, and a code stands for code * scale.  A block whose largest
+ * nearest even, and a code stands for code * scale (the scale is rounded down
+ * where code * scale would overflow).  A block whose largest
  * magnitude is under 2^-100 is held as zeros; one with an infinity or a NaN
  * reads back as NaN. */
 typedef struct {

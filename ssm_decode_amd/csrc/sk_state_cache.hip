@@ -97,7 +97,9 @@ __global__ void __launch_bounds__(SAVE_THREADS) state_save_kernel(CacheParams p)
       m = quad_max(m);
       const float amax = __uint_as_float(m);
       const bool finite = m < 0x7f800000u, live = finite && amax >= 0x1p-100f;
-      const float s = live ? amax / (BITS == 8 ? 127.f : 7.f) : (finite ? 0.f : __uint_as_float(0x7fc00000u));
+      // (127 times the scale of the largest fp32 value, rounded up, would pass it)
+      const float of = BITS == 8 ? fminf(amax / 127.f, 0x1.0204060000000p+121f) : amax / 7.f;
+      const float s = live ? of : (finite ? 0.f : __uint_as_float(0x7fc00000u));
       const float inv = live ? 1.f / s : 0.f;
       // The product with the rounded reciprocal is off by at most 2^-24 of a
       // quotient up to 127, 8e-6: a code is right where the product is no nearer

@@ -274,3 +274,23 @@ def test_many_sequences_at_once(bits, dk, dv):
         c, s = ref.quantise(S[b], bits)
         assert np.array_equal(codes[slot], c) and np.array_equal(scales[slot], s)
     assert lay.error_word() == 0
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_the_largest_fp32_values_are_read_back_finite(bits):
+    """Half a step of the scale, and the scale's own rounding (down, for the
+    largest in 8 bits)."""
+    lay = make_layer(2, 2, 64, 64)
+    top = torch.finfo(torch.float32).max
+    lay.S[0, 0] = torch.linspace(-top, top, 64, device="cuda", dtype=torch.float64).clamp(-top, top).float()
+    lay.S[0, 1, :, 32:] = -top
+    S0 = lay.S[0].double().cpu().numpy()
+    cache = StateCache(lay, 1, bits)
+    assert lay.save_state(cache, ints(0), ints(0)) == 0
+    assert lay.load_state(cache, ints(1), ints(0), prime=False) == 0
+    torch.cuda.synchronize()
+    m = 127 if bits == 8 else 7
+    amax = np.abs(S0.reshape(2, 64, 2, 32)).max(-1, keepdims=True).repeat(32, -1).reshape(S0.shape)
+    got = lay.S[1].double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert (np.abs(got - S0) <= (0.5 / m + 2.0 ** -22) * amax).all()
