@@ -15,7 +15,7 @@ namespace {
 // inverse and joins, so what counts is how many a CU has at once: K and Q come in
 // stages, and A and P, which waits in registers, take the same place in LDS (8224 of
 // 128 columns, 268 MB of K and Q in, 256 MB of T and P out: three a CU 164 us, four,
-// with A and P apart, 115, six 92, 5.7 TB/s; six with 88 bytes of spills 159).
+// with A and P apart, 115, six 94, 5.6 TB/s; six with 88 bytes of spills 159).
 constexpr int LS = PC + 4;                       // row stride of the fp32 matrices in LDS
 
 template <int DK, typename AT>
@@ -337,9 +337,9 @@ __global__ void __launch_bounds__(256, sizeof(AT) == 4 ? 4 : 6) prompt_prep_kern
 // twice: the next chunk's copy, straight from memory, is in flight over the
 // present chunk.  K^T and V's columns come by transposing LDS reads.
 //
-// What bounds it is the chain from chunk to chunk (128 x 128: 3.9 us a chunk with
-// one wave a SIMD, 6.0 with two), so a chunk's instructions
-// are laid out by hand in regions: in each, the matrix instructions of one
+// What bounds it is the chain from chunk to chunk (128 x 128: 3.7 us a chunk with
+// one wave a SIMD, of which its matrix instructions are 1.8, and 7.8 with two), so
+// a chunk's instructions are laid out by hand in regions: in each, the matrix instructions of one
 // step, the LDS reads of the next step's fragments, and the vector work (three
 // value splits above all) that a later step needs; the vector work runs in the
 // shadow of the matrix instructions only where it stands between them.
@@ -589,11 +589,10 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     split8(x, ss[0]);
   }
   // Where R is no finite number it is left out, so that it reaches no earlier
-  // token, and the state's column becomes NaN; `wrong`: the wave's columns to
-  // which that came, from the chunk at wrong_t0 on, whose outputs are put right at
-  // the end.
-  uint32_t wrong = 0;
-  int wrong_t0 = 0;
+  // token, and the state's column becomes NaN; `since`: the first token at which
+  // that came to the lane's rows of its column, whose outputs from the column's
+  // first on are put right at the end.
+  int since = NEVER;
   int t0 = 0, buf = 0;
   // one chunk; `more`: a whole one follows (no branch may then stand between
   // two regions, or work for the second is not done in the first)
@@ -672,7 +671,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     if (OUT && t0 > 0) store_out(t0 - PC, PC);
     __builtin_amdgcn_sched_barrier(0);
     bf16x8 br[2][3];
-    bool bad = false;                            // R has no finite number there: left out (see `wrong`)
+    int low = 16;                                // the first of the lane's values of R that is none (8 rb + e)
     auto load_t = [&](int kb) {
 #pragma unroll
       for (int rb = kb; rb < 2; ++rb)
@@ -683,14 +682,16 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     };
     auto split_r = [&](int rb) {
       float x[8];
+      int l = 16;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 7; e >= 0; --e) {
         const float v = !OUT && unit ? 0.f : (float)vv[rb][e];
         x[e] = v - gm[rb][e] * R[rb][e >> 2][e & 3];
         const bool ok = finite(x[e]);
-        bad |= !ok;
+        l = ok ? l : 8 * rb + e;
         x[e] = ok ? x[e] : 0.f;
       }
+      low = min(low, l);
       split8<true>(x, br[rb]);
     };
     // O = Q S (three values);  R = V - g (K S) and its split meanwhile
@@ -748,7 +749,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
 #pragma unroll
           for (int t = 0; t < 2; ++t) U[rb][t] = mm32(ft[kb][rb][t][TA[v]], br[kb][TB[v]], U[rb][t]);
       if (kb == 0) {
-        const float gS = column_poison(bad, gC, t0, &wrong, &wrong_t0);
+        const float gS = column_poison(low < 16, gC);
+        if (OUT) since = low < 16 && since == NEVER ? t0 + 32 * (low >> 3) + 8 * hi + (low & 7) : since;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
 #pragma unroll
@@ -815,14 +817,10 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_kernel(PromptParams p
     store_out(t0 - PC, len - (t0 - PC));
   }
 
-  if (OUT && wrong) {                            // (g says where a key or factor has one)
-    const int first = first_wrong(wrong, wrong_t0, len, [&](int t) {
-      const float g = reinterpret_cast<const float*>(wp + (size_t)(t >> 6) * p.H * CHUNK_WORK_BYTES + T_BYTES + P_BYTES)[t & 63];
-      return !finite(g) || (vp[t * p.vs + n] & 0x7f80) == 0x7f80;
-    });
+  if (OUT && __any(since != NEVER)) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (wrong >> n & 1)
-      for (int t = first + hi; t < len; t += 4) op[t * p.os + n] = 0x7fc0;
+    const int first = column_first(since);
+    for (int64_t t = (int64_t)first + hi; t < len; t += 4) op[t * p.os + n] = 0x7fc0;
   }
   if (OUT && !last) return;                      // (the state behind a segment is known already)
   float* to = OUT ? Sg : own + (unit ? DK * DV : 0) + c0 + n;
@@ -963,8 +961,8 @@ int launch(int act, const PromptParams& p, hipStream_t st) {
     launch_chunks<DK, DV, NW, true>(p, st);
   } else if (p.nchunked * p.H <= 128) {
     // .. unless that leaves CUs idle (128 x 128, 2048 tokens each, with four and
-    // eight waves: 64 tiles 136 and 181 us, 128 190 and 229, 160 292 and 246,
-    // 256 359 and 334)
+    // eight waves: 64 tiles 152 and 217 us, 128 205 and 258, 160 321 and 277,
+    // 256 387 and 360)
     launch_chunks<DK, DV, 4, true>(p, st);
   } else {
     launch_chunks<DK, DV, NW, true>(p, st);

@@ -162,37 +162,18 @@ __device__ __forceinline__ int chunked_prompt(const PromptParams& p, int x, int*
 // statement; it has nothing there to save.)
 #pragma clang diagnostic ignored "-Winline-asm"
 
-// x, or NaN in the columns (n = lane % 16) of which a lane of the four has `bad`;
-// `wrong` collects these columns, and *t0 becomes the first `now` that had one.
-__device__ __forceinline__ float column_poison(bool bad, float x, int now, uint32_t* wrong, int* t0) {
+// x, or NaN in the columns (n = lane % 16) of which one of the four lanes has `bad`.
+__device__ __forceinline__ float column_poison(bool bad, float x) {
   const unsigned long long all = __ballot(bad);
   uint32_t m = (uint32_t)(all | all >> 32);
-  m = (m | m >> 16) & 0xffff;
-  *t0 = *wrong ? *t0 : now;
-  *wrong |= m;
+  m |= m >> 16;
   return m >> (threadIdx.x & 15) & 1 ? __builtin_nanf("") : x;
 }
-
-// For the columns in `wrong`: the token from which on their outputs are NaN, the
-// first behind `from` (a chunk's start) for which bad(token) says so of the lane's
-// column, or all where there is none (the state or a sum has one).  A chunk at a
-// time, 16 tokens a lane; the whole wave takes part.
-template <typename Bad>
-__device__ __forceinline__ int first_wrong(uint32_t wrong, int from, int len, Bad bad) {
-  const int n = threadIdx.x & 15, hi = threadIdx.x >> 4 & 3;
-  int first = -1;
-  for (int c = from; c < len && __any((wrong >> n & 1) && first < 0); c += PC) {
-    int f = PC;
-#pragma unroll
-    for (int j = 15; j >= 0; --j) {
-      const int t = c + 16 * hi + j;
-      if (bad(t < len ? t : len - 1) && t < len) f = 16 * hi + j;
-    }
-    f = min(f, __shfl_xor(f, 16));
-    f = min(f, __shfl_xor(f, 32));
-    if (first < 0 && f < PC) first = c + f;
-  }
-  return first < 0 ? from : first;
+// The first of the four lanes' tokens.
+constexpr int NEVER = INT32_MAX;
+__device__ __forceinline__ int column_first(int t) {
+  t = min(t, __shfl_xor(t, 16));
+  return min(t, __shfl_xor(t, 32));
 }
 
 // 16 bytes of each lane, from base + its offset in memory to lds + 16 * lane

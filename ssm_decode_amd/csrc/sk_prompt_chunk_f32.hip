@@ -8,9 +8,9 @@
 // nothing moves between K S, T R, P U and K^T U; the A operands are runs of
 // four columns from LDS (of K^T, single values: four rows of 16 in 64 banks).
 //
-// Bound by the matrix instructions: 64 x 64, 272 a wave and chunk at 32 cycles, 4.0
-// of the 5.1 us that a chunk takes (45 us for 8; branches between the products and
-// outputs stored in their own chunk: 56).  K and T, P are in LDS twice, Q
+// Bound by the matrix instructions: 64 x 64, 272 a wave and chunk at 32 cycles, 3.6
+// of the 5.3 us that a chunk takes (47 us for 8; branches between the products and
+// outputs stored in their own chunk took 11 more).  K and T, P are in LDS twice, Q
 // once (its next copy starts when the chunk's outputs have it behind them), V
 // comes to registers a chunk ahead.
 #include <type_traits>
@@ -155,8 +155,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
   }
 
   // (as in bf16: columns where R is no finite number)
-  uint32_t wrong = 0;
-  int wrong_t0 = 0;
+  int since = NEVER;
   int t0 = 0, buf = 0;
   // one chunk; `more`: a whole one follows.  Steps of up to 16 matrix
   // instructions, in each the reads of the next one's A operands.
@@ -225,7 +224,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
       }
     }
     // Q S;  R = V - g (K S) meanwhile
-    bool bad = false;
+    int low = 16;
 #pragma unroll
     for (int kb = 0; kb < MB; ++kb) {
       if (kb + 1 < MB) load_rows(s_q, kb + 1, kb + 1);
@@ -233,11 +232,12 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
       if (kb < TB) {
         ld4(s_g + PC + 16 * kb + 4 * hi, d[kb]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 3, l = 16; r >= 0; --r) {
           const float x = vv[kb][r] - g[kb][r] * R[kb][r];
           const bool ok = finite(x);
-          bad |= !ok;
+          l = ok ? l : 4 * kb + r;
           R[kb][r] = ok ? x : 0.f;
+          if (r == 0) low = min(low, l);
         }
       }
       times(kb, S[kb], O, 0);
@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) store_out(t0 - PC, tb, PC);
     }
-    const float gC = column_poison(bad, s_g[PC - 1], t0, &wrong, &wrong_t0);
+    const float gC = column_poison(low < 16, s_g[PC - 1]);
+    since = low < 16 && since == NEVER ? t0 + 16 * (low >> 2) + 4 * hi + (low & 3) : since;
     __syncthreads();                             // everybody has read Q
     if (tail) {
       copy_rows(qp, p.qs, t0 + PC, lds0 + L::Q);
@@ -304,14 +305,10 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_chunk_f32_kernel(PromptPara
     for (int tb = 0; tb < TB; ++tb) store_out(t0 - PC, tb, len - (t0 - PC));
   }
 
-  if (wrong) {
-    const int first = first_wrong(wrong, wrong_t0, len, [&](int t) {
-      const float g = reinterpret_cast<const float*>(wp + (size_t)(t >> 6) * p.H * CHUNK_WORK_F32 + 2 * F32_TILES * FRAG_BYTES)[t & 63];
-      return !finite(g) || !finite(vp[t * p.vs + n]);
-    });
+  if (__any(since != NEVER)) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (wrong >> n & 1)
-      for (int t = first + hi; t < len; t += 4) op[t * p.os + n] = __builtin_nanf("");
+    const int first = column_first(since);
+    for (int64_t t = (int64_t)first + hi; t < len; t += 4) op[t * p.os + n] = __builtin_nanf("");
   }
   float s[MB][1][4];
 #pragma unroll

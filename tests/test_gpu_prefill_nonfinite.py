@@ -84,3 +84,33 @@ def test_several_in_one_prompt(act):
     S0 = lay.S.clone()
     run(lay, tok, [400])
     compare(lay, 0, S0[0], tok, slice(0, 400))
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_an_overflow_reaches_back_to_its_own_chunk_at_most(act):
+    """A column of 2^127 whose product with a late key overflows, beside one that
+    has had a NaN since the first chunk, or has one later."""
+    for early, late in ((10, None), (None, 250), (10, 250)):
+        lay = make_layer(1, 1, 64, 64, act, seed=506, ranks=[0])
+        q, k, v, al, be, o = make_tokens(300, 1, 64, 64, act, seed=507)
+        lay.S[:, :, :, 7] = 2.0 ** 127
+        k.zero_()
+        k[:, 0, 0], k[:, 0, 1] = 0.75, -0.75       # nothing of it, but for token 200
+        k[200, 0, :4] = 0.75
+        q.mul_(2.0 ** -10)
+        al.fill_(1.0)
+        be.zero_()
+        if early is not None:
+            v[early, 0, 3] = NAN
+        if late is not None:
+            v[late, 0, 7] = NAN
+        want = torch.einsum("tk,kc->tc", q[:, 0].double(), lay.S[0, 0].double())
+        run(lay, (q, k, v, al, be, o), [300])
+        got = o[:, 0].double()
+        assert torch.isfinite(got[:192, 7]).all() and not torch.isfinite(got[200:, 7]).any()
+        assert ((got[:192, 7] - want[:192, 7]).abs() <= 2.0 ** -7 * want[:192, 7].abs() + 2.0 ** 127 * 64 * 2.0 ** -34 * 8).all()
+        fine = torch.isfinite(got[:, 3])
+        assert fine.tolist() == [early is None or t < early for t in range(300)]
+        others = [c for c in range(64) if c not in (3, 7)]
+        assert torch.isfinite(got[:, others]).all() and torch.isfinite(lay.S[0, 0][:, others]).all()
+        assert not torch.isfinite(lay.S[0, 0, :, 7]).any()
