@@ -18,19 +18,24 @@ constexpr int64_t kMaxTiles = (1 << 22) - 1;
 // Prompts of up to this many tokens go token by token where the launch has
 // both kinds.  A chunk's two launches take about as long for 4 tokens as for 64,
 // the other form's time grows by the token; measured, token by token and in
-// chunks (us): bf16 128 x 128, 1024 tiles of 24 tokens 76 and 97, of 32 92 and 99,
-// 64 tiles of 16 22 and 25, of 24 29 and 25; fp32 128 x 128, 1024 tiles of 32 133
-// and 160, 64 tiles of 32 32 and 31; 64 x 64, 1024 tiles of 64 tokens 60 and 82
-// (fp32 68 and 97), 128 tiles of fp32 of 32 18 and 24, of 64 30 and 25.
+// chunks (us): bf16 128 x 128, 1024 tiles of 24 tokens 75 and 109, of 32 89 and 110,
+// 64 tiles of 16 21 and 25, of 24 28 and 24; fp32 128 x 128, 1024 tiles of 32 133
+// and 155, 64 tiles of 32 30 and 27; 64 x 64, 1024 tiles of 64 tokens 57 and 73
+// (fp32 64 and 80), 128 tiles of fp32 of 32 17 and 21, of 64 28 and 22.
 int short_prompt(const sketchssm_layer* L) { return L->dk == 64 ? 48 : L->act_dtype == SKSSM_F32 ? 32 : 24; }
 // Prompts in segments: up to kSplitTiles (prompt, head) tiles, at least kMinSegs
 // segments of 2^kMinSegShift tokens or more to a prompt on average, at most
 // kMaxSegs (the states between them are joined in order, 4 us each) and kSegTiles
 // of all tiles (the CUs).  Measured on 128 x 128 tiles, whole and in segments (us): 8
-// tiles of 2048 tokens 100 and 94, of 4096 185 and 112, of 12000 505 and 205; 32 of
-// 2048 112 and 112, of 16384 815 and 574; 4 of 32768 1322 and 265 (in at most 24, 319);
-// what stays whole: 8 of 1600 in three 82 and 88; 48 of 4096 221 and 253; 64 of 16384
-// 953 and 1035.
+// tiles of 2048 tokens 126 and 109, of 4096 238 and 127, of 12000 654 and 211; 32 of
+// 2048 137 and 124, of 16384 1011 and 600; 4 of 32768 1724 and 289; what stays whole:
+// 8 of 1600 in three 102 and 103; 48 of 4096 275 and 282; 64 of 16384 1126 and 1156.
+// The smaller shapes, whose transitions cost less, gain within these limits (32 tiles
+// of 2048 tokens: 128 x 64 142 and 96, 64 x 64 109 and 73; of 16384, 1053 and 513, 844
+// and 345) and would beyond (64 of 16384: 1154 and 808, 925 and 642).  fp32 has no
+// launch without outputs and goes whole.  The rule knows totals alone: one prompt of
+// 16384 tokens of 32 heads goes whole, in 1020 us in place of 600, with any other
+// prompt beside it.
 constexpr int kSplitTiles = 32, kSegTiles = 256, kMinSegShift = 9, kMinSegs = 4, kMaxSegs = 48;
 
 // How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
@@ -47,9 +52,9 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   if (!sk::prompt_chunked(L->dk) || nseq == 0) return p;
   // No prompt is longer unless others are empty (a decode batch through this
   // call): one launch for all, which takes a long prompt too (32 heads of 128 x
-  // 128, with the chunks' launches and without: 256 sequences, a token each, 209 and
-  // 195 us, 100 in one prompt 208 and 182, 200 in one 218 and 230; 48 sequences 50
-  // and 43; 1024 780 and 750, 1018 tokens in one prompt 807 and 1044).
+  // 128, with the chunks' launches and without: 256 sequences, a token each, 217 and
+  // 212 us; 48 50 and 42; 1024 819 and 787; all others empty, a prompt of 100 tokens
+  // in the middle of 256 223 and 214, of 200 241 and 295, of 1018 in 1024 910 and 1338).
   if (tokens - nseq < shrt) return p;
   // mostly long prompts: the chunked form takes the short ones too, and one
   // launch is saved
