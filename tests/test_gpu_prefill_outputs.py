@@ -89,3 +89,63 @@ def test_outputs_of_the_last_of_very_many_states(act, n):
         o, S, scale = rule(*(x[i * n:(i + 1) * n] for x in tok[:5]), first[i])
         assert wrong_outputs(tok[5][i * n:(i + 1) * n], o, scale, dk) == (0, 0)
         assert state_off(lay.S[b], S, dk) == 0
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(16, 32), (64, 64), (128, 64), (128, 128)])
+def test_single_tokens_agree_with_the_decode_step(act, dk, dv):
+    """A token through sketchssm_prefill and through sketchssm_full_step: each
+    is off by at most (dk + 8) roundings of 2^-24 of the column's norm (the sum
+    over a column, the update, the output), the outputs by half a step more."""
+    B, H = 5, 3
+    lay, other = (make_layer(B, H, dk, dv, act, seed=360) for _ in range(2))
+    tok = make_tokens(B, H, dk, dv, act, seed=361)
+    S0 = lay.S.clone()
+    run(lay, tok, [1] * B)
+    st = other.new_step()
+    for dst, src in zip((st.q, st.k, st.v, st.gate, st.beta), tok):
+        dst.copy_(src)
+    assert other.full_step(st) == 0
+    torch.cuda.synchronize()
+    assert lay.error_word() == other.error_word() == 0
+    for b in range(B):
+        o, S, scale = rule(*(x[b:b + 1] for x in tok[:5]), S0[b])
+        column = torch.maximum(S.norm(dim=1, keepdim=True), S0[b].double().norm(dim=1, keepdim=True))
+        noise = (dk + 8) * 2.0 ** -24
+        assert ((lay.S[b].double() - other.S[b].double()).abs() <= 2 * noise * column).all()
+        lim = 2 * noise * column[:, 0] * tok[0][b].double().norm(dim=-1, keepdim=True)
+        lim = lim + torch.finfo(tok[5].dtype).eps * (o[0].abs() + lim)
+        assert ((tok[5][b].double() - st.o[b].double()).abs() <= lim).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[2300], [300, 90], [9, 3]], ids=lambda x: "-".join(map(str, x)))
+def test_two_calls_at_once_on_one_layer(act, lens):
+    """Disjoint sequences of one layer, a stream and a ``Prompts`` each, again and
+    again."""
+    n, N = len(lens), sum(lens)
+    lay = make_layer(2 * n + 1, 3, 128, 128, act, seed=370)
+    toks = [make_tokens(N, 3, 128, 128, act, seed=371 + i) for i in range(2)]
+    starts = [sum(lens[:i]) for i in range(n + 1)]
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    from ssm_decode_amd.serving import Prompts
+    seqs = [list(range(0, 2 * n, 2)), list(range(1, 2 * n, 2))]
+    prs = [Prompts(lay, *t, dev(starts), dev(s)) for t, s in zip(toks, seqs)]
+    S0 = lay.S.clone()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for rep in range(3):
+        lay.S.copy_(S0)
+        for t in toks:
+            t[5].fill_(SENTINEL)
+        torch.cuda.synchronize()
+        for st, p in zip(streams, prs):
+            assert lay.prefill(p, stream=st.cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert lay.error_word() == 0
+        for t, s in zip(toks, seqs):
+            for i in range(n):
+                part = slice(starts[i], starts[i + 1])
+                o, S, scale = rule(*(x[part] for x in t[:5]), S0[s[i]])
+                assert wrong_outputs(t[5][part], o, scale, 128) == (0, 0)
+                assert state_off(lay.S[s[i]], S, 128) == 0
+        assert torch.equal(lay.S[2 * n], S0[2 * n])
