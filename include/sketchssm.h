@@ -120,12 +120,15 @@ extern "C" {
 /* bits OR-ed into *err by the kernels */
 #define SKSSM_ERRBIT_COUNT 1  /* count outside [0, W] (or == W at a read) */
 #define SKSSM_ERRBIT_GROUP 2  /* Mamba-2 heads of one B/C group disagree on count */
-#define SKSSM_ERRBIT_SEQ 4    /* sketchssm_flush_seqs, _prefill, _state_save, _state_load: a
-                                 listed index outside [0, batch), or a sequence listed twice
-                                 (flush_seqs: a tile claimed twice); _prefill: a list of
-                                 first tokens that falls, or leaves [0, tokens] */
+#define SKSSM_ERRBIT_SEQ 4    /* sketchssm_flush_seqs, _prefill, _scan, _conv, _state_save,
+                                 _state_load: a listed index outside [0, batch), or a sequence
+                                 listed twice (flush_seqs: a tile claimed twice); _prefill, _scan,
+                                 _conv: a list of first tokens that falls, or leaves [0, tokens];
+                                 _reorder: a parent outside its group */
 #define SKSSM_ERRBIT_SLOT 8   /* sketchssm_state_save/_load: a cache slot outside [0, slots), or
                                  a slot that an earlier entry of a save's list has */
+#define SKSSM_ERRBIT_LOGIT 16 /* sketchssm_beam_select: a logit or a score that is a NaN or a
+                                 positive infinity */
 
 /* activations of sketchssm_group_norm */
 #define SKSSM_ACT_NONE 0
@@ -441,6 +444,135 @@ typedef struct {
   float eps;                 /* finite, >= 0 */
 } sketchssm_norm;
 int sketchssm_group_norm(const sketchssm_norm* norm, void* hip_stream);
+
+/* Prompts of the selective state space scan (SKSSM_MAMBA2): token rows of nseq
+ * prompts, one behind the other, as sketchssm_prompts, with the queries and keys of
+ * the layer's groups (all strides but dt's a multiple of 16 bytes). */
+typedef struct {
+  const void* q;             /* [tokens][G][dk] act dtype */
+  const void* k;             /* [tokens][G][dk] act dtype */
+  const void* v;             /* [tokens][H][dv] act dtype */
+  const void* dt;            /* [tokens][H] act dtype, as sketchssm_read takes it; 0 or more */
+  void* o;                   /* [tokens][H][dv] act dtype (output); overlaps no input */
+  int64_t q_stride, k_stride, v_stride, dt_stride, o_stride;
+  int32_t tokens;            /* rows of q, k, v, dt and o */
+  int32_t nseq;              /* prompts, at most layer->batch */
+  const int32_t* seq_start;  /* as sketchssm_prompts */
+  const int32_t* seqs;
+  const int32_t* has_state;
+  int32_t prime;
+  void* work;                /* workspace of sketchssm_scan_workspace_bytes (16-byte aligned; may be
+                                NULL when that is 0), overwritten by the call */
+  int64_t work_bytes;
+} sketchssm_scan_prompts;
+
+/* Prompts through the selective state space scan: for each of a prompt's tokens
+ * in order, as sketchssm_full_step,
+ *   S <- a S + dt k v^T,  a = exp(-dt exp(A_h)),  o = S^T q,
+ * with bufs->A, and, with prime, the sketch that sketchssm_read starts from.  Rings,
+ * lists, empty prompts, errors and the workspace as for sketchssm_prefill.  Sums run
+ * in fp32, and products are those of fp32 operands; the decays' logarithms are
+ * summed in 64 bits.  An infinity or a NaN in a token's row or in the state reaches
+ * what the recurrence brings it to (as one or the other) and no earlier token.
+ * Other families return SKSSM_EDIM; prime with SKSSM_COEF_STATE is SKSSM_EFLAG. */
+int sketchssm_scan(const sketchssm_layer* layer, const sketchssm_buffers* bufs,
+                   const sketchssm_scan_prompts* prompts, void* hip_stream);
+
+/* Bytes of prompts->work that sketchssm_scan needs for this many tokens and
+ * prompts, or a negative SKSSM_E* code, as sketchssm_prefill_workspace_bytes. */
+int64_t sketchssm_scan_workspace_bytes(const sketchssm_layer* layer, int32_t tokens, int32_t nseq);
+
+/* Part of a convolution's channels, written to rows of their own. */
+typedef struct {
+  void* y;                   /* [tokens][channels of the piece]; overlaps no input */
+  int64_t y_stride;          /* elements from a token's row to the next: as sketchssm_prompts */
+  int32_t channels;          /* 0 (the piece is left out) or more, a multiple of 8 */
+  int32_t unit;              /* 0, or the width of the heads that are brought to unit length:
+                                16, 64 or 128, of which channels is a multiple */
+} sketchssm_conv_piece;
+
+/* The short causal convolution of the rows that a layer's queries, keys and
+ * values come from, with the inputs that each sequence holds:
+ *   y_t = a(bias + sum_j weight_j x_(t - taps + 1 + j)),  j = 0 .. taps - 1,
+ * for each channel, with a = the activation; x before a prompt's first token is what
+ * its sequence holds (has_state 0: zeros).  A unit piece's heads are divided by
+ * sqrt(sum of their squares + eps) behind the activation.  Afterwards the sequence
+ * holds its last taps - 1 inputs.  Sums are fp32, rounded once to y. */
+typedef struct {
+  const void* x;             /* [tokens][channels] */
+  int64_t x_stride;
+  const float* weight;       /* [channels][taps]; the last tap is the token's own */
+  const float* bias;         /* [channels], or NULL */
+  void* state;               /* [batch][taps - 1][channels]: the sequences' last inputs, oldest first */
+  sketchssm_conv_piece piece[3]; /* the channels in order, the channels of a row together */
+  int32_t taps;              /* 2 to 8 */
+  int32_t dtype;             /* of x, y and state: SKSSM_F32 or SKSSM_BF16 */
+  int32_t activation;        /* SKSSM_ACT_* */
+  float eps;                 /* finite, >= 0 */
+  int32_t batch;             /* sequences of state */
+  int32_t tokens;            /* rows of x and of the pieces */
+  int32_t nseq;              /* prompts, at most batch */
+  const int32_t* seq_start;  /* as sketchssm_prompts; NULL: one token to each (tokens = nseq), a decode step */
+  const int32_t* seqs;       /* as sketchssm_prompts */
+  const int32_t* has_state;  /* as sketchssm_prompts */
+  int32_t* err;              /* [1] device error word (SKSSM_ERRBIT_SEQ), never cleared here */
+} sketchssm_convolution;
+
+/* Lists and errors as for sketchssm_prefill: a list that falls or leaves [0, tokens]
+ * is refused whole, a sequence outside the batch or listed before refuses its
+ * prompt; a prompt of no tokens leaves what its sequence holds (has_state 0: zeros).
+ * Rows that no prompt holds are neither read nor written. */
+int sketchssm_conv(const sketchssm_convolution* conv, void* hip_stream);
+
+/* Selection of beams.  Sequences are in groups of `beams` consecutive ones (a
+ * request's beams).  From each group the best `beams` candidates of
+ *   score_b + x_bj - log sum_j' exp(x_bj')
+ * over its sequences b and the vocabulary j are taken, in falling order of that
+ * number, ties to the lowest b * vocab + j.  A logit of minus infinity rules its
+ * token out, a score of minus infinity its beam (as the second and further beams of a
+ * first step).  An ended beam has one candidate: end_token at its own score.  A NaN or
+ * a positive infinity sets SKSSM_ERRBIT_LOGIT and takes its beam out.  Where a group has
+ * too few candidates, the places behind them are empty: parent the sequence itself,
+ * token -1, score minus infinity, not ended.  Scores are formed in 64 bits from sums
+ * of exponentials in fp32, and rounded once. */
+typedef struct {
+  const void* logits;        /* [groups * beams][vocab], rows at any alignment of an element */
+  int64_t stride;            /* elements from a row to the next: at least vocab, at most 2^31 - 1 */
+  const float* scores;       /* [groups * beams] sums of the logarithms so far */
+  const int32_t* ended;      /* [groups * beams] not 0: the beam has ended; NULL: none has */
+  float* new_scores;         /* [groups * beams]; may be scores */
+  int32_t* new_ended;        /* [groups * beams]; may be ended.  1 where a parent had ended or the
+                                token is end_token */
+  int32_t* parents;          /* [groups * beams]: the sequence that each goes on from */
+  int32_t* tokens;           /* [groups * beams] */
+  int32_t* err;              /* [1] device error word, never cleared here */
+  int32_t groups, beams;     /* beams: 1 to 16 */
+  int32_t vocab;             /* 1 to 2^24 */
+  int32_t dtype;             /* of the logits: SKSSM_F32 or SKSSM_BF16 */
+  int32_t end_token;         /* -1 (none) to vocab - 1 */
+  void* work;                /* workspace of sketchssm_beam_workspace_bytes (16-byte aligned) */
+  int64_t work_bytes;
+} sketchssm_beams;
+int sketchssm_beam_select(const sketchssm_beams* beams, void* hip_stream);
+
+/* Bytes of beams->work, or a negative SKSSM_E* code. */
+int64_t sketchssm_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int32_t dtype);
+
+/* Rows of sequences besides a layer's buffers, such as a convolution's state. */
+typedef struct {
+  void* data;                /* DEVICE [batch] rows, 16-byte aligned */
+  int64_t row_bytes;         /* a multiple of 16 */
+} sketchssm_rows;
+
+/* Behind a selection of beams: within each group of `beams` (1 to 16) consecutive
+ * sequences, sequence b becomes a copy of sequence parents[b] (DEVICE [batch], 4-byte
+ * aligned, each within the group) in every buffer of the layer that holds something
+ * of a sequence (S, U, the ring with its counts, maps, state copies and factors, as
+ * the layer has them) and in nextra (0 to 4) further ones, in place.  A group with a
+ * parent outside it sets SKSSM_ERRBIT_SEQ and is left as it is.  layer->batch is a
+ * multiple of beams. */
+int sketchssm_reorder(const sketchssm_layer* layer, const sketchssm_buffers* bufs, const sketchssm_rows* extra,
+                      int32_t nextra, const int32_t* parents, int32_t beams, void* hip_stream);
 
 /* Library version (major * 10000 + minor * 100 + patch). */
 int sketchssm_version(void);

@@ -23,13 +23,15 @@ SKSSM_PULLBACK_SERIAL, SKSSM_PULLBACK_WY, SKSSM_PULLBACK_PROJ = 0, 1, 2
 SKSSM_OK, SKSSM_EINVAL, SKSSM_EDIM, SKSSM_EDTYPE, SKSSM_EFLAG, SKSSM_ELAUNCH = 0, -1, -2, -3, -4, -5
 SKSSM_ESCRATCH = -6
 SKSSM_NOALLOC_SCRATCH_BYTES = 16777216
-SKSSM_ERRBIT_COUNT, SKSSM_ERRBIT_GROUP, SKSSM_ERRBIT_SEQ, SKSSM_ERRBIT_SLOT = 1, 2, 4, 8
+SKSSM_ERRBIT_COUNT, SKSSM_ERRBIT_GROUP, SKSSM_ERRBIT_SEQ, SKSSM_ERRBIT_SLOT, SKSSM_ERRBIT_LOGIT = 1, 2, 4, 8, 16
 SKSSM_ACT_NONE, SKSSM_ACT_SILU, SKSSM_ACT_SIGMOID = 0, 1, 2
 
 ENTRY_POINTS = ("sketchssm_read", "sketchssm_flush", "sketchssm_flush_seqs", "sketchssm_full_step",
                 "sketchssm_replay_step", "sketchssm_workspace_bytes", "sketchssm_read_noalloc",
                 "sketchssm_prefill", "sketchssm_prefill_workspace_bytes", "sketchssm_state_save",
-                "sketchssm_state_load", "sketchssm_group_norm", "sketchssm_version")
+                "sketchssm_state_load", "sketchssm_group_norm", "sketchssm_scan", "sketchssm_scan_workspace_bytes",
+                "sketchssm_conv", "sketchssm_beam_select", "sketchssm_beam_workspace_bytes", "sketchssm_reorder",
+                "sketchssm_version")
 
 
 class sketchssm_layer(C.Structure):
@@ -76,6 +78,39 @@ class sketchssm_norm(C.Structure):
                 ("activation", C.c_int32), ("gate_first", C.c_int32), ("eps", C.c_float)]
 
 
+class sketchssm_scan_prompts(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("dt", C.c_void_p), ("o", C.c_void_p),
+                ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("dt_stride", C.c_int64), ("o_stride", C.c_int64),
+                ("tokens", C.c_int32), ("nseq", C.c_int32), ("seq_start", C.c_void_p),
+                ("seqs", C.c_void_p), ("has_state", C.c_void_p), ("prime", C.c_int32),
+                ("work", C.c_void_p), ("work_bytes", C.c_int64)]
+
+
+class sketchssm_conv_piece(C.Structure):
+    _fields_ = [("y", C.c_void_p), ("y_stride", C.c_int64), ("channels", C.c_int32), ("unit", C.c_int32)]
+
+
+class sketchssm_convolution(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("x_stride", C.c_int64), ("weight", C.c_void_p), ("bias", C.c_void_p),
+                ("state", C.c_void_p), ("piece", sketchssm_conv_piece * 3), ("taps", C.c_int32),
+                ("dtype", C.c_int32), ("activation", C.c_int32), ("eps", C.c_float), ("batch", C.c_int32),
+                ("tokens", C.c_int32), ("nseq", C.c_int32), ("seq_start", C.c_void_p), ("seqs", C.c_void_p),
+                ("has_state", C.c_void_p), ("err", C.c_void_p)]
+
+
+class sketchssm_beams(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("stride", C.c_int64), ("scores", C.c_void_p), ("ended", C.c_void_p),
+                ("new_scores", C.c_void_p), ("new_ended", C.c_void_p), ("parents", C.c_void_p),
+                ("tokens", C.c_void_p), ("err", C.c_void_p), ("groups", C.c_int32), ("beams", C.c_int32),
+                ("vocab", C.c_int32), ("dtype", C.c_int32), ("end_token", C.c_int32), ("work", C.c_void_p),
+                ("work_bytes", C.c_int64)]
+
+
+class sketchssm_rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("row_bytes", C.c_int64)]
+
+
 _lib = None
 
 
@@ -116,8 +151,18 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         lib.sketchssm_state_load.argtypes = [L, Bf, Ca, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
                                              C.c_void_p]
         lib.sketchssm_group_norm.argtypes = [C.POINTER(sketchssm_norm), C.c_void_p]
+        Sc = C.POINTER(sketchssm_scan_prompts)
+        lib.sketchssm_scan.argtypes = [L, Bf, Sc, C.c_void_p]
+        lib.sketchssm_scan_workspace_bytes.argtypes = [L, C.c_int32, C.c_int32]
+        lib.sketchssm_scan_workspace_bytes.restype = C.c_int64
+        lib.sketchssm_conv.argtypes = [C.POINTER(sketchssm_convolution), C.c_void_p]
+        lib.sketchssm_beam_select.argtypes = [C.POINTER(sketchssm_beams), C.c_void_p]
+        lib.sketchssm_beam_workspace_bytes.argtypes = [C.c_int32] * 4
+        lib.sketchssm_beam_workspace_bytes.restype = C.c_int64
+        lib.sketchssm_reorder.argtypes = [L, Bf, C.POINTER(sketchssm_rows), C.c_int32, C.c_void_p, C.c_int32, C.c_void_p]
         for name in ("sketchssm_prefill", "sketchssm_state_save", "sketchssm_state_load",
-                     "sketchssm_group_norm"):
+                     "sketchssm_group_norm", "sketchssm_scan", "sketchssm_conv", "sketchssm_beam_select",
+                     "sketchssm_reorder"):
             getattr(lib, name).restype = C.c_int
         lib.sketchssm_version.argtypes = []
         lib.sketchssm_version.restype = C.c_int
@@ -193,6 +238,33 @@ def sketchssm_state_load(layer, bufs, cache, seqs, slots, n, prime, stream=None)
 
 def sketchssm_group_norm(norm, stream=None) -> int:
     return load().sketchssm_group_norm(_ref(norm, sketchssm_norm), stream)
+
+
+def sketchssm_scan(layer, bufs, prompts, stream=None) -> int:
+    return load().sketchssm_scan(_ref(layer, sketchssm_layer), _ref(bufs, sketchssm_buffers),
+                                 _ref(prompts, sketchssm_scan_prompts), stream)
+
+
+def sketchssm_scan_workspace_bytes(layer, tokens, nseq) -> int:
+    return load().sketchssm_scan_workspace_bytes(_ref(layer, sketchssm_layer), int(tokens), int(nseq))
+
+
+def sketchssm_conv(conv, stream=None) -> int:
+    return load().sketchssm_conv(_ref(conv, sketchssm_convolution), stream)
+
+
+def sketchssm_beam_select(beams, stream=None) -> int:
+    return load().sketchssm_beam_select(_ref(beams, sketchssm_beams), stream)
+
+
+def sketchssm_beam_workspace_bytes(groups, beams, vocab, dtype) -> int:
+    return load().sketchssm_beam_workspace_bytes(int(groups), int(beams), int(vocab), int(dtype))
+
+
+def sketchssm_reorder(layer, bufs, extra, nextra, parents, beams, stream=None) -> int:
+    """extra: an array of nextra sketchssm_rows (or None); parents: a device address."""
+    return load().sketchssm_reorder(_ref(layer, sketchssm_layer), _ref(bufs, sketchssm_buffers), extra, int(nextra),
+                                    parents, int(beams), stream)
 
 
 def sketchssm_version() -> int:

@@ -1,0 +1,248 @@
+// Selection of beams: for each group of `beams` sequences, the best `beams` of
+//   score_b + x_bj - log sum_j' exp(x_bj')
+// over its beams b and the vocabulary j, in falling order, ties to the lowest
+// b * vocab + j.  An ended beam has one candidate, its end token at its own score.
+//
+// Bound by memory: the logits, once.  One launch takes each row in parts, a part's
+// values in registers: their maximum, the sum of their exponentials and the best of
+// them, by value (a row's order is that of its values, so no rounding enters it);
+// a second joins a group's parts in 64 bits and takes the best of its candidates.
+#include "sk_beam.hpp"
+#include "sk_device.hpp"
+
+namespace sk {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A value and its index as one number that is larger for the better candidate:
+// the value's order above, the lower index above the higher.  (+ 0.f: a negative
+// zero is a zero.)
+__device__ __forceinline__ uint64_t beam_key(float x, int index) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  const uint32_t order = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return (uint64_t)order << 32 | (uint32_t)~index;
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t order = (uint32_t)(k >> 32);
+  return __uint_as_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);
+}
+__device__ __forceinline__ int key_index(uint64_t k) { return (int)~(uint32_t)k; }
+
+__device__ __forceinline__ uint64_t wave_max(uint64_t k) {
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const uint64_t o = (uint64_t)__shfl_xor((unsigned long long)k, s);
+    k = o > k ? o : k;
+  }
+  return k;
+}
+__device__ __forceinline__ float wave_maxf(float x) {
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) x = fmaxf(x, __shfl_xor(x, s));
+  return x;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
+  constexpr int N = 16 / (int)sizeof(T), E = 64 / (int)sizeof(T), V = E / N;      // values of a vector, of a lane; vectors
+  __shared__ uint64_t s_key[4 * BEAM_MAX];
+  const int row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  if (p.ended && p.ended[row] != 0) return;
+  const T* X = reinterpret_cast<const T*>(p.logits) + (int64_t)row * p.stride;
+  // Rows of any length begin anywhere: vectors of whole 16 bytes of memory, the
+  // first of which may begin before the row.
+  const int skew = (int)((reinterpret_cast<uintptr_t>(X) & 15) / sizeof(T));
+  const int first = part * beam_part((int)sizeof(T)) - skew;
+  float x[E];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int at = first + (v * BEAM_THREADS + tid) * N;
+    if (at >= 0 && at + N <= p.vocab) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(X + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) {
+          x[v * N + 2 * e] = __uint_as_float(w[e] << 16);
+          x[v * N + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        } else {
+          x[v * N + e] = __uint_as_float(w[e]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[v * N + e] = at + e >= 0 && at + e < p.vocab ? ld(X + at + e) : -__builtin_inff();
+    }
+  }
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);
+  top = wave_maxf(top);
+  // (an infinity or a NaN among the values makes the sum a NaN)
+  float sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum += x[e] == -__builtin_inff() ? 0.f : expf(x[e] - top);
+  sum = wave_sum(sum);
+  BeamPart* out = p.part + (int64_t)row * p.parts + part;
+  if (lane == 0) {
+    out->top[wv] = top;
+    out->sum[wv] = sum;
+  }
+  auto index = [&](int e) { return first + ((e / N) * BEAM_THREADS + tid) * N + e % N; };
+  uint64_t last = ~0ull;
+  for (int r = 0; r < p.beams; ++r) {            // the best of what is worse than the last
+    uint64_t best = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint64_t k = x[e] > -__builtin_inff() ? beam_key(x[e], index(e)) : 0;
+      best = k < last && k > best ? k : best;
+    }
+    last = wave_max(best);
+    if (lane == 0) s_key[wv * BEAM_MAX + r] = last;
+    if (last == 0) last = 1;                     // (none is left)
+  }
+  __syncthreads();
+  if (wv == 0) {                                 // the best of the waves': a lane's place is how many are better
+    const int n = 4 * p.beams;
+    const uint64_t k = lane < n ? s_key[lane / p.beams * BEAM_MAX + lane % p.beams] : 0;
+    int place = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint64_t o = s_key[j / p.beams * BEAM_MAX + j % p.beams];
+      place += o > k || (o == k && j < lane);
+    }
+    if (lane < n && place < p.beams) {
+      out->value[place] = k ? key_value(k) : -__builtin_inff();
+      out->index[place] = key_index(k);
+    }
+  }
+}
+
+// One workgroup per group.
+__global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(BeamParams p) {
+  __shared__ double s_lse[BEAM_MAX], s_best[4], s_score[BEAM_MAX];
+  __shared__ float s_in[BEAM_MAX];
+  __shared__ int s_ended[BEAM_MAX];
+  __shared__ int64_t s_at[4], s_pick[BEAM_MAX];
+  const int g = blockIdx.x, k = p.beams, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  constexpr double NONE = -__builtin_inf();
+  constexpr int64_t FAR = INT64_MAX;
+  if (tid < k) {
+    const int row = g * k + tid;
+    s_in[tid] = p.scores[row];
+    s_ended[tid] = p.ended ? p.ended[row] != 0 : 0;
+  }
+  __syncthreads();
+  for (int b = wv; b < k; b += 4) {              // the rows' sums: a wave a row
+    const BeamPart* part = p.part + (int64_t)(g * k + b) * p.parts;
+    const int n = s_ended[b] ? 0 : 4 * p.parts;
+    float top = -__builtin_inff();
+    for (int j = lane; j < n; j += 64) top = fmaxf(top, part[j >> 2].top[j & 3]);
+    top = wave_maxf(top);
+    double sum = 0;
+    for (int j = lane; j < n; j += 64) {
+      const float t = part[j >> 2].top[j & 3], s = part[j >> 2].sum[j & 3];
+      sum += s == 0.f ? 0. : exp((double)t - top) * s;
+    }
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) sum += __shfl_xor(sum, s);
+    if (lane == 0) {
+      // a row without a finite sum, and a score that is none, take the beam out; all
+      // ruled out is no error
+      const float in = s_in[b];
+      const bool wrong = !(fabs(sum) < __builtin_inf()) || in != in || in == __builtin_inff();
+      if (wrong) atomicOr(p.err, ERRBIT_LOGIT);
+      if (wrong || in == -__builtin_inff()) s_in[b] = -__builtin_inff();
+      s_lse[b] = (double)top + log(sum);
+    }
+  }
+  __syncthreads();
+  // candidate c of beam b: its score and b * vocab + j
+  const int per = p.parts * k, all = per * k;
+  auto candidate = [&](int c, double* score, int64_t* at) {
+    const int b = c / per, j = c - b * per;
+    *score = NONE;
+    *at = FAR;
+    const float in = s_in[b];
+    if (in == -__builtin_inff()) return;
+    if (s_ended[b]) {
+      if (j == 0) {
+        *score = in;
+        *at = (int64_t)b * p.vocab + (p.end_token > 0 ? p.end_token : 0);
+      }
+      return;
+    }
+    const BeamPart* part = p.part + (int64_t)(g * k + b) * p.parts + j / k;
+    const float v = part->value[j % k];
+    if (v == -__builtin_inff()) return;
+    *score = (double)in + ((double)v - s_lse[b]);
+    *at = (int64_t)b * p.vocab + part->index[j % k];
+  };
+  auto better = [](double s, int64_t a, double t, int64_t b) { return s > t || (s == t && a < b); };
+  double last = __builtin_inf();
+  int64_t last_at = -1;
+  for (int r = 0; r < k; ++r) {                  // the best behind the last
+    double best = NONE;
+    int64_t best_at = FAR;
+    for (int c = tid; c < all; c += BEAM_THREADS) {
+      double s;
+      int64_t a;
+      candidate(c, &s, &a);
+      if (better(last, last_at, s, a) && better(s, a, best, best_at)) {
+        best = s;
+        best_at = a;
+      }
+    }
+    for (int s = 1; s < 64; s *= 2) {
+      const double t = __shfl_xor(best, s);
+      const int64_t a = __shfl_xor((long long)best_at, s);
+      if (better(t, a, best, best_at)) {
+        best = t;
+        best_at = a;
+      }
+    }
+    if (lane == 0) {
+      s_best[wv] = best;
+      s_at[wv] = best_at;
+    }
+    __syncthreads();
+    best = s_best[0];
+    best_at = s_at[0];
+    for (int w = 1; w < 4; ++w)
+      if (better(s_best[w], s_at[w], best, best_at)) {
+        best = s_best[w];
+        best_at = s_at[w];
+      }
+    if (tid == 0) {
+      s_score[r] = best;
+      s_pick[r] = best_at;
+    }
+    last = best;
+    last_at = best_at;
+    __syncthreads();
+  }
+  if (tid < k) {
+    const int row = g * k + tid;
+    const int64_t at = s_pick[tid];
+    const bool none = at == FAR;
+    const int b = none ? tid : (int)(at / p.vocab);
+    const bool over = !none && s_ended[b];
+    const int token = none ? -1 : over ? p.end_token : (int)(at % p.vocab);
+    p.parents[row] = g * k + b;
+    p.tokens[row] = token;
+    p.new_scores[row] = none ? -__builtin_inff() : (float)s_score[tid];
+    p.new_ended[row] = over || (!none && token == p.end_token);
+  }
+}
+
+}  // namespace
+
+int launch_beam_select(int dtype, const BeamParams& p, hipStream_t st) {
+  const dim3 grid((unsigned)p.parts * p.groups * p.beams), block(BEAM_THREADS);
+  if (dtype == DT_F32) hipLaunchKernelGGL((beam_part_kernel<float>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((beam_part_kernel<bf16>), grid, block, 0, st, p);
+  hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)p.groups), block, 0, st, p);
+  return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+}  // namespace sk

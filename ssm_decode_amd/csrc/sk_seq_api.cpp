@@ -1,0 +1,265 @@
+// C ABI of the scan over prompts, the short convolution, the selection of beams
+// and the sequences' reordering.  Every check runs before any HIP call, so an
+// invalid call launches nothing and writes nothing.
+#include <math.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+#include "sketchssm.h"
+#include "sk_beam.hpp"
+#include "sk_conv.hpp"
+#include "sk_scan.hpp"
+#include "sk_serve_host.hpp"
+
+using namespace sk::host;
+
+namespace {
+
+int es_of(int32_t dtype) { return dtype == SKSSM_F32 ? 4 : 2; }
+
+// How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
+// none), all of them or those of more than `shrt` tokens; in segments of
+// 2^seg_shift tokens (0: whole), with the bytes of their states.
+struct Plan {
+  int64_t chunked, nsegs, bytes;
+  bool all;
+  int seg_shift, shrt;
+};
+Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
+  (void)L; (void)tokens; (void)nseq;
+  return Plan{};
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sketchssm_scan_workspace_bytes(const sketchssm_layer* layer, int32_t tokens, int32_t nseq) {
+  try {
+    if (int rc = check_layer(layer)) return rc;
+    if (layer->family != SKSSM_MAMBA2 || tokens < 0 || nseq < 0 || nseq > layer->batch) return SKSSM_EDIM;
+    if ((int64_t)nseq * layer->heads > kMaxTiles) return SKSSM_EDIM;
+    const Plan pl = plan(layer, tokens, nseq);
+    return pl.nsegs * layer->heads > kMaxTiles ? SKSSM_EDIM : pl.bytes;
+  } catch (...) {
+    return SKSSM_ELAUNCH;
+  }
+}
+
+int sketchssm_scan(const sketchssm_layer* layer, const sketchssm_buffers* bufs, const sketchssm_scan_prompts* pr,
+                   void* hip_stream) {
+  try {
+    int rc = check_layer(layer);
+    if (rc) return rc;
+    if (!bufs || !pr) return SKSSM_EINVAL;
+    const int64_t need = sketchssm_scan_workspace_bytes(layer, pr->tokens, pr->nseq);
+    if (need < 0) return (int)need;
+    if ((rc = check_sketch(layer, bufs, pr->prime))) return rc;
+    if (pr->nseq == 0) return SKSSM_OK;
+    const int H = layer->heads, G = layer->qk_groups, dk = layer->dk, dv = layer->dv;
+    const int es = es_of(layer->act_dtype);
+    if (!aligned(bufs->S, 16) || !aligned(bufs->count, 16) || !aligned(bufs->err, 16) || !aligned(bufs->A, 16))
+      return SKSSM_EINVAL;
+    if (!aligned(pr->seq_start, 4)) return SKSSM_EINVAL;
+    if ((pr->seqs && !aligned(pr->seqs, 4)) || (pr->has_state && !aligned(pr->has_state, 4))) return SKSSM_EINVAL;
+    if (pr->tokens > 0) {
+      if (!aligned(pr->q, 16) || !aligned(pr->k, 16) || !aligned(pr->v, 16) || !aligned(pr->o, 16) ||
+          !aligned(pr->dt, es))
+        return SKSSM_EINVAL;
+      if (!row_stride(pr->q_stride, (int64_t)G * dk, es) || !row_stride(pr->k_stride, (int64_t)G * dk, es) ||
+          !row_stride(pr->v_stride, (int64_t)H * dv, es) || !row_stride(pr->o_stride, (int64_t)H * dv, es) ||
+          pr->dt_stride < H || pr->dt_stride > kMaxStride)
+        return SKSSM_EDIM;
+    }
+    if (need > 0 && (!aligned(pr->work, 16) || pr->work_bytes < need)) return SKSSM_EINVAL;
+    sk::ScanParams p{};
+    p.B = layer->batch;
+    p.H = H;
+    p.G = G;
+    p.A = bufs->A;
+    p.tokens = pr->tokens;
+    p.nseq = pr->nseq;
+    p.q = pr->q;
+    p.k = pr->k;
+    p.v = pr->v;
+    p.gate = static_cast<const float*>(pr->dt);
+    p.o = pr->o;
+    p.qs = pr->q_stride;
+    p.ks = pr->k_stride;
+    p.vs = pr->v_stride;
+    p.gs = pr->dt_stride;
+    p.os = pr->o_stride;
+    p.start = pr->seq_start;
+    p.seqs = pr->seqs;
+    p.has_state = pr->has_state;
+    p.S = bufs->S;
+    p.count = bufs->count;
+    p.err = bufs->err;
+    p.prime = pr->prime;
+    if (pr->prime) fill_sketch(&p.sk, layer, bufs);
+    hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
+    p.len_hi = INT32_MAX;
+    return sk::launch_scan_step(dk, dv, layer->act_dtype, p, st);
+  } catch (...) {
+    return SKSSM_ELAUNCH;
+  }
+}
+
+int sketchssm_conv(const sketchssm_convolution* cv, void* hip_stream) {
+  try {
+    if (!cv) return SKSSM_EINVAL;
+    if (cv->dtype != SKSSM_F32 && cv->dtype != SKSSM_BF16) return SKSSM_EDTYPE;
+    const int es = es_of(cv->dtype);
+    if (cv->activation < SKSSM_ACT_NONE || cv->activation > SKSSM_ACT_SIGMOID) return SKSSM_EFLAG;
+    if (cv->taps < 2 || cv->taps > sk::CONV_MAX_TAPS) return SKSSM_EDIM;
+    if (!(isfinite(cv->eps) && cv->eps >= 0.f)) return SKSSM_EINVAL;
+    if (cv->batch < 0 || cv->tokens < 0 || cv->nseq < 0 || cv->nseq > cv->batch || cv->nseq > kMaxTiles) return SKSSM_EDIM;
+    if (!cv->seq_start && cv->tokens != cv->nseq) return SKSSM_EDIM;
+    sk::ConvParams p{};
+    int64_t channels = 0;
+    for (int i = 0; i < sk::CONV_PIECES; ++i) {
+      const sketchssm_conv_piece& q = cv->piece[i];
+      if (q.channels < 0 || q.channels % 8 != 0) return SKSSM_EDIM;
+      if (q.unit != 0 && q.unit != 16 && q.unit != 64 && q.unit != 128) return SKSSM_EDIM;
+      if (q.unit != 0 && q.channels % q.unit != 0) return SKSSM_EDIM;
+      p.piece[i].y = q.y;
+      p.piece[i].ys = q.y_stride;
+      p.piece[i].first = (int)channels;
+      p.piece[i].size = q.channels;
+      p.piece[i].unit = q.unit;
+      channels += q.channels;
+    }
+    if (channels > kMaxStride) return SKSSM_EDIM;
+    if (cv->nseq == 0 || channels == 0) return SKSSM_OK;
+    if (!aligned(cv->weight, 16) || (cv->bias && !aligned(cv->bias, 16)) || !aligned(cv->state, 16) ||
+        !aligned(cv->err, 4))
+      return SKSSM_EINVAL;
+    if ((cv->seq_start && !aligned(cv->seq_start, 4)) || (cv->seqs && !aligned(cv->seqs, 4)) ||
+        (cv->has_state && !aligned(cv->has_state, 4)))
+      return SKSSM_EINVAL;
+    if (cv->tokens > 0) {
+      if (!aligned(cv->x, 16)) return SKSSM_EINVAL;
+      if (!row_stride(cv->x_stride, channels, es)) return SKSSM_EDIM;
+      for (int i = 0; i < sk::CONV_PIECES; ++i) {
+        if (p.piece[i].size == 0) continue;
+        if (!aligned(p.piece[i].y, 16)) return SKSSM_EINVAL;
+        if (!row_stride(p.piece[i].ys, p.piece[i].size, es)) return SKSSM_EDIM;
+      }
+    }
+    p.x = cv->x;
+    p.xs = cv->x_stride;
+    p.weight = cv->weight;
+    p.bias = cv->bias;
+    p.state = cv->state;
+    p.B = cv->batch;
+    p.channels = (int)channels;
+    p.act = cv->activation;
+    p.tokens = cv->tokens;
+    p.nseq = cv->nseq;
+    p.start = cv->seq_start;
+    p.seqs = cv->seqs;
+    p.has_state = cv->has_state;
+    p.err = cv->err;
+    p.eps = cv->eps;
+    p.shift = 5;
+    return sk::launch_conv(cv->dtype, cv->taps, p, reinterpret_cast<hipStream_t>(hip_stream));
+  } catch (...) {
+    return SKSSM_ELAUNCH;
+  }
+}
+
+int64_t sketchssm_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int32_t dtype) {
+  if (dtype != SKSSM_F32 && dtype != SKSSM_BF16) return SKSSM_EDTYPE;
+  if (groups < 0 || beams < 1 || beams > sk::BEAM_MAX || vocab < 1 || vocab > 1 << 24) return SKSSM_EDIM;
+  const int64_t parts = (int64_t)groups * beams * sk::beam_parts(vocab, es_of(dtype));
+  return parts > kMaxTiles ? SKSSM_EDIM : parts * (int64_t)sizeof(sk::BeamPart);
+}
+
+int sketchssm_beam_select(const sketchssm_beams* bm, void* hip_stream) {
+  try {
+    if (!bm) return SKSSM_EINVAL;
+    const int64_t need = sketchssm_beam_workspace_bytes(bm->groups, bm->beams, bm->vocab, bm->dtype);
+    if (need < 0) return (int)need;
+    if (bm->end_token < -1 || bm->end_token >= bm->vocab) return SKSSM_EDIM;
+    if (bm->stride < bm->vocab || bm->stride > INT32_MAX) return SKSSM_EDIM;
+    if (bm->groups == 0) return SKSSM_OK;
+    if (!aligned(bm->logits, es_of(bm->dtype)) || !aligned(bm->scores, 4) || (bm->ended && !aligned(bm->ended, 4)) ||
+        !aligned(bm->new_scores, 4) || !aligned(bm->new_ended, 4) || !aligned(bm->parents, 4) ||
+        !aligned(bm->tokens, 4) || !aligned(bm->err, 4))
+      return SKSSM_EINVAL;
+    if (!aligned(bm->work, 16) || bm->work_bytes < need) return SKSSM_EINVAL;
+    sk::BeamParams p{};
+    p.logits = bm->logits;
+    p.stride = bm->stride;
+    p.scores = bm->scores;
+    p.ended = bm->ended;
+    p.new_scores = bm->new_scores;
+    p.new_ended = bm->new_ended;
+    p.parents = bm->parents;
+    p.tokens = bm->tokens;
+    p.err = bm->err;
+    p.groups = bm->groups;
+    p.beams = bm->beams;
+    p.vocab = bm->vocab;
+    p.end_token = bm->end_token;
+    p.parts = sk::beam_parts(bm->vocab, es_of(bm->dtype));
+    p.part = static_cast<sk::BeamPart*>(bm->work);
+    return sk::launch_beam_select(bm->dtype, p, reinterpret_cast<hipStream_t>(hip_stream));
+  } catch (...) {
+    return SKSSM_ELAUNCH;
+  }
+}
+
+int sketchssm_reorder(const sketchssm_layer* layer, const sketchssm_buffers* bufs, const sketchssm_rows* extra,
+                      int32_t nextra, const int32_t* parents, int32_t beams, void* hip_stream) {
+  try {
+    if (int rc = check_layer(layer)) return rc;
+    if (!bufs || (nextra > 0 && !extra)) return SKSSM_EINVAL;
+    if (beams < 1 || beams > sk::BEAM_MAX || layer->batch % beams != 0 || nextra < 0 || nextra > 4) return SKSSM_EDIM;
+    if (!aligned(parents, 4) || !aligned(bufs->err, 16)) return SKSSM_EINVAL;
+    const int64_t B = layer->batch, H = layer->heads, G = layer->qk_groups, dk = layer->dk, dv = layer->dv;
+    const int64_t W = layer->window, R = layer->rank_offsets_host[layer->heads], es = es_of(layer->act_dtype);
+    const bool m2 = layer->family == SKSSM_MAMBA2;
+    int64_t dense = 0;
+    for (int h = 0; h < H; ++h) dense += layer->rank_offsets_host[h + 1] == layer->rank_offsets_host[h];
+    sk::ReorderParams p{};
+    int64_t blocks = 0;
+    bool ok = true;
+    auto add = [&](void* data, int64_t bytes) {
+      if (bytes == 0) return;
+      ok = ok && aligned(data, 16);
+      auto& r = p.rows[p.nrows++];
+      r.data = static_cast<char*>(data);
+      r.bytes = bytes;
+      r.unit = bytes % 16 == 0 ? 16 : bytes % 4 == 0 ? 4 : 2;
+      blocks += bytes / r.unit / 256 + 1;
+    };
+    add(bufs->S, H * dk * dv * 4);
+    add(bufs->U, R * dv * es);
+    if (layer->coef_map == SKSSM_COEF_STATE) add(bufs->Cstate, R * dk * es);
+    add(bufs->Scopy, dense * dk * dv * es);
+    add(bufs->ring_k, G * W * dk * es);
+    add(bufs->ring_v, H * W * dv * es);
+    add(bufs->ring_gate, layer->family == SKSSM_KDA ? H * W * dk * 4 : H * W * (m2 ? es : 4));
+    if (!m2) add(bufs->ring_beta, H * W * 4);
+    if (!m2 && layer->pullback == SKSSM_PULLBACK_PROJ) add(bufs->ring_pc, H * W * 64);
+    add(bufs->count, H * 4);
+    for (int i = 0; i < nextra; ++i) {
+      if (extra[i].row_bytes < 0 || extra[i].row_bytes % 16 != 0) return SKSSM_EDIM;
+      add(extra[i].data, extra[i].row_bytes);
+    }
+    if (!ok) return SKSSM_EINVAL;
+    if (blocks * (B / beams) > kMaxTiles) return SKSSM_EDIM;
+    p.groups = (int)(B / beams);
+    p.beams = beams;
+    p.parents = parents;
+    p.err = bufs->err;
+    if (p.groups == 0) return SKSSM_OK;
+    return sk::launch_reorder(p, reinterpret_cast<hipStream_t>(hip_stream));
+  } catch (...) {
+    return SKSSM_ELAUNCH;
+  }
+}
+
+}  // extern "C"

@@ -212,6 +212,35 @@ class DecodeLayer:
             rc = self.normalise(prompts.o, prompts.norm, prompts.norm_gate, stream, prompts.seq_start)
         return rc
 
+    def scan(self, prompts, stream=None) -> int:
+        """Prompts (serving.ScanPrompts) through the selective state space scan:
+        their outputs, the sequences' new states and, with prompts.prime, their
+        sketches."""
+        prompts.check(self)
+        return _on_device(self.S.device.index, lambda st: abi.sketchssm_scan(
+            self._layer, self._bufs, prompts.struct, prompts.uses.add(st)), stream)
+
+    def convolve(self, conv, x, q, k, v, seq_start=None, seqs=None, has_state=None, stream=None) -> int:
+        """The short convolution (serving.ShortConv) of rows x [tokens, channels]
+        into q, k [tokens, G, dk] and v [tokens, H, dv] (rows at any stride of
+        whole 16 bytes): prompts as ScanPrompts describes them, or, without
+        seq_start, one token of every sequence (of seqs), into a step's tensors,
+        say."""
+        return conv.call(self, x, q, k, v, seq_start, seqs, has_state, stream)
+
+    def reorder(self, parents, beams: int, convs=(), stream=None) -> int:
+        """Within each group of ``beams`` consecutive sequences, sequence b becomes
+        a copy of sequence parents[b] (an int32 device tensor [batch], say
+        BeamSearch.parents) in every buffer of the layer and in what convs
+        (serving.ShortConv of this layer) hold, in place."""
+        from .serving import _indices
+        _indices("parents", parents.flatten() if parents.is_contiguous() else parents, self.B, self.S.device)
+        for c in convs:
+            c.check(self)
+        extra = (abi.sketchssm_rows * max(1, len(convs)))(*(c.rows for c in convs))
+        return _on_device(self.S.device.index, lambda st: abi.sketchssm_reorder(
+            self._layer, self._bufs, extra, len(convs), parents.data_ptr(), int(beams), st), stream)
+
     def normalise(self, o, norm, gate=None, stream=None, rows=None) -> int:
         """The norm (serving.OutputNorm) of outputs o [rows, H, dv] (a step's or
         prompts'), in place; gate: a tensor like o; rows as serving.group_norm's."""

@@ -1,8 +1,11 @@
 """What a serving loop runs around the decode steps, on torch tensors: prompts
 through the gated delta rule (``Prompts``, ``DecodeLayer.prefill``), the
 quantised state cache (``StateCache``, ``DecodeLayer.save_state`` and
-``load_state``) and the norm of the layers' outputs (``OutputNorm``,
-``group_norm``).  The tensors are checked here, where a wrong one would have
+``load_state``), the norm of the layers' outputs (``OutputNorm``,
+``group_norm``), prompts through the selective state space scan
+(``ScanPrompts``, ``DecodeLayer.scan``), the short convolution in front of the
+layers (``ShortConv``, ``DecodeLayer.convolve``) and beams (``BeamSearch``,
+``DecodeLayer.reorder``).  The tensors are checked here, where a wrong one would have
 a kernel read what it must not; the work runs in the HIP library."""
 from __future__ import annotations
 
@@ -45,6 +48,18 @@ def _shape(layer: DecodeLayer) -> tuple:
     return layer.family, layer.B, layer.H, layer.dk, layer.dv, layer.act, layer.S.device
 
 
+def _prompt_lists(seq_start, seqs, has_state, dev) -> int:
+    """Checks prompts' lists and gives the number of prompts."""
+    _indices("seq_start", seq_start, None, dev)
+    n = seq_start.numel() - 1
+    if n < 0:
+        raise ValueError("seq_start: the prompts' first tokens and the end of the last")
+    for name, x in (("seqs", seqs), ("has_state", has_state)):
+        if x is not None:
+            _indices(name, x, n, dev)
+    return n
+
+
 class Prompts:
     """Token rows of several prompts, one behind the other, for
     ``DecodeLayer.prefill``: q, k [tokens, H, dk], v, o [tokens, H, dv] in the
@@ -72,13 +87,7 @@ class Prompts:
         strides = [_rows("q", q, (N, H, layer.dk), at, dev), _rows("k", k, (N, H, layer.dk), at, dev),
                    _rows("v", v, (N, H, layer.dv), at, dev), _rows("gate", gate, (N, H), torch.float32, dev),
                    _rows("beta", beta, (N, H), torch.float32, dev), _rows("o", o, (N, H, layer.dv), at, dev)]
-        _indices("seq_start", seq_start, None, dev)
-        n = seq_start.numel() - 1
-        if n < 0:
-            raise ValueError("seq_start: the prompts' first tokens and the end of the last")
-        for name, x in (("seqs", seqs), ("has_state", has_state)):
-            if x is not None:
-                _indices(name, x, n, dev)
+        n = _prompt_lists(seq_start, seqs, has_state, dev)
         if norm_gate is not None:
             # (what the norm would refuse is refused here: behind the prompts the states have moved on)
             st, es = _rows("norm_gate", norm_gate, (N, H, layer.dv), at, dev), norm_gate.element_size()
@@ -112,6 +121,161 @@ class Prompts:
         """Raises ValueError where these prompts are none of the layer's."""
         if self.shape != _shape(layer):
             raise ValueError(f"prompts of a layer {self.shape}, not {_shape(layer)}")
+
+
+class ScanPrompts:
+    """Token rows of several prompts, one behind the other, for
+    ``DecodeLayer.scan`` (Mamba-2 layers): q, k [tokens, G, dk], v, o
+    [tokens, H, dv] and dt [tokens, H] (as the decode steps take it: 0 or more)
+    in the layer's activation dtype, q, k, v and o rows at any stride of whole
+    16 bytes; seq_start, seqs, has_state and prime as for ``Prompts``, and so are
+    the workspace, held tensors and when it may be dropped."""
+
+    def __init__(self, layer: DecodeLayer, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dt: torch.Tensor,
+                 o: torch.Tensor, seq_start: torch.Tensor, seqs: Optional[torch.Tensor] = None,
+                 has_state: Optional[torch.Tensor] = None, prime: bool = True):
+        dev, at = layer.S.device, TORCH_DTYPE[layer.act]
+        N, H, G = q.shape[0], layer.H, layer.G
+        strides = [_rows("q", q, (N, G, layer.dk), at, dev), _rows("k", k, (N, G, layer.dk), at, dev),
+                   _rows("v", v, (N, H, layer.dv), at, dev), _rows("dt", dt, (N, H), at, dev),
+                   _rows("o", o, (N, H, layer.dv), at, dev)]
+        n = _prompt_lists(seq_start, seqs, has_state, dev)
+        self.shape = _shape(layer) + (G,)
+        need = abi.sketchssm_scan_workspace_bytes(layer.layer_struct, N, n)
+        if need < 0:
+            raise ValueError(f"prompts that this layer does not take (code {need})")
+        self.q, self.k, self.v, self.dt, self.o = q, k, v, dt, o
+        self.seq_start, self.seqs, self.has_state, self.prime = seq_start, seqs, has_state, prime
+        self.work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        self.uses = _StreamUses(q, k, v, dt, o, seq_start, seqs, has_state, self.work)
+        self._struct = abi.sketchssm_scan_prompts(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(o), *strides, N, n, _ptr(seq_start), _ptr(seqs),
+            _ptr(has_state), int(prime), _ptr(self.work), need)
+
+    @property
+    def struct(self) -> abi.sketchssm_scan_prompts:
+        return self._struct
+
+    def check(self, layer: DecodeLayer) -> None:
+        """Raises ValueError where these prompts are none of the layer's."""
+        if self.shape != _shape(layer) + (layer.G,):
+            raise ValueError(f"prompts of a layer {self.shape}, not {_shape(layer) + (layer.G,)}")
+
+
+class ShortConv:
+    """The short causal convolution in front of a layer, with the inputs that its
+    sequences hold (``state`` [B, taps - 1, channels], oldest first, in the layer's
+    activation dtype): weight [channels, taps] (the last tap is the token's own;
+    2 to 8 taps) and bias [channels] in fp32, an activation behind it.  order: how
+    the channels lie, a permutation of "q", "k" and "v"; unit: the heads of queries
+    and keys are divided by sqrt(sum of squares + eps)."""
+
+    def __init__(self, layer: DecodeLayer, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "silu",
+                 order: str = "vkq", unit: bool = False, eps: float = 1e-6):
+        dev, at = layer.S.device, TORCH_DTYPE[layer.act]
+        self.sizes = {"q": layer.G * layer.dk, "k": layer.G * layer.dk, "v": layer.H * layer.dv}
+        if sorted(order) != ["k", "q", "v"]:
+            raise ValueError('order: a permutation of "q", "k" and "v"')
+        if act not in ACT:
+            raise ValueError(f"act: one of {tuple(ACT)}")
+        if not (math.isfinite(C.c_float(eps).value) and eps >= 0):
+            raise ValueError("eps: finite in fp32, 0 or more")
+        channels = sum(self.sizes.values())
+        if weight.dim() != 2 or weight.shape[0] != channels or not 2 <= weight.shape[1] <= 8:
+            raise ValueError(f"weight: [{channels}, 2 to 8 taps], got {tuple(weight.shape)}")
+        for name, x, shape in (("weight", weight, weight.shape), ("bias", bias, (channels,))):
+            if x is not None and (x.dtype != torch.float32 or x.shape != shape or not x.is_contiguous() or x.device != dev or
+                                  x.data_ptr() % 16):
+                raise ValueError(f"{name}: a contiguous fp32 tensor {tuple(shape)} on {dev} at whole 16 bytes")
+        self.weight, self.bias, self.act, self.order, self.unit, self.eps = weight, bias, act, order, bool(unit), float(eps)
+        self.channels, self.taps, self.shape = channels, weight.shape[1], _shape(layer) + (layer.G,)
+        self.state = torch.zeros((layer.B, self.taps - 1, channels), dtype=at, device=dev)
+        self.err = torch.zeros(4, dtype=torch.int32, device=dev)
+        self.rows = abi.sketchssm_rows(self.state.data_ptr(), self.state[:1].numel() * self.state.element_size())
+        self.uses = _StreamUses(weight, bias, self.state, self.err)
+
+    def check(self, layer: DecodeLayer) -> None:
+        """Raises ValueError where this is no convolution of the layer's."""
+        if self.shape != _shape(layer) + (layer.G,):
+            raise ValueError(f"a convolution of a layer {self.shape}, not {_shape(layer) + (layer.G,)}")
+
+    def call(self, layer, x, q, k, v, seq_start=None, seqs=None, has_state=None, stream=None) -> int:
+        """``DecodeLayer.convolve``."""
+        self.check(layer)
+        dev, at = layer.S.device, TORCH_DTYPE[layer.act]
+        N = x.shape[0]
+        xs = _rows("x", x, (N, self.channels), at, dev)
+        out = {"q": (q, (N, layer.G, layer.dk)), "k": (k, (N, layer.G, layer.dk)), "v": (v, (N, layer.H, layer.dv))}
+        pieces = [abi.sketchssm_conv_piece(t.data_ptr(), _rows(c, t, shape, at, dev), self.sizes[c],
+                                           layer.dk if self.unit and c != "v" else 0)
+                  for c, (t, shape) in ((c, out[c]) for c in self.order)]
+        n = N
+        if seq_start is not None:
+            n = _prompt_lists(seq_start, seqs, has_state, dev)
+        else:
+            for name, t in (("seqs", seqs), ("has_state", has_state)):
+                if t is not None:
+                    _indices(name, t, n, dev)
+        st = abi.sketchssm_convolution(
+            x.data_ptr(), xs, self.weight.data_ptr(), None if self.bias is None else self.bias.data_ptr(),
+            self.state.data_ptr(), (abi.sketchssm_conv_piece * 3)(*pieces), self.taps, DTYPE[layer.act], ACT[self.act],
+            self.eps, layer.B, N, n, _ptr(seq_start), _ptr(seqs), _ptr(has_state), self.err.data_ptr())
+        return _on_device(dev.index, lambda s: abi.sketchssm_conv(st, self.uses.add(s)), stream)
+
+    def error_word(self) -> int:
+        return int(self.err[0].item())
+
+
+class BeamSearch:
+    """Selection of beams: ``groups`` requests of ``beams`` (1 to 16) consecutive
+    sequences each.  ``select`` takes the sequences' logits [groups * beams,
+    vocab] (bf16 or fp32, rows contiguous at any stride) and leaves, [groups,
+    beams] each, ``parents`` (int32: the sequence that each goes on from, for
+    ``DecodeLayer.reorder``), ``tokens`` (int32), ``scores`` (fp32: the sums of
+    the tokens' log probabilities) and ``ended`` (int32: the end token has come).
+    At first each request has its first beam alone (the others' scores are minus
+    infinity)."""
+
+    def __init__(self, groups: int, beams: int, vocab: int, end: int = -1, device="cuda"):
+        if groups < 0 or not 1 <= beams <= 16 or not 1 <= vocab <= 1 << 24 or not -1 <= end < vocab:
+            raise ValueError("groups: 0 or more, beams: 1 to 16, vocab: 1 to 2^24, end: -1 (none) to vocab - 1")
+        need = max(abi.sketchssm_beam_workspace_bytes(groups, beams, vocab, d) for d in DTYPE.values())
+        if need < 0:
+            raise ValueError(f"beams of this many requests and tokens are not taken (code {need})")
+        z = lambda dt: torch.zeros((groups, beams), dtype=dt, device=device)  # noqa: E731
+        self.groups, self.beams, self.vocab, self.end = groups, beams, vocab, end
+        self.scores, self.ended, self.parents, self.tokens = z(torch.float32), z(torch.int32), z(torch.int32), z(torch.int32)
+        self.err = torch.zeros(4, dtype=torch.int32, device=device)
+        self.work = torch.empty(need, dtype=torch.uint8, device=device)
+        self.uses = _StreamUses(self.scores, self.ended, self.parents, self.tokens, self.err, self.work)
+        self.reset()
+
+    def reset(self) -> None:
+        """A new search: every request's first beam alone."""
+        self.scores.fill_(-math.inf)
+        self.scores[:, 0] = 0.0
+        self.ended.zero_()
+
+    def select(self, logits: torch.Tensor, scores: Optional[torch.Tensor] = None, ended: Optional[torch.Tensor] = None,
+               stream=None) -> int:
+        """The next beams; scores and ended: others than the search's own as the
+        beams' present ones.  Returns the library's code."""
+        dev, rows = self.scores.device, self.groups * self.beams
+        if logits.dtype not in _DTYPES or dev.type != "cuda":
+            raise ValueError("logits: a bf16 or fp32 device tensor [groups * beams, vocab]")
+        stride = _rows("logits", logits, (rows, self.vocab), logits.dtype, dev)
+        for name, t, own in (("scores", scores, self.scores), ("ended", ended, self.ended)):
+            if t is not None and (t.shape != own.shape or t.dtype != own.dtype or t.device != dev or not t.is_contiguous()):
+                raise ValueError(f"{name}: a contiguous {own.dtype} tensor {tuple(own.shape)} on {dev}")
+        scores, ended = self.scores if scores is None else scores, self.ended if ended is None else ended
+        st = abi.sketchssm_beams(
+            logits.data_ptr(), stride, scores.data_ptr(), ended.data_ptr(), self.scores.data_ptr(), self.ended.data_ptr(),
+            self.parents.data_ptr(), self.tokens.data_ptr(), self.err.data_ptr(), self.groups, self.beams, self.vocab,
+            _DTYPES[logits.dtype], self.end, self.work.data_ptr(), self.work.numel())
+        return _on_device(dev.index, lambda s: abi.sketchssm_beam_select(st, self.uses.add(s)), stream)
+
+    def error_word(self) -> int:
+        return int(self.err[0].item())
 
 
 class StateCache:
