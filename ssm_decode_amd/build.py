@@ -21,7 +21,7 @@ CFLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 SOURCES = ["sk_api.cpp", "sk_m2.hip", "sk_gdn.hip", "sk_kda.hip", "sk_m2_f32.hip", "sk_gdn_f32.hip",
            "sk_kda_f32.hip", "sk_noalloc.hip", "sk_serve_api.cpp", "sk_prompt_step.hip", "sk_prompt_chunk.hip",
            "sk_prompt_chunk_f32.hip",
-           "sk_state_cache.hip", "sk_norm.hip", "sk_seq_api.cpp", "sk_scan_step.hip", "sk_conv.hip",
+           "sk_state_cache.hip", "sk_norm.hip", "sk_seq_api.cpp", "sk_scan_step.hip", "sk_scan_chunk.hip", "sk_conv.hip",
            "sk_beam.hip", "sk_reorder.hip"]
 
 

@@ -366,17 +366,6 @@ __device__ __forceinline__ void copy16x4(const void* base, uint32_t offset, uint
       "s"(reinterpret_cast<uint64_t>(base)), "s"(lds)
       : "memory", "m0");
 }
-// Within each 16 lanes, lane i gives the address of four values: 4 rows (i / 4)
-// of 16 (4 (i % 4) ..); it receives column i of the four rows.
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ bf16x4 read_tr(const void* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-      (__attribute__((address_space(3))) bf16x4*)const_cast<void*>(p));
-}
-__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
 // Where few tiles have many tokens (p.seg_shift != 0), prompts are cut into
 // segments of 2^seg_shift tokens, and three launches take the place of one:
 //   1. STATE: the segments but the last, at once, without outputs: each from a

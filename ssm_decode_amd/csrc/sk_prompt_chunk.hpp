@@ -189,6 +189,17 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
+// Within each 16 lanes, lane i gives the address of four values: 4 rows (i / 4)
+// of 16 (4 (i % 4) ..); it receives column i of the four rows.
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bf16x4 read_tr(const void* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+      (__attribute__((address_space(3))) bf16x4*)const_cast<void*>(p));
+}
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 // The end of a region: its instructions in the order of N times a matrix
 // instruction, READS LDS reads and VALU vector instructions (as far as there
 // are any), and nothing moved across.

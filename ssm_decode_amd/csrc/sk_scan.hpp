@@ -6,17 +6,18 @@
 
 namespace sk {
 
-// (q and k hold G groups' rows, gate holds dt in the activation dtype; beta is unused)
+// (q and k hold G groups' rows, gate holds dt in the activation dtype; beta is unused;
+// seg: [nsegs][H] states behind the segments, dk x dv)
 struct ScanParams : PromptParams {
   int G;
   int waves, parts;         // chunked form: waves of a workgroup, workgroups of a group's heads
   const float* A;           // [H]
+  float* seg_decay;         // [nsegs][H] products of the segments' decays
 };
 
-// Chunked form: tokens of a chunk, and the bytes of a segment's workspace (a
-// head's state and its decay).
-constexpr int SCAN_CHUNK = 64;
-inline int64_t scan_seg_floats(int dk, int dv) { return (int64_t)dk * dv; }
+// Chunked form: a wave has 64 columns of a head's state, a workgroup up to eight
+// waves with the keys and queries of one group.
+constexpr int SCAN_COLS = 64, SCAN_WAVES = 8;
 
 int launch_scan_step(int dk, int dv, int act, const ScanParams& p, hipStream_t st);
 int launch_scan_chunks(int dk, int dv, const ScanParams& p, hipStream_t st);

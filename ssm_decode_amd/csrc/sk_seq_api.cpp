@@ -18,17 +18,40 @@ namespace {
 
 int es_of(int32_t dtype) { return dtype == SKSSM_F32 ? 4 : 2; }
 
+// Prompts of up to this many tokens go token by token where the launch has both
+// kinds.
+int short_prompt(const sketchssm_layer* L) { return L->dk == 64 ? 32 : 16; }
+
 // How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
-// none), all of them or those of more than `shrt` tokens; in segments of
-// 2^seg_shift tokens (0: whole), with the bytes of their states.
+// none), all of them or those of more than short_prompt tokens; in segments of
+// 2^seg_shift tokens (0: whole), with the bytes of their states and decays.
 struct Plan {
-  int64_t chunked, nsegs, bytes;
+  int64_t chunked, nsegs, decay_at, bytes;
   bool all;
-  int seg_shift, shrt;
+  int seg_shift, waves, parts;
 };
+constexpr int kMinSegShift = 9;
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
-  (void)L; (void)tokens; (void)nseq;
-  return Plan{};
+  Plan p{};
+  const int shrt = short_prompt(L);
+  if (L->dk < 64 || L->act_dtype != SKSSM_BF16 || nseq == 0) return p;
+  if (tokens - nseq < shrt) return p;            // (no prompt is longer unless others are empty)
+  p.all = tokens > 64 * nseq;
+  const int64_t most = tokens / (shrt + 1);
+  p.chunked = p.all || nseq < most ? nseq : most;
+  const int units = L->heads / L->qk_groups * (L->dv / sk::SCAN_COLS);
+  p.parts = (units + sk::SCAN_WAVES - 1) / sk::SCAN_WAVES;
+  p.waves = (units + p.parts - 1) / p.parts;
+  const int64_t row = L->qk_groups * p.parts;    // workgroups of a segment
+  int shift = kMinSegShift;
+  while ((tokens >> shift) * row > 1024) ++shift;
+  if (tokens >> shift >= 2 && p.chunked * row < 1024) {
+    p.seg_shift = shift;
+    p.nsegs = sk::prompt_slots(tokens, p.chunked, shift);
+    p.decay_at = p.nsegs * L->heads * (int64_t)L->dk * L->dv * 4;
+    p.bytes = p.decay_at + (p.nsegs * L->heads * 4 + 15) / 16 * 16;
+  }
+  return p;
 }
 
 }  // namespace
@@ -100,6 +123,19 @@ int sketchssm_scan(const sketchssm_layer* layer, const sketchssm_buffers* bufs, 
     if (pr->prime) fill_sketch(&p.sk, layer, bufs);
     hipStream_t st = reinterpret_cast<hipStream_t>(hip_stream);
     p.len_hi = INT32_MAX;
+    const Plan pl = plan(layer, pr->tokens, pr->nseq);
+    if (pl.chunked > 0) {
+      p.nchunked = (int)pl.chunked;
+      p.seg_shift = pl.seg_shift;
+      p.nsegs = (int)pl.nsegs;
+      p.seg = static_cast<float*>(pr->work);
+      p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(pr->work) + pl.decay_at);
+      p.waves = pl.waves;
+      p.parts = pl.parts;
+      p.len_lo = pl.all ? -1 : short_prompt(layer);
+      if ((rc = sk::launch_scan_chunks(dk, dv, p, st)) || pl.all) return rc;
+      p.len_hi = short_prompt(layer);
+    }
     return sk::launch_scan_step(dk, dv, layer->act_dtype, p, st);
   } catch (...) {
     return SKSSM_ELAUNCH;

@@ -18,13 +18,12 @@ __device__ __forceinline__ bool listed_before(const int32_t* list, int i, int id
 }
 
 // Prompt i and its sequence, checked.  A list of first tokens that falls
-// anywhere, or leaves [0, tokens], reports ERRBIT_SEQ and is refused whole (so
+// anywhere, or leaves [0, tokens], gives ERRBIT_SEQ and is refused whole (so
 // that no two prompts share tokens, and at most tokens / n prompts have n
 // tokens); an index outside the batch, or a sequence that an earlier prompt
-// has (which keeps it), refuses this prompt; a tile whose ring still holds
-// entries reports ERRBIT_COUNT.  Uniform over the workgroup, whose threads
-// all take part.
-__device__ __forceinline__ bool prompt_ok(const PromptParams& p, int i, int h, int b) {
+// has (which keeps it), refuses this prompt.  Uniform over the workgroup, whose
+// threads all take part.
+__device__ __forceinline__ int prompt_wrong(const PromptParams& p, int i, int b) {
   int wrong = 0;
   for (int j = threadIdx.x; j < p.nseq; j += blockDim.x) {
     const int s0 = p.start[j], s1 = p.start[j + 1];
@@ -32,7 +31,13 @@ __device__ __forceinline__ bool prompt_ok(const PromptParams& p, int i, int h, i
     if (p.seqs && j < i) wrong |= p.seqs[j] == b;
   }
   wrong |= b < 0 || b >= p.B;
-  int bad = __syncthreads_or(wrong) ? ERRBIT_SEQ : 0;
+  return __syncthreads_or(wrong) ? ERRBIT_SEQ : 0;
+}
+
+// .. and the tile of its head h: one whose ring still holds entries gives
+// ERRBIT_COUNT.  What is wrong is reported.
+__device__ __forceinline__ bool prompt_ok(const PromptParams& p, int i, int h, int b) {
+  int bad = prompt_wrong(p, i, b);
   if (!bad && p.count[(size_t)b * p.H + h] != 0) bad = ERRBIT_COUNT;
   if (bad && threadIdx.x == 0) atomicOr(p.err, bad);
   return bad == 0;
