@@ -15,9 +15,9 @@ struct ScanParams : PromptParams {
   float* seg_decay;         // [nsegs][H] products of the segments' decays
 };
 
-// Chunked form: a wave has 64 columns of a head's state, a workgroup up to eight
+// Chunked form: a wave has 32 columns of a head's state, a workgroup up to eight
 // waves with the keys and queries of one group.
-constexpr int SCAN_COLS = 64, SCAN_WAVES = 8;
+constexpr int SCAN_COLS = 32, SCAN_WAVES = 8;
 
 int launch_scan_step(int dk, int dv, int act, const ScanParams& p, hipStream_t st);
 int launch_scan_chunks(int dk, int dv, const ScanParams& p, hipStream_t st);

@@ -12,12 +12,12 @@
 // cores with each fp32 operand (S_0, P, the weighted V) as an exact sum of three
 // bf16 values, so a product with bf16 data (Q, V, K^T) takes three instructions.
 //
-// Layout.  A wave has 64 columns of one head's state, all rows, in registers, and a
-// workgroup up to eight waves of one group, whose keys and queries it shares: K and Q
-// are in LDS twice (the next chunk's copy, straight from memory, is in flight over
-// the present one), the triangle of K Q^T is formed once a chunk by all waves, and V,
-// which is a wave's own, comes through registers one chunk ahead.  All products are
-// the transposed ones, so that a lane's results are runs of columns of one token.
+// Layout.  A wave has 32 columns of one head's state, all rows, in registers, and a
+// workgroup up to eight waves of one group, whose keys and queries it shares.  K, Q
+// and each wave's columns of V are in LDS twice: the next chunk's copy, straight from
+// memory, is in flight over the present one.  All products are the transposed ones,
+// so that a lane's results are runs of columns of one token, and K Q^T leaves each
+// wave the triangle as the operand that P V needs.
 #include <type_traits>
 
 #include "sk_prompt_chunk.hpp"
@@ -26,17 +26,30 @@
 namespace sk {
 namespace {
 
-constexpr int NCB = SCAN_COLS / 16;              // 16-column tiles of a wave
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Operands of v_mfma_f32_32x32x16_bf16 (h = lane / 32, ln = lane % 32): row or column
+// ln, eight of the 16 products' terms from 8 h on.  Register r of a result is row
+// 8 (r / 4) + 4 h + r % 4 of column ln; row m stands for row swap23(m) of the block,
+// so that registers 8 s .. 8 s + 7 are its rows 16 s + 8 h .. + 7: an operand of the
+// next product as they stand, and runs of eight columns or tokens.
+__device__ __forceinline__ int swap23(int m) { return (m & ~12) | (m & 4) << 1 | (m & 8) >> 1; }
+__device__ __forceinline__ f32x16 mm16(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ void rows8(const f32x16& a, int s, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = a[8 * s + e];
+}
 
 template <int DK, bool OUT>
 struct ScanLds {
   static constexpr int K = 0;                    // [2][64][DK]
   static constexpr int Q = K + 2 * PC * DK * 2;
-  static constexpr int QK = Q + (OUT ? 2 * PC * DK * 2 : 0);      // six fragments of K Q^T in fp32
-  static constexpr int V = QK + (OUT ? FRAGS * 2 * FRAG_BYTES : 0);
-  static constexpr int V_BYTES = PC * SCAN_COLS * 2, F_BYTES = 6 * PC * 4;
-  static constexpr int bytes(int waves) { return V + waves * (V_BYTES + F_BYTES); }
+  static constexpr int V = Q + (OUT ? 2 * PC * DK * 2 : 0);      // wave after wave: [2][64][32], then the factors
+  static constexpr int V_BYTES = PC * SCAN_COLS * 2, WAVE = 2 * V_BYTES + 6 * PC * 4;
+  static constexpr int bytes(int waves) { return V + waves * WAVE; }
 };
 
 // Sum of the lanes up to this one, in 64 bits.
@@ -76,11 +89,6 @@ __device__ __forceinline__ const void* uniform(const void* x) {
   return reinterpret_cast<const void*>((uint64_t)uniform((uint32_t)(u >> 32)) << 32 | uniform((uint32_t)u));
 }
 
-// Fragment f of the triangle: rows (tokens i) 16 rb .., columns (tokens j) 32 kh ..
-__device__ __forceinline__ constexpr int frag_rb(int f) { return f < 2 ? f : 2 + (f - 2) / 2; }
-__device__ __forceinline__ constexpr int frag_kh(int f) { return f < 2 ? 0 : (f - 2) & 1; }
-constexpr int frag_of(int rb, int kh) { return rb < 2 ? rb : 2 + 2 * (rb - 2) + kh; }
-
 // One workgroup per (segment or prompt, group, part of its heads).  Where prompts are
 // cut into segments of 2^seg_shift tokens, three launches take the place of one:
 //   1. without outputs, the segments but the last, at once: each from a zero state
@@ -97,7 +105,7 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
   constexpr int PPR = DK / 8, DB = DK / 32, UPH = DV / SCAN_COLS, UNIT = DK * SCAN_COLS;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), NW = p.waves;
-  const int n = lane & 15, hi = lane >> 4;
+  const int n = lane & 15, hi = lane >> 4, ln = lane & 31, hh = lane >> 5;
   // (the parts of a group are eight workgroups apart: on one XCD at one time)
   const int part = blockIdx.x / 8 % p.parts, tile = blockIdx.x / (8 * p.parts) * 8 + blockIdx.x % 8;
   const int g = tile % p.G, slot = tile / p.G, E = p.H / p.G;
@@ -137,362 +145,302 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
   const bf16* vp = reinterpret_cast<const bf16*>(p.v) + (int64_t)s0 * p.vs + (int64_t)h * DV + c0;
   const bf16* dp = reinterpret_cast<const bf16*>(p.gate) + (int64_t)s0 * p.gs + h;
   // Rows have their 16-byte pieces swizzled so that those of a fragment spread over
-  // the banks: piece pc of a row of 16 (K, Q; DK = 64: 8, as V) is at pc ^ swz(row).
+  // the banks: piece pc of a row of PPR (16, DK = 64: 8, V: 4) is at pc ^ swz(row).
   auto swz = [](int row, int ppr) {
     const int s = (row & 3) | ((row >> 1) & 12);
-    return (ppr == 16 ? s : s >> 1) & (ppr - 1);
+    return ppr == 16 ? s : ppr == 8 ? s >> 1 : (row >> 2) & 3;
   };
   const uint32_t lds0 = lds_address(smem);
-  // K and Q of a chunk of nt tokens into buffer buf (rows behind the end repeat the
-  // last one: their weights are zeros, and what they give is not stored)
-  auto copy = [&](int t0, int nt, int buf) {
+  const int v_at = L::V + wv * L::WAVE;
+  float* s_f = reinterpret_cast<float*>(smem + v_at + 2 * L::V_BYTES);      // L (upper and lower part), dt, weight, exp L, first wrong tokens
+  float dr = 0.f;
+  // K, Q, V and dt (a token a lane) of a chunk of nt tokens into buffer buf.  Rows
+  // behind the end repeat the last one with a dt of 0: their weights are zeros, and
+  // what they give is not stored.
+  auto fetch = [&](int t0, int nt, int buf) {
+    const int end = nt - 1;
+    if (active) {
+      const int r = lane < end ? lane : end;
+      dr = to_f32(*reinterpret_cast<const bf16*>(reinterpret_cast<const unsigned char*>(dp + (int64_t)t0 * p.gs) + (uint32_t)(r * p.gs * 2)));
+    }
     for (int c = wv; c < PPR; c += NW) {
-      const int at = c * 64 + lane, row = at / PPR, pc = (at % PPR) ^ swz(row, PPR), r = row < nt ? row : nt - 1;
+      const int at = c * 64 + lane, row = at / PPR, pc = (at % PPR) ^ swz(row, PPR), r = row < end ? row : end;
       const uint32_t to = lds0 + buf * PC * DK * 2 + c * 1024;
       copy16(uniform(kp + (int64_t)t0 * p.ks), (uint32_t)(r * p.ks * 2) + pc * 16, uniform(to + L::K));
       if (OUT) copy16(uniform(qp + (int64_t)t0 * p.qs), (uint32_t)(r * p.qs * 2) + pc * 16, uniform(to + L::Q));
     }
-  };
-  unsigned char* s_v = smem + L::V + wv * (L::V_BYTES + L::F_BYTES);
-  float* s_f = reinterpret_cast<float*>(s_v + L::V_BYTES);      // L (upper and lower part), dt, weight, exp L, first wrong tokens
-  u32x4 vr[8];
-  float dr = 0.f;
-  const uint32_t vo = (uint32_t)((lane >> 3) * p.vs * 2) + (lane & 7) * 16;
-  // V, eight rows at a time, and dt, a token a lane.  Rows behind the end repeat the
-  // last one: their dt is 0.
-  auto fetch = [&](int t0, int nt) {
-    const unsigned char* from = reinterpret_cast<const unsigned char*>(vp + (int64_t)t0 * p.vs);
-    if (nt == PC) {
+    if (active) {
 #pragma unroll
-      for (int v = 0; v < 8; ++v) vr[v] = *reinterpret_cast<const u32x4*>(from + (int64_t)(16 * v) * p.vs + vo);
-    } else {
-#pragma unroll
-      for (int v = 0; v < 8; ++v) {
-        const int row = 8 * v + (lane >> 3), r = row < nt ? row : nt - 1;
-        vr[v] = *reinterpret_cast<const u32x4*>(from + (uint32_t)(r * p.vs * 2) + (lane & 7) * 16);
+      for (int v = 0; v < 4; ++v) {
+        const int row = 16 * v + (lane >> 2), pc = (lane & 3) ^ swz(row, 4), r = row < end ? row : end;
+        copy16(uniform(vp + (int64_t)t0 * p.vs), (uint32_t)(r * p.vs * 2) + pc * 16, uniform(lds0 + v_at + buf * L::V_BYTES + v * 1024));
       }
     }
-    const int r = lane < nt ? lane : nt - 1;
-    dr = to_f32(*reinterpret_cast<const bf16*>(reinterpret_cast<const unsigned char*>(dp + (int64_t)t0 * p.gs) + (uint32_t)(r * p.gs * 2)));
-    dr = lane < nt ? dr : 0.f;
   };
 
   // -------------------------------------------------------------- state
-  f32x4s S[DB][NCB][2];                          // rows 32 kb + 8 hi + 4 e + r of column (tile cb, lane n)
-  auto col = [&](int cb) { return 32 * (cb >> 1) + block_row(n, cb & 1); };
-  float* Sg = p.S + ((size_t)b * p.H + h) * DK * DV + c0;
+  f32x16 S[DB];                                  // rows 32 db .., the wave's columns
+  const int col = swap23(ln);                    // the lane's column
+  float* Sg = p.S + ((size_t)b * p.H + h) * DK * DV + c0 + col;
   auto seg_at = [&](int s) { return reinterpret_cast<f32x4s*>(p.seg + (((size_t)s * p.H + h) * UPH + c0 / SCAN_COLS) * UNIT) + lane; };
-  auto each = [&](auto f) {
+  auto each = [&](auto f) {                      // f(block, register, row)
 #pragma unroll
-    for (int kb = 0; kb < DB; ++kb)
+    for (int db = 0; db < DB; ++db)
 #pragma unroll
-      for (int cb = 0; cb < NCB; ++cb)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) f(kb, cb, e);
+      for (int r = 0; r < 16; ++r) f(db, r, 32 * db + 16 * (r >> 3) + 8 * hh + (r & 7));
   };
-  each([&](int kb, int cb, int e) { S[kb][cb][e] = f32x4s{0.f, 0.f, 0.f, 0.f}; });
+  auto each4 = [&](auto f) {                     // f(block, four registers, place in a segment's workspace)
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f(db, q, (db * 4 + q) * 64);
+  };
+  auto four = [&](int db, int q) { return f32x4s{S[db][4 * q], S[db][4 * q + 1], S[db][4 * q + 2], S[db][4 * q + 3]}; };
+  if (len > 0) fetch(0, len < PC ? len : PC, 0);
+  each([&](int db, int r, int) { S[db][r] = 0.f; });
   if (active) {
     if (seg == 0 && !(OUT && !last)) {
-      if (!p.has_state || p.has_state[i] != 0)
-        each([&](int kb, int cb, int e) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[kb][cb][e][r] = Sg[(size_t)(32 * kb + 8 * hi + 4 * e + r) * DV + col(cb)];
-        });
+      if (!p.has_state || p.has_state[i] != 0) each([&](int db, int r, int row) { S[db][r] = Sg[(size_t)row * DV]; });
       if (!OUT) {
         f32x4s* to = seg_at(slot + slots - 1);
-        each([&](int kb, int cb, int e) { to[((kb * NCB + cb) * 2 + e) * 64] = S[kb][cb][e]; });
+        each4([&](int db, int q, int at) { to[at] = four(db, q); });
       }
     } else if (OUT) {
       const f32x4s* from = seg_at(seg == 0 ? slot + slots - 1 : slot - 1);
-      each([&](int kb, int cb, int e) { S[kb][cb][e] = from[((kb * NCB + cb) * 2 + e) * 64]; });
+      each4([&](int db, int q, int at) {
+        const f32x4s x = from[at];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[db][4 * q + r] = x[r];
+      });
     }
-    if (len > 0) fetch(0, len < PC ? len : PC);
   }
-  if (len > 0) copy(0, len < PC ? len : PC, 0);
-  const double rate = exp((double)p.A[h]) * -1.4426950408889634;
+  const double rate = wave_last(exp((double)p.A[h]) * -1.4426950408889634);
   double total = 0.;
 
   bf16* op = reinterpret_cast<bf16*>(p.o) + (int64_t)s0 * p.os + (int64_t)h * DV + c0;
-  const uint32_t oo = (uint32_t)(n * p.os * 2) + hi * 16;
+  const uint32_t oo = (uint32_t)(ln * p.os * 2) + hh * 16;
 
   // Byte addresses of a lane's fragments.  A fragment's rows differ by whole multiples
-  // of what the swizzle looks at, or by such that change one bit of it, so that a few
-  // registers and constant offsets cover all of them (checked below, at compile time).
-  const int ti = n >> 2;
-  constexpr int ROW = DK * 2;
-  //  rows 16 rb + n of Q, piece 4 kb + hi: at kq[kb ^ swizzle bits of rb] + 16 rb ROW
-  //  rows 32 kh + block_row(n, t) of K, piece 4 kb + hi: at kk[kb] + (32 kh + 4 t) ROW
-  //  K^T, rows 32 kh + 8 hi + ti (+ 4), columns 32 db + 8 (n & 3) + 4 t: at kt[db] + (32 kh (+ 4)) ROW + 8 t
-  //  V, rows as K^T's, columns 32 cp + 8 (n & 3) + 4 t: at va[cp] + (32 kh (+ 4)) 128 + 8 t
-  int kq[DB], kk[DB], kt[DB], va[NCB / 2];
-#pragma unroll
-  for (int kb = 0; kb < DB; ++kb) {
-    kq[kb] = n * ROW + ((4 * kb + hi) ^ swz(n, PPR)) * 16;
-    kk[kb] = block_row(n, 0) * ROW + ((4 * kb + hi) ^ swz(block_row(n, 0), PPR)) * 16;
-    kt[kb] = (8 * hi + ti) * ROW + ((4 * kb + (n & 3)) ^ swz(8 * hi + ti, PPR)) * 16;
-  }
-#pragma unroll
-  for (int cp = 0; cp < NCB / 2; ++cp) va[cp] = (8 * hi + ti) * 128 + ((4 * cp + (n & 3)) ^ swz(8 * hi + ti, 8)) * 16;
-  // rows of another rb: bits of the piece's number that the swizzle turns over
-  constexpr int FLIP = PPR == 16 ? 2 : 1;
-  auto frag_q = [&](const unsigned char* s, int rb, int kb) {
-    return as_frag(*reinterpret_cast<const u32x4*>(s + kq[kb ^ (rb & 1) * FLIP] + 16 * rb * ROW));
-  };
-  auto frag_k = [&](const unsigned char* s, int kh, int t, int kb) {
-    return as_frag(*reinterpret_cast<const u32x4*>(s + kk[kb] + (32 * kh + 4 * t) * ROW));
-  };
-  auto frag_kt = [&](const unsigned char* s, int db, int t, int kh) {
-    const unsigned char* at = s + kt[db] + 32 * kh * ROW + 8 * t;
-    return join(read_tr(at), read_tr(at + 4 * ROW));
-  };
-  // V^T (or V): columns of tile cb, tokens 32 kh + 8 hi ..
-  auto frag_v = [&](int cb, int kh) {
-    const unsigned char* at = s_v + va[cb >> 1] + 32 * kh * 128 + 8 * (cb & 1);
-    return join(read_tr(at), read_tr(at + 4 * 128));
-  };
+  // of what the swizzle looks at, or by such that change one bit of it, so that one
+  // register, constant offsets and flipped bits cover all of a kind:
+  //  tokens 32 tt + ln of Q, columns 32 db + 16 s + 8 h ..: (fq ^ 64 db ^ 32 s) + 32 tt ROW
+  //  tokens 32 tt + swap23(ln) of K, columns as those: (fk ^ 64 db ^ 32 s) + 32 tt ROW
+  //  K^T, tokens 16 s + 8 h + ti (+ 4), the lane's run of four of rows 32 db ..: (kt ^ 64 db ^ flip of s) + (16 s (+ 4)) ROW
+  //  V, tokens as K^T's, the lane's run of four columns: va + 16 s 64, (va ^ 16) + (16 s + 4) 64
+  constexpr int ROW = DK * 2, TFLIP = PPR == 16 ? 128 : 64;
+  const int ti = n >> 2, run = n & 3, g0 = hi & 1;
+  int fq = ln * ROW + (hh ^ swz(ln, PPR)) * 16;
+  int fk = col * ROW + (hh ^ swz(col, PPR)) * 16;
+  int kt = (8 * hh + ti) * ROW + ((2 * g0 + (run & 1)) ^ swz(8 * hh + ti, PPR)) * 16 + (run >> 1) * 8;
+  int va = (8 * hh + ti) * 64 + ((2 * g0 + (run & 1)) ^ swz(8 * hh + ti, 4)) * 16 + (run >> 1) * 8;
+  auto frag = [](const unsigned char* s, int at) { return as_frag(*reinterpret_cast<const u32x4*>(s + at)); };
 
   int buf = 0;
   for (int t0 = 0; t0 < len; t0 += PC, buf ^= 1) {
     const int nt = len - t0 < PC ? len - t0 : PC, left = len - t0 - PC;
+    // (or every fragment's address would be made in front of the loop, and held)
+    asm volatile("" : "+v"(fq), "+v"(fk), "+v"(kt), "+v"(va));
+    // this wave's copies for the chunk have landed
+    asm volatile("s_waitcnt vmcnt(0)" : "+v"(dr)::"memory");
     // the chunk's decays, a token a lane: L split so that a difference of two is exact
     // to fp32 (a decay of less than 2^-256 a token is zero)
     float decay = 0.f;
-    bool wrong = false;
     if (active) {
-      double l = (double)dr * rate;
+      const float d = lane < nt ? dr : 0.f;
+      double l = (double)d * rate;
       l = l < -256. ? -256. : l;
       const double at = wave_prefix(l), end = wave_last(at);
-      const double hid = (at + 0x1.8p42) - 0x1.8p42;      // a multiple of 2^-10, |L| <= 2^14
-      s_f[lane] = (float)hid;
-      s_f[PC + lane] = (float)(at - hid);
-      s_f[2 * PC + lane] = dr;
-      s_f[3 * PC + lane] = exp2_of(end - at) * dr;
+      const double upper = (at + 0x1.8p42) - 0x1.8p42;      // a multiple of 2^-10, |L| <= 2^14
+      s_f[lane] = (float)upper;
+      s_f[PC + lane] = (float)(at - upper);
+      s_f[2 * PC + lane] = d;
+      s_f[3 * PC + lane] = exp2_of(end - at) * d;
       s_f[4 * PC + lane] = exp2_of(at);
       decay = exp2_of(end);
-      total += end;
-      uint32_t top = 0;                          // the largest magnitudes, two values at a time
-#pragma unroll
-      for (int v = 0; v < 8; ++v) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const u16x2 a = __builtin_bit_cast(u16x2, vr[v][e] & 0x7fff7fffu), m = __builtin_bit_cast(u16x2, top);
-          top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, m));
-        }
-        const int row = 8 * v + (lane >> 3);
-        *reinterpret_cast<u32x4*>(s_v + row * 128 + ((lane & 7) ^ swz(row, 8)) * 16) = vr[v];
-      }
-      wrong = OUT && __any((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u);
+      if (!OUT) total += end;
     }
-    // this wave's copies for the chunk have landed, then everybody's; and
-    // everybody has read the other buffer
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // everybody's copies have landed, and everybody has read the other buffer
     __syncthreads();
-    if (left > 0) copy(t0 + PC, left < PC ? left : PC, buf ^ 1);
+    if (left > 0) fetch(t0 + PC, left < PC ? left : PC, buf ^ 1);
+    if (!active) continue;
     const unsigned char *s_k = smem + L::K + buf * PC * DK * 2, *s_q = smem + L::Q + buf * PC * DK * 2;
+    unsigned char* s_v = smem + v_at + buf * L::V_BYTES;
+    auto frag_v = [&](int s) {                   // V^T (or V): tokens 16 s + 8 h ..
+      return join(read_tr(s_v + va + 16 * s * 64), read_tr(s_v + (va ^ 16) + (16 * s + 4) * 64));
+    };
+    bool wrong = false;
+    int* s_bad = reinterpret_cast<int*>(s_f + 5 * PC);
 
     if constexpr (OUT) {
-      // the triangle of K Q^T: tile t of fragment f, rows j, columns i
-      for (int c = wv; c < 2 * FRAGS; c += NW) {
-        const int f = c >> 1, t = c & 1, rb = frag_rb(f), kh = frag_kh(f);
-        const bool flip = (rb & 1) != 0;
-        f32x4s a = {0.f, 0.f, 0.f, 0.f};
+      f32x16 O[2];                               // columns, tokens 32 tt + ln
+      for (;;) {
+        // (or the state's split values would be made in front of this loop, and held)
 #pragma unroll
-        for (int kb = 0; kb < DB; ++kb)
-          a = mm32(frag_k(s_k, kh, t, kb),
-                   as_frag(*reinterpret_cast<const u32x4*>(s_q + (flip ? kq[kb ^ FLIP] : kq[kb]) + 16 * rb * ROW)), a);
-        reinterpret_cast<f32x4s*>(smem + L::QK)[c * 64 + lane] = a;
-      }
-      __syncthreads();
-      if (active) {
-        f32x4s O[4][NCB];                        // columns 4 hi + r of tile cb, token 16 rb + n
+        for (int db = 0; db < DB; ++db) asm volatile("" : "+v"(S[db]));
+        asm volatile("" : "+v"(fq), "+v"(fk), "+v"(va));
+        // O = (Q S)^T and the triangle T = K Q^T: blocks of 32 x 32, rows (tokens j) 32 jb ..,
+        // columns (tokens i) 32 ib ..; (ib, jb) = (0, 0), (1, 0), (1, 1)
+        f32x16 T[3];
 #pragma unroll
-        for (int rb = 0; rb < 4; ++rb)
-#pragma unroll
-          for (int cb = 0; cb < NCB; ++cb) O[rb][cb] = f32x4s{0.f, 0.f, 0.f, 0.f};
-        // O = (Q S)^T
-#pragma unroll
-        for (int kb = 0; kb < DB; ++kb) {
-          bf16x8 fq[4];
-#pragma unroll
-          for (int rb = 0; rb < 4; ++rb) fq[rb] = frag_q(s_q, rb, kb);
-#pragma unroll
-          for (int cb = 0; cb < NCB; ++cb) {
-            float x[8];
-            bf16x8 ss[3];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = S[kb][cb][e >> 2][e & 3];
-            split8(x, ss);
-#pragma unroll
-            for (int v = 2; v >= 0; --v)
-#pragma unroll
-              for (int rb = 0; rb < 4; ++rb) O[rb][cb] = mm32(ss[v], fq[rb], O[rb][cb]);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int rb = 0; rb < 4; ++rb) {
-          const float a = s_f[4 * PC + 16 * rb + n];
-#pragma unroll
-          for (int cb = 0; cb < NCB; ++cb) O[rb][cb] *= a;
-        }
-        // values that are none: left out of the products (a zero of P would bring
-        // them to earlier tokens) and put back behind them
-        int* s_bad = reinterpret_cast<int*>(s_f + 5 * PC);
-        if (wrong) {
-          s_bad[lane] = NEVER;
-          wave_lds_sync();
-#pragma unroll
-          for (int cb = 0; cb < NCB; ++cb)
-#pragma unroll
-            for (int kh = 0; kh < 2; ++kh) {
-              const bf16x8 f = frag_v(cb, kh);
-              int first = NEVER;
-#pragma unroll
-              for (int e = 7; e >= 0; --e) first = finite((float)f[e]) ? first : 32 * kh + 8 * hi + e;
-              if (first != NEVER) atomicMin(s_bad + col(cb), first);
-            }
-          wave_lds_sync();
-        }
-        // O += (P V)^T
-#pragma unroll
-        for (int kh = 0; kh < 2; ++kh) {
-          bf16x8 fv[NCB];
-#pragma unroll
-          for (int cb = 0; cb < NCB; ++cb) {
-            fv[cb] = frag_v(cb, kh);
-            if (wrong) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) fv[cb][e] = finite((float)fv[cb][e]) ? fv[cb][e] : (__bf16)0.f;
-            }
-          }
-          float lh[8], ll[8], dt[8];
-          ldn<8>(s_f + 32 * kh + 8 * hi, lh);
-          ldn<8>(s_f + PC + 32 * kh + 8 * hi, ll);
-          ldn<8>(s_f + 2 * PC + 32 * kh + 8 * hi, dt);
-#pragma unroll
-          for (int rb = 2 * kh; rb < 4; ++rb) {
-            const float ih = s_f[16 * rb + n], il = s_f[PC + 16 * rb + n];
-            float x[8];
-            const f32x4s* qk = reinterpret_cast<const f32x4s*>(smem + L::QK) + frag_of(rb, kh) * 128 + lane;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const f32x4s a = qk[64 * t];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) x[4 * t + r] = a[r];
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float d = __builtin_amdgcn_exp2f((ih - lh[e]) + (il - ll[e]));
-              const float y = x[e] * d * dt[e];
-              x[e] = rb >= 2 * kh + 2 || 32 * kh + 8 * hi + e <= 16 * rb + n ? y : 0.f;
-            }
-            bf16x8 fp[3];
-            split8(x, fp);
-#pragma unroll
-            for (int v = 2; v >= 0; --v)
-#pragma unroll
-              for (int cb = 0; cb < NCB; ++cb) O[rb][cb] = mm32(fv[cb], fp[v], O[rb][cb]);
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        }
-#pragma unroll
-        for (int rb = 0; rb < 4; ++rb)
-#pragma unroll
-          for (int cp = 0; cp < NCB / 2; ++cp) {
-            bf16x8 w;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float y = O[rb][2 * cp + (e >> 2)][e & 3];
-              if (wrong) y = 16 * rb + n >= s_bad[32 * cp + 8 * hi + e] ? __builtin_nanf("") : y;
-              w[e] = (__bf16)y;
-            }
-            if (16 * rb + n < nt)
-              *reinterpret_cast<bf16x8*>(reinterpret_cast<unsigned char*>(op + (int64_t)(t0 + 16 * rb) * p.os + 32 * cp) + oo) = w;
-          }
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if (active) {
-      if (left > 0) fetch(t0 + PC, left < PC ? left : PC);
-      __builtin_amdgcn_sched_barrier(0);
-      // S = exp(L_C) S + K^T (w V)
-      each([&](int kb, int cb, int e) { S[kb][cb][e] *= decay; });
-#pragma unroll
-      for (int kh = 0; kh < 2; ++kh) {
-        float w[8];
-        ldn<8>(s_f + 3 * PC + 32 * kh + 8 * hi, w);
-        bf16x8 fk[DB][2];
+        for (int r = 0; r < 16; ++r) O[0][r] = O[1][r] = T[0][r] = T[1][r] = T[2][r] = 0.f;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) fk[db][t] = frag_kt(s_k, db, t, kh);
+          for (int s = 0; s < 2; ++s) {
+            const int flip = 64 * db ^ 32 * s;
+            const bf16x8 q0 = frag(s_q, fq ^ flip), q1 = frag(s_q, (fq ^ flip) + 32 * ROW);
+            const bf16x8 k0 = frag(s_k, fk ^ flip), k1 = frag(s_k, (fk ^ flip) + 32 * ROW);
+            float x[8];
+            bf16x8 ss[3];
+            rows8(S[db], s, x);
+            split8(x, ss);
+            T[0] = mm16(k0, q0, T[0]);
+            T[1] = mm16(k0, q1, T[1]);
+            T[2] = mm16(k1, q1, T[2]);
 #pragma unroll
-        for (int cb = 0; cb < NCB; ++cb) {
-          const bf16x8 f = frag_v(cb, kh);
-          float x[8];
-          bf16x8 fw[3];
+            for (int v = 2; v >= 0; --v) {
+              O[0] = mm16(ss[v], q0, O[0]);
+              O[1] = mm16(ss[v], q1, O[1]);
+            }
+          }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = w[e] * (float)f[e];
-          split8(x, fw);
+        for (int tt = 0; tt < 2; ++tt) O[tt] *= s_f[4 * PC + 32 * tt + ln];
+        // O += (P V)^T
+        uint32_t top = 0;                        // the largest magnitudes of V, two values at a time
 #pragma unroll
-          for (int v = 2; v >= 0; --v)
+        for (int s = 0; s < 4; ++s) {
+          const bf16x8 fv = frag_v(s);
+          const u32x4 w = __builtin_bit_cast(u32x4, fv);
 #pragma unroll
-            for (int db = 0; db < DB; ++db)
+          for (int e = 0; e < 4; ++e)
+            top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, w[e] & 0x7fff7fffu),
+                                                                       __builtin_bit_cast(u16x2, top)));
+          float lh[8], ll[8], dt[8];
+          ldn<8>(s_f + 16 * s + 8 * hh, lh);
+          ldn<8>(s_f + PC + 16 * s + 8 * hh, ll);
+          ldn<8>(s_f + 2 * PC + 16 * s + 8 * hh, dt);
 #pragma unroll
-              for (int t = 0; t < 2; ++t) S[db][cb][t] = mm32(fk[db][t], fw[v], S[db][cb][t]);
-          __builtin_amdgcn_sched_barrier(0);
+          for (int ib = s >> 1; ib < 2; ++ib) {
+            const float ih = s_f[32 * ib + ln], il = s_f[PC + 32 * ib + ln];
+            float x[8];
+            bf16x8 fp[3];
+            rows8(T[ib + (s >> 1)], s & 1, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float y = x[e] * __builtin_amdgcn_exp2f((ih - lh[e]) + (il - ll[e])) * dt[e];
+              x[e] = ib > s >> 1 || 16 * s + 8 * hh + e <= 32 * ib + ln ? y : 0.f;
+            }
+            split8(x, fp);
+#pragma unroll
+            for (int v = 2; v >= 0; --v) O[ib] = mm16(fv, fp[v], O[ib]);
+          }
         }
+        // Values that are none would have come to earlier tokens by zeros of P: they
+        // are taken out of V, with each column's first token that has one, and all
+        // is done again.
+        if (wrong || !__any((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u)) break;
+        wrong = true;
+        if (lane < SCAN_COLS) s_bad[lane] = NEVER;
+        wave_lds_sync();
+        for (int c = lane; c < PC * SCAN_COLS; c += 64) {
+          const int row = c / SCAN_COLS, cc = c % SCAN_COLS;
+          bf16* at = reinterpret_cast<bf16*>(s_v + row * 64 + ((cc >> 3) ^ swz(row, 4)) * 16) + (cc & 7);
+          if ((*at & 0x7f80) == 0x7f80) {
+            *at = 0;
+            atomicMin(s_bad + cc, row);
+          }
+        }
+        wave_lds_sync();
       }
+      if (wrong) {
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (32 * tt + ln >= s_bad[16 * (r >> 3) + 8 * hh + (r & 7)]) O[tt][r] = __builtin_nanf("");
+      }
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          bf16x8 w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = (__bf16)O[tt][8 * s + e];
+          if (32 * tt + ln < nt)
+            *reinterpret_cast<bf16x8*>(reinterpret_cast<unsigned char*>(op + (int64_t)(t0 + 32 * tt) * p.os + 16 * s) + oo) = w;
+        }
+    }
+    // S = exp(L_C) S + K^T (w V)
+#pragma unroll
+    for (int db = 0; db < DB; ++db) S[db] *= decay;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const bf16x8 f = frag_v(s);
+      float w[8], x[8];
+      bf16x8 fw[3];
+      ldn<8>(s_f + 3 * PC + 16 * s + 8 * hh, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = w[e] * (float)f[e];
+      split8(x, fw);
+      const int flip = (s & 1) * TFLIP;
+      bf16x8 a[DB];
+#pragma unroll
+      for (int db = 0; db < DB; ++db) {
+        const unsigned char* at = s_k + (kt ^ (64 * db ^ flip)) + 16 * s * ROW;
+        a[db] = join(read_tr(at), read_tr(at + 4 * ROW));
+      }
+#pragma unroll
+      for (int v = 2; v >= 0; --v)
+#pragma unroll
+        for (int db = 0; db < DB; ++db) S[db] = mm16(a[db], fw[v], S[db]);
+    }
+    if (wrong) {
+      const float x = s_bad[col] == NEVER ? 0.f : __builtin_nanf("");
+#pragma unroll
+      for (int db = 0; db < DB; ++db) S[db] += x;
     }
   }
   if (!active) return;
 
   if (!OUT) {
     f32x4s* to = seg_at(slot);
-    each([&](int kb, int cb, int e) { to[((kb * NCB + cb) * 2 + e) * 64] = S[kb][cb][e]; });
+    each4([&](int db, int q, int at) { to[at] = four(db, q); });
     if (lane == 0 && c0 == 0) p.seg_decay[(size_t)slot * p.H + h] = exp2_of(total);
     return;
   }
   if (!last) return;                             // (the state behind a segment is known already)
-  each([&](int kb, int cb, int e) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) Sg[(size_t)(32 * kb + 8 * hi + 4 * e + r) * DV + col(cb)] = S[kb][cb][e][r];
-  });
+  each([&](int db, int r, int row) { Sg[(size_t)row * DV] = S[db][r]; });
   if (!p.prime) return;
   const int off = p.sk.off[h], ranks = p.sk.off[h + 1] - off;
   if (ranks == 0) {                              // a dense-fallback head: the state copy
     int at = 0;
     while (at + 1 < p.sk.ndense && p.sk.dense_list[at] != h) ++at;
-    bf16* C = reinterpret_cast<bf16*>(p.sk.Sc) + ((size_t)b * p.sk.ndense + at) * DK * DV + c0;
-    each([&](int kb, int cb, int e) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) C[(size_t)(32 * kb + 8 * hi + 4 * e + r) * DV + col(cb)] = f32_to_bf16(S[kb][cb][e][r]);
-    });
+    bf16* C = reinterpret_cast<bf16*>(p.sk.Sc) + ((size_t)b * p.sk.ndense + at) * DK * DV + c0 + col;
+    each([&](int db, int r, int row) { C[(size_t)row * DV] = f32_to_bf16(S[db][r]); });
     return;
   }
-  // u_j = S^T p_j in fp32: K-step (kb, e) of v_mfma_f32_16x16x4_f32 covers rows
-  // 32 kb + 8 k + e; a lane's results are columns 4 hi + r of tile cb for j = n
-  f32x4s U[NCB];
+  // u_j = S^T p_j in fp32: register r of v_mfma_f32_32x32x2_f32's operand is rows
+  // 32 db + 16 (r / 8) + 8 k + r % 8; a lane's results are columns for j = ln
+  f32x16 U;
 #pragma unroll
-  for (int cb = 0; cb < NCB; ++cb) U[cb] = f32x4s{0.f, 0.f, 0.f, 0.f};
-  const float* P = p.sk.Pt + (size_t)(off + (n < ranks ? n : 0)) * DK + 8 * hi;
+  for (int r = 0; r < 16; ++r) U[r] = 0.f;
+  const float* P = p.sk.Pt + (size_t)(off + (ln < ranks ? ln : 0)) * DK + 8 * hh;
 #pragma unroll
-  for (int kb = 0; kb < DB; ++kb) {
-    float x[8];
-    ldn<8>(P + 32 * kb, x);
+  for (int db = 0; db < DB; ++db)
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-#pragma unroll
-      for (int cb = 0; cb < NCB; ++cb) U[cb] = mm4(S[kb][cb][e >> 2][e & 3], x[e], U[cb]);
-  }
-  if (n < ranks) {                               // (columns j >= ranks repeat row 0 and are dropped)
-    bf16* Ug = reinterpret_cast<bf16*>(p.sk.U) + ((size_t)b * p.sk.R + off + n) * DV + c0;
-#pragma unroll
-    for (int cp = 0; cp < NCB / 2; ++cp) {
+    for (int s = 0; s < 2; ++s) {
       float x[8];
+      ldn<8>(P + 32 * db + 16 * s, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = U[2 * cp + (e >> 2)][e & 3];
-      stn<8>(Ug + 32 * cp + 8 * hi, x);
+      for (int e = 0; e < 8; ++e) U = __builtin_amdgcn_mfma_f32_32x32x2f32(S[db][8 * s + e], x[e], U, 0, 0, 0);
+    }
+  if (ln < ranks) {                              // (columns j >= ranks repeat row 0 and are dropped)
+    bf16* Ug = reinterpret_cast<bf16*>(p.sk.U) + ((size_t)b * p.sk.R + off + ln) * DV + c0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float x[8];
+      rows8(U, s, x);
+      stn<8>(Ug + 16 * s + 8 * hh, x);
     }
   }
 }
