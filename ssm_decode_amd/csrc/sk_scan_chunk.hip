@@ -26,6 +26,8 @@
 namespace sk {
 namespace {
 
+// (their terms may pass 2^(128 - NEAR_BITS) only where they overflow on the way to an output)
+constexpr int NEAR_BITS = 40;
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -48,7 +50,7 @@ struct ScanLds {
   static constexpr int K = 0;                    // [2][64][DK]
   static constexpr int Q = K + 2 * PC * DK * 2;
   static constexpr int V = Q + (OUT ? 2 * PC * DK * 2 : 0);      // wave after wave: [2][64][32], then the factors
-  static constexpr int V_BYTES = PC * SCAN_COLS * 2, WAVE = 2 * V_BYTES + 6 * PC * 4;
+  static constexpr int V_BYTES = PC * SCAN_COLS * 2, WAVE = 2 * V_BYTES + 7 * PC * 4;
   static constexpr int bytes(int waves) { return V + waves * WAVE; }
 };
 
@@ -152,30 +154,30 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
   };
   const uint32_t lds0 = lds_address(smem);
   const int v_at = L::V + wv * L::WAVE;
-  float* s_f = reinterpret_cast<float*>(smem + v_at + 2 * L::V_BYTES);      // L (upper and lower part), dt, weight, exp L, first wrong tokens
+  float* s_f = reinterpret_cast<float*>(smem + v_at + 2 * L::V_BYTES);      // L (upper and lower part), dt, weight, exp L; first wrong tokens
   float dr = 0.f;
-  // K, Q, V and dt (a token a lane) of a chunk of nt tokens into buffer buf.  Rows
+  // dt (a token a lane) of a chunk of nt tokens, K and Q's pieces that this wave takes in
+  // part `at` of `of` of a chunk's time, and a quarter of its columns of V, into buffer
+  // buf.  (All at once they would stand in the way of each other, and of the wave: a
+  // prompt of 16384 tokens spent 6500 of 32000 cycles a chunk on their issue.)  Rows
   // behind the end repeat the last one with a dt of 0: their weights are zeros, and
   // what they give is not stored.
-  auto fetch = [&](int t0, int nt, int buf) {
-    const int end = nt - 1;
-    if (active) {
-      const int r = lane < end ? lane : end;
-      dr = to_f32(*reinterpret_cast<const bf16*>(reinterpret_cast<const unsigned char*>(dp + (int64_t)t0 * p.gs) + (uint32_t)(r * p.gs * 2)));
-    }
-    for (int c = wv; c < PPR; c += NW) {
-      const int at = c * 64 + lane, row = at / PPR, pc = (at % PPR) ^ swz(row, PPR), r = row < end ? row : end;
+  int fl = lane;
+  auto fetch_dt = [&](int t0, int nt) {
+    const int r = fl < nt - 1 ? fl : nt - 1;
+    dr = to_f32(*reinterpret_cast<const bf16*>(reinterpret_cast<const unsigned char*>(dp + (int64_t)t0 * p.gs) + (uint32_t)(r * p.gs * 2)));
+  };
+  auto copy_kq = [&](int t0, int nt, int buf, int at, int of) {
+    for (int c = wv + NW * at; c < PPR; c += NW * of) {
+      const int x = c * 64 + fl, row = x / PPR, pc = (x % PPR) ^ swz(row, PPR), r = row < nt - 1 ? row : nt - 1;
       const uint32_t to = lds0 + buf * PC * DK * 2 + c * 1024;
       copy16(uniform(kp + (int64_t)t0 * p.ks), (uint32_t)(r * p.ks * 2) + pc * 16, uniform(to + L::K));
       if (OUT) copy16(uniform(qp + (int64_t)t0 * p.qs), (uint32_t)(r * p.qs * 2) + pc * 16, uniform(to + L::Q));
     }
-    if (active) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int row = 16 * v + (lane >> 2), pc = (lane & 3) ^ swz(row, 4), r = row < end ? row : end;
-        copy16(uniform(vp + (int64_t)t0 * p.vs), (uint32_t)(r * p.vs * 2) + pc * 16, uniform(lds0 + v_at + buf * L::V_BYTES + v * 1024));
-      }
-    }
+  };
+  auto copy_v = [&](int t0, int nt, int buf, int v) {
+    const int row = 16 * v + (fl >> 2), pc = (fl & 3) ^ swz(row, 4), r = row < nt - 1 ? row : nt - 1;
+    copy16(uniform(vp + (int64_t)t0 * p.vs), (uint32_t)(r * p.vs * 2) + pc * 16, uniform(lds0 + v_at + buf * L::V_BYTES + v * 1024));
   };
 
   // -------------------------------------------------------------- state
@@ -196,7 +198,15 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       for (int q = 0; q < 4; ++q) f(db, q, (db * 4 + q) * 64);
   };
   auto four = [&](int db, int q) { return f32x4s{S[db][4 * q], S[db][4 * q + 1], S[db][4 * q + 2], S[db][4 * q + 3]}; };
-  if (len > 0) fetch(0, len < PC ? len : PC, 0);
+  if (len > 0) {
+    const int nt = len < PC ? len : PC;
+    copy_kq(0, nt, 0, 0, 1);
+    if (active) {
+      fetch_dt(0, nt);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) copy_v(0, nt, 0, v);
+    }
+  }
   each([&](int db, int r, int) { S[db][r] = 0.f; });
   if (active) {
     if (seg == 0 && !(OUT && !last)) {
@@ -235,16 +245,16 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
   int va = (8 * hh + ti) * 64 + ((2 * g0 + (run & 1)) ^ swz(8 * hh + ti, 4)) * 16 + (run >> 1) * 8;
   auto frag = [](const unsigned char* s, int at) { return as_frag(*reinterpret_cast<const u32x4*>(s + at)); };
 
+  asm volatile("s_waitcnt vmcnt(0)" : "+v"(dr)::"memory");
   int buf = 0;
   for (int t0 = 0; t0 < len; t0 += PC, buf ^= 1) {
-    const int nt = len - t0 < PC ? len - t0 : PC, left = len - t0 - PC;
+    const int nt = len - t0 < PC ? len - t0 : PC, left = len - t0 - PC, next = left < PC ? left : PC;
     // (or every fragment's address would be made in front of the loop, and held)
-    asm volatile("" : "+v"(fq), "+v"(fk), "+v"(kt), "+v"(va));
-    // this wave's copies for the chunk have landed
-    asm volatile("s_waitcnt vmcnt(0)" : "+v"(dr)::"memory");
+    asm volatile("" : "+v"(fq), "+v"(fk), "+v"(kt), "+v"(va), "+v"(fl));
     // the chunk's decays, a token a lane: L split so that a difference of two is exact
     // to fp32 (a decay of less than 2^-256 a token is zero)
     float decay = 0.f;
+    bool near_one = false;
     if (active) {
       const float d = lane < nt ? dr : 0.f;
       double l = (double)d * rate;
@@ -253,7 +263,8 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       const double upper = (at + 0x1.8p42) - 0x1.8p42;      // a multiple of 2^-10, |L| <= 2^14
       s_f[lane] = (float)upper;
       s_f[PC + lane] = (float)(at - upper);
-      s_f[2 * PC + lane] = d;
+      near_one = end >= -NEAR_BITS;
+      s_f[2 * PC + lane] = OUT && near_one ? exp2_of(-at) * d : d;
       s_f[3 * PC + lane] = exp2_of(end - at) * d;
       s_f[4 * PC + lane] = exp2_of(at);
       decay = exp2_of(end);
@@ -261,84 +272,82 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
     }
     // everybody's copies have landed, and everybody has read the other buffer
     __syncthreads();
-    if (left > 0) fetch(t0 + PC, left < PC ? left : PC, buf ^ 1);
-    if (!active) continue;
+    if (!active) {
+      if (left > 0) copy_kq(t0 + PC, next, buf ^ 1, 0, 1);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      continue;
+    }
+    if (left > 0) fetch_dt(t0 + PC, next);
     const unsigned char *s_k = smem + L::K + buf * PC * DK * 2, *s_q = smem + L::Q + buf * PC * DK * 2;
     unsigned char* s_v = smem + v_at + buf * L::V_BYTES;
     auto frag_v = [&](int s) {                   // V^T (or V): tokens 16 s + 8 h ..
       return join(read_tr(s_v + va + 16 * s * 64), read_tr(s_v + (va ^ 16) + (16 * s + 4) * 64));
     };
+    int* s_bad = reinterpret_cast<int*>(s_f + 6 * PC);
     bool wrong = false;
-    int* s_bad = reinterpret_cast<int*>(s_f + 5 * PC);
+    f32x16 O[2], T[3];                           // outputs: columns, tokens 32 tt + ln; K Q^T: below
 
     if constexpr (OUT) {
-      f32x16 O[2];                               // columns, tokens 32 tt + ln
-      for (;;) {
-        // (or the state's split values would be made in front of this loop, and held)
+      // O = (Q S)^T and the triangle T = K Q^T in blocks of 32 x 32, rows (tokens j)
+      // 32 jb .., columns (tokens i) 32 ib ..: (ib, jb) = (0, 0), (1, 0), (1, 1).  In each of
+      // the steps the next one's fragments are read and its values split between the
+      // matrix instructions.
+      constexpr int STEPS = 2 * DB;
+      bf16x8 fr[2][4], ss[2][3];
+      auto load = [&](int st) {
+        const int flip = 64 * (st >> 1) ^ 32 * (st & 1), u = st & 1;
+        fr[u][0] = frag(s_q, fq ^ flip);
+        fr[u][1] = frag(s_q, (fq ^ flip) + 32 * ROW);
+        fr[u][2] = frag(s_k, fk ^ flip);
+        fr[u][3] = frag(s_k, (fk ^ flip) + 32 * ROW);
+      };
+      auto split_s = [&](int st) {
+        float x[8];
+        rows8(S[st >> 1], st & 1, x);
+        split8(x, ss[st & 1]);
+      };
+      load(0);
+      split_s(0);
+      __builtin_amdgcn_sched_barrier(0);
+      uint32_t top = 0;                          // the largest magnitudes of V, two values at a time
+      f32x16 zero;
 #pragma unroll
-        for (int db = 0; db < DB; ++db) asm volatile("" : "+v"(S[db]));
-        asm volatile("" : "+v"(fq), "+v"(fk), "+v"(va));
-        // O = (Q S)^T and the triangle T = K Q^T: blocks of 32 x 32, rows (tokens j) 32 jb ..,
-        // columns (tokens i) 32 ib ..; (ib, jb) = (0, 0), (1, 0), (1, 1)
-        f32x16 T[3];
+      for (int r = 0; r < 16; ++r) zero[r] = 0.f;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) O[0][r] = O[1][r] = T[0][r] = T[1][r] = T[2][r] = 0.f;
-#pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const int flip = 64 * db ^ 32 * s;
-            const bf16x8 q0 = frag(s_q, fq ^ flip), q1 = frag(s_q, (fq ^ flip) + 32 * ROW);
-            const bf16x8 k0 = frag(s_k, fk ^ flip), k1 = frag(s_k, (fk ^ flip) + 32 * ROW);
-            float x[8];
-            bf16x8 ss[3];
-            rows8(S[db], s, x);
-            split8(x, ss);
-            T[0] = mm16(k0, q0, T[0]);
-            T[1] = mm16(k0, q1, T[1]);
-            T[2] = mm16(k1, q1, T[2]);
-#pragma unroll
-            for (int v = 2; v >= 0; --v) {
-              O[0] = mm16(ss[v], q0, O[0]);
-              O[1] = mm16(ss[v], q1, O[1]);
-            }
-          }
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) O[tt] *= s_f[4 * PC + 32 * tt + ln];
-        // O += (P V)^T
-        uint32_t top = 0;                        // the largest magnitudes of V, two values at a time
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const bf16x8 fv = frag_v(s);
-          const u32x4 w = __builtin_bit_cast(u32x4, fv);
+      for (int st = 0; st < STEPS; ++st) {
+        const int u = st & 1;
+        const bf16x8 q0 = fr[u][0], q1 = fr[u][1];
+        if (st + 1 < STEPS) {
+          load(st + 1);
+          split_s(st + 1);
+        }
+        if (st >= STEPS - 4) {
+          const u32x4 w = __builtin_bit_cast(u32x4, frag_v(st - (STEPS - 4)));
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, w[e] & 0x7fff7fffu),
                                                                        __builtin_bit_cast(u16x2, top)));
-          float lh[8], ll[8], dt[8];
-          ldn<8>(s_f + 16 * s + 8 * hh, lh);
-          ldn<8>(s_f + PC + 16 * s + 8 * hh, ll);
-          ldn<8>(s_f + 2 * PC + 16 * s + 8 * hh, dt);
-#pragma unroll
-          for (int ib = s >> 1; ib < 2; ++ib) {
-            const float ih = s_f[32 * ib + ln], il = s_f[PC + 32 * ib + ln];
-            float x[8];
-            bf16x8 fp[3];
-            rows8(T[ib + (s >> 1)], s & 1, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float y = x[e] * __builtin_amdgcn_exp2f((ih - lh[e]) + (il - ll[e])) * dt[e];
-              x[e] = ib > s >> 1 || 16 * s + 8 * hh + e <= 32 * ib + ln ? y : 0.f;
-            }
-            split8(x, fp);
-#pragma unroll
-            for (int v = 2; v >= 0; --v) O[ib] = mm16(fv, fp[v], O[ib]);
-          }
         }
-        // Values that are none would have come to earlier tokens by zeros of P: they
-        // are taken out of V, with each column's first token that has one, and all
-        // is done again.
-        if (wrong || !__any((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u)) break;
+        O[0] = mm16(ss[u][2], q0, st ? O[0] : zero);
+        O[1] = mm16(ss[u][2], q1, st ? O[1] : zero);
+        T[0] = mm16(fr[u][2], q0, st ? T[0] : zero);
+        T[1] = mm16(fr[u][2], q1, st ? T[1] : zero);
+        T[2] = mm16(fr[u][3], q1, st ? T[2] : zero);
+#pragma unroll
+        for (int v = 1; v >= 0; --v) {
+          O[0] = mm16(ss[u][v], q0, O[0]);
+          O[1] = mm16(ss[u][v], q1, O[1]);
+        }
+        region<9, 1, 5>();
+        if (left > 0) {
+          copy_kq(t0 + PC, next, buf ^ 1, st, STEPS);
+          if (st >= STEPS - 4) copy_v(t0 + PC, next, buf ^ 1, st - (STEPS - 4));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // Values that are none would come to earlier tokens by zeros of P: they are taken
+      // out of V, with each column's first token that has one.
+      if (__any((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u)) {
         wrong = true;
         if (lane < SCAN_COLS) s_bad[lane] = NEVER;
         wave_lds_sync();
@@ -352,47 +361,136 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
         }
         wave_lds_sync();
       }
-      if (wrong) {
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (32 * tt + ln >= s_bad[16 * (r >> 3) + 8 * hh + (r & 7)]) O[tt][r] = __builtin_nanf("");
-      }
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          bf16x8 w;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = (__bf16)O[tt][8 * s + e];
-          if (32 * tt + ln < nt)
-            *reinterpret_cast<bf16x8*>(reinterpret_cast<unsigned char*>(op + (int64_t)(t0 + 32 * tt) * p.os + 16 * s) + oo) = w;
-        }
     }
-    // S = exp(L_C) S + K^T (w V)
+
+    // Where a chunk's decays together are less than 2^-NEAR_BITS, P's are taken one by
+    // one, in T's place (and the factors below are 1).
+    if (OUT && !near_one) {
+#pragma unroll 1
+      for (int tt = 0; tt < 2; ++tt) {
+        const float ih = s_f[32 * tt + ln], il = s_f[PC + 32 * tt + ln], a = s_f[4 * PC + 32 * tt + ln];
 #pragma unroll
-    for (int db = 0; db < DB; ++db) S[db] *= decay;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const bf16x8 f = frag_v(s);
-      float w[8], x[8];
-      bf16x8 fw[3];
-      ldn<8>(s_f + 3 * PC + 16 * s + 8 * hh, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = w[e] * (float)f[e];
-      split8(x, fw);
+        for (int r = 0; r < 16; ++r) {
+          const int j = 16 * (r >> 3) + 8 * hh + (r & 7);
+          auto factor = [&](int jj) { return __builtin_amdgcn_exp2f((ih - s_f[jj]) + (il - s_f[PC + jj])) * s_f[2 * PC + jj]; };
+          if (tt == 0) {
+            O[0][r] *= a;
+            T[0][r] *= j <= ln ? factor(j) : 0.f;
+          } else {
+            O[1][r] *= a;
+            T[1][r] *= factor(j);
+            T[2][r] *= j <= ln ? factor(32 + j) : 0.f;
+          }
+        }
+      }
+      wave_lds_sync();
+      s_f[2 * PC + lane] = 1.f;
+      s_f[4 * PC + lane] = 1.f;
+      wave_lds_sync();
+    }
+
+    // S = exp(L_C) S + K^T (w V) and O = diag(exp L) (O + (P V)^T), in turn: the matrix
+    // instructions of one with the reads, factors and splits of the other between.
+    // P's are quotients here: exp(-L_j) dt_j on T, exp(L_i) on the outputs.
+    constexpr int FA = OUT ? 1 : 2;              // (with outputs K^T's next is read behind its last use)
+    bf16x8 fa[FA][DB], fw[3], fp[2][3], fv[2];
+    float wj[8], fj[8];
+    auto load_k = [&](int s) {
       const int flip = (s & 1) * TFLIP;
-      bf16x8 a[DB];
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
         const unsigned char* at = s_k + (kt ^ (64 * db ^ flip)) + 16 * s * ROW;
-        a[db] = join(read_tr(at), read_tr(at + 4 * ROW));
+        fa[s % FA][db] = join(read_tr(at), read_tr(at + 4 * ROW));
+      }
+    };
+    // (factors are read one region before they are needed)
+    auto load_w = [&](int s) { ldn<8>(s_f + 3 * PC + 16 * s + 8 * hh, wj); };
+    auto load_f = [&](int s) { ldn<8>(s_f + 2 * PC + 16 * s + 8 * hh, fj); };
+    auto prep_w = [&](int s) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = wj[e] * (float)fv[s & 1][e];
+      split8(x, fw);
+    };
+    auto prep_p = [&](int ib, int s) {           // of P, columns (tokens i) 32 ib .., rows (tokens j) 16 s ..
+      float x[8];
+      rows8(T[ib + (s >> 1)], s & 1, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] *= fj[e];
+        if (ib == s >> 1) x[e] = 16 * (s & 1) + 8 * hh + e <= ln ? x[e] : 0.f;
+      }
+      split8(x, fp[ib]);
+    };
+    auto store = [&](int tt) {
+      O[tt] *= s_f[4 * PC + 32 * tt + ln];
+      if (wrong) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (32 * tt + ln >= s_bad[16 * (r >> 3) + 8 * hh + (r & 7)]) O[tt][r] = __builtin_nanf("");
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        bf16x8 w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = (__bf16)O[tt][8 * s + e];
+        if (32 * tt + ln < nt)
+          *reinterpret_cast<bf16x8*>(reinterpret_cast<unsigned char*>(op + (int64_t)(t0 + 32 * tt) * p.os + 16 * s) + oo) = w;
+      }
+    };
+    fv[0] = frag_v(0);
+    load_w(0);
+    load_k(0);
+    if (OUT) load_f(0);
+#pragma unroll
+    for (int db = 0; db < DB; ++db) S[db] *= decay;
+    prep_w(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s + 1 < 4) {
+        fv[(s + 1) & 1] = frag_v(s + 1);
+        load_w(s + 1);
+      }
+      if (OUT) {
+#pragma unroll
+        for (int ib = s >> 1; ib < 2; ++ib) prep_p(ib, s);
+      } else if (s + 1 < 4) {
+        load_k(s + 1);
       }
 #pragma unroll
       for (int v = 2; v >= 0; --v)
 #pragma unroll
-        for (int db = 0; db < DB; ++db) S[db] = mm16(a[db], fw[v], S[db]);
+        for (int db = 0; db < DB; ++db) S[db] = mm16(fa[s % FA][db], fw[v], S[db]);
+      region<3 * DB, 1, OUT ? 10 : 1>();
+      if constexpr (OUT) {
+        if (s + 1 < 4) {
+          load_f(s + 1);
+          load_k(s + 1);
+        }
+#pragma unroll
+        for (int v = 2; v >= 0; --v)
+#pragma unroll
+          for (int ib = s >> 1; ib < 2; ++ib) O[ib] = mm16(fv[s & 1], fp[ib][v], O[ib]);
+      } else if (left > 0) {
+        copy_kq(t0 + PC, next, buf ^ 1, s, 4);
+        copy_v(t0 + PC, next, buf ^ 1, s);
+      }
+      if (s + 1 < 4) prep_w(s + 1);
+      if (OUT) {
+        region<6, 2, 10>();
+        if (s == 2) store(0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // This wave's copies for the next chunk have landed: all but the last two of its
+    // accesses to memory, which are the first tokens' outputs (of a chunk with a
+    // next one).
+    if (OUT) {
+      asm volatile("s_waitcnt vmcnt(2)" : "+v"(dr)::"memory");
+      store(1);
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" : "+v"(dr)::"memory");
     }
     if (wrong) {
       const float x = s_bad[col] == NEVER ? 0.f : __builtin_nanf("");
