@@ -13,11 +13,11 @@
 // bf16 values, so a product with bf16 data (Q, V, K^T) takes three instructions.
 //
 // Layout.  A wave has 32 columns of one head's state, all rows, in registers, and a
-// workgroup up to eight waves of one group, whose keys and queries it shares.  K, Q
-// and each wave's columns of V are in LDS twice: the next chunk's copy, straight from
-// memory, is in flight over the present one.  All products are the transposed ones,
-// so that a lane's results are runs of columns of one token, and K Q^T leaves each
-// wave the triangle as the operand that P V needs.
+// workgroup up to eight waves of one group, whose keys and queries it shares.  K, Q and
+// V (64 columns for two waves) are in LDS twice: the next chunk's copy, straight from
+// memory, is in flight over the present one.  The triangle of K Q^T is formed once a
+// chunk, by all waves, and left in LDS as the operand that P V needs.  All products
+// are the transposed ones, so that a lane's results are runs of columns of one token.
 #include <type_traits>
 
 #include "sk_prompt_chunk.hpp"
@@ -49,9 +49,10 @@ template <int DK, bool OUT>
 struct ScanLds {
   static constexpr int K = 0;                    // [2][64][DK]
   static constexpr int Q = K + 2 * PC * DK * 2;
-  static constexpr int V = Q + (OUT ? 2 * PC * DK * 2 : 0);      // wave after wave: [2][64][32], then the factors
-  static constexpr int V_BYTES = PC * SCAN_COLS * 2, WAVE = 2 * V_BYTES + 7 * PC * 4;
-  static constexpr int bytes(int waves) { return V + waves * WAVE; }
+  static constexpr int T = Q + (OUT ? 2 * PC * DK * 2 : 0);      // six fragments of K Q^T in fp32
+  static constexpr int V = T + (OUT ? FRAGS * 2 * FRAG_BYTES : 0);      // two waves after two: [2][64][64]
+  static constexpr int V_BYTES = PC * 2 * SCAN_COLS * 2, FACTORS = 7 * PC * 4;
+  static constexpr int bytes(int waves) { return V + waves / 2 * 2 * V_BYTES + waves * FACTORS; }
 };
 
 // Sum of the lanes up to this one, in 64 bits.
@@ -90,6 +91,12 @@ __device__ __forceinline__ const void* uniform(const void* x) {
   const uint64_t u = reinterpret_cast<uint64_t>(x);
   return reinterpret_cast<const void*>((uint64_t)uniform((uint32_t)(u >> 32)) << 32 | uniform((uint32_t)u));
 }
+
+// The f-th pair of 16 x 16 tiles of the triangle: columns (tokens i) 16 rb .., rows
+// (tokens j) 32 kh ..; and its fragment of 32 columns of block ib, rows 16 s ..
+__device__ __forceinline__ constexpr int frag_rb(int f) { return f < 2 ? f : 2 + (f - 2) / 2; }
+__device__ __forceinline__ constexpr int frag_kh(int f) { return f < 2 ? 0 : (f - 2) & 1; }
+__device__ __forceinline__ constexpr int frag_of(int ib, int s) { return ib == 0 ? s : 2 + s; }
 
 // One workgroup per (segment or prompt, group, part of its heads).  Where prompts are
 // cut into segments of 2^seg_shift tokens, three launches take the place of one:
@@ -144,20 +151,20 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
   // ------------------------------------------------------------- copies
   const bf16* kp = reinterpret_cast<const bf16*>(p.k) + (int64_t)s0 * p.ks + (int64_t)g * DK;
   const bf16* qp = reinterpret_cast<const bf16*>(p.q) + (int64_t)s0 * p.qs + (int64_t)g * DK;
-  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + (int64_t)s0 * p.vs + (int64_t)h * DV + c0;
+  const bf16* vp = reinterpret_cast<const bf16*>(p.v) + (int64_t)s0 * p.vs + (int64_t)h * DV + (c0 & -64);
   const bf16* dp = reinterpret_cast<const bf16*>(p.gate) + (int64_t)s0 * p.gs + h;
   // Rows have their 16-byte pieces swizzled so that those of a fragment spread over
-  // the banks: piece pc of a row of PPR (16, DK = 64: 8, V: 4) is at pc ^ swz(row).
+  // the banks: piece pc of a row of PPR (16, DK = 64 and V: 8) is at pc ^ swz(row).
   auto swz = [](int row, int ppr) {
     const int s = (row & 3) | ((row >> 1) & 12);
-    return ppr == 16 ? s : ppr == 8 ? s >> 1 : (row >> 2) & 3;
+    return ppr == 16 ? s : s >> 1;
   };
   const uint32_t lds0 = lds_address(smem);
-  const int v_at = L::V + wv * L::WAVE;
-  float* s_f = reinterpret_cast<float*>(smem + v_at + 2 * L::V_BYTES);      // L (upper and lower part), dt, weight, exp L; first wrong tokens
+  const int v_at = L::V + (wv >> 1) * 2 * L::V_BYTES;
+  float* s_f = reinterpret_cast<float*>(smem + L::V + NW / 2 * 2 * L::V_BYTES + wv * L::FACTORS);      // L (upper and lower part), dt, weight, exp L; first wrong tokens
   float dr = 0.f;
   // dt (a token a lane) of a chunk of nt tokens, K and Q's pieces that this wave takes in
-  // part `at` of `of` of a chunk's time, and a quarter of its columns of V, into buffer
+  // part `at` of `of` of a chunk's time, and eight of its half of V's rows, into buffer
   // buf.  (All at once they would stand in the way of each other, and of the wave: a
   // prompt of 16384 tokens spent 6500 of 32000 cycles a chunk on their issue.)  Rows
   // behind the end repeat the last one with a dt of 0: their weights are zeros, and
@@ -176,8 +183,8 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
     }
   };
   auto copy_v = [&](int t0, int nt, int buf, int v) {
-    const int row = 16 * v + (fl >> 2), pc = (fl & 3) ^ swz(row, 4), r = row < nt - 1 ? row : nt - 1;
-    copy16(uniform(vp + (int64_t)t0 * p.vs), (uint32_t)(r * p.vs * 2) + pc * 16, uniform(lds0 + v_at + buf * L::V_BYTES + v * 1024));
+    const int first = 32 * (wv & 1) + 8 * v, row = first + (fl >> 3), pc = (fl & 7) ^ swz(row, 8), r = row < nt - 1 ? row : nt - 1;
+    copy16(uniform(vp + (int64_t)t0 * p.vs), (uint32_t)(r * p.vs * 2) + pc * 16, uniform(lds0 + v_at + buf * L::V_BYTES + first * 128));
   };
 
   // -------------------------------------------------------------- state
@@ -228,21 +235,23 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
   double total = 0.;
 
   bf16* op = reinterpret_cast<bf16*>(p.o) + (int64_t)s0 * p.os + (int64_t)h * DV + c0;
-  const uint32_t oo = (uint32_t)(ln * p.os * 2) + hh * 16;
+  const uint32_t oo = (uint32_t)((lane >> 2) * p.os * 2) + (lane & 3) * 16;
 
   // Byte addresses of a lane's fragments.  A fragment's rows differ by whole multiples
   // of what the swizzle looks at, or by such that change one bit of it, so that one
   // register, constant offsets and flipped bits cover all of a kind:
   //  tokens 32 tt + ln of Q, columns 32 db + 16 s + 8 h ..: (fq ^ 64 db ^ 32 s) + 32 tt ROW
-  //  tokens 32 tt + swap23(ln) of K, columns as those: (fk ^ 64 db ^ 32 s) + 32 tt ROW
+  //  tokens 16 rb + n of Q, columns 32 kb + 8 hi .. (the triangle's tiles are 16 x 16): (q16 ^ 64 kb ^ flip of rb) + 16 rb ROW
+  //  tokens 32 kh + block_row(n, t) of K, columns as those: (kk ^ 64 kb) + (32 kh + 4 t) ROW
   //  K^T, tokens 16 s + 8 h + ti (+ 4), the lane's run of four of rows 32 db ..: (kt ^ 64 db ^ flip of s) + (16 s (+ 4)) ROW
-  //  V, tokens as K^T's, the lane's run of four columns: va + 16 s 64, (va ^ 16) + (16 s + 4) 64
+  //  V, tokens as K^T's, the lane's run of four columns: (va ^ 64 (s & 1)) + (16 s (+ 4)) 128
   constexpr int ROW = DK * 2, TFLIP = PPR == 16 ? 128 : 64;
-  const int ti = n >> 2, run = n & 3, g0 = hi & 1;
+  const int ti = n >> 2, run = n & 3, g0 = hi & 1, half = 4 * (c0 / SCAN_COLS & 1);      // the wave's first piece of V
   int fq = ln * ROW + (hh ^ swz(ln, PPR)) * 16;
-  int fk = col * ROW + (hh ^ swz(col, PPR)) * 16;
+  int q16 = n * ROW + (hi ^ swz(n, PPR)) * 16;
+  int kk = block_row(n, 0) * ROW + (hi ^ swz(block_row(n, 0), PPR)) * 16;
   int kt = (8 * hh + ti) * ROW + ((2 * g0 + (run & 1)) ^ swz(8 * hh + ti, PPR)) * 16 + (run >> 1) * 8;
-  int va = (8 * hh + ti) * 64 + ((2 * g0 + (run & 1)) ^ swz(8 * hh + ti, 4)) * 16 + (run >> 1) * 8;
+  int va = (8 * hh + ti) * 128 + ((half + 2 * g0 + (run & 1)) ^ swz(8 * hh + ti, 8)) * 16 + (run >> 1) * 8;
   auto frag = [](const unsigned char* s, int at) { return as_frag(*reinterpret_cast<const u32x4*>(s + at)); };
 
   asm volatile("s_waitcnt vmcnt(0)" : "+v"(dr)::"memory");
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
   for (int t0 = 0; t0 < len; t0 += PC, buf ^= 1) {
     const int nt = len - t0 < PC ? len - t0 : PC, left = len - t0 - PC, next = left < PC ? left : PC;
     // (or every fragment's address would be made in front of the loop, and held)
-    asm volatile("" : "+v"(fq), "+v"(fk), "+v"(kt), "+v"(va), "+v"(fl));
+    asm volatile("" : "+v"(fq), "+v"(q16), "+v"(kk), "+v"(kt), "+v"(va), "+v"(fl));
     // the chunk's decays, a token a lane: L split so that a difference of two is exact
     // to fp32 (a decay of less than 2^-256 a token is zero)
     float decay = 0.f;
@@ -272,34 +281,45 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
     }
     // everybody's copies have landed, and everybody has read the other buffer
     __syncthreads();
+    const unsigned char *s_k = smem + L::K + buf * PC * DK * 2, *s_q = smem + L::Q + buf * PC * DK * 2;
+    if constexpr (OUT) {
+      // The triangle: tile t of rows (tokens j) 32 kh .., columns (tokens i) 16 rb .., left
+      // where a lane of the 32-column fragments finds it.
+      for (int c = wv; c < 2 * FRAGS; c += NW) {
+        const int f = c >> 1, t = c & 1, rb = frag_rb(f), kh = frag_kh(f), flip = (rb & 1) * TFLIP;
+        f32x4s a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < DB; ++kb)
+          a = mm32(frag(s_k, (kk ^ 64 * kb) + (32 * kh + 4 * t) * ROW), frag(s_q, (q16 ^ 64 * kb ^ flip) + 16 * rb * ROW), a);
+        const int to = frag_of(rb >> 1, 2 * kh + (hi >> 1)) * 2 + t;
+        reinterpret_cast<f32x4s*>(smem + L::T)[to * 64 + 32 * (hi & 1) + 16 * (rb & 1) + n] = a;
+      }
+    }
     if (!active) {
       if (left > 0) copy_kq(t0 + PC, next, buf ^ 1, 0, 1);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      if (OUT) __syncthreads();
       continue;
     }
     if (left > 0) fetch_dt(t0 + PC, next);
-    const unsigned char *s_k = smem + L::K + buf * PC * DK * 2, *s_q = smem + L::Q + buf * PC * DK * 2;
     unsigned char* s_v = smem + v_at + buf * L::V_BYTES;
     auto frag_v = [&](int s) {                   // V^T (or V): tokens 16 s + 8 h ..
-      return join(read_tr(s_v + va + 16 * s * 64), read_tr(s_v + (va ^ 16) + (16 * s + 4) * 64));
+      const unsigned char* at = s_v + (va ^ (s & 1) * 64) + 16 * s * 128;
+      return join(read_tr(at), read_tr(at + 4 * 128));
     };
     int* s_bad = reinterpret_cast<int*>(s_f + 6 * PC);
     bool wrong = false;
-    f32x16 O[2], T[3];                           // outputs: columns, tokens 32 tt + ln; K Q^T: below
+    f32x16 O[2];                                 // outputs: columns, tokens 32 tt + ln
 
     if constexpr (OUT) {
-      // O = (Q S)^T and the triangle T = K Q^T in blocks of 32 x 32, rows (tokens j)
-      // 32 jb .., columns (tokens i) 32 ib ..: (ib, jb) = (0, 0), (1, 0), (1, 1).  In each of
-      // the steps the next one's fragments are read and its values split between the
-      // matrix instructions.
+      // O = (Q S)^T: in each of the steps the next one's fragments are read and its values
+      // split between the matrix instructions.
       constexpr int STEPS = 2 * DB;
-      bf16x8 fr[2][4], ss[2][3];
+      bf16x8 fr[2][2], ss[2][3];
       auto load = [&](int st) {
         const int flip = 64 * (st >> 1) ^ 32 * (st & 1), u = st & 1;
         fr[u][0] = frag(s_q, fq ^ flip);
         fr[u][1] = frag(s_q, (fq ^ flip) + 32 * ROW);
-        fr[u][2] = frag(s_k, fk ^ flip);
-        fr[u][3] = frag(s_k, (fk ^ flip) + 32 * ROW);
       };
       auto split_s = [&](int st) {
         float x[8];
@@ -316,7 +336,6 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
         const int u = st & 1;
-        const bf16x8 q0 = fr[u][0], q1 = fr[u][1];
         if (st + 1 < STEPS) {
           load(st + 1);
           split_s(st + 1);
@@ -328,23 +347,18 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
             top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, w[e] & 0x7fff7fffu),
                                                                        __builtin_bit_cast(u16x2, top)));
         }
-        O[0] = mm16(ss[u][2], q0, st ? O[0] : zero);
-        O[1] = mm16(ss[u][2], q1, st ? O[1] : zero);
-        T[0] = mm16(fr[u][2], q0, st ? T[0] : zero);
-        T[1] = mm16(fr[u][2], q1, st ? T[1] : zero);
-        T[2] = mm16(fr[u][3], q1, st ? T[2] : zero);
 #pragma unroll
-        for (int v = 1; v >= 0; --v) {
-          O[0] = mm16(ss[u][v], q0, O[0]);
-          O[1] = mm16(ss[u][v], q1, O[1]);
-        }
-        region<9, 1, 5>();
+        for (int v = 2; v >= 0; --v)
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt) O[tt] = mm16(ss[u][v], fr[u][tt], st == 0 && v == 2 ? zero : O[tt]);
+        region<6, 1, 9>();
         if (left > 0) {
           copy_kq(t0 + PC, next, buf ^ 1, st, STEPS);
           if (st >= STEPS - 4) copy_v(t0 + PC, next, buf ^ 1, st - (STEPS - 4));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      __syncthreads();                           // (the triangle is whole)
       // Values that are none would come to earlier tokens by zeros of P: they are taken
       // out of V, with each column's first token that has one.
       if (__any((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u)) {
@@ -353,7 +367,7 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
         wave_lds_sync();
         for (int c = lane; c < PC * SCAN_COLS; c += 64) {
           const int row = c / SCAN_COLS, cc = c % SCAN_COLS;
-          bf16* at = reinterpret_cast<bf16*>(s_v + row * 64 + ((cc >> 3) ^ swz(row, 4)) * 16) + (cc & 7);
+          bf16* at = reinterpret_cast<bf16*>(s_v + row * 128 + ((half + (cc >> 3)) ^ swz(row, 8)) * 16) + (cc & 7);
           if ((*at & 0x7f80) == 0x7f80) {
             *at = 0;
             atomicMin(s_bad + cc, row);
@@ -363,35 +377,15 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       }
     }
 
-    // Where a chunk's decays together are less than 2^-NEAR_BITS, P's are taken one by
-    // one, in T's place (and the factors below are 1).
+    // Where a chunk's decays together are less than 2^-NEAR_BITS, P's factors are
+    // taken one by one.
     if (OUT && !near_one) {
-#pragma unroll 1
-      for (int tt = 0; tt < 2; ++tt) {
-        const float ih = s_f[32 * tt + ln], il = s_f[PC + 32 * tt + ln], a = s_f[4 * PC + 32 * tt + ln];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int j = 16 * (r >> 3) + 8 * hh + (r & 7);
-          auto factor = [&](int jj) { return __builtin_amdgcn_exp2f((ih - s_f[jj]) + (il - s_f[PC + jj])) * s_f[2 * PC + jj]; };
-          if (tt == 0) {
-            O[0][r] *= a;
-            T[0][r] *= j <= ln ? factor(j) : 0.f;
-          } else {
-            O[1][r] *= a;
-            T[1][r] *= factor(j);
-            T[2][r] *= j <= ln ? factor(32 + j) : 0.f;
-          }
-        }
-      }
-      wave_lds_sync();
-      s_f[2 * PC + lane] = 1.f;
-      s_f[4 * PC + lane] = 1.f;
-      wave_lds_sync();
+      for (int tt = 0; tt < 2; ++tt) O[tt] *= s_f[4 * PC + 32 * tt + ln];
     }
-
     // S = exp(L_C) S + K^T (w V) and O = diag(exp L) (O + (P V)^T), in turn: the matrix
     // instructions of one with the reads, factors and splits of the other between.
-    // P's are quotients here: exp(-L_j) dt_j on T, exp(L_i) on the outputs.
+    // P's factors are a quotient: exp(-L_j) dt_j on T, exp(L_i) on the outputs.
     constexpr int FA = OUT ? 1 : 2;              // (with outputs K^T's next is read behind its last use)
     bf16x8 fa[FA][DB], fw[3], fp[2][3], fv[2];
     float wj[8], fj[8];
@@ -412,18 +406,35 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       for (int e = 0; e < 8; ++e) x[e] = wj[e] * (float)fv[s & 1][e];
       split8(x, fw);
     };
+    f32x4s tr[2][2];
+    auto load_t = [&](int s) {
+#pragma unroll
+      for (int ib = s >> 1; ib < 2; ++ib)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          tr[ib][t] = reinterpret_cast<const f32x4s*>(smem + L::T)[(frag_of(ib, s) * 2 + t) * 64 + lane];
+    };
     auto prep_p = [&](int ib, int s) {           // of P, columns (tokens i) 32 ib .., rows (tokens j) 16 s ..
       float x[8];
-      rows8(T[ib + (s >> 1)], s & 1, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] *= fj[e];
+        x[e] = tr[ib][e >> 2][e & 3] * fj[e];
         if (ib == s >> 1) x[e] = 16 * (s & 1) + 8 * hh + e <= ln ? x[e] : 0.f;
       }
       split8(x, fp[ib]);
     };
+    auto far_factors = [&](int ib, int s) {      // (in place of T)
+      const float ih = s_f[32 * ib + ln], il = s_f[PC + 32 * ib + ln];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = 16 * s + 8 * hh + e;
+        tr[ib][e >> 2][e & 3] *= __builtin_amdgcn_exp2f((ih - s_f[j]) + (il - s_f[PC + j]));
+      }
+    };
+    // columns of a token go through LDS (over V's, which are read), so that a store has
+    // runs of 64 bytes
     auto store = [&](int tt) {
-      O[tt] *= s_f[4 * PC + 32 * tt + ln];
+      if (near_one) O[tt] *= s_f[4 * PC + 32 * tt + ln];
       if (wrong) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
@@ -434,14 +445,24 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
         bf16x8 w;
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = (__bf16)O[tt][8 * s + e];
-        if (32 * tt + ln < nt)
-          *reinterpret_cast<bf16x8*>(reinterpret_cast<unsigned char*>(op + (int64_t)(t0 + 32 * tt) * p.os + 16 * s) + oo) = w;
+        const int row = 32 * tt + ln;
+        *reinterpret_cast<bf16x8*>(s_v + row * 128 + ((half + 2 * s + hh) ^ swz(row, 8)) * 16) = w;
+      }
+      wave_lds_sync();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int row = 32 * tt + 16 * s + (lane >> 2);
+        const u32x4 w = *reinterpret_cast<const u32x4*>(s_v + row * 128 + ((half + (lane & 3)) ^ swz(row, 8)) * 16);
+        if (row < nt) *reinterpret_cast<u32x4*>(reinterpret_cast<unsigned char*>(op + (int64_t)(t0 + 32 * tt + 16 * s) * p.os) + oo) = w;
       }
     };
     fv[0] = frag_v(0);
     load_w(0);
     load_k(0);
-    if (OUT) load_f(0);
+    if (OUT) {
+      load_f(0);
+      load_t(0);
+    }
 #pragma unroll
     for (int db = 0; db < DB; ++db) S[db] *= decay;
     prep_w(0);
@@ -453,6 +474,10 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
         load_w(s + 1);
       }
       if (OUT) {
+        if (!near_one) {
+#pragma unroll
+          for (int ib = s >> 1; ib < 2; ++ib) far_factors(ib, s);
+        }
 #pragma unroll
         for (int ib = s >> 1; ib < 2; ++ib) prep_p(ib, s);
       } else if (s + 1 < 4) {
@@ -466,6 +491,7 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       if constexpr (OUT) {
         if (s + 1 < 4) {
           load_f(s + 1);
+          load_t(s + 1);
           load_k(s + 1);
         }
 #pragma unroll

@@ -41,7 +41,7 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   p.chunked = p.all || nseq < most ? nseq : most;
   const int units = L->heads / L->qk_groups * (L->dv / sk::SCAN_COLS);
   p.parts = (units + sk::SCAN_WAVES - 1) / sk::SCAN_WAVES;
-  p.waves = (units + p.parts - 1) / p.parts;
+  p.waves = (units / 2 + p.parts - 1) / p.parts * 2;      // (two waves share their values' rows)
   const int64_t row = L->qk_groups * p.parts;    // workgroups of a segment
   int shift = kMinSegShift;
   while ((tokens >> shift) * row > 1024) ++shift;
