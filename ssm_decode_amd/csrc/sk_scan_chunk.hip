@@ -174,17 +174,36 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
     const int r = fl < nt - 1 ? fl : nt - 1;
     dr = to_f32(*reinterpret_cast<const bf16*>(reinterpret_cast<const unsigned char*>(dp + (int64_t)t0 * p.gs) + (uint32_t)(r * p.gs * 2)));
   };
-  auto copy_kq = [&](int t0, int nt, int buf, int at, int of) {
+  // (in a whole chunk a lane's offset from its unit's first row is the same for all
+  // units, but for a turned bit or two of the swizzle)
+  constexpr int RPU = 64 / PPR;                  // rows of a unit of K or Q
+  auto copy_kq = [&](int t0, int buf, int at, int of) {
     for (int c = wv + NW * at; c < PPR; c += NW * of) {
+      const uint32_t to = lds0 + buf * PC * DK * 2 + c * 1024, row = fl / PPR;
+      const uint32_t x = ((fl % PPR) ^ (PPR == 16 ? fl >> 4 : (fl >> 4) & 1)) * 16 ^ (PPR == 16 ? (c & 6) * 32 : (c & 3) * 32);
+      copy16(uniform(kp + (int64_t)(t0 + RPU * c) * p.ks), row * (uint32_t)(p.ks * 2) + x, uniform(to + L::K));
+      if (OUT) copy16(uniform(qp + (int64_t)(t0 + RPU * c) * p.qs), row * (uint32_t)(p.qs * 2) + x, uniform(to + L::Q));
+    }
+  };
+  auto copy_v = [&](int t0, int buf, int v) {
+    const int first = 32 * (wv & 1) + 8 * v;
+    copy16(uniform(vp + (int64_t)(t0 + first) * p.vs), (uint32_t)(fl >> 3) * (uint32_t)(p.vs * 2) + (((fl & 7) ^ ((fl >> 4) & 1)) * 16 ^ (v & 3) * 32),
+           uniform(lds0 + v_at + buf * L::V_BYTES + first * 128));
+  };
+  // .. and all of them, of a chunk that may be the last
+  auto copy_last = [&](int t0, int nt, int buf) {
+#pragma unroll 1
+    for (int c = wv; c < PPR; c += NW) {
       const int x = c * 64 + fl, row = x / PPR, pc = (x % PPR) ^ swz(row, PPR), r = row < nt - 1 ? row : nt - 1;
       const uint32_t to = lds0 + buf * PC * DK * 2 + c * 1024;
       copy16(uniform(kp + (int64_t)t0 * p.ks), (uint32_t)(r * p.ks * 2) + pc * 16, uniform(to + L::K));
       if (OUT) copy16(uniform(qp + (int64_t)t0 * p.qs), (uint32_t)(r * p.qs * 2) + pc * 16, uniform(to + L::Q));
     }
-  };
-  auto copy_v = [&](int t0, int nt, int buf, int v) {
-    const int first = 32 * (wv & 1) + 8 * v, row = first + (fl >> 3), pc = (fl & 7) ^ swz(row, 8), r = row < nt - 1 ? row : nt - 1;
-    copy16(uniform(vp + (int64_t)t0 * p.vs), (uint32_t)(r * p.vs * 2) + pc * 16, uniform(lds0 + v_at + buf * L::V_BYTES + first * 128));
+#pragma unroll 1
+    for (int v = 0; v < 4 && active; ++v) {
+      const int first = 32 * (wv & 1) + 8 * v, row = first + (fl >> 3), pc = (fl & 7) ^ swz(row, 8), r = row < nt - 1 ? row : nt - 1;
+      copy16(uniform(vp + (int64_t)t0 * p.vs), (uint32_t)(r * p.vs * 2) + pc * 16, uniform(lds0 + v_at + buf * L::V_BYTES + first * 128));
+    }
   };
 
   // -------------------------------------------------------------- state
@@ -207,12 +226,8 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
   auto four = [&](int db, int q) { return f32x4s{S[db][4 * q], S[db][4 * q + 1], S[db][4 * q + 2], S[db][4 * q + 3]}; };
   if (len > 0) {
     const int nt = len < PC ? len : PC;
-    copy_kq(0, nt, 0, 0, 1);
-    if (active) {
-      fetch_dt(0, nt);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) copy_v(0, nt, 0, v);
-    }
+    copy_last(0, nt, 0);
+    if (active) fetch_dt(0, nt);
   }
   each([&](int db, int r, int) { S[db][r] = 0.f; });
   if (active) {
@@ -296,12 +311,15 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       }
     }
     if (!active) {
-      if (left > 0) copy_kq(t0 + PC, next, buf ^ 1, 0, 1);
+      if (left > 0) copy_last(t0 + PC, next, buf ^ 1);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       if (OUT) __syncthreads();
       continue;
     }
-    if (left > 0) fetch_dt(t0 + PC, next);
+    if (left > 0) {
+      fetch_dt(t0 + PC, next);
+      if (left < PC) copy_last(t0 + PC, next, buf ^ 1);
+    }
     unsigned char* s_v = smem + v_at + buf * L::V_BYTES;
     auto frag_v = [&](int s) {                   // V^T (or V): tokens 16 s + 8 h ..
       const unsigned char* at = s_v + (va ^ (s & 1) * 64) + 16 * s * 128;
@@ -352,9 +370,9 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
 #pragma unroll
           for (int tt = 0; tt < 2; ++tt) O[tt] = mm16(ss[u][v], fr[u][tt], st == 0 && v == 2 ? zero : O[tt]);
         region<6, 1, 9>();
-        if (left > 0) {
-          copy_kq(t0 + PC, next, buf ^ 1, st, STEPS);
-          if (st >= STEPS - 4) copy_v(t0 + PC, next, buf ^ 1, st - (STEPS - 4));
+        if (left >= PC) {
+          copy_kq(t0 + PC, buf ^ 1, st, STEPS);
+          if (st >= STEPS - 4) copy_v(t0 + PC, buf ^ 1, st - (STEPS - 4));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -498,9 +516,9 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
         for (int v = 2; v >= 0; --v)
 #pragma unroll
           for (int ib = s >> 1; ib < 2; ++ib) O[ib] = mm16(fv[s & 1], fp[ib][v], O[ib]);
-      } else if (left > 0) {
-        copy_kq(t0 + PC, next, buf ^ 1, s, 4);
-        copy_v(t0 + PC, next, buf ^ 1, s);
+      } else if (left >= PC) {
+        copy_kq(t0 + PC, buf ^ 1, s, 4);
+        copy_v(t0 + PC, buf ^ 1, s);
       }
       if (s + 1 < 4) prep_w(s + 1);
       if (OUT) {

@@ -30,7 +30,7 @@ struct Plan {
   bool all;
   int seg_shift, waves, parts;
 };
-constexpr int kMinSegShift = 9;
+constexpr int kMinSegShift = 8, kCus = 256;
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   Plan p{};
   const int shrt = short_prompt(L);
@@ -43,9 +43,11 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   p.parts = (units + sk::SCAN_WAVES - 1) / sk::SCAN_WAVES;
   p.waves = (units / 2 + p.parts - 1) / p.parts * 2;      // (two waves share their values' rows)
   const int64_t row = L->qk_groups * p.parts;    // workgroups of a segment
+  // Few workgroups with many tokens: segments, as long as one of each fills the CUs
+  // about once.
   int shift = kMinSegShift;
-  while ((tokens >> shift) * row > 1024) ++shift;
-  if (tokens >> shift >= 2 && p.chunked * row < 1024) {
+  while ((tokens >> shift) * row > kCus) ++shift;
+  if (tokens >> shift >= 2 * p.chunked && p.chunked * row * 2 <= kCus) {
     p.seg_shift = shift;
     p.nsegs = sk::prompt_slots(tokens, p.chunked, shift);
     p.decay_at = p.nsegs * L->heads * (int64_t)L->dk * L->dv * 4;
