@@ -37,16 +37,27 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t k) {
   }
   return k;
 }
+// Largest of the wave's values (a NaN counts for nothing), in every lane.
 __device__ __forceinline__ float wave_maxf(float x) {
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) x = fmaxf(x, __shfl_xor(x, s));
-  return x;
+  x = fmaxf(x, dpp_f<0xB1>(x, x));
+  x = fmaxf(x, dpp_f<0x4E>(x, x));
+  x = fmaxf(x, dpp_f<0x141>(x, x));
+  x = fmaxf(x, dpp_f<0x140>(x, x));
+  x = fmaxf(x, dpp_f<0x142, 0xA>(x, x));
+  x = fmaxf(x, dpp_f<0x143, 0xC>(x, x));
+  return lane_value(x, 63);
 }
+
+// The best of a wave's values: those of at least the bound that as many lanes reach
+// as there are beams (so the best are among them) are listed, and a listed value's
+// place is how many are better.  Only where ties make the list too long are they
+// found one by one.
+constexpr int LIST = 64;
 
 template <typename T>
 __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
   constexpr int N = 16 / (int)sizeof(T), E = 64 / (int)sizeof(T), V = E / N;      // values of a vector, of a lane; vectors
-  __shared__ uint64_t s_key[4 * BEAM_MAX];
+  __shared__ uint64_t s_list[4][LIST], s_key[4 * BEAM_MAX];
   const int row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   if (p.ended && p.ended[row] != 0) return;
@@ -75,14 +86,22 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
       for (int e = 0; e < N; ++e) x[v * N + e] = at + e >= 0 && at + e < p.vocab ? ld(X + at + e) : -__builtin_inff();
     }
   }
-  float top = -__builtin_inff();
+  constexpr float NONE = -__builtin_inff();
+  float mine = NONE;
 #pragma unroll
-  for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);
-  top = wave_maxf(top);
-  // (an infinity or a NaN among the values makes the sum a NaN)
+  for (int e = 0; e < E; ++e) mine = fmaxf(mine, x[e]);
+  const float top = wave_maxf(mine);
+  // Exponentials by the instruction, of differences to the maximum: off by 2^-24 of the
+  // exponent's magnitude, and where that is large the term is small.  (A NaN, or an
+  // infinity as the maximum, makes the sum a NaN; ruled out values add nothing.)
   float sum = 0.f;
+  if (top != NONE) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) sum += x[e] == -__builtin_inff() ? 0.f : expf(x[e] - top);
+    for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f((x[e] - top) * 1.44269504f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum += x[e] == NONE ? 0.f : x[e];      // (a NaN among ruled out values)
+  }
   sum = wave_sum(sum);
   BeamPart* out = p.part + (int64_t)row * p.parts + part;
   if (lane == 0) {
@@ -90,20 +109,58 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
     out->sum[wv] = sum;
   }
   auto index = [&](int e) { return first + ((e / N) * BEAM_THREADS + tid) * N + e % N; };
-  uint64_t last = ~0ull;
-  for (int r = 0; r < p.beams; ++r) {            // the best of what is worse than the last
-    uint64_t best = 0;
+  if (lane < p.beams) s_key[wv * BEAM_MAX + lane] = 0;
+  wave_lds_sync();
+  // the bound: lanes' maxima in falling order until as many lanes as beams have one
+  float bound = top, rest = mine;
+  for (int n = 0;;) {
+    const bool it = rest == bound && bound > NONE;
+    n += __popcll(__ballot(it));
+    if (n >= p.beams) break;
+    rest = it ? NONE : rest;
+    const float next = wave_maxf(rest);
+    if (!(next > NONE)) {                        // (fewer lanes have any: all that they have)
+      bound = bound > NONE ? -3.402823466e38f : NONE;
+      break;
+    }
+    bound = next;
+  }
+  int listed = 0;
+  const unsigned long long below = (1ull << lane) - 1;
+  if (bound > NONE) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const uint64_t k = x[e] > -__builtin_inff() ? beam_key(x[e], index(e)) : 0;
-      best = k < last && k > best ? k : best;
+      const bool it = x[e] >= bound;
+      const unsigned long long m = __ballot(it);
+      if (m) {
+        const int at = listed + __popcll(m & below);
+        if (it && at < LIST) s_list[wv][at] = beam_key(x[e], index(e));
+        listed += __popcll(m);
+      }
     }
-    last = wave_max(best);
-    if (lane == 0) s_key[wv * BEAM_MAX + r] = last;
-    if (last == 0) last = 1;                     // (none is left)
+  }
+  wave_lds_sync();
+  if (listed <= LIST) {
+    const uint64_t k = lane < listed ? s_list[wv][lane] : 0;
+    int place = 0;
+    for (int j = 0; j < listed; ++j) place += s_list[wv][j] > k;
+    if (lane < listed && place < p.beams) s_key[wv * BEAM_MAX + place] = k;
+  } else {
+    uint64_t last = ~0ull;
+    for (int r = 0; r < p.beams; ++r) {          // the best of what is worse than the last
+      uint64_t best = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint64_t k = x[e] > NONE ? beam_key(x[e], index(e)) : 0;
+        best = k < last && k > best ? k : best;
+      }
+      last = wave_max(best);
+      if (lane == 0) s_key[wv * BEAM_MAX + r] = last;
+      if (last == 0) break;                      // (none is left)
+    }
   }
   __syncthreads();
-  if (wv == 0) {                                 // the best of the waves': a lane's place is how many are better
+  if (wv == 0) {                                 // the best of the waves'
     const int n = 4 * p.beams;
     const uint64_t k = lane < n ? s_key[lane / p.beams * BEAM_MAX + lane % p.beams] : 0;
     int place = 0;
@@ -112,7 +169,7 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
       place += o > k || (o == k && j < lane);
     }
     if (lane < n && place < p.beams) {
-      out->value[place] = k ? key_value(k) : -__builtin_inff();
+      out->value[place] = k ? key_value(k) : NONE;
       out->index[place] = key_index(k);
     }
   }
