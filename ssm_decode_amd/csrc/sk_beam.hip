@@ -7,6 +7,8 @@
 // values in registers: their maximum, the sum of their exponentials and the best of
 // them, by value (a row's order is that of its values, so no rounding enters it);
 // a second joins a group's parts in 64 bits and takes the best of its candidates.
+#include <type_traits>
+
 #include "sk_beam.hpp"
 #include "sk_device.hpp"
 
@@ -175,24 +177,93 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
   }
 }
 
-// One workgroup per group.
-__global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(BeamParams p) {
-  __shared__ double s_lse[BEAM_MAX], s_best[4], s_score[BEAM_MAX];
-  __shared__ float s_in[BEAM_MAX];
-  __shared__ int s_ended[BEAM_MAX];
-  __shared__ int64_t s_at[4], s_pick[BEAM_MAX];
-  const int g = blockIdx.x, k = p.beams, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  constexpr double NONE = -__builtin_inf();
-  constexpr int64_t FAR = INT64_MAX;
-  if (tid < k) {
-    const int row = g * k + tid;
-    s_in[tid] = p.scores[row];
-    s_ended[tid] = p.ended ? p.ended[row] != 0 : 0;
+// The wave's largest value, in every lane.
+__device__ __forceinline__ double wave_maxd(double x) {
+  auto with = [](double v, auto ctrl, auto mask) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const int lo = (int)(uint32_t)u, hi = (int)(uint32_t)(u >> 32);
+    const uint32_t l = __builtin_amdgcn_update_dpp(lo, lo, decltype(ctrl)::value, decltype(mask)::value, 0xF, false);
+    const uint32_t h = __builtin_amdgcn_update_dpp(hi, hi, decltype(ctrl)::value, decltype(mask)::value, 0xF, false);
+    return fmax(v, __builtin_bit_cast(double, (uint64_t)h << 32 | l));
+  };
+  typedef std::integral_constant<int, 0xF> All;
+  x = with(x, std::integral_constant<int, 0xB1>{}, All{});
+  x = with(x, std::integral_constant<int, 0x4E>{}, All{});
+  x = with(x, std::integral_constant<int, 0x141>{}, All{});
+  x = with(x, std::integral_constant<int, 0x140>{}, All{});
+  x = with(x, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
+  x = with(x, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// The wave's best of what its lanes offer, lane by lane, `take` of them at most, in
+// falling order, ties to the lower place: got(n, score, at) for each, and next(&score,
+// &at) in the lane whose offer it was.
+constexpr double NO_SCORE = -__builtin_inf();
+template <typename Got, typename Next>
+__device__ __forceinline__ void wave_best(int take, double score, int at, Got got, Next next) {
+  const int lane = threadIdx.x & 63;
+  for (int n = 0; n < take; ++n) {
+    const double top = wave_maxd(score);
+    if (!(top > NO_SCORE)) return;
+    unsigned long long m = __ballot(score == top);
+    int who = __builtin_ctzll(m), best = __builtin_amdgcn_readlane(at, who);
+    while (m &= m - 1) {                         // (a tie)
+      const int other = __builtin_ctzll(m), a = __builtin_amdgcn_readlane(at, other);
+      if (a < best) {
+        best = a;
+        who = other;
+      }
+    }
+    if (lane == who) {
+      got(n, top, best);
+      next(&score, &at);
+    }
   }
-  __syncthreads();
+}
+
+// One workgroup per group.  (Places b * vocab + j are below 16 * 2^24.)
+__global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(BeamParams p) {
+  __shared__ double s_lse[BEAM_MAX], s_score[4 * BEAM_MAX], s_out[BEAM_MAX];
+  __shared__ float s_in[BEAM_MAX];
+  __shared__ int s_ended[BEAM_MAX], s_at[4 * BEAM_MAX], s_pick[BEAM_MAX];
+  const int g = blockIdx.x, k = p.beams, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  constexpr int FAR = INT32_MAX;
+  // The first candidates of a lane are read at once with the rows' sums: k of each part
+  // of a row (an ended row's only one is its first; k: none).
+  constexpr int HELD = 4;
+  const int per = p.parts * k, all = per * k;
+  auto candidate = [&](int c, int* b, float* v, int* a) {
+    *b = c / per;
+    const int j = c - *b * per, row = g * k + *b;
+    const bool ended = p.ended && p.ended[row] != 0;
+    const BeamPart* part = p.part + (int64_t)row * p.parts + j / k;
+    *v = part->value[j % k];
+    *a = *b * p.vocab + part->index[j % k];
+    if (ended) {
+      *v = 0.f;
+      *a = *b * p.vocab + (p.end_token > 0 ? p.end_token : 0);
+      if (j > 0) *b = k;
+    }
+  };
+  float hv[HELD];
+  int hb[HELD], ha[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    hb[i] = k;
+    const int c = tid + i * BEAM_THREADS;
+    if (c < all) candidate(c, &hb[i], &hv[i], &ha[i]);
+  }
+  if (tid < 4 * BEAM_MAX) s_score[tid] = NO_SCORE;
+  if (tid < BEAM_MAX) s_pick[tid] = FAR;
   for (int b = wv; b < k; b += 4) {              // the rows' sums: a wave a row
-    const BeamPart* part = p.part + (int64_t)(g * k + b) * p.parts;
-    const int n = s_ended[b] ? 0 : 4 * p.parts;
+    const int row = g * k + b;
+    const float in = p.scores[row];
+    const bool ended = p.ended && p.ended[row] != 0;
+    const BeamPart* part = p.part + (int64_t)row * p.parts;
+    const int n = ended ? 0 : 4 * p.parts;
     float top = -__builtin_inff();
     for (int j = lane; j < n; j += 64) top = fmaxf(top, part[j >> 2].top[j & 3]);
     top = wave_maxf(top);
@@ -206,88 +277,73 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(BeamParams p) {
     if (lane == 0) {
       // a row without a finite sum, and a score that is none, take the beam out; all
       // ruled out is no error
-      const float in = s_in[b];
       const bool wrong = !(fabs(sum) < __builtin_inf()) || in != in || in == __builtin_inff();
       if (wrong) atomicOr(p.err, ERRBIT_LOGIT);
-      if (wrong || in == -__builtin_inff()) s_in[b] = -__builtin_inff();
+      s_in[b] = wrong ? -__builtin_inff() : in;
+      s_ended[b] = ended;
       s_lse[b] = (double)top + log(sum);
     }
   }
   __syncthreads();
-  // candidate c of beam b: its score and b * vocab + j
-  const int per = p.parts * k, all = per * k;
-  auto candidate = [&](int c, double* score, int64_t* at) {
-    const int b = c / per, j = c - b * per;
-    *score = NONE;
-    *at = FAR;
+  // candidates, k of each part of a row; a lane offers the best of its own behind the
+  // last that was taken from it
+  auto rate = [&](int b, float v) -> double {
     const float in = s_in[b];
-    if (in == -__builtin_inff()) return;
-    if (s_ended[b]) {
-      if (j == 0) {
-        *score = in;
-        *at = (int64_t)b * p.vocab + (p.end_token > 0 ? p.end_token : 0);
-      }
-      return;
-    }
-    const BeamPart* part = p.part + (int64_t)(g * k + b) * p.parts + j / k;
-    const float v = part->value[j % k];
-    if (v == -__builtin_inff()) return;
-    *score = (double)in + ((double)v - s_lse[b]);
-    *at = (int64_t)b * p.vocab + part->index[j % k];
+    if (s_ended[b]) return in;
+    return in > -__builtin_inff() && v > -__builtin_inff() ? (double)in + ((double)v - s_lse[b]) : NO_SCORE;
   };
-  auto better = [](double s, int64_t a, double t, int64_t b) { return s > t || (s == t && a < b); };
-  double last = __builtin_inf();
-  int64_t last_at = -1;
-  for (int r = 0; r < k; ++r) {                  // the best behind the last
-    double best = NONE;
-    int64_t best_at = FAR;
-    for (int c = tid; c < all; c += BEAM_THREADS) {
-      double s;
-      int64_t a;
-      candidate(c, &s, &a);
-      if (better(last, last_at, s, a) && better(s, a, best, best_at)) {
+  auto offer = [&](double* score, int* at) {
+    const double last = *score;
+    const int last_at = *at;
+    double best = NO_SCORE;
+    int best_at = FAR;
+    auto consider = [&](int b, float v, int a) {
+      const double s = rate(b, v);
+      const bool behind = s < last || (s == last && a > last_at);
+      if (behind && (s > best || (s == best && a < best_at))) {
         best = s;
         best_at = a;
       }
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (hb[i] < k) consider(hb[i], hv[i], ha[i]);
+    for (int c = tid + HELD * BEAM_THREADS; c < all; c += BEAM_THREADS) {
+      float v;
+      int b, a;
+      candidate(c, &b, &v, &a);
+      if (b < k) consider(b, v, a);
     }
-    for (int s = 1; s < 64; s *= 2) {
-      const double t = __shfl_xor(best, s);
-      const int64_t a = __shfl_xor((long long)best_at, s);
-      if (better(t, a, best, best_at)) {
-        best = t;
-        best_at = a;
-      }
-    }
-    if (lane == 0) {
-      s_best[wv] = best;
-      s_at[wv] = best_at;
-    }
-    __syncthreads();
-    best = s_best[0];
-    best_at = s_at[0];
-    for (int w = 1; w < 4; ++w)
-      if (better(s_best[w], s_at[w], best, best_at)) {
-        best = s_best[w];
-        best_at = s_at[w];
-      }
-    if (tid == 0) {
-      s_score[r] = best;
-      s_pick[r] = best_at;
-    }
-    last = best;
-    last_at = best_at;
-    __syncthreads();
-  }
-  if (tid < k) {
-    const int row = g * k + tid;
-    const int64_t at = s_pick[tid];
-    const bool none = at == FAR;
-    const int b = none ? tid : (int)(at / p.vocab);
+    *score = best;
+    *at = best_at;
+  };
+  double score = __builtin_inf();
+  int at = -1;
+  offer(&score, &at);
+  wave_best(k, score, at,
+            [&](int n, double s, int a) {
+              s_score[wv * BEAM_MAX + n] = s;
+              s_at[wv * BEAM_MAX + n] = a;
+            },
+            offer);
+  __syncthreads();
+  if (wv > 0) return;
+  wave_best(k, s_score[lane], s_at[lane],
+            [&](int n, double s, int a) {
+              s_out[n] = s;
+              s_pick[n] = a;
+            },
+            [](double* s, int*) { *s = NO_SCORE; });
+  wave_lds_sync();
+  if (lane < k) {
+    const int row = g * k + lane, pick = s_pick[lane];
+    const bool none = pick == FAR;
+    const int b = none ? lane : pick / p.vocab;
     const bool over = !none && s_ended[b];
-    const int token = none ? -1 : over ? p.end_token : (int)(at % p.vocab);
+    const int token = none ? -1 : over ? p.end_token : pick % p.vocab;
     p.parents[row] = g * k + b;
     p.tokens[row] = token;
-    p.new_scores[row] = none ? -__builtin_inff() : (float)s_score[tid];
+    p.new_scores[row] = none ? -__builtin_inff() : (float)s_out[lane];
     p.new_ended[row] = over || (!none && token == p.end_token);
   }
 }

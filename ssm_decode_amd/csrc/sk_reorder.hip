@@ -14,40 +14,65 @@ namespace {
 
 constexpr int MOVE_THREADS = 256;
 
-template <typename P, int K>
-__device__ __forceinline__ void move(char* data, int64_t bytes, int64_t at, int first, int beams, const int (&from)[K]) {
-  if (at >= bytes) return;
-  P x[K];
+// N pieces (a number known here: under a condition for each, the compiler keeps every
+// combination in registers of its own).
+template <typename P, int K, int N>
+__device__ __forceinline__ void move_n(char* data, int64_t bytes, const int (&from)[K], const int (&to)[K]) {
+  P x[N];
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-    if (k < beams && from[k] != k) x[k] = *reinterpret_cast<const P*>(data + (int64_t)(first + from[k]) * bytes + at);
+  for (int k = 0; k < N; ++k) x[k] = __builtin_nontemporal_load(reinterpret_cast<const P*>(data + from[k] * bytes));
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-    if (k < beams && from[k] != k) *reinterpret_cast<P*>(data + (int64_t)(first + k) * bytes + at) = x[k];
+  for (int k = 0; k < N; ++k) __builtin_nontemporal_store(x[k], reinterpret_cast<P*>(data + to[k] * bytes));
+}
+template <typename P, int K, int N = K>
+__device__ __forceinline__ void move(char* data, int64_t bytes, int n, const int (&from)[K], const int (&to)[K]) {
+  if constexpr (N > 0) {
+    if (n == N) move_n<P, K, N>(data, bytes, from, to);
+    else move<P, K, N - 1>(data, bytes, n, from, to);
+  }
 }
 
-// One workgroup per (block of a row, group).
+// One workgroup per (block of a row, group).  What a workgroup needs first, the
+// parents and its buffer, is read at once: a request's states alone are a chain of
+// reads, and no more.
 template <int K>
 __global__ void __launch_bounds__(MOVE_THREADS) reorder_kernel(ReorderParams p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   const int g = blockIdx.x / p.blocks, block = blockIdx.x - g * p.blocks, first = g * p.beams;
   int from[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) from[k] = uload(p.parents, first + (k < p.beams ? k : p.beams - 1)) - first;
+  int r = -1;                                    // (compared with all at once: no chain of loads)
+#pragma unroll
+  for (int j = 0; j < MOVE_MAX; ++j) r += j < p.nrows && block >= p.rows[j].first;
+  const ReorderParams::Rows rows = p.rows[r];
+  // the beams that move, one behind the other
+  int src[K], dst[K], n = 0;
   bool wrong = false;
 #pragma unroll
+  for (int k = 0; k < K; ++k) src[k] = dst[k] = 0;
+#pragma unroll
   for (int k = 0; k < K; ++k) {
-    from[k] = k < p.beams ? p.parents[first + k] - first : k;
-    wrong |= from[k] < 0 || from[k] >= (k < p.beams ? p.beams : K);
+    wrong |= (uint32_t)from[k] >= (uint32_t)p.beams;
+    const bool moves = k < p.beams && from[k] != k;
+#pragma unroll
+    for (int j = 0; j <= k; ++j) {
+      const bool here = moves && j == n;
+      src[j] = here ? from[k] : src[j];
+      dst[j] = here ? k : dst[j];
+    }
+    n += moves;
   }
   if (wrong) {
     if (threadIdx.x == 0 && block == 0) atomicOr(p.err, 4);
     return;
   }
-  int r = 0;
-  while (r + 1 < p.nrows && block >= p.rows[r + 1].first) ++r;
-  const ReorderParams::Rows rows = p.rows[r];
   const int64_t at = ((int64_t)(block - rows.first) * MOVE_THREADS + threadIdx.x) * rows.unit;
-  if (rows.unit == 16) move<uint4, K>(rows.data, rows.bytes, at, first, p.beams, from);
-  else if (rows.unit == 4) move<uint32_t, K>(rows.data, rows.bytes, at, first, p.beams, from);
-  else move<uint16_t, K>(rows.data, rows.bytes, at, first, p.beams, from);
+  if (at >= rows.bytes) return;
+  char* data = rows.data + (int64_t)first * rows.bytes + at;
+  if (rows.unit == 16) move<u32x4, K>(data, rows.bytes, n, src, dst);
+  else if (rows.unit == 4) move<uint32_t, K>(data, rows.bytes, n, src, dst);
+  else move<uint16_t, K>(data, rows.bytes, n, src, dst);
 }
 
 }  // namespace
@@ -61,7 +86,8 @@ int launch_reorder(const ReorderParams& q, hipStream_t st) {
   }
   p.blocks = blocks;
   const dim3 grid((unsigned)blocks * p.groups), block(MOVE_THREADS);
-  if (p.beams <= 4) hipLaunchKernelGGL((reorder_kernel<4>), grid, block, 0, st, p);
+  if (p.beams <= 2) hipLaunchKernelGGL((reorder_kernel<2>), grid, block, 0, st, p);
+  else if (p.beams <= 4) hipLaunchKernelGGL((reorder_kernel<4>), grid, block, 0, st, p);
   else if (p.beams <= 8) hipLaunchKernelGGL((reorder_kernel<8>), grid, block, 0, st, p);
   else hipLaunchKernelGGL((reorder_kernel<16>), grid, block, 0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -5;

@@ -2,6 +2,7 @@
 // and the sequences' reordering.  Every check runs before any HIP call, so an
 // invalid call launches nothing and writes nothing.
 #include <math.h>
+#include <stdlib.h>
 #include <stdint.h>
 
 #include <hip/hip_runtime.h>
@@ -200,7 +201,7 @@ int sketchssm_conv(const sketchssm_convolution* cv, void* hip_stream) {
     p.has_state = cv->has_state;
     p.err = cv->err;
     p.eps = cv->eps;
-    p.shift = 5;
+    p.shift = getenv("SK_CS") ? atoi(getenv("SK_CS")) : 5;
     return sk::launch_conv(cv->dtype, cv->taps, p, reinterpret_cast<hipStream_t>(hip_stream));
   } catch (...) {
     return SKSSM_ELAUNCH;
