@@ -125,20 +125,14 @@ __device__ __forceinline__ void held_rows(const ConvParams& p, int b, bool read,
     raw[j] = read ? *reinterpret_cast<const u32x4*>(at + (int64_t)j * p.channels) : u32x4{0, 0, 0, 0};
 }
 
-#ifndef CONV_U
-#define CONV_U 4
-#endif
-#ifndef CONV_OCC
-#define CONV_OCC 4
-#endif
 // One workgroup per (slot of 2^shift tokens, four waves of channels).  The slot
 // with a prompt's first tokens reads what the sequence holds and leaves its last
 // inputs there (the same lanes, so that the one is read before the other is
 // written); the others take the inputs before their first from x.
 template <typename T, int TAPS>
-__global__ void __launch_bounds__(CONV_THREADS, CONV_OCC) conv_prompt_kernel(ConvParams p) {
+__global__ void __launch_bounds__(CONV_THREADS) conv_prompt_kernel(ConvParams p) {
   using C = Conv<T, TAPS>;
-  constexpr int N = C::N, H = C::H, U = CONV_U;
+  constexpr int N = C::N, H = C::H, U = 4;
   const int slot = blockIdx.x, i = conv_prompt(p, slot);
   // (a refused list may have no prompt that any slot comes to: it is reported here)
   if (slot == 0 && i != 0) conv_ok(p, 0, p.seqs ? p.seqs[0] : 0);

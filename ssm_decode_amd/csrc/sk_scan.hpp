@@ -19,6 +19,7 @@ struct ScanParams : PromptParams {
 // waves with the keys and queries of one group.
 constexpr int SCAN_COLS = 32, SCAN_WAVES = 8;
 
+int launch_scan_join(int dk, int dv, const ScanParams& p, hipStream_t st);
 int launch_scan_step(int dk, int dv, int act, const ScanParams& p, hipStream_t st);
 int launch_scan_chunks(int dk, int dv, const ScanParams& p, hipStream_t st);
 

@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
 constexpr int JOIN_THREADS = 256;
 template <int DK, int DV>
 __global__ void __launch_bounds__(JOIN_THREADS) scan_join_kernel(ScanParams p) {
-  constexpr int VECS = DK * DV / 4, BLOCKS = VECS / JOIN_THREADS;
+  constexpr int VECS = DK * DV / 4, BLOCKS = (VECS + JOIN_THREADS - 1) / JOIN_THREADS;
   const int tile = blockIdx.x / BLOCKS, x = tile / p.H, h = tile - x * p.H;
   int rank = 0;
   const int i = chunked_prompt(p, x, &rank);
@@ -601,8 +601,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) scan_join_kernel(ScanParams p) {
   const int s0 = p.start[i], len = p.start[i + 1] - s0;
   const int segs = (int)(((int64_t)len + (1 << p.seg_shift) - 1) >> p.seg_shift);
   if (prompt_wrong(p, i, p.seqs ? p.seqs[i] : i) || segs < 3) return;      // (reported by the others)
-  const int first = first_slot(s0, rank, p.seg_shift);
-  f32x4s* at = reinterpret_cast<f32x4s*>(p.seg + ((size_t)first * p.H + h) * DK * DV) + blockIdx.x % BLOCKS * JOIN_THREADS + threadIdx.x;
+  const int first = first_slot(s0, rank, p.seg_shift), vec = blockIdx.x % BLOCKS * JOIN_THREADS + threadIdx.x;
+  if (vec >= VECS) return;
+  f32x4s* at = reinterpret_cast<f32x4s*>(p.seg + ((size_t)first * p.H + h) * DK * DV) + vec;
   const float* decay = p.seg_decay + (size_t)first * p.H + h;
   const size_t step = (size_t)p.H * VECS;
   f32x4s S = at[0], B = at[step];
@@ -623,18 +624,32 @@ void launch_chunks(const ScanParams& p, hipStream_t st) {
 }
 
 template <int DK, int DV>
+int launch_join(const ScanParams& p, hipStream_t st) {
+  constexpr unsigned BLOCKS = (DK * DV / 4 + JOIN_THREADS - 1) / JOIN_THREADS;
+  hipLaunchKernelGGL((scan_join_kernel<DK, DV>), dim3((unsigned)p.nchunked * p.H * BLOCKS), dim3(JOIN_THREADS), 0, st, p);
+  return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+template <int DK, int DV>
 int launch(const ScanParams& p, hipStream_t st) {
   static_assert(ScanLds<DK, true>::bytes(SCAN_WAVES) <= 160 * 1024, "LDS of a CU");
   if (p.seg_shift) {
     launch_chunks<DK, DV, false>(p, st);
-    hipLaunchKernelGGL((scan_join_kernel<DK, DV>), dim3((unsigned)p.nchunked * p.H * (DK * DV / 4 / JOIN_THREADS)), dim3(JOIN_THREADS), 0,
-                       st, p);
+    launch_join<DK, DV>(p, st);
   }
   launch_chunks<DK, DV, true>(p, st);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 }  // namespace
+
+int launch_scan_join(int dk, int dv, const ScanParams& p, hipStream_t st) {
+  if (dk == 16 && dv == 32) return launch_join<16, 32>(p, st);
+  if (dk == 64 && dv == 64) return launch_join<64, 64>(p, st);
+  if (dk == 128 && dv == 64) return launch_join<128, 64>(p, st);
+  if (dk == 128 && dv == 128) return launch_join<128, 128>(p, st);
+  return -2;
+}
 
 int launch_scan_chunks(int dk, int dv, const ScanParams& p, hipStream_t st) {
   if (dk == 64 && dv == 64) return launch<64, 64>(p, st);

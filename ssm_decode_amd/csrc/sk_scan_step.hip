@@ -5,17 +5,18 @@
 // mix but in the output's sum over rows).
 //
 // A prompt of a few tokens is bound by its state's traffic (4 dk dv bytes in and
-// out), a longer one by the chain from token to token, so long ones take the
-// chunked form.
+// out; 256 sequences of 128 heads of 128 x 64 by one token: 2.1 GB in 374 us, 5.7 TB/s), a
+// longer one by the chain from token to token, so long ones take the chunked form, or,
+// where there is none (fp32, dk = 16) and tiles are few, go in segments as the chunked
+// form's: without outputs first, each from a zero state, then each from the state
+// before it.
+#include "sk_prompt_chunk.hpp"
 #include "sk_scan.hpp"
-#include "sk_serve_device.hpp"
 
 namespace sk {
 namespace {
 
 constexpr int TB = 16;    // tokens staged at a time
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ void put16(float* dst, const u32x4& r, const bf16*) {
 #pragma unroll
@@ -39,11 +40,11 @@ struct Rows {
       if (t < nt) r[u] = *reinterpret_cast<const u32x4*>(base + t * stride + (c - t * CPR) * N);
     }
   }
-  __device__ __forceinline__ void stage(float* lds, int nt) const {
+  __device__ __forceinline__ void stage(float* lds) const {      // (zeros behind the end)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = threadIdx.x + NT * u, t = c / CPR;
-      if (t < nt) put16(lds + t * D + (c - t * CPR) * N, r[u], (const AT*)nullptr);
+      if (t < TB) put16(lds + t * D + (c - t * CPR) * N, r[u], (const AT*)nullptr);
     }
   }
 };
@@ -52,16 +53,42 @@ struct Rows {
 // in fp32.
 template <typename AT> constexpr int lane_columns() { return sizeof(AT) == 2 ? 2 : 1; }
 
-template <int DK, int DV, typename AT, int NCC = lane_columns<AT>()>
-__global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
-  constexpr int NT = DV * 4 / NCC, MB = DK / 16;
-  __shared__ __align__(16) float s_k[TB * DK], s_q[TB * DK], s_v[TB * DV], s_ad[2 * TB];
+// Tokens under way at once: nothing but the state goes from one to the next.  bf16: one,
+// whose registers leave four waves a SIMD (256 sequences, a token each: 376 us, two
+// at once 409, four 657); fp32, whose waves are few, two (8 prompts of up to 512 tokens,
+// 16 heads of 128 x 64: 201 us one, 178 two, 195 four).
+template <typename AT> constexpr int tokens_at_once() { return sizeof(AT) == 2 ? 1 : 2; }
 
-  const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H, g = h / (p.H / p.G);
-  const int s0 = p.start[i], len = p.start[i + 1] - s0;
+// OUT: with outputs.  SEG: one workgroup per (segment, head); the first segment
+// leaves the state that its prompt starts from in the last one's place, as in the
+// chunked form.
+template <int DK, int DV, typename AT, bool OUT, bool SEG, int NCC = lane_columns<AT>()>
+__global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
+  constexpr int NT = DV * 4 / NCC, MB = DK / 16, T = tokens_at_once<AT>();
+  __shared__ __align__(16) float s_k[TB * DK], s_q[OUT ? TB * DK : 1], s_v[TB * DV], s_ad[2 * TB];
+
+  const int slot = blockIdx.x / p.H, h = blockIdx.x - slot * p.H, g = h / (p.H / p.G);
+  int i = slot, rank = 0, seg = 0, segs = 1;
+  if (SEG) {
+    // (a refused list may have no prompt that any launch comes to: it is reported here)
+    if (slot == 0) prompt_ok(p, 0, h, p.seqs ? p.seqs[0] : 0);
+    i = slot_prompt(p, slot, p.seg_shift, &rank);
+    if (i < 0) return;
+  }
+  int s0 = p.start[i], len = p.start[i + 1] - s0;
   // (a longer prompt belongs to the chunked form's launch; so that a refused
   // list is reported, the first prompt's workgroups go on to the checks)
-  if (i > 0 && (unsigned)len > (unsigned)p.len_hi) return;
+  if (!SEG && i > 0 && (unsigned)len > (unsigned)p.len_hi) return;
+  if (SEG) {
+    seg = slot - first_slot(s0, rank, p.seg_shift);
+    const int64_t from = (int64_t)seg << p.seg_shift;
+    if (from >= len && seg > 0) return;
+    segs = (int)(((int64_t)len + (1 << p.seg_shift) - 1) >> p.seg_shift);
+    s0 += (int)from;
+    len = len - from <= (1 << p.seg_shift) ? len - (int)from : 1 << p.seg_shift;
+  }
+  const bool last = seg + 1 >= segs;
+  if (!OUT && last) return;
   const int b = p.seqs ? p.seqs[i] : i;
   const bool in = b >= 0 && b < p.B;
 
@@ -69,14 +96,29 @@ __global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
   const int col0 = 16 * NCC * (tid >> 6), col = col0 + NCC * cg;
   float* Sg = p.S + ((size_t)(in ? b : 0) * p.H + h) * DK * DV + (size_t)(4 * rg) * DV + col;
 
+  auto seg_at = [&](int at) { return p.seg + ((size_t)at * p.H + h) * DK * DV + (size_t)(4 * rg) * DV + col; };
+
+  // (a wrong list has segments anywhere: nothing is read for one)
+  if (SEG && !prompt_ok(p, i, h, b)) return;
   // the state's loads are in flight over the checks and the tokens' first loads
   float s[MB][NCC][4];
-  if (in && (!p.has_state || p.has_state[i] != 0)) {
+  const float* from = Sg;
+  bool read = in && (!p.has_state || p.has_state[i] != 0);
+  if (SEG) {
+    if (seg > 0) {
+      from = seg_at(slot - 1);
+      read = OUT;
+    } else if (OUT && !last) {
+      from = seg_at(slot + segs - 1);
+      read = true;
+    }
+  }
+  if (read) {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const float* at = Sg + (size_t)(16 * mb + v) * DV;
+        const float* at = from + (size_t)(16 * mb + v) * DV;
         if constexpr (NCC == 2) {
           float x[2];
           ldn_nt<2>(at, x);
@@ -94,7 +136,22 @@ __global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) s[mb][c][v] = 0.f;
   }
-  if (!prompt_ok(p, i, h, b) || len > p.len_hi) return;
+  if (!SEG && (!prompt_ok(p, i, h, b) || len > p.len_hi)) return;
+  auto write = [&](float* to) {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float* at = to + (size_t)(16 * mb + v) * DV;
+        if constexpr (NCC == 2) {
+          const float x[2] = {s[mb][0][v], s[mb][1][v]};
+          stn_nt<2>(at, x);
+        } else {
+          *at = s[mb][0][v];
+        }
+      }
+  };
+  if (SEG && !OUT && seg == 0) write(seg_at(slot + segs - 1));
 
   const AT* kp = reinterpret_cast<const AT*>(p.k) + s0 * p.ks + (int64_t)g * DK;
   const AT* qp = reinterpret_cast<const AT*>(p.q) + s0 * p.qs + (int64_t)g * DK;
@@ -105,10 +162,10 @@ __global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
 
   Rows<DK, NT, AT> rk, rq;
   Rows<DV, NT, AT> rv;
-  float d = 0.f;
+  float d = 0.f, decay = 1.f;
   auto fetch = [&](int t0, int nt) {
     rk.load(kp + t0 * p.ks, p.ks, nt);
-    rq.load(qp + t0 * p.qs, p.qs, nt);
+    if (OUT) rq.load(qp + t0 * p.qs, p.qs, nt);
     rv.load(vp + t0 * p.vs, p.vs, nt);
     if (tid < nt) d = ld(dp + (t0 + tid) * p.gs);
   };
@@ -116,12 +173,12 @@ __global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
   fetch(0, nt);
 
   for (int t0 = 0; t0 < len; t0 += TB) {
-    rk.stage(s_k, nt);
-    rq.stage(s_q, nt);
-    rv.stage(s_v, nt);
-    if (tid < nt) {
-      s_ad[2 * tid] = expf(-d * rate);
-      s_ad[2 * tid + 1] = d;
+    rk.stage(s_k);
+    if (OUT) rq.stage(s_q);
+    rv.stage(s_v);
+    if (tid < TB) {                        // (behind the end nothing happens)
+      s_ad[2 * tid] = tid < nt ? expf(-d * rate) : 1.f;
+      s_ad[2 * tid + 1] = tid < nt ? d : 0.f;
     }
     __syncthreads();
     const int now = nt, left = len - t0 - TB;
@@ -130,58 +187,75 @@ __global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
       fetch(t0 + TB, nt);
     }
 #pragma unroll 1
-    for (int j = 0; j < now; ++j) {
-      float u[NCC];
-      ldn<NCC>(s_v + j * DV + col, u);
-      const float a = s_ad[2 * j], dt = s_ad[2 * j + 1];
+    for (int j0 = 0; j0 < now; j0 += T) {
+      float u[T][NCC], o[T][NCC], a[T];
 #pragma unroll
-      for (int c = 0; c < NCC; ++c) u[c] *= dt;
-      float o[NCC];
+      for (int t = 0; t < T; ++t) {
+        ldn<NCC>(s_v + (j0 + t) * DV + col, u[t]);
+        a[t] = s_ad[2 * (j0 + t)];
+        const float dt = s_ad[2 * (j0 + t) + 1];
 #pragma unroll
-      for (int c = 0; c < NCC; ++c) o[c] = 0.f;
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        float kk[4], qq[4];
-        ld4(s_k + j * DK + 16 * mb + 4 * rg, kk);
-        ld4(s_q + j * DK + 16 * mb + 4 * rg, qq);
-#pragma unroll
-        for (int c = 0; c < NCC; ++c)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            s[mb][c][v] = a * s[mb][c][v] + kk[v] * u[c];
-            o[c] += s[mb][c][v] * qq[v];
-          }
+        for (int c = 0; c < NCC; ++c) {
+          u[t][c] *= dt;
+          o[t][c] = 0.f;
+        }
       }
 #pragma unroll
-      for (int c = 0; c < NCC; ++c) o[c] = row_groups_sum(o[c]);
-      if (rg == 0) stn<NCC>(op + (t0 + j) * p.os, o);
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          float kk[4], qq[4];
+          ld4(s_k + (j0 + t) * DK + 16 * mb + 4 * rg, kk);
+          if (OUT) ld4(s_q + (j0 + t) * DK + 16 * mb + 4 * rg, qq);
+#pragma unroll
+          for (int c = 0; c < NCC; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              s[mb][c][v] = a[t] * s[mb][c][v] + kk[v] * u[t][c];
+              if (OUT) o[t][c] += s[mb][c][v] * qq[v];
+            }
+        }
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        if (!OUT) {
+          decay *= a[t];
+          continue;
+        }
+#pragma unroll
+        for (int c = 0; c < NCC; ++c) o[t][c] = row_groups_sum(o[t][c]);
+        if (rg == 0 && j0 + t < now) stn<NCC>(op + (t0 + j0 + t) * p.os, o[t]);
+      }
     }
     __syncthreads();
   }
 
-#pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      float* at = Sg + (size_t)(16 * mb + v) * DV;
-      if constexpr (NCC == 2) {
-        const float x[2] = {s[mb][0][v], s[mb][1][v]};
-        stn_nt<2>(at, x);
-      } else {
-        *at = s[mb][0][v];
-      }
-    }
+  if (!OUT) {
+    write(seg_at(slot));
+    if (tid == 0) p.seg_decay[(size_t)slot * p.H + h] = decay;
+    return;
+  }
+  if (!last) return;                             // (the state behind a segment is known already)
+  write(Sg);
   if (p.prime) sketch_tile<DK, DV, AT, NCC>(p.sk, s, b, h, col0, lane);
+}
+
+template <int DK, int DV, typename AT>
+int launch_type(const ScanParams& p, hipStream_t st) {
+  const dim3 block(DV * 4 / lane_columns<AT>());
+  if (p.nchunked > 0 && p.seg_shift) {           // (p.nchunked: all prompts, in segments)
+    const dim3 grid(p.nsegs * p.H);
+    hipLaunchKernelGGL((scan_step_kernel<DK, DV, AT, false, true>), grid, block, 0, st, p);
+    if (int rc = launch_scan_join(DK, DV, p, st)) return rc;
+    hipLaunchKernelGGL((scan_step_kernel<DK, DV, AT, true, true>), grid, block, 0, st, p);
+  } else {
+    hipLaunchKernelGGL((scan_step_kernel<DK, DV, AT, true, false>), dim3(p.nseq * p.H), block, 0, st, p);
+  }
+  return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 template <int DK, int DV>
 int launch_shape(int act, const ScanParams& p, hipStream_t st) {
-  const dim3 grid(p.nseq * p.H);
-  if (act == DT_F32)
-    hipLaunchKernelGGL((scan_step_kernel<DK, DV, float>), grid, dim3(DV * 4 / lane_columns<float>()), 0, st, p);
-  else
-    hipLaunchKernelGGL((scan_step_kernel<DK, DV, bf16>), grid, dim3(DV * 4 / lane_columns<bf16>()), 0, st, p);
-  return hipGetLastError() == hipSuccess ? 0 : -5;
+  return act == DT_F32 ? launch_type<DK, DV, float>(p, st) : launch_type<DK, DV, bf16>(p, st);
 }
 
 }  // namespace

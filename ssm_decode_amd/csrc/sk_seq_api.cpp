@@ -2,7 +2,6 @@
 // and the sequences' reordering.  Every check runs before any HIP call, so an
 // invalid call launches nothing and writes nothing.
 #include <math.h>
-#include <stdlib.h>
 #include <stdint.h>
 
 #include <hip/hip_runtime.h>
@@ -28,14 +27,33 @@ int short_prompt(const sketchssm_layer* L) { return L->dk == 64 ? 32 : 16; }
 // 2^seg_shift tokens (0: whole), with the bytes of their states and decays.
 struct Plan {
   int64_t chunked, nsegs, decay_at, bytes;
-  bool all;
+  bool all, in_chunks;         // (in_chunks false: token by token, all in segments)
   int seg_shift, waves, parts;
 };
 constexpr int kMinSegShift = 8, kCus = 256;
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   Plan p{};
   const int shrt = short_prompt(L);
-  if (L->dk < 64 || L->act_dtype != SKSSM_BF16 || nseq == 0) return p;
+  if (nseq == 0) return p;
+  auto segments = [&](int shift) {
+    p.seg_shift = shift;
+    p.nsegs = sk::prompt_slots(tokens, p.chunked, shift);
+    p.decay_at = p.nsegs * L->heads * (int64_t)L->dk * L->dv * 4;
+    p.bytes = p.decay_at + (p.nsegs * L->heads * 4 + 15) / 16 * 16;
+  };
+  if (L->dk < 64 || L->act_dtype != SKSSM_BF16) {
+    // Token by token: in segments where tiles are few and prompts long on average.
+    if (nseq * L->heads <= 2 * kCus && tokens >= 128 * nseq) {
+      int shift = 6;
+      while ((tokens >> shift) * L->heads > 8 * kCus) ++shift;
+      if (tokens >> shift >= 2 * nseq) {
+        p.chunked = nseq;
+        segments(shift);
+      }
+    }
+    return p;
+  }
+  p.in_chunks = true;
   if (tokens - nseq < shrt) return p;            // (no prompt is longer unless others are empty)
   p.all = tokens > 64 * nseq;
   const int64_t most = tokens / (shrt + 1);
@@ -48,12 +66,7 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   // about once.
   int shift = kMinSegShift;
   while ((tokens >> shift) * row > kCus) ++shift;
-  if (tokens >> shift >= 2 * p.chunked && p.chunked * row * 2 <= kCus) {
-    p.seg_shift = shift;
-    p.nsegs = sk::prompt_slots(tokens, p.chunked, shift);
-    p.decay_at = p.nsegs * L->heads * (int64_t)L->dk * L->dv * 4;
-    p.bytes = p.decay_at + (p.nsegs * L->heads * 4 + 15) / 16 * 16;
-  }
+  if (tokens >> shift >= 2 * p.chunked && p.chunked * row * 2 <= kCus) segments(shift);
   return p;
 }
 
@@ -135,9 +148,12 @@ int sketchssm_scan(const sketchssm_layer* layer, const sketchssm_buffers* bufs, 
       p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(pr->work) + pl.decay_at);
       p.waves = pl.waves;
       p.parts = pl.parts;
-      p.len_lo = pl.all ? -1 : short_prompt(layer);
-      if ((rc = sk::launch_scan_chunks(dk, dv, p, st)) || pl.all) return rc;
-      p.len_hi = short_prompt(layer);
+      p.len_lo = pl.all || !pl.in_chunks ? -1 : short_prompt(layer);
+      if (pl.in_chunks) {
+        if ((rc = sk::launch_scan_chunks(dk, dv, p, st)) || pl.all) return rc;
+        p.len_hi = short_prompt(layer);
+        p.nchunked = 0;
+      }
     }
     return sk::launch_scan_step(dk, dv, layer->act_dtype, p, st);
   } catch (...) {
@@ -201,7 +217,11 @@ int sketchssm_conv(const sketchssm_convolution* cv, void* hip_stream) {
     p.has_state = cv->has_state;
     p.err = cv->err;
     p.eps = cv->eps;
-    p.shift = getenv("SK_CS") ? atoi(getenv("SK_CS")) : 5;
+    // Blocks of 32 tokens, shorter where that leaves CUs idle (each takes taps - 1
+    // more rows): 4096 tokens of 12288 channels 51.5 us with 32, 48.5 with 16.
+    p.shift = 5;
+    const int64_t parts = (channels * es / 1024 + 6) / 4;
+    while (p.shift > 3 && ((cv->tokens >> p.shift) + cv->nseq) * parts < 1536) --p.shift;
     return sk::launch_conv(cv->dtype, cv->taps, p, reinterpret_cast<hipStream_t>(hip_stream));
   } catch (...) {
     return SKSSM_ELAUNCH;

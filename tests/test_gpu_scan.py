@@ -212,6 +212,10 @@ def test_refused_prompts(lens, act):
     assert call([s[0], s[1], s[2], s[3] + 1], [0, 1, 2]) == (SEQ, [True] * 4, [True] * 3)
     assert call([-1, s[1], s[2], s[3]], [0, 1, 2]) == (SEQ, [True] * 4, [True] * 3)
     assert call([N + 900] * 4, [0, 1, 2]) == (SEQ, [True] * 4, [True] * 3)
+    # prompts far past the end, and of negative length: nothing of their segments is read
+    assert call([0, 1 << 30, 1 << 30, 1 << 30], [0, 1, 2]) == (SEQ, [True] * 4, [True] * 3)
+    assert call([0, 2 ** 31 - 1, 0, 2 ** 31 - 1], [0, 1, 2]) == (SEQ, [True] * 4, [True] * 3)
+    assert call([1 << 20, 0, 1 << 20, 0], [0, 1, 2]) == (SEQ, [True] * 4, [True] * 3)
 
 
 # ------------------------------------------------ streams, graphs, offsets
