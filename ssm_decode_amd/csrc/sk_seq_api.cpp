@@ -19,11 +19,14 @@ namespace {
 int es_of(int32_t dtype) { return dtype == SKSSM_F32 ? 4 : 2; }
 
 // Prompts of up to this many tokens go token by token where the launch has both
-// kinds.
-int short_prompt(const sketchssm_layer* L) { return L->dk == 64 ? 32 : 16; }
+// kinds.  Token by token and in chunks, in us at 8, 24 and 48 tokens each: one prompt of
+// 64 heads of 128 x 64 11 and 21, 21 and 21, 35 and 21; 64 prompts 79 and 120, 110 and
+// 115, 166 and 118; 64 of heads of 64 x 64 40 and 79, 64 and 80, 104 and 85; of heads of
+// 128 x 128 126 and 225, 187 and 229, 289 and 240.
+constexpr int kShort = 24;
 
 // How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
-// none), all of them or those of more than short_prompt tokens; in segments of
+// none), all of them or those of more than kShort tokens; in segments of
 // 2^seg_shift tokens (0: whole), with the bytes of their states and decays.
 struct Plan {
   int64_t chunked, nsegs, decay_at, bytes;
@@ -33,7 +36,6 @@ struct Plan {
 constexpr int kMinSegShift = 8, kCus = 256;
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   Plan p{};
-  const int shrt = short_prompt(L);
   if (nseq == 0) return p;
   auto segments = [&](int shift) {
     p.seg_shift = shift;
@@ -42,10 +44,16 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
     p.bytes = p.decay_at + (p.nsegs * L->heads * 4 + 15) / 16 * 16;
   };
   if (L->dk < 64 || L->act_dtype != SKSSM_BF16) {
-    // Token by token: in segments where tiles are few and prompts long on average.
-    if (nseq * L->heads <= 2 * kCus && tokens >= 128 * nseq) {
-      int shift = 6;
-      while ((tokens >> shift) * L->heads > 8 * kCus) ++shift;
+    // Token by token: in segments where tiles are few and prompts long on average,
+    // as short as leaves the segments' states within 16 MB.  Prompts of 512 tokens in
+    // fp32, whole and in segments: 8 with 16 heads of 64 x 64 118 us and 63 (of 64 tokens;
+    // 73 of 32, 78 of 128), 32 of them 151 and 174; 2 with 64 heads of 128 x 64 179 and 102
+    // (of 128), 4 of them 180 and 179.  8 of 256 tokens with 16 heads of 64 x 64 64 and 46
+    // (of 32), 8 of 128 tokens 34 and 34.
+    const int64_t state = (int64_t)L->heads * L->dk * L->dv;
+    if (nseq * state <= 1 << 20 && tokens >= 160 * nseq) {
+      int shift = 5;
+      while ((tokens >> shift) * state > 1 << 22) ++shift;
       if (tokens >> shift >= 2 * nseq) {
         p.chunked = nseq;
         segments(shift);
@@ -54,9 +62,9 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
     return p;
   }
   p.in_chunks = true;
-  if (tokens - nseq < shrt) return p;            // (no prompt is longer unless others are empty)
+  if (tokens - nseq < kShort) return p;            // (no prompt is longer unless others are empty)
   p.all = tokens > 64 * nseq;
-  const int64_t most = tokens / (shrt + 1);
+  const int64_t most = tokens / (kShort + 1);
   p.chunked = p.all || nseq < most ? nseq : most;
   const int units = L->heads / L->qk_groups * (L->dv / sk::SCAN_COLS);
   p.parts = (units + sk::SCAN_WAVES - 1) / sk::SCAN_WAVES;
@@ -148,10 +156,10 @@ int sketchssm_scan(const sketchssm_layer* layer, const sketchssm_buffers* bufs, 
       p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(pr->work) + pl.decay_at);
       p.waves = pl.waves;
       p.parts = pl.parts;
-      p.len_lo = pl.all || !pl.in_chunks ? -1 : short_prompt(layer);
+      p.len_lo = pl.all || !pl.in_chunks ? -1 : kShort;
       if (pl.in_chunks) {
         if ((rc = sk::launch_scan_chunks(dk, dv, p, st)) || pl.all) return rc;
-        p.len_hi = short_prompt(layer);
+        p.len_hi = kShort;
         p.nchunked = 0;
       }
     }
@@ -218,10 +226,11 @@ int sketchssm_conv(const sketchssm_convolution* cv, void* hip_stream) {
     p.err = cv->err;
     p.eps = cv->eps;
     // Blocks of 32 tokens, shorter where that leaves CUs idle (each takes taps - 1
-    // more rows): 4096 tokens of 12288 channels 51.5 us with 32, 48.5 with 16.
+    // more rows).  12288 channels in bf16, in blocks of 8, 16 and 32 tokens: one prompt
+    // of 517 12.3, 14.0 and 22.3 us, of 2048 29, 26 and 31, of 4096 50, 47 and 43.
     p.shift = 5;
     const int64_t parts = (channels * es / 1024 + 6) / 4;
-    while (p.shift > 3 && ((cv->tokens >> p.shift) + cv->nseq) * parts < 1536) --p.shift;
+    while (p.shift > 3 && ((cv->tokens >> p.shift) + cv->nseq) * parts < 800) --p.shift;
     return sk::launch_conv(cv->dtype, cv->taps, p, reinterpret_cast<hipStream_t>(hip_stream));
   } catch (...) {
     return SKSSM_ELAUNCH;
