@@ -132,6 +132,7 @@ __device__ __forceinline__ int chunked_prompt(const PromptParams& p, int x, int*
     const int len = p.start[j + 1] - p.start[j];
     const bool mine = lane < p.nseq && len > p.len_lo;
     const unsigned long long all = __ballot(mine);
+    if (x >= __popcll(all)) return -1;
     int before = 0;
     for (int k = 0; k < p.nseq; ++k) {
       const int other = __builtin_amdgcn_readlane(len, k);

@@ -25,6 +25,9 @@ int es_of(int32_t dtype) { return dtype == SKSSM_F32 ? 4 : 2; }
 // 128 x 128 126 and 225, 187 and 229, 289 and 240.
 constexpr int kShort = 24;
 
+// Workgroups of a convolution's launch along the tokens: its threads are 32 bits.
+constexpr int64_t kMaxConvSlots = (1 << 24) - 1;
+
 // How prompts of these sizes are taken: `chunked` prompts at most in chunks (0:
 // none), all of them or those of more than kShort tokens; in segments of
 // 2^seg_shift tokens (0: whole), with the bytes of their states and decays.
@@ -231,6 +234,7 @@ int sketchssm_conv(const sketchssm_convolution* cv, void* hip_stream) {
     p.shift = 5;
     const int64_t parts = (channels * es / 1024 + 6) / 4;
     while (p.shift > 3 && ((cv->tokens >> p.shift) + cv->nseq) * parts < 800) --p.shift;
+    while (((int64_t)cv->tokens >> p.shift) + cv->nseq > kMaxConvSlots) ++p.shift;
     return sk::launch_conv(cv->dtype, cv->taps, p, reinterpret_cast<hipStream_t>(hip_stream));
   } catch (...) {
     return SKSSM_ELAUNCH;
