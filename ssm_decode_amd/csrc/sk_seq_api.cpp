@@ -318,7 +318,7 @@ int sketchssm_reorder(const sketchssm_layer* layer, const sketchssm_buffers* buf
     if (!m2 && layer->pullback == SKSSM_PULLBACK_PROJ) add(bufs->ring_pc, H * W * 64);
     add(bufs->count, H * 4);
     for (int i = 0; i < nextra; ++i) {
-      if (extra[i].row_bytes < 0 || extra[i].row_bytes % 16 != 0) return SKSSM_EDIM;
+      if (extra[i].row_bytes < 0 || extra[i].row_bytes % 16 != 0 || extra[i].row_bytes > kMaxTiles * 4096) return SKSSM_EDIM;
       add(extra[i].data, extra[i].row_bytes);
     }
     if (!ok) return SKSSM_EINVAL;

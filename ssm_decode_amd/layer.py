@@ -238,8 +238,12 @@ class DecodeLayer:
         for c in convs:
             c.check(self)
         extra = (abi.sketchssm_rows * max(1, len(convs)))(*(c.rows for c in convs))
-        return _on_device(self.S.device.index, lambda st: abi.sketchssm_reorder(
-            self._layer, self._bufs, extra, len(convs), parents.data_ptr(), int(beams), st), stream)
+
+        def call(st):
+            for c in convs:
+                c.uses.add(st)
+            return abi.sketchssm_reorder(self._layer, self._bufs, extra, len(convs), parents.data_ptr(), int(beams), st)
+        return _on_device(self.S.device.index, call, stream)
 
     def normalise(self, o, norm, gate=None, stream=None, rows=None) -> int:
         """The norm (serving.OutputNorm) of outputs o [rows, H, dv] (a step's or
