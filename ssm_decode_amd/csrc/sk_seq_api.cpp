@@ -36,7 +36,7 @@ struct Plan {
   bool all, in_chunks;         // (in_chunks false: token by token, all in segments)
   int seg_shift, waves, parts;
 };
-constexpr int kMinSegShift = 8, kCus = 256;
+constexpr int kMinSegShift = 7, kCus = 256;
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   Plan p{};
   if (nseq == 0) return p;
@@ -74,8 +74,17 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   p.waves = (units / 2 + p.parts - 1) / p.parts * 2;      // (two waves share their values' rows)
   const int64_t row = L->qk_groups * p.parts;    // workgroups of a segment
   // Few workgroups with many tokens: segments, as long as one of each fills the CUs
-  // about once.
+  // about once (what the prompts' last ones have more than that is short on average);
+  // 128 tokens only where even those fit.  Heads of 128 x 64 in 8 groups of 16, us of one
+  // prompt in segments of 128, 256 and 512 tokens: of 517 49, 65 and 92; of 1100 87, 71 and
+  // 91; of 2100 -, 102 and 113.  16384 tokens in segments of 512, 1024, 2048, 4096 and
+  // whole: 618, 597, 498, 805 and 2075.  24 prompts of 15715 tokens together 530 in
+  // segments of 2048, 387 whole.
+  auto most_segs = [&](int s) {
+    return p.chunked == 1 ? (tokens + ((int64_t)1 << s) - 1) >> s : (tokens >> s) + p.chunked;
+  };
   int shift = kMinSegShift;
+  if (most_segs(shift) * row > kCus) ++shift;
   while ((tokens >> shift) * row > kCus) ++shift;
   if (tokens >> shift >= 2 * p.chunked && p.chunked * row * 2 <= kCus) segments(shift);
   return p;
