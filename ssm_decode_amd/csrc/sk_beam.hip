@@ -7,6 +7,9 @@
 // values in registers: their maximum, the sum of their exponentials and the best of
 // them, by value (a row's order is that of its values, so no rounding enters it);
 // a second joins a group's parts in 64 bits and takes the best of its candidates.
+// 320 rows of 128000 bf16 logits: 24 us (3.4 TB/s; half of it vector instructions, the
+// exponentials and the search for the best) and 8 us, a chain of reads, of logarithms and of
+// one maximum after the other.  Five rows of 50001 fp32 logits: 6 and 9 us.
 #include <type_traits>
 
 #include "sk_beam.hpp"
@@ -52,8 +55,8 @@ __device__ __forceinline__ float wave_maxf(float x) {
 
 // The best of a wave's values: those of at least the bound that as many lanes reach
 // as there are beams (so the best are among them) are listed, and a listed value's
-// place is how many are better.  Only where ties make the list too long are they
-// found one by one.
+// place is how many are better (found one by one: 61 us for the 320 rows, not 33).  Only
+// where ties make the list too long are they found one by one.
 constexpr int LIST = 64;
 
 template <typename T>

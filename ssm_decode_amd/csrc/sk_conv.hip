@@ -6,9 +6,14 @@
 // held for the next call.  Heads of queries and keys may be brought to unit
 // length on the way, y / sqrt(sum of squares + eps), in 32 bits, rounded once.
 //
-// Bound by memory.  A lane has 16 bytes of a row, its weights in registers, and goes
-// from token to token with the last inputs in registers; a wave's channels are of
-// one piece (queries, keys or values), so that a head is a whole group of lanes.
+// Bound by memory: a row in, a row out, and the held inputs once a call.  A lane has 16
+// bytes of a row, its weights in registers, and goes from token to token with the last
+// inputs in registers, the next two rows in flight (four or eight at once: 1 and 3% slower,
+// their registers cost waves); a block of a prompt's tokens reads the taps - 1 rows before
+// it again, from the caches.  A wave's channels are of one piece (queries, keys or
+// values), so that a head is a whole group of lanes.  Outputs go past the caches: 15715
+// tokens of 10240 channels in bf16 135 us, 4.7 TB/s (through them 145).  A decode step of 320
+// such tokens 10.2 us, 5.2 TB/s.
 #include "sk_act.hpp"
 #include "sk_conv.hpp"
 
@@ -132,7 +137,7 @@ __device__ __forceinline__ void held_rows(const ConvParams& p, int b, bool read,
 template <typename T, int TAPS>
 __global__ void __launch_bounds__(CONV_THREADS) conv_prompt_kernel(ConvParams p) {
   using C = Conv<T, TAPS>;
-  constexpr int N = C::N, H = C::H, U = 4;
+  constexpr int N = C::N, H = C::H, U = 2;
   const int slot = blockIdx.x, i = conv_prompt(p, slot);
   // (a refused list may have no prompt that any slot comes to: it is reported here)
   if (slot == 0 && i != 0) conv_ok(p, 0, p.seqs ? p.seqs[0] : 0);
@@ -197,16 +202,15 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_prompt_kernel(ConvParams p)
 }
 
 // Single tokens: one workgroup per (ROWS tokens, four waves of channels).
-constexpr int STEP_ROWS = 4;
-template <typename T, int TAPS>
+template <typename T, int TAPS, int ROWS>
 __global__ void __launch_bounds__(CONV_THREADS) conv_step_kernel(ConvParams p) {
   using C = Conv<T, TAPS>;
   constexpr int N = C::N, H = C::H;
-  const int i0 = blockIdx.x * STEP_ROWS, rows = p.nseq - i0 < STEP_ROWS ? p.nseq - i0 : STEP_ROWS;
-  bool ok[STEP_ROWS];
-  int seq[STEP_ROWS];
+  const int i0 = blockIdx.x * ROWS, rows = p.nseq - i0 < ROWS ? p.nseq - i0 : ROWS;
+  bool ok[ROWS];
+  int seq[ROWS];
 #pragma unroll
-  for (int r = 0; r < STEP_ROWS; ++r) {
+  for (int r = 0; r < ROWS; ++r) {
     seq[r] = r < rows ? (p.seqs ? p.seqs[i0 + r] : i0 + r) : 0;
     ok[r] = r < rows && (!p.seqs ? seq[r] < p.B : conv_ok(p, i0 + r, seq[r]));
   }
@@ -215,9 +219,9 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_step_kernel(ConvParams p) {
   if (!conv_piece(p, blockIdx.y * CONV_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), N, &pc, &cp) || cp >= pc.size)
     return;
   const int c = pc.first + cp;
-  u32x4 raw[STEP_ROWS][H], x[STEP_ROWS];
+  u32x4 raw[ROWS][H], x[ROWS];
 #pragma unroll
-  for (int r = 0; r < STEP_ROWS; ++r)
+  for (int r = 0; r < ROWS; ++r)
     if (ok[r]) {
       held_rows<T, H>(p, seq[r], !p.has_state || p.has_state[i0 + r] != 0, c, raw[r]);
       x[r] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const T*>(p.x) + (int64_t)(i0 + r) * p.xs + c);
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(CONV_THREADS) conv_step_kernel(ConvParams p) {
   C k;
   k.weights(p, c);
 #pragma unroll
-  for (int r = 0; r < STEP_ROWS; ++r)
+  for (int r = 0; r < ROWS; ++r)
     if (ok[r]) {
 #pragma unroll
       for (int j = 0; j < H; ++j) unpack(raw[r][j], k.hist[j]);
@@ -249,8 +253,14 @@ int launch(ConvParams p, hipStream_t st) {
     const unsigned slots = (unsigned)((p.tokens >> p.shift) + p.nseq);
     hipLaunchKernelGGL((conv_prompt_kernel<T, TAPS>), dim3(slots, parts), dim3(CONV_THREADS), 0, st, p);
   } else {
-    const unsigned rows = (unsigned)(p.nseq + STEP_ROWS - 1) / STEP_ROWS;
-    hipLaunchKernelGGL((conv_step_kernel<T, TAPS>), dim3(rows, parts), dim3(CONV_THREADS), 0, st, p);
+    // Four tokens share the weights' loads; where the CUs have few workgroups each has its
+    // own: us with one and four, 10240 channels in bf16, of 16 tokens 3.5 and 5.6, of 96
+    // 5.6 and 6.5, of 128 7.1 and 6.8, of 320 13.6 and 10.2 (two 11.2, eight 11.1).
+    if ((int64_t)p.nseq * parts <= 640) {
+      hipLaunchKernelGGL((conv_step_kernel<T, TAPS, 1>), dim3(p.nseq, parts), dim3(CONV_THREADS), 0, st, p);
+    } else {
+      hipLaunchKernelGGL((conv_step_kernel<T, TAPS, 4>), dim3((unsigned)(p.nseq + 3) / 4, parts), dim3(CONV_THREADS), 0, st, p);
+    }
   }
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }

@@ -5,7 +5,10 @@
 // Bound by memory: what moves is read once (a parent of several beams comes again
 // from the caches) and written once; a beam that stays is not touched.  A lane holds
 // the pieces of all beams of its group at one place of a row before it writes any of
-// them, so no copy of the states is needed and no order among lanes matters.
+// them, so no copy of the states is needed and no order among lanes matters.  Loads and
+// stores go past the caches: 320 sequences of 128 heads of 128 x 64 in groups of four, a
+// random choice of parents, 1.99 GB in 336 us, 5.9 TB/s (through the caches, a beam at a
+// time: 376).  Four beams of 32 heads of 128 x 128: 5.4 us.
 #include "sk_beam.hpp"
 #include "sk_device.hpp"
 

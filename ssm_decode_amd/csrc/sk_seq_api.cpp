@@ -76,10 +76,11 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   // Few workgroups with many tokens: segments, as long as one of each fills the CUs
   // about once (what the prompts' last ones have more than that is short on average);
   // 128 tokens only where even those fit.  Heads of 128 x 64 in 8 groups of 16, us of one
-  // prompt in segments of 128, 256 and 512 tokens: of 517 49, 65 and 92; of 1100 87, 71 and
-  // 91; of 2100 -, 102 and 113.  16384 tokens in segments of 512, 1024, 2048, 4096 and
-  // whole: 618, 597, 498, 805 and 2075.  24 prompts of 15715 tokens together 530 in
-  // segments of 2048, 387 whole.
+  // prompt in segments of 128, 256 and 512 tokens, and whole: of 517 tokens 48, 63, 98 and
+  // 83; of 1100 84, 69, 106 and 154; of 2100 127, 100, 113 and 270.  16384 tokens in
+  // segments of 512, 1024, 2048, 4096 and whole: 528, 473, 449, 749 and 2041.  24 prompts
+  // of 15715 tokens together in segments of 1024, 2048, 4096 and whole: 493, 527, 406 and
+  // 344.
   auto most_segs = [&](int s) {
     return p.chunked == 1 ? (tokens + ((int64_t)1 << s) - 1) >> s : (tokens >> s) + p.chunked;
   };

@@ -99,7 +99,7 @@ def test_prompts(shape, taps, act):
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
-@pytest.mark.parametrize("B", [1, 7, 64])
+@pytest.mark.parametrize("B", [1, 7, 64, 702])
 @pytest.mark.parametrize("taps", [2, 4])
 def test_single_tokens(B, taps, act):
     c = Case(B, B, act=act, taps=taps, unit=True, H=4, G=2, dk=128, dv=64, seed=B)
@@ -111,6 +111,27 @@ def test_single_tokens(B, taps, act):
     seqs, has = [B - 1 - 2 * i for i in range(n)], [i % 2 for i in range(n)]
     assert c.call(seqs=ints(seqs), has_state=ints(has)) == 0
     c.check(range(n + 1), seqs, has)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [641, 703])
+def test_many_single_tokens(n, act):
+    """Workgroups of four tokens each; sequences in another order, refused ones among them."""
+    B = n + 5
+    c = Case(n, B, act=act, unit=True, H=2, G=1, dk=64, dv=64, seed=n)
+    seqs, has = [B - 1 - i for i in range(n)], [int(i % 3 > 0) for i in range(n)]
+    assert c.call(seqs=ints(seqs), has_state=ints(has)) == 0
+    c.check(range(n + 1), seqs, has)
+    c = Case(n, B, act=act, unit=True, H=2, G=1, dk=64, dv=64, seed=n + 1)
+    seqs[3], seqs[n - 1], seqs[9] = B, seqs[0], -1       # outside, listed before, outside
+    assert c.call(seqs=ints(seqs), has_state=ints(has)) == 0
+    assert c.conv.error_word() == 4
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[[3, 9, n - 1]] = True
+    assert ((c.y[:, :256] == 5).all(1) == bad).all()
+    kept = sorted(set(range(B)) - {x for i, x in enumerate(seqs) if i not in (3, 9, n - 1)})
+    same = (c.conv.state == c.held).flatten(1).all(1)
+    assert torch.nonzero(same).flatten().tolist() == kept
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
