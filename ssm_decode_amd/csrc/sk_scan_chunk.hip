@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
 
 // The states between a prompt's segments: S behind segment s is g_s S + B_s,
 // written over B_s.  Element by element (in whatever order the waves left them), so
-// bound by memory; one lane a vector of four, the next segment's in flight.
-constexpr int JOIN_THREADS = 256;
+// bound by memory; one lane a vector of four, the next four segments' in flight.
+constexpr int JOIN_THREADS = 256, JOIN_AHEAD = 4;
 template <int DK, int DV>
 __global__ void __launch_bounds__(JOIN_THREADS) scan_join_kernel(ScanParams p) {
   constexpr int VECS = DK * DV / 4, BLOCKS = (VECS + JOIN_THREADS - 1) / JOIN_THREADS;
@@ -614,13 +614,30 @@ __global__ void __launch_bounds__(JOIN_THREADS) scan_join_kernel(ScanParams p) {
   f32x4s* at = reinterpret_cast<f32x4s*>(p.seg + ((size_t)first * p.H + h) * DK * DV) + vec;
   const float* decay = p.seg_decay + (size_t)first * p.H + h;
   const size_t step = (size_t)p.H * VECS;
-  f32x4s S = at[0], B = at[step];
-  for (int s = 1; s + 1 < segs; ++s) {
-    f32x4s next = B;
-    if (s + 2 < segs) next = at[(s + 1) * step];
-    S = decay[(size_t)s * p.H] * S + B;
-    at[s * step] = S;
-    B = next;
+  f32x4s S = at[0], B[2][JOIN_AHEAD];
+  float g[2][JOIN_AHEAD];
+  auto fetch = [&](int s, int buf) {
+#pragma unroll
+    for (int u = 0; u < JOIN_AHEAD; ++u) {
+      const int t = s + u < segs - 2 ? s + u : segs - 2;
+      B[buf][u] = at[t * step];
+      g[buf][u] = decay[(size_t)t * p.H];
+    }
+  };
+  auto go = [&](int s, int buf) {
+#pragma unroll
+    for (int u = 0; u < JOIN_AHEAD; ++u) {
+      if (s + u + 1 >= segs) return;
+      S = g[buf][u] * S + B[buf][u];
+      at[(s + u) * step] = S;
+    }
+  };
+  fetch(1, 0);
+  for (int s = 1; s + 1 < segs; s += 2 * JOIN_AHEAD) {
+    if (s + JOIN_AHEAD + 1 < segs) fetch(s + JOIN_AHEAD, 1);
+    go(s, 0);
+    if (s + 2 * JOIN_AHEAD + 1 < segs) fetch(s + 2 * JOIN_AHEAD, 0);
+    go(s + JOIN_AHEAD, 1);
   }
 }
 
