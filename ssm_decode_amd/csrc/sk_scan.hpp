@@ -11,6 +11,7 @@ namespace sk {
 struct ScanParams : PromptParams {
   int G;
   int waves, parts;         // chunked form: waves of a workgroup, workgroups of a group's heads
+  bool joined;              // .. the segments' states by a launch of their own
   const float* A;           // [H]
   float* seg_decay;         // [nsegs][H] products of the segments' decays
 };

@@ -111,7 +111,8 @@ __device__ __forceinline__ constexpr int frag_of(int ib, int s) { return ib == 0
 //   1. without outputs, the segments but the last, at once: each from a zero state
 //      (the first from the prompt's) its state behind it, B, and the product g of
 //      its decays: the state behind a segment is g S + B;
-//   2. scan_join_kernel: the states between the segments, in order;
+//   2. scan_join_kernel: the states between the segments, in order (few segments: the
+//      third launch's do that, each for itself);
 //   3. the segments at once, each from the state before it, with outputs.
 // The first segment leaves the state that the prompt starts from in the last one's
 // place, which has no use for it: the prompt's own place is written by the third
@@ -246,12 +247,23 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
         each4([&](int db, int q, int at) { to[at] = four(db, q); });
       }
     } else if (OUT) {
-      const f32x4s* from = seg_at(seg == 0 ? slot + slots - 1 : slot - 1);
+      // (joined: the state before it; few: the segments' from the first one's on)
+      const bool chain = seg > 0 && !p.joined;
+      const f32x4s* from = seg_at(seg == 0 ? slot + slots - 1 : chain ? slot - seg : slot - 1);
       each4([&](int db, int q, int at) {
         const f32x4s x = from[at];
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[db][4 * q + r] = x[r];
       });
+      for (int s = slot - seg + 1; chain && s < slot; ++s) {
+        const float g = p.seg_decay[(size_t)s * p.H + h];
+        const f32x4s* B = seg_at(s);
+        each4([&](int db, int q, int at) {
+          const f32x4s x = B[at];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[db][4 * q + r] = g * S[db][4 * q + r] + x[r];
+        });
+      }
     }
   }
   const double rate = wave_last(exp((double)p.A[h]) * -1.4426950408889634);
@@ -660,7 +672,7 @@ int launch(const ScanParams& p, hipStream_t st) {
   static_assert(ScanLds<DK, true>::bytes(SCAN_WAVES) <= 160 * 1024, "LDS of a CU");
   if (p.seg_shift) {
     launch_chunks<DK, DV, false>(p, st);
-    launch_join<DK, DV>(p, st);
+    if (p.joined) launch_join<DK, DV>(p, st);
   }
   launch_chunks<DK, DV, true>(p, st);
   return hipGetLastError() == hipSuccess ? 0 : -5;

@@ -37,6 +37,13 @@ struct Plan {
   int seg_shift, waves, parts;
 };
 constexpr int kMinSegShift = 7, kCus = 256;
+
+// Up to so many segments in chunks are joined by those that start from them, each for
+// itself, and by a launch of their own where there are more.  128 heads of 128 x 64 in 8
+// groups, us with a launch and without: a prompt of 300 tokens (3 segments) 46 and 38, 517
+// (5) 51 and 43, 900 (8) 57 and 50, 16384 (8) 449 and 449.
+constexpr int kFewSegs = 8;
+
 Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   Plan p{};
   if (nseq == 0) return p;
@@ -169,6 +176,7 @@ int sketchssm_scan(const sketchssm_layer* layer, const sketchssm_buffers* bufs, 
       p.seg_decay = reinterpret_cast<float*>(static_cast<char*>(pr->work) + pl.decay_at);
       p.waves = pl.waves;
       p.parts = pl.parts;
+      p.joined = pl.nsegs > kFewSegs;
       p.len_lo = pl.all || !pl.in_chunks ? -1 : kShort;
       if (pl.in_chunks) {
         if ((rc = sk::launch_scan_chunks(dk, dv, p, st)) || pl.all) return rc;
