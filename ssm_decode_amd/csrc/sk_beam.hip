@@ -9,7 +9,7 @@
 // a second joins a group's parts in 64 bits and takes the best of its candidates.
 // 320 rows of 128000 bf16 logits: 24 us (3.4 TB/s; half of it vector instructions, the
 // exponentials and the search for the best) and 8 us, a chain of reads, of logarithms and of
-// one maximum after the other.  Five rows of 50001 fp32 logits: 6 and 9 us.
+// one maximum after the other.  Five rows of 50001 fp32 logits: 7 and 7 us.
 #include <type_traits>
 
 #include "sk_beam.hpp"
@@ -61,7 +61,7 @@ constexpr int LIST = 64;
 
 template <typename T>
 __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
-  constexpr int N = 16 / (int)sizeof(T), E = 64 / (int)sizeof(T), V = E / N;      // values of a vector, of a lane; vectors
+  constexpr int N = 16 / (int)sizeof(T), E = BEAM_VALUES, V = E / N;      // values of a vector, of a lane; vectors
   __shared__ uint64_t s_list[4][LIST], s_key[4 * BEAM_MAX];
   const int row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
   // Rows of any length begin anywhere: vectors of whole 16 bytes of memory, the
   // first of which may begin before the row.
   const int skew = (int)((reinterpret_cast<uintptr_t>(X) & 15) / sizeof(T));
-  const int first = part * beam_part((int)sizeof(T)) - skew;
+  const int first = part * BEAM_PART - skew;
   float x[E];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
   if (listed <= LIST) {
     const uint64_t k = lane < listed ? s_list[wv][lane] : 0;
     int place = 0;
-    for (int j = 0; j < listed; ++j) place += s_list[wv][j] > k;
+    for (int j = 0; j < listed; j += 8)          // (eight reads at once: LIST is a multiple of it)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) place += s_list[wv][j + e] > k && j + e < listed;
     if (lane < listed && place < p.beams) s_key[wv * BEAM_MAX + place] = k;
   } else {
     uint64_t last = ~0ull;
@@ -166,14 +168,16 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
   }
   __syncthreads();
   if (wv == 0) {                                 // the best of the waves'
-    const int n = 4 * p.beams;
-    const uint64_t k = lane < n ? s_key[lane / p.beams * BEAM_MAX + lane % p.beams] : 0;
+    const bool mine = lane % BEAM_MAX < p.beams;
+    const uint64_t k = mine ? s_key[lane] : 0;
     int place = 0;
-    for (int j = 0; j < n; ++j) {
-      const uint64_t o = s_key[j / p.beams * BEAM_MAX + j % p.beams];
-      place += o > k || (o == k && j < lane);
-    }
-    if (lane < n && place < p.beams) {
+    for (int r = 0; r < p.beams; ++r)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint64_t o = s_key[w * BEAM_MAX + r];
+        place += o > k || (o == k && w * BEAM_MAX + r < lane);
+      }
+    if (mine && place < p.beams) {
       out->value[place] = k ? key_value(k) : NONE;
       out->index[place] = key_index(k);
     }
@@ -228,23 +232,32 @@ __device__ __forceinline__ void wave_best(int take, double score, int at, Got go
 }
 
 // One workgroup per group.  (Places b * vocab + j are below 16 * 2^24.)
+// JOIN_CHAIN: up to as many beams the best are taken one by one, more from a list: 16
+// groups over 128000 bf16 logits, both launches, 14 and 22 us with 4 beams, 29 and 33 with
+// 8, 42 and 40 with 10, 86 and 79 with 16.
+constexpr int JOIN_LIST = 256, JOIN_CHAIN = 8;
+// HELD: a lane's candidates that are read at once with the rows' sums: k of each part
+// of a row (an ended row's only one is its first; k: none).  (Those beyond are read again
+// for each that is taken: with four 16 groups of 16 beams 229 us.)
+template <int HELD>
 __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(BeamParams p) {
   __shared__ double s_lse[BEAM_MAX], s_score[4 * BEAM_MAX], s_out[BEAM_MAX];
   __shared__ float s_in[BEAM_MAX];
   __shared__ int s_ended[BEAM_MAX], s_at[4 * BEAM_MAX], s_pick[BEAM_MAX];
+  __shared__ double s_list[4][JOIN_LIST];
+  __shared__ int s_place[4][JOIN_LIST];
   const int g = blockIdx.x, k = p.beams, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   constexpr int FAR = INT32_MAX;
-  // The first candidates of a lane are read at once with the rows' sums: k of each part
-  // of a row (an ended row's only one is its first; k: none).
-  constexpr int HELD = 4;
   const int per = p.parts * k, all = per * k;
+  // (c < 2^20: the quotients' errors are less than the half)
+  const float by_per = 1.f / per, by_k = 1.f / k;
   auto candidate = [&](int c, int* b, float* v, int* a) {
-    *b = c / per;
-    const int j = c - *b * per, row = g * k + *b;
+    *b = (int)((c + 0.5f) * by_per);
+    const int j = c - *b * per, row = g * k + *b, x = (int)((j + 0.5f) * by_k);
     const bool ended = p.ended && p.ended[row] != 0;
-    const BeamPart* part = p.part + (int64_t)row * p.parts + j / k;
-    *v = part->value[j % k];
-    *a = *b * p.vocab + part->index[j % k];
+    const BeamPart* part = p.part + (int64_t)row * p.parts + x;
+    *v = part->value[j - x * k];
+    *a = *b * p.vocab + part->index[j - x * k];
     if (ended) {
       *v = 0.f;
       *a = *b * p.vocab + (p.end_token > 0 ? p.end_token : 0);
@@ -256,28 +269,39 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(BeamParams p) {
 #pragma unroll
   for (int i = 0; i < HELD; ++i) {
     hb[i] = k;
+    ha[i] = FAR;
     const int c = tid + i * BEAM_THREADS;
     if (c < all) candidate(c, &hb[i], &hv[i], &ha[i]);
   }
-  if (tid < 4 * BEAM_MAX) s_score[tid] = NO_SCORE;
+  if (tid < 4 * BEAM_MAX) {
+    s_score[tid] = NO_SCORE;
+    s_at[tid] = FAR;
+  }
   if (tid < BEAM_MAX) s_pick[tid] = FAR;
-  for (int b = wv; b < k; b += 4) {              // the rows' sums: a wave a row
+  // the rows' sums: a wave a row, or 16 lanes where there are more rows than waves
+  auto row_sums = [&](auto lanes) {
+    constexpr int LANES = decltype(lanes)::value;
+    const int b = tid / LANES, first = tid % LANES;
+    if (b >= k) return;                          // (whole groups of lanes)
     const int row = g * k + b;
     const float in = p.scores[row];
     const bool ended = p.ended && p.ended[row] != 0;
     const BeamPart* part = p.part + (int64_t)row * p.parts;
     const int n = ended ? 0 : 4 * p.parts;
     float top = -__builtin_inff();
-    for (int j = lane; j < n; j += 64) top = fmaxf(top, part[j >> 2].top[j & 3]);
-    top = wave_maxf(top);
+#pragma unroll 4
+    for (int j = first; j < n; j += LANES) top = fmaxf(top, part[j >> 2].top[j & 3]);
+#pragma unroll
+    for (int s = 1; s < LANES; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
     double sum = 0;
-    for (int j = lane; j < n; j += 64) {
+#pragma unroll 4
+    for (int j = first; j < n; j += LANES) {
       const float t = part[j >> 2].top[j & 3], s = part[j >> 2].sum[j & 3];
       sum += s == 0.f ? 0. : exp((double)t - top) * s;
     }
 #pragma unroll
-    for (int s = 1; s < 64; s *= 2) sum += __shfl_xor(sum, s);
-    if (lane == 0) {
+    for (int s = 1; s < LANES; s *= 2) sum += __shfl_xor(sum, s);
+    if (first == 0) {
       // a row without a finite sum, and a score that is none, take the beam out; all
       // ruled out is no error
       const bool wrong = !(fabs(sum) < __builtin_inf()) || in != in || in == __builtin_inff();
@@ -286,57 +310,134 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(BeamParams p) {
       s_ended[b] = ended;
       s_lse[b] = (double)top + log(sum);
     }
-  }
+  };
+  if (k <= 4) row_sums(std::integral_constant<int, 64>{});
+  else row_sums(std::integral_constant<int, 16>{});
   __syncthreads();
-  // candidates, k of each part of a row; a lane offers the best of its own behind the
-  // last that was taken from it
+  // candidates, k of each part of a row
   auto rate = [&](int b, float v) -> double {
     const float in = s_in[b];
     if (s_ended[b]) return in;
-    return in > -__builtin_inff() && v > -__builtin_inff() ? (double)in + ((double)v - s_lse[b]) : NO_SCORE;
+    return in > -__builtin_inf() && v > -__builtin_inf() ? (double)in + ((double)v - s_lse[b]) : NO_SCORE;
   };
-  auto offer = [&](double* score, int* at) {
-    const double last = *score;
-    const int last_at = *at;
-    double best = NO_SCORE;
-    int best_at = FAR;
-    auto consider = [&](int b, float v, int a) {
-      const double s = rate(b, v);
-      const bool behind = s < last || (s == last && a > last_at);
-      if (behind && (s > best || (s == best && a < best_at))) {
-        best = s;
-        best_at = a;
-      }
-    };
+  double hs[HELD];
 #pragma unroll
-    for (int i = 0; i < HELD; ++i)
-      if (hb[i] < k) consider(hb[i], hv[i], ha[i]);
-    for (int c = tid + HELD * BEAM_THREADS; c < all; c += BEAM_THREADS) {
-      float v;
-      int b, a;
-      candidate(c, &b, &v, &a);
-      if (b < k) consider(b, v, a);
-    }
-    *score = best;
-    *at = best_at;
+  for (int i = 0; i < HELD; ++i) hs[i] = hb[i] < k ? rate(hb[i], hv[i]) : NO_SCORE;
+  // (where a row has more parts than lanes hold candidates of, the others are read again)
+  auto further = [&](int c, int* a) -> double {
+    int b;
+    float v;
+    candidate(c, &b, &v, a);
+    return b < k ? rate(b, v) : NO_SCORE;
   };
-  double score = __builtin_inf();
-  int at = -1;
-  offer(&score, &at);
-  wave_best(k, score, at,
-            [&](int n, double s, int a) {
-              s_score[wv * BEAM_MAX + n] = s;
-              s_at[wv * BEAM_MAX + n] = a;
-            },
-            offer);
+  // A wave's best, as the parts': those of at least the bound that as many lanes reach as
+  // there are beams are listed, and a listed one's place is how many are better.
+  int listed = JOIN_LIST + 1;
+  if (k > JOIN_CHAIN) {
+    double mine = NO_SCORE;
+  #pragma unroll
+    for (int i = 0; i < HELD; ++i) mine = fmax(mine, hs[i]);
+    for (int c = tid + HELD * BEAM_THREADS, a; c < all; c += BEAM_THREADS) mine = fmax(mine, further(c, &a));
+    s_list[wv][lane] = mine;
+    wave_lds_sync();
+    int place = 0;
+  #pragma unroll 16
+    for (int j = 0; j < 64; ++j) {
+      const double o = s_list[wv][j];
+      place += o > mine || (o == mine && j < lane);
+    }
+    const double bound = s_list[wv][__builtin_ctzll(__ballot(place == k - 1))];
+    wave_lds_sync();
+    listed = 0;
+    auto list = [&](double score, int a) {
+      const bool it = score > NO_SCORE && score >= bound;
+      const unsigned long long m = __ballot(it);
+      const int to = listed + __popcll(m & ((1ull << lane) - 1));
+      if (it && to < JOIN_LIST) {
+        s_list[wv][to] = score;
+        s_place[wv][to] = a;
+      }
+      listed += __popcll(m);
+    };
+  #pragma unroll
+    for (int i = 0; i < HELD; ++i) list(hs[i], ha[i]);
+    for (int c = tid + HELD * BEAM_THREADS; c - tid < all; c += BEAM_THREADS) {
+      int a = FAR;
+      const double score = c < all ? further(c, &a) : NO_SCORE;
+      list(score, a);
+    }
+    wave_lds_sync();
+  }
+  if (listed <= JOIN_LIST) {
+    for (int e = lane; e < listed; e += 64) {
+      const double score = s_list[wv][e];
+      const int a = s_place[wv][e];
+      int better = 0;
+      for (int j = 0; j < listed; j += 8)
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          const double o = s_list[wv][j + f];
+          better += (o > score || (o == score && s_place[wv][j + f] < a)) && j + f < listed;
+        }
+      if (better < k) {
+        s_score[wv * BEAM_MAX + better] = score;
+        s_at[wv * BEAM_MAX + better] = a;
+      }
+    }
+  } else {                                       // (one by one)
+    auto offer = [&](double* score, int* at) {   // the lane's best behind the last that was taken
+      const double last = *score;
+      const int last_at = *at;
+      double best = NO_SCORE;
+      int best_at = FAR;
+      auto consider = [&](double x, int a) {
+        const bool behind = x < last || (x == last && a > last_at);
+        if (behind && (x > best || (x == best && a < best_at))) {
+          best = x;
+          best_at = a;
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (hb[i] < k) consider(hs[i], ha[i]);
+      for (int c = tid + HELD * BEAM_THREADS; c < all; c += BEAM_THREADS) {
+        int a;
+        const double x = further(c, &a);
+        consider(x, a);
+      }
+      *score = best;
+      *at = best_at;
+    };
+    double score = __builtin_inf();
+    int at = -1;
+    offer(&score, &at);
+    wave_best(k, score, at,
+              [&](int n, double x, int a) {
+                s_score[wv * BEAM_MAX + n] = x;
+                s_at[wv * BEAM_MAX + n] = a;
+              },
+              offer);
+  }
   __syncthreads();
   if (wv > 0) return;
-  wave_best(k, s_score[lane], s_at[lane],
-            [&](int n, double s, int a) {
-              s_out[n] = s;
-              s_pick[n] = a;
-            },
-            [](double* s, int*) { *s = NO_SCORE; });
+  if (k > JOIN_CHAIN) {                          // the best of the waves'
+    const double score = s_score[lane];
+    const int a = s_at[lane];
+    int better = 0;
+#pragma unroll 16
+    for (int j = 0; j < 4 * BEAM_MAX; ++j) better += s_score[j] > score || (s_score[j] == score && s_at[j] < a);
+    if (score > NO_SCORE && better < k) {
+      s_out[better] = score;
+      s_pick[better] = a;
+    }
+  } else {
+    wave_best(k, s_score[lane], s_at[lane],
+              [&](int n, double x, int a) {
+                s_out[n] = x;
+                s_pick[n] = a;
+              },
+              [](double* x, int*) { *x = NO_SCORE; });
+  }
   wave_lds_sync();
   if (lane < k) {
     const int row = g * k + lane, pick = s_pick[lane];
@@ -357,7 +458,10 @@ int launch_beam_select(int dtype, const BeamParams& p, hipStream_t st) {
   const dim3 grid((unsigned)p.parts * p.groups * p.beams), block(BEAM_THREADS);
   if (dtype == DT_F32) hipLaunchKernelGGL((beam_part_kernel<float>), grid, block, 0, st, p);
   else hipLaunchKernelGGL((beam_part_kernel<bf16>), grid, block, 0, st, p);
-  hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)p.groups), block, 0, st, p);
+  if (p.parts * p.beams * p.beams <= 4 * BEAM_THREADS)
+    hipLaunchKernelGGL((beam_join_kernel<4>), dim3((unsigned)p.groups), block, 0, st, p);
+  else
+    hipLaunchKernelGGL((beam_join_kernel<16>), dim3((unsigned)p.groups), block, 0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 

@@ -10,7 +10,7 @@
 namespace sk {
 
 constexpr int BEAM_MAX = 16;             // beams of a group
-constexpr int BEAM_THREADS = 256;
+constexpr int BEAM_THREADS = 256, BEAM_VALUES = 32;      // .. and a lane's values of a part
 enum BeamErrBit { ERRBIT_LOGIT = 16 };
 
 // A workgroup's part of a row: its values' maximum and the sum of their
@@ -36,11 +36,12 @@ struct BeamParams {
   BeamPart* part;           // [groups * beams][parts]
 };
 
-// Elements of a workgroup's part of a row.
-constexpr int beam_part(int esize) { return BEAM_THREADS * 64 / esize; }
+// Elements of a workgroup's part of a row.  (Half as many: 320 rows of 128000 in bf16 37 us,
+// not 31; 256 in fp32 83, not 49; twice as many: 35 in bf16.)
+constexpr int BEAM_PART = BEAM_THREADS * BEAM_VALUES;
 // (a row's first vector may begin up to 16 bytes less an element before it)
 inline int beam_parts(int vocab, int esize) {
-  return (int)(((int64_t)vocab + 16 / esize - 1 + beam_part(esize) - 1) / beam_part(esize));
+  return (int)(((int64_t)vocab + 16 / esize - 1 + BEAM_PART - 1) / BEAM_PART);
 }
 
 int launch_beam_select(int dtype, const BeamParams& p, hipStream_t st);

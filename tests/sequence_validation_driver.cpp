@@ -136,7 +136,7 @@ int launch_conv(int dtype, int taps, const ConvParams& p, hipStream_t) {
 int launch_beam_select(int dtype, const BeamParams& p, hipStream_t) {
   ++g_launches;
   const int64_t rows = (int64_t)p.groups * p.beams, es = dtype == SKSSM_F32 ? 4 : 2;
-  EXPECT((int64_t)p.parts * BEAM_THREADS * 64 >= (p.vocab + 16 / es - 1) * es);      // at any alignment
+  EXPECT((int64_t)p.parts * BEAM_PART >= p.vocab + 16 / es - 1);      // at any alignment
   EXPECT(rows * p.parts * 256 <= UINT32_MAX && rows * p.parts * (int64_t)sizeof(BeamPart) <= g_need);
   EXPECT((int64_t)p.beams * p.vocab <= INT32_MAX);
   return 0;

@@ -45,7 +45,7 @@ def check(search, x, scores, ended, err=0):
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("n,k,V,pad", [(1, 1, 1, 0), (2, 4, 3, 0), (3, 16, 5, 3), (3, 5, 97, 1), (1, 4, 4099, 0), (2, 16, 8192, 8), (5, 3, 50001, 0),
-                                       (1, 8, 128000, 0), (40, 2, 1000, 7)])
+                                       (1, 8, 128000, 0), (40, 2, 1000, 7), (2, 16, 100000, 0), (1, 16, 170001, 3)])
 def test_selection(n, k, V, pad, act):
     x, s = inputs(n, k, V, act, seed=V, pad=pad)
     search = BeamSearch(n, k, V, end=V - 1)
@@ -89,9 +89,9 @@ def test_ended_beams_and_ruled_out_tokens(act):
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("value", [0.0, -0.0, 3.0, -1e30])
-def test_ties_go_to_the_lowest_index(value, act):
+@pytest.mark.parametrize("n,k,V", [(2, 6, 40000), (2, 16, 40000), (1, 16, 170000)])
+def test_ties_go_to_the_lowest_index(n, k, V, value, act):
     """All logits alike: every wave's and part's list is full of ties."""
-    n, k, V = 2, 6, 40000
     x = torch.full((n * k, V), value, device="cuda", dtype=TORCH_DTYPE[act])
     x[:, 1::2] *= -1 if value == 0 else 1
     s = torch.zeros((n, k), device="cuda")
