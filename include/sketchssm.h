@@ -570,9 +570,9 @@ typedef struct {
  * sequences, sequence b becomes a copy of sequence parents[b] (DEVICE [batch], 4-byte
  * aligned, each within the group) in every buffer of the layer that holds something
  * of a sequence (S, U, the ring with its counts, maps, state copies and factors, as
- * the layer has them) and in nextra (0 to 4) further ones, in place.  A group with a
- * parent outside it sets SKSSM_ERRBIT_SEQ and is left as it is.  layer->batch is a
- * multiple of beams. */
+ * the layer has them) and in nextra (0 to 4) further ones, which overlap neither those
+ * nor each other (SKSSM_EINVAL), in place.  A group with a parent outside it sets
+ * SKSSM_ERRBIT_SEQ and is left as it is.  layer->batch is a multiple of beams. */
 int sketchssm_reorder(const sketchssm_layer* layer, const sketchssm_buffers* bufs, const sketchssm_rows* extra,
                       int32_t nextra, const int32_t* parents, int32_t beams, void* hip_stream);
 

@@ -335,12 +335,19 @@ int sketchssm_reorder(const sketchssm_layer* layer, const sketchssm_buffers* buf
     if (!m2) add(bufs->ring_beta, H * W * 4);
     if (!m2 && layer->pullback == SKSSM_PULLBACK_PROJ) add(bufs->ring_pc, H * W * 64);
     add(bufs->count, H * 4);
+    const int own = p.nrows;
     for (int i = 0; i < nextra; ++i) {
       if (extra[i].row_bytes < 0 || extra[i].row_bytes % 16 != 0 || extra[i].row_bytes > kMaxTiles * 4096) return SKSSM_EDIM;
       add(extra[i].data, extra[i].row_bytes);
     }
     if (!ok) return SKSSM_EINVAL;
     if (blocks * (B / beams) > kMaxTiles) return SKSSM_EDIM;
+    // (rows listed twice would be moved twice, at once)
+    for (int i = own; i < p.nrows; ++i)
+      for (int j = 0; j < i; ++j) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(p.rows[i].data), y = reinterpret_cast<uintptr_t>(p.rows[j].data);
+        if (x < y + B * p.rows[j].bytes && y < x + B * p.rows[i].bytes) return SKSSM_EINVAL;
+      }
     p.groups = (int)(B / beams);
     p.beams = beams;
     p.parents = parents;

@@ -355,7 +355,7 @@ int main() {
     const sketchssm_layer L = layer(family, beams * draw(1, 20), heads, family == SKSSM_MAMBA2 ? 1 : heads, sh[0], sh[1],
                                     draw(0, 1) ? SKSSM_F32 : SKSSM_BF16);
     sketchssm_rows x[4];
-    for (auto& r : x) r = {FAKE, 16 * (int64_t)draw(0, 5000)};
+    for (int i = 0; i < 4; ++i) x[i] = {reinterpret_cast<void*>((uintptr_t)(i + 1) << 40), 16 * (int64_t)draw(0, 5000)};
     int now = g_launches;
     EXPECT(sketchssm_reorder(&L, &B, x, 4, ix, beams, nullptr) == SKSSM_OK);
     EXPECT(sketchssm_reorder(&L, &B, nullptr, 0, ix, beams, nullptr) == SKSSM_OK);
@@ -366,6 +366,9 @@ int main() {
     EXPECT(sketchssm_reorder(&L, &B, nullptr, 1, ix, beams, nullptr) == SKSSM_EINVAL);
     EXPECT(sketchssm_reorder(&L, &B, x, 1, nullptr, beams, nullptr) == SKSSM_EINVAL);
     EXPECT(sketchssm_reorder(&L, &B, x, 1, ix, 17, nullptr) == SKSSM_EDIM);
+    x[2] = x[3];
+    x[2].row_bytes += 16;
+    EXPECT(x[3].row_bytes == 0 || sketchssm_reorder(&L, &B, x, 4, ix, beams, nullptr) == SKSSM_EINVAL);
     x[0].row_bytes = INT64_MAX / 16 * 16;
     EXPECT(sketchssm_reorder(&L, &B, x, 1, ix, beams, nullptr) == SKSSM_EDIM);
     x[1].row_bytes = x[2].row_bytes = x[3].row_bytes = x[0].row_bytes;

@@ -69,14 +69,15 @@ def test_a_first_step_has_one_beam(act):
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
-def test_ended_beams_and_ruled_out_tokens(act):
-    n, k, V = 6, 4, 900
+@pytest.mark.parametrize("k,V", [(4, 900), (14, 900), (14, 60000)])
+def test_ended_beams_and_ruled_out_tokens(k, V, act):
+    n = 6
     x, s = inputs(n, k, V, act, seed=3)
     ended = torch.zeros((n, k), dtype=torch.int32, device="cuda")
     ended[0, 1] = ended[1, 0] = 7
     ended[2] = 1                                  # all of them
     x[3 * k:4 * k] = -INF                         # nothing is left
-    x[4 * k + 1:4 * k + 4] = -INF                 # one beam is left ..
+    x[4 * k + 1:5 * k] = -INF                     # one beam is left ..
     x[4 * k, 2:] = -INF                           # .. with two tokens
     s[5, 0] = -INF
     x[:, ::3] = -INF
@@ -103,18 +104,19 @@ def test_ties_go_to_the_lowest_index(n, k, V, value, act):
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("value", [float("nan"), INF])
-def test_wrong_logits_take_their_beam_out(value, act):
-    x, s = inputs(3, 4, 5000, act, seed=5)
+@pytest.mark.parametrize("k", [4, 9])
+def test_wrong_logits_take_their_beam_out(k, value, act):
+    x, s = inputs(3, k, 5000, act, seed=5)
     clean = x.clone()
-    x[5, 4321] = value
-    x[5, 7] = value
-    search = BeamSearch(3, 4, 5000)
+    x[k + 1, 4321] = value
+    x[k + 1, 7] = value
+    search = BeamSearch(3, k, 5000)
     e = torch.zeros_like(search.ended)
     assert search.select(x, s, e) == 0
     out = s.clone()
     out[1, 1] = -INF
     check(search, clean, out, e, err=LOGIT)
-    search = BeamSearch(3, 4, 5000)
+    search = BeamSearch(3, k, 5000)
     wrong = s.clone()
     wrong[1, 1] = value
     assert search.select(clean, wrong, e) == 0

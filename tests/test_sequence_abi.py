@@ -161,6 +161,8 @@ def test_reorder_refusals():
     for name in ("S", "U", "ring_k", "ring_v", "ring_gate", "count", "err"):
         assert call(B=_bufs(**{name: None})) == E and call(B=_bufs(**{name: FAKE + 4})) == E, name
     assert call(x=((FAKE, 8),)) == D and call(x=((FAKE, -16),)) == D and call(x=((FAKE + 8, 16),)) == E and call(x=((None, 16),)) == E
+    far = FAKE << 20                             # (rows listed twice, one behind the other's start, the layer's own)
+    assert call(x=((far, 16), (far, 16))) == E and call(x=((far, 32), (far + 48, 16))) == E and call(x=((FAKE, 16),)) == E
     gdn = m2(family=abi.SKSSM_GDN)
     assert call(gdn, _bufs(ring_beta=None)) == E
     assert call(_layer([0, 4, 4, 8, 12]), _bufs(Scopy=None)) == E
