@@ -73,7 +73,11 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   }
   p.in_chunks = true;
   if (tokens - nseq < kShort) return p;            // (no prompt is longer unless others are empty)
-  p.all = tokens > 64 * nseq;
+  // Of a mean length above 40, all in chunks.  64 heads of 128 x 64 in 4 groups, us of both
+  // launches and of one: 8 prompts of 300 tokens and 64 of 2 (mean 35) 117 and 149; 48 of 48
+  // 92 and 88; 4 of 1000 and 60 of 1 (63) 200 and 152; 8 of 600 and 32 of 5 (124) 139 and
+  // 111; 16 of 300 and 16 of 5 (153) 101 and 105.
+  p.all = tokens > 40 * nseq;
   const int64_t most = tokens / (kShort + 1);
   p.chunked = p.all || nseq < most ? nseq : most;
   const int units = L->heads / L->qk_groups * (L->dv / sk::SCAN_COLS);
