@@ -19,6 +19,9 @@ namespace sk {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+template <typename T> using u32x4_at = std::conditional_t<sizeof(T) == 2, u32x4_at2, u32x4_at4>;
 
 // A value and its index as one number that is larger for the better candidate:
 // the value's order above, the lower index above the higher.  (+ 0.f: a negative
@@ -67,16 +70,16 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   if (p.ended && p.ended[row] != 0) return;
   const T* X = reinterpret_cast<const T*>(p.logits) + (int64_t)row * p.stride;
-  // Rows of any length begin anywhere: vectors of whole 16 bytes of memory, the
-  // first of which may begin before the row.
-  const int skew = (int)((reinterpret_cast<uintptr_t>(X) & 15) / sizeof(T));
-  const int first = part * BEAM_PART - skew;
+  // Rows of any length begin anywhere.  A value's lane goes by its index, not by its
+  // address, so that equal rows have equal sums (or equal beams would be no ties): the
+  // vectors are at the alignment of an element.
+  const int first = part * BEAM_PART;
   float x[E];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int at = first + (v * BEAM_THREADS + tid) * N;
-    if (at >= 0 && at + N <= p.vocab) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(X + at);
+    if (at + N <= p.vocab) {
+      const u32x4 w = *reinterpret_cast<const u32x4_at<T>*>(X + at);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if constexpr (sizeof(T) == 2) {
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_part_kernel(BeamParams p) {
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[v * N + e] = at + e >= 0 && at + e < p.vocab ? ld(X + at + e) : -__builtin_inff();
+      for (int e = 0; e < N; ++e) x[v * N + e] = at + e < p.vocab ? ld(X + at + e) : -__builtin_inff();
     }
   }
   constexpr float NONE = -__builtin_inff();

@@ -39,7 +39,8 @@ struct BeamParams {
 // Elements of a workgroup's part of a row.  (Half as many: 320 rows of 128000 in bf16 37 us,
 // not 31; 256 in fp32 83, not 49; twice as many: 35 in bf16.)
 constexpr int BEAM_PART = BEAM_THREADS * BEAM_VALUES;
-// (a row's first vector may begin up to 16 bytes less an element before it)
+// (a vector's elements less one more than the row has: where the row ends just at a
+// part's end the last part is empty, which adds nothing)
 inline int beam_parts(int vocab, int esize) {
   return (int)(((int64_t)vocab + 16 / esize - 1 + BEAM_PART - 1) / BEAM_PART);
 }
