@@ -29,7 +29,7 @@
 #include <type_traits>
 
 #include "sk_prompt_chunk.hpp"
-#include "sk_scan.hpp"
+#include "sk_scan_device.hpp"
 
 namespace sk {
 namespace {
@@ -62,36 +62,6 @@ struct ScanLds {
   static constexpr int V_BYTES = PC * 2 * SCAN_COLS * 2, FACTORS = 7 * PC * 4;
   static constexpr int bytes(int waves) { return V + waves / 2 * 2 * V_BYTES + waves * FACTORS; }
 };
-
-// Sum of the lanes up to this one, in 64 bits.
-__device__ __forceinline__ double wave_prefix(double x) {
-  auto from = [](double v, auto ctrl, auto mask) {
-    constexpr int C = decltype(ctrl)::value, M = decltype(mask)::value;
-    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, C, M, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), C, M, 0xF, false);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-  };
-  typedef std::integral_constant<int, 0xF> All;
-  x += from(x, std::integral_constant<int, 0x111>{}, All{});      // row_shr:1, 2, 4, 8
-  x += from(x, std::integral_constant<int, 0x112>{}, All{});
-  x += from(x, std::integral_constant<int, 0x114>{}, All{});
-  x += from(x, std::integral_constant<int, 0x118>{}, All{});
-  x += from(x, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});      // row_bcast:15, 31
-  x += from(x, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
-  return x;
-}
-// Lane 63's value in every lane.
-__device__ __forceinline__ double wave_last(double x) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-// 2^x in fp32 of an exponent in 64 bits: of what rounding it leaves, to first order.
-__device__ __forceinline__ float exp2_of(double x) {
-  const float f = (float)x, e = __builtin_amdgcn_exp2f(f);
-  return fmaf(e, (float)(x - (double)f) * 0.693147182f, e);
-}
 
 // A value that is the same in every lane, in scalar registers.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane((int)x); }
@@ -266,7 +236,7 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       }
     }
   }
-  const double rate = wave_last(exp((double)p.A[h]) * -1.4426950408889634);
+  const double rate = wave_last(exp((double)p.A[h]) * -LOG2E);
   double total = 0.;
 
   bf16* op = reinterpret_cast<bf16*>(p.o) + (int64_t)s0 * p.os + (int64_t)h * DV + c0;

@@ -4,6 +4,13 @@
 // of its rows, in registers for the whole prompt (rows and columns of S never
 // mix but in the output's sum over rows).
 //
+// The state is held as S = g S', g in (1, 2], and the logarithms of the decays are summed in 64
+// bits: with x their sum to the base 2, negated, g is 2^(1 - (x - floor x)), and where
+// floor x grows S' is scaled by that many powers of two, exactly.  So
+//   S' <- S' + k (dt v / g)^T,  o = g (S'^T q),
+// and no decay rounds the state.  (Each rounded, and its product with the state, steps
+// that are alike err to one side: 16000 tokens of dt = 3e-4 put the state off by 8e-5 of itself.)
+//
 // A prompt of a few tokens is bound by its state's traffic (4 dk dv bytes in and
 // out; 256 sequences of 128 heads of 128 x 64 by one token: 2.1 GB in 374 us, 5.7 TB/s), a
 // longer one by the chain from token to token, so long ones take the chunked form, or,
@@ -11,12 +18,13 @@
 // form's: without outputs first, each from a zero state, then each from the state
 // before it.
 #include "sk_prompt_chunk.hpp"
-#include "sk_scan.hpp"
+#include "sk_scan_device.hpp"
 
 namespace sk {
 namespace {
 
 constexpr int TB = 16;    // tokens staged at a time
+constexpr int DTB = 64;   // .. and their decays: a lane each of one wave
 
 __device__ __forceinline__ void put16(float* dst, const u32x4& r, const bf16*) {
 #pragma unroll
@@ -54,18 +62,27 @@ struct Rows {
 template <typename AT> constexpr int lane_columns() { return sizeof(AT) == 2 ? 2 : 1; }
 
 // Tokens under way at once: nothing but the state goes from one to the next.  bf16: one,
-// whose registers leave four waves a SIMD (256 sequences, a token each: 376 us, two
-// at once 409, four 657); fp32, whose waves are few, two (8 prompts of up to 512 tokens,
-// 16 heads of 128 x 64: 201 us one, 178 two, 195 four).
-template <typename AT> constexpr int tokens_at_once() { return sizeof(AT) == 2 ? 1 : 2; }
+// whose registers leave three waves a SIMD.  fp32: two where waves are few, in segments and
+// for small heads (us, one and two: 8 prompts of 512 tokens with 16 heads of 64 x 64 64
+// and 64, of 128 x 64 124 and 112; 2 with 64 heads of 128 x 64 105 and 104), else one (64 prompts of
+// 200 tokens with 64 heads of 128 x 64 556 and 604; 16 with heads of 128 x 128 274 and 364).
+template <int DK, int DV, typename AT, bool SEG>
+constexpr int tokens_at_once() { return sizeof(AT) == 4 && (SEG || DK * DV <= 64 * 64) ? 2 : 1; }
+
+// (64 prompts of 5 tokens with 128 heads of 128 x 64 in fp32: 123 us, 136 with three waves)
+template <int DK, int DV, typename AT, bool SEG>
+constexpr int MIN_WAVES = sizeof(AT) == 4 && DK == 128 && DV == 64 && !SEG ? 4 : 1;
+
+// A decay of less than 2^-1024 a token is zero (an infinite step would leave no sum).
+constexpr double FORGOTTEN = 1024.;
 
 // OUT: with outputs.  SEG: one workgroup per (segment, head); the first segment
 // leaves the state that its prompt starts from in the last one's place, as in the
 // chunked form.
 template <int DK, int DV, typename AT, bool OUT, bool SEG, int NCC = lane_columns<AT>()>
-__global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
-  constexpr int NT = DV * 4 / NCC, MB = DK / 16, T = tokens_at_once<AT>();
-  __shared__ __align__(16) float s_k[TB * DK], s_q[OUT ? TB * DK : 1], s_v[TB * DV], s_ad[2 * TB];
+__global__ void __launch_bounds__(DV * 4 / NCC, (MIN_WAVES<DK, DV, AT, SEG>)) scan_step_kernel(ScanParams p) {
+  constexpr int NT = DV * 4 / NCC, MB = DK / 16, T = tokens_at_once<DK, DV, AT, SEG>();
+  __shared__ __align__(16) float s_k[TB * DK], s_q[OUT ? TB * DK : 1], s_v[TB * DV], s_ad[4 * DTB];
 
   const int slot = blockIdx.x / p.H, h = blockIdx.x - slot * p.H, g = h / (p.H / p.G);
   int i = slot, rank = 0, seg = 0, segs = 1;
@@ -158,27 +175,42 @@ __global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
   const AT* vp = reinterpret_cast<const AT*>(p.v) + s0 * p.vs + (int64_t)h * DV;
   const AT* dp = reinterpret_cast<const AT*>(p.gate) + s0 * p.gs + h;
   AT* op = reinterpret_cast<AT*>(p.o) + s0 * p.os + (int64_t)h * DV + col;
-  const float rate = expf(p.A[h]);
+  const double rate = (double)expf(p.A[h]) * LOG2E;
 
   Rows<DK, NT, AT> rk, rq;
   Rows<DV, NT, AT> rv;
-  float d = 0.f, decay = 1.f;
+  float d = 0.f, g_last = 1.f;
+  double frac = 0., gone = 0.;                   // x - floor x and floor x, of the tokens staged so far
   auto fetch = [&](int t0, int nt) {
     rk.load(kp + t0 * p.ks, p.ks, nt);
     if (OUT) rq.load(qp + t0 * p.qs, p.qs, nt);
     rv.load(vp + t0 * p.vs, p.vs, nt);
-    if (tid < nt) d = ld(dp + (t0 + tid) * p.gs);
+  };
+  auto fetch_dt = [&](int t0) {                  // (behind the end nothing happens)
+    d = tid < DTB && t0 + tid < len ? ld(dp + (t0 + tid) * p.gs) : 0.f;
   };
   int nt = len < TB ? len : TB;
   fetch(0, nt);
+  fetch_dt(0);
 
   for (int t0 = 0; t0 < len; t0 += TB) {
     rk.stage(s_k);
     if (OUT) rq.stage(s_q);
     rv.stage(s_v);
-    if (tid < TB) {                        // (behind the end nothing happens)
-      s_ad[2 * tid] = tid < nt ? expf(-d * rate) : 1.f;
-      s_ad[2 * tid + 1] = tid < nt ? d : 0.f;
+    const float* s_now = s_ad + 4 * (t0 % DTB);
+    if (t0 % DTB == 0 && tid < DTB) {
+      double x = (double)d * rate;
+      x = x > FORGOTTEN ? FORGOTTEN : x;
+      const double at = frac + wave_prefix(x), whole = floor(at), part = at - whole;
+      const double from = dpp_d<0x138>(whole), before = tid > 0 ? from : t0 > 0 ? 0. : -1.;
+      // (wave_shr:1, in which all lanes take part; the first token's S' is half of S)
+      const int drop = part == part ? (int)(whole - before) : 0;
+      const f32x4s ad = {d * exp2_of(part - 1.), exp2_of(1. - part), ldexpf(1.f, -drop),
+                         __uint_as_float((uint32_t)(__ballot(drop != 0) >> (tid & -TB)))};
+      reinterpret_cast<f32x4s*>(s_ad)[tid] = ad;
+      frac = wave_last(part);
+      gone += wave_last(whole);
+      fetch_dt(t0 + DTB);
     }
     __syncthreads();
     const int now = nt, left = len - t0 - TB;
@@ -186,52 +218,88 @@ __global__ void __launch_bounds__(DV * 4 / NCC) scan_step_kernel(ScanParams p) {
       nt = left < TB ? left : TB;
       fetch(t0 + TB, nt);
     }
+    g_last = s_now[4 * (TB - 1) + 1];
+    const uint32_t drops = __builtin_amdgcn_readfirstlane(__float_as_uint(s_now[3]));
 #pragma unroll 1
     for (int j0 = 0; j0 < now; j0 += T) {
-      float u[T][NCC], o[T][NCC], a[T];
+      float u[T][NCC], o[T][NCC], o2[T][NCC], g[T], drop[T];       // (drop: the power of two that S' is scaled by)
 #pragma unroll
       for (int t = 0; t < T; ++t) {
+        float x[4];
         ldn<NCC>(s_v + (j0 + t) * DV + col, u[t]);
-        a[t] = s_ad[2 * (j0 + t)];
-        const float dt = s_ad[2 * (j0 + t) + 1];
+        ld4(s_now + 4 * (j0 + t), x);
+        g[t] = x[1];
+        drop[t] = x[2];
 #pragma unroll
         for (int c = 0; c < NCC; ++c) {
-          u[t][c] *= dt;
-          o[t][c] = 0.f;
+          u[t][c] *= x[0];
+          o[t][c] = o2[t][c] = 0.f;
         }
       }
+      if (drops >> j0 & 1) {
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-          float kk[4], qq[4];
-          ld4(s_k + (j0 + t) * DK + 16 * mb + 4 * rg, kk);
-          if (OUT) ld4(s_q + (j0 + t) * DK + 16 * mb + 4 * rg, qq);
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int c = 0; c < NCC; ++c)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              s[mb][c][v] = a[t] * s[mb][c][v] + kk[v] * u[t][c];
-              if (OUT) o[t][c] += s[mb][c][v] * qq[v];
-            }
+            for (int v = 0; v < 4; ++v) s[mb][c][v] *= drop[0];
+      }
+      // row block mb of S' for token t, and its part of the output
+      auto update = [&](int mb, int t, const float (&kk)[4], const float (&qq)[4]) {
+#pragma unroll
+        for (int c = 0; c < NCC; ++c)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            if (t > 0) s[mb][c][v] *= drop[t];
+            s[mb][c][v] += kk[v] * u[t][c];
+            if (OUT) (v & 1 ? o2 : o)[t][c] += s[mb][c][v] * qq[v];
+          }
+      };
+      auto read = [&](int mb, int t, float (&kk)[4], float (&qq)[4]) {
+        ld4(s_k + (j0 + t) * DK + 16 * mb + 4 * rg, kk);
+        if (OUT) ld4(s_q + (j0 + t) * DK + 16 * mb + 4 * rg, qq);
+      };
+      if constexpr (T > 1) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            float kk[4], qq[4];
+            read(mb, t, kk, qq);
+            update(mb, t, kk, qq);
+          }
+      } else {                                   // (one token: the next row blocks' are read ahead)
+        constexpr int N = sizeof(AT) == 2 ? 2 : 3;
+        float kk[N][4], qq[N][4];
+#pragma unroll
+        for (int mb = 0; mb < N - 1 && mb < MB; ++mb) read(mb, 0, kk[mb], qq[mb]);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          const int far = mb + N - 1;
+          if (far < MB) read(far, 0, kk[far % N], qq[far % N]);
+          update(mb, 0, kk[mb % N], qq[mb % N]);
         }
+      }
+      if (!OUT) continue;
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        if (!OUT) {
-          decay *= a[t];
-          continue;
-        }
 #pragma unroll
-        for (int c = 0; c < NCC; ++c) o[t][c] = row_groups_sum(o[t][c]);
+        for (int c = 0; c < NCC; ++c) o[t][c] = g[t] * row_groups_sum(o[t][c] + o2[t][c]);
         if (rg == 0 && j0 + t < now) stn<NCC>(op + (t0 + j0 + t) * p.os, o[t]);
       }
     }
     __syncthreads();
   }
 
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int c = 0; c < NCC; ++c)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) s[mb][c][v] *= g_last;
   if (!OUT) {
     write(seg_at(slot));
-    if (tid == 0) p.seg_decay[(size_t)slot * p.H + h] = decay;
+    if (tid == 0) p.seg_decay[(size_t)slot * p.H + h] = exp2_of(-(gone + frac));
     return;
   }
   if (!last) return;                             // (the state behind a segment is known already)
