@@ -474,8 +474,9 @@ typedef struct {
  * in fp32, and products are those of fp32 operands; the decays' logarithms are
  * summed in 64 bits.  An infinity or a NaN in a token's row or in the state reaches
  * what the recurrence brings it to (as one or the other) and no earlier token.  (In
- * bf16, terms dt_j (q_i . k_j) v_j of 2^87 and more may overflow on the way to an output
- * that they would not.)
+ * bf16, terms dt_j (q_i . k_j) v_j of 2^87 and more, and factors q_i . k_j or
+ * dt_j (q_i . k_j) of 2^127 and more whatever v_j is, may overflow on the way to an
+ * output that they would not.)
  * Other families return SKSSM_EDIM; prime with SKSSM_COEF_STATE is SKSSM_EFLAG. */
 int sketchssm_scan(const sketchssm_layer* layer, const sketchssm_buffers* bufs,
                    const sketchssm_scan_prompts* prompts, void* hip_stream);

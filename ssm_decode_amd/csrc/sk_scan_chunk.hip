@@ -5,8 +5,10 @@
 //   O = diag(exp L) Q S_0 + P V
 //   S = exp(L_C) S_0 + K^T diag(exp(L_C - L_j) dt_j) V
 // The sums L run in 64 bits, so that a difference of two is that of the tokens
-// between them, whatever came before; decays are exponentials of differences of the
-// right sign, so no quotient overflows.
+// between them, whatever came before.  P's factors are a quotient, exp(-L_j) dt_j on K Q^T and
+// exp(L_i) on the outputs, where a chunk's decays together are 2^-NEAR_BITS or more and
+// the factors so far from the type's end that no quotient overflows; elsewhere each is the
+// exponential of a difference.
 //
 // Precision.  The state is fp32, and so is every product.  They run on the bf16 matrix
 // cores with each fp32 operand (S_0, P, the weighted V) as an exact sum of three
@@ -34,8 +36,10 @@
 namespace sk {
 namespace {
 
-// (their terms may pass 2^(128 - NEAR_BITS) only where they overflow on the way to an output)
+// (terms with V may pass 2^(128 - NEAR_BITS) only where they overflow on the way to an output)
 constexpr int NEAR_BITS = 40;
+constexpr uint32_t BIG_T = 0x5f800000u;          // 2^64: |K Q^T| from here on, and steps of 2^23 and more, take no quotient
+constexpr float BIG_DT = 0x1p23f;
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -60,7 +64,8 @@ struct ScanLds {
   static constexpr int T = Q + (OUT ? 2 * PC * DK * 2 : 0);      // six fragments of K Q^T in fp32
   static constexpr int V = T + (OUT ? FRAGS * 2 * FRAG_BYTES : 0);      // two waves after two: [2][64][64]
   static constexpr int V_BYTES = PC * 2 * SCAN_COLS * 2, FACTORS = 7 * PC * 4;
-  static constexpr int bytes(int waves) { return V + waves / 2 * 2 * V_BYTES + waves * FACTORS; }
+  static constexpr int big(int waves) { return V + waves / 2 * 2 * V_BYTES + waves * FACTORS; }      // [2] whether K Q^T has a large element
+  static constexpr int bytes(int waves) { return big(waves) + (OUT ? 16 : 0); }
 };
 
 // A value that is the same in every lane, in scalar registers.
@@ -260,6 +265,8 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
   auto frag = [](const unsigned char* s, int at) { return as_frag(*reinterpret_cast<const u32x4*>(s + at)); };
 
   asm volatile("s_waitcnt vmcnt(0)" : "+v"(dr)::"memory");
+  int* s_big = reinterpret_cast<int*>(smem + L::big(NW));
+  if (OUT && tid < 2) s_big[tid] = 0;
   int buf = 0;
   for (int t0 = 0; t0 < len; t0 += PC, buf ^= 1) {
     const int nt = len - t0 < PC ? len - t0 : PC, left = len - t0 - PC, next = left < PC ? left : PC;
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       const double upper = (at + 0x1.8p42) - 0x1.8p42;      // a multiple of 2^-10, |L| <= 2^14
       s_f[lane] = (float)upper;
       s_f[PC + lane] = (float)(at - upper);
-      near_one = end >= -NEAR_BITS;
+      near_one = end >= -NEAR_BITS && !__any(d >= BIG_DT);
       s_f[2 * PC + lane] = OUT && near_one ? exp2_of(-at) * d : d;
       s_f[3 * PC + lane] = exp2_of(end - at) * d;
       s_f[4 * PC + lane] = exp2_of(at);
@@ -290,6 +297,7 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
     if constexpr (OUT) {
       // The triangle: tile t of rows (tokens j) 32 kh .., columns (tokens i) 16 rb .., left
       // where a lane of the 32-column fragments finds it.
+      uint32_t big = 0;
       for (int c = wv; c < 2 * FRAGS; c += NW) {
         const int f = c >> 1, t = c & 1, rb = frag_rb(f), kh = frag_kh(f), flip = (rb & 1) * TFLIP;
         f32x4s a = {0.f, 0.f, 0.f, 0.f};
@@ -298,7 +306,11 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
           a = mm32(frag(s_k, (kk ^ 64 * kb) + (32 * kh + 4 * t) * ROW), frag(s_q, (q16 ^ 64 * kb ^ flip) + 16 * rb * ROW), a);
         const int to = frag_of(rb >> 1, 2 * kh + (hi >> 1)) * 2 + t;
         reinterpret_cast<f32x4s*>(smem + L::T)[to * 64 + 32 * (hi & 1) + 16 * (rb & 1) + n] = a;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) big = max(big, __float_as_uint(a[r]) & 0x7fffffffu);
       }
+      if (tid == 0) s_big[buf ^ 1] = 0;          // (read behind the last chunk's triangle, set behind the next barrier)
+      if (__any(big >= BIG_T) && lane == 0) s_big[buf] = 1;
     }
     if (!active) {
       if (left > 0) copy_last(t0 + PC, next, buf ^ 1);
@@ -367,6 +379,11 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
         __builtin_amdgcn_sched_barrier(0);
       }
       __syncthreads();                           // (the triangle is whole)
+      if (near_one && __builtin_amdgcn_readfirstlane(s_big[buf])) {
+        near_one = false;
+        s_f[2 * PC + lane] = lane < nt ? to_f32(dp[(int64_t)(t0 + lane) * p.gs]) : 0.f;
+        wave_lds_sync();
+      }
       // Values that are none would come to earlier tokens by zeros of P: they are taken
       // out of V, with each column's first token that has one.
       if (__any((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u)) {
@@ -385,15 +402,13 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       }
     }
 
-    // Where a chunk's decays together are less than 2^-NEAR_BITS, P's factors are
-    // taken one by one.
+    // Where P's factors are no quotient, they are taken one by one.
     if (OUT && !near_one) {
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt) O[tt] *= s_f[4 * PC + 32 * tt + ln];
     }
     // S = exp(L_C) S + K^T (w V) and O = diag(exp L) (O + (P V)^T), in turn: the matrix
     // instructions of one with the reads, factors and splits of the other between.
-    // P's factors are a quotient: exp(-L_j) dt_j on T, exp(L_i) on the outputs.
     constexpr int FA = OUT ? 1 : 2;              // (with outputs K^T's next is read behind its last use)
     bf16x8 fa[FA][DB], fw[3], fp[2][3], fv[2];
     float wj[8], fj[8];
