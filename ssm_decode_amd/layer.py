@@ -223,7 +223,7 @@ class DecodeLayer:
     def convolve(self, conv, x, q, k, v, seq_start=None, seqs=None, has_state=None, stream=None) -> int:
         """The short convolution (serving.ShortConv) of rows x [tokens, channels]
         into q, k [tokens, G, dk] and v [tokens, H, dv] (rows at any stride of
-        whole 16 bytes): prompts as ScanPrompts describes them, or, without
+        whole 16 bytes, which share no memory with x or each other): prompts as ScanPrompts describes them, or, without
         seq_start, one token of every sequence (of seqs), into a step's tensors,
         say."""
         return conv.call(self, x, q, k, v, seq_start, seqs, has_state, stream)

@@ -13,12 +13,14 @@ import ctypes as C
 import math
 from typing import Optional
 
+import numpy as np
 import torch
 
 from . import abi
 from .layer import DTYPE, TORCH_DTYPE, DecodeLayer, _on_device, _ptr, _StreamUses
 
 _DTYPES = {TORCH_DTYPE[k]: v for k, v in DTYPE.items()}
+_PIECES = abi.sketchssm_conv_piece * 3
 ACT = {"none": abi.SKSSM_ACT_NONE, "silu": abi.SKSSM_ACT_SILU, "sigmoid": abi.SKSSM_ACT_SIGMOID}
 
 
@@ -35,6 +37,31 @@ def _rows(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: 
             raise ValueError(f"{name}: every row has to be contiguous, got strides {strides}")
         row *= shape[d]
     return strides[0] if shape[0] > 1 else row
+
+
+def _shared(spans: list, n: int) -> Optional[tuple]:
+    """The first two of several tensors of n token rows each that share memory (slices
+    of the same rows may lie between each other), or None.  spans: in bytes, a tensor's
+    first row's place, from a row to the next, and of a row."""
+    if n == 0:
+        return None
+    ends = [p + (n - 1) * ps + pl for p, ps, pl in spans]
+    for i in range(1, len(spans)):
+        p, ps, pl = spans[i]
+        for j in range(i):
+            q, qs, ql = spans[j]
+            if ends[i] <= q or ends[j] <= p or ps < pl or qs < ql:
+                continue                         # (rows that overlap themselves are refused by the call)
+            if ps == qs:
+                if pl <= (q - p) % ps <= ps - ql:
+                    continue
+            else:                                # each row against the last of the others' that begins before its end
+                start = q + qs * np.arange(n)
+                at = np.minimum((start + ql - 1 - p) // ps, n - 1)
+                if not ((at >= 0) & (p + at * ps + pl > start)).any():
+                    continue
+            return j, i
+    return None
 
 
 def _indices(name: str, x: torch.Tensor, n: Optional[int], device: torch.device) -> None:
@@ -128,7 +155,7 @@ class ScanPrompts:
     ``DecodeLayer.scan`` (Mamba-2 layers): q, k [tokens, G, dk], v, o
     [tokens, H, dv] and dt [tokens, H] (as the decode steps take it: 0 or more)
     in the layer's activation dtype, q, k, v and o rows at any stride of whole
-    16 bytes; seq_start, seqs, has_state and prime as for ``Prompts``, and so are
+    16 bytes (o's share no memory with the others'); seq_start, seqs, has_state and prime as for ``Prompts``, and so are
     the workspace, held tensors and when it may be dropped."""
 
     def __init__(self, layer: DecodeLayer, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dt: torch.Tensor,
@@ -139,6 +166,11 @@ class ScanPrompts:
         strides = [_rows("q", q, (N, G, layer.dk), at, dev), _rows("k", k, (N, G, layer.dk), at, dev),
                    _rows("v", v, (N, H, layer.dv), at, dev), _rows("dt", dt, (N, H), at, dev),
                    _rows("o", o, (N, H, layer.dv), at, dev)]
+        spans = [(x.data_ptr(), st * x.element_size(), w * x.element_size())
+                 for x, st, w in zip((q, k, v, dt, o), strides, (G * layer.dk, G * layer.dk, H * layer.dv, H, H * layer.dv))]
+        for name, span in zip(("q", "k", "v", "dt"), spans):
+            if _shared([span, spans[4]], N):
+                raise ValueError(f"o shares memory with {name}, which other workgroups still read")
         n = _prompt_lists(seq_start, seqs, has_state, dev)
         self.shape = _shape(layer) + (G,)
         need = abi.sketchssm_scan_workspace_bytes(layer.layer_struct, N, n)
@@ -206,9 +238,16 @@ class ShortConv:
         N = x.shape[0]
         xs = _rows("x", x, (N, self.channels), at, dev)
         out = {"q": (q, (N, layer.G, layer.dk)), "k": (k, (N, layer.G, layer.dk)), "v": (v, (N, layer.H, layer.dv))}
-        pieces = [abi.sketchssm_conv_piece(t.data_ptr(), _rows(c, t, shape, at, dev), self.sizes[c],
-                                           layer.dk if self.unit and c != "v" else 0)
-                  for c, (t, shape) in ((c, out[c]) for c in self.order)]
+        es = x.element_size()
+        pieces, spans = [], [(x.data_ptr(), xs * es, self.channels * es)]
+        for c in self.order:
+            t, shape = out[c]
+            place, st, size = t.data_ptr(), _rows(c, t, shape, at, dev), self.sizes[c]
+            pieces.append((place, st, size, layer.dk if self.unit and c != "v" else 0))
+            spans.append((place, st * es, size * es))
+        both = _shared(spans, N)
+        if both:
+            raise ValueError(" and ".join(("x" + self.order)[i] for i in both) + " share memory")
         n = N
         if seq_start is not None:
             n = _prompt_lists(seq_start, seqs, has_state, dev)
@@ -218,7 +257,7 @@ class ShortConv:
                     _indices(name, t, n, dev)
         st = abi.sketchssm_convolution(
             x.data_ptr(), xs, self.weight.data_ptr(), None if self.bias is None else self.bias.data_ptr(),
-            self.state.data_ptr(), (abi.sketchssm_conv_piece * 3)(*pieces), self.taps, DTYPE[layer.act], ACT[self.act],
+            self.state.data_ptr(), _PIECES(*pieces), self.taps, DTYPE[layer.act], ACT[self.act],
             self.eps, layer.B, N, n, _ptr(seq_start), _ptr(seqs), _ptr(has_state), self.err.data_ptr())
         return _on_device(dev.index, lambda s: abi.sketchssm_conv(st, self.uses.add(s)), stream)
 
