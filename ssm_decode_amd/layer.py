@@ -39,6 +39,21 @@ def _on_device(index: int, call, stream):
         return call(_stream_of(stream))
 
 
+def _stream_at(handle: int, dev: torch.device):
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
+def _mark(stream, dev: torch.device, *tensors) -> None:
+    """Tensors of one call alone, on a stream that is given: dropped behind the call,
+    their memory waits for it.  (On the current stream torch's own rule is enough:
+    memory that this stream gave goes to its later work.)"""
+    if stream is not None and stream != torch._C._cuda_getCurrentRawStream(dev.index):
+        st = _stream_at(stream, dev)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(st)
+
+
 class _StreamUses:
     """The streams that calls have put work with these tensors on: dropped while
     it runs, their memory waits for it (the allocator knows of the stream alone
@@ -51,7 +66,7 @@ class _StreamUses:
     def add(self, handle: int) -> int:
         if handle not in self.seen and self.tensors:
             dev = self.tensors[0].device
-            st = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+            st = _stream_at(handle, dev)
             for t in self.tensors:
                 t.record_stream(st)
             self.seen.add(handle)
@@ -225,19 +240,22 @@ class DecodeLayer:
         into q, k [tokens, G, dk] and v [tokens, H, dv] (rows at any stride of
         whole 16 bytes, which share no memory with x or each other): prompts as ScanPrompts describes them, or, without
         seq_start, one token of every sequence (of seqs), into a step's tensors,
-        say."""
+        say.  Where a stream is given the tensors may be dropped once the call is
+        made; on the current stream torch's own rule for them holds."""
         return conv.call(self, x, q, k, v, seq_start, seqs, has_state, stream)
 
     def reorder(self, parents, beams: int, convs=(), stream=None) -> int:
         """Within each group of ``beams`` consecutive sequences, sequence b becomes
         a copy of sequence parents[b] (an int32 device tensor [batch], say
         BeamSearch.parents) in every buffer of the layer and in what convs
-        (serving.ShortConv of this layer) hold, in place."""
+        (serving.ShortConv of this layer) hold, in place.  parents may be
+        dropped as convolve's tensors may."""
         from .serving import _indices
         _indices("parents", parents.flatten() if parents.is_contiguous() else parents, self.B, self.S.device)
         for c in convs:
             c.check(self)
         extra = (abi.sketchssm_rows * max(1, len(convs)))(*(c.rows for c in convs))
+        _mark(stream, self.S.device, parents)
 
         def call(st):
             for c in convs:

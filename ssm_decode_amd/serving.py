@@ -17,7 +17,7 @@ import numpy as np
 import torch
 
 from . import abi
-from .layer import DTYPE, TORCH_DTYPE, DecodeLayer, _on_device, _ptr, _StreamUses
+from .layer import DTYPE, TORCH_DTYPE, DecodeLayer, _mark, _on_device, _ptr, _StreamUses
 
 _DTYPES = {TORCH_DTYPE[k]: v for k, v in DTYPE.items()}
 _PIECES = abi.sketchssm_conv_piece * 3
@@ -259,6 +259,7 @@ class ShortConv:
             x.data_ptr(), xs, self.weight.data_ptr(), None if self.bias is None else self.bias.data_ptr(),
             self.state.data_ptr(), _PIECES(*pieces), self.taps, DTYPE[layer.act], ACT[self.act],
             self.eps, layer.B, N, n, _ptr(seq_start), _ptr(seqs), _ptr(has_state), self.err.data_ptr())
+        _mark(stream, dev, x, q, k, v, seq_start, seqs, has_state)
         return _on_device(dev.index, lambda s: abi.sketchssm_conv(st, self.uses.add(s)), stream)
 
     def error_word(self) -> int:
@@ -298,7 +299,8 @@ class BeamSearch:
     def select(self, logits: torch.Tensor, scores: Optional[torch.Tensor] = None, ended: Optional[torch.Tensor] = None,
                stream=None) -> int:
         """The next beams; scores and ended: others than the search's own as the
-        beams' present ones.  Returns the library's code."""
+        beams' present ones.  Where a stream is given the tensors may be dropped once
+        the call is made, as ``DecodeLayer.convolve``'s.  Returns the library's code."""
         dev, rows = self.scores.device, self.groups * self.beams
         if logits.dtype not in _DTYPES or dev.type != "cuda":
             raise ValueError("logits: a bf16 or fp32 device tensor [groups * beams, vocab]")
@@ -311,6 +313,7 @@ class BeamSearch:
             logits.data_ptr(), stride, scores.data_ptr(), ended.data_ptr(), self.scores.data_ptr(), self.ended.data_ptr(),
             self.parents.data_ptr(), self.tokens.data_ptr(), self.err.data_ptr(), self.groups, self.beams, self.vocab,
             _DTYPES[logits.dtype], self.end, self.work.data_ptr(), self.work.numel())
+        _mark(stream, dev, logits, scores, ended)
         return _on_device(dev.index, lambda s: abi.sketchssm_beam_select(st, self.uses.add(s)), stream)
 
     def error_word(self) -> int:
