@@ -241,7 +241,9 @@ __global__ void __launch_bounds__(64 * SCAN_WAVES, 2) scan_chunk_kernel(ScanPara
       }
     }
   }
-  const double rate = wave_last(exp((double)p.A[h]) * -LOG2E);
+  // (finite also where exp(A) is not, so that a step of zero takes nothing)
+  const float rate_log = p.A[h];
+  const double rate = wave_last(exp(rate_log > 700.f ? 700. : (double)rate_log) * -LOG2E);
   double total = 0.;
 
   bf16* op = reinterpret_cast<bf16*>(p.o) + (int64_t)s0 * p.os + (int64_t)h * DV + c0;

@@ -175,7 +175,9 @@ __global__ void __launch_bounds__(DV * 4 / NCC, (MIN_WAVES<DK, DV, AT, SEG>)) sc
   const AT* vp = reinterpret_cast<const AT*>(p.v) + s0 * p.vs + (int64_t)h * DV;
   const AT* dp = reinterpret_cast<const AT*>(p.gate) + s0 * p.gs + h;
   AT* op = reinterpret_cast<AT*>(p.o) + s0 * p.os + (int64_t)h * DV + col;
-  const double rate = (double)expf(p.A[h]) * LOG2E;
+  // (finite also where exp(A) is not, so that a step of zero takes nothing)
+  const float rate_log = p.A[h];
+  const double rate = (double)expf(rate_log > 88.f ? 88.f : rate_log) * LOG2E;
 
   Rows<DK, NT, AT> rk, rq;
   Rows<DV, NT, AT> rv;

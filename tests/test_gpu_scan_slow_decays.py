@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_scan import ints, make_layer, make_tokens
+from tests.test_gpu_scan import ints, make_layer, make_tokens, starts
 
 pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
@@ -57,4 +57,31 @@ def test_slow_steady_decays(n, H, G, dk, dv, act, T, dt):
         assert off(lay.S[0, h], SS) <= bound, (h, off(lay.S[0, h], SS) / bound)
         if act == "f32":
             assert off(o[:T, h], oo) <= bound, (h, off(o[:T, h], oo) / bound)
+    assert lay.error_word() == 0
+
+
+@pytest.mark.parametrize("A", [95.0, 800.0])
+@pytest.mark.parametrize("lens", [[3, 1, 20], [70, 5, 130]])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_rates_past_the_types_end(act, lens, A):
+    """exp(A) past fp32's end, and past that of 64 bits: every step forgets all, and one of 0 nothing."""
+    n, N = len(lens), sum(lens)
+    lay = make_layer(n, 4, 2, 64, 64, act, seed=610)
+    q, k, v, d, o = make_tokens(N, 4, 2, 64, 64, act, seed=611)
+    lay.A[1::2] = A
+    d[::3] = 0
+    S0 = lay.S.double()
+    assert lay.scan(ScanPrompts(lay, q, k, v, d, o, ints(starts(lens)))) == 0
+    at, unit = starts(lens), 2.0 ** -24
+    for i in range(n):
+        s = slice(at[i], at[i + 1])
+        for h in (1, 3):
+            S, K, Q = S0[i, h].clone(), k[s, h // 2].double(), q[s, h // 2].double()
+            V, D = v[s, h].double(), d[s, h].double()
+            for t in range(lens[i]):
+                S = (S if D[t] == 0 else 0 * S) + D[t] * K[t][:, None] * V[t][None, :]
+                want = (Q[t][:, None] * S).sum(0)
+                off = 300 * unit * (Q[t].abs()[:, None] * S.abs()).sum(0) + (2.0 ** -8 if act == "bf16" else unit) * want.abs()
+                assert bool(((o[at[i] + t, h].double() - want).abs() <= off).all()), (i, h, t)
+            assert bool(((lay.S[i, h].double() - S).abs() <= 16 * unit * S.abs()).all()), (i, h)
     assert lay.error_word() == 0
