@@ -7,9 +7,9 @@
 // values in registers: their maximum, the sum of their exponentials and the best of
 // them, by value (a row's order is that of its values, so no rounding enters it);
 // a second joins a group's parts in 64 bits and takes the best of its candidates.
-// 320 rows of 128000 bf16 logits: 24 us (3.4 TB/s; half of it vector instructions, the
+// 320 rows of 128000 bf16 logits: 22 us (3.6 TB/s; half of it vector instructions, the
 // exponentials and the search for the best) and 8 us, a chain of reads, of logarithms and of
-// one maximum after the other.  Five rows of 50001 fp32 logits: 7 and 7 us.
+// one maximum after the other.  Five rows of 50001 fp32 logits: 6 and 7 us.
 #include <type_traits>
 
 #include "sk_beam.hpp"

@@ -22,12 +22,12 @@
 // are the transposed ones, so that a lane's results are runs of columns of one token.
 //
 // Bound by the waves' instructions.  128 heads of 128 x 64 in 8 groups: one prompt of
-// 16384 tokens 133 us without outputs, 11 between the segments and 320 with outputs, 24
-// prompts of 15715 tokens together 350.  A wave's chunk of 64 tokens is 114 of the matrix
+// 16384 tokens 132 us without outputs, 11 between the segments and 342 with outputs, 24
+// prompts of 15715 tokens together 371.  A wave's chunk of 64 tokens is 114 of the matrix
 // instructions of 32 x 32 x 16 and about 2000 others, two waves to a SIMD (a lane's state,
-// outputs and operands take 256 registers): over the last launch vector instructions take 58% of the time, the matrix cores 36%, and a
+// outputs and operands take 256 registers): over the last launch vector instructions take 56% of the time, the matrix cores 34%, and a
 // wave waits 29% of its own for the other's issue and 31% at counters and barriers.  Its
-// memory runs at 2.1 TB/s.  64 columns a wave halve the reads of K and Q and spill.
+// memory runs at 1.9 TB/s.  64 columns a wave halve the reads of K and Q and spill.
 #include <type_traits>
 
 #include "sk_prompt_chunk.hpp"

@@ -12,7 +12,7 @@
 // that are alike err to one side: 16000 tokens of dt = 3e-4 put the state off by 8e-5 of itself.)
 //
 // A prompt of a few tokens is bound by its state's traffic (4 dk dv bytes in and
-// out; 256 sequences of 128 heads of 128 x 64 by one token: 2.1 GB in 374 us, 5.7 TB/s), a
+// out; 256 sequences of 128 heads of 128 x 64 by one token: 2.1 GB in 371 us, 5.7 TB/s), a
 // longer one by the chain from token to token, so long ones take the chunked form, or,
 // where there is none (fp32, dk = 16) and tiles are few, go in segments as the chunked
 // form's: without outputs first, each from a zero state, then each from the state

@@ -20,9 +20,9 @@ int es_of(int32_t dtype) { return dtype == SKSSM_F32 ? 4 : 2; }
 
 // Prompts of up to this many tokens go token by token where the launch has both
 // kinds.  Token by token and in chunks, in us at 8, 24 and 48 tokens each: one prompt of
-// 64 heads of 128 x 64 11 and 21, 21 and 21, 35 and 21; 64 prompts 79 and 120, 110 and
-// 115, 166 and 118; 64 of heads of 64 x 64 40 and 79, 64 and 80, 104 and 85; of heads of
-// 128 x 128 126 and 225, 187 and 229, 289 and 240.
+// 64 heads of 128 x 64 11 and 21, 21 and 22, 35 and 22; 64 prompts 66 and 114, 96 and
+// 115, 148 and 117; 64 of heads of 64 x 64 38 and 79, 58 and 80, 87 and 83; of heads of
+// 128 x 128 119 and 223, 175 and 231, 264 and 238.
 constexpr int kShort = 24;
 
 // Workgroups of a convolution's launch along the tokens: its threads are 32 bits.
@@ -56,10 +56,10 @@ Plan plan(const sketchssm_layer* L, int64_t tokens, int64_t nseq) {
   if (L->dk < 64 || L->act_dtype != SKSSM_BF16) {
     // Token by token: in segments where tiles are few and prompts long on average,
     // as short as leaves the segments' states within 16 MB.  Prompts of 512 tokens in
-    // fp32, whole and in segments: 8 with 16 heads of 64 x 64 118 us and 63 (of 64 tokens;
-    // 73 of 32, 78 of 128), 32 of them 151 and 174; 2 with 64 heads of 128 x 64 179 and 102
-    // (of 128), 4 of them 180 and 179.  8 of 256 tokens with 16 heads of 64 x 64 64 and 46
-    // (of 32), 8 of 128 tokens 34 and 34.
+    // fp32, whole and in segments: 8 with 16 heads of 64 x 64 122 us and 64 (of 64 tokens;
+    // 73 of 32, 81 of 128), 32 of them 141 and 182; 2 with 64 heads of 128 x 64 183 and 107
+    // (of 128), 4 of them 183 and 185.  8 of 256 tokens with 16 heads of 64 x 64 65 and 46
+    // (of 32), 8 of 128 tokens 34 and 35.
     const int64_t state = (int64_t)L->heads * L->dk * L->dv;
     if (nseq * state <= 1 << 20 && tokens >= 160 * nseq) {
       int shift = 5;

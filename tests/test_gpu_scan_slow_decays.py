@@ -35,7 +35,8 @@ def off(x, y):
 
 @pytest.mark.parametrize("T,dt", [(4000, 1e-3), (16000, 3e-4), (16000, 2e-5)])
 @pytest.mark.parametrize("n,H,G,dk,dv,act", [(1, 2, 1, 64, 64, "f32"), (2, 3, 3, 16, 32, "f32"), (1, 2, 1, 128, 128, "f32"),
-                                             (33, 16, 1, 128, 64, "f32"), (1, 2, 2, 16, 32, "bf16")])
+                                             (33, 16, 1, 128, 64, "f32"), (1, 2, 2, 16, 32, "bf16"), (1, 2, 1, 64, 64, "bf16"),
+                                             (33, 16, 1, 128, 64, "bf16"), (2, 4, 4, 128, 128, "bf16")])
 def test_slow_steady_decays(n, H, G, dk, dv, act, T, dt):
     """n > 1: the others are short; 33 of 16 heads are too many states for segments."""
     lens = [T] + [3] * (n - 1)
