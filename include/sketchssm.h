@@ -487,7 +487,7 @@ int64_t sketchssm_scan_workspace_bytes(const sketchssm_layer* layer, int32_t tok
 
 /* Part of a convolution's channels, written to rows of their own. */
 typedef struct {
-  void* y;                   /* [tokens][channels of the piece]; overlaps no input */
+  void* y;                   /* [tokens][channels of the piece]; overlaps no input and no other piece */
   int64_t y_stride;          /* elements from a token's row to the next: as sketchssm_prompts */
   int32_t channels;          /* 0 (the piece is left out) or more, a multiple of 8 */
   int32_t unit;              /* 0, or the width of the heads that are brought to unit length:

@@ -63,9 +63,10 @@ template <typename AT> constexpr int lane_columns() { return sizeof(AT) == 2 ? 2
 
 // Tokens under way at once: nothing but the state goes from one to the next.  bf16: one,
 // whose registers leave three waves a SIMD.  fp32: two where waves are few, in segments and
-// for small heads (us, one and two: 8 prompts of 512 tokens with 16 heads of 64 x 64 64
-// and 64, of 128 x 64 124 and 112; 2 with 64 heads of 128 x 64 105 and 104), else one (64 prompts of
-// 200 tokens with 64 heads of 128 x 64 556 and 604; 16 with heads of 128 x 128 274 and 364).
+// for small heads (us, one and two: 8 prompts of 512 tokens with 16 heads of 64 x 64 67
+// and 65, 32 of them, whole, 146 and 141; 8 with 16 heads of 128 x 64 125 and 116, 2 with
+// 64 heads 106 and 107), else one (64 prompts of 200 tokens with 64 heads of 128 x 64 556
+// and 604; 16 with heads of 128 x 128 274 and 364).
 template <int DK, int DV, typename AT, bool SEG>
 constexpr int tokens_at_once() { return sizeof(AT) == 4 && (SEG || DK * DV <= 64 * 64) ? 2 : 1; }
 
